@@ -28,6 +28,7 @@ _STATUS = {
     4: "FA512_ERR_TIMEOUT",
     5: "FA512_ERR_WORKSPACE",
     6: "FA512_ERR_DEVICE_INDEX",
+    7: "FA512_ERR_OUT_OF_PAGES",
 }
 
 
@@ -82,6 +83,25 @@ def load_library():
         lib.fa512_decode_auto_splits_fp8.restype = I
         lib.fa512_decode_workspace_bytes_fp8.argtypes = [I, I, I, I, I, I, I]
         lib.fa512_decode_workspace_bytes_fp8.restype = Z
+        L = ctypes.c_int64
+        lib.fa512_decode_paged_tree.argtypes = [P] * 9 + [I] * 8 + [F, I, I, I, P, Z, P]
+        lib.fa512_decode_paged_tree.restype = I
+        lib.fa512_decode_paged_tree_fp8.argtypes = [P] * 9 + [I] * 8 + [F, F, F, I, I, I, P, Z, P]
+        lib.fa512_decode_paged_tree_fp8.restype = I
+        lib.fa512_decode_auto_splits_tree.argtypes = [I] * 7
+        lib.fa512_decode_auto_splits_tree.restype = I
+        lib.fa512_decode_workspace_bytes_tree.argtypes = [I] * 8
+        lib.fa512_decode_workspace_bytes_tree.restype = Z
+        lib.fa512_cache_append.argtypes = [P, P, L, L, L, L, P, P, P, P, P] + [I] * 6 + [P]
+        lib.fa512_cache_append.restype = I
+        lib.fa512_cache_append_fp8.argtypes = [P, P, L, L, L, L, P, P, P, P, P, F, F] + [I] * 6 + [P]
+        lib.fa512_cache_append_fp8.restype = I
+        lib.fa512_cache_compact.argtypes = [P] * 8 + [I] * 9 + [P]
+        lib.fa512_cache_compact.restype = I
+        lib.fa512_cache_fork.argtypes = [P] * 9 + [I] * 8 + [P]
+        lib.fa512_cache_fork.restype = I
+        lib.fa512_cache_resize.argtypes = [P] * 6 + [I] * 4 + [P]
+        lib.fa512_cache_resize.restype = I
         lib.fa512_device_status.argtypes = [P, I]
         lib.fa512_device_status.restype = I
         lib.fa512_status_string.argtypes = [I]
@@ -415,6 +435,321 @@ def fa512_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
         float(scale), float(k_scale), float(v_scale), int(window), int(num_splits),
         _dptr(workspace, "workspace"), ws_bytes, _stream(stream)))
     return out, lse
+
+
+def _shape(t, name: str, shape) -> None:
+    """Refuses a tensor of another shape (an argument that the kernels index by it)."""
+    if t is not None and (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape)):
+        raise Fa512Error(1, "%s must have shape %s" % (name, tuple(shape)))
+
+
+def _one_device(*tensors) -> None:
+    """The library works on the current device: refuses tensors of another one."""
+    devices = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda}
+    if len(devices) > 1:
+        raise Fa512Error(1, "the tensors are on different devices")
+    if devices and devices.pop().index != torch.cuda.current_device():
+        raise Fa512Error(1, "the tensors are not on the current device")
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tells the allocator that tensors it made here are used on another stream."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if s != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def fa512_decode_auto_splits_tree(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                  max_kv_len: int, window: int = 0, n_sinks: int = 0) -> int:
+    return int(load_library().fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
+                                                            max_kv_len, window, n_sinks))
+
+
+def fa512_decode_workspace_bytes_tree(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                      max_kv_len: int, window: int = 0, n_sinks: int = 0,
+                                      num_splits: int = 0) -> int:
+    return int(load_library().fa512_decode_workspace_bytes_tree(
+        batch, q_len, n_q_heads, n_kv_heads, max_kv_len, window, n_sinks, num_splits))
+
+
+def _decode_tree(fp8, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, lse, q_lens, k_scale,
+                 v_scale, max_kv_len, scale, window, n_sinks, num_splits, workspace, return_lse, stream):
+    if q.dim() != 4 or k_pages.dim() != 4 or k_pages.shape != v_pages.shape or q.shape[3] != HEAD_DIM \
+            or k_pages.shape[3] != HEAD_DIM:
+        raise Fa512Error(1, "q must be [batch, q_len, heads, 512], pages [n, page, heads, 512]")
+    bsz, qlen, hq, d = q.shape
+    npages, psz, hk, _ = k_pages.shape
+    if page_table.dim() != 2 or page_table.shape[0] != bsz:
+        raise Fa512Error(1, "page_table must be [batch, max_pages_per_seq]")
+    mpps = page_table.shape[1]
+    _shape(kv_lens, "kv_lens", (bsz,))
+    _shape(q_lens, "q_lens", (bsz,))
+    _shape(tree_mask, "tree_mask", (bsz, qlen, (qlen + 31) // 32))
+    _shape(out, "out", q.shape)
+    _shape(lse, "lse", q.shape[:3])
+    _one_device(q, k_pages, v_pages, page_table, kv_lens, q_lens, tree_mask, out, lse, workspace)
+    if max_kv_len is None:
+        max_kv_len = mpps * psz
+    if scale is None:
+        scale = d ** -0.5
+    lib = load_library()
+    mine = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        mine.append(out)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        mine.append(lse)
+    if workspace is None:
+        need = int(lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, int(max_kv_len), int(window),
+                                                         int(n_sinks), int(num_splits)))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        mine.append(workspace)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    pages = _e4m3_bytes if fp8 else lambda t, name: _dptr(t, name, torch.bfloat16)
+    head = (_dptr(q, "q", torch.bfloat16), pages(k_pages, "k_pages"), pages(v_pages, "v_pages"),
+            _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
+            _dptr(q_lens, "q_lens", torch.int32), _dptr(tree_mask, "tree_mask", torch.int32),
+            _dptr(out, "out", torch.bfloat16), _dptr(lse, "lse", torch.float32), bsz, qlen, hq, hk, psz,
+            npages, mpps, int(max_kv_len), float(scale))
+    tail = (int(window), int(n_sinks), int(num_splits), _dptr(workspace, "workspace"), ws_bytes,
+            _stream(stream))
+    if fp8:
+        _check(lib.fa512_decode_paged_tree_fp8(*head, float(k_scale), float(v_scale), *tail))
+    else:
+        _check(lib.fa512_decode_paged_tree(*head, *tail))
+    _used_on(stream, *mine)
+    return out, lse
+
+
+def fa512_decode_paged_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                            page_table: torch.Tensor, kv_lens: torch.Tensor,
+                            tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            lse: torch.Tensor | None = None, *, q_lens: torch.Tensor | None = None,
+                            max_kv_len: int | None = None, scale: float | None = None, window: int = 0,
+                            n_sinks: int = 0, num_splits: int = 0, workspace: torch.Tensor | None = None,
+                            return_lse: bool = True, stream=None):
+    """The drafted tokens of each sequence (its last ``q_lens[b]`` cached
+    positions) over a paged KV cache; returns ``(out, lse)``.
+
+    q [batch, q_len, n_q_heads, 512]; ``tree_mask`` [batch, q_len, ceil(q_len / 32)]
+    int32, bit j of row t: token t sees token j (None: a plain run, token t
+    sees tokens 0 .. t); ``q_lens`` [batch] int32 (None: q_len each).  With
+    ``window`` > 0 the first ``n_sinks`` positions stay visible.  Rows of
+    padding tokens get O = 0, LSE = -inf.  Other arguments as
+    :func:`fa512_decode_paged_q`.
+    """
+    return _decode_tree(False, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, lse, q_lens, 1.0,
+                        1.0, max_kv_len, scale, window, n_sinks, num_splits, workspace, return_lse, stream)
+
+
+def fa512_decode_paged_tree_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                page_table: torch.Tensor, kv_lens: torch.Tensor,
+                                tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                lse: torch.Tensor | None = None, *, q_lens: torch.Tensor | None = None,
+                                k_scale: float = 1.0, v_scale: float = 1.0,
+                                max_kv_len: int | None = None, scale: float | None = None,
+                                window: int = 0, n_sinks: int = 0, num_splits: int = 0,
+                                workspace: torch.Tensor | None = None, return_lse: bool = True,
+                                stream=None):
+    """:func:`fa512_decode_paged_tree` over a cache stored in FP8 E4M3 (uint8
+    codes or torch.float8_e4m3fn; a key element is k_scale * e4m3, a value
+    element v_scale * e4m3)."""
+    return _decode_tree(True, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, lse, q_lens, k_scale,
+                        v_scale, max_kv_len, scale, window, n_sinks, num_splits, workspace, return_lse,
+                        stream)
+
+
+def _new_rows(t: torch.Tensor, name: str):
+    """(pointer, batch stride, token stride) of new rows whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise Fa512Error(1, "%s must be a bf16 CUDA tensor" % name)
+    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+        raise Fa512Error(1, "the heads of a token of %s must be contiguous" % name)
+    # the stride of a dimension of one entry says nothing
+    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _append(fp8, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale, stream):
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_pages.dim() != 4 \
+            or k_pages.shape != v_pages.shape or tuple(k_new.shape[2:]) != tuple(k_pages.shape[2:]) \
+            or k_pages.shape[3] != HEAD_DIM:
+        raise Fa512Error(1, "k_new, v_new must be [batch, q_len, heads, 512], pages [n, page, heads, 512]")
+    bsz, qlen = k_new.shape[:2]
+    npages, psz, hk, _ = k_pages.shape
+    if page_table.dim() != 2 or page_table.shape[0] != bsz:
+        raise Fa512Error(1, "page_table must be [batch, max_pages_per_seq]")
+    _shape(kv_lens, "kv_lens", (bsz,))
+    _shape(q_lens, "q_lens", (bsz,))
+    _one_device(k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens)
+    kp, kb, kt = _new_rows(k_new, "k_new")
+    vp, vb, vt = _new_rows(v_new, "v_new")
+    pages = _e4m3_bytes if fp8 else lambda t, name: _dptr(t, name, torch.bfloat16)
+    head = (kp, vp, kb, kt, vb, vt, pages(k_pages, "k_pages"), pages(v_pages, "v_pages"),
+            _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
+            _dptr(q_lens, "q_lens", torch.int32))
+    tail = (bsz, qlen, hk, psz, npages, page_table.shape[1], _stream(stream))
+    lib = load_library()
+    if fp8:
+        _check(lib.fa512_cache_append_fp8(*head, float(k_scale), float(v_scale), *tail))
+    else:
+        _check(lib.fa512_cache_append(*head, *tail))
+    return k_pages, v_pages
+
+
+def fa512_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                       v_pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                       q_lens: torch.Tensor | None = None, stream=None):
+    """Writes the newest tokens' keys and values into the pages; returns
+    ``(k_pages, v_pages)``, which are written in place.
+
+    k_new / v_new [batch, q_len, n_kv_heads, 512] bf16, contiguous heads, any
+    sequence and token strides that are multiples of 8; ``kv_lens`` counts the
+    new tokens, ``q_lens`` [batch] int32 says how many there are (None: q_len).
+    """
+    return _append(False, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, 1.0, 1.0, stream)
+
+
+def fa512_cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                           q_lens: torch.Tensor | None = None, k_scale: float = 1.0,
+                           v_scale: float = 1.0, stream=None):
+    """:func:`fa512_cache_append` into an FP8 E4M3 cache (uint8 codes or
+    torch.float8_e4m3fn): x is stored as the E4M3 value nearest to x / scale,
+    beyond +-448 as +-448."""
+    return _append(True, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale,
+                   stream)
+
+
+def _whole_cache(k_pages, v_pages):
+    """(k pointer, v pointer, layers, pages, page size, heads, bytes) of a cache of one or several layers."""
+    if k_pages.dim() not in (4, 5) or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
+            or k_pages.shape[-1] != HEAD_DIM:
+        raise Fa512Error(1, "pages must be [(layers,) n, page, heads, 512], k_pages like v_pages")
+    if k_pages.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise Fa512Error(1, "pages must be bf16, uint8 or float8_e4m3fn, got %s" % k_pages.dtype)
+    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    npages, psz, hk, _ = k_pages.shape[-4:]
+    return (_dptr(k_pages, "k_pages"), _dptr(v_pages, "v_pages"), layers, npages, psz, hk,
+            k_pages.element_size())
+
+
+def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                        kv_lens: torch.Tensor, accepted: torch.Tensor, n_accepted: torch.Tensor,
+                        new_kv_lens: torch.Tensor | None = None, *, q_len: int,
+                        q_lens: torch.Tensor | None = None, stream=None):
+    """Moves the accepted drafted tokens' rows together; returns ``new_kv_lens``.
+
+    k_pages / v_pages [(n_layers,) num_pages, page_size, n_kv_heads, 512], bf16
+    or E4M3, changed in place; accepted [batch, max_accepted] int32, rising,
+    the first n_accepted[b] of each row used; ``q_len`` drafted tokens per
+    sequence (or ``q_lens`` [batch] int32, each at most q_len), which kv_lens
+    counts.
+    """
+    kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
+    if page_table.dim() != 2 or accepted.dim() != 2 or accepted.shape[0] != page_table.shape[0]:
+        raise Fa512Error(1, "page_table must be [batch, pages], accepted [batch, max_accepted]")
+    bsz, mpps = page_table.shape
+    for t, name in ((kv_lens, "kv_lens"), (n_accepted, "n_accepted"), (new_kv_lens, "new_kv_lens"),
+                    (q_lens, "q_lens")):
+        _shape(t, name, (bsz,))
+    _one_device(k_pages, v_pages, page_table, kv_lens, accepted, n_accepted, new_kv_lens, q_lens)
+    mine = []
+    if new_kv_lens is None:
+        new_kv_lens = torch.empty((bsz,), dtype=torch.int32, device=kv_lens.device)
+        mine.append(new_kv_lens)
+    _check(load_library().fa512_cache_compact(
+        kp, vp, _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
+        _dptr(q_lens, "q_lens", torch.int32), _dptr(accepted, "accepted", torch.int32),
+        _dptr(n_accepted, "n_accepted", torch.int32), _dptr(new_kv_lens, "new_kv_lens", torch.int32),
+        layers, bsz, int(q_len), accepted.shape[1], hk, eb, psz, npages, mpps, _stream(stream)))
+    _used_on(stream, *mine)
+    return new_kv_lens
+
+
+def fa512_cache_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                     kv_lens: torch.Tensor, parents: torch.Tensor, page_refs: torch.Tensor,
+                     new_page_table: torch.Tensor | None = None,
+                     new_kv_lens: torch.Tensor | None = None,
+                     new_page_refs: torch.Tensor | None = None, *, stream=None):
+    """Replaces the sequences of a cache by children of them; returns
+    ``(new_page_table, new_kv_lens, new_page_refs)``.
+
+    parents [n_children] int32; page_refs [num_pages] int32, 0 = free.  Whole
+    pages are shared, a partly filled last page goes to its parent's first
+    child and is copied (all layers) into a free page for every other one.
+    ``new_page_refs`` may be ``page_refs`` itself.
+    """
+    kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
+    if page_table.dim() != 2 or parents.dim() != 1:
+        raise Fa512Error(1, "page_table must be [batch, pages], parents [n_children]")
+    bsz, mpps = page_table.shape
+    kids = parents.shape[0]
+    _shape(kv_lens, "kv_lens", (bsz,))
+    _shape(page_refs, "page_refs", (npages,))
+    _shape(new_page_table, "new_page_table", (kids, mpps))
+    _shape(new_kv_lens, "new_kv_lens", (kids,))
+    _shape(new_page_refs, "new_page_refs", (npages,))
+    _one_device(k_pages, v_pages, page_table, kv_lens, parents, page_refs, new_page_table, new_kv_lens,
+                new_page_refs)
+    mine = []
+
+    def out(t, like, shape):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=like.device)
+            mine.append(t)
+        return t
+    new_page_table = out(new_page_table, page_table, (kids, mpps))
+    new_kv_lens = out(new_kv_lens, kv_lens, (kids,))
+    new_page_refs = out(new_page_refs, page_refs, (npages,))
+    _check(load_library().fa512_cache_fork(
+        kp, vp, _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
+        _dptr(parents, "parents", torch.int32), _dptr(page_refs, "page_refs", torch.int32),
+        _dptr(new_page_table, "new_page_table", torch.int32),
+        _dptr(new_kv_lens, "new_kv_lens", torch.int32),
+        _dptr(new_page_refs, "new_page_refs", torch.int32), layers, bsz, kids, hk, eb, psz, npages, mpps,
+        _stream(stream)))
+    _used_on(stream, *mine)
+    return new_page_table, new_kv_lens, new_page_refs
+
+
+def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_lens: torch.Tensor,
+                       page_refs: torch.Tensor, new_page_table: torch.Tensor | None = None,
+                       new_page_refs: torch.Tensor | None = None, *, page_size: int, stream=None):
+    """Gives each sequence the pages of its new length and takes back those
+    behind it; returns ``(new_page_table, new_page_refs)``.
+
+    page_table [batch, max_pages_per_seq]; page_refs [num_pages] int32, 0 =
+    free.  The outputs may be the inputs themselves.
+    """
+    if page_table.dim() != 2 or page_refs.dim() != 1:
+        raise Fa512Error(1, "page_table must be [batch, pages], page_refs [num_pages]")
+    bsz, mpps = page_table.shape
+    npages = page_refs.shape[0]
+    _shape(kv_lens, "kv_lens", (bsz,))
+    _shape(new_kv_lens, "new_kv_lens", (bsz,))
+    _shape(new_page_table, "new_page_table", (bsz, mpps))
+    _shape(new_page_refs, "new_page_refs", (npages,))
+    _one_device(page_table, kv_lens, new_kv_lens, page_refs, new_page_table, new_page_refs)
+    mine = []
+    if new_page_table is None:
+        new_page_table = torch.empty_like(page_table)
+        mine.append(new_page_table)
+    if new_page_refs is None:
+        new_page_refs = torch.empty_like(page_refs)
+        mine.append(new_page_refs)
+    _check(load_library().fa512_cache_resize(
+        _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
+        _dptr(new_kv_lens, "new_kv_lens", torch.int32), _dptr(page_refs, "page_refs", torch.int32),
+        _dptr(new_page_table, "new_page_table", torch.int32),
+        _dptr(new_page_refs, "new_page_refs", torch.int32), bsz, int(page_size), npages, mpps,
+        _stream(stream)))
+    _used_on(stream, *mine)
+    return new_page_table, new_page_refs
 
 
 def fa512_device_status(stream=None, clear: bool = True) -> int:

@@ -222,6 +222,7 @@ const char* fa512_status_string(fa512_status s) {
         case FA512_ERR_TIMEOUT: return "FA512_ERR_TIMEOUT";
         case FA512_ERR_WORKSPACE: return "FA512_ERR_WORKSPACE";
         case FA512_ERR_DEVICE_INDEX: return "FA512_ERR_DEVICE_INDEX";
+        case FA512_ERR_OUT_OF_PAGES: return "FA512_ERR_OUT_OF_PAGES";
     }
     return "FA512_UNKNOWN_STATUS";
 }
@@ -750,7 +751,438 @@ fa512_status fa512_device_status(fa512_stream_t stream, int clear) {
     }
     if (word & 1u) return fail(FA512_ERR_TIMEOUT, "a kernel pipeline wait exceeded its bound");
     if (word & 2u) return fail(FA512_ERR_DEVICE_INDEX, "a page index or kv length was out of range");
+    if (word & 8u) return fail(FA512_ERR_OUT_OF_PAGES, "more pages were asked for than are free");
     if (word & 4u) return fail(FA512_ERR_UNSUPPORTED, "the dynamic shared-memory window was not 1 KiB aligned");
+    return FA512_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// ------------------------------------------- drafted tokens, cache management
+
+constexpr int kTreeRows = 64;     // (token, query head) rows that share one pass over the keys
+constexpr int kTreeTile = 128;    // keys per tile
+
+// Most key tiles that one row tile of a tree call walks: every sink tile and
+// the tiles of its band (with a window: the window, the places its rows span
+// and one tile more for a band that starts inside a tile).
+long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks) {
+    const long long all = (static_cast<long long>(max_kv_len) + kTreeTile - 1) / kTreeTile;
+    if (window <= 0) return all;
+    const long long tokens = q_len < kTreeRows ? q_len : kTreeRows;
+    (void)group;
+    const long long band = (static_cast<long long>(window) + tokens + kTreeTile - 1) / kTreeTile + 1;
+    const long long sinks = (static_cast<long long>(n_sinks) + kTreeTile - 1) / kTreeTile;
+    return sinks + band < all ? sinks + band : all;
+}
+
+bool tree_shape_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int n_sinks) {
+    return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
+           max_kv_len >= 0 && n_sinks >= 0;
+}
+
+fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                       const int32_t* kv_lens, const int32_t* q_lens, const int32_t* tree_mask, void* out,
+                       float* lse, int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                       int num_pages, int max_pages_per_seq, int max_kv_len, float scale, int window,
+                       int n_sinks, int num_splits, void* workspace, size_t workspace_bytes, bool fp8,
+                       float k_scale, float v_scale, fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    if (batch < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch");
+    if (q_len < 1) return fail(FA512_ERR_INVALID_ARG, "q_len must be >= 1");
+    if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0)
+        return fail(FA512_ERR_INVALID_ARG, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)",
+                    n_q_heads, n_kv_heads);
+    const int G = n_q_heads / n_kv_heads;
+    if (G > 128) return fail(FA512_ERR_UNSUPPORTED, "more than 128 query heads per KV head");
+    if (tree_mask && q_len > fa512::tree_max_nodes())
+        return fail(FA512_ERR_UNSUPPORTED, "a tree_mask covers at most %d tokens", fa512::tree_max_nodes());
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 256 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+        return fail(FA512_ERR_UNSUPPORTED, "page pool or page table too large for int32 key rows");
+    if (max_kv_len < 0 || static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages_per_seq) * page_size)
+        return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
+    if (num_splits < 0 || num_splits > 1024) return fail(FA512_ERR_INVALID_ARG, "num_splits outside [0, 1024]");
+    if (n_sinks < 0) return fail(FA512_ERR_INVALID_ARG, "negative n_sinks");
+    if (!(scale == scale) || isinf(scale)) return fail(FA512_ERR_INVALID_ARG, "scale is not finite");
+    if (fp8 && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
+        return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
+    if (batch > 65535 || n_kv_heads > 65535 ||
+        static_cast<long long>(q_len) * G > 0x7fffffffLL / kTreeRows / 1024)
+        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0) return FA512_OK;
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out)
+        return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+        return fail(FA512_ERR_INVALID_ARG, "q, pages and out must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
+         reinterpret_cast<uintptr_t>(q_lens) | reinterpret_cast<uintptr_t>(tree_mask) |
+         reinterpret_cast<uintptr_t>(lse)) & 3u)
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays and lse must be 4-byte aligned");
+    const int splits = num_splits > 0 ? num_splits
+                                      : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
+                                                                      max_kv_len, window, n_sinks);
+    if (splits > 1) {
+        if (static_cast<long long>(batch) * q_len > 65535)
+            return fail(FA512_ERR_UNSUPPORTED, "more than 65535 tokens with more than one split");
+        const size_t need = workspace_for(batch * q_len, n_q_heads, splits);
+        if (!workspace || workspace_bytes < need)
+            return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+        if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+            return fail(FA512_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    }
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+
+    fa512::TreeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.tree_mask = tree_mask;
+    const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
+    if (splits > 1) {
+        p.ws_o = static_cast<float*>(workspace);
+        p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows * kHeadDim * sizeof(float)));
+    }
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = G;
+    p.mask_words = (q_len + 31) / 32;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.len_cap = max_kv_len;
+    p.window = window > 0 ? window : 0;
+    p.n_sinks = n_sinks;
+    p.num_splits = splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    if (fp8) p.scale_log2 *= k_scale;
+    p.o_scale = fp8 ? v_scale : 1.f;
+    p.err = err;
+    e = fa512::launch_decode_tree(p, fp8, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tree decode launch");
+    return FA512_OK;
+}
+
+fa512_status append_call(const void* k_new, const void* v_new, int64_t kb, int64_t kt, int64_t vb, int64_t vt,
+                         void* k_pages, void* v_pages, const int32_t* page_table, const int32_t* kv_lens,
+                         const int32_t* q_lens, int batch, int q_len, int n_kv_heads, int page_size,
+                         int num_pages, int max_pages_per_seq, bool fp8, float k_scale, float v_scale,
+                         fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    if (batch < 0 || q_len < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch or q_len");
+    if (n_kv_heads < 1) return fail(FA512_ERR_INVALID_ARG, "n_kv_heads must be >= 1");
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
+    if ((kb | kt | vb | vt) & 7)
+        return fail(FA512_ERR_INVALID_ARG, "strides of k_new and v_new must be multiples of 8 elements");
+    if (fp8 && (!(k_scale > 0.f) || isinf(k_scale) || !(v_scale > 0.f) || isinf(v_scale)))
+        return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite and above 0");
+    if (batch > 65535 || static_cast<long long>(q_len) * n_kv_heads > 0x7fffffffLL / 64)
+        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0 || q_len == 0) return FA512_OK;
+    if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !kv_lens)
+        return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages))
+        return fail(FA512_ERR_INVALID_ARG, "k_new, v_new and pages must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
+         reinterpret_cast<uintptr_t>(q_lens)) & 3u)
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::AppendParams p;
+    memset(&p, 0, sizeof p);
+    p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    p.k_batch_stride = kb;
+    p.k_token_stride = kt;
+    p.v_batch_stride = vb;
+    p.v_token_stride = vt;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.n_kv_heads = n_kv_heads;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.err = err;
+    e = fa512::launch_cache_append(p, fp8, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+    return FA512_OK;
+}
+
+// Shared checks of the calls that take a whole cache of several layers.
+fa512_status cache_shape(int n_layers, int batch, int n_kv_heads, int element_bytes, int page_size,
+                         int num_pages, int max_pages_per_seq) {
+    if (batch < 0 || n_layers < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch or n_layers");
+    if (n_kv_heads < 1 || n_kv_heads > 65535) return fail(FA512_ERR_INVALID_ARG, "n_kv_heads outside [1, 65535]");
+    if (element_bytes != 1 && element_bytes != 2)
+        return fail(FA512_ERR_INVALID_ARG, "element_bytes must be 1 (E4M3) or 2 (bf16)");
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL ||
+        static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "page pool or page table too large for int32 rows");
+    if (n_layers > 32767) return fail(FA512_ERR_UNSUPPORTED, "more than 32767 layers");
+    return FA512_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+extern "C" {
+
+int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len,
+                                  int window, int n_sinks) {
+    if (!tree_shape_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, n_sinks) || batch == 0) return 1;
+    return 1;
+}
+
+size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                         int max_kv_len, int window, int n_sinks, int num_splits) {
+    if (!tree_shape_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, n_sinks) || num_splits < 0 ||
+        num_splits > 1024)
+        return 0;
+    const int s = num_splits > 0 ? num_splits
+                                 : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
+                                                                 max_kv_len, window, n_sinks);
+    if (s == 1 || batch == 0) return 256;
+    const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * s;
+    return round256(rows * kHeadDim * sizeof(float)) + round256(rows * 2 * sizeof(float));
+}
+
+fa512_status fa512_decode_paged_tree(const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, const int32_t* kv_lens,
+                                     const int32_t* q_lens, const int32_t* tree_mask, void* out, float* lse,
+                                     int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                     int num_pages, int max_pages_per_seq, int max_kv_len, float scale,
+                                     int window, int n_sinks, int num_splits, void* workspace,
+                                     size_t workspace_bytes, fa512_stream_t stream) {
+    return tree_call(q, k_pages, v_pages, page_table, kv_lens, q_lens, tree_mask, out, lse, batch, q_len,
+                     n_q_heads, n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, window,
+                     n_sinks, num_splits, workspace, workspace_bytes, false, 1.f, 1.f, stream);
+}
+
+fa512_status fa512_decode_paged_tree_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                         const int32_t* page_table, const int32_t* kv_lens,
+                                         const int32_t* q_lens, const int32_t* tree_mask, void* out,
+                                         float* lse, int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                         int page_size, int num_pages, int max_pages_per_seq, int max_kv_len,
+                                         float scale, float k_scale, float v_scale, int window, int n_sinks,
+                                         int num_splits, void* workspace, size_t workspace_bytes,
+                                         fa512_stream_t stream) {
+    return tree_call(q, k_pages, v_pages, page_table, kv_lens, q_lens, tree_mask, out, lse, batch, q_len,
+                     n_q_heads, n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, window,
+                     n_sinks, num_splits, workspace, workspace_bytes, true, k_scale, v_scale, stream);
+}
+
+fa512_status fa512_cache_append(const void* k_new, const void* v_new, int64_t k_batch_stride,
+                                int64_t k_token_stride, int64_t v_batch_stride, int64_t v_token_stride,
+                                void* k_pages, void* v_pages, const int32_t* page_table,
+                                const int32_t* kv_lens, const int32_t* q_lens, int batch, int q_len,
+                                int n_kv_heads, int page_size, int num_pages, int max_pages_per_seq,
+                                fa512_stream_t stream) {
+    return append_call(k_new, v_new, k_batch_stride, k_token_stride, v_batch_stride, v_token_stride, k_pages,
+                       v_pages, page_table, kv_lens, q_lens, batch, q_len, n_kv_heads, page_size, num_pages,
+                       max_pages_per_seq, false, 1.f, 1.f, stream);
+}
+
+fa512_status fa512_cache_append_fp8(const void* k_new, const void* v_new, int64_t k_batch_stride,
+                                    int64_t k_token_stride, int64_t v_batch_stride, int64_t v_token_stride,
+                                    void* k_pages, void* v_pages, const int32_t* page_table,
+                                    const int32_t* kv_lens, const int32_t* q_lens, float k_scale,
+                                    float v_scale, int batch, int q_len, int n_kv_heads, int page_size,
+                                    int num_pages, int max_pages_per_seq, fa512_stream_t stream) {
+    return append_call(k_new, v_new, k_batch_stride, k_token_stride, v_batch_stride, v_token_stride, k_pages,
+                       v_pages, page_table, kv_lens, q_lens, batch, q_len, n_kv_heads, page_size, num_pages,
+                       max_pages_per_seq, true, k_scale, v_scale, stream);
+}
+
+fa512_status fa512_cache_compact(void* k_pages, void* v_pages, const int32_t* page_table,
+                                 const int32_t* kv_lens, const int32_t* q_lens, const int32_t* accepted,
+                                 const int32_t* n_accepted, int32_t* new_kv_lens, int n_layers, int batch,
+                                 int q_len, int max_accepted, int n_kv_heads, int element_bytes, int page_size,
+                                 int num_pages, int max_pages_per_seq, fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    fa512_status st = cache_shape(n_layers, batch, n_kv_heads, element_bytes, page_size, num_pages,
+                                  max_pages_per_seq);
+    if (st != FA512_OK) return st;
+    if (q_len < 0 || max_accepted < 0) return fail(FA512_ERR_INVALID_ARG, "negative q_len or max_accepted");
+    if (max_accepted > fa512::compact_max_accepted())
+        return fail(FA512_ERR_UNSUPPORTED, "max_accepted above %d", fa512::compact_max_accepted());
+    if (batch > 65535) return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0) return FA512_OK;
+    if (!kv_lens || !n_accepted || !new_kv_lens || !page_table || (max_accepted > 0 && !accepted) ||
+        (n_layers > 0 && (!k_pages || !v_pages)))
+        return fail(FA512_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k_pages) || !aligned16(v_pages))
+        return fail(FA512_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+    if (misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(q_lens) || misaligned4(accepted) ||
+        misaligned4(n_accepted) || misaligned4(new_kv_lens))
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    const size_t nb = static_cast<size_t>(batch) * 4;
+    if (overlap(new_kv_lens, nb, kv_lens, nb) || overlap(new_kv_lens, nb, q_lens, nb) ||
+        overlap(new_kv_lens, nb, n_accepted, nb) || overlap(new_kv_lens, nb, accepted, nb * max_accepted) ||
+        overlap(new_kv_lens, nb, page_table, nb * max_pages_per_seq))
+        return fail(FA512_ERR_INVALID_ARG, "new_kv_lens overlaps an input");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::CompactParams p;
+    memset(&p, 0, sizeof p);
+    p.k_pages = static_cast<uint8_t*>(k_pages);
+    p.v_pages = static_cast<uint8_t*>(v_pages);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.accepted = accepted;
+    p.n_accepted = n_accepted;
+    p.new_kv_lens = new_kv_lens;
+    p.n_layers = n_layers;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.max_accepted = max_accepted;
+    p.row_bytes = n_kv_heads * kHeadDim * element_bytes;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.err = err;
+    e = fa512::launch_cache_compact(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache compact launch");
+    return FA512_OK;
+}
+
+fa512_status fa512_cache_fork(void* k_pages, void* v_pages, const int32_t* page_table, const int32_t* kv_lens,
+                              const int32_t* parents, const int32_t* page_refs, int32_t* new_page_table,
+                              int32_t* new_kv_lens, int32_t* new_page_refs, int n_layers, int batch,
+                              int n_children, int n_kv_heads, int element_bytes, int page_size, int num_pages,
+                              int max_pages_per_seq, fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    fa512_status st = cache_shape(n_layers, batch, n_kv_heads, element_bytes, page_size, num_pages,
+                                  max_pages_per_seq);
+    if (st != FA512_OK) return st;
+    if (n_children < 0) return fail(FA512_ERR_INVALID_ARG, "negative n_children");
+    if (batch > fa512::page_plan_max_batch() || n_children > fa512::page_plan_max_batch())
+        return fail(FA512_ERR_UNSUPPORTED, "more than %d sequences", fa512::page_plan_max_batch());
+    if (!page_refs || !new_page_refs || (batch > 0 && (!page_table || !kv_lens)) ||
+        (n_children > 0 && (!parents || !new_page_table || !new_kv_lens)) ||
+        (n_layers > 0 && (!k_pages || !v_pages)))
+        return fail(FA512_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k_pages) || !aligned16(v_pages))
+        return fail(FA512_ERR_INVALID_ARG, "pages must be 16-byte aligned");
+    if (misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(parents) || misaligned4(page_refs) ||
+        misaligned4(new_page_table) || misaligned4(new_kv_lens) || misaligned4(new_page_refs))
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    const size_t row = static_cast<size_t>(max_pages_per_seq) * 4, pool = static_cast<size_t>(num_pages) * 4;
+    struct { const void* p; size_t n; } in[] = {{page_table, row * batch}, {kv_lens, 4ull * batch},
+                                                {parents, 4ull * n_children}, {page_refs, pool}},
+                                        outs[] = {{new_page_table, row * n_children},
+                                                  {new_kv_lens, 4ull * n_children}, {new_page_refs, pool}};
+    for (auto& o : outs)
+        for (auto& i : in)
+            if (overlap(o.p, o.n, i.p, i.n) && !(o.p == new_page_refs && i.p == page_refs && o.p == i.p))
+                return fail(FA512_ERR_INVALID_ARG, "an output overlaps an input");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::PagePlanParams p;
+    memset(&p, 0, sizeof p);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.page_refs = page_refs;
+    p.parents = parents;
+    p.new_table = new_page_table;
+    p.new_lens = new_kv_lens;
+    p.new_refs = new_page_refs;
+    p.batch = batch;
+    p.n_new = n_children;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.k_pages = static_cast<uint8_t*>(k_pages);
+    p.v_pages = static_cast<uint8_t*>(v_pages);
+    p.n_layers = n_layers;
+    p.row_bytes = n_kv_heads * kHeadDim * element_bytes;
+    p.err = err;
+    e = fa512::launch_page_plan(p, true, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache fork launch");
+    return FA512_OK;
+}
+
+fa512_status fa512_cache_resize(const int32_t* page_table, const int32_t* kv_lens, const int32_t* new_kv_lens,
+                                const int32_t* page_refs, int32_t* new_page_table, int32_t* new_page_refs,
+                                int batch, int page_size, int num_pages, int max_pages_per_seq,
+                                fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    fa512_status st = cache_shape(0, batch, 1, 2, page_size, num_pages, max_pages_per_seq);
+    if (st != FA512_OK) return st;
+    if (batch > fa512::page_plan_max_batch())
+        return fail(FA512_ERR_UNSUPPORTED, "more than %d sequences", fa512::page_plan_max_batch());
+    if (!page_refs || !new_page_refs ||
+        (batch > 0 && (!page_table || !kv_lens || !new_kv_lens || !new_page_table)))
+        return fail(FA512_ERR_INVALID_ARG, "null pointer");
+    if (misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(new_kv_lens) || misaligned4(page_refs) ||
+        misaligned4(new_page_table) || misaligned4(new_page_refs))
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    const size_t tb = static_cast<size_t>(max_pages_per_seq) * 4 * batch, pool = static_cast<size_t>(num_pages) * 4,
+                 lb = 4ull * batch;
+    if ((new_page_table != page_table && overlap(new_page_table, tb, page_table, tb)) ||
+        (new_page_refs != page_refs && overlap(new_page_refs, pool, page_refs, pool)) ||
+        overlap(new_page_table, tb, kv_lens, lb) || overlap(new_page_table, tb, new_kv_lens, lb) ||
+        overlap(new_page_table, tb, page_refs, pool) || overlap(new_page_table, tb, new_page_refs, pool) ||
+        overlap(new_page_refs, pool, kv_lens, lb) || overlap(new_page_refs, pool, new_kv_lens, lb) ||
+        overlap(new_page_refs, pool, page_table, tb))
+        return fail(FA512_ERR_INVALID_ARG, "an output overlaps another array");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::PagePlanParams p;
+    memset(&p, 0, sizeof p);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.page_refs = page_refs;
+    p.next_lens = new_kv_lens;
+    p.new_table = new_page_table;
+    p.new_refs = new_page_refs;
+    p.batch = batch;
+    p.n_new = batch;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.err = err;
+    e = fa512::launch_page_plan(p, false, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache resize launch");
     return FA512_OK;
 }
 

@@ -53,6 +53,67 @@ bool decode_merge_sliced(long long rows);
 cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const DecodeParams& p, cudaStream_t stream);
 
+// Drafted tokens (a tree or a run of them) over a paged cache.
+struct TreeParams {
+    const __nv_bfloat16* q;        // [batch, q_len, n_q_heads, 512]
+    const void* k_pages;           // [num_pages, page_size, n_kv_heads, 512] bf16 or E4M3
+    const void* v_pages;
+    const int32_t* page_table;     // [batch, max_pages_per_seq]
+    const int32_t* kv_lens;        // [batch]
+    const int32_t* q_lens;         // [batch] or null: q_len each
+    const int32_t* tree_mask;      // [batch, q_len, mask_words] or null: a run of tokens
+    float* ws_o;                   // [batch, q_len, n_q_heads, num_splits, 512] unnormalised O
+    float* ws_ml;                  // [batch, q_len, n_q_heads, num_splits, 2]
+    __nv_bfloat16* out;            // [batch, q_len, n_q_heads, 512]
+    float* lse;                    // [batch, q_len, n_q_heads] or null
+    int batch, q_len, n_q_heads, n_kv_heads, group, mask_words;
+    int page_size, num_pages, max_pages_per_seq, len_cap;
+    int window, n_sinks;
+    int num_splits;
+    float scale_log2;              // scale * log2(e) (E4M3 cache: * k_scale)
+    float o_scale;                 // E4M3 cache: v_scale; else 1
+    unsigned* err;
+};
+
+int tree_max_nodes();              // most tokens a tree_mask covers
+cudaError_t launch_decode_tree(const TreeParams& p, bool fp8, cudaStream_t stream);
+
+struct AppendParams {
+    const __nv_bfloat16 *k_new, *v_new;
+    long long k_batch_stride, k_token_stride, v_batch_stride, v_token_stride;   // elements
+    void *k_pages, *v_pages;
+    const int32_t *page_table, *kv_lens, *q_lens;
+    float k_scale, v_scale;        // E4M3 cache
+    int batch, q_len, n_kv_heads, page_size, num_pages, max_pages_per_seq;
+    unsigned* err;
+};
+cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t stream);
+
+struct CompactParams {
+    uint8_t *k_pages, *v_pages;    // rows of row_bytes (all KV heads of a position)
+    const int32_t *page_table, *kv_lens, *q_lens, *accepted, *n_accepted;
+    int32_t* new_kv_lens;
+    int n_layers, batch, q_len, max_accepted, row_bytes, page_size, num_pages, max_pages_per_seq;
+    unsigned* err;
+};
+int compact_max_accepted();
+cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream);
+
+// Fork and resize of a cache's page tables.
+struct PagePlanParams {
+    const int32_t *page_table, *kv_lens, *page_refs;
+    const int32_t* parents;        // fork: [n_new]
+    const int32_t* next_lens;      // resize: [batch]
+    int32_t *new_table, *new_lens, *new_refs;
+    int batch, n_new, page_size, num_pages, max_pages_per_seq;
+    // fork: the pages to copy
+    uint8_t *k_pages, *v_pages;
+    int n_layers, row_bytes;
+    unsigned* err;
+};
+int page_plan_max_batch();
+cudaError_t launch_page_plan(const PagePlanParams& p, bool fork, cudaStream_t stream);
+
 struct PrefillParams {
     __nv_bfloat16* out;            // [total_q, n_q_heads, 512]
     float* lse;                    // [n_q_heads, total_q] or null

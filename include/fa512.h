@@ -38,6 +38,17 @@
  *    textbook"; vllm-project/flash-attention PR #199, "Performance" table
  *    (q_len 1, 8 query heads over 4 KV heads, head dim 512, page size 64).
  *
+ *  fa512_decode_paged_tree, fa512_decode_paged_tree_fp8 -- the drafted tokens
+ *    of each sequence, a tree of them or a plain run of any length, against
+ *    the cache they were just appended to; with a window, the first n_sinks
+ *    positions can stay visible.
+ *
+ *  fa512_cache_append, _append_fp8, _compact, _fork, _resize -- the cache
+ *    around those calls: writing new rows, moving accepted rows together,
+ *    sharing and copying pages between sequences, handing out and taking back
+ *    pages by reference counts.  The pages read a cache that a serving system
+ *    manages; these have no counterpart there.
+ *
  * Numerics: bf16 inputs and outputs, fp32 accumulation and softmax state.
  * LSE is the natural logarithm of sum_j exp(scale * q.k_j) over the visible
  * keys; a row with no visible key gets O = 0 and LSE = -inf
@@ -71,7 +82,8 @@ typedef enum {
     FA512_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed              */
     FA512_ERR_TIMEOUT = 4,     /* device: a pipeline wait exceeded its bound     */
     FA512_ERR_WORKSPACE = 5,   /* workspace missing or smaller than required     */
-    FA512_ERR_DEVICE_INDEX = 6 /* device: page index or kv length out of range   */
+    FA512_ERR_DEVICE_INDEX = 6, /* device: page index or kv length out of range  */
+    FA512_ERR_OUT_OF_PAGES = 7  /* device: more pages asked for than are free    */
 } fa512_status;
 
 /* Head dimension of every tensor this library accepts. */
@@ -336,6 +348,212 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
                                         fa512_stream_t stream);
 
 /*
+ * fa512_decode_paged_tree -- the drafted tokens of each sequence over a paged
+ * KV cache that already holds their keys and values.
+ *
+ *   q          [batch, q_len, n_q_heads, 512] bf16, device
+ *   k_pages, v_pages, page_table, kv_lens as fa512_decode_paged
+ *   q_lens     [batch] int32, device: drafted tokens of sequence b, its last
+ *              q_lens[b] cached positions; NULL: q_len for every sequence
+ *   tree_mask  [batch, q_len, ceil(q_len / 32)] int32, device: bit j % 32 of
+ *              word j / 32 of row t says that token t sees token j; NULL: a
+ *              plain run of tokens (token t sees tokens 0 .. t)
+ *   out        [batch, q_len, n_q_heads, 512] bf16, device, written
+ *   lse        [batch, q_len, n_q_heads] fp32, device, written; may be NULL
+ *
+ * With start = kv_lens[b] - q_lens[b], token t's key is cached at position
+ * start + t.  Every token sees the positions before start and the tokens its
+ * mask names (usually itself and the tokens on its way to the root).  The
+ * place of a cached key is its position; the place of token t is start + d,
+ * d the number of tokens it sees less one: in a tree, its depth.  With
+ * window > 0 a key is visible only if its place is above the token's own
+ * place less window, or below n_sinks (the first positions, which stay
+ * visible whatever the window).  Rows of tokens from q_lens[b] on, and of
+ * tokens whose cached position would be negative, see nothing: O = 0,
+ * LSE = -inf.
+ *
+ * A row is a (token, query head) pair; 64 rows of a KV head share one pass
+ * over the keys, and the keys are split over CTAs as in fa512_decode_paged
+ * (num_splits 0: fa512_decode_auto_splits_tree()).  Only pages that hold
+ * positions inside the band of some row are read; slots that no row sees may
+ * hold anything (NaN included) without reaching the output.
+ *
+ * workspace must be at least fa512_decode_workspace_bytes_tree() bytes for
+ * the split count used, 256-byte aligned; with one split it is not used and
+ * may be NULL.
+ *
+ * Requirements: q_len >= 1 (at most 256 with a tree_mask), page_size one of
+ * 16, 32, 64, 128, 256, n_q_heads a multiple of n_kv_heads with G <= 128,
+ * num_pages >= 1, max_kv_len <= max_pages_per_seq * page_size, n_sinks >= 0
+ * (it only matters with window > 0), batch and n_kv_heads at most 65535, and
+ * with more than one split batch * q_len <= 65535.  On the device, kv_lens[b]
+ * outside [0, max_kv_len], q_lens[b] outside [0, q_len] and page indices
+ * outside the pool are recorded in the error word and clipped or read as
+ * zeros.
+ */
+fa512_status fa512_decode_paged_tree(const void *q, const void *k_pages, const void *v_pages,
+                                     const int32_t *page_table, const int32_t *kv_lens,
+                                     const int32_t *q_lens, const int32_t *tree_mask, void *out,
+                                     float *lse, int batch, int q_len, int n_q_heads,
+                                     int n_kv_heads, int page_size, int num_pages,
+                                     int max_pages_per_seq, int max_kv_len, float scale,
+                                     int window, int n_sinks, int num_splits, void *workspace,
+                                     size_t workspace_bytes, fa512_stream_t stream);
+
+/* The same over a cache stored in FP8 E4M3 (as fa512_decode_paged_fp8: a key
+ * element is k_scale * e4m3(byte), a value element v_scale * e4m3(byte)). */
+fa512_status fa512_decode_paged_tree_fp8(const void *q, const void *k_pages, const void *v_pages,
+                                         const int32_t *page_table, const int32_t *kv_lens,
+                                         const int32_t *q_lens, const int32_t *tree_mask,
+                                         void *out, float *lse, int batch, int q_len,
+                                         int n_q_heads, int n_kv_heads, int page_size,
+                                         int num_pages, int max_pages_per_seq, int max_kv_len,
+                                         float scale, float k_scale, float v_scale, int window,
+                                         int n_sinks, int num_splits, void *workspace,
+                                         size_t workspace_bytes, fa512_stream_t stream);
+
+/* Split count of the tree calls when num_splits == 0.  Returns 1 when there
+ * is nothing to split. */
+int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                  int max_kv_len, int window, int n_sinks);
+
+/* Workspace bytes of the tree calls for this shape and split count
+ * (num_splits 0: the automatic choice); at least 256 for a valid shape, 0
+ * for an invalid one. */
+size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                         int max_kv_len, int window, int n_sinks, int num_splits);
+
+/*
+ * fa512_cache_append -- writes the newest tokens' keys and values into the
+ * pages of a cache.
+ *
+ *   k_new, v_new [batch, q_len, n_kv_heads, 512] bf16, device; the heads of a
+ *                token are contiguous, sequences and tokens are
+ *                k_batch_stride / v_batch_stride and k_token_stride /
+ *                v_token_stride elements apart (multiples of 8), so slices of
+ *                a fused projection's output need no copy
+ *   k_pages, v_pages as fa512_decode_paged, written
+ *   kv_lens      [batch] int32, device: cached positions of sequence b, the
+ *                new tokens included
+ *   q_lens       [batch] int32, device: new tokens of sequence b; NULL: q_len
+ *
+ * Token t of sequence b goes to position kv_lens[b] - q_lens[b] + t; tokens
+ * from q_lens[b] on are padding and are not written.  Nothing else in the
+ * pages is touched.  Two positions that share a slot are the caller's error.
+ * On the device, q_lens[b] outside [0, q_len], positions outside
+ * [0, max_pages_per_seq * page_size) and page indices outside the pool are
+ * recorded in the error word and their rows are not written.
+ */
+fa512_status fa512_cache_append(const void *k_new, const void *v_new, int64_t k_batch_stride,
+                                int64_t k_token_stride, int64_t v_batch_stride,
+                                int64_t v_token_stride, void *k_pages, void *v_pages,
+                                const int32_t *page_table, const int32_t *kv_lens,
+                                const int32_t *q_lens, int batch, int q_len, int n_kv_heads,
+                                int page_size, int num_pages, int max_pages_per_seq,
+                                fa512_stream_t stream);
+
+/* The same into an FP8 E4M3 cache: the byte of x is the E4M3 value nearest to
+ * x / k_scale (x / v_scale), ties to even, values beyond +-448 stored as
+ * +-448, NaN as the NaN code.  The scales must be finite and above 0. */
+fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_t k_batch_stride,
+                                    int64_t k_token_stride, int64_t v_batch_stride,
+                                    int64_t v_token_stride, void *k_pages, void *v_pages,
+                                    const int32_t *page_table, const int32_t *kv_lens,
+                                    const int32_t *q_lens, float k_scale, float v_scale,
+                                    int batch, int q_len, int n_kv_heads, int page_size,
+                                    int num_pages, int max_pages_per_seq, fa512_stream_t stream);
+
+/*
+ * fa512_cache_compact -- after a verification step: moves the accepted
+ * tokens' rows together, in all layers of a cache.
+ *
+ *   k_pages, v_pages [n_layers, num_pages, page_size, n_kv_heads, 512] of
+ *                element_bytes 1 (E4M3) or 2 (bf16), device, written
+ *   kv_lens      [batch] int32, device: cached positions, the q_lens[b]
+ *                (NULL: q_len) drafted tokens included
+ *   accepted     [batch, max_accepted] int32, device: the accepted tokens of
+ *                sequence b in rising order, each in [0, q_lens[b])
+ *   n_accepted   [batch] int32, device: how many
+ *   new_kv_lens  [batch] int32, device, written: start + n_accepted[b], with
+ *                start = kv_lens[b] - q_lens[b]; must not overlap the inputs
+ *
+ * The row of token accepted[b, i] moves to position start + i.  Rows behind
+ * the new length keep what they held.  A sequence whose entries do not rise
+ * inside [0, q_lens[b]), whose n_accepted[b] is outside
+ * [0, min(max_accepted, q_lens[b])] or whose lengths are impossible is
+ * recorded in the error word; it is left as it is, its new length kv_lens[b].
+ * The same holds for pages outside the pool: such rows are neither read nor
+ * written.  max_accepted is at most 1024.
+ */
+fa512_status fa512_cache_compact(void *k_pages, void *v_pages, const int32_t *page_table,
+                                 const int32_t *kv_lens, const int32_t *q_lens,
+                                 const int32_t *accepted, const int32_t *n_accepted,
+                                 int32_t *new_kv_lens, int n_layers, int batch, int q_len,
+                                 int max_accepted, int n_kv_heads, int element_bytes,
+                                 int page_size, int num_pages, int max_pages_per_seq,
+                                 fa512_stream_t stream);
+
+/*
+ * fa512_cache_fork -- replaces the sequences of a cache by children of them
+ * (beam search, several samples of one prompt, dropped sequences), in all
+ * layers at once.
+ *
+ *   k_pages, v_pages as fa512_cache_compact, written where pages are copied
+ *   page_table   [batch, max_pages_per_seq], kv_lens [batch] int32, device
+ *   parents      [n_children] int32, device: the sequence child c continues
+ *   page_refs    [num_pages] int32, device: how many sequences (and other
+ *                holders) refer to each page; 0 is free
+ *   new_page_table [n_children, max_pages_per_seq], new_kv_lens [n_children],
+ *   new_page_refs [num_pages] int32, device, written; new_page_refs may be
+ *                page_refs itself, the other two must not overlap the inputs
+ *
+ * A sequence of n positions holds its first ceil(n / page_size) entries.
+ * Child c shares the pages of parents[c].  A last page that is only partly
+ * filled goes to the first child of its parent; every other child gets a free
+ * page of its own with the filled rows copied, the lowest free pages in the
+ * order of the children.  Table entries that a child does not hold are -1.
+ * The counts lose one for each entry the old sequences held and gain one for
+ * each the children hold; pages whose count comes to 0 are free, also within
+ * this call.  When the free pages do not suffice, the children without one
+ * get -1 there and FA512_ERR_OUT_OF_PAGES is recorded in the error word.
+ * Parents outside [0, batch), lengths outside the table and page indices
+ * outside the pool are recorded too: such a child is empty, such a length is
+ * clipped, such a page is -1 in the new table and not counted.
+ *
+ * batch and n_children are at most 8192.
+ */
+fa512_status fa512_cache_fork(void *k_pages, void *v_pages, const int32_t *page_table,
+                              const int32_t *kv_lens, const int32_t *parents,
+                              const int32_t *page_refs, int32_t *new_page_table,
+                              int32_t *new_kv_lens, int32_t *new_page_refs, int n_layers,
+                              int batch, int n_children, int n_kv_heads, int element_bytes,
+                              int page_size, int num_pages, int max_pages_per_seq,
+                              fa512_stream_t stream);
+
+/*
+ * fa512_cache_resize -- gives each sequence the pages of its new length and
+ * takes back those behind it.
+ *
+ *   page_table [batch, max_pages_per_seq], kv_lens [batch], new_kv_lens
+ *   [batch], page_refs [num_pages] int32, device
+ *   new_page_table, new_page_refs: like page_table and page_refs, written;
+ *                each may be its input itself
+ *
+ * Sequence b holds its first ceil(kv_lens[b] / page_size) entries before and
+ * ceil(new_kv_lens[b] / page_size) after the call.  Entries that it gives up
+ * become -1 and the count of their page falls by one; then the entries that
+ * it gains get the lowest pages whose count is 0, in the order of (sequence,
+ * entry), with a count of 1.  All other entries behind the new length are -1.
+ * Pages of a full pool, bad lengths and bad pages as fa512_cache_fork.
+ * new_kv_lens 0 ends a sequence.  batch is at most 8192.
+ */
+fa512_status fa512_cache_resize(const int32_t *page_table, const int32_t *kv_lens,
+                                const int32_t *new_kv_lens, const int32_t *page_refs,
+                                int32_t *new_page_table, int32_t *new_page_refs, int batch,
+                                int page_size, int num_pages, int max_pages_per_seq,
+                                fa512_stream_t stream);
+
+/*
  * fa512_test_prefill_missing_load -- test hook, not a step of the method.
  * (The pages have no counterpart: it exists so that tests can drive the
  * kernels' bounded waits, which ordinary inputs never exhaust.)
@@ -361,7 +579,7 @@ fa512_status fa512_test_prefill_missing_load(const void *q, const void *k, const
 
 /* Reads and optionally clears the device-side error word after
  * synchronising `stream`.  Returns FA512_OK, FA512_ERR_TIMEOUT,
- * FA512_ERR_DEVICE_INDEX or FA512_ERR_CUDA. */
+ * FA512_ERR_DEVICE_INDEX, FA512_ERR_OUT_OF_PAGES or FA512_ERR_CUDA. */
 fa512_status fa512_device_status(fa512_stream_t stream, int clear);
 
 /* Static, human-readable name of a status code. */
