@@ -762,19 +762,16 @@ namespace {
 
 // ------------------------------------------- drafted tokens, cache management
 
-constexpr int kTreeRows = 64;     // (token, query head) rows that share one pass over the keys
-constexpr int kTreeTile = 128;    // keys per tile
-
 // Most key tiles that one row tile of a tree call walks: every sink tile and
 // the tiles of its band (with a window: the window, the places its rows span
 // and one tile more for a band that starts inside a tile).
-long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks) {
-    const long long all = (static_cast<long long>(max_kv_len) + kTreeTile - 1) / kTreeTile;
+long long tree_tiles(int q_len, int max_kv_len, int window, int n_sinks) {
+    const int tile = fa512::tree_tile(), rows = fa512::tree_rows();
+    const long long all = (static_cast<long long>(max_kv_len) + tile - 1) / tile;
     if (window <= 0) return all;
-    const long long tokens = q_len < kTreeRows ? q_len : kTreeRows;
-    (void)group;
-    const long long band = (static_cast<long long>(window) + tokens + kTreeTile - 1) / kTreeTile + 1;
-    const long long sinks = (static_cast<long long>(n_sinks) + kTreeTile - 1) / kTreeTile;
+    const long long tokens = q_len < rows ? q_len : rows;
+    const long long band = (static_cast<long long>(window) + tokens + tile - 1) / tile + 1;
+    const long long sinks = (static_cast<long long>(n_sinks) + tile - 1) / tile;
     return sinks + band < all ? sinks + band : all;
 }
 
@@ -813,7 +810,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     if (fp8 && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
     if (batch > 65535 || n_kv_heads > 65535 ||
-        static_cast<long long>(q_len) * G > 0x7fffffffLL / kTreeRows / 1024)
+        static_cast<long long>(q_len) * G > 0x7fffffffLL / 1024)
         return fail(FA512_ERR_UNSUPPORTED, "grid too large");
     if (batch == 0) return FA512_OK;
     if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out)
@@ -873,7 +870,20 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     if (fp8) p.scale_log2 *= k_scale;
     p.o_scale = fp8 ? v_scale : 1.f;
     p.err = err;
-    e = fa512::launch_decode_tree(p, fp8, reinterpret_cast<cudaStream_t>(stream));
+    const uint64_t eb = fp8 ? 1 : 2;
+    const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(n_kv_heads),
+                              static_cast<uint64_t>(num_pages) * page_size};
+    const uint64_t strides[2] = {kHeadDim * eb, static_cast<uint64_t>(n_kv_heads) * kHeadDim * eb};
+    const uint32_t tile = static_cast<uint32_t>(fa512::tree_tile());
+    const uint32_t box[3] = {static_cast<uint32_t>(128 / eb), 1u,
+                             static_cast<uint32_t>(page_size) < tile ? static_cast<uint32_t>(page_size) : tile};
+    CUtensorMap tmk, tmv;
+    const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    fa512_status st = encode_map(&tmk, type, CU_TENSOR_MAP_SWIZZLE_128B, k_pages, 3, dims, strides, box);
+    if (st != FA512_OK) return st;
+    st = encode_map(&tmv, type, CU_TENSOR_MAP_SWIZZLE_128B, v_pages, 3, dims, strides, box);
+    if (st != FA512_OK) return st;
+    e = fa512::launch_decode_tree(tmk, tmv, p, fp8, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tree decode launch");
     return FA512_OK;
 }
@@ -966,7 +976,11 @@ extern "C" {
 int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len,
                                   int window, int n_sinks) {
     if (!tree_shape_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, n_sinks) || batch == 0) return 1;
-    return 1;
+    if (static_cast<long long>(batch) * q_len > 65535) return 1;   // the merge's grid
+    const long long rows = static_cast<long long>(q_len) * (n_q_heads / n_kv_heads);
+    const long long row_tiles = (rows + fa512::tree_rows() - 1) / fa512::tree_rows();
+    return choose_splits(static_cast<long long>(batch) * n_kv_heads * row_tiles,
+                         tree_tiles(q_len, max_kv_len, window, n_sinks), sm_count());
 }
 
 size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,

@@ -52,6 +52,9 @@ int decode_fp8_ctas_per_sm();
 bool decode_merge_sliced(long long rows);
 cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const DecodeParams& p, cudaStream_t stream);
+// Combines the (O, m, l) partials of [batch, q_len, n_q_heads, num_splits]
+// (only these sizes, ws_o, ws_ml, out and lse of p are read).
+cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
 
 // Drafted tokens (a tree or a run of them) over a paged cache.
 struct TreeParams {
@@ -76,7 +79,11 @@ struct TreeParams {
 };
 
 int tree_max_nodes();              // most tokens a tree_mask covers
-cudaError_t launch_decode_tree(const TreeParams& p, bool fp8, cudaStream_t stream);
+int tree_rows();                   // rows that share one pass over the keys
+int tree_tile();                   // keys per tile
+// Both maps: {128 bytes of the head dim, 1 KV head, min(page_size, 128) positions} boxes, 128-byte swizzle.
+cudaError_t launch_decode_tree(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
+                               cudaStream_t stream);
 
 struct AppendParams {
     const __nv_bfloat16 *k_new, *v_new;

@@ -257,6 +257,18 @@ def test_repeats_are_bitwise_equal_and_leave_padding_alone(fa, fp8):
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
+@FP8
+def test_many_tiles_of_edges_repeat_bitwise(fa, fp8):
+    """Bands that start and end inside tiles, in more blocks than fit the GPU at once: every run gives the same bits."""
+    lens = [4000 - 37 * i for i in range(8)]
+    pc, q, s = make(lens, 75, 32, 4, 64, 90, fp8)
+    args = dict(window=1000, n_sinks=4)
+    a = check(fa, pc, q, None, s, **args)
+    for _ in range(4):
+        b = call(fa, pc, q, None, s, **args)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
 def test_outputs_may_sit_inside_larger_buffers(fa):
     """Bytes before and behind out and lse keep what they held."""
     pc, q, s = make([300, 90], 7, 8, 4, 64, 86)
