@@ -762,17 +762,28 @@ namespace {
 
 // ------------------------------------------- drafted tokens, cache management
 
-// Most key tiles that one row tile of a tree call walks: every sink tile and
+// Most key tiles that a row group of a tree call walks: every sink tile and
 // the tiles of its band (with a window: the window, the places its rows span
 // and one tile more for a band that starts inside a tile).
-long long tree_tiles(int q_len, int max_kv_len, int window, int n_sinks) {
-    const int tile = fa512::tree_tile(), rows = fa512::tree_rows();
+long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks) {
+    const int tile = fa512::tree_tile();
+    const fa512::TreeShape s = fa512::tree_shape(q_len, group);
     const long long all = (static_cast<long long>(max_kv_len) + tile - 1) / tile;
     if (window <= 0) return all;
-    const long long tokens = q_len < rows ? q_len : rows;
-    const long long band = (static_cast<long long>(window) + tokens + tile - 1) / tile + 1;
+    // a run's rows span their own tokens; a masked tree's all of its tokens
+    const long long span = static_cast<long long>(s.rows) * s.cluster / group + 2;
+    const long long tokens = q_len <= fa512::tree_max_nodes() || q_len < span ? q_len : span;
+    const long long band = (static_cast<long long>(window) + tokens + 1 + tile - 1) / tile + 1;
     const long long sinks = (static_cast<long long>(n_sinks) + tile - 1) / tile;
     return sinks + band < all ? sinks + band : all;
+}
+
+// Partials of `rows` rows in `splits` segments, and the items' segment counts.
+size_t tree_workspace(long long batch, int q_len, int n_q_heads, int n_kv_heads, int splits) {
+    const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
+    const fa512::TreeShape s = fa512::tree_shape(q_len, n_q_heads / n_kv_heads);
+    return round256(rows * kHeadDim * sizeof(float)) + round256(rows * 2 * sizeof(float)) +
+           round256(static_cast<size_t>(batch) * s.groups * n_kv_heads * sizeof(int32_t));
 }
 
 bool tree_shape_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int n_sinks) {
@@ -827,7 +838,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     if (splits > 1) {
         if (static_cast<long long>(batch) * q_len > 65535)
             return fail(FA512_ERR_UNSUPPORTED, "more than 65535 tokens with more than one split");
-        const size_t need = workspace_for(batch * q_len, n_q_heads, splits);
+        const size_t need = tree_workspace(batch, q_len, n_q_heads, n_kv_heads, splits);
         if (!workspace || workspace_bytes < need)
             return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
         if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -848,8 +859,12 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.tree_mask = tree_mask;
     const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
     if (splits > 1) {
-        p.ws_o = static_cast<float*>(workspace);
-        p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows * kHeadDim * sizeof(float)));
+        char* ws = static_cast<char*>(workspace);
+        p.ws_o = reinterpret_cast<float*>(ws);
+        ws += round256(rows * kHeadDim * sizeof(float));
+        p.ws_ml = reinterpret_cast<float*>(ws);
+        ws += round256(rows * 2 * sizeof(float));
+        p.ws_count = reinterpret_cast<int32_t*>(ws);
     }
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
@@ -858,6 +873,11 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.n_q_heads = n_q_heads;
     p.n_kv_heads = n_kv_heads;
     p.group = G;
+    const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
+    p.rows = shape.rows;
+    p.cluster = shape.cluster;
+    p.row_groups = shape.groups;
+    p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks));
     p.mask_words = (q_len + 31) / 32;
     p.page_size = page_size;
     p.num_pages = num_pages;
@@ -874,9 +894,8 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(n_kv_heads),
                               static_cast<uint64_t>(num_pages) * page_size};
     const uint64_t strides[2] = {kHeadDim * eb, static_cast<uint64_t>(n_kv_heads) * kHeadDim * eb};
-    const uint32_t tile = static_cast<uint32_t>(fa512::tree_tile());
-    const uint32_t box[3] = {static_cast<uint32_t>(128 / eb), 1u,
-                             static_cast<uint32_t>(page_size) < tile ? static_cast<uint32_t>(page_size) : tile};
+    const uint32_t tile = static_cast<uint32_t>(fa512::tree_tile()), page = static_cast<uint32_t>(page_size);
+    const uint32_t box[3] = {static_cast<uint32_t>(128 / eb), 1u, page < tile ? page : tile};
     CUtensorMap tmk, tmv;
     const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     fa512_status st = encode_map(&tmk, type, CU_TENSOR_MAP_SWIZZLE_128B, k_pages, 3, dims, strides, box);
@@ -977,10 +996,17 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
                                   int window, int n_sinks) {
     if (!tree_shape_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, n_sinks) || batch == 0) return 1;
     if (static_cast<long long>(batch) * q_len > 65535) return 1;   // the merge's grid
-    const long long rows = static_cast<long long>(q_len) * (n_q_heads / n_kv_heads);
-    const long long row_tiles = (rows + fa512::tree_rows() - 1) / fa512::tree_rows();
-    return choose_splits(static_cast<long long>(batch) * n_kv_heads * row_tiles,
-                         tree_tiles(q_len, max_kv_len, window, n_sinks), sm_count());
+    const int G = n_q_heads / n_kv_heads;
+    const fa512::TreeShape s = fa512::tree_shape(q_len, G);
+    const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks);
+    const long long clusters = sm_count() / s.cluster > 0 ? sm_count() / s.cluster : 1;
+    const long long per = (static_cast<long long>(batch) * n_kv_heads * s.groups * tiles + clusters - 1) / clusters;
+    if (tiles <= 1 || per <= 0) return 1;
+    // the ranges of a batch of this length touch ceil(tiles / per) + 1 of an
+    // item's segments at most; a batch with shorter sequences has shorter
+    // ranges, so twice as many are allowed
+    const long long most = 2 * ((tiles + per - 1) / per) + 1;
+    return static_cast<int>(most < tiles + 1 ? (most < 1024 ? most : 1024) : (tiles + 1 < 1024 ? tiles + 1 : 1024));
 }
 
 size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
@@ -992,8 +1018,7 @@ size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, in
                                  : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
                                                                  max_kv_len, window, n_sinks);
     if (s == 1 || batch == 0) return 256;
-    const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * s;
-    return round256(rows * kHeadDim * sizeof(float)) + round256(rows * 2 * sizeof(float));
+    return tree_workspace(batch, q_len, n_q_heads, n_kv_heads, s);
 }
 
 fa512_status fa512_decode_paged_tree(const void* q, const void* k_pages, const void* v_pages,

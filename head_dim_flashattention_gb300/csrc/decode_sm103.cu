@@ -1600,26 +1600,6 @@ static cudaError_t launch_fp8_mma(const DecodeParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// The merge may be scheduled while the split kernel before it runs (it waits
-// for it); rows too few to spread over the SMs are merged in four column
-// slices each.
-cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream) {
-    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
-    cfg.blockDim = dim3(decode::MERGE_THREADS);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return sliced ? cudaLaunchKernelEx(&cfg, decode::decode_merge_kernel<4>, p)
-                  : cudaLaunchKernelEx(&cfg, decode::decode_merge_kernel<1>, p);
-}
-
 template <bool FP8>
 static cudaError_t launch_split_and_merge(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                           const DecodeParams& p, cudaStream_t stream) {
@@ -1644,7 +1624,23 @@ static cudaError_t launch_split_and_merge(const CUtensorMap& tmk, const CUtensor
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    return launch_decode_merge(p, stream);
+    // the merge may be scheduled while the split kernel runs (it waits for
+    // it); rows too few to spread over the SMs are merged in four column
+    // slices each
+    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
+    cfg.blockDim = dim3(decode::MERGE_THREADS);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return sliced ? cudaLaunchKernelEx(&cfg, decode::decode_merge_kernel<4>, p)
+                  : cudaLaunchKernelEx(&cfg, decode::decode_merge_kernel<1>, p);
 }
 
 cudaError_t launch_decode(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,

@@ -7,26 +7,25 @@
 // token's place - window or below n_sinks, where the place of a cached key is
 // its position and that of token t is start + (tokens it sees) - 1.
 //
-// A CTA takes 64 rows ((token, query head) pairs) of one KV head and one
-// split of their key tiles of 128, and computes both products transposed on
-// tcgen05: S^T = K Q^T (M = 128 keys, N = 64 rows, K = 512) and
-// O^T += V^T P^T (four M = 128 blocks of the head dim, N = 64 rows, K = 128
+// A CTA takes ROWS = 64 (or 32) rows ((token, query head) pairs) of one KV
+// head and walks key tiles of 128, computing both products transposed on
+// tcgen05: S^T = K Q^T (M = 128 keys, N = ROWS, K = 512) and
+// O^T += V^T P^T (four M = 128 blocks of the head dim, N = ROWS, K = 128
 // keys).  So the whole fp32 O of 64 rows takes 256 TMEM columns and leaves
-// room for two S^T buffers, and the operands that are streamed, K and V, are
-// read once from shared memory as they arrive:
+// room for three S^T buffers, and K and V stream through shared memory once:
 //   K rows are the K-major A operand, V rows the MN-major A operand (its M
 //   dimension, the head dim, is the contiguous one), Q stays in shared memory
 //   as the K-major B operand, and P^T is written by the softmax threads as
-//   an MN-major B operand: a thread holds one key, so its 64 (32) values are
+//   an MN-major B operand: a thread holds one key, so its rows' values are
 //   contiguous.
-// Per 128 keys the CTA streams 256 KiB (bf16): ~5.9 us at an SM's share of
-// the measured HBM rate, against ~1.6 us of tensor work: HBM-bound for up to
-// 64 rows; more rows share the keys through L2.
+// Per 128 keys a CTA streams 256 KiB (bf16): ~5.9 us at an SM's share of the
+// measured HBM rate, against ~0.85 us of tensor work.  Row tiles of the same
+// keys form a cluster that loads each slot once and multicasts it.
 //
 // The row maxima lie across lanes here, so they are not reduced every tile:
 // each thread compares its scores with the reference its rows hold, and only
 // when some score is above it by 2^THR (a vote at the tile's one barrier) do
-// the four warps of a column half reduce the maxima and rescale O.  The row
+// the four warps of a column group reduce the maxima and rescale O.  The row
 // sums stay per-thread partials until the end.
 //
 // FP8 E4M3 cache: the bytes are MMA operands as stored (kind::f8f6f4).  Each
@@ -36,6 +35,12 @@
 // sum of three E5M2 terms (relative error 2^-9, down to 2^-28 of the
 // reference), so every product keeps at least the accuracy of the bf16 path
 // without widening a byte of the cache.
+//
+// Work: the (sequence, row group, KV head) items' tiles, one after another,
+// are cut into equal ranges, one per resident cluster, so every SM streams
+// the same number of tiles whatever the lengths; an item that spans several
+// ranges leaves (O, m, l) partials that merge_kernel combines, any other is
+// written directly.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,6 +48,8 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <mutex>
 
 #include "fa512_device.cuh"
 #include "fa512_internal.h"
@@ -56,45 +63,57 @@ using pair::wait_or_abort;
 
 constexpr int D = 512;
 constexpr int MAX_NODES = 256;
-constexpr int ROWS = 64;                 // rows of a CTA: N of both products
 constexpr int TILE = 128;                // keys per tile: M of S^T
-constexpr int SLOT = 16384;              // 128 keys x 128 bytes of the head dim
-constexpr int NS = 8;                    // ring slots
-constexpr int SOFTMAX_WARPS = 8;         // (TMEM lane quadrant, half of the rows)
-constexpr int THREADS = 64 + SOFTMAX_WARPS * 32;
-constexpr int HALF = ROWS / 2;
+constexpr int SIDE = 16384;              // 128 keys x 128 bytes of the head dim
+constexpr int SLOT = 2 * SIDE;           // a ring slot: 256 bytes of the head dim of a key tile
+constexpr int GW = 16;                   // rows (columns of S^T) of a softmax warp
+constexpr int LOOK = 2;                  // S^T tiles computed ahead of O^T += V^T P^T
+constexpr int NB = LOOK + 1;             // S^T buffers
+constexpr int MAX_CLUSTER = 8;
 
-template <bool FP8>
+template <bool FP8, int ROWS>
 struct Cfg {
     static constexpr int EB = FP8 ? 1 : 2;
-    static constexpr int CHUNKS = D * EB / 128;          // slots of a K (V) tile: 8 or 4
+    static constexpr int GROUPS = ROWS / GW;
+    static constexpr int SOFTMAX_WARPS = 4 * GROUPS;     // (column group, TMEM lane quadrant)
+    static constexpr int THREADS = 64 + SOFTMAX_WARPS * 32;
+    static constexpr int CHUNKS = D * EB / 128;          // 128-byte column chunks of the head dim: 8 or 4
+    static constexpr int SLOTS = CHUNKS / 2;             // ring slots of a K (V) tile: 4 or 2
     static constexpr int Q_CHUNK = ROWS * 128;           // one 128-byte column chunk of Q
-    static constexpr int Q_TERM = CHUNKS * Q_CHUNK;      // 64 or 32 KiB; FP8 holds two terms
+    static constexpr int Q_TERM = CHUNKS * Q_CHUNK;
     static constexpr int Q_TERMS = FP8 ? 2 : 1;
-    static constexpr int P_LINE = ROWS * EB;             // bytes of a key's row values
+    static constexpr int P_LINE = ROWS * EB;             // bytes of a key's row values: 128, 64 or 32
     static constexpr int P_TERM = TILE * P_LINE;
     static constexpr int P_TERMS = FP8 ? 3 : 1;
     static constexpr float THR = FP8 ? 4.f : 8.f;        // log2 of the growth that rescales
     static constexpr float P_SCALE = FP8 ? 2048.f : 1.f; // keeps E5M2 terms of small p normal
+    static constexpr uint32_t TM_O = 0, TM_S = 4 * ROWS;
+    static constexpr uint32_t TM_COLS = ROWS == 64 ? 512 : 256;
+    static_assert(TM_S + NB * ROWS <= TM_COLS, "tensor memory");
     // shared memory, from a 1 KiB aligned base
-    static constexpr int ring = 0;
-    static constexpr int q = NS * SLOT;
-    static constexpr int p = q + Q_TERMS * Q_TERM;
-    static constexpr int mask = p + P_TERMS * P_TERM;    // [ROWS tokens][words]
+    static constexpr int p = 0;
+    static constexpr int q = p + ((P_TERMS * P_TERM + 1023) & ~1023);
+    static constexpr int mask = q + Q_TERMS * Q_TERM;    // [ROWS tokens][words]
     static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int mult = red + 4 * ROWS * 4;      // [ROWS] float: score -> log2 units
     static constexpr int place = mult + ROWS * 4;        // [ROWS] int
-    static constexpr int tok = place + ROWS * 4;         // [ROWS] int, -1: not a row
-    static constexpr int bars = tok + ROWS * 4;
-    static constexpr int FULL = 0, EMPTY = NS, S_FULL = 2 * NS, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
-                         PV_DONE = P_FULL + 1, DRAIN = PV_DONE + 1, N_BARS = DRAIN + 1;
+    static constexpr int tok = place + ROWS * 4;         // [ROWS] int, -1: sees nothing
+    static constexpr int rows = tok + ROWS * 4;          // [4 tiles][8 boxes] int: the producer's pool rows
+    static constexpr int seen = rows + 4 * 8 * 4;         // [GROUPS][TILE] bytes: some row of the group sees the key
+    static constexpr int scan = seen + GROUPS * TILE;    // 32 long long, then the walk's start
+    static constexpr int bars = scan + 32 * 8 + 64;
+    static constexpr int MAX_NS = 6;
+    static constexpr int FULL = 0, EMPTY = MAX_NS, S_FULL = 2 * MAX_NS, S_FREE = S_FULL + NB, P_FULL = S_FREE + NB,
+                         PV_DONE = P_FULL + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1, DRAIN = O_FREE + 1,
+                         N_BARS = DRAIN + 1;
     static constexpr int misc = bars + N_BARS * 8;       // tmem address, abort flag
-    static constexpr int total = misc + 16;
+    static constexpr int ring = (misc + 16 + 1023) & ~1023;
+    static constexpr int NS_FIT = (232448 - 1024 - ring) / SLOT;
+    static constexpr int NS = NS_FIT < MAX_NS ? NS_FIT : MAX_NS;
+    static constexpr int total = ring + NS * SLOT;
+    static_assert(NS >= 4, "ring slots");
 };
-static_assert(Cfg<false>::total + 1024 <= 232448 && Cfg<true>::total + 1024 <= 232448, "shared memory of an SM");
-
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
 
 // D[tmem] (+)= A[smem] * B[smem]^T, 8-bit floating-point operands.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -106,17 +125,45 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-// Instruction descriptors: M = 128, N = ROWS, fp32 accumulator.
-constexpr uint32_t SHAPE = (1u << 4) | (static_cast<uint32_t>(ROWS >> 3) << 17) | (128u >> 4 << 24);
+// Instruction descriptors: M = 128, N = rows, fp32 accumulator.
+__host__ __device__ constexpr uint32_t shape(int rows) { return (1u << 4) | (static_cast<uint32_t>(rows >> 3) << 17) | (128u >> 4 << 24); }
+constexpr uint32_t BF16_AB = (1u << 7) | (1u << 10);
+constexpr uint32_t B_E5M2 = 1u << 10;                    // beside an E4M3 A
 constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
-constexpr uint32_t IDESC_QK16 = SHAPE | (1u << 7) | (1u << 10);                   // bf16 x bf16, both K-major
-constexpr uint32_t IDESC_PV16 = IDESC_QK16 | A_MN | B_MN;
-constexpr uint32_t IDESC_QK8 = SHAPE;                                             // e4m3 x e4m3
-constexpr uint32_t IDESC_PV8 = SHAPE | (1u << 10) | A_MN | B_MN;                  // e4m3 x e5m2
 
-// The same descriptor with 64-byte swizzle (rows of 64 bytes, 8-row atoms of 512 B).
-__device__ __forceinline__ uint64_t make_sdesc_sw64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
-    return (make_sdesc_sw128(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (4ull << 61);
+// The descriptor of an MN-major operand whose lines are `line` = 128, 64 or
+// 32 bytes, swizzled over their own length (atoms of 8 lines).
+template <int LINE>
+__device__ __forceinline__ uint64_t make_sdesc_lines(uint32_t saddr) {
+    constexpr uint64_t mode = LINE == 128 ? 2 : LINE == 64 ? 4 : 6;
+    return (make_sdesc_sw128(saddr, 16, 8 * LINE) & ~(7ull << 61)) | (mode << 61);
+}
+// Place of 16-byte piece c of line k under that swizzle.
+template <int LINE>
+__device__ __forceinline__ int line_piece(int k, int c) {
+    if constexpr (LINE == 128) return (c ^ (k & 7)) << 4;
+    if constexpr (LINE == 64) return (c ^ ((k >> 1) & 3)) << 4;
+    return (c ^ ((k >> 2) & 1)) << 4;
+}
+
+// Arrives on the barrier at this offset in CTA `rank` of the cluster when
+// every MMA issued so far has completed.
+__device__ __forceinline__ void tc_commit_to(uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(1u << rank))
+        : "memory");
+}
+// A tile load into the same shared-memory place of every CTA in `ctas`,
+// counted on each one's barrier at this offset.
+__device__ __forceinline__ void tma_load_3d_multicast(void* smem_dst, const CUtensorMap* m, uint64_t* bar, int c0,
+                                                      int c1, int c2, uint16_t ctas) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "h"(ctas)
+        : "memory");
 }
 
 // Named barrier over `count` threads that also ORs a predicate across them.
@@ -131,14 +178,14 @@ __device__ __forceinline__ void bar_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Reduces 32 values per lane over the warp's 32 lanes at once: lane i gets
-// the reduction of everyone's v[i] (31 shuffles: halves swap the values that
-// the other half keeps).
+// Reduces 16 values per lane over the warp at once: lane i gets everyone's
+// v[i % 16] (15 shuffles in which halves swap the values that the other half
+// keeps, and one that joins the warp's halves).
 template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[32], Op op) {
+__device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
+    for (int o = GW / 2; o >= 1; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int j = 0; j < o; ++j) {
@@ -146,24 +193,10 @@ __device__ __forceinline__ float reduce_columns(float (&v)[32], Op op) {
             v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
         }
     }
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// What a CTA knows of its sequence and rows.
-struct Band {
-    int len, cnt, start;        // cached positions, tokens, first token's position
-    int lo, hi;                 // keys that some row may see: [lo, hi) and the sinks below n_sinks
-    int sink_end;               // min(n_sinks, hi) with a window, else 0
-    int sink_tiles, lo_tile;    // tile i of the band is tile i < sink_tiles ? i : lo_tile + i - sink_tiles
-    int place_max;
-    int first, n_tiles;         // this split's tiles
-    __device__ __forceinline__ int key0(int i) const {
-        const int g = first + i;
-        return (g < sink_tiles ? g : lo_tile + g - sink_tiles) * TILE;
-    }
-};
-
-// E4M3 pair of two fp32 values (low byte first) and the pair's values.
+// E4M3 (E5M2) pair of two fp32 values (low byte first) and the pair's values.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float& vlo, float& vhi) {
     uint16_t e;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
@@ -183,11 +216,107 @@ __device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi, float& vlo, fl
     return e;
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(THREADS, 1)
+// The keys that a row group of a sequence walks.
+struct Band {
+    int len, cnt, start;        // cached positions, tokens, first token's position
+    int lo, hi;                 // keys that some row may see: [lo, hi) and those below sink_end
+    int sink_end;
+    int sink_tiles, lo_tile;    // tile i is i < sink_tiles ? i : lo_tile + i - sink_tiles
+    int place_max;              // no row's place is above
+    int tiles;
+    __device__ __forceinline__ int key0(int i) const {
+        return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+    }
+};
+
+// Band of row group `grp` (group_rows rows) of sequence b.  It follows from
+// the lengths alone: with a mask a token's place is only known to lie in
+// [start - 1, start + cnt - 1], and its own tokens' keys are always walked.
+__device__ __forceinline__ Band band_of(const TreeParams& p, int b, int grp, int group_rows, bool record) {
+    Band d;
+    d.len = p.kv_lens[b];
+    d.cnt = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (d.len < 0 || d.len > p.len_cap || d.cnt < 0 || d.cnt > p.q_len) {
+        if (record) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        d.len = max(0, min(d.len, p.len_cap));
+        d.cnt = max(0, min(d.cnt, p.q_len));
+    }
+    d.start = d.len - d.cnt;
+    const int r0 = grp * group_rows;
+    const int first = max(r0 / p.group, -d.start);
+    const int last = min((r0 + group_rows - 1) / p.group, d.cnt - 1);
+    d.hi = first > last ? 0 : p.tree_mask ? d.len : min(d.len, d.start + last + 1);
+    d.lo = 0;
+    d.sink_end = 0;
+    d.place_max = d.start + (p.tree_mask ? d.cnt - 1 : last);
+    if (p.window > 0 && d.hi > 0) {
+        d.lo = max(0, p.tree_mask ? d.start - p.window : d.start + first - p.window + 1);
+        d.sink_end = min(p.n_sinks, d.hi);
+    }
+    d.lo_tile = d.lo / TILE;
+    d.sink_tiles = min((d.sink_end + TILE - 1) / TILE, d.lo_tile);
+    d.tiles = d.hi <= 0 ? 0 : d.sink_tiles + (d.hi + TILE - 1) / TILE - d.lo_tile;
+    return d;
+}
+
+// Walk over this cluster's range of the items' tiles (an item without tiles
+// counts as one, so that somebody writes its empty rows).
+struct Walk {
+    long long pos, end, base;   // next unit, end of the range, first unit of the current item
+    long long per;
+    int entry, kvh;             // current item: entry = sequence * groups + row group
+    int entries, groups, group_rows;
+    Band band;
+    // the current segment
+    int b, grp, first, n;       // tiles [first, first + n) of the band
+    int index, count;           // which of how many segments of the item
+
+    __device__ __forceinline__ int units() const { return max(1, band.tiles); }
+    __device__ __forceinline__ void load(const TreeParams& p) {
+        b = entry / groups;
+        grp = entry - b * groups;
+        band = band_of(p, b, grp, group_rows, false);
+    }
+    __device__ __forceinline__ bool next(const TreeParams& p) {
+        while (pos < end) {
+            const int w = units();
+            if (pos >= base + w || (p.num_splits == 1 && pos > base)) {
+                // a whole item belongs to the range that holds its first unit
+                if (pos < base + w) pos = base + w;
+                base += w;
+                if (++kvh == p.n_kv_heads) {
+                    kvh = 0;
+                    if (++entry == entries) return false;
+                    load(p);
+                }
+                continue;
+            }
+            first = static_cast<int>(pos - base);
+            if (p.num_splits == 1) {
+                index = 0;
+                count = 1;
+                n = band.tiles;
+                pos = base + w;
+            } else {
+                const int take = static_cast<int>(min(static_cast<long long>(w - first), end - pos));
+                const long long seg0 = base / per;
+                index = static_cast<int>(pos / per - seg0);
+                count = static_cast<int>((base + w - 1) / per - seg0) + 1;
+                n = min(take, band.tiles);
+                pos += take;
+            }
+            return true;
+        }
+        return false;
+    }
+};
+
+template <bool FP8, int ROWS>
+__global__ void __launch_bounds__(Cfg<FP8, ROWS>::THREADS, 1)
 tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
             const __grid_constant__ TreeParams p) {
-    using C = Cfg<FP8>;
+    using C = Cfg<FP8, ROWS>;
+    constexpr int NS = C::NS, THREADS = C::THREADS;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -195,43 +324,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::bars);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
-    int* s_depth = reinterpret_cast<int*>(smem + C::depth);
-    uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
-    float* s_red = reinterpret_cast<float*>(smem + C::red);
-    float* s_mult = reinterpret_cast<float*>(smem + C::mult);
-    int* s_place = reinterpret_cast<int*>(smem + C::place);
-    int* s_tok = reinterpret_cast<int*>(smem + C::tok);
-
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row_tiles = (p.q_len * p.group + ROWS - 1) / ROWS;
-    const int rt = blockIdx.x % row_tiles, split = blockIdx.x / row_tiles;
-    const int kvh = blockIdx.y, b = blockIdx.z;
-    const int G = p.group, W = p.mask_words;
-    const int row0 = rt * ROWS;
-    const int tok0 = row0 / G;                                   // first token of this row tile
-    const int tok_last = min((row0 + ROWS - 1) / G, p.q_len - 1);
+    const int cs = p.cluster;
+    const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
 
-    // ---- lengths, masks and places
-    Band bd;
-    bd.len = p.kv_lens[b];
-    bd.cnt = p.q_lens ? p.q_lens[b] : p.q_len;
-    if (bd.len < 0 || bd.len > p.len_cap || bd.cnt < 0 || bd.cnt > p.q_len) {
-        if (tid == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        bd.len = max(0, min(bd.len, p.len_cap));
-        bd.cnt = max(0, min(bd.cnt, p.q_len));
-    }
-    bd.start = bd.len - bd.cnt;
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&bars[C::FULL + i], 1);
-            mbar_init(&bars[C::EMPTY + i], 1);
+            mbar_init(&bars[C::EMPTY + i], cs);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&bars[C::S_FULL + i], 1);
-            mbar_init(&bars[C::S_FREE + i], SOFTMAX_WARPS);
+            mbar_init(&bars[C::S_FREE + i], C::SOFTMAX_WARPS);
         }
-        mbar_init(&bars[C::P_FULL], SOFTMAX_WARPS);
+        mbar_init(&bars[C::P_FULL], C::SOFTMAX_WARPS);
         mbar_init(&bars[C::PV_DONE], 1);
+        mbar_init(&bars[C::Q_FULL], C::SOFTMAX_WARPS);
+        mbar_init(&bars[C::O_FREE], C::SOFTMAX_WARPS);
         mbar_init(&bars[C::DRAIN], 1);
         *abort = 0;
         fence_mbar_init();
@@ -239,430 +348,591 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         tma_prefetch_desc(&tmv);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, TM_COLS);
+        tmem_alloc(tmem_slot, C::TM_COLS);
         tmem_relinquish();
     }
-    if (p.tree_mask) {
-        // bits at and behind cnt name no token
-        auto word = [&](int t, int w) -> uint32_t {
-            const int left = bd.cnt - 32 * w;
-            const uint32_t m = static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * W + w]);
-            return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
+
+    // ---- this cluster's range: total units, then the item that holds its start
+    Walk walk;
+    walk.groups = p.row_groups;
+    walk.group_rows = ROWS * cs;
+    walk.entries = p.batch * p.row_groups;
+    {
+        long long* s_scan = reinterpret_cast<long long*>(smem + C::scan);
+        long long* s_at = s_scan + 32;                   // start's entry, unit
+        constexpr int NW = THREADS / 32;
+        const int clusters = gridDim.x / cs, me = blockIdx.x / cs;
+        auto entry_units = [&](int e, bool record) -> long long {
+            if (e >= walk.entries) return 0;
+            const int eb = e / walk.groups;
+            const Band d = band_of(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
+            return static_cast<long long>(max(1, d.tiles)) * p.n_kv_heads;
         };
-        for (int t = tid; t < bd.cnt; t += THREADS) {
-            int n = 0;
-            for (int w = 0; w < W; ++w) n += __popc(word(t, w));
-            s_depth[t] = n - 1;
+        long long total = 0;
+        for (int e = tid; e < walk.entries; e += THREADS) total += entry_units(e, blockIdx.x == 0);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0) s_scan[warp] = total;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < NW; ++w) total += s_scan[w];
+        // ranges short enough to balance, long enough that no item has more
+        // than num_splits segments
+        walk.per = (total + clusters - 1) / clusters;
+        if (p.num_splits > 1)
+            walk.per = max(walk.per, static_cast<long long>((p.max_tiles + p.num_splits - 2) / (p.num_splits - 1)));
+        walk.per = max(walk.per, 1ll);
+        walk.pos = me * walk.per;
+        walk.end = min(total, walk.pos + walk.per);
+        long long before = 0;
+        if (walk.pos < walk.end) {
+            for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
+                const long long u = entry_units(e0 + tid, false);
+                long long x = u;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                __syncthreads();
+                if (lane == 31) s_scan[warp] = x;
+                __syncthreads();
+                long long sum = before;
+                for (int w = 0; w < NW; ++w) {
+                    if (w == warp) x += sum;
+                    sum += s_scan[w];
+                }
+                if (walk.pos >= x - u && walk.pos < x) {
+                    s_at[0] = e0 + tid;
+                    s_at[1] = x - u;
+                }
+                before = sum;
+                if (walk.pos < before) break;
+            }
         }
-        const int toks = tok_last - tok0 + 1;
-        for (int i = tid; i < toks * W; i += THREADS) {
-            const int t = tok0 + i / W, w = i % W;
-            s_mask[i] = t < bd.cnt ? word(t, w) : 0u;
+        __syncthreads();
+        walk.entry = static_cast<int>(s_at[0]);
+        walk.kvh = 0;
+        walk.base = s_at[1];
+        if (walk.pos < walk.end) {
+            walk.load(p);
+            walk.kvh = static_cast<int>((walk.pos - walk.base) / walk.units());
+            walk.base += static_cast<long long>(walk.kvh) * walk.units();
         }
     }
-    __syncthreads();
+    if (cs > 1) cluster_sync_all(); else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    {
-        // places of the rows (every warp the same; warp 2 keeps them for the softmax)
-        int pmin = INT_MAX, pmax = INT_MIN;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = row0 + lane + 32 * i, t = r / G;
-            const bool real = t < bd.cnt && bd.start + t >= 0;
-            const int place = real ? bd.start + (p.tree_mask ? s_depth[t] : t) : 0;
-            if (real) {
-                pmin = min(pmin, place);
-                pmax = max(pmax, place);
-            }
-            if (warp == 2) {
-                s_place[lane + 32 * i] = place;
-                s_tok[lane + 32 * i] = real ? t : -1;
-            }
-        }
-        pmin = __reduce_min_sync(0xffffffffu, pmin);
-        pmax = __reduce_max_sync(0xffffffffu, pmax);
-        bd.place_max = pmax;
-        bd.hi = pmax == INT_MIN ? 0 : p.tree_mask ? bd.len : min(bd.len, bd.start + min(tok_last, bd.cnt - 1) + 1);
-        bd.lo = 0;
-        bd.sink_end = 0;
-        if (p.window > 0 && bd.hi > 0) {
-            // a mask may name any token, so the tokens' own keys are always walked then
-            bd.lo = max(0, p.tree_mask ? min(bd.start, pmin - p.window + 1) : pmin - p.window + 1);
-            bd.sink_end = min(p.n_sinks, bd.hi);
-        }
-        bd.lo_tile = bd.lo / TILE;
-        bd.sink_tiles = min((bd.sink_end + TILE - 1) / TILE, bd.lo_tile);
-        const int all = bd.sink_tiles + (bd.hi + TILE - 1) / TILE - bd.lo_tile;
-        const int per = (all + p.num_splits - 1) / p.num_splits;
-        bd.first = split * per;
-        bd.n_tiles = max(0, min(per, all - bd.first));
-        if (bd.hi <= 0) bd.n_tiles = 0;
-    }
-    const int n = bd.n_tiles;
-    // ring position of the first slot of K(t) and V(t): K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
-    auto k_seq = [&](int t) { return (t == 0 ? 0 : 2 * t - 1) * C::CHUNKS; };
-    auto v_seq = [&](int t) { return (t < n - 1 ? 2 * t + 2 : 2 * n - 1) * C::CHUNKS; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        // lane i < boxes brings the i-th run of box_rows positions of each slot
+        // The warp walks the slots and waits; one elected lane issues.  Slot s
+        // is loaded by CTA s % cs for the whole cluster, in boxes of
+        // {128 bytes of the head dim, box_rows positions of a page}.
+        const int oob = p.num_pages * p.page_size;           // past the pool: filled with zeros
+        const uint16_t everyone = static_cast<uint16_t>((1u << cs) - 1u);
         const int box_rows = min(p.page_size, TILE), boxes = TILE / box_rows;
-        auto row_of = [&](int t) -> int {
-            const int oob = p.num_pages * p.page_size;       // past the pool: filled with zeros
-            if (t >= n || lane >= boxes) return oob;
-            const int pos = bd.key0(t) + lane * box_rows;
-            const bool live = pos < bd.hi && (pos + box_rows > bd.lo || pos < bd.sink_end);
-            if (!live) return oob;
-            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + pos / p.page_size];
-            if (page < 0 || page >= p.num_pages) {
-                report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                return oob;
-            }
-            return page * p.page_size + pos % p.page_size;
-        };
-        int seq = 0;
+        int* s_rows = reinterpret_cast<int*>(smem + C::rows);
+        int slot = 0, owner = 0;
+        uint32_t use = 0;                                    // use number of the slot
         bool ok = true;
-        auto load_tile = [&](const CUtensorMap* tm, int row) {
-            for (int c = 0; c < C::CHUNKS && ok; ++c, ++seq) {
-                const int s = seq % NS;
-                if (seq >= NS &&
-                    !__all_sync(0xffffffffu, wait_or_abort(&bars[C::EMPTY + s], ((seq / NS) & 1) ^ 1, p.err, abort))) {
-                    ok = false;
-                    break;
+        int seq = 0;
+        auto load_tile = [&](const CUtensorMap* tm, int kvh, const int* rows) {
+            for (int c = 0; c < C::SLOTS; ++c) {
+                const bool mine = owner == rank;
+                if (use > 0) {
+                    // issuer: everyone has read the slot; others: it was filled here
+                    const int bar = mine ? C::EMPTY : C::FULL;
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&bars[bar + slot], (use & 1) ^ 1, p.err, abort));
+                    if (!ok) return;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&bars[C::FULL + s], SLOT);
+                if (elect_one()) {
+                    uint64_t* full = &bars[C::FULL + slot];
+                    mbar_arrive_expect_tx(full, SLOT);
+                    if (mine) {
+                        uint8_t* dst = smem + C::ring + slot * SLOT;
+                        const int c0 = c * (256 / C::EB);
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i) {
+                            const int row = rows[i];
+                            if (cs > 1) {
+                                tma_load_3d_multicast(dst, tm, full, c0, kvh, row, everyone);
+                                tma_load_3d_multicast(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, row, everyone);
+                            } else {
+                                tma_load_3d(dst, tm, full, c0, kvh, row);
+                                tma_load_3d(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, row);
+                            }
+                            dst += box_rows * 128;
+                        }
+                    }
+                }
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_3d(smem + C::ring + s * SLOT + lane * box_rows * 128, tm, &bars[C::FULL + s],
-                                c * (128 / C::EB), kvh, row);
+                ++seq;
+                owner = owner + 1 == cs ? 0 : owner + 1;
+                if (++slot == NS) {
+                    slot = 0;
+                    owner = 0;
+                    ++use;
+                }
             }
         };
-        int cur = row_of(0), next = row_of(1);
-        if (n > 0) load_tile(&tmk, cur);
-        for (int t = 0; t < n && ok; ++t) {
-            const int after = row_of(t + 2);                 // a tile ahead of its use
-            if (t + 1 < n) load_tile(&tmk, next);
-            if (ok) load_tile(&tmv, cur);
-            cur = next;
-            next = after;
+        while (ok && walk.next(p)) {
+            const int n = walk.n;
+            // lane i: pool row of box i of tile t, or oob where no row sees a position of it
+            auto row_of = [&](int t) -> int {
+                if (t >= n || lane >= boxes) return oob;
+                const Band& d = walk.band;
+                const int pos = d.key0(walk.first + t) + lane * box_rows;
+                if (pos >= d.hi || !(pos + box_rows > d.lo || pos < d.sink_end)) return oob;
+                const int page = p.page_table[static_cast<size_t>(walk.b) * p.max_pages_per_seq + pos / p.page_size];
+                if (page < 0 || page >= p.num_pages) {
+                    report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                    return oob;
+                }
+                return page * p.page_size + pos % p.page_size;
+            };
+            int row = row_of(0);
+            for (int j = 0; j < n + LOOK && ok; ++j) {
+                const int row_next = row_of(j + 1);          // a step ahead of its use
+                if (j < n) {
+                    if (lane < 8) s_rows[(j & 3) * 8 + lane] = row;
+                    __syncwarp();
+                    load_tile(&tmk, walk.kvh, s_rows + (j & 3) * 8);
+                }
+                if (ok && j >= LOOK) load_tile(&tmv, walk.kvh, s_rows + ((j - LOOK) & 3) * 8);
+                row = row_next;
+            }
         }
         // after an abort: no copy may land once this CTA has gone
         if (!ok)
             for (int i = max(0, seq - NS); i < seq; ++i)
                 (void)mbar_wait(&bars[C::FULL + i % NS], (i / NS) & 1, p.err);
-    } else {
-        // ---- Q: 64 rows as K-major B operand, zeros where there is no row
-        const int wid = warp - 1;                            // 0..8
-        constexpr int QW = THREADS / 32 - 1;
-        constexpr int PER = (ROWS + QW - 1) / QW;            // rows of a warp
-        uint4 x[PER][2];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = wid + i * QW, t = (row0 + r) / G;
-            const bool real = r < ROWS && t < bd.cnt;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + ((static_cast<size_t>(b) * p.q_len + (real ? t : 0)) * p.n_q_heads + kvh * G +
-                       (real ? (row0 + r) % G : 0)) * D) + 2 * lane;
-            x[i][0] = real ? src[0] : make_uint4(0u, 0u, 0u, 0u);
-            x[i][1] = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = wid + i * QW;
-            if (r >= ROWS) break;
-            if constexpr (!FP8) {
-                // this lane's 32 bytes: chunk lane / 4, pieces 2 (lane % 4) and + 1
-                uint8_t* line = smem + C::q + (lane >> 2) * C::Q_CHUNK + r * 128;
-                const int c = 2 * (lane & 3);
-                *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = x[i][0];
-                *reinterpret_cast<uint4*>(line + (((c + 1) ^ (r & 7)) << 4)) = x[i][1];
-                if (lane == 0) s_mult[r] = p.scale_log2;
-            } else {
-                const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                                       x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-                float amax = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
-                                             fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                // 2^(7 - exponent of amax): the largest element comes to [128, 256)
-                const int E = (__float_as_uint(amax) >> 23) & 0xff;
-                const int biased = min(7 + 2 * 127 - E, 254);
-                const float qs = (amax > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi[j] = lo[j] = 0u;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float a = __uint_as_float(w[2 * j + k] << 16) * qs;
-                        const float c = __uint_as_float(w[2 * j + k] & 0xffff0000u) * qs;
-                        float va, vc, ra, rc;
-                        hi[j] |= e4m3_pair(a, c, va, vc) << (16 * k);
-                        lo[j] |= e4m3_pair(a - va, c - vc, ra, rc) << (16 * k);
-                    }
-                }
-                // this lane's 16 bytes: chunk lane / 8, piece lane % 8
-                uint8_t* line = smem + C::q + (lane >> 3) * C::Q_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(line + C::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (lane == 0) s_mult[r] = p.scale_log2 / qs;
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        // the whole warp walks the tiles and waits; one elected lane issues
+        const uint32_t ring = smem_u32(smem + C::ring);
+        const uint64_t qd = make_sdesc_sw128(smem_u32(smem + C::q), 16, 1024);
+        const uint64_t pd = make_sdesc_lines<C::P_LINE>(smem_u32(smem + C::p));
+        constexpr uint32_t IDESC_QK = shape(ROWS) | (FP8 ? 0u : BF16_AB);
+        constexpr uint32_t IDESC_PV = shape(ROWS) | (FP8 ? B_E5M2 : BF16_AB) | A_MN | B_MN;
+        bool ok = true;
+        int slot = 0, segment = 0;
+        uint32_t use = 0;
+        int g_p = 0;                                         // running tile number of P V
+        int sbuf = 0;
+        uint32_t suse = 0;
+        auto wait = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, p.err, abort));
+        };
+        int owner = 0;                                       // the CTA that loads the slot
+        auto next_slot = [&]() {
+            owner = owner + 1 == cs ? 0 : owner + 1;
+            if (++slot == NS) {
+                slot = 0;
+                owner = 0;
+                ++use;
             }
-        }
-        fence_proxy_async_smem();
-        bar_sync(3, THREADS - 32);
-
-        if (warp == 1) {
-            // -------------------------------------------------------------- MMA issue
-            // the whole warp walks the tiles and waits; one elected lane issues
-            const uint32_t ring = smem_u32(smem + C::ring);
-            const uint64_t qd = make_sdesc_sw128(smem_u32(smem + C::q), 16, 1024);
-            bool ok = true;
-            auto wait = [&](int bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, p.err, abort));
-            };
-            auto issue_qk = [&](int t) -> bool {
-                if (t >= 2 && !wait(C::S_FREE + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
-                const uint32_t sb = tmem + TM_S + static_cast<uint32_t>(t & 1) * ROWS;
-                const int seq0 = k_seq(t);
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    const int s = (seq0 + c) % NS;
-                    if (!wait(C::FULL + s, ((seq0 + c) / NS) & 1)) return false;
-                    tc_fence_after_sync();
-                    const uint64_t kd = make_sdesc_sw128(ring + s * SLOT, 16, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {            // 32 bytes of the head dim at a time
-                            const uint64_t off = static_cast<uint64_t>(2 * k);
-                            if constexpr (FP8) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    tc_mma_f8(sb, kd + off,
-                                              qd + off + static_cast<uint64_t>((e * C::Q_TERM + c * C::Q_CHUNK) >> 4),
-                                              IDESC_QK8, (c | k | e) ? 1u : 0u);
-                            } else {
-                                tc_mma_ss(sb, kd + off, qd + off + static_cast<uint64_t>((c * C::Q_CHUNK) >> 4),
-                                          IDESC_QK16, (c | k) ? 1u : 0u);
-                            }
-                        }
-                        tc_commit(&bars[C::EMPTY + s]);
-                        if (c == C::CHUNKS - 1) tc_commit(&bars[C::S_FULL + (t & 1)]);
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
-            auto issue_pv = [&](int t) -> bool {
-                if (!wait(C::P_FULL, t & 1)) return false;
-                const uint64_t pd = FP8 ? make_sdesc_sw64(smem_u32(smem + C::p), 16, 512)
-                                        : make_sdesc_sw128(smem_u32(smem + C::p), 16, 1024);
-                const int seq0 = v_seq(t);
-                constexpr int PER_M = C::CHUNKS / 4;             // slots of 128 head-dim elements
+        };
+        auto free_slot = [&]() {                             // by the issuing lane
+            if (cs > 1) tc_commit_to(&bars[C::EMPTY + slot], owner); else tc_commit(&bars[C::EMPTY + slot]);
+        };
+        auto issue_qk = [&]() -> bool {
+            if (suse > 0 && !wait(C::S_FREE + sbuf, (suse & 1) ^ 1)) return false;
+            const uint32_t sb = tmem + C::TM_S + static_cast<uint32_t>(sbuf * ROWS);
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-                    const int s = (seq0 + m * PER_M) % NS;       // two neighbours in the ring (bf16)
+            for (int c = 0; c < C::SLOTS; ++c) {
+                if (!wait(C::FULL + slot, use & 1)) return false;
+                tc_fence_after_sync();
+                const uint64_t kd = make_sdesc_sw128(ring + slot * SLOT, 16, 1024);
+                const uint64_t qc = qd + static_cast<uint64_t>((c * 2 * C::Q_CHUNK) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < PER_M; ++j)
-                        if (!wait(C::FULL + s + j, ((seq0 + m * PER_M) / NS) & 1)) return false;
-                    tc_fence_after_sync();
-                    const uint64_t vd = make_sdesc_sw128(ring + s * SLOT, SLOT, 1024);
-                    const uint32_t ob = tmem + TM_O + static_cast<uint32_t>(m * ROWS);
-                    if (elect_one()) {
+                    for (int k = 0; k < 8; ++k) {            // 32 bytes of the head dim at a time
+                        const uint64_t a = kd + static_cast<uint64_t>(((k >> 2) * SIDE + (k & 3) * 32) >> 4);
+                        const uint64_t q = qc + static_cast<uint64_t>(((k >> 2) * C::Q_CHUNK + (k & 3) * 32) >> 4);
                         if constexpr (FP8) {
+                            tc_mma_f8(sb, a, q, IDESC_QK, (c | k) ? 1u : 0u);
+                            tc_mma_f8(sb, a, q + static_cast<uint64_t>(C::Q_TERM >> 4), IDESC_QK, 1u);
+                        } else {
+                            tc_mma_ss(sb, a, q, IDESC_QK, (c | k) ? 1u : 0u);
+                        }
+                    }
+                    free_slot();
+                    if (c == C::SLOTS - 1) tc_commit(&bars[C::S_FULL + sbuf]);
+                }
+                __syncwarp();
+                next_slot();
+            }
+            if (++sbuf == NB) {
+                sbuf = 0;
+                ++suse;
+            }
+            return true;
+        };
+        auto issue_pv = [&](bool fresh) -> bool {
+            if (!wait(C::P_FULL, g_p & 1)) return false;
+            const uint32_t acc0 = fresh ? 0u : 1u;
+#pragma unroll 1
+            for (int c = 0; c < C::SLOTS; ++c) {
+                if (!wait(C::FULL + slot, use & 1)) return false;
+                tc_fence_after_sync();
+                const uint64_t vd = make_sdesc_sw128(ring + slot * SLOT, SIDE, 1024);
+                if (elect_one()) {
+                    if constexpr (FP8) {
+                        // two 128-element blocks of the head dim
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
                             for (int k = 0; k < TILE / 32; ++k)
 #pragma unroll
                                 for (int e = 0; e < C::P_TERMS; ++e)
-                                    tc_mma_f8(ob, vd + static_cast<uint64_t>((k * 32 * 128) >> 4),
+                                    tc_mma_f8(tmem + C::TM_O + static_cast<uint32_t>((2 * c + m) * ROWS),
+                                              vd + static_cast<uint64_t>((m * SIDE + k * 32 * 128) >> 4),
                                               pd + static_cast<uint64_t>((e * C::P_TERM + k * 32 * C::P_LINE) >> 4),
-                                              IDESC_PV8, (t | k | e) ? 1u : 0u);
-                        } else {
+                                              IDESC_PV, (k | e) ? 1u : acc0);
+                    } else {
+                        // one block of 128: two boxes of 64 elements
 #pragma unroll
-                            for (int k = 0; k < TILE / 16; ++k)
-                                tc_mma_ss(ob, vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
-                                          pd + static_cast<uint64_t>((k * 16 * C::P_LINE) >> 4), IDESC_PV16,
-                                          (t | k) ? 1u : 0u);
-                        }
-#pragma unroll
-                        for (int j = 0; j < PER_M; ++j) tc_commit(&bars[C::EMPTY + s + j]);
-                        if (m == 3) tc_commit(&bars[C::PV_DONE]);
+                        for (int k = 0; k < TILE / 16; ++k)
+                            tc_mma_ss(tmem + C::TM_O + static_cast<uint32_t>(c * ROWS),
+                                      vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
+                                      pd + static_cast<uint64_t>((k * 16 * C::P_LINE) >> 4), IDESC_PV, k ? 1u : acc0);
                     }
-                    __syncwarp();
+                    free_slot();
+                    if (c == C::SLOTS - 1) tc_commit(&bars[C::PV_DONE]);
                 }
-                return true;
-            };
-            if (n > 0) ok = issue_qk(0);
-            for (int t = 0; t < n && ok; ++t) {
-                if (t + 1 < n) ok = issue_qk(t + 1);
-                if (ok) ok = issue_pv(t);
+                __syncwarp();
+                next_slot();
             }
-            if (elect_one()) tc_commit(&bars[C::DRAIN]);
-            __syncwarp();
-            (void)mbar_wait(&bars[C::DRAIN], 0, p.err);
-        } else {
-            // ---------------------------------------------------------------- softmax
-            const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
-            const int bar = 1 + half;                        // the half's four warps
-            const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-            const int kk = quad * 32 + lane;                 // this thread's key of a tile
-            const int col0 = half * HALF;                    // its rows
-            float m[HALF], l[HALF];
+            ++g_p;
+            return true;
+        };
+        while (ok && walk.next(p)) {
+            const int n = walk.n;
+            if (n == 0) continue;
+            if (!(ok = wait(C::Q_FULL, segment & 1))) break;
+            for (int j = 0; j < n + LOOK && ok; ++j) {
+                if (j < n) ok = issue_qk();
+                if (ok && j >= LOOK) {
+                    // an item's first P V overwrites O: the last one's must have been read
+                    if (j == LOOK && segment > 0) {
+                        ok = wait(C::O_FREE, (segment - 1) & 1);
+                        tc_fence_after_sync();
+                    }
+                    if (ok) ok = issue_pv(j == LOOK);
+                }
+            }
+            ++segment;
+        }
+        if (elect_one()) tc_commit(&bars[C::DRAIN]);
+        __syncwarp();
+        (void)mbar_wait(&bars[C::DRAIN], 0, p.err);
+    } else {
+        // -------------------------------------------------------------------- softmax
+        constexpr int SW = C::SOFTMAX_WARPS;
+        const int sw = warp - 2, quad = warp & 3, grp = sw >> 2;
+        const int bar = 1 + grp;                             // the column group's four warps
+        constexpr int ALL = 7;                               // barrier of all softmax warps
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const int kk = quad * 32 + lane;                     // this thread's key of a tile
+        const int col0 = grp * GW;                           // its rows
+        const int W = p.mask_words, G = p.group;
+        int* s_depth = reinterpret_cast<int*>(smem + C::depth);
+        uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
+        float* s_red = reinterpret_cast<float*>(smem + C::red);
+        float* s_mult = reinterpret_cast<float*>(smem + C::mult);
+        int* s_place = reinterpret_cast<int*>(smem + C::place);
+        int* s_tok = reinterpret_cast<int*>(smem + C::tok);
+        uint8_t* s_seen = smem + C::seen;
+        bool ok = true;
+        int g = 0;                                           // running tile number
+        int sbuf = 0;
+        uint32_t suse = 0;
+        int ring_base = 0;                                   // ring entries of the segments before
+        while (walk.next(p)) {
+            const Band& bd = walk.band;
+            const int n = walk.n, b = walk.b;
+            const int row0 = (walk.grp * cs + rank) * ROWS;
+            const int tok0 = row0 / G;
+            if (n > 0) {
+                // ---- Q: rows as K-major B operand, zeros where there is no row.
+                // The last segment's S^T tiles have been read, so its Q has too.
+                constexpr int PER = ROWS / SW;               // rows of a warp: 4
+                uint4 x[PER][2];
 #pragma unroll
-            for (int i = 0; i < HALF; ++i) {
+                for (int i = 0; i < PER; ++i) {
+                    const int r = sw + i * SW, t = (row0 + r) / G;
+                    const bool real = t < bd.cnt;
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        p.q + ((static_cast<size_t>(b) * p.q_len + (real ? t : 0)) * p.n_q_heads + walk.kvh * G +
+                               (real ? (row0 + r) % G : 0)) * D) + 2 * lane;
+                    x[i][0] = real ? src[0] : make_uint4(0u, 0u, 0u, 0u);
+                    x[i][1] = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
+                }
+                bar_sync(ALL, SW * 32);                      // nobody uses the last segment's tables any more
+                const int toks = max(0, min((row0 + ROWS - 1) / G, p.q_len - 1) - tok0 + 1);
+                if (p.tree_mask) {
+                    // bits at and behind cnt name no token
+                    auto word = [&](int t, int w) -> uint32_t {
+                        const int left = bd.cnt - 32 * w;
+                        const uint32_t m = static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * W + w]);
+                        return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
+                    };
+                    for (int t = tid - 64; t < bd.cnt; t += SW * 32) {
+                        int c = 0;
+                        for (int w = 0; w < W; ++w) c += __popc(word(t, w));
+                        s_depth[t] = c - 1;
+                    }
+                    for (int i = tid - 64; i < toks * W; i += SW * 32) {
+                        const int t = tok0 + i / W, w = i % W;
+                        s_mask[i] = t < bd.cnt ? word(t, w) : 0u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int r = sw + i * SW;
+                    if constexpr (!FP8) {
+                        // this lane's 32 bytes: chunk lane / 4, pieces 2 (lane % 4) and + 1
+                        uint8_t* line = smem + C::q + (lane >> 2) * C::Q_CHUNK + r * 128;
+                        const int c = 2 * (lane & 3);
+                        *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = x[i][0];
+                        *reinterpret_cast<uint4*>(line + (((c + 1) ^ (r & 7)) << 4)) = x[i][1];
+                        if (lane == 0) s_mult[r] = p.scale_log2;
+                    } else {
+                        const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                                               x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                        float amax = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
+                                                     fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+#pragma unroll
+                        for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        // 2^(7 - exponent of amax): the largest element comes to [128, 256)
+                        const int E = (__float_as_uint(amax) >> 23) & 0xff;
+                        const int biased = min(7 + 2 * 127 - E, 254);
+                        const float qs = (amax > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            hi[j] = lo[j] = 0u;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float a = __uint_as_float(w[2 * j + k] << 16) * qs;
+                                const float c = __uint_as_float(w[2 * j + k] & 0xffff0000u) * qs;
+                                float va, vc, ra, rc;
+                                hi[j] |= e4m3_pair(a, c, va, vc) << (16 * k);
+                                lo[j] |= e4m3_pair(a - va, c - vc, ra, rc) << (16 * k);
+                            }
+                        }
+                        // this lane's 16 bytes: chunk lane / 8, piece lane % 8
+                        uint8_t* line = smem + C::q + (lane >> 3) * C::Q_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                        *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(line + C::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (lane == 0) s_mult[r] = p.scale_log2 / qs;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C::Q_FULL]);
+            }
+            // ---- what the rows are (tables of this segment visible to all after it)
+            if (n == 0) bar_sync(ALL, SW * 32);
+            bar_sync(ALL, SW * 32);
+            if (sw < ROWS / 32) {
+                const int r = sw * 32 + lane, t = (row0 + r) / G;
+                const bool real = t < bd.cnt && bd.start + t >= 0;
+                s_place[r] = real ? bd.start + (p.tree_mask && n > 0 ? s_depth[t] : t) : 0;
+                s_tok[r] = real ? t : -1;
+            }
+            bar_sync(ALL, SW * 32);
+
+            float m[GW], l[GW];
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {
                 m[i] = -INFINITY;
                 l[i] = 0.f;
             }
-            bool ok = true;
-            for (int t = 0; t < n; ++t) {
-                const int key0 = bd.key0(t), key = key0 + kk;
-                ok = ok && wait_or_abort(&bars[C::S_FULL + (t & 1)], (t >> 1) & 1, p.err, abort);
+            bool out = false;
+            bool fresh = true;                               // some row may not have a reference yet
+            for (int t = 0; t < n; ++t, ++g) {
+                const int key0 = bd.key0(walk.first + t), key = key0 + kk;
+                ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
-                float x[HALF];
+                float x[GW];
                 {
-                    uint32_t raw[32];
-                    tmem_ld32(tmem + lanes + TM_S + static_cast<uint32_t>((t & 1) * ROWS + col0), raw);
+                    uint32_t raw[GW];
+                    pair::tmem_ld16(tmem + lanes + C::TM_S + static_cast<uint32_t>(sbuf * ROWS + col0), raw);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i) x[i] = __uint_as_float(raw[i]);
+                    for (int i = 0; i < GW; ++i) x[i] = __uint_as_float(raw[i]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[C::S_FREE + (t & 1)]);
+                if (lane == 0) mbar_arrive(&bars[C::S_FREE + sbuf]);
+                if (++sbuf == NB) {
+                    sbuf = 0;
+                    ++suse;
+                }
+                // log2 units, less the rows' references
 #pragma unroll
-                for (int i = 0; i < HALF; i += 4) {
+                for (int i = 0; i < GW; i += 4) {
                     const float4 f = *reinterpret_cast<const float4*>(&s_mult[col0 + i]);
-                    x[i] *= f.x;
-                    x[i + 1] *= f.y;
-                    x[i + 2] *= f.z;
-                    x[i + 3] *= f.w;
+                    x[i] = fmaf(x[i], f.x, fresh && m[i] == -INFINITY ? 0.f : -m[i]);
+                    x[i + 1] = fmaf(x[i + 1], f.y, fresh && m[i + 1] == -INFINITY ? 0.f : -m[i + 1]);
+                    x[i + 2] = fmaf(x[i + 2], f.z, fresh && m[i + 2] == -INFINITY ? 0.f : -m[i + 2]);
+                    x[i + 3] = fmaf(x[i + 3], f.w, fresh && m[i + 3] == -INFINITY ? 0.f : -m[i + 3]);
                 }
                 // a tile of cached keys inside every row's window needs no mask
-                const bool whole = key0 + TILE <= bd.start &&
+                const bool whole = key0 + TILE <= min(bd.start, bd.hi) &&
                                    (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
-                // keys that no row sees: their V rows may hold anything
-                bool live = true;
+                bool seen = true;                            // by some row of the group
                 if (!whole) {
-                    live = key < bd.hi && (key >= bd.lo || key < bd.sink_end);
+                    const bool live = key < bd.hi && (key >= bd.lo || key < bd.sink_end);
                     const int c = key - bd.start;
-                    const int kp = c < 0 || !p.tree_mask ? key : bd.start + s_depth[min(c, MAX_NODES - 1)];
+                    seen = false;
+                    const int kp = c < 0 || !p.tree_mask ? key : bd.start + s_depth[max(0, min(c, bd.cnt - 1))];
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i) {
+                    for (int i = 0; i < GW; ++i) {
                         const int tk = s_tok[col0 + i], pl = s_place[col0 + i];
                         bool see = live && tk >= 0;
                         if (see && c >= 0)
                             see = p.tree_mask ? (s_mask[(tk - tok0) * W + (c >> 5)] >> (c & 31)) & 1u : c <= tk;
                         if (p.window > 0) see = see && (kp > pl - p.window || kp < p.n_sinks);
                         x[i] = see ? x[i] : -INFINITY;
+                        seen = seen || see;
                     }
                 }
-                bool over = !ok;
+                float high = x[0];
 #pragma unroll
-                for (int i = 0; i < HALF; ++i) over = over || x[i] > m[i] + C::THR;
-                bool pv_waited = t == 0;
-                if (bar_or(bar, 128, over)) {
+                for (int i = 1; i < GW; ++i) high = fmaxf(high, x[i]);
+                bool pv_waited = g == 0;
+                if (bar_or(bar, 128, high > C::THR || fresh || !ok)) {
                     if (!(ok = pair::bar_and(bar, 128, ok))) break;
-                    float v[HALF];
+                    float v[GW];
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i) v[i] = x[i];
+                    for (int i = 0; i < GW; ++i) v[i] = x[i];
                     const float mx = reduce_columns(v, [](float a, float c) { return fmaxf(a, c); });
-                    s_red[quad * ROWS + col0 + lane] = mx;
+                    if (lane < GW) s_red[quad * ROWS + col0 + lane] = mx;
                     bar_sync(bar, 128);
-                    const float top = fmaxf(fmaxf(s_red[col0 + lane], s_red[ROWS + col0 + lane]),
-                                            fmaxf(s_red[2 * ROWS + col0 + lane], s_red[3 * ROWS + col0 + lane]));
+                    const int cl = col0 + (lane & (GW - 1));
+                    const float top = fmaxf(fmaxf(s_red[cl], s_red[ROWS + cl]),
+                                            fmaxf(s_red[2 * ROWS + cl], s_red[3 * ROWS + cl]));
                     float mine = 1.f;                        // lane i: the factor of row col0 + i
+                    fresh = false;
 #pragma unroll
-                    for (int i = 0; i < HALF; ++i) {
-                        const float mn = fmaxf(m[i], __shfl_sync(0xffffffffu, top, i));
-                        const float a = mn == -INFINITY ? 1.f : fast_exp2(m[i] - mn);
-                        l[i] *= a;
-                        m[i] = mn;
+                    for (int i = 0; i < GW; ++i) {
+                        // growth over the reference (over 0 where there was none)
+                        const float up = __shfl_sync(0xffffffffu, top, i);
+                        float a = 1.f;
+                        if (m[i] == -INFINITY) {
+                            if (up > -INFINITY) {
+                                m[i] = up;
+                                x[i] -= up;
+                            } else {
+                                fresh = true;
+                            }
+                        } else if (up > 0.f) {
+                            a = fast_exp2(-up);
+                            m[i] += up;
+                            x[i] -= up;
+                            l[i] *= a;
+                        }
                         mine = lane == i ? a : mine;
                     }
                     if (t > 0) {
                         // O is at rest once P V of the last tile has completed
-                        ok = wait_or_abort(&bars[C::PV_DONE], (t - 1) & 1, p.err, abort);
+                        ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
                         ok = __all_sync(0xffffffffu, ok);
                         pv_waited = true;
                         tc_fence_after_sync();
+                        if (__any_sync(0xffffffffu, mine != 1.f)) {
 #pragma unroll 1
-                        for (int o = 0; o < 4; ++o) {
-                            const uint32_t ta = tmem + lanes + TM_O + static_cast<uint32_t>(o * ROWS + col0);
-                            uint32_t r[32];
-                            tmem_ld32(ta, r);
-                            tmem_ld_wait();
+                            for (int o = 0; o < 4; ++o) {
+                                const uint32_t ta = tmem + lanes + C::TM_O + static_cast<uint32_t>(o * ROWS + col0);
+                                uint32_t r[GW];
+                                pair::tmem_ld16(ta, r);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < HALF; ++i) 
-                                r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, mine, i));
-                            tmem_st32(ta, r);
+                                for (int i = 0; i < GW; ++i)
+                                    r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, mine, i));
+                                pair::tmem_st16(ta, r);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
                     }
                     bar_sync(bar, 128);                      // s_red is free again
                 }
 #pragma unroll
-                for (int i = 0; i < HALF; ++i) {
-                    x[i] = fast_exp2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                for (int i = 0; i < GW; ++i) {
+                    x[i] = fast_exp2(x[i]);
                     l[i] += x[i];
                 }
                 // P's buffer is free, and V of this tile will be read, after P V of the last tile
                 if (!pv_waited) {
-                    ok = wait_or_abort(&bars[C::PV_DONE], (t - 1) & 1, p.err, abort);
+                    ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
                     ok = __all_sync(0xffffffffu, ok);
                 }
+                uint8_t* line = smem + C::p + kk * C::P_LINE;
                 if constexpr (FP8) {
-                    uint8_t* line = smem + C::p + kk * C::P_LINE;
+                    uint32_t w[3][4] = {};
 #pragma unroll
-                    for (int c = 0; c < HALF / 16; ++c) {
-                        uint32_t w[3][4] = {};
+                    for (int j = 0; j < 8; ++j) {
+                        float a = x[2 * j] * C::P_SCALE, d = x[2 * j + 1] * C::P_SCALE;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float a = x[16 * c + 2 * j] * C::P_SCALE, d = x[16 * c + 2 * j + 1] * C::P_SCALE;
-#pragma unroll
-                            for (int e = 0; e < 3; ++e) {
-                                float va, vd;
-                                w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
-                                a -= va;
-                                d -= vd;
-                            }
+                        for (int e = 0; e < 3; ++e) {
+                            float va, vd;
+                            w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
+                            a -= va;
+                            d -= vd;
                         }
-                        const int piece = ((col0 / 16 + c) ^ ((kk >> 1) & 3)) << 4;
-#pragma unroll
-                        for (int e = 0; e < 3; ++e)
-                            *reinterpret_cast<uint4*>(line + e * C::P_TERM + piece) =
-                                make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
                     }
-                } else {
-                    uint8_t* line = smem + C::p + kk * C::P_LINE;
+                    const int piece = line_piece<C::P_LINE>(kk, grp);
 #pragma unroll
-                    for (int c = 0; c < HALF / 8; ++c)
-                        *reinterpret_cast<uint4*>(line + (((col0 / 8 + c) ^ (kk & 7)) << 4)) =
+                    for (int e = 0; e < 3; ++e)
+                        *reinterpret_cast<uint4*>(line + e * C::P_TERM + piece) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < GW / 8; ++c)
+                        *reinterpret_cast<uint4*>(line + line_piece<C::P_LINE>(kk, grp * (GW / 8) + c)) =
                             make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
                                        pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
                 }
-                // P = 0 must not meet stale or poisoned V rows: each half's
-                // threads clear their key's row in half of the tile's slots.
-                // Before V(t) a slot held K(t + 1): S^T of that tile says that
-                // it has been read, so the wait for V(t) is one phase ahead
-                // at most.
-                if (!whole && pair::bar_and(bar, 128, live) == false) {
-                    if (t + 1 < n) {
-                        const bool got = wait_or_abort(&bars[C::S_FULL + ((t + 1) & 1)], ((t + 1) >> 1) & 1, p.err, abort);
+                // P = 0 must not meet the V row of a key that no row sees: it
+                // may hold anything.  The column groups share out the tile's
+                // slots and clear such a key's row there.  Every ring entry
+                // before V(t) has been read once the last S^T tile before it
+                // is complete (and P V of t - 1 is), so the wait for a slot is
+                // one phase ahead at most.
+                bool clear = false;
+                if (!whole) {
+                    s_seen[grp * TILE + kk] = seen;
+                    if (!(ok = pair::bar_and(ALL, SW * 32, ok))) {
+                        out = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < C::GROUPS; ++i) seen = seen || s_seen[i * TILE + kk];
+                    clear = !pair::bar_and(ALL, SW * 32, seen);
+                }
+                if (clear) {
+                    const int ahead = min(t + LOOK, n - 1);
+                    for (int a = t + 1; a <= ahead; ++a) {
+                        const int gs = g + a - t;
+                        const bool got = wait_or_abort(&bars[C::S_FULL + gs % NB], (gs / NB) & 1, p.err, abort);
                         ok = __all_sync(0xffffffffu, got) && ok;
                     }
-                    const int seq0 = v_seq(t) + half * (C::CHUNKS / 2);
+                    const int seq0 = ring_base + (ahead + 1 + t) * C::SLOTS;
 #pragma unroll 1
-                    for (int j = 0; j < C::CHUNKS / 2; ++j) {
-                        const int s = (seq0 + j) % NS;
-                        const bool got = wait_or_abort(&bars[C::FULL + s], ((seq0 + j) / NS) & 1, p.err, abort);
+                    for (int c = grp; c < C::SLOTS; c += C::GROUPS) {
+                        const int s = (seq0 + c) % NS;
+                        const bool got = wait_or_abort(&bars[C::FULL + s], ((seq0 + c) / NS) & 1, p.err, abort);
                         ok = __all_sync(0xffffffffu, got) && ok;
-                        if (got && !live) {
-                            uint4* line = reinterpret_cast<uint4*>(smem + C::ring + s * SLOT + kk * 128);
+                        if (got && !seen) {
+                            uint4* v = reinterpret_cast<uint4*>(smem + C::ring + s * SLOT + kk * 128);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) line[e] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < 8; ++e) v[e] = v[SIDE / 16 + e] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                 }
@@ -671,95 +941,207 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C::P_FULL]);
             }
-            if (n > 0 && ok)
-                ok = wait_or_abort(&bars[C::PV_DONE], (n - 1) & 1, p.err, abort);
-            ok = pair::bar_and(bar, 128, ok);
+            ring_base += 2 * n * C::SLOTS;
+            if (n > 0 && ok) ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+            // all go on or all stop (here or at a vote inside a tile): no warp
+            // may wait at a barrier for one that has left
+            if (out || !(ok = pair::bar_and(ALL, SW * 32, ok))) break;
             tc_fence_after_sync();
             // ---- row sums: lanes, then the four quadrants' warps
             const float part = reduce_columns(l, [](float a, float c) { return a + c; });
-            s_red[quad * ROWS + col0 + lane] = part;
+            if (lane < GW) s_red[quad * ROWS + col0 + lane] = part;
             bar_sync(bar, 128);
-            const float sum = (s_red[col0 + lane] + s_red[ROWS + col0 + lane]) +
-                              (s_red[2 * ROWS + col0 + lane] + s_red[3 * ROWS + col0 + lane]);
-            float top = -INFINITY;                           // lane i: row col0 + i
+            const int cl = col0 + (lane & (GW - 1));
+            const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
+            float top = -INFINITY;                           // lane i: row col0 + i % GW
 #pragma unroll
-            for (int i = 0; i < HALF; ++i) top = lane == i ? m[i] : top;
-            const int my_row = row0 + col0 + lane, my_tok = my_row / G;
+            for (int i = 0; i < GW; ++i) top = (lane & (GW - 1)) == i ? m[i] : top;
+            const int my_row = row0 + cl, my_tok = my_row / G;
             const bool mine = my_tok < p.q_len;
-            const bool some = ok && s_tok[col0 + lane] >= 0 && top != -INFINITY;
-            const size_t my_out = (static_cast<size_t>(b) * p.q_len + my_tok) * p.n_q_heads + kvh * G + my_row % G;
+            const bool some = s_tok[cl] >= 0 && top != -INFINITY;
+            const size_t my_out = (static_cast<size_t>(b) * p.q_len + my_tok) * p.n_q_heads + walk.kvh * G + my_row % G;
             const size_t S = static_cast<size_t>(p.num_splits);
+            const bool direct = walk.count == 1;
             // O / sum where this is the whole row, else the unnormalised partial
             const float unit = p.o_scale * (1.f / C::P_SCALE);
-            const float factor = !some ? 0.f : p.num_splits == 1 ? unit / sum : unit;
-            if (quad == 0 && mine) {
-                if (p.num_splits == 1) {
+            const float factor = !some ? 0.f : direct ? unit / sum : unit;
+            if (quad == 0 && lane < GW && mine) {
+                if (direct) {
                     if (p.lse) p.lse[my_out] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
                 } else {
-                    p.ws_ml[(my_out * S + split) * 2] = some ? top : -INFINITY;
-                    p.ws_ml[(my_out * S + split) * 2 + 1] = some ? sum : 0.f;
+                    float* ml = p.ws_ml + (my_out * S + walk.index) * 2;
+                    ml[0] = some ? top : -INFINITY;
+                    ml[1] = some ? sum : 0.f;
                 }
             }
+            if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0 && rank == 0)
+                p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
 #pragma unroll 1
             for (int o = 0; o < 4; ++o) {
-                uint32_t r[32];
+                uint32_t r[GW];
                 if (n > 0) {
-                    tmem_ld32(tmem + lanes + TM_O + static_cast<uint32_t>(o * ROWS + col0), r);
+                    pair::tmem_ld16(tmem + lanes + C::TM_O + static_cast<uint32_t>(o * ROWS + col0), r);
                     tmem_ld_wait();
+                }
+                if (o == 3) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0 && n > 0) mbar_arrive(&bars[C::O_FREE]);
                 }
                 const int d = o * 128 + kk;
 #pragma unroll
-                for (int i = 0; i < HALF; ++i) {
+                for (int i = 0; i < GW; ++i) {
                     const float f = __shfl_sync(0xffffffffu, factor, i);
                     const size_t row = __shfl_sync(0xffffffffu, my_out, i);
                     const bool there = __shfl_sync(0xffffffffu, mine ? 1 : 0, i);
                     if (!there) continue;
                     const float val = f != 0.f ? __uint_as_float(r[i]) * f : 0.f;
-                    if (p.num_splits == 1)
+                    if (direct)
                         p.out[row * D + d] = __float2bfloat16_rn(val);
                     else
-                        p.ws_o[(row * S + split) * D + d] = val;
+                        p.ws_o[(row * S + walk.index) * D + d] = val;
                 }
             }
-            tc_fence_before_sync();
         }
     }
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, TM_COLS);
+    // all threads of all CTAs: no copy or arrival may reach a CTA that has gone
+    if (cs > 1) cluster_sync_all(); else __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::TM_COLS);
 }
 
-template <bool FP8>
+// One block per row that was left in segments: combines the segments' (O, m,
+// l) -- M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s.
+constexpr int MERGE_THREADS = 128;       // a quad of columns each
+
+__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p, int group_rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h = blockIdx.x, bt = blockIdx.y;
+    const int b = bt / p.q_len, t = bt - b * p.q_len;
+    const int grp = (t * p.group + h % p.group) / group_rows;
+    const int S = p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group];
+    if (S <= 1) return;
+    const size_t row = static_cast<size_t>(bt) * p.n_q_heads + h;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.num_splits;
+    const float* ob = p.ws_o + row * p.num_splits * D + threadIdx.x * 4;
+    float M = -INFINITY;
+    for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll 8
+        for (int s = 0; s < S; ++s) {
+            const float2 v = ml[s];
+            const float4 o = *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D);
+            const float w = fast_exp2(v.x - M);
+            L = fmaf(w, v.y, L);
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    uint2 packed;
+    packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + row * D + threadIdx.x * 4) = packed;
+    if (p.lse && threadIdx.x == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+// Resident clusters of `cs` CTAs of one kernel variant on the current device
+// (0 when the query fails), asked once per device.
+template <bool FP8, int ROWS>
+int resident_clusters(int cs) {
+    static std::mutex mu;
+    static int known[64][MAX_CLUSTER + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = known[dev][cs];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(cs);
+        cfg.blockDim = dim3(Cfg<FP8, ROWS>::THREADS);
+        cfg.dynamicSmemBytes = Cfg<FP8, ROWS>::total + 1024;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cs;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int got = 0;
+        if (cudaFuncSetAttribute(tree_kernel<FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<FP8, ROWS>::total + 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&got, tree_kernel<FP8, ROWS>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        n = got;
+    }
+    return n;
+}
+
+template <bool FP8, int ROWS>
 cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
-    const int smem = Cfg<FP8>::total + 1024;
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int clusters = resident_clusters<FP8, ROWS>(p.cluster);
+    if (clusters < 1) return cudaErrorLaunchOutOfResources;
+    const int smem = Cfg<FP8, ROWS>::total + 1024;
+    cudaError_t e = cudaFuncSetAttribute(tree_kernel<FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int row_tiles = (p.q_len * p.group + ROWS - 1) / ROWS;
-    const dim3 grid(row_tiles * p.num_splits, p.n_kv_heads, p.batch);
-    tree_kernel<FP8><<<grid, THREADS, smem, stream>>>(tmk, tmv, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    const long long units = static_cast<long long>(p.batch) * p.row_groups * p.n_kv_heads *
+                            (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(units < clusters ? units : clusters) * p.cluster);
+    cfg.blockDim = dim3(Cfg<FP8, ROWS>::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, tree_kernel<FP8, ROWS>, tmk, tmv, p);
+    if (e != cudaSuccess || p.num_splits == 1) return e;
+    // the merge may be scheduled while the tiles are walked (it waits for them)
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len);
+    cfg.blockDim = dim3(MERGE_THREADS);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel, p, ROWS * p.cluster);
 }
 
 }  // namespace tree
 
 int tree_max_nodes() { return tree::MAX_NODES; }
-int tree_rows() { return tree::ROWS; }
 int tree_tile() { return tree::TILE; }
+
+// 32-row CTAs where all rows of a KV head fit one, else 64-row CTAs, the row
+// tiles of a KV head in clusters of at most 4 (as even as possible).
+TreeShape tree_shape(int q_len, int group) {
+    const long long rows = static_cast<long long>(q_len) * group;
+    TreeShape s;
+    s.rows = rows <= 32 ? 32 : 64;
+    const long long tiles = (rows + s.rows - 1) / s.rows;
+    const long long groups = (tiles + 3) / 4;
+    s.cluster = static_cast<int>((tiles + groups - 1) / groups);
+    s.groups = static_cast<int>((tiles + s.cluster - 1) / s.cluster);
+    return s;
+}
 
 cudaError_t launch_decode_tree(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
                                cudaStream_t stream) {
-    const cudaError_t e = fp8 ? tree::launch<true>(tmk, tmv, p, stream) : tree::launch<false>(tmk, tmv, p, stream);
-    if (e != cudaSuccess || p.num_splits == 1) return e;
-    DecodeParams m;
-    memset(&m, 0, sizeof m);
-    m.ws_o = p.ws_o;
-    m.ws_ml = p.ws_ml;
-    m.out = p.out;
-    m.lse = p.lse;
-    m.batch = p.batch;
-    m.q_len = p.q_len;
-    m.n_q_heads = p.n_q_heads;
-    m.num_splits = p.num_splits;
-    return launch_decode_merge(m, stream);
+    if (p.rows == 32)
+        return fp8 ? tree::launch<true, 32>(tmk, tmv, p, stream) : tree::launch<false, 32>(tmk, tmv, p, stream);
+    return fp8 ? tree::launch<true, 64>(tmk, tmv, p, stream) : tree::launch<false, 64>(tmk, tmv, p, stream);
 }
 
 }  // namespace fa512

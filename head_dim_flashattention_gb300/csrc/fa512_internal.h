@@ -52,9 +52,6 @@ int decode_fp8_ctas_per_sm();
 bool decode_merge_sliced(long long rows);
 cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const DecodeParams& p, cudaStream_t stream);
-// Combines the (O, m, l) partials of [batch, q_len, n_q_heads, num_splits]
-// (only these sizes, ws_o, ws_ml, out and lse of p are read).
-cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
 
 // Drafted tokens (a tree or a run of them) over a paged cache.
 struct TreeParams {
@@ -67,21 +64,29 @@ struct TreeParams {
     const int32_t* tree_mask;      // [batch, q_len, mask_words] or null: a run of tokens
     float* ws_o;                   // [batch, q_len, n_q_heads, num_splits, 512] unnormalised O
     float* ws_ml;                  // [batch, q_len, n_q_heads, num_splits, 2]
+    int32_t* ws_count;             // [batch, row_groups, n_kv_heads] segments of each item
     __nv_bfloat16* out;            // [batch, q_len, n_q_heads, 512]
     float* lse;                    // [batch, q_len, n_q_heads] or null
     int batch, q_len, n_q_heads, n_kv_heads, group, mask_words;
+    int rows, cluster, row_groups; // TreeShape
+    int max_tiles;                 // most key tiles of an item
     int page_size, num_pages, max_pages_per_seq, len_cap;
     int window, n_sinks;
-    int num_splits;
+    int num_splits;                // most segments of an item; 1: no partials
     float scale_log2;              // scale * log2(e) (E4M3 cache: * k_scale)
     float o_scale;                 // E4M3 cache: v_scale; else 1
     unsigned* err;
 };
 
 int tree_max_nodes();              // most tokens a tree_mask covers
-int tree_rows();                   // rows that share one pass over the keys
 int tree_tile();                   // keys per tile
-// Both maps: {128 bytes of the head dim, 1 KV head, min(page_size, 128) positions} boxes, 128-byte swizzle.
+struct TreeShape {
+    int rows;                      // rows of a CTA
+    int cluster;                   // CTAs that share their keys
+    int groups;                    // row groups (clusters) of a KV head
+};
+TreeShape tree_shape(int q_len, int group);
+// Both maps: {128 bytes of the head dim, 1 KV head, min(page_size, tree_tile()) positions} boxes, 128-byte swizzle.
 cudaError_t launch_decode_tree(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
                                cudaStream_t stream);
 
