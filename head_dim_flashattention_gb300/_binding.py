@@ -131,8 +131,16 @@ def _dptr(t: torch.Tensor | None, name: str, dtype=None) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+# The current stream's handle without building a Stream object (2.9 us of a
+# call's host time against 0.1 us on the GB300's host), and the device.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream(stream, dev: int | None = None) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -437,19 +445,39 @@ def fa512_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     return out, lse
 
 
-def _shape(t, name: str, shape) -> None:
-    """Refuses a tensor of another shape (an argument that the kernels index by it)."""
-    if t is not None and (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape)):
-        raise Fa512Error(1, "%s must have shape %s" % (name, tuple(shape)))
+def _device(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device that ``t`` and all other tensors of a call must be on: the current one, on which the
+    library works."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise Fa512Error(1, "%s must be a CUDA tensor" % name)
+    dev = t.get_device()
+    if dev != _current_device():
+        raise Fa512Error(1, "%s is not on the current device" % name)
+    return dev
 
 
-def _one_device(*tensors) -> None:
-    """The library works on the current device: refuses tensors of another one."""
-    devices = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda}
-    if len(devices) > 1:
-        raise Fa512Error(1, "the tensors are on different devices")
-    if devices and devices.pop().index != torch.cuda.current_device():
-        raise Fa512Error(1, "the tensors are not on the current device")
+def _arg(t: torch.Tensor | None, name: str, dtype, dev: int, shape=None) -> int | None:
+    """Device pointer of a contiguous tensor of this type (one of these types), device and shape; None of None."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()
+            and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype))
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise Fa512Error(1, "%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise Fa512Error(1, "%s is on another device than the other tensors" % name)
+    if not t.is_contiguous():
+        raise Fa512Error(1, "%s must be contiguous" % name)
+    if shape is not None and t.shape != shape:
+        raise Fa512Error(1, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise Fa512Error(1, "%s must be %s, got %s" % (name, dtype, t.dtype))
+
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_CACHE = (torch.bfloat16,) + _E4M3
 
 
 def _used_on(stream, *tensors) -> None:
@@ -478,46 +506,43 @@ def fa512_decode_workspace_bytes_tree(batch: int, q_len: int, n_q_heads: int, n_
 
 def _decode_tree(fp8, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, lse, q_lens, k_scale,
                  v_scale, max_kv_len, scale, window, n_sinks, num_splits, workspace, return_lse, stream):
-    if q.dim() != 4 or k_pages.dim() != 4 or k_pages.shape != v_pages.shape or q.shape[3] != HEAD_DIM \
+    if q.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2 or q.shape[3] != HEAD_DIM \
             or k_pages.shape[3] != HEAD_DIM:
-        raise Fa512Error(1, "q must be [batch, q_len, heads, 512], pages [n, page, heads, 512]")
+        raise Fa512Error(1, "q must be [batch, q_len, heads, 512], pages [n, page, heads, 512], page_table "
+                            "[batch, max_pages_per_seq]")
     bsz, qlen, hq, d = q.shape
     npages, psz, hk, _ = k_pages.shape
-    if page_table.dim() != 2 or page_table.shape[0] != bsz:
-        raise Fa512Error(1, "page_table must be [batch, max_pages_per_seq]")
     mpps = page_table.shape[1]
-    _shape(kv_lens, "kv_lens", (bsz,))
-    _shape(q_lens, "q_lens", (bsz,))
-    _shape(tree_mask, "tree_mask", (bsz, qlen, (qlen + 31) // 32))
-    _shape(out, "out", q.shape)
-    _shape(lse, "lse", q.shape[:3])
-    _one_device(q, k_pages, v_pages, page_table, kv_lens, q_lens, tree_mask, out, lse, workspace)
+    dev = _device(q, "q")
+    rows = (bsz, qlen, hq)
     if max_kv_len is None:
         max_kv_len = mpps * psz
     if scale is None:
         scale = d ** -0.5
-    lib = load_library()
+    lib = _lib or load_library()
     mine = []
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(rows + (d,), dtype=_BF16, device=q.device)
         mine.append(out)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = torch.empty(rows, dtype=_F32, device=q.device)
         mine.append(lse)
     if workspace is None:
-        need = int(lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, int(max_kv_len), int(window),
-                                                         int(n_sinks), int(num_splits)))
+        need = lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, int(max_kv_len), int(window),
+                                                     int(n_sinks), int(num_splits))
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         mine.append(workspace)
     ws_bytes = workspace.numel() * workspace.element_size()
-    pages = _e4m3_bytes if fp8 else lambda t, name: _dptr(t, name, torch.bfloat16)
-    head = (_dptr(q, "q", torch.bfloat16), pages(k_pages, "k_pages"), pages(v_pages, "v_pages"),
-            _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
-            _dptr(q_lens, "q_lens", torch.int32), _dptr(tree_mask, "tree_mask", torch.int32),
-            _dptr(out, "out", torch.bfloat16), _dptr(lse, "lse", torch.float32), bsz, qlen, hq, hk, psz,
-            npages, mpps, int(max_kv_len), float(scale))
-    tail = (int(window), int(n_sinks), int(num_splits), _dptr(workspace, "workspace"), ws_bytes,
-            _stream(stream))
+    kind = _E4M3 if fp8 else _BF16
+    head = (_arg(q, "q", _BF16, dev), _arg(k_pages, "k_pages", kind, dev),
+            _arg(v_pages, "v_pages", kind, dev, k_pages.shape),
+            _arg(page_table, "page_table", _I32, dev, (bsz, mpps)), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
+            _arg(q_lens, "q_lens", _I32, dev, (bsz,)),
+            _arg(tree_mask, "tree_mask", _I32, dev, (bsz, qlen, (qlen + 31) // 32)),
+            _arg(out, "out", _BF16, dev, rows + (d,)), _arg(lse, "lse", _F32, dev, rows), bsz, qlen, hq, hk,
+            psz, npages, mpps, int(max_kv_len), float(scale))
+    tail = (int(window), int(n_sinks), int(num_splits), _arg(workspace, "workspace", workspace.dtype, dev),
+            ws_bytes, _stream(stream, dev))
     if fp8:
         _check(lib.fa512_decode_paged_tree_fp8(*head, float(k_scale), float(v_scale), *tail))
     else:
@@ -564,36 +589,34 @@ def fa512_decode_paged_tree_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages:
                         stream)
 
 
-def _new_rows(t: torch.Tensor, name: str):
+def _new_rows(t: torch.Tensor, name: str, dev: int, shape):
     """(pointer, batch stride, token stride) of new rows whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
-        raise Fa512Error(1, "%s must be a bf16 CUDA tensor" % name)
-    if t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not _BF16 or t.shape != shape:
+        raise Fa512Error(1, "%s must be a bf16 tensor of shape %s on the pages' device" % (name, tuple(shape)))
+    b, n, h, d = t.stride()
+    if d != 1 or (h != HEAD_DIM and shape[2] > 1):
         raise Fa512Error(1, "the heads of a token of %s must be contiguous" % name)
     # the stride of a dimension of one entry says nothing
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), b if shape[0] > 1 else 0, n if shape[1] > 1 else 0
 
 
 def _append(fp8, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale, stream):
-    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_pages.dim() != 4 \
-            or k_pages.shape != v_pages.shape or tuple(k_new.shape[2:]) != tuple(k_pages.shape[2:]) \
-            or k_pages.shape[3] != HEAD_DIM:
-        raise Fa512Error(1, "k_new, v_new must be [batch, q_len, heads, 512], pages [n, page, heads, 512]")
-    bsz, qlen = k_new.shape[:2]
+    if k_new.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2 or k_pages.shape[3] != HEAD_DIM:
+        raise Fa512Error(1, "k_new, v_new must be [batch, q_len, heads, 512], pages [n, page, heads, 512], "
+                            "page_table [batch, max_pages_per_seq]")
     npages, psz, hk, _ = k_pages.shape
-    if page_table.dim() != 2 or page_table.shape[0] != bsz:
-        raise Fa512Error(1, "page_table must be [batch, max_pages_per_seq]")
-    _shape(kv_lens, "kv_lens", (bsz,))
-    _shape(q_lens, "q_lens", (bsz,))
-    _one_device(k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens)
-    kp, kb, kt = _new_rows(k_new, "k_new")
-    vp, vb, vt = _new_rows(v_new, "v_new")
-    pages = _e4m3_bytes if fp8 else lambda t, name: _dptr(t, name, torch.bfloat16)
-    head = (kp, vp, kb, kt, vb, vt, pages(k_pages, "k_pages"), pages(v_pages, "v_pages"),
-            _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
-            _dptr(q_lens, "q_lens", torch.int32))
-    tail = (bsz, qlen, hk, psz, npages, page_table.shape[1], _stream(stream))
-    lib = load_library()
+    bsz, mpps = page_table.shape
+    qlen = k_new.shape[1]
+    shape = (bsz, qlen, hk, HEAD_DIM)
+    dev = _device(k_pages, "k_pages")
+    kp, kb, kt = _new_rows(k_new, "k_new", dev, shape)
+    vp, vb, vt = _new_rows(v_new, "v_new", dev, shape)
+    kind = _E4M3 if fp8 else _BF16
+    head = (kp, vp, kb, kt, vb, vt, _arg(k_pages, "k_pages", kind, dev),
+            _arg(v_pages, "v_pages", kind, dev, k_pages.shape), _arg(page_table, "page_table", _I32, dev),
+            _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)), _arg(q_lens, "q_lens", _I32, dev, (bsz,)))
+    tail = (bsz, qlen, hk, psz, npages, mpps, _stream(stream, dev))
+    lib = _lib or load_library()
     if fp8:
         _check(lib.fa512_cache_append_fp8(*head, float(k_scale), float(v_scale), *tail))
     else:
@@ -626,16 +649,14 @@ def fa512_cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: to
 
 
 def _whole_cache(k_pages, v_pages):
-    """(k pointer, v pointer, layers, pages, page size, heads, bytes) of a cache of one or several layers."""
-    if k_pages.dim() not in (4, 5) or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype \
-            or k_pages.shape[-1] != HEAD_DIM:
+    """(device, k pointer, v pointer, layers, pages, page size, heads, bytes) of a cache of one or several layers."""
+    if k_pages.dim() not in (4, 5) or k_pages.dtype is not v_pages.dtype or k_pages.shape[-1] != HEAD_DIM:
         raise Fa512Error(1, "pages must be [(layers,) n, page, heads, 512], k_pages like v_pages")
-    if k_pages.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
-        raise Fa512Error(1, "pages must be bf16, uint8 or float8_e4m3fn, got %s" % k_pages.dtype)
-    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-    npages, psz, hk, _ = k_pages.shape[-4:]
-    return (_dptr(k_pages, "k_pages"), _dptr(v_pages, "v_pages"), layers, npages, psz, hk,
-            k_pages.element_size())
+    dev = _device(k_pages, "k_pages")
+    shape = k_pages.shape
+    layers = shape[0] if len(shape) == 5 else 1
+    return (dev, _arg(k_pages, "k_pages", _CACHE, dev), _arg(v_pages, "v_pages", _CACHE, dev, shape), layers,
+            shape[-4], shape[-3], shape[-2], k_pages.element_size())
 
 
 def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -650,23 +671,21 @@ def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table
     sequence (or ``q_lens`` [batch] int32, each at most q_len), which kv_lens
     counts.
     """
-    kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
-    if page_table.dim() != 2 or accepted.dim() != 2 or accepted.shape[0] != page_table.shape[0]:
+    dev, kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
+    if page_table.dim() != 2 or accepted.dim() != 2:
         raise Fa512Error(1, "page_table must be [batch, pages], accepted [batch, max_accepted]")
     bsz, mpps = page_table.shape
-    for t, name in ((kv_lens, "kv_lens"), (n_accepted, "n_accepted"), (new_kv_lens, "new_kv_lens"),
-                    (q_lens, "q_lens")):
-        _shape(t, name, (bsz,))
-    _one_device(k_pages, v_pages, page_table, kv_lens, accepted, n_accepted, new_kv_lens, q_lens)
+    most = accepted.shape[1]
+    one = (bsz,)
     mine = []
     if new_kv_lens is None:
-        new_kv_lens = torch.empty((bsz,), dtype=torch.int32, device=kv_lens.device)
+        new_kv_lens = torch.empty(one, dtype=_I32, device=k_pages.device)
         mine.append(new_kv_lens)
-    _check(load_library().fa512_cache_compact(
-        kp, vp, _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
-        _dptr(q_lens, "q_lens", torch.int32), _dptr(accepted, "accepted", torch.int32),
-        _dptr(n_accepted, "n_accepted", torch.int32), _dptr(new_kv_lens, "new_kv_lens", torch.int32),
-        layers, bsz, int(q_len), accepted.shape[1], hk, eb, psz, npages, mpps, _stream(stream)))
+    _check((_lib or load_library()).fa512_cache_compact(
+        kp, vp, _arg(page_table, "page_table", _I32, dev), _arg(kv_lens, "kv_lens", _I32, dev, one),
+        _arg(q_lens, "q_lens", _I32, dev, one), _arg(accepted, "accepted", _I32, dev, (bsz, most)),
+        _arg(n_accepted, "n_accepted", _I32, dev, one), _arg(new_kv_lens, "new_kv_lens", _I32, dev, one),
+        layers, bsz, int(q_len), most, hk, eb, psz, npages, mpps, _stream(stream, dev)))
     _used_on(stream, *mine)
     return new_kv_lens
 
@@ -684,35 +703,28 @@ def fa512_cache_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: t
     child and is copied (all layers) into a free page for every other one.
     ``new_page_refs`` may be ``page_refs`` itself.
     """
-    kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
+    dev, kp, vp, layers, npages, psz, hk, eb = _whole_cache(k_pages, v_pages)
     if page_table.dim() != 2 or parents.dim() != 1:
         raise Fa512Error(1, "page_table must be [batch, pages], parents [n_children]")
     bsz, mpps = page_table.shape
     kids = parents.shape[0]
-    _shape(kv_lens, "kv_lens", (bsz,))
-    _shape(page_refs, "page_refs", (npages,))
-    _shape(new_page_table, "new_page_table", (kids, mpps))
-    _shape(new_kv_lens, "new_kv_lens", (kids,))
-    _shape(new_page_refs, "new_page_refs", (npages,))
-    _one_device(k_pages, v_pages, page_table, kv_lens, parents, page_refs, new_page_table, new_kv_lens,
-                new_page_refs)
     mine = []
 
-    def out(t, like, shape):
+    def out(t, shape):
         if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=like.device)
+            t = torch.empty(shape, dtype=_I32, device=k_pages.device)
             mine.append(t)
         return t
-    new_page_table = out(new_page_table, page_table, (kids, mpps))
-    new_kv_lens = out(new_kv_lens, kv_lens, (kids,))
-    new_page_refs = out(new_page_refs, page_refs, (npages,))
-    _check(load_library().fa512_cache_fork(
-        kp, vp, _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
-        _dptr(parents, "parents", torch.int32), _dptr(page_refs, "page_refs", torch.int32),
-        _dptr(new_page_table, "new_page_table", torch.int32),
-        _dptr(new_kv_lens, "new_kv_lens", torch.int32),
-        _dptr(new_page_refs, "new_page_refs", torch.int32), layers, bsz, kids, hk, eb, psz, npages, mpps,
-        _stream(stream)))
+    new_page_table = out(new_page_table, (kids, mpps))
+    new_kv_lens = out(new_kv_lens, (kids,))
+    new_page_refs = out(new_page_refs, (npages,))
+    _check((_lib or load_library()).fa512_cache_fork(
+        kp, vp, _arg(page_table, "page_table", _I32, dev), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
+        _arg(parents, "parents", _I32, dev), _arg(page_refs, "page_refs", _I32, dev, (npages,)),
+        _arg(new_page_table, "new_page_table", _I32, dev, (kids, mpps)),
+        _arg(new_kv_lens, "new_kv_lens", _I32, dev, (kids,)),
+        _arg(new_page_refs, "new_page_refs", _I32, dev, (npages,)), layers, bsz, kids, hk, eb, psz, npages,
+        mpps, _stream(stream, dev)))
     _used_on(stream, *mine)
     return new_page_table, new_kv_lens, new_page_refs
 
@@ -730,11 +742,7 @@ def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_l
         raise Fa512Error(1, "page_table must be [batch, pages], page_refs [num_pages]")
     bsz, mpps = page_table.shape
     npages = page_refs.shape[0]
-    _shape(kv_lens, "kv_lens", (bsz,))
-    _shape(new_kv_lens, "new_kv_lens", (bsz,))
-    _shape(new_page_table, "new_page_table", (bsz, mpps))
-    _shape(new_page_refs, "new_page_refs", (npages,))
-    _one_device(page_table, kv_lens, new_kv_lens, page_refs, new_page_table, new_page_refs)
+    dev = _device(page_table, "page_table")
     mine = []
     if new_page_table is None:
         new_page_table = torch.empty_like(page_table)
@@ -742,12 +750,12 @@ def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_l
     if new_page_refs is None:
         new_page_refs = torch.empty_like(page_refs)
         mine.append(new_page_refs)
-    _check(load_library().fa512_cache_resize(
-        _dptr(page_table, "page_table", torch.int32), _dptr(kv_lens, "kv_lens", torch.int32),
-        _dptr(new_kv_lens, "new_kv_lens", torch.int32), _dptr(page_refs, "page_refs", torch.int32),
-        _dptr(new_page_table, "new_page_table", torch.int32),
-        _dptr(new_page_refs, "new_page_refs", torch.int32), bsz, int(page_size), npages, mpps,
-        _stream(stream)))
+    _check((_lib or load_library()).fa512_cache_resize(
+        _arg(page_table, "page_table", _I32, dev), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
+        _arg(new_kv_lens, "new_kv_lens", _I32, dev, (bsz,)), _arg(page_refs, "page_refs", _I32, dev),
+        _arg(new_page_table, "new_page_table", _I32, dev, (bsz, mpps)),
+        _arg(new_page_refs, "new_page_refs", _I32, dev, (npages,)), bsz, int(page_size), npages, mpps,
+        _stream(stream, dev)))
     _used_on(stream, *mine)
     return new_page_table, new_page_refs
 

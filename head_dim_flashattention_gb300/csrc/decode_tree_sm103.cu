@@ -1049,7 +1049,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
 }
 
 // Resident clusters of `cs` CTAs of one kernel variant on the current device
-// (0 when the query fails), asked once per device.
+// (0 when the query fails), asked once per device, which also opts the kernel
+// into its shared memory there.
 template <bool FP8, int ROWS>
 int resident_clusters(int cs) {
     static std::mutex mu;
@@ -1087,16 +1088,13 @@ template <bool FP8, int ROWS>
 cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
     const int clusters = resident_clusters<FP8, ROWS>(p.cluster);
     if (clusters < 1) return cudaErrorLaunchOutOfResources;
-    const int smem = Cfg<FP8, ROWS>::total + 1024;
-    cudaError_t e = cudaFuncSetAttribute(tree_kernel<FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     const long long units = static_cast<long long>(p.batch) * p.row_groups * p.n_kv_heads *
                             (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
     cfg.gridDim = dim3(static_cast<unsigned>(units < clusters ? units : clusters) * p.cluster);
     cfg.blockDim = dim3(Cfg<FP8, ROWS>::THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = Cfg<FP8, ROWS>::total + 1024;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1105,7 +1103,7 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, tree_kernel<FP8, ROWS>, tmk, tmv, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<FP8, ROWS>, tmk, tmv, p);
     if (e != cudaSuccess || p.num_splits == 1) return e;
     // the merge may be scheduled while the tiles are walked (it waits for them)
     memset(&cfg, 0, sizeof cfg);
