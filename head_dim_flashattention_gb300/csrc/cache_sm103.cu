@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -22,76 +23,92 @@ constexpr int D = 512;
 
 // ------------------------------------------------------------------- append
 //
-// One thread moves 16 stored bytes of a key row and of the value row beside
-// it (8 bf16 elements, or 16 elements rounded to E4M3).  blockIdx.y is the
-// sequence; the units of its tokens are dealt along blockIdx.x.
+// A thread moves 16 stored bytes (8 bf16 elements, or 16 elements rounded to
+// E4M3) of the key row and of the value row of up to APPEND_RUN places of its
+// sequence (blockIdx.y), all its loads before the first store.
+// Bound: bytes.  The division by a scale that is no power of two costs about
+// as many issue slots as the bytes take; a power of two (whose reciprocal is
+// exact) multiplies, which gives the same quotients.
 constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_RUN = 2;
 
-__device__ __forceinline__ uint32_t e4m3x4(const float (&x)[4]) {
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// 16 bf16 elements -> the 16 E4M3 bytes of x / scale (an IEEE division: the
-// nearest fp32 quotient, then the nearest code, ties to even).
-__device__ __forceinline__ uint4 quantise16(const uint4 a, const uint4 b, float scale) {
+// 16 bf16 elements -> the 16 E4M3 bytes of x / scale (the nearest fp32
+// quotient, then the nearest code, ties to even).  POW2: `by` is 1 / scale.
+template <bool POW2>
+__device__ __forceinline__ uint4 quantise16(const uint4 a, const uint4 b, float by) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t r[4];
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x[4] = {__fdiv_rn(__uint_as_float(w[2 * i] << 16), scale),
-                            __fdiv_rn(__uint_as_float(w[2 * i] & 0xffff0000u), scale),
-                            __fdiv_rn(__uint_as_float(w[2 * i + 1] << 16), scale),
-                            __fdiv_rn(__uint_as_float(w[2 * i + 1] & 0xffff0000u), scale)};
-        r[i] = e4m3x4(x);
+    for (int i = 0; i < 8; ++i) {
+        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+        x[2 * i] = POW2 ? lo * by : __fdiv_rn(lo, by);
+        x[2 * i + 1] = POW2 ? hi * by : __fdiv_rn(hi, by);
     }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+    return make_uint4(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]),
+                      e4m3x4(x[8], x[9], x[10], x[11]), e4m3x4(x[12], x[13], x[14], x[15]));
 }
 
-template <bool FP8>
+// MODE 0: bf16, 1: E4M3, 2: E4M3 with scales that are powers of two
+template <int MODE>
 __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams p) {
-    constexpr int UNITS_PER_HEAD = FP8 ? D / 16 : D / 8;
+    constexpr int UNIT = MODE ? 16 : 8;                   // elements of a place
+    constexpr int V = UNIT / 8;                           // 16-byte loads of one
     const int b = blockIdx.y;
-    const int units = p.n_kv_heads * UNITS_PER_HEAD;      // per token
-    const long long idx = static_cast<long long>(blockIdx.x) * APPEND_THREADS + threadIdx.x;
-    const int t = static_cast<int>(idx / units);
-    const int u = static_cast<int>(idx - static_cast<long long>(t) * units);
-    if (t >= p.q_len) return;
+    const int units = p.n_kv_heads * (D / UNIT);          // per token
     int n_new = p.q_lens ? p.q_lens[b] : p.q_len;
+    const int len = p.kv_lens[b];
     if (n_new < 0 || n_new > p.q_len) {
-        if (idx == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
         n_new = n_new < 0 ? 0 : p.q_len;
     }
-    if (t >= n_new) return;
-    const long long pos = static_cast<long long>(p.kv_lens[b]) - n_new + t;
-    if (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size) {
-        if (u == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        return;
+    uint4 k[APPEND_RUN][V], v[APPEND_RUN][V];
+    size_t at[APPEND_RUN];
+    bool there[APPEND_RUN];
+#pragma unroll
+    for (int r = 0; r < APPEND_RUN; ++r) {
+        const unsigned idx = (blockIdx.x * APPEND_RUN + r) * APPEND_THREADS + threadIdx.x;
+        const int t = static_cast<int>(idx / static_cast<unsigned>(units));
+        const int u = static_cast<int>(idx) - t * units;
+        const long long pos = static_cast<long long>(len) - n_new + t;
+        there[r] = t < n_new;
+        if (there[r] && (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size)) {
+            if (u == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            there[r] = false;
+        }
+        if (!there[r]) continue;
+        const int lp = static_cast<int>(pos) / p.page_size;
+        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
+        const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + b * p.k_batch_stride + t * p.k_token_stride) + V * u;
+        const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + b * p.v_batch_stride + t * p.v_token_stride) + V * u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            k[r][i] = ks[i];
+            v[r][i] = vs[i];
+        }
+        if (page < 0 || page >= p.num_pages) {
+            if (u == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            there[r] = false;
+        }
+        at[r] = (static_cast<size_t>(page) * p.page_size + static_cast<int>(pos) % p.page_size) * units + u;
     }
-    const int lp = static_cast<int>(pos / p.page_size);
-    const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
-    if (page < 0 || page >= p.num_pages) {
-        if (u == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        return;
-    }
-    const size_t row = static_cast<size_t>(page) * p.page_size + static_cast<size_t>(pos - static_cast<long long>(lp) * p.page_size);
-    const long long ks = b * p.k_batch_stride + t * p.k_token_stride;
-    const long long vs = b * p.v_batch_stride + t * p.v_token_stride;
-    uint4* kd = static_cast<uint4*>(p.k_pages) + row * units + u;
-    uint4* vd = static_cast<uint4*>(p.v_pages) + row * units + u;
-    if constexpr (FP8) {
-        const uint4* k = reinterpret_cast<const uint4*>(p.k_new + ks) + 2 * u;
-        const uint4* v = reinterpret_cast<const uint4*>(p.v_new + vs) + 2 * u;
-        const uint4 k0 = k[0], k1 = k[1], v0 = v[0], v1 = v[1];
-        *kd = quantise16(k0, k1, p.k_scale);
-        *vd = quantise16(v0, v1, p.v_scale);
-    } else {
-        const uint4 k = reinterpret_cast<const uint4*>(p.k_new + ks)[u];
-        const uint4 v = reinterpret_cast<const uint4*>(p.v_new + vs)[u];
-        *kd = k;
-        *vd = v;
+#pragma unroll
+    for (int r = 0; r < APPEND_RUN; ++r) {
+        if (!there[r]) continue;
+        uint4 *kd = static_cast<uint4*>(p.k_pages) + at[r], *vd = static_cast<uint4*>(p.v_pages) + at[r];
+        if constexpr (MODE == 0) {
+            *kd = k[r][0];
+            *vd = v[r][0];
+        } else {
+            *kd = quantise16<MODE == 2>(k[r][0], k[r][V - 1], p.k_scale);
+            *vd = quantise16<MODE == 2>(v[r][0], v[r][V - 1], p.v_scale);
+        }
     }
 }
 
@@ -166,23 +183,37 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const CompactP
 
 // -------------------------------------------------------- fork and resize
 //
-// One cluster of blocks plans the pages: (A) copies the reference counts and
-// (fork) finds the first child of every parent, (B) writes the new tables,
-// moves the counts by integer atomics (their order does not matter) and scans
-// how many fresh pages each sequence needs, (C) counts the free pages of its
-// part of the pool, learns the other blocks' counts through distributed
-// shared memory, and deals the free pages, lowest first, to the needs in
-// order: the page of rank r goes to the sequence whose scan interval holds r.
+// One cluster of blocks plans the pages, so that its phases are separated by
+// the cluster's barrier and not by launches: (A) copy the reference counts
+// and find how many fresh pages each sequence needs (fork: the first child of
+// every parent), with a scan over the sequences; (B) write the new tables and
+// move the counts by integer atomics (their order does not matter); (C) mark
+// the free pages of the block's part of the pool in a bit map, learn the
+// other blocks' counts through distributed shared memory, and deal the free
+// pages, lowest first, to the needs in order: the page of rank r goes to the
+// sequence whose scan interval holds r.
+//
+// Bound: chains of dependent loads, not bytes (2.3 MB for 512 sequences of
+// 448 pages and a pool of 178,000 pages), so every pass keeps 8 loads a
+// thread in flight and nothing is looked up twice: lengths, parents and needs
+// stay in shared memory.
 constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_MAX_BATCH = 8192;
-constexpr int PLAN_CLUSTER = 8;
+constexpr int PLAN_CLUSTER = 8;          // blocks, at most
+constexpr int PLAN_RUN = 8;              // loads in flight per thread
+constexpr int PLAN_CHUNK = PLAN_THREADS; // words (of 32 pages) of the bit map
 
+// Shared memory: fixed part, then the arrays of the call's sizes.
 struct PlanSmem {
-    int off[PLAN_MAX_BATCH + 1];        // fresh pages needed before sequence b
-    int first[PLAN_MAX_BATCH];          // fork: first child of each parent
-    int warp_sum[PLAN_THREADS / 32];
-    int counts[PLAN_CLUSTER];           // free pages of each block's part
+    int warp_sum[PLAN_WARPS];
+    int counts[PLAN_CLUSTER];            // free pages of each block's part
+    uint32_t bits[PLAN_CHUNK];           // free pages of a chunk
+    int rank[PLAN_CHUNK];                // free pages before each word of it
 };
+inline size_t plan_smem_bytes(int n_new, int batch, bool fork) {
+    return sizeof(PlanSmem) + 4 * (3 * static_cast<size_t>(n_new) + 1 + (fork ? batch : 0));
+}
 
 // Exclusive scan of one value per thread; *total gets the block's sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
@@ -196,7 +227,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
     __syncthreads();                    // the last scan's readers are done
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int w = warp_sum[lane];             // 32 warps
+    const int w = warp_sum[lane];       // 32 warps
     int ws = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -208,28 +239,46 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
     return before + x - v;
 }
 
-// A length clipped to the table, recorded when it was outside.
-__device__ __forceinline__ int clip_len(int n, const PagePlanParams& p) {
+// Pages of a length, clipped to the table (recorded when it was outside).
+__device__ __forceinline__ int pages_of(int n, const PagePlanParams& p) {
     const long long cap = static_cast<long long>(p.max_pages_per_seq) * p.page_size;
     if (n < 0 || n > cap) {
         report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        return n < 0 ? 0 : static_cast<int>(cap);
+        return n < 0 ? 0 : p.max_pages_per_seq;
     }
-    return n;
+    return static_cast<int>((static_cast<long long>(n) + p.page_size - 1) / p.page_size);
 }
 
-__device__ __forceinline__ int pages_of(int n, int page_size) {
-    return static_cast<int>((static_cast<long long>(n) + page_size - 1) / page_size);
-}
-
-// The page of a held entry, -1 (recorded) outside the pool.
-__device__ __forceinline__ int held_page(const PagePlanParams& p, size_t entry) {
-    const int page = p.page_table[entry];
-    if (page < 0 || page >= p.num_pages) {
-        report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        return -1;
+// Walks the first held(b) entries of `rows` table rows in runs of 32 x
+// PLAN_RUN entries, a warp each: f(row, entry, page) with page = the entry's
+// page, -1 where the row does not hold the entry or (recorded) where it lies
+// outside the pool.
+template <class Held, class Row, class F>
+__device__ __forceinline__ void walk_tables(const PagePlanParams& p, int rows, Held held, Row row_of, F f) {
+    const int lane = threadIdx.x & 31;
+    const int width = p.max_pages_per_seq;
+    constexpr int RUN = 32 * PLAN_RUN;
+    const int runs = (width + RUN - 1) / RUN;
+    const long long all = static_cast<long long>(rows) * runs;
+    const int step = gridDim.x * PLAN_WARPS;
+    for (long long u = blockIdx.x * PLAN_WARPS + (threadIdx.x >> 5); u < all; u += step) {
+        const int b = static_cast<int>(u / runs), i0 = static_cast<int>(u - static_cast<long long>(b) * runs) * RUN + lane;
+        const int n = held(b);
+        const int32_t* row = p.page_table + static_cast<size_t>(row_of(b)) * width;
+        int page[PLAN_RUN];
+#pragma unroll
+        for (int k = 0; k < PLAN_RUN; ++k) page[k] = i0 + 32 * k < n ? row[i0 + 32 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < PLAN_RUN; ++k) {
+            const int i = i0 + 32 * k;
+            if (i >= width) break;
+            if (i < n && (page[k] < 0 || page[k] >= p.num_pages)) {
+                report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                page[k] = -1;
+            }
+            f(b, i, page[k]);
+        }
     }
-    return page;
 }
 
 template <bool FORK>
@@ -237,101 +286,138 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) uint8_t raw[];
     PlanSmem& s = *reinterpret_cast<PlanSmem*>(raw);
-    const int tid = threadIdx.x;
-    const int rank = blockIdx.x, blocks = gridDim.x;     // the grid is one cluster
+    int* s_off = reinterpret_cast<int*>(raw + sizeof(PlanSmem));   // fresh pages needed before sequence b
+    int* s_from = s_off + p.n_new + 1;                             // fork: parent or -1; resize: pages held now
+    int* s_held = s_from + p.n_new;                                // pages held by the new table
+    int* s_first = s_held + p.n_new;                               // fork: first child of each parent
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x, blocks = gridDim.x;               // the grid is one cluster
     const int gtid = rank * PLAN_THREADS + tid, all = blocks * PLAN_THREADS;
     const int width = p.max_pages_per_seq, ps = p.page_size;
 
-    // ---- A
-    if (p.new_refs != p.page_refs)
-        for (int i = gtid; i < p.num_pages; i += all) p.new_refs[i] = p.page_refs[i];
+    // ---- A: counts; needs
+    if (p.new_refs != p.page_refs) {
+        int done = 0;
+        if (((reinterpret_cast<uintptr_t>(p.new_refs) | reinterpret_cast<uintptr_t>(p.page_refs)) & 15) == 0) {
+            const int4* src = reinterpret_cast<const int4*>(p.page_refs);
+            int4* dst = reinterpret_cast<int4*>(p.new_refs);
+            const int quads = p.num_pages / 4;
+            for (int i0 = gtid; i0 < quads; i0 += 4 * all) {
+                int4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k * all < quads) x[k] = src[i0 + k * all];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k * all < quads) dst[i0 + k * all] = x[k];
+            }
+            done = quads * 4;
+        }
+        for (int i = done + gtid; i < p.num_pages; i += all) p.new_refs[i] = p.page_refs[i];
+    }
     if constexpr (FORK) {
-        for (int i = tid; i < p.batch; i += PLAN_THREADS) s.first[i] = INT_MAX;
+        for (int i = tid; i < p.batch; i += PLAN_THREADS) s_first[i] = INT_MAX;
         __syncthreads();
         for (int c = tid; c < p.n_new; c += PLAN_THREADS) {
-            const int a = p.parents[c];
-            if (a >= 0 && a < p.batch) atomicMin(&s.first[a], c);
+            int a = p.parents[c];
+            if (a < 0 || a >= p.batch) {
+                if (rank == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                a = -1;
+            } else {
+                atomicMin(&s_first[a], c);
+            }
+            s_from[c] = a;
         }
+        __syncthreads();
     }
-    cluster_sync_all();
-
-    // ---- B: needs
     int total = 0;
     for (int b0 = 0; b0 < p.n_new; b0 += PLAN_THREADS) {
         const int b = b0 + tid;
         int need = 0;
         if (b < p.n_new) {
             if constexpr (FORK) {
-                const int a = p.parents[b];
-                int n = 0;
-                if (a >= 0 && a < p.batch) {
-                    n = clip_len(p.kv_lens[a], p);
-                    need = (n % ps != 0 && s.first[a] != b) ? 1 : 0;
-                } else if (rank == 0) {
-                    report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                }
+                const int a = s_from[b];
+                int n = a >= 0 ? p.kv_lens[a] : 0;
+                s_held[b] = pages_of(n, p);
+                n = n < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(width) * ps));
+                need = n % ps != 0 && s_first[a] != b ? 1 : 0;
                 if (rank == 0) p.new_lens[b] = n;
             } else {
-                need = pages_of(clip_len(p.next_lens[b], p), ps) - pages_of(clip_len(p.kv_lens[b], p), ps);
-                need = need > 0 ? need : 0;
+                s_from[b] = pages_of(p.kv_lens[b], p);
+                s_held[b] = pages_of(p.next_lens[b], p);
+                need = max(0, s_held[b] - s_from[b]);
             }
         }
         int sum;
         const int before = block_scan(need, s.warp_sum, &sum);
-        if (b < p.n_new) s.off[b] = total + before;
+        if (b < p.n_new) s_off[b] = total + before;
         total += sum;
     }
-    if (tid == 0) s.off[p.n_new] = total;
-    __syncthreads();
-
-    // ---- B: tables and counts
-    const long long entries = static_cast<long long>(p.n_new) * width;
-    for (long long e = gtid; e < entries; e += all) {
-        const int b = static_cast<int>(e / width), i = static_cast<int>(e - static_cast<long long>(b) * width);
-        int page = -1;
-        if constexpr (FORK) {
-            const int a = p.parents[b];
-            if (a >= 0 && a < p.batch) {
-                const int n = clip_len(p.kv_lens[a], p);
-                const bool fresh = s.off[b + 1] > s.off[b] && i == n / ps;
-                if (i < pages_of(n, ps) && !fresh) {
-                    page = held_page(p, static_cast<size_t>(a) * width + i);
-                    if (page >= 0) atomicAdd(&p.new_refs[page], 1);
-                }
-            }
-        } else {
-            const bool now = i < pages_of(clip_len(p.kv_lens[b], p), ps);
-            const bool then = i < pages_of(clip_len(p.next_lens[b], p), ps);
-            if (now) {
-                page = held_page(p, static_cast<size_t>(e));
-                if (!then) {
-                    if (page >= 0) atomicAdd(&p.new_refs[page], -1);
-                    page = -1;
-                }
-            }
-        }
-        p.new_table[e] = page;
-    }
-    if constexpr (FORK) {
-        const long long old = static_cast<long long>(p.batch) * width;
-        for (long long e = gtid; e < old; e += all) {
-            const int a = static_cast<int>(e / width), i = static_cast<int>(e - static_cast<long long>(a) * width);
-            if (i < pages_of(clip_len(p.kv_lens[a], p), ps)) {
-                const int page = held_page(p, static_cast<size_t>(e));
-                if (page >= 0) atomicAdd(&p.new_refs[page], -1);
-            }
-        }
-    }
+    if (tid == 0) s_off[p.n_new] = total;
     cluster_sync_all();
 
-    // ---- C: free pages of this block's part
-    const int part = (p.num_pages + blocks - 1) / blocks;
-    const int lo = min(p.num_pages, rank * part), hi = min(p.num_pages, lo + part);
-    int mine = 0;
-    for (int i = lo + tid; i < hi; i += PLAN_THREADS) mine += __ldcg(&p.new_refs[i]) == 0;
-    int part_free;
-    block_scan(mine, s.warp_sum, &part_free);
-    if (tid < blocks) pair::st_cluster_u32(map_to_cta(smem_u32(&s.counts[rank]), tid), static_cast<uint32_t>(part_free));
+    // ---- B: tables and counts
+    if constexpr (FORK) {
+        // a fresh last page is not the parent's: the table gets it in C
+        walk_tables(
+            p, p.n_new, [&](int c) { return s_held[c] - (s_off[c + 1] - s_off[c]); },
+            [&](int c) { return max(s_from[c], 0); },
+            [&](int c, int i, int page) {
+                if (page >= 0) atomicAdd(&p.new_refs[page], 1);
+                p.new_table[static_cast<size_t>(c) * width + i] = page;
+            });
+        walk_tables(
+            p, p.batch, [&](int a) { return pages_of(p.kv_lens[a], p); }, [](int a) { return a; },
+            [&](int, int, int page) {
+                if (page >= 0) atomicAdd(&p.new_refs[page], -1);
+            });
+    } else {
+        walk_tables(
+            p, p.n_new, [&](int b) { return s_from[b]; }, [](int b) { return b; },
+            [&](int b, int i, int page) {
+                if (i >= s_held[b] && page >= 0) {
+                    atomicAdd(&p.new_refs[page], -1);
+                    page = -1;
+                }
+                p.new_table[static_cast<size_t>(b) * width + i] = page;
+            });
+    }
+    if (total == 0) return;              // the same in every block: no fresh page to deal
+    cluster_sync_all();
+
+    // ---- C: free pages of this block's part, in chunks of the bit map
+    const int words = (p.num_pages + 31) / 32;
+    const int part = (words + blocks - 1) / blocks;
+    const int lo = min(words, rank * part), hi = min(words, lo + part);
+    auto mark = [&](int c0) -> int {     // fills s.bits with the words from c0 on; their number
+        const int n = min(PLAN_CHUNK, hi - c0);
+        for (int w0 = warp; w0 < n; w0 += PLAN_WARPS * PLAN_RUN) {
+            int refs[PLAN_RUN];
+#pragma unroll
+            for (int k = 0; k < PLAN_RUN; ++k) {
+                const int w = w0 + k * PLAN_WARPS, page = (c0 + w) * 32 + lane;
+                refs[k] = w < n && page < p.num_pages ? __ldcg(&p.new_refs[page]) : 1;
+            }
+#pragma unroll
+            for (int k = 0; k < PLAN_RUN; ++k) {
+                const int w = w0 + k * PLAN_WARPS;
+                const uint32_t free_bits = __ballot_sync(0xffffffffu, refs[k] == 0);
+                if (lane == 0 && w < n) s.bits[w] = free_bits;
+            }
+        }
+        __syncthreads();
+        return n;
+    };
+    int part_free = 0;
+    for (int c0 = lo; c0 < hi; c0 += PLAN_CHUNK) {
+        const int n = mark(c0);
+        int sum;
+        block_scan(tid < n ? __popc(s.bits[tid]) : 0, s.warp_sum, &sum);
+        part_free += sum;
+        if (c0 + PLAN_CHUNK < hi) __syncthreads();
+    }
+    if (tid < blocks)
+        pair::st_cluster_u32(map_to_cta(smem_u32(&s.counts[rank]), tid), static_cast<uint32_t>(part_free));
     cluster_sync_all();
     int base = 0, free_pages = 0;
     for (int r = 0; r < blocks; ++r) {
@@ -339,27 +425,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
         free_pages += s.counts[r];
     }
     if (total > free_pages && rank == 0 && tid == 0) report_error(p.err, FA512_DEVICE_ERR_PAGES);
-    for (int i0 = lo; i0 < hi && base < total; i0 += PLAN_THREADS) {
-        const int i = i0 + tid;
-        const bool free_here = i < hi && __ldcg(&p.new_refs[i]) == 0;
+    for (int c0 = lo; c0 < hi && base < total; c0 += PLAN_CHUNK) {
+        const int n = hi - lo > PLAN_CHUNK ? mark(c0) : hi - lo;   // one chunk: its bits are still there
         int sum;
-        const int r = base + block_scan(free_here ? 1 : 0, s.warp_sum, &sum);
-        if (free_here && r < total) {
-            // the last b with off[b] <= r
-            int a = 0, z = p.n_new;
-            while (z - a > 1) {
-                const int m = (a + z) >> 1;
-                if (s.off[m] <= r) a = m; else z = m;
+        const int before = block_scan(tid < n ? __popc(s.bits[tid]) : 0, s.warp_sum, &sum);
+        if (tid < n) s.rank[tid] = base + before;
+        __syncthreads();
+        for (int w = warp; w < n; w += PLAN_WARPS) {
+            const uint32_t free_bits = s.bits[w];
+            const int r = s.rank[w] + __popc(free_bits & ((1u << lane) - 1u));
+            if (s.rank[w] >= total) break;
+            if (((free_bits >> lane) & 1u) && r < total) {
+                // the last b with off[b] <= r
+                int a = 0, z = p.n_new;
+                while (z - a > 1) {
+                    const int m = (a + z) >> 1;
+                    if (s_off[m] <= r) a = m; else z = m;
+                }
+                const int page = (c0 + w) * 32 + lane;
+                const int entry = FORK ? s_held[a] - 1 : s_from[a] + r - s_off[a];
+                p.new_table[static_cast<size_t>(a) * width + entry] = page;
+                p.new_refs[page] = 1;
             }
-            int entry;
-            if constexpr (FORK)
-                entry = clip_len(p.kv_lens[p.parents[a]], p) / ps;
-            else
-                entry = pages_of(clip_len(p.kv_lens[a], p), ps) + (r - s.off[a]);
-            p.new_table[static_cast<size_t>(a) * width + entry] = i;
-            p.new_refs[i] = 1;
         }
         base += sum;
+        __syncthreads();
     }
 }
 
@@ -402,11 +492,23 @@ __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const PagePlanP
 cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t stream) {
     using namespace cache;
     const long long units = static_cast<long long>(p.q_len) * p.n_kv_heads * (fp8 ? D / 16 : D / 8);
-    const dim3 grid(static_cast<unsigned>((units + APPEND_THREADS - 1) / APPEND_THREADS), p.batch);
-    if (fp8)
-        append_kernel<true><<<grid, APPEND_THREADS, 0, stream>>>(p);
-    else
-        append_kernel<false><<<grid, APPEND_THREADS, 0, stream>>>(p);
+    constexpr int BLOCK = APPEND_THREADS * APPEND_RUN;
+    const dim3 grid(static_cast<unsigned>((units + BLOCK - 1) / BLOCK), p.batch);
+    // scales that are powers of two with a normal reciprocal
+    auto pow2 = [](float x) {
+        int e;
+        return frexpf(x, &e) == 0.5f && e > -100 && e < 100;
+    };
+    if (!fp8) {
+        append_kernel<0><<<grid, APPEND_THREADS, 0, stream>>>(p);
+    } else if (pow2(p.k_scale) && pow2(p.v_scale)) {
+        AppendParams q = p;
+        q.k_scale = 1.f / p.k_scale;
+        q.v_scale = 1.f / p.v_scale;
+        append_kernel<2><<<grid, APPEND_THREADS, 0, stream>>>(q);
+    } else {
+        append_kernel<1><<<grid, APPEND_THREADS, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 
@@ -425,18 +527,25 @@ int page_plan_max_batch() { return cache::PLAN_MAX_BATCH; }
 cudaError_t launch_page_plan(const PagePlanParams& p, bool fork, cudaStream_t stream) {
     using namespace cache;
     auto kernel = fork ? page_plan_kernel<true> : page_plan_kernel<false>;
-    const int smem = static_cast<int>(sizeof(PlanSmem));
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    const size_t smem = plan_smem_bytes(p.n_new, p.batch, fork);
+    cudaError_t e;
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(plan_smem_bytes(PLAN_MAX_BATCH, PLAN_MAX_BATCH, true)));
+        if (e != cudaSuccess) return e;
+    }
+    // a block for every 4,096 table entries and counts (4 per thread)
+    const long long work = static_cast<long long>(p.n_new + (fork ? p.batch : 0)) * p.max_pages_per_seq + p.num_pages;
+    const int blocks = static_cast<int>(work >= PLAN_CLUSTER * 4096LL ? PLAN_CLUSTER : work / 4096 + 1);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(PLAN_CLUSTER);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(PLAN_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PLAN_CLUSTER;
+    attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
