@@ -425,28 +425,37 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
         free_pages += s.counts[r];
     }
     if (total > free_pages && rank == 0 && tid == 0) report_error(p.err, FA512_DEVICE_ERR_PAGES);
+    const int top = 1 << (31 - __clz(p.n_new));                    // highest power of two up to n_new
     for (int c0 = lo; c0 < hi && base < total; c0 += PLAN_CHUNK) {
         const int n = hi - lo > PLAN_CHUNK ? mark(c0) : hi - lo;   // one chunk: its bits are still there
         int sum;
         const int before = block_scan(tid < n ? __popc(s.bits[tid]) : 0, s.warp_sum, &sum);
         if (tid < n) s.rank[tid] = base + before;
         __syncthreads();
-        for (int w = warp; w < n; w += PLAN_WARPS) {
-            const uint32_t free_bits = s.bits[w];
-            const int r = s.rank[w] + __popc(free_bits & ((1u << lane) - 1u));
-            if (s.rank[w] >= total) break;
-            if (((free_bits >> lane) & 1u) && r < total) {
-                // the last b with off[b] <= r
-                int a = 0, z = p.n_new;
-                while (z - a > 1) {
-                    const int m = (a + z) >> 1;
-                    if (s_off[m] <= r) a = m; else z = m;
-                }
-                const int page = (c0 + w) * 32 + lane;
-                const int entry = FORK ? s_held[a] - 1 : s_from[a] + r - s_off[a];
-                p.new_table[static_cast<size_t>(a) * width + entry] = page;
-                p.new_refs[page] = 1;
+        // four words a warp at a time, so that their searches overlap
+        constexpr int DEAL = 4;
+        for (int w0 = warp; w0 < n && s.rank[w0] < total; w0 += DEAL * PLAN_WARPS) {
+            int r[DEAL], at[DEAL];
+#pragma unroll
+            for (int k = 0; k < DEAL; ++k) {
+                const int w = w0 + k * PLAN_WARPS;
+                const uint32_t free_bits = w < n ? s.bits[w] : 0u;
+                r[k] = (free_bits >> lane) & 1u ? s.rank[w] + __popc(free_bits & ((1u << lane) - 1u)) : total;
+                at[k] = 0;
             }
+            // the last b with off[b] <= r
+            for (int step = top; step > 0; step >>= 1)
+#pragma unroll
+                for (int k = 0; k < DEAL; ++k)
+                    if (at[k] + step < p.n_new && s_off[at[k] + step] <= r[k]) at[k] += step;
+#pragma unroll
+            for (int k = 0; k < DEAL; ++k)
+                if (r[k] < total) {
+                    const int b = at[k], page = (c0 + w0 + k * PLAN_WARPS) * 32 + lane;
+                    const int entry = FORK ? s_held[b] - 1 : s_from[b] + r[k] - s_off[b];
+                    p.new_table[static_cast<size_t>(b) * width + entry] = page;
+                    p.new_refs[page] = 1;
+                }
         }
         base += sum;
         __syncthreads();

@@ -368,8 +368,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             const Band d = band_of(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
             return static_cast<long long>(max(1, d.tiles)) * p.n_kv_heads;
         };
-        long long total = 0;
-        for (int e = tid; e < walk.entries; e += THREADS) total += entry_units(e, blockIdx.x == 0);
+        long long total = 0, mine0 = 0;                  // mine0: entry tid's units
+        for (int e = tid; e < walk.entries; e += THREADS) {
+            const long long u = entry_units(e, blockIdx.x == 0);
+            if (e == tid) mine0 = u;
+            total += u;
+        }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         if (lane == 0) s_scan[warp] = total;
@@ -387,7 +391,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         long long before = 0;
         if (walk.pos < walk.end) {
             for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
-                const long long u = entry_units(e0 + tid, false);
+                const long long u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
                 long long x = u;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -1009,43 +1013,95 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
     if (warp == 1) tmem_dealloc(tmem, C::TM_COLS);
 }
 
-// One block per row that was left in segments: combines the segments' (O, m,
-// l) -- M = max m_s, w_s = 2^(m_s - M), O = sum w_s O_s / sum w_s l_s.
-constexpr int MERGE_THREADS = 128;       // a quad of columns each
+// One block per row that was left in segments and slice of its columns:
+// combines the segments' (O, m, l) -- M = max m_s, w_s = 2^(m_s - M),
+// O = sum w_s O_s / sum w_s l_s.  256 threads: column quads x groups of
+// segments; every thread issues its first 16 segments' O loads before it
+// needs a weight, so the merge costs about one round trip to memory.  Few
+// rows are merged in four column slices each (CS = 4).
+constexpr int MERGE_THREADS = 256;
+constexpr int MERGE_AHEAD = 16;
+constexpr int MAX_SPLITS = 1024;
 
+template <int CS>
 __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p, int group_rows) {
+    constexpr int QB = D / 4 / CS;                  // column quads of the slice
+    constexpr int NG = MERGE_THREADS / QB;          // groups of segments
+    __shared__ float sw[MAX_SPLITS];                // weights
+    __shared__ float4 sacc[NG - 1][QB];
+    __shared__ float sred[2][MERGE_THREADS / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int h = blockIdx.x, bt = blockIdx.y;
     const int b = bt / p.q_len, t = bt - b * p.q_len;
     const int grp = (t * p.group + h % p.group) / group_rows;
     const int S = p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group];
     if (S <= 1) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int quad = tid % QB, g = tid / QB;
+    const int col = blockIdx.z * (D / CS) + quad * 4;
     const size_t row = static_cast<size_t>(bt) * p.n_q_heads + h;
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.num_splits;
-    const float* ob = p.ws_o + row * p.num_splits * D + threadIdx.x * 4;
+    const float* ob = p.ws_o + row * p.num_splits * D + col;
+    float4 x[MERGE_AHEAD];
+#pragma unroll
+    for (int i = 0; i < MERGE_AHEAD; ++i) {
+        const int s = g + i * NG;
+        if (s < S) x[i] = *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D);
+    }
     float M = -INFINITY;
-    for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = tid; s < S; s += MERGE_THREADS) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) sred[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < MERGE_THREADS / 32; ++w) M = fmaxf(M, sred[0][w]);
     float L = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 8
-        for (int s = 0; s < S; ++s) {
-            const float2 v = ml[s];
-            const float4 o = *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D);
-            const float w = fast_exp2(v.x - M);
-            L = fmaf(w, v.y, L);
-            acc.x = fmaf(w, o.x, acc.x);
-            acc.y = fmaf(w, o.y, acc.y);
-            acc.z = fmaf(w, o.z, acc.z);
-            acc.w = fmaf(w, o.w, acc.w);
-        }
+    for (int s = tid; s < S; s += MERGE_THREADS) {
+        const float2 v = ml[s];
+        const float w = M == -INFINITY ? 0.f : fast_exp2(v.x - M);
+        sw[s] = w;
+        L = fmaf(w, v.y, L);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) sred[1][warp] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < MERGE_THREADS / 32; ++w) L += sred[1][w];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int s, const float4& v) {
+        const float w = sw[s];
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < MERGE_AHEAD; ++i)
+        if (g + i * NG < S) add(g + i * NG, x[i]);
+#pragma unroll 4
+    for (int s = g + MERGE_AHEAD * NG; s < S; s += NG)
+        add(s, *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D));
+    if (g > 0) sacc[g - 1][quad] = acc;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 0; i < NG - 1; ++i) {
+        const float4 a = sacc[i][quad];
+        acc.x += a.x;
+        acc.y += a.y;
+        acc.z += a.z;
+        acc.w += a.w;
     }
     const float inv = M == -INFINITY ? 0.f : 1.f / L;
     uint2 packed;
     packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + row * D + threadIdx.x * 4) = packed;
-    if (p.lse && threadIdx.x == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+    *reinterpret_cast<uint2*>(p.out + row * D + col) = packed;
+    if (p.lse && tid == 0 && blockIdx.z == 0)
+        p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 // Resident clusters of `cs` CTAs of one kernel variant on the current device
@@ -1107,14 +1163,16 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
     if (e != cudaSuccess || p.num_splits == 1) return e;
     // the merge may be scheduled while the tiles are walked (it waits for them)
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len);
+    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
+    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
     cfg.blockDim = dim3(MERGE_THREADS);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel, p, ROWS * p.cluster);
+    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, ROWS * p.cluster)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, ROWS * p.cluster);
 }
 
 }  // namespace tree
