@@ -878,6 +878,9 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.cluster = shape.cluster;
     p.row_groups = shape.groups;
     p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks));
+    p.min_range = splits > 1 ? (p.max_tiles + splits - 2) / (splits - 1) : 0;
+    if (static_cast<long long>(batch) * shape.groups * n_kv_heads * (p.max_tiles > 1 ? p.max_tiles : 1) > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
     p.mask_words = (q_len + 31) / 32;
     p.page_size = page_size;
     p.num_pages = num_pages;

@@ -59,7 +59,17 @@ namespace fa512 {
 namespace tree {
 
 using pair::elect_one;
-using pair::wait_or_abort;
+
+// The kernel's code is kept small enough for the instruction cache (roles run
+// side by side, and what a segment runs once would otherwise be fetched from
+// L2 between the streams' loads): what is seldom run or run from many places
+// is not inlined.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    return pair::wait_or_abort(bar, parity, err, abort);
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    return mbar_try_wait(smem_u32(bar), parity) || wait_slow(bar, parity, err, abort);
+}
 
 constexpr int D = 512;
 constexpr int MAX_NODES = 256;
@@ -97,12 +107,12 @@ struct Cfg {
     static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int mult = red + 4 * ROWS * 4;      // [ROWS] float: score -> log2 units
-    static constexpr int place = mult + ROWS * 4;        // [ROWS] int
-    static constexpr int tok = place + ROWS * 4;         // [ROWS] int, -1: sees nothing
-    static constexpr int rows = tok + ROWS * 4;          // [4 tiles][8 boxes] int: the producer's pool rows
+    static constexpr int see = mult + ROWS * 4;          // [ROWS] int4: last key, key below the window, mask row
+    static constexpr int rows = see + ROWS * 16;         // [4 tiles][8 boxes] int: the producer's pool rows
     static constexpr int seen = rows + 4 * 8 * 4;         // [GROUPS][TILE] bytes: some row of the group sees the key
-    static constexpr int scan = seen + GROUPS * TILE;    // 32 long long, then the walk's start
-    static constexpr int bars = scan + 32 * 8 + 64;
+    static constexpr int scan = seen + GROUPS * TILE;    // 32 int, then the walk's start
+    static constexpr int info = scan + 32 * 4 + 16;      // [ROWS] 16 bytes: what the epilogue writes
+    static constexpr int bars = info + ROWS * 16;
     static constexpr int MAX_NS = 6;
     static constexpr int FULL = 0, EMPTY = MAX_NS, S_FULL = 2 * MAX_NS, S_FREE = S_FULL + NB, P_FULL = S_FREE + NB,
                          PV_DONE = P_FULL + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1, DRAIN = O_FREE + 1,
@@ -232,7 +242,7 @@ struct Band {
 // Band of row group `grp` (group_rows rows) of sequence b.  It follows from
 // the lengths alone: with a mask a token's place is only known to lie in
 // [start - 1, start + cnt - 1], and its own tokens' keys are always walked.
-__device__ __forceinline__ Band band_of(const TreeParams& p, int b, int grp, int group_rows, bool record) {
+__device__ __noinline__ Band band_of(const TreeParams& p, int b, int grp, int group_rows, bool record) {
     Band d;
     d.len = p.kv_lens[b];
     d.cnt = p.q_lens ? p.q_lens[b] : p.q_len;
@@ -262,8 +272,8 @@ __device__ __forceinline__ Band band_of(const TreeParams& p, int b, int grp, int
 // Walk over this cluster's range of the items' tiles (an item without tiles
 // counts as one, so that somebody writes its empty rows).
 struct Walk {
-    long long pos, end, base;   // next unit, end of the range, first unit of the current item
-    long long per;
+    int pos, end, base;         // next unit, end of the range, first unit of the current item
+    int per;
     int entry, kvh;             // current item: entry = sequence * groups + row group
     int entries, groups, group_rows;
     Band band;
@@ -277,7 +287,7 @@ struct Walk {
         grp = entry - b * groups;
         band = band_of(p, b, grp, group_rows, false);
     }
-    __device__ __forceinline__ bool next(const TreeParams& p) {
+    __device__ __noinline__ bool next(const TreeParams& p) {
         while (pos < end) {
             const int w = units();
             if (pos >= base + w || (p.num_splits == 1 && pos > base)) {
@@ -291,17 +301,17 @@ struct Walk {
                 }
                 continue;
             }
-            first = static_cast<int>(pos - base);
+            first = pos - base;
             if (p.num_splits == 1) {
                 index = 0;
                 count = 1;
                 n = band.tiles;
                 pos = base + w;
             } else {
-                const int take = static_cast<int>(min(static_cast<long long>(w - first), end - pos));
-                const long long seg0 = base / per;
-                index = static_cast<int>(pos / per - seg0);
-                count = static_cast<int>((base + w - 1) / per - seg0) + 1;
+                const int take = min(w - first, end - pos);
+                const int seg0 = base / per;
+                index = pos / per - seg0;
+                count = (base + w - 1) / per - seg0 + 1;
                 n = min(take, band.tiles);
                 pos += take;
             }
@@ -358,54 +368,50 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
     walk.group_rows = ROWS * cs;
     walk.entries = p.batch * p.row_groups;
     {
-        long long* s_scan = reinterpret_cast<long long*>(smem + C::scan);
-        long long* s_at = s_scan + 32;                   // start's entry, unit
+        int* s_scan = reinterpret_cast<int*>(smem + C::scan);
+        int* s_at = s_scan + 32;                         // start's entry, unit
         constexpr int NW = THREADS / 32;
         const int clusters = gridDim.x / cs, me = blockIdx.x / cs;
-        auto entry_units = [&](int e, bool record) -> long long {
+        auto entry_units = [&](int e, bool record) -> int {
             if (e >= walk.entries) return 0;
             const int eb = e / walk.groups;
             const Band d = band_of(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
-            return static_cast<long long>(max(1, d.tiles)) * p.n_kv_heads;
+            return max(1, d.tiles) * p.n_kv_heads;
         };
-        long long total = 0, mine0 = 0;                  // mine0: entry tid's units
+        int total = 0, mine0 = 0;                        // mine0: entry tid's units
         for (int e = tid; e < walk.entries; e += THREADS) {
-            const long long u = entry_units(e, blockIdx.x == 0);
+            const int u = entry_units(e, blockIdx.x == 0);
             if (e == tid) mine0 = u;
             total += u;
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total = __reduce_add_sync(0xffffffffu, total);
         if (lane == 0) s_scan[warp] = total;
         __syncthreads();
-        total = 0;
-        for (int w = 0; w < NW; ++w) total += s_scan[w];
+        total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
         // ranges short enough to balance, long enough that no item has more
         // than num_splits segments
         walk.per = (total + clusters - 1) / clusters;
-        if (p.num_splits > 1)
-            walk.per = max(walk.per, static_cast<long long>((p.max_tiles + p.num_splits - 2) / (p.num_splits - 1)));
-        walk.per = max(walk.per, 1ll);
-        walk.pos = me * walk.per;
-        walk.end = min(total, walk.pos + walk.per);
-        long long before = 0;
+        if (p.num_splits > 1) walk.per = max(walk.per, p.min_range);
+        walk.per = max(walk.per, 1);
+        const long long begin = static_cast<long long>(me) * walk.per;
+        walk.pos = static_cast<int>(min(begin, static_cast<long long>(total)));
+        walk.end = min(total - walk.pos, walk.per) + walk.pos;
+        int before = 0;
         if (walk.pos < walk.end) {
             for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
-                const long long u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
-                long long x = u;
+                const int u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
+                int x = u;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
                     if (lane >= o) x += y;
                 }
                 __syncthreads();
                 if (lane == 31) s_scan[warp] = x;
                 __syncthreads();
-                long long sum = before;
-                for (int w = 0; w < NW; ++w) {
-                    if (w == warp) x += sum;
-                    sum += s_scan[w];
-                }
+                const int ws = lane < NW ? s_scan[lane] : 0;
+                x += before + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+                const int sum = before + __reduce_add_sync(0xffffffffu, ws);
                 if (walk.pos >= x - u && walk.pos < x) {
                     s_at[0] = e0 + tid;
                     s_at[1] = x - u;
@@ -415,13 +421,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             }
         }
         __syncthreads();
-        walk.entry = static_cast<int>(s_at[0]);
+        walk.entry = s_at[0];
         walk.kvh = 0;
         walk.base = s_at[1];
         if (walk.pos < walk.end) {
             walk.load(p);
-            walk.kvh = static_cast<int>((walk.pos - walk.base) / walk.units());
-            walk.base += static_cast<long long>(walk.kvh) * walk.units();
+            walk.kvh = (walk.pos - walk.base) / walk.units();
+            walk.base += walk.kvh * walk.units();
         }
     }
     if (cs > 1) cluster_sync_all(); else __syncthreads();
@@ -442,6 +448,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         bool ok = true;
         int seq = 0;
         auto load_tile = [&](const CUtensorMap* tm, int kvh, const int* rows) {
+#pragma unroll 1
             for (int c = 0; c < C::SLOTS; ++c) {
                 const bool mine = owner == rank;
                 if (use > 0) {
@@ -495,16 +502,20 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 }
                 return page * p.page_size + pos % p.page_size;
             };
-            int row = row_of(0);
-            for (int j = 0; j < n + LOOK && ok; ++j) {
-                const int row_next = row_of(j + 1);          // a step ahead of its use
-                if (j < n) {
-                    if (lane < 8) s_rows[(j & 3) * 8 + lane] = row;
+            // K(0) .. K(LOOK - 1), then K(j) V(j - LOOK) by turns
+            int row_next = n > 0 ? row_of(0) : oob;          // of K(j), a step ahead of its use
+            for (int j2 = 0; j2 < 2 * (n + LOOK) && ok; ++j2) {
+                const int j = j2 >> 1, t = j - LOOK;
+                const bool v = j2 & 1;
+                if (v ? t < 0 : j >= n) continue;
+                const int slot_rows = ((v ? t : j) & 3) * 8;
+                if (!v) {
+                    const int row = row_next;
+                    row_next = row_of(j + 1);
+                    if (lane < 8) s_rows[slot_rows + lane] = row;
                     __syncwarp();
-                    load_tile(&tmk, walk.kvh, s_rows + (j & 3) * 8);
                 }
-                if (ok && j >= LOOK) load_tile(&tmv, walk.kvh, s_rows + ((j - LOOK) & 3) * 8);
-                row = row_next;
+                load_tile(v ? &tmv : &tmk, walk.kvh, s_rows + slot_rows);
             }
         }
         // after an abort: no copy may land once this CTA has gone
@@ -645,22 +656,22 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
         float* s_red = reinterpret_cast<float*>(smem + C::red);
         float* s_mult = reinterpret_cast<float*>(smem + C::mult);
-        int* s_place = reinterpret_cast<int*>(smem + C::place);
-        int* s_tok = reinterpret_cast<int*>(smem + C::tok);
+        int4* s_see = reinterpret_cast<int4*>(smem + C::see);
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
         int g = 0;                                           // running tile number
         int sbuf = 0;
         uint32_t suse = 0;
         int ring_base = 0;                                   // ring entries of the segments before
-        while (walk.next(p)) {
+        // Brings a segment's Q and tables in: after the S^T tiles of the last
+        // segment (its Q has been read by then) and while its last P V runs.
+        auto prologue = [&]() {
             const Band& bd = walk.band;
             const int n = walk.n, b = walk.b;
             const int row0 = (walk.grp * cs + rank) * ROWS;
             const int tok0 = row0 / G;
             if (n > 0) {
-                // ---- Q: rows as K-major B operand, zeros where there is no row.
-                // The last segment's S^T tiles have been read, so its Q has too.
+                // Q: rows as K-major B operand, zeros where there is no row
                 constexpr int PER = ROWS / SW;               // rows of a warp: 4
                 uint4 x[PER][2];
 #pragma unroll
@@ -740,17 +751,63 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C::Q_FULL]);
             }
-            // ---- what the rows are (tables of this segment visible to all after it)
             if (n == 0) bar_sync(ALL, SW * 32);
             bar_sync(ALL, SW * 32);
             if (sw < ROWS / 32) {
+                // row r sees key k iff k <= x and (k > y or k is a sink), and
+                // its mask (from word z on) allows; x = INT_MIN: nothing
                 const int r = sw * 32 + lane, t = (row0 + r) / G;
                 const bool real = t < bd.cnt && bd.start + t >= 0;
-                s_place[r] = real ? bd.start + (p.tree_mask && n > 0 ? s_depth[t] : t) : 0;
-                s_tok[r] = real ? t : -1;
+                const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
+                s_see[r] = make_int4(!real ? INT_MIN : p.tree_mask ? bd.len : place,
+                                     p.window > 0 ? place - p.window : INT_MIN, real ? (t - tok0) * W : 0, 0);
             }
             bar_sync(ALL, SW * 32);
-
+        };
+        int done = -1;                                       // tiles of the segment whose O is to be read, -1: none
+        bool direct = false;                                 // its rows are whole
+        for (;;) {
+            const bool have = walk.next(p);
+            if (have) prologue();
+            if (done >= 0) {
+                // ---- O of the last segment: four 128-element blocks, this
+                // thread's element of each; the new one's S^T runs meanwhile
+                if (!have) bar_sync(bar, 128);               // what to write is in shared memory
+                if (done > 0) ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+                if (!(ok = pair::bar_and(ALL, SW * 32, ok))) break;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int o = 0; o < 4; ++o) {
+                    uint32_t r[GW];
+                    if (done > 0) {
+                        pair::tmem_ld16(tmem + lanes + C::TM_O + static_cast<uint32_t>(o * ROWS + col0), r);
+                        tmem_ld_wait();
+                        if (o == 3) {
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars[C::O_FREE]);
+                        }
+                    }
+                    const int d = o * 128 + kk;
+#pragma unroll
+                    for (int i = 0; i < GW; ++i) {
+                        const uint4 info = *reinterpret_cast<const uint4*>(smem + C::info + (col0 + i) * 16);
+                        const float f = __uint_as_float(info.z);
+                        const size_t at = (static_cast<size_t>(info.y) << 32 | info.x) * D + d;
+                        const float val = f != 0.f ? __uint_as_float(r[i]) * f : 0.f;
+                        if (info.w) {
+                            if (direct)
+                                p.out[at] = __float2bfloat16_rn(val);
+                            else
+                                p.ws_o[at] = val;
+                        }
+                    }
+                }
+            }
+            if (!have) break;
+            const Band bd = walk.band;
+            const int n = walk.n, first = walk.first;
+            const int row0 = (walk.grp * cs + rank) * ROWS;
             float m[GW], l[GW];
 #pragma unroll
             for (int i = 0; i < GW; ++i) {
@@ -760,7 +817,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             bool out = false;
             bool fresh = true;                               // some row may not have a reference yet
             for (int t = 0; t < n; ++t, ++g) {
-                const int key0 = bd.key0(walk.first + t), key = key0 + kk;
+                const int key0 = bd.key0(first + t), key = key0 + kk;
                 ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
@@ -793,17 +850,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                                    (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
                 bool seen = true;                            // by some row of the group
                 if (!whole) {
-                    const bool live = key < bd.hi && (key >= bd.lo || key < bd.sink_end);
                     const int c = key - bd.start;
+                    const bool drafted = c >= 0 && p.tree_mask;
+                    // the key's place; its own mask says whether a drafted one is seen
+                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
+                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
+                    const bool sink = kp < bd.sink_end;
+                    uint32_t bits = 0xffffffffu;
+                    if (drafted && key < bd.hi) {
+                        bits = 0u;
+#pragma unroll
+                        for (int i = 0; i < GW; ++i)
+                            bits |= ((s_mask[s_see[col0 + i].z + (c >> 5)] >> (c & 31)) & 1u) << i;
+                    }
                     seen = false;
-                    const int kp = c < 0 || !p.tree_mask ? key : bd.start + s_depth[max(0, min(c, bd.cnt - 1))];
 #pragma unroll
                     for (int i = 0; i < GW; ++i) {
-                        const int tk = s_tok[col0 + i], pl = s_place[col0 + i];
-                        bool see = live && tk >= 0;
-                        if (see && c >= 0)
-                            see = p.tree_mask ? (s_mask[(tk - tok0) * W + (c >> 5)] >> (c & 31)) & 1u : c <= tk;
-                        if (p.window > 0) see = see && (kp > pl - p.window || kp < p.n_sinks);
+                        const int4 r = s_see[col0 + i];
+                        const bool see = last <= r.x && (kp > r.y || sink) && ((bits >> i) & 1u);
                         x[i] = see ? x[i] : -INFINITY;
                         seen = seen || see;
                     }
@@ -829,20 +893,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     for (int i = 0; i < GW; ++i) {
                         // growth over the reference (over 0 where there was none)
                         const float up = __shfl_sync(0xffffffffu, top, i);
-                        float a = 1.f;
-                        if (m[i] == -INFINITY) {
-                            if (up > -INFINITY) {
-                                m[i] = up;
-                                x[i] -= up;
-                            } else {
-                                fresh = true;
-                            }
-                        } else if (up > 0.f) {
-                            a = fast_exp2(-up);
-                            m[i] += up;
-                            x[i] -= up;
-                            l[i] *= a;
-                        }
+                        const bool none = m[i] == -INFINITY;
+                        const float shift = none ? (up == -INFINITY ? 0.f : up) : fmaxf(up, 0.f);
+                        const float a = none ? 1.f : fast_exp2(-shift);
+                        m[i] = none ? up : m[i] + shift;
+                        x[i] -= shift;
+                        l[i] *= a;
+                        fresh = fresh || m[i] == -INFINITY;
                         mine = lane == i ? a : mine;
                     }
                     if (t > 0) {
@@ -946,66 +1003,43 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 if (lane == 0) mbar_arrive(&bars[C::P_FULL]);
             }
             ring_base += 2 * n * C::SLOTS;
-            if (n > 0 && ok) ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
             // all go on or all stop (here or at a vote inside a tile): no warp
             // may wait at a barrier for one that has left
             if (out || !(ok = pair::bar_and(ALL, SW * 32, ok))) break;
-            tc_fence_after_sync();
             // ---- row sums: lanes, then the four quadrants' warps
             const float part = reduce_columns(l, [](float a, float c) { return a + c; });
             if (lane < GW) s_red[quad * ROWS + col0 + lane] = part;
             bar_sync(bar, 128);
-            const int cl = col0 + (lane & (GW - 1));
-            const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
-            float top = -INFINITY;                           // lane i: row col0 + i % GW
-#pragma unroll
-            for (int i = 0; i < GW; ++i) top = (lane & (GW - 1)) == i ? m[i] : top;
-            const int my_row = row0 + cl, my_tok = my_row / G;
-            const bool mine = my_tok < p.q_len;
-            const bool some = s_tok[cl] >= 0 && top != -INFINITY;
-            const size_t my_out = (static_cast<size_t>(b) * p.q_len + my_tok) * p.n_q_heads + walk.kvh * G + my_row % G;
+            // ---- what to write: O / sum where this is the whole row, else the
+            // unnormalised partial (zeros for a row that saw nothing)
+            direct = walk.count == 1;
             const size_t S = static_cast<size_t>(p.num_splits);
-            const bool direct = walk.count == 1;
-            // O / sum where this is the whole row, else the unnormalised partial
-            const float unit = p.o_scale * (1.f / C::P_SCALE);
-            const float factor = !some ? 0.f : direct ? unit / sum : unit;
-            if (quad == 0 && lane < GW && mine) {
-                if (direct) {
-                    if (p.lse) p.lse[my_out] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
-                } else {
-                    float* ml = p.ws_ml + (my_out * S + walk.index) * 2;
-                    ml[0] = some ? top : -INFINITY;
-                    ml[1] = some ? sum : 0.f;
+            if (quad == 0) {
+                float top = -INFINITY;                       // lane i: row col0 + i
+#pragma unroll
+                for (int i = 0; i < GW; ++i) top = lane == i ? m[i] : top;
+                const int cl = col0 + (lane & (GW - 1)), r = row0 + cl, t = r / G;
+                const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
+                const bool some = s_see[cl].x != INT_MIN && top != -INFINITY;
+                const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
+                const size_t at = direct ? row : row * S + walk.index;
+                const float unit = p.o_scale * (1.f / C::P_SCALE);
+                const float factor = !some ? 0.f : direct ? unit / sum : unit;
+                if (lane < GW) {
+                    const bool mine = t < p.q_len;
+                    *reinterpret_cast<uint4*>(smem + C::info + cl * 16) =
+                        make_uint4(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), __float_as_uint(factor), mine);
+                    if (mine && direct && p.lse)
+                        p.lse[row] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+                    if (mine && !direct) {
+                        p.ws_ml[at * 2] = some ? top : -INFINITY;
+                        p.ws_ml[at * 2 + 1] = some ? sum : 0.f;
+                    }
                 }
             }
             if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0 && rank == 0)
                 p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
-#pragma unroll 1
-            for (int o = 0; o < 4; ++o) {
-                uint32_t r[GW];
-                if (n > 0) {
-                    pair::tmem_ld16(tmem + lanes + C::TM_O + static_cast<uint32_t>(o * ROWS + col0), r);
-                    tmem_ld_wait();
-                }
-                if (o == 3) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0 && n > 0) mbar_arrive(&bars[C::O_FREE]);
-                }
-                const int d = o * 128 + kk;
-#pragma unroll
-                for (int i = 0; i < GW; ++i) {
-                    const float f = __shfl_sync(0xffffffffu, factor, i);
-                    const size_t row = __shfl_sync(0xffffffffu, my_out, i);
-                    const bool there = __shfl_sync(0xffffffffu, mine ? 1 : 0, i);
-                    if (!there) continue;
-                    const float val = f != 0.f ? __uint_as_float(r[i]) * f : 0.f;
-                    if (direct)
-                        p.out[row * D + d] = __float2bfloat16_rn(val);
-                    else
-                        p.ws_o[(row * S + walk.index) * D + d] = val;
-                }
-            }
+            done = n;
         }
     }
     // all threads of all CTAs: no copy or arrival may reach a CTA that has gone

@@ -70,6 +70,7 @@ struct TreeParams {
     int batch, q_len, n_q_heads, n_kv_heads, group, mask_words;
     int rows, cluster, row_groups; // TreeShape
     int max_tiles;                 // most key tiles of an item
+    int min_range;                 // shortest range of tiles that keeps an item to num_splits segments
     int page_size, num_pages, max_pages_per_seq, len_cap;
     int window, n_sinks;
     int num_splits;                // most segments of an item; 1: no partials
