@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(CSRC, "_build")
 OUT = os.path.join(HERE, "libfa512.so")
 SOURCES = ["api.cu", "prefill_so_sm103.cu", "prefill256_sm103.cu", "decode_sm103.cu", "decode_noalloc.cu",
-           "decode_tree_sm103.cu", "cache_sm103.cu"]
+           "decode_tree_sm103.cu", "decode_tree_pair_sm103.cu", "cache_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

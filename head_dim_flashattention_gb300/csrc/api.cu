@@ -766,12 +766,12 @@ namespace {
 // the tiles of its band (with a window: the window, the places its rows span
 // and one tile more for a band that starts inside a tile).
 long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks) {
-    const int tile = fa512::tree_tile();
     const fa512::TreeShape s = fa512::tree_shape(q_len, group);
+    const int tile = s.tile;
     const long long all = (static_cast<long long>(max_kv_len) + tile - 1) / tile;
     if (window <= 0) return all;
     // a run's rows span their own tokens; a masked tree's all of its tokens
-    const long long span = static_cast<long long>(s.rows) * s.cluster / group + 2;
+    const long long span = static_cast<long long>(s.rows) / group + 2;
     const long long tokens = q_len <= fa512::tree_max_nodes() || q_len < span ? q_len : span;
     const long long band = (static_cast<long long>(window) + tokens + 1 + tile - 1) / tile + 1;
     const long long sinks = (static_cast<long long>(n_sinks) + tile - 1) / tile;
@@ -875,7 +875,6 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.group = G;
     const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
     p.rows = shape.rows;
-    p.cluster = shape.cluster;
     p.row_groups = shape.groups;
     p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks));
     p.min_range = splits > 1 ? (p.max_tiles + splits - 2) / (splits - 1) : 0;
@@ -897,8 +896,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(n_kv_heads),
                               static_cast<uint64_t>(num_pages) * page_size};
     const uint64_t strides[2] = {kHeadDim * eb, static_cast<uint64_t>(n_kv_heads) * kHeadDim * eb};
-    const uint32_t tile = static_cast<uint32_t>(fa512::tree_tile()), page = static_cast<uint32_t>(page_size);
-    const uint32_t box[3] = {static_cast<uint32_t>(128 / eb), 1u, page < tile ? page : tile};
+    const uint32_t box[3] = {static_cast<uint32_t>(128 / eb), 1u, static_cast<uint32_t>(page_size < 128 ? page_size : 128)};
     CUtensorMap tmk, tmv;
     const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     fa512_status st = encode_map(&tmk, type, CU_TENSOR_MAP_SWIZZLE_128B, k_pages, 3, dims, strides, box);
@@ -1002,7 +1000,7 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
     const int G = n_q_heads / n_kv_heads;
     const fa512::TreeShape s = fa512::tree_shape(q_len, G);
     const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks);
-    const long long clusters = sm_count() / s.cluster > 0 ? sm_count() / s.cluster : 1;
+    const long long clusters = sm_count() / s.ctas > 0 ? sm_count() / s.ctas : 1;
     const long long per = (static_cast<long long>(batch) * n_kv_heads * s.groups * tiles + clusters - 1) / clusters;
     if (tiles <= 1 || per <= 0) return 1;
     // the ranges of a batch of this length touch ceil(tiles / per) + 1 of an

@@ -1,0 +1,917 @@
+// Tree decode of more than 64 rows per KV head: pairs of SMs, 128 rows each.
+//
+// The single-CTA kernel's products (S^T = K Q^T and O^T += V^T P^T) as 2-SM
+// MMAs M = 256, N = 128: of a tile of 256 keys each CTA holds 128 keys of K
+// (its 128 lanes of S^T, all 128 rows as columns) and the V of all 256 keys
+// for half of the head dim (its 128 lanes of each of the two 256-element
+// blocks of O^T).  So a pair streams every byte once, and a row of N costs an
+// SM half its shared-memory reads: 48 cycles of operand reads per 64-cycle MMA
+// where the single-CTA form reads 48 cycles for half the rows.
+// Tensor memory: O^T 2 x 128 columns, S^T 2 buffers x 128 columns.
+//
+// A CTA's softmax threads hold its 128 keys against all 128 rows; Q and P^T,
+// the B operands, are split by rows, 64 in each CTA, so half of each P^T tile
+// is stored into the other CTA's shared memory.  Both CTAs have to scale by
+// the same references: every tile, each column group (32 rows) swaps its vote
+// on "a score outgrew the reference" with the same group of the other CTA,
+// and, when either says so, the column maxima; at the end of a segment the row
+// sums.
+//
+// Keys that no row sees may hold anything, also NaN, which P = 0 would not
+// silence: in the tiles where some may be (a sequence's end, a window's edges,
+// the drafted tokens) V arrives on barriers of its own, the softmax threads
+// clear the rows of such keys and hand each slot to the MMA themselves.
+#include <cuda.h>
+
+#include "fa512_tree.cuh"
+
+namespace fa512 {
+namespace tree {
+namespace pairs {
+
+using namespace fa512::pair;
+using tree::wait_or_abort;
+using tree::bar_sync;
+
+constexpr int TILE = 256;                // keys per tile
+constexpr int HALF_TILE = 128;           // keys of a CTA
+constexpr int ROWS = 128;
+constexpr int HALF_ROWS = 64;            // rows of a CTA's B operands
+constexpr int GW = 32;                   // rows (columns of S^T) of a softmax warp
+constexpr int GROUPS = ROWS / GW;
+constexpr int SW = 4 * GROUPS;           // softmax warps: (column group, TMEM lane quadrant)
+constexpr int THREADS = 64 + SW * 32;
+constexpr int LOOK = 1;                  // S^T tiles computed ahead of O^T += V^T P^T
+constexpr int NB = LOOK + 1;
+constexpr int NS = 3;                    // ring slots
+constexpr uint32_t TM_O = 0, TM_S = 256;
+using Walk = WalkOf<TILE>;
+using Band = BandOf<TILE>;
+
+template <bool FP8>
+struct Cfg {
+    static constexpr int EB = FP8 ? 1 : 2;
+    static constexpr int CHUNKS = D * EB / 128;          // 128-byte column chunks of the head dim
+    static constexpr int SLOTS = CHUNKS / 2;             // ring slots of a K (V) tile in a CTA: 4 or 2
+    static constexpr int Q_CHUNK = HALF_ROWS * 128;
+    static constexpr int Q_TERM = CHUNKS * Q_CHUNK;
+    static constexpr int Q_TERMS = FP8 ? 2 : 1;
+    static constexpr int P_LINE = HALF_ROWS * EB;        // a key's values of this CTA's rows
+    static constexpr int P_TERM = TILE * P_LINE;
+    static constexpr int P_TERMS = FP8 ? 3 : 1;
+    static constexpr float THR = FP8 ? 4.f : 8.f;
+    static constexpr float P_SCALE = FP8 ? 2048.f : 1.f;
+    // shared memory, from a 1 KiB aligned base
+    static constexpr int ring = 0;
+    static constexpr int q = ring + NS * SLOT;
+    static constexpr int p = q + Q_TERMS * Q_TERM;
+    static constexpr int mask = p + P_TERMS * P_TERM;    // [ROWS tokens][words]
+    static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
+    static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
+    static constexpr int m = red + 4 * ROWS * 4;         // [ROWS] float: references
+    static constexpr int mb = m + ROWS * 4;              // [ROWS] float2: score -> log2 units, less the reference
+    static constexpr int see = mb + ROWS * 8;            // [ROWS] int4: last key, key below the window, mask row
+    static constexpr int info = see + ROWS * 16;         // [ROWS] 16 bytes: what the epilogue writes
+    static constexpr int rows = info + ROWS * 16;        // [4 tiles][16 boxes] int: the producer's pool rows
+    static constexpr int seen = rows + 4 * 16 * 4;       // [GROUPS][HALF_TILE] bytes
+    static constexpr int pseen = seen + GROUPS * HALF_TILE;          // [2][HALF_TILE] int: the other CTA's keys
+    static constexpr int vote = pseen + 2 * HALF_TILE * 4;           // [2][GROUPS] int
+    static constexpr int top = vote + 2 * GROUPS * 4;                // [2][ROWS] float
+    static constexpr int scan = top + 2 * ROWS * 4;
+    static constexpr int bars = scan + 160;
+    static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, S_FULL = 4 * NS, S_FREE = S_FULL + NB,
+                         P_FULL = S_FREE + NB, PV_DONE = P_FULL + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
+                         DRAIN = O_FREE + 1, VOTE = DRAIN + 1, TOP = VOTE + 2 * GROUPS, SEEN = TOP + 2 * GROUPS,
+                         N_BARS = SEEN + 2;
+    static constexpr int misc = bars + N_BARS * 8;       // tmem address, abort flag
+    static constexpr int total = misc + 16;
+    static_assert(total + 1024 <= 232448, "shared memory of an SM");
+};
+
+__device__ __forceinline__ void mma2_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                 ::"r"(addr), "r"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+// Orders this thread's shared-memory writes, in either CTA, before later
+// accesses of them by the async proxy (the tensor cores).
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Waits, bounded, with cluster-scope acquire: for arrivals of the other CTA.
+static __device__ __noinline__ bool wait_cluster_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    const uint32_t a = smem_u32(bar);
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_cluster(a, parity)) return true;
+        if ((i & 255u) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                report_error(err, FA512_DEVICE_ERR_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    return mbar_try_wait_cluster(smem_u32(bar), parity) || wait_cluster_slow(bar, parity, err, abort);
+}
+
+// Reduces 32 values per lane over the warp at once: lane i gets everyone's
+// v[i] (31 shuffles in which halves swap the values that the other half keeps).
+template <class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = GW / 2; o >= 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float keep = up ? v[j + o] : v[j], give = up ? v[j] : v[j + o];
+            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+    return v[0];
+}
+
+// A tile of cached keys inside every row's window: no key of it needs a mask.
+__device__ __forceinline__ bool whole_tile(const TreeParams& p, const Band& bd, int key0) {
+    return key0 + TILE <= min(bd.start, bd.hi) &&
+           (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(THREADS, 1)
+tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                 const __grid_constant__ TreeParams p) {
+    using C = Cfg<FP8>;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::bars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    auto bar_of = [&](int i, int cta) -> uint32_t { return map_to_cta(smem_u32(&bars[i]), cta); };
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bars[C::FULL + i], 1);
+            mbar_init(&bars[C::EMPTY + i], 1);
+            mbar_init(&bars[C::V_RAW + i], 1);
+            mbar_init(&bars[C::V_CLEAN + i], 2 * SW);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&bars[C::S_FULL + i], 1);
+            mbar_init(&bars[C::S_FREE + i], 2 * SW);
+        }
+        mbar_init(&bars[C::P_FULL], 2 * SW);
+        mbar_init(&bars[C::PV_DONE], 1);
+        mbar_init(&bars[C::Q_FULL], 2 * SW);
+        mbar_init(&bars[C::O_FREE], 2 * SW);
+        mbar_init(&bars[C::DRAIN], 1);
+        for (int i = 0; i < 2 * GROUPS; ++i) {
+            mbar_init(&bars[C::VOTE + i], 1);
+            mbar_init(&bars[C::TOP + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&bars[C::SEEN + i], 1);
+        *abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    // ---- this pair's range of the items' tiles
+    Walk walk;
+    walk.groups = p.row_groups;
+    walk.group_rows = ROWS;
+    start_walk<TILE, THREADS>(walk, p, gridDim.x / 2, blockIdx.x / 2, reinterpret_cast<int*>(smem + C::scan));
+    cluster_sync_all();
+    if (warp == 1) {
+        tmem_alloc2(tmem_slot, 512);
+        tmem_relinquish2();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        // Each CTA loads its own operands; a slot of both is counted on the
+        // leader's barrier, a slot of V that has to be cleared on each CTA's own.
+        const int oob = p.num_pages * p.page_size;           // past the pool: filled with zeros
+        const int box_rows = min(p.page_size, HALF_TILE), boxes = HALF_TILE / box_rows;
+        int* s_rows = reinterpret_cast<int*>(smem + C::rows);
+        int slot = 0;
+        uint32_t use = 0;
+        bool ok = true;
+        uint32_t raw_used = 0, full_used = 0;                // per slot: parity of the uses of the two barriers
+        while (ok && walk.next(p)) {
+            const int n = walk.n;
+            const Band& d = walk.band;
+            // lane i: pool row of box i of tile t, or oob where no row sees a position of it
+            auto row_of = [&](int t) -> int {
+                if (t >= n || lane >= 2 * boxes) return oob;
+                const int pos = d.key0(walk.first + t) + lane * box_rows;
+                if (pos >= d.hi || !(pos + box_rows > d.lo || pos < d.sink_end)) return oob;
+                const int page = p.page_table[static_cast<size_t>(walk.b) * p.max_pages_per_seq + pos / p.page_size];
+                if (page < 0 || page >= p.num_pages) {
+                    report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                    return oob;
+                }
+                return page * p.page_size + pos % p.page_size;
+            };
+            // K(0), then K(j) V(j - 1) by turns
+            int row_next = n > 0 ? row_of(0) : oob;          // of K(j), a step ahead of its use
+#pragma unroll 1
+            for (int j2 = 0; j2 < 2 * (n + LOOK) && ok; ++j2) {
+                const int j = j2 >> 1;
+                const bool v = j2 & 1;
+                const int t = v ? j - LOOK : j;
+                if (t < 0 || t >= n) continue;
+                int* rows = s_rows + (t & 3) * 16;
+                if (!v) {
+                    const int row = row_next;
+                    row_next = row_of(j + 1);
+                    if (lane < 16) rows[lane] = row;
+                    __syncwarp();
+                }
+                const bool raw = v && !whole_tile(p, d, d.key0(walk.first + t));
+                const CUtensorMap* tm = v ? &tmv : &tmk;
+#pragma unroll 1
+                for (int c = 0; c < C::SLOTS; ++c) {
+                    if (use > 0) {
+                        ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::EMPTY + slot], (use & 1) ^ 1, p.err, abort));
+                        if (!ok) break;
+                    }
+                    if (elect_one()) {
+                        uint64_t* full = &bars[(raw ? C::V_RAW : C::FULL) + slot];
+                        const uint32_t bar = raw ? smem_u32(full) : bar_of(C::FULL + slot, 0);
+                        if (raw) mbar_arrive_expect_tx(full, SLOT);
+                        else if (rank == 0) mbar_arrive_expect_tx(full, 2 * SLOT);
+#pragma unroll
+                        for (int side = 0; side < 2; ++side) {
+                            // K: columns of chunk 2c + side, this CTA's keys.  V: bf16 block c / 2, key
+                            // half c % 2, its 64 elements `side`; FP8 block c, key half `side`.
+                            const int col = !v ? (2 * c + side) * (128 / C::EB)
+                                               : FP8 ? 256 * c + 128 * rank : 256 * (c >> 1) + 128 * rank + 64 * side;
+                            const int half = !v ? rank : FP8 ? side : c & 1;
+                            uint8_t* dst = smem + C::ring + slot * SLOT + side * SIDE;
+#pragma unroll 1
+                            for (int i = 0; i < boxes; ++i) {
+                                tma2_load_3d(dst, tm, bar, col, walk.kvh, rows[half * boxes + i]);
+                                dst += box_rows * 128;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (raw) raw_used ^= 1u << slot; else full_used ^= 1u << slot;
+                    if (++slot == NS) {
+                        slot = 0;
+                        ++use;
+                    }
+                }
+            }
+        }
+        // after an abort: no copy may land once this CTA has gone (the leader
+        // sees its own and the other's slots, the other its clearing slots;
+        // the cluster's barrier at the end holds both)
+        if (!ok)
+            for (int i = 0; i < NS; ++i) {
+                if (rank == 0) (void)mbar_wait(&bars[C::FULL + i], ((full_used >> i) & 1) ^ 1, p.err);
+                (void)mbar_wait(&bars[C::V_RAW + i], ((raw_used >> i) & 1) ^ 1, p.err);
+            }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ------------------------------------------------------------ MMA issue, both SMs
+            const uint32_t ring = smem_u32(smem + C::ring);
+            const uint64_t qd = make_sdesc_sw128(smem_u32(smem + C::q), 16, 1024);
+            const uint64_t pd = make_sdesc_lines<C::P_LINE>(smem_u32(smem + C::p));
+            constexpr uint32_t IDESC_QK = idesc_shape(2 * 128, ROWS) | (FP8 ? 0u : BF16_AB);
+            constexpr uint32_t IDESC_PV = idesc_shape(2 * 128, ROWS) | (FP8 ? B_E5M2 : BF16_AB) | A_MN | B_MN;
+            bool ok = true;
+            int slot = 0, segment = 0, g_p = 0, sbuf = 0;
+            uint32_t suse = 0, full_used = 0, clean_used = 0;
+            auto wait = [&](int bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait_cluster(&bars[bar], parity, p.err, abort));
+            };
+            auto next_slot = [&]() {
+                if (++slot == NS) slot = 0;
+            };
+            auto issue_qk = [&]() -> bool {
+                if (suse > 0 && !wait(C::S_FREE + sbuf, (suse & 1) ^ 1)) return false;
+                const uint32_t sb = tmem + TM_S + static_cast<uint32_t>(sbuf * ROWS);
+#pragma unroll 1
+                for (int c = 0; c < C::SLOTS; ++c) {
+                    if (!wait(C::FULL + slot, (full_used >> slot) & 1)) return false;
+                    full_used ^= 1u << slot;
+                    tc_fence_after_sync();
+                    const uint64_t kd = make_sdesc_sw128(ring + slot * SLOT, 16, 1024);
+                    const uint64_t qc = qd + static_cast<uint64_t>((c * 2 * C::Q_CHUNK) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {        // 32 bytes of the head dim at a time
+                            const uint64_t a = kd + static_cast<uint64_t>(((k >> 2) * SIDE + (k & 3) * 32) >> 4);
+                            const uint64_t q = qc + static_cast<uint64_t>(((k >> 2) * C::Q_CHUNK + (k & 3) * 32) >> 4);
+                            if constexpr (FP8) {
+                                mma2_f8(sb, a, q, IDESC_QK, (c | k) ? 1u : 0u);
+                                mma2_f8(sb, a, q + static_cast<uint64_t>(C::Q_TERM >> 4), IDESC_QK, 1u);
+                            } else {
+                                mma2_ss(sb, a, q, IDESC_QK, (c | k) ? 1u : 0u);
+                            }
+                        }
+                        commit2_both(&bars[C::EMPTY + slot]);
+                        if (c == C::SLOTS - 1) commit2_both(&bars[C::S_FULL + sbuf]);
+                    }
+                    __syncwarp();
+                    next_slot();
+                }
+                if (++sbuf == NB) {
+                    sbuf = 0;
+                    ++suse;
+                }
+                return true;
+            };
+            auto issue_pv = [&](bool fresh, bool raw) -> bool {
+                if (!wait(C::P_FULL, g_p & 1)) return false;
+                const uint32_t acc0 = fresh ? 0u : 1u;
+#pragma unroll 1
+                for (int c = 0; c < C::SLOTS; ++c) {
+                    uint32_t& used = raw ? clean_used : full_used;
+                    if (!wait((raw ? C::V_CLEAN : C::FULL) + slot, (used >> slot) & 1)) return false;
+                    used ^= 1u << slot;
+                    tc_fence_after_sync();
+                    const uint64_t vd = make_sdesc_sw128(ring + slot * SLOT, SIDE, 1024);
+                    if (elect_one()) {
+                        if constexpr (FP8) {
+                            // block c of the head dim, both key halves
+                            const uint32_t ob = tmem + TM_O + static_cast<uint32_t>(c * ROWS);
+#pragma unroll
+                            for (int k = 0; k < TILE / 32; ++k)
+#pragma unroll
+                                for (int e = 0; e < C::P_TERMS; ++e)
+                                    mma2_f8(ob, vd + static_cast<uint64_t>((k * 32 * 128) >> 4),
+                                            pd + static_cast<uint64_t>((e * C::P_TERM + k * 32 * C::P_LINE) >> 4),
+                                            IDESC_PV, (k | e) ? 1u : acc0);
+                        } else {
+                            // block c / 2, key half c % 2
+                            const uint32_t ob = tmem + TM_O + static_cast<uint32_t>((c >> 1) * ROWS);
+                            const uint64_t ph = pd + static_cast<uint64_t>(((c & 1) * HALF_TILE * C::P_LINE) >> 4);
+#pragma unroll
+                            for (int k = 0; k < HALF_TILE / 16; ++k)
+                                mma2_ss(ob, vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
+                                        ph + static_cast<uint64_t>((k * 16 * C::P_LINE) >> 4), IDESC_PV,
+                                        (k | (c & 1)) ? 1u : acc0);
+                        }
+                        commit2_both(&bars[C::EMPTY + slot]);
+                        if (c == C::SLOTS - 1) commit2_both(&bars[C::PV_DONE]);
+                    }
+                    __syncwarp();
+                    next_slot();
+                }
+                ++g_p;
+                return true;
+            };
+            while (ok && walk.next(p)) {
+                const int n = walk.n;
+                if (n == 0) continue;
+                if (!(ok = wait(C::Q_FULL, segment & 1))) break;
+#pragma unroll 1
+                for (int j = 0; j < n + LOOK && ok; ++j) {
+                    if (j < n) ok = issue_qk();
+                    if (ok && j >= LOOK) {
+                        // an item's first P V overwrites O: the last one's must have been read
+                        if (j == LOOK && segment > 0) {
+                            ok = wait(C::O_FREE, (segment - 1) & 1);
+                            tc_fence_after_sync();
+                        }
+                        if (ok)
+                            ok = issue_pv(j == LOOK,
+                                          !whole_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK)));
+                    }
+                }
+                ++segment;
+            }
+            if (elect_one()) commit2_local(&bars[C::DRAIN]);
+            __syncwarp();
+            (void)mbar_wait(&bars[C::DRAIN], 0, p.err);
+        }
+    } else {
+        // -------------------------------------------------------------------- softmax
+        const int sw = warp - 2, quad = warp & 3, grp = sw >> 2;
+        const int bar = 1 + grp;                             // the column group's four warps
+        constexpr int ALL = 7;                               // barrier of all softmax warps
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const int kk = quad * 32 + lane;                     // this thread's key of the CTA's half
+        const int col0 = grp * GW;                           // its rows
+        const int W = p.mask_words, G = p.group;
+        const int peer = rank ^ 1;
+        const bool speaker = (sw & 3) == 0;                  // the group's warp that talks to the other CTA
+        int* s_depth = reinterpret_cast<int*>(smem + C::depth);
+        uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
+        float* s_red = reinterpret_cast<float*>(smem + C::red);
+        float* s_m = reinterpret_cast<float*>(smem + C::m);
+        float2* s_mb = reinterpret_cast<float2*>(smem + C::mb);
+        int4* s_see = reinterpret_cast<int4*>(smem + C::see);
+        uint8_t* s_seen = smem + C::seen;
+        bool ok = true;
+        int g = 0;                                           // running tile number
+        int sbuf = 0, swaps = 0, partial_tiles = 0;          // S^T buffer; column swaps, tiles with masks so far
+        uint32_t suse = 0, raw_used = 0;
+        int ring_base = 0;                                   // ring entries of the segments before, mod NS
+
+        // Swaps a value per column (lane) with the same group of the other
+        // CTA; the answer comes to every warp of the group.
+        auto swap_columns = [&](float v) -> float {
+            const int par = swaps & 1;
+            const int at = C::top + (par * ROWS + col0 + lane) * 4;
+            if (speaker) {
+                if (lane == 0) mbar_arrive_expect_tx(&bars[C::TOP + par * GROUPS + grp], 32 * 4);
+                __syncwarp();
+                st_async_b32(map_to_cta(smem_u32(smem + at), peer), __float_as_uint(v), bar_of(C::TOP + par * GROUPS + grp, peer));
+            }
+            const bool got = wait_cluster(&bars[C::TOP + par * GROUPS + grp], (swaps >> 1) & 1, p.err, abort);
+            ok = __all_sync(0xffffffffu, got) && ok;
+            ++swaps;
+            return *reinterpret_cast<volatile float*>(smem + at);
+        };
+
+        // Brings a segment's Q and tables in: after the S^T tiles of the last
+        // segment (its Q has been read by then) and while its last P V runs.
+        auto prologue = [&]() {
+            const Band& bd = walk.band;
+            const int n = walk.n, b = walk.b;
+            const int row0 = walk.grp * ROWS;
+            const int tok0 = row0 / G;
+            bar_sync(ALL, SW * 32);                          // nobody uses the last segment's tables any more
+            if (n > 0) {
+                const int toks = max(0, min((row0 + ROWS - 1) / G, p.q_len - 1) - tok0 + 1);
+                if (p.tree_mask) load_masks(p, b, bd.cnt, tok0, toks, s_depth, s_mask, tid - 64, SW * 32);
+                // Q: this CTA's 64 rows as K-major B operand (FP8: the scales of all 128), zeros where there is no row
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!FP8 && half != rank) continue;
+                    constexpr int PER = HALF_ROWS / SW;      // rows of a warp: 4
+                    uint4 x[PER][2];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int row = row0 + half * HALF_ROWS + sw + i * SW, t = row / G;
+                        const bool real = t < bd.cnt;
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            p.q + ((static_cast<size_t>(b) * p.q_len + (real ? t : 0)) * p.n_q_heads + walk.kvh * G +
+                                   (real ? row - t * G : 0)) * D) + 2 * lane;
+                        x[i][0] = real ? src[0] : make_uint4(0u, 0u, 0u, 0u);
+                        x[i][1] = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int r = sw + i * SW;           // line of the operand
+                        if constexpr (!FP8) {
+                            uint8_t* line = smem + C::q + (lane >> 2) * C::Q_CHUNK + r * 128;
+                            const int c = 2 * (lane & 3);
+                            *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = x[i][0];
+                            *reinterpret_cast<uint4*>(line + (((c + 1) ^ (r & 7)) << 4)) = x[i][1];
+                        } else {
+                            const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                                                   x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                            float amax = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
+                                                         fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+#pragma unroll
+                            for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                            // 2^(7 - exponent of amax): the largest element comes to [128, 256)
+                            const int E = (__float_as_uint(amax) >> 23) & 0xff;
+                            const int biased = min(7 + 2 * 127 - E, 254);
+                            const float qs = (amax > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+                            if (lane == 0) s_mb[half * HALF_ROWS + r] = make_float2(p.scale_log2 / qs, 0.f);
+                            if (half != rank) continue;
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                hi[j] = lo[j] = 0u;
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const float a = __uint_as_float(w[2 * j + k] << 16) * qs;
+                                    const float c = __uint_as_float(w[2 * j + k] & 0xffff0000u) * qs;
+                                    float va, vc, ra, rc;
+                                    hi[j] |= e4m3_pair(a, c, va, vc) << (16 * k);
+                                    lo[j] |= e4m3_pair(a - va, c - vc, ra, rc) << (16 * k);
+                                }
+                            }
+                            uint8_t* line = smem + C::q + (lane >> 3) * C::Q_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                            *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(line + C::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(bar_of(C::Q_FULL, 0));
+            }
+            bar_sync(ALL, SW * 32);                          // the depths are there
+            if (sw < ROWS / 32) {
+                // row r sees key k iff k <= x and (k > y or k is a sink), and
+                // its mask (from word z on) allows; x = INT_MIN: nothing
+                const int r = sw * 32 + lane, t = (row0 + r) / G;
+                const bool real = t < bd.cnt && bd.start + t >= 0;
+                const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
+                s_see[r] = make_int4(!real ? INT_MIN : p.tree_mask ? bd.len : place,
+                                     p.window > 0 ? place - p.window : INT_MIN, real ? (t - tok0) * W : 0, 0);
+                s_m[r] = -INFINITY;
+                if (!FP8) s_mb[r] = make_float2(p.scale_log2, 0.f);
+            }
+            bar_sync(ALL, SW * 32);
+        };
+
+        int done = -1;                                       // tiles of the segment whose O is to be read, -1: none
+        bool direct = false;                                 // its rows are whole
+        for (;;) {
+            const bool have = walk.next(p);
+            if (have) prologue();
+            if (done >= 0) {
+                // ---- O of the last segment: this CTA's element of each of the
+                // two blocks; the new segment's S^T runs meanwhile
+                if (!have) bar_sync(bar, 128);               // what to write is in shared memory
+                if (done > 0) ok = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+                if (!(ok = bar_and(ALL, SW * 32, ok))) break;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int o = 0; o < 4; ++o) {                // (block, half of the group's rows)
+                    uint32_t r[16];
+                    const int c0 = col0 + (o & 1) * 16;
+                    if (done > 0) {
+                        tmem_ld16(tmem + lanes + TM_O + static_cast<uint32_t>((o >> 1) * ROWS + c0), r);
+                        tmem_ld_wait();
+                        if (o == 3) {
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote_relaxed(bar_of(C::O_FREE, 0));
+                        }
+                    }
+                    const int d = (o >> 1) * 256 + rank * 128 + kk;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint4 info = *reinterpret_cast<const uint4*>(smem + C::info + (c0 + i) * 16);
+                        const float f = __uint_as_float(info.z);
+                        const size_t at = (static_cast<size_t>(info.y) << 32 | info.x) * D + d;
+                        const float val = f != 0.f ? __uint_as_float(r[i]) * f : 0.f;
+                        if (info.w) {
+                            if (direct)
+                                p.out[at] = __float2bfloat16_rn(val);
+                            else
+                                p.ws_o[at] = val;
+                        }
+                    }
+                }
+            }
+            if (!have) break;
+            const Band bd = walk.band;
+            const int n = walk.n, first = walk.first;
+            const int row0 = walk.grp * ROWS;
+            float l[GW];
+#pragma unroll
+            for (int i = 0; i < GW; ++i) l[i] = 0.f;
+            bool out = false;
+            bool fresh = true;                               // some row may not have a reference yet
+#pragma unroll 1
+            for (int t = 0; t < n; ++t, ++g) {
+                const int key0 = bd.key0(first + t), key = key0 + rank * HALF_TILE + kk;
+                ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after_sync();
+                float x[GW];
+                {
+                    uint32_t raw[GW];
+                    tmem_ld32(tmem + lanes + TM_S + static_cast<uint32_t>(sbuf * ROWS + col0), raw);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < GW; ++i) x[i] = __uint_as_float(raw[i]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(bar_of(C::S_FREE + sbuf, 0));
+                if (++sbuf == NB) {
+                    sbuf = 0;
+                    ++suse;
+                }
+                // log2 units, less the rows' references
+#pragma unroll
+                for (int i = 0; i < GW; i += 2) {
+                    const float4 f = *reinterpret_cast<const float4*>(&s_mb[col0 + i]);
+                    x[i] = fmaf(x[i], f.x, f.y);
+                    x[i + 1] = fmaf(x[i + 1], f.z, f.w);
+                }
+                const bool whole = whole_tile(p, bd, key0);
+                bool seen = true;                            // by some row of the group
+                if (!whole) {
+                    const int c = key - bd.start;
+                    const bool drafted = c >= 0 && p.tree_mask;
+                    // the key's place; its own mask says whether a drafted one is seen
+                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
+                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
+                    const bool sink = kp < bd.sink_end;
+                    uint32_t bits = 0xffffffffu;
+                    if (drafted && key < bd.hi) {
+                        bits = 0u;
+#pragma unroll
+                        for (int i = 0; i < GW; ++i)
+                            bits |= ((s_mask[s_see[col0 + i].z + (c >> 5)] >> (c & 31)) & 1u) << i;
+                    }
+                    seen = false;
+#pragma unroll
+                    for (int i = 0; i < GW; ++i) {
+                        const int4 r = s_see[col0 + i];
+                        const bool see = last <= r.x && (kp > r.y || sink) && ((bits >> i) & 1u);
+                        x[i] = see ? x[i] : -INFINITY;
+                        seen = seen || see;
+                    }
+                }
+                float high = x[0];
+#pragma unroll
+                for (int i = 1; i < GW; ++i) high = fmaxf(high, x[i]);
+                // ---- the vote, with the other CTA's keys
+                bool over = bar_or(bar, 128, high > C::THR || fresh || !ok);
+                {
+                    const int par = g & 1;
+                    uint64_t* vb = &bars[C::VOTE + par * GROUPS + grp];
+                    int* sv = reinterpret_cast<int*>(smem + C::vote) + par * GROUPS + grp;
+                    if (speaker && lane == 0) {
+                        mbar_arrive_expect_tx(vb, 4);
+                        st_async_b32(map_to_cta(smem_u32(sv), peer), over ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
+                    }
+                    const bool got = wait_cluster(vb, (g >> 1) & 1, p.err, abort);
+                    ok = __all_sync(0xffffffffu, got) && ok;
+                    over = over || !ok || *reinterpret_cast<volatile int*>(sv) != 0;
+                }
+                bool pv_waited = g == 0;
+                if (over) {
+                    if (!(ok = bar_and(bar, 128, ok))) break;
+                    float v[GW];
+#pragma unroll
+                    for (int i = 0; i < GW; ++i) v[i] = x[i];
+                    const float mx = reduce_columns(v, [](float a, float c) { return fmaxf(a, c); });
+                    s_red[quad * ROWS + col0 + lane] = mx;
+                    bar_sync(bar, 128);
+                    const int cl = col0 + lane;
+                    float up = fmaxf(fmaxf(s_red[cl], s_red[ROWS + cl]), fmaxf(s_red[2 * ROWS + cl], s_red[3 * ROWS + cl]));
+                    up = fmaxf(up, swap_columns(up));
+                    // column `lane`: growth over the reference (over 0 where there was none)
+                    const float m0 = s_m[cl];
+                    const bool none = m0 == -INFINITY;
+                    const float shift = none ? (up == -INFINITY ? 0.f : up) : fmaxf(up, 0.f);
+                    const float a = none ? 1.f : fast_exp2(-shift);
+                    const float m1 = none ? up : m0 + shift;
+                    fresh = __any_sync(0xffffffffu, m1 == -INFINITY);
+#pragma unroll
+                    for (int i = 0; i < GW; ++i) {
+                        x[i] -= __shfl_sync(0xffffffffu, shift, i);
+                        l[i] *= __shfl_sync(0xffffffffu, a, i);
+                    }
+                    if (t > 0) {
+                        // O is at rest once P V of the last tile has completed
+                        const bool got = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+                        ok = __all_sync(0xffffffffu, got) && ok;
+                        pv_waited = true;
+                        tc_fence_after_sync();
+                        if (__any_sync(0xffffffffu, a != 1.f)) {
+#pragma unroll 1
+                            for (int o = 0; o < 4; ++o) {
+                                const uint32_t ta = tmem + lanes + TM_O + static_cast<uint32_t>((o >> 1) * ROWS + col0 + (o & 1) * 16);
+                                uint32_t r[16];
+                                tmem_ld16(ta, r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xffffffffu, a, (o & 1) * 16 + i));
+                                tmem_st16(ta, r);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    bar_sync(bar, 128);                      // everyone has read the references
+                    if (speaker) {
+                        s_m[cl] = m1;
+                        s_mb[cl].y = m1 == -INFINITY ? 0.f : -m1;
+                    }
+                    bar_sync(bar, 128);
+                }
+#pragma unroll
+                for (int i = 0; i < GW; ++i) {
+                    x[i] = fast_exp2(x[i]);
+                    l[i] += x[i];
+                }
+                // P's buffers are free, and V of this tile will be read, after P V of the last tile
+                if (!pv_waited) {
+                    const bool got = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+                    ok = __all_sync(0xffffffffu, got) && ok;
+                }
+                {
+                    // rows 0-63 are CTA 0's operand, 64-127 CTA 1's
+                    const int line = rank * HALF_TILE + kk;
+                    const uint32_t dst = map_to_cta(smem_u32(smem + C::p + line * C::P_LINE), grp >> 1);
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int c = 0; c < GW / 16; ++c) {
+                            uint32_t w[3][4] = {};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float a = x[16 * c + 2 * j] * C::P_SCALE, d = x[16 * c + 2 * j + 1] * C::P_SCALE;
+#pragma unroll
+                                for (int e = 0; e < 3; ++e) {
+                                    float va, vd;
+                                    w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
+                                    a -= va;
+                                    d -= vd;
+                                }
+                            }
+                            const int piece = line_piece<C::P_LINE>(line, (grp & 1) * (GW / 16) + c);
+#pragma unroll
+                            for (int e = 0; e < 3; ++e)
+                                st_cluster_u4(dst + e * C::P_TERM + piece, w[e][0], w[e][1], w[e][2], w[e][3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < GW / 8; ++c)
+                            st_cluster_u4(dst + line_piece<C::P_LINE>(line, (grp & 1) * (GW / 8) + c),
+                                          pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                                          pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+                    }
+                }
+                fence_proxy_async_all();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(bar_of(C::P_FULL, 0));
+
+                // ---- a tile with masks: clear the V rows of keys that no row
+                // sees (of both CTAs' keys) and hand the slots to the MMA
+                if (!whole) {
+                    s_seen[grp * HALF_TILE + kk] = seen;
+                    if (!(ok = bar_and(ALL, SW * 32, ok))) {
+                        out = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < GROUPS; ++i) seen = seen || s_seen[i * HALF_TILE + kk];
+                    const int par = partial_tiles & 1;
+                    int* theirs = reinterpret_cast<int*>(smem + C::pseen) + par * HALF_TILE + kk;
+                    if (grp == 0) {
+                        if (kk == 0) mbar_arrive_expect_tx(&bars[C::SEEN + par], HALF_TILE * 4);
+                        st_async_b32(map_to_cta(smem_u32(theirs), peer), seen ? 1u : 0u, bar_of(C::SEEN + par, peer));
+                    }
+                    const bool got = wait_cluster(&bars[C::SEEN + par], (partial_tiles >> 1) & 1, p.err, abort);
+                    ok = __all_sync(0xffffffffu, got) && ok;
+                    ++partial_tiles;
+                    const bool their_seen = *reinterpret_cast<volatile int*>(theirs) != 0;
+                    const int seq = ring_base + (min(t + LOOK + 1, n) + t) * C::SLOTS;
+#pragma unroll 1
+                    for (int c = 0; c < C::SLOTS; ++c) {
+                        const int s = (seq + c) % NS;
+                        const bool in = wait_or_abort(&bars[C::V_RAW + s], (raw_used >> s) & 1, p.err, abort);
+                        ok = __all_sync(0xffffffffu, in) && ok;
+                        raw_used ^= 1u << s;
+                        // the groups share out a key's line: side grp / 2, pieces 4 (grp % 2) ..
+                        const int side = grp >> 1;
+                        const int half = FP8 ? side : c & 1;
+                        if (in && !(half == rank ? seen : their_seen)) {
+                            uint4* v = reinterpret_cast<uint4*>(smem + C::ring + s * SLOT + side * SIDE + kk * 128) + 4 * (grp & 1);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(bar_of(C::V_CLEAN + s, 0));
+                    }
+                    // the flags may be written again once everyone has read them
+                    if (!(ok = bar_and(ALL, SW * 32, ok))) {
+                        out = true;
+                        break;
+                    }
+                }
+            }
+            ring_base = (ring_base + 2 * n * C::SLOTS) % NS;
+            // all go on or all stop (here or at a vote inside a tile): no warp
+            // may wait at a barrier for one that has left
+            if (out || !(ok = bar_and(ALL, SW * 32, ok))) break;
+            // ---- row sums: lanes, the four quadrants' warps, the other CTA
+            const float part = reduce_columns(l, [](float a, float c) { return a + c; });
+            s_red[quad * ROWS + col0 + lane] = part;
+            bar_sync(bar, 128);
+            const int cl = col0 + lane;
+            const float mine = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
+            const float other = swap_columns(mine);
+            // in one order, so that both CTAs have the same sum
+            const float sum = rank == 0 ? mine + other : other + mine;
+            // ---- what to write: O / sum where this is the whole row, else the
+            // unnormalised partial (zeros for a row that saw nothing)
+            direct = walk.count == 1;
+            if (speaker) {
+                const float top = s_m[cl];
+                const int r = row0 + cl, t = r / G;
+                const bool some = s_see[cl].x != INT_MIN && top != -INFINITY;
+                const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
+                const size_t at = direct ? row : row * static_cast<size_t>(p.num_splits) + walk.index;
+                const float unit = p.o_scale * (1.f / C::P_SCALE);
+                const float factor = !some ? 0.f : direct ? unit / sum : unit;
+                const bool real = t < p.q_len;
+                *reinterpret_cast<uint4*>(smem + C::info + cl * 16) =
+                    make_uint4(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), __float_as_uint(factor), real);
+                if (real && rank == 0) {
+                    if (!direct) {
+                        p.ws_ml[at * 2] = some ? top : -INFINITY;
+                        p.ws_ml[at * 2 + 1] = some ? sum : 0.f;
+                    } else if (p.lse) {
+                        p.lse[row] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+                    }
+                }
+            }
+            if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0 && rank == 0)
+                p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
+            done = n;
+        }
+    }
+    // all threads of both CTAs: no copy or arrival may reach a CTA that has gone
+    tc_fence_before_sync();
+    cluster_sync_all();
+    if (warp == 1) tmem_dealloc2(tmem, 512);
+}
+
+// Resident pairs on the current device (0: a query failed), asked once per
+// device, which also opts the kernel into its shared memory there.
+template <bool FP8>
+int resident_pairs() {
+    static std::mutex mu;
+    static int known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev] == 0) {
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = Cfg<FP8>::total + 1024;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(tree_pair_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<FP8>::total + 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, tree_pair_kernel<FP8>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        known[dev] = n;
+    }
+    return known[dev];
+}
+
+template <bool FP8>
+cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
+    const int resident = resident_pairs<FP8>();
+    if (resident < 1) return cudaErrorLaunchOutOfResources;
+    const long long units = static_cast<long long>(p.batch) * p.row_groups * p.n_kv_heads *
+                            (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(units < resident ? units : resident) * 2);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Cfg<FP8>::total + 1024;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_pair_kernel<FP8>, tmk, tmv, p);
+}
+
+}  // namespace pairs
+}  // namespace tree
+
+cudaError_t launch_tree_pair(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
+                             cudaStream_t stream) {
+    return fp8 ? tree::pairs::launch<true>(tmk, tmv, p, stream) : tree::pairs::launch<false>(tmk, tmv, p, stream);
+}
+
+}  // namespace fa512

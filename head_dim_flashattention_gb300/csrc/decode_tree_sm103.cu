@@ -1,12 +1,6 @@
 // Drafted tokens (a tree of them, or a plain run) over a paged cache, head
 // dim 512, sm_103a.
 //
-// With start = len - cnt the last cnt cached positions are the tokens' own.
-// Token t sees a key j < start always and a key start + c if its mask has bit
-// c (no mask: c <= t); with a window, only keys whose place is above the
-// token's place - window or below n_sinks, where the place of a cached key is
-// its position and that of token t is start + (tokens it sees) - 1.
-//
 // A CTA takes ROWS = 64 (or 32) rows ((token, query head) pairs) of one KV
 // head and walks key tiles of 128, computing both products transposed on
 // tcgen05: S^T = K Q^T (M = 128 keys, N = ROWS, K = 512) and
@@ -42,44 +36,19 @@
 // ranges leaves (O, m, l) partials that merge_kernel combines, any other is
 // written directly.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <limits.h>
-#include <math.h>
-#include <stdint.h>
-#include <string.h>
 
-#include <mutex>
-
-#include "fa512_device.cuh"
-#include "fa512_internal.h"
-#include "fa512_pair.cuh"
+#include "fa512_tree.cuh"
 
 namespace fa512 {
 namespace tree {
+namespace single {
 
-using pair::elect_one;
-
-// The kernel's code is kept small enough for the instruction cache (roles run
-// side by side, and what a segment runs once would otherwise be fetched from
-// L2 between the streams' loads): what is seldom run or run from many places
-// is not inlined.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
-    return pair::wait_or_abort(bar, parity, err, abort);
-}
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
-    return mbar_try_wait(smem_u32(bar), parity) || wait_slow(bar, parity, err, abort);
-}
-
-constexpr int D = 512;
-constexpr int MAX_NODES = 256;
 constexpr int TILE = 128;                // keys per tile: M of S^T
-constexpr int SIDE = 16384;              // 128 keys x 128 bytes of the head dim
-constexpr int SLOT = 2 * SIDE;           // a ring slot: 256 bytes of the head dim of a key tile
 constexpr int GW = 16;                   // rows (columns of S^T) of a softmax warp
 constexpr int LOOK = 2;                  // S^T tiles computed ahead of O^T += V^T P^T
 constexpr int NB = LOOK + 1;             // S^T buffers
-constexpr int MAX_CLUSTER = 8;
+using Walk = WalkOf<TILE>;
+using Band = BandOf<TILE>;
 
 template <bool FP8, int ROWS>
 struct Cfg {
@@ -135,59 +104,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-// Instruction descriptors: M = 128, N = rows, fp32 accumulator.
-__host__ __device__ constexpr uint32_t shape(int rows) { return (1u << 4) | (static_cast<uint32_t>(rows >> 3) << 17) | (128u >> 4 << 24); }
-constexpr uint32_t BF16_AB = (1u << 7) | (1u << 10);
-constexpr uint32_t B_E5M2 = 1u << 10;                    // beside an E4M3 A
-constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
-
-// The descriptor of an MN-major operand whose lines are `line` = 128, 64 or
-// 32 bytes, swizzled over their own length (atoms of 8 lines).
-template <int LINE>
-__device__ __forceinline__ uint64_t make_sdesc_lines(uint32_t saddr) {
-    constexpr uint64_t mode = LINE == 128 ? 2 : LINE == 64 ? 4 : 6;
-    return (make_sdesc_sw128(saddr, 16, 8 * LINE) & ~(7ull << 61)) | (mode << 61);
-}
-// Place of 16-byte piece c of line k under that swizzle.
-template <int LINE>
-__device__ __forceinline__ int line_piece(int k, int c) {
-    if constexpr (LINE == 128) return (c ^ (k & 7)) << 4;
-    if constexpr (LINE == 64) return (c ^ ((k >> 1) & 3)) << 4;
-    return (c ^ ((k >> 2) & 1)) << 4;
-}
-
-// Arrives on the barrier at this offset in CTA `rank` of the cluster when
-// every MMA issued so far has completed.
-__device__ __forceinline__ void tc_commit_to(uint64_t* bar, uint32_t rank) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"(static_cast<uint16_t>(1u << rank))
-        : "memory");
-}
-// A tile load into the same shared-memory place of every CTA in `ctas`,
-// counted on each one's barrier at this offset.
-__device__ __forceinline__ void tma_load_3d_multicast(void* smem_dst, const CUtensorMap* m, uint64_t* bar, int c0,
-                                                      int c1, int c2, uint16_t ctas) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "h"(ctas)
-        : "memory");
-}
-
-// Named barrier over `count` threads that also ORs a predicate across them.
-__device__ __forceinline__ bool bar_or(int id, int count, bool pred) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                 "barrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"(id), "r"(count), "r"(pred ? 1u : 0u) : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void bar_sync(int id, int count) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 // Reduces 16 values per lane over the warp at once: lane i gets everyone's
 // v[i % 16] (15 shuffles in which halves swap the values that the other half
 // keeps, and one that joins the warp's halves).
@@ -206,121 +122,6 @@ __device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// E4M3 (E5M2) pair of two fp32 values (low byte first) and the pair's values.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float& vlo, float& vhi) {
-    uint16_t e;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(e));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(vlo), "=f"(vhi) : "r"(h2));
-    return e;
-}
-__device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi, float& vlo, float& vhi) {
-    uint16_t e;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"(e));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(vlo), "=f"(vhi) : "r"(h2));
-    return e;
-}
-
-// The keys that a row group of a sequence walks.
-struct Band {
-    int len, cnt, start;        // cached positions, tokens, first token's position
-    int lo, hi;                 // keys that some row may see: [lo, hi) and those below sink_end
-    int sink_end;
-    int sink_tiles, lo_tile;    // tile i is i < sink_tiles ? i : lo_tile + i - sink_tiles
-    int place_max;              // no row's place is above
-    int tiles;
-    __device__ __forceinline__ int key0(int i) const {
-        return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
-    }
-};
-
-// Band of row group `grp` (group_rows rows) of sequence b.  It follows from
-// the lengths alone: with a mask a token's place is only known to lie in
-// [start - 1, start + cnt - 1], and its own tokens' keys are always walked.
-__device__ __noinline__ Band band_of(const TreeParams& p, int b, int grp, int group_rows, bool record) {
-    Band d;
-    d.len = p.kv_lens[b];
-    d.cnt = p.q_lens ? p.q_lens[b] : p.q_len;
-    if (d.len < 0 || d.len > p.len_cap || d.cnt < 0 || d.cnt > p.q_len) {
-        if (record) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        d.len = max(0, min(d.len, p.len_cap));
-        d.cnt = max(0, min(d.cnt, p.q_len));
-    }
-    d.start = d.len - d.cnt;
-    const int r0 = grp * group_rows;
-    const int first = max(r0 / p.group, -d.start);
-    const int last = min((r0 + group_rows - 1) / p.group, d.cnt - 1);
-    d.hi = first > last ? 0 : p.tree_mask ? d.len : min(d.len, d.start + last + 1);
-    d.lo = 0;
-    d.sink_end = 0;
-    d.place_max = d.start + (p.tree_mask ? d.cnt - 1 : last);
-    if (p.window > 0 && d.hi > 0) {
-        d.lo = max(0, p.tree_mask ? d.start - p.window : d.start + first - p.window + 1);
-        d.sink_end = min(p.n_sinks, d.hi);
-    }
-    d.lo_tile = d.lo / TILE;
-    d.sink_tiles = min((d.sink_end + TILE - 1) / TILE, d.lo_tile);
-    d.tiles = d.hi <= 0 ? 0 : d.sink_tiles + (d.hi + TILE - 1) / TILE - d.lo_tile;
-    return d;
-}
-
-// Walk over this cluster's range of the items' tiles (an item without tiles
-// counts as one, so that somebody writes its empty rows).
-struct Walk {
-    int pos, end, base;         // next unit, end of the range, first unit of the current item
-    int per;
-    int entry, kvh;             // current item: entry = sequence * groups + row group
-    int entries, groups, group_rows;
-    Band band;
-    // the current segment
-    int b, grp, first, n;       // tiles [first, first + n) of the band
-    int index, count;           // which of how many segments of the item
-
-    __device__ __forceinline__ int units() const { return max(1, band.tiles); }
-    __device__ __forceinline__ void load(const TreeParams& p) {
-        b = entry / groups;
-        grp = entry - b * groups;
-        band = band_of(p, b, grp, group_rows, false);
-    }
-    __device__ __noinline__ bool next(const TreeParams& p) {
-        while (pos < end) {
-            const int w = units();
-            if (pos >= base + w || (p.num_splits == 1 && pos > base)) {
-                // a whole item belongs to the range that holds its first unit
-                if (pos < base + w) pos = base + w;
-                base += w;
-                if (++kvh == p.n_kv_heads) {
-                    kvh = 0;
-                    if (++entry == entries) return false;
-                    load(p);
-                }
-                continue;
-            }
-            first = pos - base;
-            if (p.num_splits == 1) {
-                index = 0;
-                count = 1;
-                n = band.tiles;
-                pos = base + w;
-            } else {
-                const int take = min(w - first, end - pos);
-                const int seg0 = base / per;
-                index = pos / per - seg0;
-                count = (base + w - 1) / per - seg0 + 1;
-                n = min(take, band.tiles);
-                pos += take;
-            }
-            return true;
-        }
-        return false;
-    }
-};
-
 template <bool FP8, int ROWS>
 __global__ void __launch_bounds__(Cfg<FP8, ROWS>::THREADS, 1)
 tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -335,13 +136,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::misc + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cs = p.cluster;
-    const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&bars[C::FULL + i], 1);
-            mbar_init(&bars[C::EMPTY + i], cs);
+            mbar_init(&bars[C::EMPTY + i], 1);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&bars[C::S_FULL + i], 1);
@@ -362,127 +161,49 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         tmem_relinquish();
     }
 
-    // ---- this cluster's range: total units, then the item that holds its start
+    // ---- this block's range of the items' tiles
     Walk walk;
-    walk.groups = p.row_groups;
-    walk.group_rows = ROWS * cs;
-    walk.entries = p.batch * p.row_groups;
-    {
-        int* s_scan = reinterpret_cast<int*>(smem + C::scan);
-        int* s_at = s_scan + 32;                         // start's entry, unit
-        constexpr int NW = THREADS / 32;
-        const int clusters = gridDim.x / cs, me = blockIdx.x / cs;
-        auto entry_units = [&](int e, bool record) -> int {
-            if (e >= walk.entries) return 0;
-            const int eb = e / walk.groups;
-            const Band d = band_of(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
-            return max(1, d.tiles) * p.n_kv_heads;
-        };
-        int total = 0, mine0 = 0;                        // mine0: entry tid's units
-        for (int e = tid; e < walk.entries; e += THREADS) {
-            const int u = entry_units(e, blockIdx.x == 0);
-            if (e == tid) mine0 = u;
-            total += u;
-        }
-        total = __reduce_add_sync(0xffffffffu, total);
-        if (lane == 0) s_scan[warp] = total;
-        __syncthreads();
-        total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
-        // ranges short enough to balance, long enough that no item has more
-        // than num_splits segments
-        walk.per = (total + clusters - 1) / clusters;
-        if (p.num_splits > 1) walk.per = max(walk.per, p.min_range);
-        walk.per = max(walk.per, 1);
-        const long long begin = static_cast<long long>(me) * walk.per;
-        walk.pos = static_cast<int>(min(begin, static_cast<long long>(total)));
-        walk.end = min(total - walk.pos, walk.per) + walk.pos;
-        int before = 0;
-        if (walk.pos < walk.end) {
-            for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
-                const int u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
-                int x = u;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                __syncthreads();
-                if (lane == 31) s_scan[warp] = x;
-                __syncthreads();
-                const int ws = lane < NW ? s_scan[lane] : 0;
-                x += before + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
-                const int sum = before + __reduce_add_sync(0xffffffffu, ws);
-                if (walk.pos >= x - u && walk.pos < x) {
-                    s_at[0] = e0 + tid;
-                    s_at[1] = x - u;
-                }
-                before = sum;
-                if (walk.pos < before) break;
-            }
-        }
-        __syncthreads();
-        walk.entry = s_at[0];
-        walk.kvh = 0;
-        walk.base = s_at[1];
-        if (walk.pos < walk.end) {
-            walk.load(p);
-            walk.kvh = (walk.pos - walk.base) / walk.units();
-            walk.base += walk.kvh * walk.units();
-        }
-    }
-    if (cs > 1) cluster_sync_all(); else __syncthreads();
+    walk.groups = 1;
+    walk.group_rows = ROWS;
+    start_walk<TILE, THREADS>(walk, p, gridDim.x, blockIdx.x, reinterpret_cast<int*>(smem + C::scan));
+    __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        // The warp walks the slots and waits; one elected lane issues.  Slot s
-        // is loaded by CTA s % cs for the whole cluster, in boxes of
+        // The warp walks the slots and waits; one elected lane issues boxes of
         // {128 bytes of the head dim, box_rows positions of a page}.
         const int oob = p.num_pages * p.page_size;           // past the pool: filled with zeros
-        const uint16_t everyone = static_cast<uint16_t>((1u << cs) - 1u);
         const int box_rows = min(p.page_size, TILE), boxes = TILE / box_rows;
         int* s_rows = reinterpret_cast<int*>(smem + C::rows);
-        int slot = 0, owner = 0;
+        int slot = 0;
         uint32_t use = 0;                                    // use number of the slot
         bool ok = true;
         int seq = 0;
         auto load_tile = [&](const CUtensorMap* tm, int kvh, const int* rows) {
 #pragma unroll 1
             for (int c = 0; c < C::SLOTS; ++c) {
-                const bool mine = owner == rank;
                 if (use > 0) {
-                    // issuer: everyone has read the slot; others: it was filled here
-                    const int bar = mine ? C::EMPTY : C::FULL;
-                    ok = __all_sync(0xffffffffu, wait_or_abort(&bars[bar + slot], (use & 1) ^ 1, p.err, abort));
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::EMPTY + slot], (use & 1) ^ 1, p.err, abort));
                     if (!ok) return;
                 }
                 if (elect_one()) {
                     uint64_t* full = &bars[C::FULL + slot];
                     mbar_arrive_expect_tx(full, SLOT);
-                    if (mine) {
-                        uint8_t* dst = smem + C::ring + slot * SLOT;
-                        const int c0 = c * (256 / C::EB);
+                    uint8_t* dst = smem + C::ring + slot * SLOT;
+                    const int c0 = c * (256 / C::EB);
 #pragma unroll 1
-                        for (int i = 0; i < boxes; ++i) {
-                            const int row = rows[i];
-                            if (cs > 1) {
-                                tma_load_3d_multicast(dst, tm, full, c0, kvh, row, everyone);
-                                tma_load_3d_multicast(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, row, everyone);
-                            } else {
-                                tma_load_3d(dst, tm, full, c0, kvh, row);
-                                tma_load_3d(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, row);
-                            }
-                            dst += box_rows * 128;
-                        }
+                    for (int i = 0; i < boxes; ++i) {
+                        tma_load_3d(dst, tm, full, c0, kvh, rows[i]);
+                        tma_load_3d(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, rows[i]);
+                        dst += box_rows * 128;
                     }
                 }
                 __syncwarp();
                 ++seq;
-                owner = owner + 1 == cs ? 0 : owner + 1;
                 if (++slot == NS) {
                     slot = 0;
-                    owner = 0;
                     ++use;
                 }
             }
@@ -528,8 +249,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         const uint32_t ring = smem_u32(smem + C::ring);
         const uint64_t qd = make_sdesc_sw128(smem_u32(smem + C::q), 16, 1024);
         const uint64_t pd = make_sdesc_lines<C::P_LINE>(smem_u32(smem + C::p));
-        constexpr uint32_t IDESC_QK = shape(ROWS) | (FP8 ? 0u : BF16_AB);
-        constexpr uint32_t IDESC_PV = shape(ROWS) | (FP8 ? B_E5M2 : BF16_AB) | A_MN | B_MN;
+        constexpr uint32_t IDESC_QK = idesc_shape(128, ROWS) | (FP8 ? 0u : BF16_AB);
+        constexpr uint32_t IDESC_PV = idesc_shape(128, ROWS) | (FP8 ? B_E5M2 : BF16_AB) | A_MN | B_MN;
         bool ok = true;
         int slot = 0, segment = 0;
         uint32_t use = 0;
@@ -539,17 +260,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         auto wait = [&](int bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_abort(&bars[bar], parity, p.err, abort));
         };
-        int owner = 0;                                       // the CTA that loads the slot
         auto next_slot = [&]() {
-            owner = owner + 1 == cs ? 0 : owner + 1;
             if (++slot == NS) {
                 slot = 0;
-                owner = 0;
                 ++use;
             }
-        };
-        auto free_slot = [&]() {                             // by the issuing lane
-            if (cs > 1) tc_commit_to(&bars[C::EMPTY + slot], owner); else tc_commit(&bars[C::EMPTY + slot]);
         };
         auto issue_qk = [&]() -> bool {
             if (suse > 0 && !wait(C::S_FREE + sbuf, (suse & 1) ^ 1)) return false;
@@ -572,7 +287,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                             tc_mma_ss(sb, a, q, IDESC_QK, (c | k) ? 1u : 0u);
                         }
                     }
-                    free_slot();
+                    tc_commit(&bars[C::EMPTY + slot]);
                     if (c == C::SLOTS - 1) tc_commit(&bars[C::S_FULL + sbuf]);
                 }
                 __syncwarp();
@@ -613,7 +328,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                                       vd + static_cast<uint64_t>((k * 16 * 128) >> 4),
                                       pd + static_cast<uint64_t>((k * 16 * C::P_LINE) >> 4), IDESC_PV, k ? 1u : acc0);
                     }
-                    free_slot();
+                    tc_commit(&bars[C::EMPTY + slot]);
                     if (c == C::SLOTS - 1) tc_commit(&bars[C::PV_DONE]);
                 }
                 __syncwarp();
@@ -668,8 +383,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         auto prologue = [&]() {
             const Band& bd = walk.band;
             const int n = walk.n, b = walk.b;
-            const int row0 = (walk.grp * cs + rank) * ROWS;
-            const int tok0 = row0 / G;
+            constexpr int row0 = 0, tok0 = 0;                // one row group
             if (n > 0) {
                 // Q: rows as K-major B operand, zeros where there is no row
                 constexpr int PER = ROWS / SW;               // rows of a warp: 4
@@ -685,24 +399,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     x[i][1] = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
                 }
                 bar_sync(ALL, SW * 32);                      // nobody uses the last segment's tables any more
-                const int toks = max(0, min((row0 + ROWS - 1) / G, p.q_len - 1) - tok0 + 1);
-                if (p.tree_mask) {
-                    // bits at and behind cnt name no token
-                    auto word = [&](int t, int w) -> uint32_t {
-                        const int left = bd.cnt - 32 * w;
-                        const uint32_t m = static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * W + w]);
-                        return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
-                    };
-                    for (int t = tid - 64; t < bd.cnt; t += SW * 32) {
-                        int c = 0;
-                        for (int w = 0; w < W; ++w) c += __popc(word(t, w));
-                        s_depth[t] = c - 1;
-                    }
-                    for (int i = tid - 64; i < toks * W; i += SW * 32) {
-                        const int t = tok0 + i / W, w = i % W;
-                        s_mask[i] = t < bd.cnt ? word(t, w) : 0u;
-                    }
-                }
+                const int toks = min((ROWS - 1) / G, p.q_len - 1) + 1;
+                if (p.tree_mask) load_masks(p, b, bd.cnt, tok0, toks, s_depth, s_mask, tid - 64, SW * 32);
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int r = sw + i * SW;
@@ -807,7 +505,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             if (!have) break;
             const Band bd = walk.band;
             const int n = walk.n, first = walk.first;
-            const int row0 = (walk.grp * cs + rank) * ROWS;
+            constexpr int row0 = 0;
             float m[GW], l[GW];
 #pragma unroll
             for (int i = 0; i < GW; ++i) {
@@ -1037,15 +735,50 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     }
                 }
             }
-            if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0 && rank == 0)
+            if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0)
                 p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
             done = n;
         }
     }
     // all threads of all CTAs: no copy or arrival may reach a CTA that has gone
-    if (cs > 1) cluster_sync_all(); else __syncthreads();
+    __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, C::TM_COLS);
 }
+
+// SMs of the current device once the kernel is opted into its shared memory
+// there (0: a query failed); asked once per device.
+template <bool FP8, int ROWS>
+int resident_blocks() {
+    static std::mutex mu;
+    static int known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev] == 0) {
+        int n = 0;
+        if (cudaFuncSetAttribute(tree_kernel<FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<FP8, ROWS>::total + 1024) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        known[dev] = n;
+    }
+    return known[dev];
+}
+
+template <bool FP8, int ROWS>
+cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
+    const int blocks = resident_blocks<FP8, ROWS>();
+    if (blocks < 1) return cudaErrorLaunchOutOfResources;
+    const long long units = static_cast<long long>(p.batch) * p.n_kv_heads *
+                            (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
+    tree_kernel<FP8, ROWS><<<static_cast<unsigned>(units < blocks ? units : blocks), Cfg<FP8, ROWS>::THREADS,
+                             Cfg<FP8, ROWS>::total + 1024, stream>>>(tmk, tmv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace single
 
 // One block per row that was left in segments and slice of its columns:
 // combines the segments' (O, m, l) -- M = max m_s, w_s = 2^(m_s - M),
@@ -1138,100 +871,51 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
         p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
-// Resident clusters of `cs` CTAs of one kernel variant on the current device
-// (0 when the query fails), asked once per device, which also opts the kernel
-// into its shared memory there.
-template <bool FP8, int ROWS>
-int resident_clusters(int cs) {
-    static std::mutex mu;
-    static int known[64][MAX_CLUSTER + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lk(mu);
-    int& n = known[dev][cs];
-    if (n == 0) {
-        cudaLaunchConfig_t cfg;
-        memset(&cfg, 0, sizeof cfg);
-        cfg.gridDim = dim3(cs);
-        cfg.blockDim = dim3(Cfg<FP8, ROWS>::THREADS);
-        cfg.dynamicSmemBytes = Cfg<FP8, ROWS>::total + 1024;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cs;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int got = 0;
-        if (cudaFuncSetAttribute(tree_kernel<FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Cfg<FP8, ROWS>::total + 1024) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&got, tree_kernel<FP8, ROWS>, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        n = got;
-    }
-    return n;
-}
+}  // namespace tree
 
-template <bool FP8, int ROWS>
-cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
-    const int clusters = resident_clusters<FP8, ROWS>(p.cluster);
-    if (clusters < 1) return cudaErrorLaunchOutOfResources;
+// The merge may be scheduled while the tiles are walked (it waits for them).
+cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t stream) {
+    using namespace tree;
+    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    const long long units = static_cast<long long>(p.batch) * p.row_groups * p.n_kv_heads *
-                            (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(units < clusters ? units : clusters) * p.cluster);
-    cfg.blockDim = dim3(Cfg<FP8, ROWS>::THREADS);
-    cfg.dynamicSmemBytes = Cfg<FP8, ROWS>::total + 1024;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_kernel<FP8, ROWS>, tmk, tmv, p);
-    if (e != cudaSuccess || p.num_splits == 1) return e;
-    // the merge may be scheduled while the tiles are walked (it waits for them)
-    memset(&cfg, 0, sizeof cfg);
-    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
     cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
     cfg.blockDim = dim3(MERGE_THREADS);
     cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, ROWS * p.cluster)
-                  : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, ROWS * p.cluster);
+    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, group_rows)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, group_rows);
 }
 
-}  // namespace tree
-
 int tree_max_nodes() { return tree::MAX_NODES; }
-int tree_tile() { return tree::TILE; }
 
-// 32-row CTAs where all rows of a KV head fit one, else 64-row CTAs, the row
-// tiles of a KV head in clusters of at most 4 (as even as possible).
+// One CTA with 32 or 64 rows where all rows of a KV head fit, else CTA pairs
+// with 128 rows each.
 TreeShape tree_shape(int q_len, int group) {
     const long long rows = static_cast<long long>(q_len) * group;
     TreeShape s;
-    s.rows = rows <= 32 ? 32 : 64;
-    const long long tiles = (rows + s.rows - 1) / s.rows;
-    const long long groups = (tiles + 3) / 4;
-    s.cluster = static_cast<int>((tiles + groups - 1) / groups);
-    s.groups = static_cast<int>((tiles + s.cluster - 1) / s.cluster);
+    s.rows = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    s.ctas = rows <= 64 ? 1 : 2;
+    s.tile = 128 * s.ctas;
+    s.groups = static_cast<int>((rows + s.rows - 1) / s.rows);
     return s;
 }
 
 cudaError_t launch_decode_tree(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
                                cudaStream_t stream) {
-    if (p.rows == 32)
-        return fp8 ? tree::launch<true, 32>(tmk, tmv, p, stream) : tree::launch<false, 32>(tmk, tmv, p, stream);
-    return fp8 ? tree::launch<true, 64>(tmk, tmv, p, stream) : tree::launch<false, 64>(tmk, tmv, p, stream);
+    using namespace tree;
+    cudaError_t e;
+    if (p.rows == 128)
+        e = launch_tree_pair(tmk, tmv, p, fp8, stream);
+    else if (p.rows == 64)
+        e = fp8 ? single::launch<true, 64>(tmk, tmv, p, stream) : single::launch<false, 64>(tmk, tmv, p, stream);
+    else
+        e = fp8 ? single::launch<true, 32>(tmk, tmv, p, stream) : single::launch<false, 32>(tmk, tmv, p, stream);
+    return e != cudaSuccess || p.num_splits == 1 ? e : launch_tree_merge(p, p.rows, stream);
 }
 
 }  // namespace fa512

@@ -68,7 +68,7 @@ struct TreeParams {
     __nv_bfloat16* out;            // [batch, q_len, n_q_heads, 512]
     float* lse;                    // [batch, q_len, n_q_heads] or null
     int batch, q_len, n_q_heads, n_kv_heads, group, mask_words;
-    int rows, cluster, row_groups; // TreeShape
+    int rows, row_groups;          // TreeShape
     int max_tiles;                 // most key tiles of an item
     int min_range;                 // shortest range of tiles that keeps an item to num_splits segments
     int page_size, num_pages, max_pages_per_seq, len_cap;
@@ -80,14 +80,14 @@ struct TreeParams {
 };
 
 int tree_max_nodes();              // most tokens a tree_mask covers
-int tree_tile();                   // keys per tile
 struct TreeShape {
-    int rows;                      // rows of a CTA
-    int cluster;                   // CTAs that share their keys
-    int groups;                    // row groups (clusters) of a KV head
+    int rows;                      // rows of a KV head that share a walk over its keys
+    int ctas;                      // CTAs that hold them
+    int tile;                      // keys per tile
+    int groups;                    // row groups of a KV head
 };
 TreeShape tree_shape(int q_len, int group);
-// Both maps: {128 bytes of the head dim, 1 KV head, min(page_size, tree_tile()) positions} boxes, 128-byte swizzle.
+// Both maps: {128 bytes of the head dim, 1 KV head, min(page_size, 128) positions} boxes, 128-byte swizzle.
 cudaError_t launch_decode_tree(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
                                cudaStream_t stream);
 

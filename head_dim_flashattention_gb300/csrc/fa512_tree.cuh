@@ -1,0 +1,300 @@
+// What the tree decode kernels share: the keys that the rows of a (sequence,
+// row group, KV head) item walk, the equal ranges of those keys' tiles that
+// the resident clusters take, operand layouts and small device helpers.
+//
+// With start = len - cnt the last cnt cached positions are the tokens' own.
+// Token t sees a key j < start always and a key start + c if its mask has bit
+// c (no mask: c <= t); with a window, only keys whose place is above the
+// token's place - window or below n_sinks, where the place of a cached key is
+// its position and that of token t is start + (tokens it sees) - 1.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <mutex>
+
+#include "fa512_device.cuh"
+#include "fa512_internal.h"
+#include "fa512_pair.cuh"
+
+namespace fa512 {
+namespace tree {
+
+using pair::elect_one;
+
+// The kernel's code is kept small enough for the instruction cache (roles run
+// side by side, and what a segment runs once would otherwise be fetched from
+// L2 between the streams' loads): what is seldom run or run from many places
+// is not inlined.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    return pair::wait_or_abort(bar, parity, err, abort);
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+    return mbar_try_wait(smem_u32(bar), parity) || wait_slow(bar, parity, err, abort);
+}
+
+constexpr int D = 512;
+constexpr int MAX_NODES = 256;
+constexpr int SIDE = 16384;              // 128 keys x 128 bytes of the head dim
+constexpr int SLOT = 2 * SIDE;           // a ring slot
+
+// Instruction descriptor of M x N products with an fp32 accumulator, without
+// the operand types.
+__host__ __device__ constexpr uint32_t idesc_shape(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+constexpr uint32_t BF16_AB = (1u << 7) | (1u << 10);
+constexpr uint32_t B_E5M2 = 1u << 10;                    // beside an E4M3 A
+constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;
+
+// The descriptor of an MN-major operand whose lines are `line` = 128, 64 or
+// 32 bytes, swizzled over their own length (atoms of 8 lines).
+template <int LINE>
+__device__ __forceinline__ uint64_t make_sdesc_lines(uint32_t saddr) {
+    constexpr uint64_t mode = LINE == 128 ? 2 : LINE == 64 ? 4 : 6;
+    return (make_sdesc_sw128(saddr, 16, 8 * LINE) & ~(7ull << 61)) | (mode << 61);
+}
+// Place of 16-byte piece c of line k under that swizzle.
+template <int LINE>
+__device__ __forceinline__ int line_piece(int k, int c) {
+    if constexpr (LINE == 128) return (c ^ (k & 7)) << 4;
+    if constexpr (LINE == 64) return (c ^ ((k >> 1) & 3)) << 4;
+    return (c ^ ((k >> 2) & 1)) << 4;
+}
+
+// Named barrier over `count` threads that also ORs a predicate across them.
+__device__ __forceinline__ bool bar_or(int id, int count, bool pred) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "barrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(count), "r"(pred ? 1u : 0u) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// E4M3 (E5M2) pair of two fp32 values (low byte first) and the pair's values.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float& vlo, float& vhi) {
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(e));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(vlo), "=f"(vhi) : "r"(h2));
+    return e;
+}
+__device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi, float& vlo, float& vhi) {
+    uint16_t e;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"(e));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(vlo), "=f"(vhi) : "r"(h2));
+    return e;
+}
+
+// The keys that a row group of a sequence walks.
+template <int TILE>
+struct BandOf {
+    int len, cnt, start;        // cached positions, tokens, first token's position
+    int lo, hi;                 // keys that some row may see: [lo, hi) and those below sink_end
+    int sink_end;
+    int sink_tiles, lo_tile;    // tile i is i < sink_tiles ? i : lo_tile + i - sink_tiles
+    int place_max;              // no row's place is above
+    int tiles;
+    __device__ __forceinline__ int key0(int i) const {
+        return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+    }
+};
+
+// Band of row group `grp` (group_rows rows) of sequence b.  It follows from
+// the lengths alone: with a mask a token's place is only known to lie in
+// [start - 1, start + cnt - 1], and its own tokens' keys are always walked.
+template <int TILE>
+__device__ __noinline__ BandOf<TILE> band_of(const TreeParams& p, int b, int grp, int group_rows, bool record) {
+    BandOf<TILE> d;
+    d.len = p.kv_lens[b];
+    d.cnt = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (d.len < 0 || d.len > p.len_cap || d.cnt < 0 || d.cnt > p.q_len) {
+        if (record) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        d.len = max(0, min(d.len, p.len_cap));
+        d.cnt = max(0, min(d.cnt, p.q_len));
+    }
+    d.start = d.len - d.cnt;
+    const int r0 = grp * group_rows;
+    const int first = max(r0 / p.group, -d.start);
+    const int last = min((r0 + group_rows - 1) / p.group, d.cnt - 1);
+    d.hi = first > last ? 0 : p.tree_mask ? d.len : min(d.len, d.start + last + 1);
+    d.lo = 0;
+    d.sink_end = 0;
+    d.place_max = d.start + (p.tree_mask ? d.cnt - 1 : last);
+    if (p.window > 0 && d.hi > 0) {
+        d.lo = max(0, p.tree_mask ? d.start - p.window : d.start + first - p.window + 1);
+        d.sink_end = min(p.n_sinks, d.hi);
+    }
+    d.lo_tile = d.lo / TILE;
+    d.sink_tiles = min((d.sink_end + TILE - 1) / TILE, d.lo_tile);
+    d.tiles = d.hi <= 0 ? 0 : d.sink_tiles + (d.hi + TILE - 1) / TILE - d.lo_tile;
+    return d;
+}
+
+// Walk over this cluster's range of the items' tiles (an item without tiles
+// counts as one, so that somebody writes its empty rows).
+template <int TILE>
+struct WalkOf {
+    int pos, end, base;         // next unit, end of the range, first unit of the current item
+    int per;
+    int entry, kvh;             // current item: entry = sequence * groups + row group
+    int entries, groups, group_rows;
+    BandOf<TILE> band;
+    // the current segment
+    int b, grp, first, n;       // tiles [first, first + n) of the band
+    int index, count;           // which of how many segments of the item
+
+    __device__ __forceinline__ int units() const { return max(1, band.tiles); }
+    __device__ __forceinline__ void load(const TreeParams& p) {
+        b = entry / groups;
+        grp = entry - b * groups;
+        band = band_of<TILE>(p, b, grp, group_rows, false);
+    }
+    __device__ __noinline__ bool next(const TreeParams& p) {
+        while (pos < end) {
+            const int w = units();
+            if (pos >= base + w || (p.num_splits == 1 && pos > base)) {
+                // a whole item belongs to the range that holds its first unit
+                if (pos < base + w) pos = base + w;
+                base += w;
+                if (++kvh == p.n_kv_heads) {
+                    kvh = 0;
+                    if (++entry == entries) return false;
+                    load(p);
+                }
+                continue;
+            }
+            first = pos - base;
+            if (p.num_splits == 1) {
+                index = 0;
+                count = 1;
+                n = band.tiles;
+                pos = base + w;
+            } else {
+                const int take = min(w - first, end - pos);
+                const int seg0 = base / per;
+                index = pos / per - seg0;
+                count = (base + w - 1) / per - seg0 + 1;
+                n = min(take, band.tiles);
+                pos += take;
+            }
+            return true;
+        }
+        return false;
+    }
+};
+
+// The range of cluster `me` of `clusters`: the total of all items' units, then
+// the item that holds the range's first unit.  Every thread of the block calls
+// it; s_scan: 36 int of shared memory.
+template <int TILE, int THREADS>
+__device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams& p, int clusters, int me, int* s_scan) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    walk.entries = p.batch * walk.groups;
+    int* s_at = s_scan + 32;                                // start's entry, unit
+    constexpr int NW = THREADS / 32;
+    auto entry_units = [&](int e, bool record) -> int {
+        if (e >= walk.entries) return 0;
+        const int eb = e / walk.groups;
+        const BandOf<TILE> d = band_of<TILE>(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
+        return max(1, d.tiles) * p.n_kv_heads;
+    };
+    int total = 0, mine0 = 0;                        // mine0: entry tid's units
+    for (int e = tid; e < walk.entries; e += THREADS) {
+        const int u = entry_units(e, blockIdx.x == 0);
+        if (e == tid) mine0 = u;
+        total += u;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) s_scan[warp] = total;
+    __syncthreads();
+    total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
+    // ranges short enough to balance, long enough that no item has more
+    // than num_splits segments
+    walk.per = (total + clusters - 1) / clusters;
+    if (p.num_splits > 1) walk.per = max(walk.per, p.min_range);
+    walk.per = max(walk.per, 1);
+    const long long begin = static_cast<long long>(me) * walk.per;
+    walk.pos = static_cast<int>(min(begin, static_cast<long long>(total)));
+    walk.end = min(total - walk.pos, walk.per) + walk.pos;
+    int before = 0;
+    if (walk.pos < walk.end) {
+        for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
+            const int u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
+            int x = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[warp] = x;
+            __syncthreads();
+            const int ws = lane < NW ? s_scan[lane] : 0;
+            x += before + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
+            const int sum = before + __reduce_add_sync(0xffffffffu, ws);
+            if (walk.pos >= x - u && walk.pos < x) {
+                s_at[0] = e0 + tid;
+                s_at[1] = x - u;
+            }
+            before = sum;
+            if (walk.pos < before) break;
+        }
+    }
+    __syncthreads();
+    walk.entry = s_at[0];
+    walk.kvh = 0;
+    walk.base = s_at[1];
+    if (walk.pos < walk.end) {
+        walk.load(p);
+        walk.kvh = (walk.pos - walk.base) / walk.units();
+        walk.base += walk.kvh * walk.units();
+    }
+}
+
+// The mask words of the tokens tok0 .. tok0 + toks - 1 (bits at and behind cnt
+// name no token) and the depths of all cnt tokens, by `threads` threads.
+__device__ __forceinline__ void load_masks(const TreeParams& p, int b, int cnt, int tok0, int toks, int* s_depth,
+                                           uint32_t* s_mask, int thread, int threads) {
+    const int W = p.mask_words;
+    auto word = [&](int t, int w) -> uint32_t {
+        const int left = cnt - 32 * w;
+        const uint32_t m = static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * W + w]);
+        return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
+    };
+#pragma unroll 1
+    for (int t = thread; t < cnt; t += threads) {
+        int c = 0;
+#pragma unroll 1
+        for (int w = 0; w < W; ++w) c += __popc(word(t, w));
+        s_depth[t] = c - 1;
+    }
+#pragma unroll 1
+    for (int i = thread; i < toks * W; i += threads) {
+        const int t = tok0 + i / W, w = i % W;
+        s_mask[i] = t < cnt ? word(t, w) : 0u;
+    }
+}
+
+}  // namespace tree
+
+// decode_tree_pair_sm103.cu: more than 64 rows per KV head.
+cudaError_t launch_tree_pair(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p, bool fp8,
+                             cudaStream_t stream);
+// decode_tree_sm103.cu: combines the segments' partials of rows in groups of group_rows.
+cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t stream);
+
+}  // namespace fa512
