@@ -79,7 +79,7 @@ struct Cfg {
     static constexpr int top = vote + 2 * GROUPS * 4;                // [2][ROWS] float
     static constexpr int scan = top + 2 * ROWS * 4;
     static constexpr int bars = scan + 160;
-    static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, S_FULL = 4 * NS, S_FREE = S_FULL + NB,
+    static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, V_PEER = 4 * NS, S_FULL = 5 * NS, S_FREE = S_FULL + NB,
                          P_FULL = S_FREE + NB, PV_DONE = P_FULL + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
                          DRAIN = O_FREE + 1, VOTE = DRAIN + 1, TOP = VOTE + 2 * GROUPS, SEEN = TOP + 2 * GROUPS,
                          N_BARS = SEEN + 2;
@@ -128,13 +128,14 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uns
     return mbar_try_wait_cluster(smem_u32(bar), parity) || wait_cluster_slow(bar, parity, err, abort);
 }
 
-// Reduces 32 values per lane over the warp at once: lane i gets everyone's
-// v[i] (31 shuffles in which halves swap the values that the other half keeps).
+// Reduces 16 values per lane over the warp at once: lane i gets everyone's
+// v[i % 16] (15 shuffles in which halves swap the values that the other half
+// keeps, and one that joins the warp's halves).
 template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
+__device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = GW / 2; o >= 1; o >>= 1) {
+    for (int o = 8; o >= 1; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int j = 0; j < o; ++j) {
@@ -142,13 +143,22 @@ __device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
             v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
         }
     }
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 // A tile of cached keys inside every row's window: no key of it needs a mask.
 __device__ __forceinline__ bool whole_tile(const TreeParams& p, const Band& bd, int key0) {
     return key0 + TILE <= min(bd.start, bd.hi) &&
            (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
+}
+
+// Whether some key of a tile may be seen by no row, so that its V row has to
+// be cleared.  Without a mask every key of [lo, hi) and every sink is seen by
+// some row; with one, a drafted key may be named by nobody, and the window's
+// lower edge is known only to lie in [lo, place_max - window].
+__device__ __forceinline__ bool dirty_tile(const TreeParams& p, const Band& bd, int key0) {
+    if (p.tree_mask) return !whole_tile(p, bd, key0);
+    return key0 + TILE > bd.hi || (key0 < bd.lo && key0 + TILE > bd.sink_end);
 }
 
 template <bool FP8>
@@ -172,7 +182,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             mbar_init(&bars[C::FULL + i], 1);
             mbar_init(&bars[C::EMPTY + i], 1);
             mbar_init(&bars[C::V_RAW + i], 1);
-            mbar_init(&bars[C::V_CLEAN + i], 2 * SW);
+            mbar_init(&bars[C::V_CLEAN + i], SW);
+            mbar_init(&bars[C::V_PEER + i], 1);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&bars[C::S_FULL + i], 1);
@@ -249,7 +260,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     if (lane < 16) rows[lane] = row;
                     __syncwarp();
                 }
-                const bool raw = v && !whole_tile(p, d, d.key0(walk.first + t));
+                const bool raw = v && dirty_tile(p, d, d.key0(walk.first + t));
                 const CUtensorMap* tm = v ? &tmv : &tmk;
 #pragma unroll 1
                 for (int c = 0; c < C::SLOTS; ++c) {
@@ -352,6 +363,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 for (int c = 0; c < C::SLOTS; ++c) {
                     uint32_t& used = raw ? clean_used : full_used;
                     if (!wait((raw ? C::V_CLEAN : C::FULL) + slot, (used >> slot) & 1)) return false;
+                    if (raw && !wait(C::V_PEER + slot, (used >> slot) & 1)) return false;
                     used ^= 1u << slot;
                     tc_fence_after_sync();
                     const uint64_t vd = make_sdesc_sw128(ring + slot * SLOT, SIDE, 1024);
@@ -400,7 +412,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                         if (ok)
                             ok = issue_pv(j == LOOK,
-                                          !whole_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK)));
+                                          dirty_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK)));
                     }
                 }
                 ++segment;
@@ -408,6 +420,31 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             if (elect_one()) commit2_local(&bars[C::DRAIN]);
             __syncwarp();
             (void)mbar_wait(&bars[C::DRAIN], 0, p.err);
+        } else {
+            // ------------------------------------------- cleared slots, told to the leader's MMA
+            // (a remote arrival holds its thread about a microsecond: not the softmax warps')
+            int slot = 0;
+            uint32_t used = 0;
+            bool ok = true;
+            while (ok && walk.next(p)) {
+                const int n = walk.n;
+#pragma unroll 1
+                for (int j = 0; j < n + LOOK && ok; ++j) {
+                    if (j < n) slot = (slot + C::SLOTS) % NS;
+                    if (j < LOOK) continue;
+                    if (!dirty_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK))) {
+                        slot = (slot + C::SLOTS) % NS;
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < C::SLOTS && ok; ++c) {
+                        ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::V_CLEAN + slot], (used >> slot) & 1, p.err, abort));
+                        used ^= 1u << slot;
+                        if (ok && lane == 0) mbar_arrive_remote(bar_of(C::V_PEER + slot, 0));
+                        slot = slot + 1 == NS ? 0 : slot + 1;
+                    }
+                }
+            }
         }
     } else {
         // -------------------------------------------------------------------- softmax
@@ -538,6 +575,17 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             bar_sync(ALL, SW * 32);
         };
 
+        // P of the last tile is published (made visible to the tensor cores of
+        // both CTAs) during the next tile's vote: by then its stores into the
+        // other CTA have arrived, and neither the fence nor the arrival waits.
+        bool unpublished = false;
+        auto publish = [&]() {
+            fence_proxy_async_all();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(bar_of(C::P_FULL, 0));
+            unpublished = false;
+        };
         int done = -1;                                       // tiles of the segment whose O is to be read, -1: none
         bool direct = false;                                 // its rows are whole
         for (;;) {
@@ -594,56 +642,54 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
-                float x[GW];
-                {
-                    uint32_t raw[GW];
-                    tmem_ld32(tmem + lanes + TM_S + static_cast<uint32_t>(sbuf * ROWS + col0), raw);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < GW; ++i) x[i] = __uint_as_float(raw[i]);
-                }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(bar_of(C::S_FREE + sbuf, 0));
+                const uint32_t s_at = tmem + lanes + TM_S + static_cast<uint32_t>(sbuf * ROWS + col0);
+                const int s_free = C::S_FREE + sbuf;
                 if (++sbuf == NB) {
                     sbuf = 0;
                     ++suse;
                 }
-                // log2 units, less the rows' references
-#pragma unroll
-                for (int i = 0; i < GW; i += 2) {
-                    const float4 f = *reinterpret_cast<const float4*>(&s_mb[col0 + i]);
-                    x[i] = fmaf(x[i], f.x, f.y);
-                    x[i + 1] = fmaf(x[i + 1], f.z, f.w);
-                }
                 const bool whole = whole_tile(p, bd, key0);
-                bool seen = true;                            // by some row of the group
-                if (!whole) {
-                    const int c = key - bd.start;
-                    const bool drafted = c >= 0 && p.tree_mask;
-                    // the key's place; its own mask says whether a drafted one is seen
-                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
-                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
-                    const bool sink = kp < bd.sink_end;
-                    uint32_t bits = 0xffffffffu;
-                    if (drafted && key < bd.hi) {
-                        bits = 0u;
+                bool seen = whole;                           // by some row of the group
+                // Scores of 16 of the group's rows, log2 units less the rows'
+                // references.  They are read from tensor memory where they are
+                // needed, not kept: 32 scores beside the 32 row sums would spill.
+                auto scores = [&](int c0, float (&x)[16]) {
+                    uint32_t raw[16];
+                    tmem_ld16(s_at + static_cast<uint32_t>(c0), raw);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < GW; ++i)
-                            bits |= ((s_mask[s_see[col0 + i].z + (c >> 5)] >> (c & 31)) & 1u) << i;
+                    for (int i = 0; i < 16; i += 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(&s_mb[col0 + c0 + i]);
+                        x[i] = fmaf(__uint_as_float(raw[i]), f.x, f.y);
+                        x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f.z, f.w);
                     }
-                    seen = false;
+                    if (!whole) {
+                        const int c = key - bd.start;
+                        const bool drafted = c >= 0 && p.tree_mask;
+                        // the key's place; its own mask says whether a drafted one is seen
+                        const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
+                        const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
+                        const bool sink = kp < bd.sink_end;
+                        const uint32_t* words = s_mask + (drafted && key < bd.hi ? c >> 5 : 0);
+                        const bool bits = drafted && key < bd.hi;
 #pragma unroll
-                    for (int i = 0; i < GW; ++i) {
-                        const int4 r = s_see[col0 + i];
-                        const bool see = last <= r.x && (kp > r.y || sink) && ((bits >> i) & 1u);
-                        x[i] = see ? x[i] : -INFINITY;
-                        seen = seen || see;
+                        for (int i = 0; i < 16; ++i) {
+                            const int4 r = s_see[col0 + c0 + i];
+                            bool see = last <= r.x && (kp > r.y || sink);
+                            if (bits) see = see && ((words[r.z] >> (c & 31)) & 1u);
+                            x[i] = see ? x[i] : -INFINITY;
+                            seen = seen || see;
+                        }
                     }
+                };
+                float high = -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < GW; c0 += 16) {
+                    float x[16];
+                    scores(c0, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
                 }
-                float high = x[0];
-#pragma unroll
-                for (int i = 1; i < GW; ++i) high = fmaxf(high, x[i]);
                 // ---- the vote, with the other CTA's keys
                 bool over = bar_or(bar, 128, high > C::THR || fresh || !ok);
                 {
@@ -654,6 +700,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         mbar_arrive_expect_tx(vb, 4);
                         st_async_b32(map_to_cta(smem_u32(sv), peer), over ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
                     }
+                    if (unpublished) publish();
                     const bool got = wait_cluster(vb, (g >> 1) & 1, p.err, abort);
                     ok = __all_sync(0xffffffffu, got) && ok;
                     over = over || !ok || *reinterpret_cast<volatile int*>(sv) != 0;
@@ -661,11 +708,13 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 bool pv_waited = g == 0;
                 if (over) {
                     if (!(ok = bar_and(bar, 128, ok))) break;
-                    float v[GW];
-#pragma unroll
-                    for (int i = 0; i < GW; ++i) v[i] = x[i];
-                    const float mx = reduce_columns(v, [](float a, float c) { return fmaxf(a, c); });
-                    s_red[quad * ROWS + col0 + lane] = mx;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < GW; c0 += 16) {
+                        float x[16];
+                        scores(c0, x);
+                        const float mx = reduce_columns(x, [](float a, float c) { return fmaxf(a, c); });
+                        if (lane < 16) s_red[quad * ROWS + col0 + c0 + lane] = mx;
+                    }
                     bar_sync(bar, 128);
                     const int cl = col0 + lane;
                     float up = fmaxf(fmaxf(s_red[cl], s_red[ROWS + cl]), fmaxf(s_red[2 * ROWS + cl], s_red[3 * ROWS + cl]));
@@ -678,10 +727,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     const float m1 = none ? up : m0 + shift;
                     fresh = __any_sync(0xffffffffu, m1 == -INFINITY);
 #pragma unroll
-                    for (int i = 0; i < GW; ++i) {
-                        x[i] -= __shfl_sync(0xffffffffu, shift, i);
-                        l[i] *= __shfl_sync(0xffffffffu, a, i);
-                    }
+                    for (int i = 0; i < GW; ++i) l[i] *= __shfl_sync(0xffffffffu, a, i);
                     if (t > 0) {
                         // O is at rest once P V of the last tile has completed
                         const bool got = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
@@ -710,56 +756,59 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     bar_sync(bar, 128);
                 }
+                // rows 0-63 are CTA 0's operand, 64-127 CTA 1's
+                const int line = rank * HALF_TILE + kk;
+                const uint32_t dst = map_to_cta(smem_u32(smem + C::p + line * C::P_LINE), grp >> 1);
 #pragma unroll
-                for (int i = 0; i < GW; ++i) {
-                    x[i] = fast_exp2(x[i]);
-                    l[i] += x[i];
-                }
-                // P's buffers are free, and V of this tile will be read, after P V of the last tile
-                if (!pv_waited) {
-                    const bool got = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
-                    ok = __all_sync(0xffffffffu, got) && ok;
-                }
-                {
-                    // rows 0-63 are CTA 0's operand, 64-127 CTA 1's
-                    const int line = rank * HALF_TILE + kk;
-                    const uint32_t dst = map_to_cta(smem_u32(smem + C::p + line * C::P_LINE), grp >> 1);
+                for (int h = 0; h < GW / 16; ++h) {
+                    float x[16];
+                    scores(16 * h, x);
+                    if (h == GW / 16 - 1) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote_relaxed(bar_of(s_free, 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[i] = fast_exp2(x[i]);
+                        l[16 * h + i] += x[i];
+                    }
+                    // P's buffers are free, and V of this tile will be read, after P V of the last tile
+                    if (h == 0 && !pv_waited) {
+                        const bool got = wait_or_abort(&bars[C::PV_DONE], (g - 1) & 1, p.err, abort);
+                        ok = __all_sync(0xffffffffu, got) && ok;
+                    }
                     if constexpr (FP8) {
+                        uint32_t w[3][4] = {};
 #pragma unroll
-                        for (int c = 0; c < GW / 16; ++c) {
-                            uint32_t w[3][4] = {};
+                        for (int j = 0; j < 8; ++j) {
+                            float a = x[2 * j] * C::P_SCALE, d = x[2 * j + 1] * C::P_SCALE;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float a = x[16 * c + 2 * j] * C::P_SCALE, d = x[16 * c + 2 * j + 1] * C::P_SCALE;
-#pragma unroll
-                                for (int e = 0; e < 3; ++e) {
-                                    float va, vd;
-                                    w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
-                                    a -= va;
-                                    d -= vd;
-                                }
+                            for (int e = 0; e < 3; ++e) {
+                                float va, vd;
+                                w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
+                                a -= va;
+                                d -= vd;
                             }
-                            const int piece = line_piece<C::P_LINE>(line, (grp & 1) * (GW / 16) + c);
-#pragma unroll
-                            for (int e = 0; e < 3; ++e)
-                                st_cluster_u4(dst + e * C::P_TERM + piece, w[e][0], w[e][1], w[e][2], w[e][3]);
                         }
+                        const int piece = line_piece<C::P_LINE>(line, (grp & 1) * (GW / 16) + h);
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            st_cluster_u4(dst + e * C::P_TERM + piece, w[e][0], w[e][1], w[e][2], w[e][3]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < GW / 8; ++c)
-                            st_cluster_u4(dst + line_piece<C::P_LINE>(line, (grp & 1) * (GW / 8) + c),
+                        for (int c = 0; c < 2; ++c)
+                            st_cluster_u4(dst + line_piece<C::P_LINE>(line, (grp & 1) * (GW / 8) + 2 * h + c),
                                           pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
                                           pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
                     }
                 }
-                fence_proxy_async_all();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(bar_of(C::P_FULL, 0));
+                unpublished = true;
 
-                // ---- a tile with masks: clear the V rows of keys that no row
-                // sees (of both CTAs' keys) and hand the slots to the MMA
-                if (!whole) {
+                // ---- clear the V rows of keys that no row sees (of both CTAs'
+                // keys) and hand the slots to the MMA
+                if (dirty_tile(p, bd, key0)) {
+                    publish();
                     s_seen[grp * HALF_TILE + kk] = seen;
                     if (!(ok = bar_and(ALL, SW * 32, ok))) {
                         out = true;
@@ -794,7 +843,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(bar_of(C::V_CLEAN + s, 0));
+                        if (lane == 0) mbar_arrive(&bars[C::V_CLEAN + s]);
                     }
                     // the flags may be written again once everyone has read them
                     if (!(ok = bar_and(ALL, SW * 32, ok))) {
@@ -803,13 +852,20 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                 }
             }
+            if (unpublished) publish();
             ring_base = (ring_base + 2 * n * C::SLOTS) % NS;
             // all go on or all stop (here or at a vote inside a tile): no warp
             // may wait at a barrier for one that has left
             if (out || !(ok = bar_and(ALL, SW * 32, ok))) break;
             // ---- row sums: lanes, the four quadrants' warps, the other CTA
-            const float part = reduce_columns(l, [](float a, float c) { return a + c; });
-            s_red[quad * ROWS + col0 + lane] = part;
+#pragma unroll
+            for (int h = 0; h < GW / 16; ++h) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = l[16 * h + i];
+                const float part = reduce_columns(v, [](float a, float c) { return a + c; });
+                if (lane < 16) s_red[quad * ROWS + col0 + 16 * h + lane] = part;
+            }
             bar_sync(bar, 128);
             const int cl = col0 + lane;
             const float mine = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
