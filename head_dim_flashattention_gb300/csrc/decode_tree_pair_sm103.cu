@@ -11,7 +11,9 @@
 //
 // A CTA's softmax threads hold its 128 keys against all 128 rows; Q and P^T,
 // the B operands, are split by rows, 64 in each CTA, so half of each P^T tile
-// is stored into the other CTA's shared memory.  Both CTAs have to scale by
+// belongs in the other CTA: it is staged here, and a courier warp moves it
+// with one bulk copy (a store into the other CTA would hold the softmax
+// threads at their fence and release for two microseconds a tile).  Both CTAs have to scale by
 // the same references: every tile, each column group (32 rows) swaps its vote
 // on "a score outgrew the reference" with the same group of the other CTA,
 // and, when either says so, the column maxima; at the end of a segment the row
@@ -40,10 +42,10 @@ constexpr int HALF_ROWS = 64;            // rows of a CTA's B operands
 constexpr int GW = 32;                   // rows (columns of S^T) of a softmax warp
 constexpr int GROUPS = ROWS / GW;
 constexpr int SW = 4 * GROUPS;           // softmax warps: (column group, TMEM lane quadrant)
-constexpr int THREADS = 64 + SW * 32;
+constexpr int COURIER = 2 + SW;          // warp that moves P to the other CTA
+constexpr int THREADS = (COURIER + 1) * 32;
 constexpr int LOOK = 1;                  // S^T tiles computed ahead of O^T += V^T P^T
 constexpr int NB = LOOK + 1;
-constexpr int NS = 3;                    // ring slots
 constexpr uint32_t TM_O = 0, TM_S = 256;
 using Walk = WalkOf<TILE>;
 using Band = BandOf<TILE>;
@@ -51,6 +53,7 @@ using Band = BandOf<TILE>;
 template <bool FP8>
 struct Cfg {
     static constexpr int EB = FP8 ? 1 : 2;
+    static constexpr int NS = FP8 ? 2 : 3;               // ring slots
     static constexpr int CHUNKS = D * EB / 128;          // 128-byte column chunks of the head dim
     static constexpr int SLOTS = CHUNKS / 2;             // ring slots of a K (V) tile in a CTA: 4 or 2
     static constexpr int Q_CHUNK = HALF_ROWS * 128;
@@ -65,7 +68,10 @@ struct Cfg {
     static constexpr int ring = 0;
     static constexpr int q = ring + NS * SLOT;
     static constexpr int p = q + Q_TERMS * Q_TERM;
-    static constexpr int mask = p + P_TERMS * P_TERM;    // [ROWS tokens][words]
+    static constexpr int HALF_TERM = P_TERM / 2;         // one CTA's keys
+    static constexpr int stage = p + P_TERMS * P_TERM;   // P of this CTA's keys for the other CTA's rows
+    static constexpr int STAGE_BYTES = P_TERMS * HALF_TERM;
+    static constexpr int mask = stage + STAGE_BYTES;     // [ROWS tokens][words]
     static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int m = red + 4 * ROWS * 4;         // [ROWS] float: references
@@ -80,7 +86,7 @@ struct Cfg {
     static constexpr int scan = top + 2 * ROWS * 4;
     static constexpr int bars = scan + 160;
     static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, V_PEER = 4 * NS, S_FULL = 5 * NS, S_FREE = S_FULL + NB,
-                         P_FULL = S_FREE + NB, PV_DONE = P_FULL + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
+                         P_FULL = S_FREE + NB, P_PEER = P_FULL + 1, STAGED = P_PEER + 1, PV_DONE = STAGED + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
                          DRAIN = O_FREE + 1, VOTE = DRAIN + 1, TOP = VOTE + 2 * GROUPS, SEEN = TOP + 2 * GROUPS,
                          N_BARS = SEEN + 2;
     static constexpr int misc = bars + N_BARS * 8;       // tmem address, abort flag
@@ -99,14 +105,14 @@ __device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t
                  ::"r"(addr), "r"(v), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+// Bulk copy of `bytes` from this CTA's shared memory into another CTA's; the
+// bytes complete_tx on the destination CTA's mbarrier.
+__device__ __forceinline__ void bulk_copy_to_cluster(uint32_t dst_cluster, uint32_t src_cta, uint32_t bytes,
+                                                     uint32_t bar_cluster) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst_cluster), "r"(src_cta), "r"(bytes), "r"(bar_cluster)
                  : "memory");
 }
-// Orders this thread's shared-memory writes, in either CTA, before later
-// accesses of them by the async proxy (the tensor cores).
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Waits, bounded, with cluster-scope acquire: for arrivals of the other CTA.
 static __device__ __noinline__ bool wait_cluster_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
@@ -166,6 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ TreeParams p) {
     using C = Cfg<FP8>;
+    constexpr int NS = C::NS;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -189,7 +196,9 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             mbar_init(&bars[C::S_FULL + i], 1);
             mbar_init(&bars[C::S_FREE + i], 2 * SW);
         }
-        mbar_init(&bars[C::P_FULL], 2 * SW);
+        mbar_init(&bars[C::P_FULL], SW);
+        mbar_init(&bars[C::P_PEER], 1);
+        mbar_init(&bars[C::STAGED], SW);
         mbar_init(&bars[C::PV_DONE], 1);
         mbar_init(&bars[C::Q_FULL], 2 * SW);
         mbar_init(&bars[C::O_FREE], 2 * SW);
@@ -357,7 +366,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 return true;
             };
             auto issue_pv = [&](bool fresh, bool raw) -> bool {
-                if (!wait(C::P_FULL, g_p & 1)) return false;
+                if (!wait(C::P_FULL, g_p & 1) || !wait(C::P_PEER, g_p & 1)) return false;
                 const uint32_t acc0 = fresh ? 0u : 1u;
 #pragma unroll 1
                 for (int c = 0; c < C::SLOTS; ++c) {
@@ -443,6 +452,31 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         if (ok && lane == 0) mbar_arrive_remote(bar_of(C::V_PEER + slot, 0));
                         slot = slot + 1 == NS ? 0 : slot + 1;
                     }
+                }
+            }
+        }
+    } else if (warp == COURIER) {
+        // ------------------------------------------------ P for the other CTA's rows
+        int g = 0;
+        bool ok = true;
+        while (ok && walk.next(p)) {
+            const int n = walk.n;
+#pragma unroll 1
+            for (int t = 0; t < n && ok; ++t, ++g) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::STAGED], g & 1, p.err, abort));
+                if (!ok) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int e = 0; e < C::P_TERMS; ++e)
+                        bulk_copy_to_cluster(map_to_cta(smem_u32(smem + C::p + e * C::P_TERM + rank * C::HALF_TERM), rank ^ 1),
+                                             smem_u32(smem + C::stage + e * C::HALF_TERM), C::HALF_TERM,
+                                             bar_of(C::P_FULL, rank ^ 1));
+                }
+                __syncwarp();
+                if (rank == 1) {
+                    // this CTA's operand is complete: the leader's MMA may read it
+                    ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::P_FULL], g & 1, p.err, abort));
+                    if (ok && lane == 0) mbar_arrive_remote(bar_of(C::P_PEER, 0));
                 }
             }
         }
@@ -575,17 +609,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             bar_sync(ALL, SW * 32);
         };
 
-        // P of the last tile is published (made visible to the tensor cores of
-        // both CTAs) during the next tile's vote: by then its stores into the
-        // other CTA have arrived, and neither the fence nor the arrival waits.
-        bool unpublished = false;
-        auto publish = [&]() {
-            fence_proxy_async_all();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(bar_of(C::P_FULL, 0));
-            unpublished = false;
-        };
         int done = -1;                                       // tiles of the segment whose O is to be read, -1: none
         bool direct = false;                                 // its rows are whole
         for (;;) {
@@ -700,7 +723,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         mbar_arrive_expect_tx(vb, 4);
                         st_async_b32(map_to_cta(smem_u32(sv), peer), over ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
                     }
-                    if (unpublished) publish();
                     const bool got = wait_cluster(vb, (g >> 1) & 1, p.err, abort);
                     ok = __all_sync(0xffffffffu, got) && ok;
                     over = over || !ok || *reinterpret_cast<volatile int*>(sv) != 0;
@@ -756,9 +778,11 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     bar_sync(bar, 128);
                 }
-                // rows 0-63 are CTA 0's operand, 64-127 CTA 1's
-                const int line = rank * HALF_TILE + kk;
-                const uint32_t dst = map_to_cta(smem_u32(smem + C::p + line * C::P_LINE), grp >> 1);
+                // rows 0-63 are CTA 0's operand, 64-127 CTA 1's: this CTA's go
+                // into its operand, the other's are staged
+                const bool own = (grp >> 1) == rank;
+                uint8_t* dst = smem + (own ? C::p + rank * C::HALF_TERM : C::stage) + kk * C::P_LINE;
+                const int term = own ? C::P_TERM : C::HALF_TERM;
 #pragma unroll
                 for (int h = 0; h < GW / 16; ++h) {
                     float x[16];
@@ -791,24 +815,30 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                                 d -= vd;
                             }
                         }
-                        const int piece = line_piece<C::P_LINE>(line, (grp & 1) * (GW / 16) + h);
+                        const int piece = line_piece<C::P_LINE>(kk, (grp & 1) * (GW / 16) + h);
 #pragma unroll
                         for (int e = 0; e < 3; ++e)
-                            st_cluster_u4(dst + e * C::P_TERM + piece, w[e][0], w[e][1], w[e][2], w[e][3]);
+                            *reinterpret_cast<uint4*>(dst + e * term + piece) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
                     } else {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            st_cluster_u4(dst + line_piece<C::P_LINE>(line, (grp & 1) * (GW / 8) + 2 * h + c),
-                                          pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
-                                          pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+                            *reinterpret_cast<uint4*>(dst + line_piece<C::P_LINE>(kk, (grp & 1) * (GW / 8) + 2 * h + c)) =
+                                make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                                           pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
                     }
                 }
-                unpublished = true;
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[C::STAGED]);
+                    if (sw == 0) mbar_arrive_expect_tx(&bars[C::P_FULL], C::STAGE_BYTES);
+                    else mbar_arrive(&bars[C::P_FULL]);
+                }
 
                 // ---- clear the V rows of keys that no row sees (of both CTAs'
                 // keys) and hand the slots to the MMA
                 if (dirty_tile(p, bd, key0)) {
-                    publish();
                     s_seen[grp * HALF_TILE + kk] = seen;
                     if (!(ok = bar_and(ALL, SW * 32, ok))) {
                         out = true;
@@ -852,7 +882,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                 }
             }
-            if (unpublished) publish();
             ring_base = (ring_base + 2 * n * C::SLOTS) % NS;
             // all go on or all stop (here or at a vote inside a tile): no warp
             // may wait at a barrier for one that has left
