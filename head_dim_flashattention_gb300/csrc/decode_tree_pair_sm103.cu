@@ -672,7 +672,25 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     ++suse;
                 }
                 const bool whole = whole_tile(p, bd, key0);
-                bool seen = whole;                           // by some row of the group
+                uint32_t vis = 0xffffffffu;                  // bit i: row col0 + i sees this thread's key
+                if (!whole) {
+                    const int c = key - bd.start;
+                    const bool drafted = c >= 0 && p.tree_mask;
+                    // the key's place; its own mask says whether a drafted one is seen
+                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
+                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
+                    const bool sink = kp < bd.sink_end;
+                    const bool bits = drafted && key < bd.hi;
+                    const uint32_t* words = s_mask + (bits ? c >> 5 : 0);
+                    vis = 0u;
+#pragma unroll 4
+                    for (int i = 0; i < GW; ++i) {
+                        const int4 r = s_see[col0 + i];
+                        bool see = last <= r.x && (kp > r.y || sink);
+                        if (bits) see = see && ((words[r.z] >> (c & 31)) & 1u);
+                        vis |= see ? 1u << i : 0u;
+                    }
+                }
                 // Scores of 16 of the group's rows, log2 units less the rows'
                 // references.  They are read from tensor memory where they are
                 // needed, not kept: 32 scores beside the 32 row sums would spill.
@@ -687,22 +705,9 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f.z, f.w);
                     }
                     if (!whole) {
-                        const int c = key - bd.start;
-                        const bool drafted = c >= 0 && p.tree_mask;
-                        // the key's place; its own mask says whether a drafted one is seen
-                        const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
-                        const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
-                        const bool sink = kp < bd.sink_end;
-                        const uint32_t* words = s_mask + (drafted && key < bd.hi ? c >> 5 : 0);
-                        const bool bits = drafted && key < bd.hi;
+                        const uint32_t v = vis >> c0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int4 r = s_see[col0 + c0 + i];
-                            bool see = last <= r.x && (kp > r.y || sink);
-                            if (bits) see = see && ((words[r.z] >> (c & 31)) & 1u);
-                            x[i] = see ? x[i] : -INFINITY;
-                            seen = seen || see;
-                        }
+                        for (int i = 0; i < 16; ++i) x[i] = v & (1u << i) ? x[i] : -INFINITY;
                     }
                 };
                 float high = -INFINITY;
@@ -839,23 +844,32 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 // ---- clear the V rows of keys that no row sees (of both CTAs'
                 // keys) and hand the slots to the MMA
                 if (dirty_tile(p, bd, key0)) {
-                    s_seen[grp * HALF_TILE + kk] = seen;
-                    if (!(ok = bar_and(ALL, SW * 32, ok))) {
-                        out = true;
-                        break;
-                    }
+                    bool seen, their_seen;
+                    if (!p.tree_mask) {
+                        const int their_key = key0 + peer * HALF_TILE + kk;
+                        seen = key < bd.hi && (key >= bd.lo || key < bd.sink_end);
+                        their_seen = their_key < bd.hi && (their_key >= bd.lo || their_key < bd.sink_end);
+                    } else {
+                        // with masks only the rows know: OR over the groups, then both CTAs swap
+                        s_seen[grp * HALF_TILE + kk] = vis != 0u;
+                        if (!(ok = bar_and(ALL, SW * 32, ok))) {
+                            out = true;
+                            break;
+                        }
+                        seen = false;
 #pragma unroll
-                    for (int i = 0; i < GROUPS; ++i) seen = seen || s_seen[i * HALF_TILE + kk];
-                    const int par = partial_tiles & 1;
-                    int* theirs = reinterpret_cast<int*>(smem + C::pseen) + par * HALF_TILE + kk;
-                    if (grp == 0) {
-                        if (kk == 0) mbar_arrive_expect_tx(&bars[C::SEEN + par], HALF_TILE * 4);
-                        st_async_b32(map_to_cta(smem_u32(theirs), peer), seen ? 1u : 0u, bar_of(C::SEEN + par, peer));
+                        for (int i = 0; i < GROUPS; ++i) seen = seen || s_seen[i * HALF_TILE + kk];
+                        const int par = partial_tiles & 1;
+                        int* theirs = reinterpret_cast<int*>(smem + C::pseen) + par * HALF_TILE + kk;
+                        if (grp == 0) {
+                            if (kk == 0) mbar_arrive_expect_tx(&bars[C::SEEN + par], HALF_TILE * 4);
+                            st_async_b32(map_to_cta(smem_u32(theirs), peer), seen ? 1u : 0u, bar_of(C::SEEN + par, peer));
+                        }
+                        const bool got = wait_cluster(&bars[C::SEEN + par], (partial_tiles >> 1) & 1, p.err, abort);
+                        ok = __all_sync(0xffffffffu, got) && ok;
+                        ++partial_tiles;
+                        their_seen = *reinterpret_cast<volatile int*>(theirs) != 0;
                     }
-                    const bool got = wait_cluster(&bars[C::SEEN + par], (partial_tiles >> 1) & 1, p.err, abort);
-                    ok = __all_sync(0xffffffffu, got) && ok;
-                    ++partial_tiles;
-                    const bool their_seen = *reinterpret_cast<volatile int*>(theirs) != 0;
                     const int seq = ring_base + (min(t + LOOK + 1, n) + t) * C::SLOTS;
 #pragma unroll 1
                     for (int c = 0; c < C::SLOTS; ++c) {
@@ -876,7 +890,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         if (lane == 0) mbar_arrive(&bars[C::V_CLEAN + s]);
                     }
                     // the flags may be written again once everyone has read them
-                    if (!(ok = bar_and(ALL, SW * 32, ok))) {
+                    if (p.tree_mask && !(ok = bar_and(ALL, SW * 32, ok))) {
                         out = true;
                         break;
                     }
