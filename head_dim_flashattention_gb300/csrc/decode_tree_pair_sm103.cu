@@ -21,8 +21,8 @@
 //
 // Keys that no row sees may hold anything, also NaN, which P = 0 would not
 // silence: in the tiles where some may be (a sequence's end, a window's edges,
-// the drafted tokens) V arrives on barriers of its own, the softmax threads
-// clear the rows of such keys and hand each slot to the MMA themselves.
+// the drafted tokens) V arrives on barriers of its own, and a cleaner warp
+// clears the rows of such keys and hands each slot to the MMA.
 #include <cuda.h>
 
 #include "fa512_tree.cuh"
@@ -43,7 +43,8 @@ constexpr int GW = 32;                   // rows (columns of S^T) of a softmax w
 constexpr int GROUPS = ROWS / GW;
 constexpr int SW = 4 * GROUPS;           // softmax warps: (column group, TMEM lane quadrant)
 constexpr int COURIER = 2 + SW;          // warp that moves P to the other CTA
-constexpr int THREADS = (COURIER + 1) * 32;
+constexpr int CLEANER = COURIER + 1;     // warp that clears V rows
+constexpr int THREADS = (CLEANER + 1) * 32;
 constexpr int LOOK = 1;                  // S^T tiles computed ahead of O^T += V^T P^T
 constexpr int NB = LOOK + 1;
 constexpr uint32_t TM_O = 0, TM_S = 256;
@@ -85,10 +86,10 @@ struct Cfg {
     static constexpr int top = vote + 2 * GROUPS * 4;                // [2][ROWS] float
     static constexpr int scan = top + 2 * ROWS * 4;
     static constexpr int bars = scan + 160;
-    static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, V_PEER = 4 * NS, S_FULL = 5 * NS, S_FREE = S_FULL + NB,
+    static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, S_FULL = 4 * NS, S_FREE = S_FULL + NB,
                          P_FULL = S_FREE + NB, P_PEER = P_FULL + 1, STAGED = P_PEER + 1, PV_DONE = STAGED + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
                          DRAIN = O_FREE + 1, VOTE = DRAIN + 1, TOP = VOTE + 2 * GROUPS, SEEN = TOP + 2 * GROUPS,
-                         N_BARS = SEEN + 2;
+                         SEEN_HERE = SEEN + 2, N_BARS = SEEN_HERE + 1;
     static constexpr int misc = bars + N_BARS * 8;       // tmem address, abort flag
     static constexpr int total = misc + 16;
     static_assert(total + 1024 <= 232448, "shared memory of an SM");
@@ -189,8 +190,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             mbar_init(&bars[C::FULL + i], 1);
             mbar_init(&bars[C::EMPTY + i], 1);
             mbar_init(&bars[C::V_RAW + i], 1);
-            mbar_init(&bars[C::V_CLEAN + i], SW);
-            mbar_init(&bars[C::V_PEER + i], 1);
+            mbar_init(&bars[C::V_CLEAN + i], 2);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&bars[C::S_FULL + i], 1);
@@ -208,6 +208,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             mbar_init(&bars[C::TOP + i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars[C::SEEN + i], 1);
+        mbar_init(&bars[C::SEEN_HERE], SW);
         *abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmk);
@@ -372,7 +373,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 for (int c = 0; c < C::SLOTS; ++c) {
                     uint32_t& used = raw ? clean_used : full_used;
                     if (!wait((raw ? C::V_CLEAN : C::FULL) + slot, (used >> slot) & 1)) return false;
-                    if (raw && !wait(C::V_PEER + slot, (used >> slot) & 1)) return false;
                     used ^= 1u << slot;
                     tc_fence_after_sync();
                     const uint64_t vd = make_sdesc_sw128(ring + slot * SLOT, SIDE, 1024);
@@ -429,31 +429,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             if (elect_one()) commit2_local(&bars[C::DRAIN]);
             __syncwarp();
             (void)mbar_wait(&bars[C::DRAIN], 0, p.err);
-        } else {
-            // ------------------------------------------- cleared slots, told to the leader's MMA
-            // (a remote arrival holds its thread about a microsecond: not the softmax warps')
-            int slot = 0;
-            uint32_t used = 0;
-            bool ok = true;
-            while (ok && walk.next(p)) {
-                const int n = walk.n;
-#pragma unroll 1
-                for (int j = 0; j < n + LOOK && ok; ++j) {
-                    if (j < n) slot = (slot + C::SLOTS) % NS;
-                    if (j < LOOK) continue;
-                    if (!dirty_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK))) {
-                        slot = (slot + C::SLOTS) % NS;
-                        continue;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < C::SLOTS && ok; ++c) {
-                        ok = __all_sync(0xffffffffu, wait_or_abort(&bars[C::V_CLEAN + slot], (used >> slot) & 1, p.err, abort));
-                        used ^= 1u << slot;
-                        if (ok && lane == 0) mbar_arrive_remote(bar_of(C::V_PEER + slot, 0));
-                        slot = slot + 1 == NS ? 0 : slot + 1;
-                    }
-                }
-            }
         }
     } else if (warp == COURIER) {
         // ------------------------------------------------ P for the other CTA's rows
@@ -480,6 +455,81 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
             }
         }
+    } else if (warp == CLEANER) {
+        // --------------------------------------- V rows of keys that no row sees
+        int* s_pseen = reinterpret_cast<int*>(smem + C::pseen);
+        const uint8_t* s_seen = smem + C::seen;
+        int slot = 0, masked = 0;
+        uint32_t used = 0;
+        bool ok = true;
+        auto wait = [&](int bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_cluster(&bars[bar], parity, p.err, abort));
+        };
+        while (ok && walk.next(p)) {
+            const int n = walk.n;
+            const Band& bd = walk.band;
+#pragma unroll 1
+            for (int j = 0; j < n + LOOK && ok; ++j) {
+                if (j < n) slot = (slot + C::SLOTS) % NS;    // K(j)
+                if (j < LOOK) continue;
+                const int key0 = bd.key0(walk.first + j - LOOK);
+                if (!dirty_tile(p, bd, key0)) {
+                    slot = (slot + C::SLOTS) % NS;
+                    continue;
+                }
+                // bits k + 4 h: this lane's key lane + 32 k of key half h is seen
+                uint32_t seen = 0u;
+                if (p.tree_mask) {
+                    // this CTA's keys: over the column groups; then both CTAs swap
+                    const int par = masked & 1, peer = rank ^ 1;
+                    ok = wait(C::SEEN_HERE, masked & 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[C::SEEN + par], HALF_TILE * 4);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int kk = lane + 32 * k;
+                        const bool any = s_seen[kk] || s_seen[HALF_TILE + kk] || s_seen[2 * HALF_TILE + kk] || s_seen[3 * HALF_TILE + kk];
+                        seen |= any ? 1u << (k + 4 * rank) : 0u;
+                        st_async_b32(map_to_cta(smem_u32(&s_pseen[par * HALF_TILE + kk]), peer), any ? 1u : 0u,
+                                     bar_of(C::SEEN + par, peer));
+                    }
+                    ok = wait(C::SEEN + par, (masked >> 1) & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        seen |= *const_cast<volatile int*>(&s_pseen[par * HALF_TILE + lane + 32 * k]) ? 1u << (k + 4 * peer) : 0u;
+                    ++masked;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int key = key0 + lane + 32 * k;
+                        seen |= key < bd.hi && (key >= bd.lo || key < bd.sink_end) ? 1u << k : 0u;
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < C::SLOTS && ok; ++c) {
+                    ok = wait(C::V_RAW + slot, (used >> slot) & 1);
+                    if (!ok) break;
+                    used ^= 1u << slot;
+#pragma unroll 1
+                    for (int side = 0; side < 2; ++side) {
+                        const uint32_t here = seen >> (4 * (FP8 ? side : c & 1));
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k)
+                            if (!((here >> k) & 1u)) {
+                                uint4* v = reinterpret_cast<uint4*>(smem + C::ring + slot * SLOT + side * SIDE + (lane + 32 * k) * 128);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(bar_of(C::V_CLEAN + slot, 0));
+                    slot = slot + 1 == NS ? 0 : slot + 1;
+                }
+            }
+        }
     } else {
         // -------------------------------------------------------------------- softmax
         const int sw = warp - 2, quad = warp & 3, grp = sw >> 2;
@@ -500,9 +550,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
         int g = 0;                                           // running tile number
-        int sbuf = 0, swaps = 0, partial_tiles = 0;          // S^T buffer; column swaps, tiles with masks so far
-        uint32_t suse = 0, raw_used = 0;
-        int ring_base = 0;                                   // ring entries of the segments before, mod NS
+        int sbuf = 0, swaps = 0;                             // S^T buffer; column swaps so far
+        uint32_t suse = 0;
 
         // Swaps a value per column (lane) with the same group of the other
         // CTA; the answer comes to every warp of the group.
@@ -636,16 +685,22 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     const int d = (o >> 1) * 256 + rank * 128 + kk;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 info = *reinterpret_cast<const uint4*>(smem + C::info + (c0 + i) * 16);
-                        const float f = __uint_as_float(info.z);
-                        const size_t at = (static_cast<size_t>(info.y) << 32 | info.x) * D + d;
-                        const float val = f != 0.f ? __uint_as_float(r[i]) * f : 0.f;
-                        if (info.w) {
-                            if (direct)
-                                p.out[at] = __float2bfloat16_rn(val);
-                            else
-                                p.ws_o[at] = val;
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint4 ia = *reinterpret_cast<const uint4*>(smem + C::info + (c0 + i) * 16);
+                        const uint4 ib = *reinterpret_cast<const uint4*>(smem + C::info + (c0 + i + 1) * 16);
+                        const float fa = __uint_as_float(ia.z), fb = __uint_as_float(ib.z);
+                        const float a = fa != 0.f ? __uint_as_float(r[i]) * fa : 0.f;
+                        const float b = fb != 0.f ? __uint_as_float(r[i + 1]) * fb : 0.f;
+                        if (direct) {
+                            // lane pairs trade: the even lane stores both elements of row i, the odd one of row i + 1
+                            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+                            const uint4 info = lane & 1 ? ib : ia;
+                            const size_t at = (static_cast<size_t>(info.y) << 32 | info.x) * D + (d & ~1);
+                            const uint32_t two = lane & 1 ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                            if (info.w) *reinterpret_cast<uint32_t*>(p.out + at) = two;
+                        } else {
+                            if (ia.w) p.ws_o[(static_cast<size_t>(ia.y) << 32 | ia.x) * D + d] = a;
+                            if (ib.w) p.ws_o[(static_cast<size_t>(ib.y) << 32 | ib.x) * D + d] = b;
                         }
                     }
                 }
@@ -657,7 +712,6 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             float l[GW];
 #pragma unroll
             for (int i = 0; i < GW; ++i) l[i] = 0.f;
-            bool out = false;
             bool fresh = true;                               // some row may not have a reference yet
 #pragma unroll 1
             for (int t = 0; t < n; ++t, ++g) {
@@ -841,65 +895,15 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     else mbar_arrive(&bars[C::P_FULL]);
                 }
 
-                // ---- clear the V rows of keys that no row sees (of both CTAs'
-                // keys) and hand the slots to the MMA
-                if (dirty_tile(p, bd, key0)) {
-                    bool seen, their_seen;
-                    if (!p.tree_mask) {
-                        const int their_key = key0 + peer * HALF_TILE + kk;
-                        seen = key < bd.hi && (key >= bd.lo || key < bd.sink_end);
-                        their_seen = their_key < bd.hi && (their_key >= bd.lo || their_key < bd.sink_end);
-                    } else {
-                        // with masks only the rows know: OR over the groups, then both CTAs swap
-                        s_seen[grp * HALF_TILE + kk] = vis != 0u;
-                        if (!(ok = bar_and(ALL, SW * 32, ok))) {
-                            out = true;
-                            break;
-                        }
-                        seen = false;
-#pragma unroll
-                        for (int i = 0; i < GROUPS; ++i) seen = seen || s_seen[i * HALF_TILE + kk];
-                        const int par = partial_tiles & 1;
-                        int* theirs = reinterpret_cast<int*>(smem + C::pseen) + par * HALF_TILE + kk;
-                        if (grp == 0) {
-                            if (kk == 0) mbar_arrive_expect_tx(&bars[C::SEEN + par], HALF_TILE * 4);
-                            st_async_b32(map_to_cta(smem_u32(theirs), peer), seen ? 1u : 0u, bar_of(C::SEEN + par, peer));
-                        }
-                        const bool got = wait_cluster(&bars[C::SEEN + par], (partial_tiles >> 1) & 1, p.err, abort);
-                        ok = __all_sync(0xffffffffu, got) && ok;
-                        ++partial_tiles;
-                        their_seen = *reinterpret_cast<volatile int*>(theirs) != 0;
-                    }
-                    const int seq = ring_base + (min(t + LOOK + 1, n) + t) * C::SLOTS;
-#pragma unroll 1
-                    for (int c = 0; c < C::SLOTS; ++c) {
-                        const int s = (seq + c) % NS;
-                        const bool in = wait_or_abort(&bars[C::V_RAW + s], (raw_used >> s) & 1, p.err, abort);
-                        ok = __all_sync(0xffffffffu, in) && ok;
-                        raw_used ^= 1u << s;
-                        // the groups share out a key's line: side grp / 2, pieces 4 (grp % 2) ..
-                        const int side = grp >> 1;
-                        const int half = FP8 ? side : c & 1;
-                        if (in && !(half == rank ? seen : their_seen)) {
-                            uint4* v = reinterpret_cast<uint4*>(smem + C::ring + s * SLOT + side * SIDE + kk * 128) + 4 * (grp & 1);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[C::V_CLEAN + s]);
-                    }
-                    // the flags may be written again once everyone has read them
-                    if (p.tree_mask && !(ok = bar_and(ALL, SW * 32, ok))) {
-                        out = true;
-                        break;
-                    }
+                // with masks only the rows know whether some row sees a key
+                if (p.tree_mask && dirty_tile(p, bd, key0)) {
+                    s_seen[grp * HALF_TILE + kk] = vis != 0u;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::SEEN_HERE]);
                 }
             }
-            ring_base = (ring_base + 2 * n * C::SLOTS) % NS;
-            // all go on or all stop (here or at a vote inside a tile): no warp
-            // may wait at a barrier for one that has left
-            if (out || !(ok = bar_and(ALL, SW * 32, ok))) break;
+            // all go on or all stop: no warp may wait at a barrier for one that has left
+            if (!(ok = bar_and(ALL, SW * 32, ok))) break;
             // ---- row sums: lanes, the four quadrants' warps, the other CTA
 #pragma unroll
             for (int h = 0; h < GW / 16; ++h) {
