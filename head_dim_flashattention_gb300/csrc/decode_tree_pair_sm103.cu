@@ -72,13 +72,13 @@ struct Cfg {
     static constexpr int HALF_TERM = P_TERM / 2;         // one CTA's keys
     static constexpr int stage = p + P_TERMS * P_TERM;   // P of this CTA's keys for the other CTA's rows
     static constexpr int STAGE_BYTES = P_TERMS * HALF_TERM;
-    static constexpr int mask = stage + STAGE_BYTES;     // [ROWS tokens][words]
-    static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
+    static constexpr int cols = stage + STAGE_BYTES;     // [MAX_NODES][GROUPS]: the rows that see a token
+    static constexpr int depth = cols + MAX_NODES * GROUPS * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int m = red + 4 * ROWS * 4;         // [ROWS] float: references
     static constexpr int mb = m + ROWS * 4;              // [ROWS] float2: score -> log2 units, less the reference
-    static constexpr int see = mb + ROWS * 8;            // [ROWS] int4: last key, key below the window, mask row
-    static constexpr int info = see + ROWS * 16;         // [ROWS] 16 bytes: what the epilogue writes
+    static constexpr int low = mb + ROWS * 8;            // [ROWS] int: the rows' last key below the window; INT_MAX: sees nothing
+    static constexpr int info = low + ROWS * 4;        // [ROWS] 16 bytes: what the epilogue writes
     static constexpr int rows = info + ROWS * 16;        // [4 tiles][16 boxes] int: the producer's pool rows
     static constexpr int seen = rows + 4 * 16 * 4;       // [GROUPS][HALF_TILE] bytes
     static constexpr int pseen = seen + GROUPS * HALF_TILE;          // [2][HALF_TILE] int: the other CTA's keys
@@ -542,11 +542,11 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         const int peer = rank ^ 1;
         const bool speaker = (sw & 3) == 0;                  // the group's warp that talks to the other CTA
         int* s_depth = reinterpret_cast<int*>(smem + C::depth);
-        uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
+        uint32_t* s_cols = reinterpret_cast<uint32_t*>(smem + C::cols);
         float* s_red = reinterpret_cast<float*>(smem + C::red);
         float* s_m = reinterpret_cast<float*>(smem + C::m);
         float2* s_mb = reinterpret_cast<float2*>(smem + C::mb);
-        int4* s_see = reinterpret_cast<int4*>(smem + C::see);
+        int* s_low = reinterpret_cast<int*>(smem + C::low);
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
         int g = 0;                                           // running tile number
@@ -575,11 +575,25 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             const Band& bd = walk.band;
             const int n = walk.n, b = walk.b;
             const int row0 = walk.grp * ROWS;
-            const int tok0 = row0 / G;
             bar_sync(ALL, SW * 32);                          // nobody uses the last segment's tables any more
             if (n > 0) {
-                const int toks = max(0, min((row0 + ROWS - 1) / G, p.q_len - 1) - tok0 + 1);
-                if (p.tree_mask) load_masks(p, b, bd.cnt, tok0, toks, s_depth, s_mask, tid - 64, SW * 32);
+                if (p.tree_mask) {
+                    load_depths(p, b, bd.cnt, s_depth, tid - 64, SW * 32);
+                    // a warp per (word, group): lane i brings row i's word, ballots turn it over
+#pragma unroll 1
+                    for (int u = sw; u < W * GROUPS && 32 * (u / GROUPS) < bd.cnt; u += SW) {
+                        const int w = u / GROUPS, gr = u % GROUPS;
+                        const int t = (row0 + gr * GW + lane) / G;
+                        const uint32_t word = t < bd.cnt && bd.start + t >= 0 ? mask_word(p, b, bd.cnt, t, w) : 0u;
+                        uint32_t mine = 0u;
+#pragma unroll 4
+                        for (int i = 0; i < 32; ++i) {
+                            const uint32_t col = __ballot_sync(0xffffffffu, (word >> i) & 1u);
+                            mine = lane == i ? col : mine;
+                        }
+                        s_cols[(32 * w + lane) * GROUPS + gr] = mine;
+                    }
+                }
                 // Q: this CTA's 64 rows as K-major B operand (FP8: the scales of all 128), zeros where there is no row
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -645,13 +659,10 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             }
             bar_sync(ALL, SW * 32);                          // the depths are there
             if (sw < ROWS / 32) {
-                // row r sees key k iff k <= x and (k > y or k is a sink), and
-                // its mask (from word z on) allows; x = INT_MIN: nothing
                 const int r = sw * 32 + lane, t = (row0 + r) / G;
                 const bool real = t < bd.cnt && bd.start + t >= 0;
                 const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
-                s_see[r] = make_int4(!real ? INT_MIN : p.tree_mask ? bd.len : place,
-                                     p.window > 0 ? place - p.window : INT_MIN, real ? (t - tok0) * W : 0, 0);
+                s_low[r] = !real ? INT_MAX : p.window > 0 ? place - p.window : INT_MIN;
                 s_m[r] = -INFINITY;
                 if (!FP8) s_mb[r] = make_float2(p.scale_log2, 0.f);
             }
@@ -729,20 +740,27 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 uint32_t vis = 0xffffffffu;                  // bit i: row col0 + i sees this thread's key
                 if (!whole) {
                     const int c = key - bd.start;
-                    const bool drafted = c >= 0 && p.tree_mask;
-                    // the key's place; its own mask says whether a drafted one is seen
-                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
-                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
-                    const bool sink = kp < bd.sink_end;
-                    const bool bits = drafted && key < bd.hi;
-                    const uint32_t* words = s_mask + (bits ? c >> 5 : 0);
-                    vis = 0u;
-#pragma unroll 4
-                    for (int i = 0; i < GW; ++i) {
-                        const int4 r = s_see[col0 + i];
-                        bool see = last <= r.x && (kp > r.y || sink);
-                        if (bits) see = see && ((words[r.z] >> (c & 31)) & 1u);
-                        vis |= see ? 1u << i : 0u;
+                    if (key >= bd.hi) {
+                        vis = 0u;
+                    } else if (!p.tree_mask) {
+                        // token t sees the key iff c <= t and (t < c + window or the key is a sink):
+                        // the rows [t0 G, t1 G) of the item, here [t0 G - r0, t1 G - r0) of the group
+                        const int r0 = row0 + col0;
+                        const int t0 = max(c, 0);
+                        const bool ends = p.window > 0 && key >= bd.sink_end && c < bd.cnt - p.window;
+                        const int t1 = ends ? max(0, c + p.window) : bd.cnt;
+                        const int a = max(0, t0 * G - r0), z = min(GW, t1 * G - r0);
+                        vis = a >= z ? 0u : (0xffffffffu >> (GW - z)) & (0xffffffffu << a);
+                    } else {
+                        // the key's place; a drafted key's rows by their masks
+                        const int kp = c >= 0 ? bd.start + s_depth[c] : key;
+                        vis = c >= 0 ? s_cols[c * GROUPS + grp] : 0xffffffffu;
+                        if (p.window > 0 && kp >= bd.sink_end) {
+                            uint32_t in = 0u;
+#pragma unroll 8
+                            for (int i = 0; i < GW; ++i) in |= kp > s_low[col0 + i] ? 1u << i : 0u;
+                            vis &= in;
+                        }
                     }
                 }
                 // Scores of 16 of the group's rows, log2 units less the rows'
@@ -925,7 +943,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             if (speaker) {
                 const float top = s_m[cl];
                 const int r = row0 + cl, t = r / G;
-                const bool some = s_see[cl].x != INT_MIN && top != -INFINITY;
+                const bool some = s_low[cl] != INT_MAX && top != -INFINITY;
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
                 const size_t at = direct ? row : row * static_cast<size_t>(p.num_splits) + walk.index;
                 const float unit = p.o_scale * (1.f / C::P_SCALE);

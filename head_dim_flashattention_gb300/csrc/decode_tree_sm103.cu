@@ -72,12 +72,12 @@ struct Cfg {
     // shared memory, from a 1 KiB aligned base
     static constexpr int p = 0;
     static constexpr int q = p + ((P_TERMS * P_TERM + 1023) & ~1023);
-    static constexpr int mask = q + Q_TERMS * Q_TERM;    // [ROWS tokens][words]
-    static constexpr int depth = mask + ROWS * (MAX_NODES / 32) * 4;
+    static constexpr int cols = q + Q_TERMS * Q_TERM;    // [MAX_NODES][ROWS / 32]: the rows that see a token
+    static constexpr int depth = cols + MAX_NODES * (ROWS / 32) * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int mult = red + 4 * ROWS * 4;      // [ROWS] float: score -> log2 units
-    static constexpr int see = mult + ROWS * 4;          // [ROWS] int4: last key, key below the window, mask row
-    static constexpr int rows = see + ROWS * 16;         // [4 tiles][8 boxes] int: the producer's pool rows
+    static constexpr int low = mult + ROWS * 4;            // [ROWS] int: the rows' last key below the window; INT_MAX: sees nothing
+    static constexpr int rows = low + ROWS * 4;        // [4 tiles][8 boxes] int: the producer's pool rows
     static constexpr int seen = rows + 4 * 8 * 4;         // [GROUPS][TILE] bytes: some row of the group sees the key
     static constexpr int scan = seen + GROUPS * TILE;    // 32 int, then the walk's start
     static constexpr int info = scan + 32 * 4 + 16;      // [ROWS] 16 bytes: what the epilogue writes
@@ -368,10 +368,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         const int col0 = grp * GW;                           // its rows
         const int W = p.mask_words, G = p.group;
         int* s_depth = reinterpret_cast<int*>(smem + C::depth);
-        uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + C::mask);
+        uint32_t* s_cols = reinterpret_cast<uint32_t*>(smem + C::cols);
         float* s_red = reinterpret_cast<float*>(smem + C::red);
         float* s_mult = reinterpret_cast<float*>(smem + C::mult);
-        int4* s_see = reinterpret_cast<int4*>(smem + C::see);
+        int* s_low = reinterpret_cast<int*>(smem + C::low);
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
         int g = 0;                                           // running tile number
@@ -383,7 +383,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         auto prologue = [&]() {
             const Band& bd = walk.band;
             const int n = walk.n, b = walk.b;
-            constexpr int row0 = 0, tok0 = 0;                // one row group
+            constexpr int row0 = 0;                // one row group
             if (n > 0) {
                 // Q: rows as K-major B operand, zeros where there is no row
                 constexpr int PER = ROWS / SW;               // rows of a warp: 4
@@ -399,8 +399,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     x[i][1] = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
                 }
                 bar_sync(ALL, SW * 32);                      // nobody uses the last segment's tables any more
-                const int toks = min((ROWS - 1) / G, p.q_len - 1) + 1;
-                if (p.tree_mask) load_masks(p, b, bd.cnt, tok0, toks, s_depth, s_mask, tid - 64, SW * 32);
+                if (p.tree_mask) {
+                    load_depths(p, b, bd.cnt, s_depth, tid - 64, SW * 32);
+                    // a warp per (word, 32 rows): lane i brings row i's word, ballots turn it over
+#pragma unroll 1
+                    for (int u = sw; u < W * (ROWS / 32) && 32 * (u / (ROWS / 32)) < bd.cnt; u += SW) {
+                        const int w = u / (ROWS / 32), half = u % (ROWS / 32);
+                        const int t = (half * 32 + lane) / G;
+                        const uint32_t word = t < bd.cnt && bd.start + t >= 0 ? mask_word(p, b, bd.cnt, t, w) : 0u;
+                        uint32_t mine = 0u;
+#pragma unroll 4
+                        for (int i = 0; i < 32; ++i) {
+                            const uint32_t col = __ballot_sync(0xffffffffu, (word >> i) & 1u);
+                            mine = lane == i ? col : mine;
+                        }
+                        s_cols[(32 * w + lane) * (ROWS / 32) + half] = mine;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int r = sw + i * SW;
@@ -452,13 +467,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             if (n == 0) bar_sync(ALL, SW * 32);
             bar_sync(ALL, SW * 32);
             if (sw < ROWS / 32) {
-                // row r sees key k iff k <= x and (k > y or k is a sink), and
-                // its mask (from word z on) allows; x = INT_MIN: nothing
                 const int r = sw * 32 + lane, t = (row0 + r) / G;
                 const bool real = t < bd.cnt && bd.start + t >= 0;
                 const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
-                s_see[r] = make_int4(!real ? INT_MIN : p.tree_mask ? bd.len : place,
-                                     p.window > 0 ? place - p.window : INT_MIN, real ? (t - tok0) * W : 0, 0);
+                s_low[r] = !real ? INT_MAX : p.window > 0 ? place - p.window : INT_MIN;
             }
             bar_sync(ALL, SW * 32);
         };
@@ -549,26 +561,32 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 bool seen = true;                            // by some row of the group
                 if (!whole) {
                     const int c = key - bd.start;
-                    const bool drafted = c >= 0 && p.tree_mask;
-                    // the key's place; its own mask says whether a drafted one is seen
-                    const int kp = drafted ? bd.start + s_depth[max(0, min(c, bd.cnt - 1))] : key;
-                    const int last = key < bd.hi ? (drafted ? bd.start : key) : INT_MAX;
-                    const bool sink = kp < bd.sink_end;
-                    uint32_t bits = 0xffffffffu;
-                    if (drafted && key < bd.hi) {
-                        bits = 0u;
-#pragma unroll
-                        for (int i = 0; i < GW; ++i)
-                            bits |= ((s_mask[s_see[col0 + i].z + (c >> 5)] >> (c & 31)) & 1u) << i;
+                    uint32_t vis;                            // bit i: row col0 + i sees this thread's key
+                    if (key >= bd.hi) {
+                        vis = 0u;
+                    } else if (!p.tree_mask) {
+                        // token t sees the key iff c <= t and (t < c + window or the key is a sink):
+                        // the rows [t0 G, t1 G), here [t0 G - col0, t1 G - col0) of the group
+                        const int t0 = max(c, 0);
+                        const bool ends = p.window > 0 && key >= bd.sink_end && c < bd.cnt - p.window;
+                        const int t1 = ends ? max(0, c + p.window) : bd.cnt;
+                        const int a = max(0, t0 * G - col0), z = min(GW, t1 * G - col0);
+                        vis = a >= z ? 0u : (0xffffffffu >> (32 - z)) & (0xffffffffu << a);
+                    } else {
+                        // the key's place; a drafted key's rows by their masks
+                        const int kp = c >= 0 ? bd.start + s_depth[c] : key;
+                        vis = c >= 0 ? s_cols[c * (ROWS / 32) + (col0 >> 5)] >> (col0 & 31) : 0xffffffffu;
+                        if (p.window > 0 && kp >= bd.sink_end) {
+                            uint32_t in = 0u;
+#pragma unroll 8
+                            for (int i = 0; i < GW; ++i) in |= kp > s_low[col0 + i] ? 1u << i : 0u;
+                            vis &= in;
+                        }
+                        vis &= (1u << GW) - 1u;
                     }
-                    seen = false;
+                    seen = vis != 0u;
 #pragma unroll
-                    for (int i = 0; i < GW; ++i) {
-                        const int4 r = s_see[col0 + i];
-                        const bool see = last <= r.x && (kp > r.y || sink) && ((bits >> i) & 1u);
-                        x[i] = see ? x[i] : -INFINITY;
-                        seen = seen || see;
-                    }
+                    for (int i = 0; i < GW; ++i) x[i] = vis & (1u << i) ? x[i] : -INFINITY;
                 }
                 float high = x[0];
 #pragma unroll
@@ -718,7 +736,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 for (int i = 0; i < GW; ++i) top = lane == i ? m[i] : top;
                 const int cl = col0 + (lane & (GW - 1)), r = row0 + cl, t = r / G;
                 const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
-                const bool some = s_see[cl].x != INT_MIN && top != -INFINITY;
+                const bool some = s_low[cl] != INT_MAX && top != -INFINITY;
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
                 const size_t at = direct ? row : row * S + walk.index;
                 const float unit = p.o_scale * (1.f / C::P_SCALE);

@@ -265,27 +265,23 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
     }
 }
 
-// The mask words of the tokens tok0 .. tok0 + toks - 1 (bits at and behind cnt
-// name no token) and the depths of all cnt tokens, by `threads` threads.
-__device__ __forceinline__ void load_masks(const TreeParams& p, int b, int cnt, int tok0, int toks, int* s_depth,
-                                           uint32_t* s_mask, int thread, int threads) {
-    const int W = p.mask_words;
-    auto word = [&](int t, int w) -> uint32_t {
-        const int left = cnt - 32 * w;
-        const uint32_t m = static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * W + w]);
-        return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
-    };
+// Word w of token t's mask; bits at and behind cnt name no token.
+__device__ __forceinline__ uint32_t mask_word(const TreeParams& p, int b, int cnt, int t, int w) {
+    const int left = cnt - 32 * w;
+    const uint32_t m =
+        static_cast<uint32_t>(p.tree_mask[(static_cast<size_t>(b) * p.q_len + t) * p.mask_words + w]);
+    return left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
+}
+
+// The depths of all cnt tokens, by `threads` threads.
+__device__ __forceinline__ void load_depths(const TreeParams& p, int b, int cnt, int* s_depth, int thread,
+                                            int threads) {
 #pragma unroll 1
     for (int t = thread; t < cnt; t += threads) {
         int c = 0;
 #pragma unroll 1
-        for (int w = 0; w < W; ++w) c += __popc(word(t, w));
+        for (int w = 0; w < p.mask_words; ++w) c += __popc(mask_word(p, b, cnt, t, w));
         s_depth[t] = c - 1;
-    }
-#pragma unroll 1
-    for (int i = thread; i < toks * W; i += threads) {
-        const int t = tok0 + i / W, w = i % W;
-        s_mask[i] = t < cnt ? word(t, w) : 0u;
     }
 }
 
