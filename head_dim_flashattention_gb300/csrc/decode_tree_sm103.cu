@@ -889,24 +889,88 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
         p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
+// The same for many rows of at most 32 segments: a warp per row, a lane per
+// segment for the weights and per 16 columns for the sum, so that a row costs
+// no block barrier and an SM has dozens of rows in flight.
+constexpr int MERGE_ROWS = 8;                       // warps, rows, of a block
+__global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeParams p, int group_rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const size_t row = static_cast<size_t>(blockIdx.x) * MERGE_ROWS + (threadIdx.x >> 5);
+    if (row >= static_cast<size_t>(p.batch) * p.q_len * p.n_q_heads) return;
+    const int h = static_cast<int>(row % p.n_q_heads);
+    const size_t bt = row / p.n_q_heads;
+    const int b = static_cast<int>(bt / p.q_len), t = static_cast<int>(bt - static_cast<size_t>(b) * p.q_len);
+    const int grp = (t * p.group + h % p.group) / group_rows;
+    const int S = p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group];
+    if (S <= 1) return;
+    const float4* ob = reinterpret_cast<const float4*>(p.ws_o + row * p.num_splits * D) + lane;
+    constexpr int Q = D / 128, AHEAD = 2;           // column quads of a lane; segments loaded at once
+    float4 x[AHEAD][Q];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (s0 + a < S)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) x[a][q] = ob[(s0 + a) * (D / 4) + 32 * q];
+    };
+    load(0);
+    const float2 ml = lane < S ? reinterpret_cast<const float2*>(p.ws_ml)[row * p.num_splits + lane]
+                               : make_float2(-INFINITY, 0.f);
+    float M = ml.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float w = M == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    float L = w * ml.y;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 acc[Q] = {};
+    for (int s0 = 0;;) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const float ws = __shfl_sync(0xffffffffu, w, (s0 + a) & 31);
+            if (s0 + a < S)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    acc[q].x = fmaf(ws, x[a][q].x, acc[q].x);
+                    acc[q].y = fmaf(ws, x[a][q].y, acc[q].y);
+                    acc[q].z = fmaf(ws, x[a][q].z, acc[q].z);
+                    acc[q].w = fmaf(ws, x[a][q].w, acc[q].w);
+                }
+        }
+        if ((s0 += AHEAD) >= S) break;
+        load(s0);
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    uint2* out = reinterpret_cast<uint2*>(p.out + row * D) + lane;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        out[32 * q] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
+    if (p.lse && lane == 0) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
 }  // namespace tree
 
 // The merge may be scheduled while the tiles are walked (it waits for them).
 cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t stream) {
     using namespace tree;
-    const bool sliced = decode_merge_sliced(static_cast<long long>(p.n_q_heads) * p.batch * p.q_len);
+    const long long rows = static_cast<long long>(p.n_q_heads) * p.batch * p.q_len;
+    const bool sliced = decode_merge_sliced(rows);
+    const bool by_warp = !sliced && p.num_splits <= 32;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
-    cfg.blockDim = dim3(MERGE_THREADS);
+    cfg.gridDim = by_warp ? dim3(static_cast<unsigned>((rows + MERGE_ROWS - 1) / MERGE_ROWS))
+                          : dim3(p.n_q_heads, p.batch * p.q_len, sliced ? 4 : 1);
+    cfg.blockDim = dim3(by_warp ? MERGE_ROWS * 32 : MERGE_THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, group_rows)
-                  : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, group_rows);
+    return by_warp ? cudaLaunchKernelEx(&cfg, merge_rows_kernel, p, group_rows)
+           : sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, group_rows)
+                    : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, group_rows);
 }
 
 int tree_max_nodes() { return tree::MAX_NODES; }
