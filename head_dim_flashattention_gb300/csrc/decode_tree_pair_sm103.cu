@@ -457,6 +457,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         }
     } else if (warp == CLEANER) {
         // --------------------------------------- V rows of keys that no row sees
+        const int box_rows = min(p.page_size, HALF_TILE);
         int* s_pseen = reinterpret_cast<int*>(smem + C::pseen);
         const uint8_t* s_seen = smem + C::seen;
         int slot = 0, masked = 0;
@@ -477,7 +478,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     slot = (slot + C::SLOTS) % NS;
                     continue;
                 }
-                // bits k + 4 h: this lane's key lane + 32 k of key half h is seen
+                // bits k + 4 h: this lane's key lane + 32 k of key half h is seen,
+                // or lies in a box that no row needs and was filled with zeros
                 uint32_t seen = 0u;
                 if (p.tree_mask) {
                     // this CTA's keys: over the column groups; then both CTAs swap
@@ -500,12 +502,13 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     for (int k = 0; k < 4; ++k)
                         seen |= *const_cast<volatile int*>(&s_pseen[par * HALF_TILE + lane + 32 * k]) ? 1u << (k + 4 * peer) : 0u;
                     ++masked;
-                } else {
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int key = key0 + lane + 32 * k;
-                        seen |= key < bd.hi && (key >= bd.lo || key < bd.sink_end) ? 1u << k : 0u;
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    const int key = key0 + lane + 32 * k, pos = key & ~(box_rows - 1);
+                    const bool loaded = pos < bd.hi && (pos + box_rows > bd.lo || pos < bd.sink_end);
+                    const bool some = !p.tree_mask && key < bd.hi && (key >= bd.lo || key < bd.sink_end);
+                    seen |= some || !loaded ? 1u << k : 0u;
                 }
 #pragma unroll 1
                 for (int c = 0; c < C::SLOTS && ok; ++c) {
@@ -520,7 +523,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             if (!((here >> k) & 1u)) {
                                 uint4* v = reinterpret_cast<uint4*>(smem + C::ring + slot * SLOT + side * SIDE + (lane + 32 * k) * 128);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
+                                for (int e = 0; e < 8; ++e) v[(e + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);   // no bank twice
                             }
                     }
                     fence_proxy_async_smem();

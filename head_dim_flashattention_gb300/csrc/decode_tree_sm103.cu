@@ -709,7 +709,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                         if (got && !seen) {
                             uint4* v = reinterpret_cast<uint4*>(smem + C::ring + s * SLOT + kk * 128);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = v[SIDE / 16 + e] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < 8; ++e)                // no bank twice
+                                v[(e + lane) & 7] = v[SIDE / 16 + ((e + lane) & 7)] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                 }
