@@ -553,7 +553,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
         int g = 0;                                           // running tile number
-        int sbuf = 0, swaps = 0;                             // S^T buffer; column swaps so far
+        int sbuf = 0, swaps = 0, votes = 0;                  // S^T buffer; column swaps and votes so far
         uint32_t suse = 0;
 
         // Swaps a value per column (lane) with the same group of the other
@@ -785,27 +785,30 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         for (int i = 0; i < 16; ++i) x[i] = v & (1u << i) ? x[i] : -INFINITY;
                     }
                 };
-                float high = -INFINITY;
+                // ---- the vote, with the other CTA's keys; a segment's first tile
+                // sets the references in any case
+                bool over = true;
+                if (t > 0) {
+                    float high = -INFINITY;
 #pragma unroll 1
-                for (int c0 = 0; c0 < GW; c0 += 16) {
-                    float x[16];
-                    scores(c0, x);
+                    for (int c0 = 0; c0 < GW; c0 += 16) {
+                        float x[16];
+                        scores(c0, x);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
-                }
-                // ---- the vote, with the other CTA's keys
-                bool over = bar_or(bar, 128, high > C::THR || fresh || !ok);
-                {
-                    const int par = g & 1;
+                        for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
+                    }
+                    over = bar_or(bar, 128, high > C::THR || fresh || !ok);
+                    const int par = votes & 1;
                     uint64_t* vb = &bars[C::VOTE + par * GROUPS + grp];
                     int* sv = reinterpret_cast<int*>(smem + C::vote) + par * GROUPS + grp;
                     if (speaker && lane == 0) {
                         mbar_arrive_expect_tx(vb, 4);
                         st_async_b32(map_to_cta(smem_u32(sv), peer), over ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
                     }
-                    const bool got = wait_cluster(vb, (g >> 1) & 1, p.err, abort);
+                    const bool got = wait_cluster(vb, (votes >> 1) & 1, p.err, abort);
                     ok = __all_sync(0xffffffffu, got) && ok;
                     over = over || !ok || *reinterpret_cast<volatile int*>(sv) != 0;
+                    ++votes;
                 }
                 bool pv_waited = g == 0;
                 if (over) {
