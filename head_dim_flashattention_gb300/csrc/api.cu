@@ -1153,6 +1153,9 @@ fa512_status fa512_cache_fork(void* k_pages, void* v_pages, const int32_t* page_
         for (auto& i : in)
             if (overlap(o.p, o.n, i.p, i.n) && !(o.p == new_page_refs && i.p == page_refs && o.p == i.p))
                 return fail(FA512_ERR_INVALID_ARG, "an output overlaps an input");
+    if (overlap(outs[0].p, outs[0].n, outs[1].p, outs[1].n) || overlap(outs[0].p, outs[0].n, outs[2].p, outs[2].n) ||
+        overlap(outs[1].p, outs[1].n, outs[2].p, outs[2].n))
+        return fail(FA512_ERR_INVALID_ARG, "two outputs overlap");
     unsigned* err = nullptr;
     cudaError_t e = device_error_ptr(&err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word");

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
     for (int r = 0; r < APPEND_RUN; ++r) {
         const unsigned idx = (blockIdx.x * APPEND_RUN + r) * APPEND_THREADS + threadIdx.x;
         const int t = static_cast<int>(idx / static_cast<unsigned>(units));
-        const int u = static_cast<int>(idx) - t * units;
+        const int u = static_cast<int>(idx % static_cast<unsigned>(units));
         const long long pos = static_cast<long long>(len) - n_new + t;
         there[r] = t < n_new;
         if (there[r] && (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size)) {

@@ -665,7 +665,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const int r = sw * 32 + lane, t = (row0 + r) / G;
                 const bool real = t < bd.cnt && bd.start + t >= 0;
                 const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
-                s_low[r] = !real ? INT_MAX : p.window > 0 ? place - p.window : INT_MIN;
+                s_low[r] = !real ? INT_MAX : p.window > 0 && place >= INT_MIN + p.window ? place - p.window : INT_MIN;
                 s_m[r] = -INFINITY;
                 if (!FP8) s_mb[r] = make_float2(p.scale_log2, 0.f);
             }
@@ -971,9 +971,24 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             done = n;
         }
     }
-    // all threads of both CTAs: no copy or arrival may reach a CTA that has gone
+    // all threads of both CTAs: no copy or arrival may reach a CTA that has
+    // gone.  After a timeout in either CTA a courier's copy may still be on its
+    // way with nobody to wait for it: then both stay until P's barrier has
+    // counted it, or a millisecond.
     tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0 && *abort)
+        st_cluster_u32(map_to_cta(smem_u32(smem + C::misc + 4), rank ^ 1), 1u);
+    __syncwarp();
     cluster_sync_all();
+    if (*abort) {
+        if (tid == 0) {
+            (void)mbar_wait(&bars[C::P_FULL], 0, p.err, 1000000ull);
+            (void)mbar_wait(&bars[C::P_FULL], 1, p.err, 1000000ull);
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 

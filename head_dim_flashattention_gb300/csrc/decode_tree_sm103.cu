@@ -470,7 +470,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 const int r = sw * 32 + lane, t = (row0 + r) / G;
                 const bool real = t < bd.cnt && bd.start + t >= 0;
                 const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
-                s_low[r] = !real ? INT_MAX : p.window > 0 ? place - p.window : INT_MIN;
+                s_low[r] = !real ? INT_MAX : p.window > 0 && place >= INT_MIN + p.window ? place - p.window : INT_MIN;
             }
             bar_sync(ALL, SW * 32);
         };

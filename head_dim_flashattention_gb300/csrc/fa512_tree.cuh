@@ -135,7 +135,9 @@ __device__ __noinline__ BandOf<TILE> band_of(const TreeParams& p, int b, int grp
     d.sink_end = 0;
     d.place_max = d.start + (p.tree_mask ? d.cnt - 1 : last);
     if (p.window > 0 && d.hi > 0) {
-        d.lo = max(0, p.tree_mask ? d.start - p.window : d.start + first - p.window + 1);
+        // (start may be below 0: less the window it could leave int32)
+        const int from = p.tree_mask ? d.start : d.start + first + 1;
+        d.lo = from > p.window ? from - p.window : 0;
         d.sink_end = min(p.n_sinks, d.hi);
     }
     d.lo_tile = d.lo / TILE;

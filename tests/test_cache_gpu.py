@@ -385,3 +385,51 @@ def test_the_page_calls_can_be_captured(fa):
             assert np.array_equal(got.cpu().numpy(), want)
         assert np.array_equal(bits(kc), wk)
     assert fa.fa512_device_status() == 0
+
+
+@FP8
+def test_rows_far_into_a_large_pool(fa, fp8):
+    """Append, compact and fork past 32 bits of elements give what they give in a small pool."""
+    psz, hk, n = 64, 4, 24
+    far = 34000 if fp8 else 17000
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    append = fa.fa512_cache_append_fp8 if fp8 else fa.fa512_cache_append
+    kw = {"k_scale": 0.03, "v_scale": 0.5} if fp8 else {}
+    pt, refs = tables([300, 170], psz, 8, n, 110, -1)
+    rows = [workloads.randn_bf16((2, 300, hk, D), 520 + i).cuda() for i in range(2)]
+    acc = torch.tensor([[0, 3, 4, 9], [2, 5, 6, 7]], dtype=torch.int32).cuda()
+    tails = []
+    for first in (0, far):
+        k, v = (torch.empty((1, first + n, psz, hk, D), dtype=dt, device="cuda") for _ in range(2))
+        k[:, first:].zero_()
+        v[:, first:].zero_()
+        table = torch.where(pt >= 0, pt + first, pt).cuda()
+        counts = torch.cat([torch.ones(first, dtype=torch.int32), refs]).cuda()
+        lens = i32([300, 170]).cuda()
+        append(rows[0], rows[1], k[0], v[0], table, lens, q_lens=lens, **kw)
+        lens = fa.fa512_cache_compact(k, v, table, lens, acc, i32([4, 3]).cuda(), q_len=10)
+        table, lens, counts = fa.fa512_cache_fork(k, v, table, lens, i32([0, 1, 0, 0]).cuda(), counts)
+        table = table.cpu()
+        tails.append((bits(k[:, first:]), bits(v[:, first:]), torch.where(table >= 0, table - first, table), lens.cpu(),
+                      counts[first:].cpu()))
+        del k, v
+    for a, b in zip(*tails):
+        assert np.array_equal(np.asarray(a), np.asarray(b))
+    assert np.any(tails[0][0] != 0) and fa.fa512_device_status() == 0
+
+
+def test_the_last_page_and_a_full_pool_on_two_streams(fa):
+    """Resizes of two caches at once; one takes its pool's last free page, the other one more than there is."""
+    psz, pool = 16, 40
+    jobs = []
+    for new in ([320, 320], [320, 336]):
+        table = torch.full((2, 30), -1, dtype=torch.int32, device="cuda")
+        jobs.append((table, i32([0, 0]).cuda(), i32(new).cuda(), torch.zeros(pool, dtype=torch.int32, device="cuda"),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [fa.fa512_cache_resize(t, z, n, r, page_size=psz, stream=st) for t, z, n, r, st in jobs]
+    torch.cuda.synchronize()
+    assert fa.fa512_device_status() == 7 and fa.fa512_device_status() == 0
+    for t, r in outs:
+        t = t.cpu().numpy()
+        assert sorted(t[t >= 0]) == list(range(pool)) and np.all(r.cpu().numpy() == 1)

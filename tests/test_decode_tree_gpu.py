@@ -330,3 +330,112 @@ def test_bad_pages_and_lengths_are_reported_not_read(fa, fp8):
     call(fa, pc, q, None, s, q_lens=torch.tensor([-1, 5], dtype=torch.int32))
     assert fa.fa512_device_status() == 6
     check(fa, pc, q, None, s)
+
+
+@FP8
+@pytest.mark.parametrize("window,n_sinks", [(1, 1), (5, 4), (200, 128), (200, 300), (700, 0), (5000, 4)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_windows_and_sinks_of_many_rows(fa, window, n_sinks, tree, fp8):
+    """Several row groups of one KV head; slots that no row sees hold NaN."""
+    lens = [75, 333, 1200, 2049]
+    pc, q, s = make(lens, 75, 8, 2, 32, 91, fp8)
+    mask = random_masks(4, 75, 91) if tree else None
+    poison_unseen(pc, mask, [75] * 4, window, n_sinks)
+    check(fa, pc, q, mask, s, window=window, n_sinks=n_sinks)
+    check(fa, pc, q, mask, s, window=window, n_sinks=n_sinks, num_splits=1)
+
+
+@FP8
+@pytest.mark.parametrize("hq", [4, 8, 16])
+@pytest.mark.parametrize("window", [0, 3, 2 ** 31 - 1])
+def test_trees_longer_than_the_cache(fa, window, hq, fp8):
+    """Tokens whose position would be negative are not there; 32, 64 or 128 rows of a KV head."""
+    lens, cnts = [20, 3, 0, 21, 90], [32, 30, 32, 21, 0]
+    pc, q, s = make(lens, 32, hq, 4, 16, 92, fp8)
+    ql = torch.tensor(cnts, dtype=torch.int32)
+    mask = random_masks(5, 32, 92)
+    mask[3, 5] = 0
+    check(fa, pc, q, mask, s, window=window, q_lens=ql)
+    check(fa, pc, q, mask, s, window=window, n_sinks=2, q_lens=ql)
+    check(fa, pc, q, None, s, window=window, n_sinks=2, q_lens=ql)
+
+
+@FP8
+@pytest.mark.parametrize("nodes", [1, 20, 70])
+@pytest.mark.parametrize("splits", [2, 32, 33, 60])
+def test_each_way_of_merging(fa, splits, nodes, fp8):
+    """Few rows or many, few segments or many; one sequence has none."""
+    pc, q, s = make([9000, 0], nodes, 4, 2, 64, 93, fp8)
+    pc.kv_lens[1] = 0
+    check(fa, pc, q, None, s, num_splits=splits, q_lens=torch.tensor([nodes, 0], dtype=torch.int32))
+
+
+@FP8
+def test_sequences_may_share_pages(fa, fp8):
+    """Two sequences over the same pages, a third with one page at several places."""
+    pc, q, s = make([300, 300, 256], 40, 8, 4, 64, 94, fp8)
+    pc.page_table[1] = pc.page_table[0]
+    pc.page_table[2, 1:4] = pc.page_table[2, 0]
+    q[1] = q[0]
+    o, l = check(fa, pc, q, None, s)
+    assert np.array_equal(o[0], o[1]) and np.array_equal(l[0], l[1])
+
+
+@FP8
+def test_pages_far_into_a_large_pool(fa, fp8):
+    """Byte and element offsets past 32 bits: the same bits as over a small pool."""
+    far, n, psz, hk = (34000 if fp8 else 17000), 25, 64, 4
+    pc, q, s = make([700, 333], 33, 8, hk, psz, 95, fp8, poison=False)
+    used = pc.k_pages.shape[0]
+    assert used <= n and far * psz * hk * D > 2 ** 32 // (1 if fp8 else 2)
+    big = [torch.empty((far + n,) + tuple(pc.k_pages.shape[1:]), dtype=pc.k_pages.dtype, device="cuda") for _ in range(2)]
+    big[0][far:far + used].copy_(pc.k_pages)
+    big[1][far:far + used].copy_(pc.v_pages)
+    want = call(fa, pc, q, None, s)
+    f = fa.fa512_decode_paged_tree_fp8 if fp8 else fa.fa512_decode_paged_tree
+    o, l = f(q.cuda(), *big, (pc.page_table + far).cuda(), pc.kv_lens.cuda(), max_kv_len=pc.max_kv_len, **s)
+    assert np.array_equal(o.float().cpu().numpy().astype(np.float64), want[0])
+    assert np.array_equal(l.cpu().numpy().astype(np.float64), want[1])
+    assert fa.fa512_device_status() == 0
+
+
+def test_two_streams_at_once(fa):
+    """Calls on two streams, of different shapes and each with its own workspace, give what they give alone."""
+    jobs = []
+    for nodes, seed in ((40, 96), (7, 97)):
+        pc, q, _ = make([3000, 1500, 77], nodes, 8, 4, 64, seed)
+        args = [t.cuda() for t in (q, pc.k_pages, pc.v_pages, pc.page_table, pc.kv_lens)]
+        ws = torch.empty(fa.fa512_decode_workspace_bytes_tree(3, nodes, 8, 4, 3000), dtype=torch.uint8, device="cuda")
+        want = [t.clone() for t in fa.fa512_decode_paged_tree(*args, max_kv_len=3000, workspace=ws)]
+        jobs.append((args, ws, want, torch.cuda.Stream(), [torch.empty_like(t) for t in want]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, ws, _, st, got in jobs:
+            fa.fa512_decode_paged_tree(*args, None, *got, max_kv_len=3000, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for _, _, want, _, got in jobs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_graphs_share_a_workspace(fa):
+    """Captured calls of different shapes over one workspace, replayed by turns on one stream."""
+    ws = torch.empty(max(fa.fa512_decode_workspace_bytes_tree(2, n, 8, 4, 2000) for n in (33, 6)), dtype=torch.uint8,
+                     device="cuda")
+    graphs = []
+    for nodes in (33, 6):
+        pc, q, _ = make([2000, 900], nodes, 8, 4, 64, 98 + nodes)
+        args = [t.cuda() for t in (q, pc.k_pages, pc.v_pages, pc.page_table, pc.kv_lens)]
+        want = fa.fa512_decode_paged_tree(*args, max_kv_len=2000)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = fa.fa512_decode_paged_tree(*args, max_kv_len=2000, workspace=ws)
+        graphs.append((g, got, want, args))
+    for _ in range(3):
+        for _, got, _, _ in graphs:
+            got[0].fill_(9)
+        for g, _, _, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, got, want, _ in graphs:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -234,3 +234,8 @@ def test_bindings_refuse_before_the_library():
         with pytest.raises(fa.Fa512Error):
             f()
             pytest.fail("call %d was not refused" % i)
+
+
+def test_fork_refuses_outputs_that_overlap(lib):
+    for kw in (dict(nkl=(5 << 20) + 44), dict(npt=(7 << 20) + 36), dict(nrefs=(6 << 20) + 8)):
+        assert _fork(lib, **kw) == 1, kw
