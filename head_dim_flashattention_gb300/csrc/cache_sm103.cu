@@ -12,6 +12,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
+#include <mutex>
+
 #include "fa512_device.cuh"
 #include "fa512_internal.h"
 #include "fa512_pair.cuh"
@@ -26,9 +29,11 @@ constexpr int D = 512;
 // A thread moves 16 stored bytes (8 bf16 elements, or 16 elements rounded to
 // E4M3) of the key row and of the value row of up to APPEND_RUN places of its
 // sequence (blockIdx.y), all its loads before the first store.
-// Bound: bytes.  The division by a scale that is no power of two costs about
-// as many issue slots as the bytes take; a power of two (whose reciprocal is
-// exact) multiplies, which gives the same quotients.
+// Bound: bytes (8 sequences of up to 4,096 new tokens, 4 heads, into E4M3: 394
+// MB in 58.9 us, 6.7 TB/s); one token of 16 sequences takes 2.4 us, the chain
+// of three dependent loads.  The division by a scale that is no power of two
+// costs more issue slots than the bytes take (83.0 us); a power of two (whose
+// reciprocal is exact) multiplies, which gives the same quotients.
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_RUN = 2;
 
@@ -120,6 +125,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // row (accepted[i'] >= i' > i), and it can only hit a source of an earlier
 // row, which this thread has read already; so loading a batch of sources
 // ahead and storing afterwards is safe, and no two threads touch one byte.
+// Bound: bytes, in rows of 1 KiB a head (64 sequences, 8 layers, ragged trees of
+// 64: 21.4 us); small calls the loads in a row (16 sequences, one layer: 3.2 us).
 constexpr int COMPACT_THREADS = 256;
 constexpr int COMPACT_BATCH = 8;        // rows in flight per thread
 constexpr int COMPACT_MAX = 1024;
@@ -196,11 +203,13 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const CompactP
 // Bound: chains of dependent loads, not bytes (2.3 MB for 512 sequences of
 // 448 pages and a pool of 178,000 pages), so every pass keeps 8 loads a
 // thread in flight and nothing is looked up twice: lengths, parents and needs
-// stay in shared memory.
+// stay in shared memory.  Those 512 sequences take 18.2 us with 16 blocks (27.5
+// with 8, 109 with one); 16 sequences 6.9 us, of which the launch of a cluster and
+// its barriers are most.
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_MAX_BATCH = 8192;
-constexpr int PLAN_CLUSTER = 8;          // blocks, at most
+constexpr int PLAN_CLUSTER = 16;         // blocks, at most (8 where a cluster of 16 does not fit)
 constexpr int PLAN_RUN = 8;              // loads in flight per thread
 constexpr int PLAN_CHUNK = PLAN_THREADS; // words (of 32 pages) of the bit map
 
@@ -533,19 +542,57 @@ cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream) {
 
 int page_plan_max_batch() { return cache::PLAN_MAX_BATCH; }
 
+// Most blocks of the plan's cluster on the current device, asked once per
+// device (0: a query failed); it also opts the kernels into their shared
+// memory and into clusters above the portable 8 there.
+static int plan_blocks() {
+    using namespace cache;
+    static std::mutex mu;
+    static int known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev] != 0) return known[dev];
+    const int smem = static_cast<int>(plan_smem_bytes(PLAN_MAX_BATCH, PLAN_MAX_BATCH, true));
+    int fits = PLAN_CLUSTER;
+    for (auto kernel : {page_plan_kernel<true>, page_plan_kernel<false>}) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(PLAN_CLUSTER);
+        cfg.blockDim = dim3(PLAN_THREADS);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = PLAN_CLUSTER;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            fits = 8;
+        }
+    }
+    return known[dev] = fits;
+}
+
 cudaError_t launch_page_plan(const PagePlanParams& p, bool fork, cudaStream_t stream) {
     using namespace cache;
     auto kernel = fork ? page_plan_kernel<true> : page_plan_kernel<false>;
     const size_t smem = plan_smem_bytes(p.n_new, p.batch, fork);
+    const int most = plan_blocks();
+    if (most < 1) return cudaErrorLaunchOutOfResources;
     cudaError_t e;
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(plan_smem_bytes(PLAN_MAX_BATCH, PLAN_MAX_BATCH, true)));
-        if (e != cudaSuccess) return e;
-    }
-    // a block for every 4,096 table entries and counts (4 per thread)
+    // a block for every 4,096 table entries and counts (4 per thread): 4 sequences
+    // fork in 9.1 us with the blocks they need, in 9.4 with 8
     const long long work = static_cast<long long>(p.n_new + (fork ? p.batch : 0)) * p.max_pages_per_seq + p.num_pages;
-    const int blocks = static_cast<int>(work >= PLAN_CLUSTER * 4096LL ? PLAN_CLUSTER : work / 4096 + 1);
+    const int blocks = static_cast<int>(work >= most * 4096LL ? most : work / 4096 + 1);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(blocks);

@@ -9,6 +9,16 @@
 // where the single-CTA form reads 48 cycles for half the rows.
 // Tensor memory: O^T 2 x 128 columns, S^T 2 buffers x 128 columns.
 //
+// Bound: the bytes of a cache that is read once (16 caches of 20,000 to 28,672
+// positions, 128 rows: 514 us, 5.7 TB/s, 84 % of the measured copy rate,
+// what 96 KiB in flight an SM bring); the L2 and the changes of item where
+// several row groups share the keys (8 sequences, 600 rows a KV head,
+// window 4,096 and 4 sinks: 261 us, 0.47 PFLOP/s; a tile of 512 KiB takes
+// 4.6 us a pair, 8 TB/s over all pairs; a change of item costs a pair ~15 us of
+// row sums, next Q, O and first references).  Slots of 16 KiB instead of 32
+// made both slower (564 -> 589, 355 -> 378 us: barriers and commits a slot), as
+// did fetching the next tile into L2 ahead (567 -> 635, 354 -> 367).
+//
 // A CTA's softmax threads hold its 128 keys against all 128 rows; Q and P^T,
 // the B operands, are split by rows, 64 in each CTA, so half of each P^T tile
 // belongs in the other CTA: it is staged here, and a courier warp moves it

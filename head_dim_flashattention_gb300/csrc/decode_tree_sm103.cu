@@ -12,9 +12,16 @@
 //   as the K-major B operand, and P^T is written by the softmax threads as
 //   an MN-major B operand: a thread holds one key, so its rows' values are
 //   contiguous.
-// Per 128 keys a CTA streams 256 KiB (bf16): ~5.9 us at an SM's share of the
-// measured HBM rate, against ~0.85 us of tensor work.  Row tiles of the same
-// keys form a cluster that loads each slot once and multicasts it.
+// Bound: the cache's bytes.  Per 128 keys a CTA streams 256 KiB (bf16), ~5.9 us
+// at an SM's share of the measured 6.77 TB/s, against ~1.6 us of tensor work
+// (an M = 128, N = 64, K = 16 MMA takes 48 cycles: it reads its operands from
+// shared memory at 128 bytes a cycle).  So the ring takes all shared memory
+// that Q and P leave, in slots of 32 KiB (few barriers, one elected lane that
+// issues; slots of 8 KiB left the producer the bound: 889 -> 617 us for 64
+// rows over 16 caches of 20,000 to 28,672 positions).  Measured: 64 sequences
+// of 16,384 positions in E4M3, 32 rows: 660 us, 6.5 TB/s, 96 % of the measured
+// copy rate; 16 sequences of 8,192 positions in bf16: 184 us with 32 rows,
+// 199 us with 64.
 //
 // The row maxima lie across lanes here, so they are not reduced every tile:
 // each thread compares its scores with the reference its rows hold, and only
@@ -31,10 +38,10 @@
 // without widening a byte of the cache.
 //
 // Work: the (sequence, row group, KV head) items' tiles, one after another,
-// are cut into equal ranges, one per resident cluster, so every SM streams
-// the same number of tiles whatever the lengths; an item that spans several
-// ranges leaves (O, m, l) partials that merge_kernel combines, any other is
-// written directly.
+// are cut into equal ranges, one per SM, so every SM streams the same number
+// of tiles whatever the lengths; an item that spans several ranges leaves
+// (O, m, l) partials that a merge kernel combines, any other is written
+// directly.
 #include <cuda.h>
 
 #include "fa512_tree.cuh"
@@ -803,8 +810,9 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
 // combines the segments' (O, m, l) -- M = max m_s, w_s = 2^(m_s - M),
 // O = sum w_s O_s / sum w_s l_s.  256 threads: column quads x groups of
 // segments; every thread issues its first 16 segments' O loads before it
-// needs a weight, so the merge costs about one round trip to memory.  Few
-// rows are merged in four column slices each (CS = 4).
+// needs a weight, so the merge costs about one round trip to memory.  Rows too
+// few to give every SM a block are merged in four column slices each (CS = 4):
+// 8 rows of 131,072 positions 96.0 us instead of 99.7 with the attention.
 constexpr int MERGE_THREADS = 256;
 constexpr int MERGE_AHEAD = 16;
 constexpr int MAX_SPLITS = 1024;
@@ -892,7 +900,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
 
 // The same for many rows of at most 32 segments: a warp per row, a lane per
 // segment for the weights and per 16 columns for the sum, so that a row costs
-// no block barrier and an SM has dozens of rows in flight.
+// no block barrier and an SM has dozens of rows in flight: 19,200 rows of two
+// segments in 15 us instead of 74.  It reads its segments one pair after
+// another, so it pays from the fourth wave of blocks (two an SM) on; whole
+// calls, warps against blocks: 512 rows 73.6 / 69.1 us, 768 89.3 / 88.3, 1,024
+// 107.3 / 108.8, 2,048 92.2 / 100.5, 4,096 83.0 / 105.2.
 constexpr int MERGE_ROWS = 8;                       // warps, rows, of a block
 __global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeParams p, int group_rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -957,7 +969,7 @@ cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t 
     using namespace tree;
     const long long rows = static_cast<long long>(p.n_q_heads) * p.batch * p.q_len;
     const bool sliced = decode_merge_sliced(rows);
-    const bool by_warp = !sliced && p.num_splits <= 32;
+    const bool by_warp = rows > 3 * 2 * 152 && p.num_splits <= 32;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = by_warp ? dim3(static_cast<unsigned>((rows + MERGE_ROWS - 1) / MERGE_ROWS))
@@ -977,7 +989,11 @@ cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t 
 int tree_max_nodes() { return tree::MAX_NODES; }
 
 // One CTA with 32 or 64 rows where all rows of a KV head fit, else CTA pairs
-// with 128 rows each.
+// with 128 rows each.  32 rows in the kernel for 32 / for 64 rows: 184 / 195 us
+// (16 caches of 8,192 positions, bf16), 660 / 708 us (64 of 16,384, E4M3): the
+// operands of the products that multiply zeros cost shared-memory reads and the
+// softmax their time.  64 rows in the kernel for 64 / in a pair: 199 / 212 us
+// (the 16), 46.6 / 51.3 us (one of 16,384), 137 / 189 us (the 16 in E4M3).
 TreeShape tree_shape(int q_len, int group) {
     const long long rows = static_cast<long long>(q_len) * group;
     TreeShape s;

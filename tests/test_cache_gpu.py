@@ -433,3 +433,20 @@ def test_the_last_page_and_a_full_pool_on_two_streams(fa):
     for t, r in outs:
         t = t.cpu().numpy()
         assert sorted(t[t >= 0]) == list(range(pool)) and np.all(r.cpu().numpy() == 1)
+
+
+def test_page_plans_of_large_caches(fa):
+    """As many blocks as the plan takes: hundreds of sequences of hundreds of pages, a pool of tens of thousands."""
+    test_resize(fa, 16, 512, 3200, 3001)
+    psz, pool = 16, 70001
+    rng = np.random.RandomState(7)
+    lens = rng.randint(0, 1700, 500)
+    parents = rng.randint(0, 500, 700).astype(np.int32)
+    pt, refs = tables(list(lens), psz, 110, pool, 111, 10 ** 7)
+    none = np.zeros((0, pool, psz, 1, D), dtype=np.uint16)
+    _, _, wt, wl, wr = paged.cache_fork(none, none, pt, lens, parents, refs)
+    k = torch.empty((0, pool, psz, 1, D), dtype=torch.bfloat16, device="cuda")
+    t, n, r = fa.fa512_cache_fork(k, k, pt.cuda(), i32(list(lens)).cuda(), torch.from_numpy(parents).cuda(), refs.cuda())
+    assert fa.fa512_device_status() == 0
+    assert np.array_equal(t.cpu().numpy(), wt) and np.array_equal(n.cpu().numpy(), wl)
+    assert np.array_equal(r.cpu().numpy(), wr)
