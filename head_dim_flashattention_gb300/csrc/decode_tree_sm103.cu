@@ -101,6 +101,15 @@ struct Cfg {
     static_assert(NS >= 4, "ring slots");
 };
 
+__device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1,
+                                                 int c2, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, 8-bit floating-point operands.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -184,6 +193,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         const int oob = p.num_pages * p.page_size;           // past the pool: filled with zeros
         const int box_rows = min(p.page_size, TILE), boxes = TILE / box_rows;
         int* s_rows = reinterpret_cast<int*>(smem + C::rows);
+        const uint64_t stream = pair::l2_policy_stream();    // the cache is read once (184 -> 175 us)
         int slot = 0;
         uint32_t use = 0;                                    // use number of the slot
         bool ok = true;
@@ -202,8 +212,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     const int c0 = c * (256 / C::EB);
 #pragma unroll 1
                     for (int i = 0; i < boxes; ++i) {
-                        tma_load_3d(dst, tm, full, c0, kvh, rows[i]);
-                        tma_load_3d(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, rows[i]);
+                        tma_load_3d_hint(dst, tm, full, c0, kvh, rows[i], stream);
+                        tma_load_3d_hint(dst + SIDE, tm, full, c0 + 128 / C::EB, kvh, rows[i], stream);
                         dst += box_rows * 128;
                     }
                 }
