@@ -10,24 +10,29 @@
 // Tensor memory: O^T 2 x 128 columns, S^T 2 buffers x 128 columns.
 //
 // Bound: the bytes of a cache that is read once (16 caches of 20,000 to 28,672
-// positions, 128 rows: 514 us, 5.7 TB/s, 84 % of the measured copy rate,
-// what 96 KiB in flight an SM bring); the L2 and the changes of item where
-// several row groups share the keys (8 sequences, 600 rows a KV head,
-// window 4,096 and 4 sinks: 261 us, 0.47 PFLOP/s; a tile of 512 KiB takes
-// 4.6 us a pair, 8 TB/s over all pairs; a change of item costs a pair ~15 us of
-// row sums, next Q, O and first references).  Slots of 16 KiB instead of 32
-// made both slower (564 -> 589, 355 -> 378 us: barriers and commits a slot), as
-// did fetching the next tile into L2 ahead (567 -> 635, 354 -> 367).
+// positions, 128 rows: 478 us, 6.1 TB/s, 90 % of the measured copy rate).
+// Where several row groups share the keys, which come from L2 then, the shared
+// memory of a pair and the changes of item (8 sequences, 600 rows a KV head,
+// window 4,096 and 4 sinks: 260 us, 0.47 PFLOP/s, 25 % of the measured rate): a
+// tile takes 4.2 us where a quarter of the pairs runs, 4.6 where all do, of
+// which 2.9 us are 128 bytes a cycle for the operands of 64 MMAs and the
+// loads; a change of item costs ~15 us of row sums, next Q, O and first
+// references.  Measured and not taken: slots of 16 KiB (window and sinks
+// 355 -> 378 us: barriers and commits a slot; two slots of 32 KiB instead of
+// three cost 12 us, so depth is not what bounds it), fetching the next tile
+// into L2 ahead (354 -> 367), a second warp that loads (262 -> 264; one alone
+// issues 76 bytes a ns, a tile wants 57), S^T two tiles ahead and P held in
+// registers until P V is done (262 -> 264 each).
 //
 // A CTA's softmax threads hold its 128 keys against all 128 rows; Q and P^T,
 // the B operands, are split by rows, 64 in each CTA, so half of each P^T tile
 // belongs in the other CTA: it is staged here, and a courier warp moves it
 // with one bulk copy (a store into the other CTA would hold the softmax
-// threads at their fence and release for two microseconds a tile).  Both CTAs have to scale by
-// the same references: every tile, each column group (32 rows) swaps its vote
-// on "a score outgrew the reference" with the same group of the other CTA,
-// and, when either says so, the column maxima; at the end of a segment the row
-// sums.
+// threads at their fence and release for two microseconds a tile).  Both CTAs
+// have to scale by the same references: every tile, each column group (32
+// rows) swaps its vote on "a score outgrew the reference" with the same group
+// of the other CTA, and, when either says so, the column maxima; at the end of
+// a segment the row sums.
 //
 // Keys that no row sees may hold anything, also NaN, which P = 0 would not
 // silence: in the tiles where some may be (a sequence's end, a window's edges,

@@ -19,9 +19,11 @@
 // that Q and P leave, in slots of 32 KiB (few barriers, one elected lane that
 // issues; slots of 8 KiB left the producer the bound: 889 -> 617 us for 64
 // rows over 16 caches of 20,000 to 28,672 positions).  Measured: 64 sequences
-// of 16,384 positions in E4M3, 32 rows: 660 us, 6.5 TB/s, 96 % of the measured
-// copy rate; 16 sequences of 8,192 positions in bf16: 184 us with 32 rows,
-// 199 us with 64.
+// of 16,384 positions in E4M3, 32 rows: 629-647 us, 6.7-6.9 TB/s, 98-101 % of
+// the measured copy rate; 16 sequences of 8,192 positions in bf16: 172 us with
+// 32 rows, 183 us with 64; one of 4,096 positions with 16 rows: 19.2 us, of
+// which the stream of its 128 tiles, one an SM, is ~8: the rest is the chain of
+// launch, lengths, Q, one tile's two products and the merge.
 //
 // The row maxima lie across lanes here, so they are not reduced every tile:
 // each thread compares its scores with the reference its rows hold, and only
@@ -193,7 +195,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
         const int oob = p.num_pages * p.page_size;           // past the pool: filled with zeros
         const int box_rows = min(p.page_size, TILE), boxes = TILE / box_rows;
         int* s_rows = reinterpret_cast<int*>(smem + C::rows);
-        const uint64_t stream = pair::l2_policy_stream();    // the cache is read once (184 -> 175 us)
+        const uint64_t stream = pair::l2_policy_stream();    // the cache is read once (199 -> 187 us)
         int slot = 0;
         uint32_t use = 0;                                    // use number of the slot
         bool ok = true;
@@ -822,7 +824,7 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
 // segments; every thread issues its first 16 segments' O loads before it
 // needs a weight, so the merge costs about one round trip to memory.  Rows too
 // few to give every SM a block are merged in four column slices each (CS = 4):
-// 8 rows of 131,072 positions 96.0 us instead of 99.7 with the attention.
+// 16 rows of 131,072 positions 91 us instead of 94 with the attention.
 constexpr int MERGE_THREADS = 256;
 constexpr int MERGE_AHEAD = 16;
 constexpr int MAX_SPLITS = 1024;
@@ -838,7 +840,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
     const int h = blockIdx.x, bt = blockIdx.y;
     const int b = bt / p.q_len, t = bt - b * p.q_len;
     const int grp = (t * p.group + h % p.group) / group_rows;
-    const int S = p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group];
+    // an attention that ran into a timeout may not have left its counts
+    const int S = min(p.num_splits, p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group]);
     if (S <= 1) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = tid % QB, g = tid / QB;
@@ -910,11 +913,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
 
 // The same for many rows of at most 32 segments: a warp per row, a lane per
 // segment for the weights and per 16 columns for the sum, so that a row costs
-// no block barrier and an SM has dozens of rows in flight: 19,200 rows of two
-// segments in 15 us instead of 74.  It reads its segments one pair after
-// another, so it pays from the fourth wave of blocks (two an SM) on; whole
-// calls, warps against blocks: 512 rows 73.6 / 69.1 us, 768 89.3 / 88.3, 1,024
-// 107.3 / 108.8, 2,048 92.2 / 100.5, 4,096 83.0 / 105.2.
+// no block barrier and an SM has dozens of rows in flight.  It reads its
+// segments one pair after another, so it pays from the fourth wave of blocks
+// (two an SM) on; whole calls, warps / blocks: 512 rows 65.9 / 61.4 us, 768
+// 81.8 / 80.8, 1,024 98.2 / 100.3, 2,048 81.0 / 88.7, 4,096 83.7 / 105.7,
+// 19,200 260 / 322.
 constexpr int MERGE_ROWS = 8;                       // warps, rows, of a block
 __global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeParams p, int group_rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -925,7 +928,7 @@ __global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeP
     const size_t bt = row / p.n_q_heads;
     const int b = static_cast<int>(bt / p.q_len), t = static_cast<int>(bt - static_cast<size_t>(b) * p.q_len);
     const int grp = (t * p.group + h % p.group) / group_rows;
-    const int S = p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group];
+    const int S = min(p.num_splits, p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group]);
     if (S <= 1) return;
     const float4* ob = reinterpret_cast<const float4*>(p.ws_o + row * p.num_splits * D) + lane;
     constexpr int Q = D / 128, AHEAD = 2;           // column quads of a lane; segments loaded at once
@@ -999,11 +1002,11 @@ cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t 
 int tree_max_nodes() { return tree::MAX_NODES; }
 
 // One CTA with 32 or 64 rows where all rows of a KV head fit, else CTA pairs
-// with 128 rows each.  32 rows in the kernel for 32 / for 64 rows: 184 / 195 us
-// (16 caches of 8,192 positions, bf16), 660 / 708 us (64 of 16,384, E4M3): the
+// with 128 rows each.  32 rows in the kernel for 32 / for 64 rows: 172 / 178 us
+// (16 caches of 8,192 positions, bf16), 629 / 676 us (64 of 16,384, E4M3): the
 // operands of the products that multiply zeros cost shared-memory reads and the
-// softmax their time.  64 rows in the kernel for 64 / in a pair: 199 / 212 us
-// (the 16), 46.6 / 51.3 us (one of 16,384), 137 / 189 us (the 16 in E4M3).
+// softmax their time.  64 rows in the kernel for 64 / in a pair: 183 / 191 us
+// (the 16), 38.6 / 46.5 us (one of 16,384), 119 / 177 us (the 16 in E4M3).
 TreeShape tree_shape(int q_len, int group) {
     const long long rows = static_cast<long long>(q_len) * group;
     TreeShape s;
