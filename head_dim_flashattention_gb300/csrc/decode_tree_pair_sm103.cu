@@ -100,7 +100,7 @@ struct Cfg {
     static constexpr int vote = pseen + 2 * HALF_TILE * 4;           // [2][GROUPS] int
     static constexpr int top = vote + 2 * GROUPS * 4;                // [2][ROWS] float
     static constexpr int scan = top + 2 * ROWS * 4;
-    static constexpr int bars = scan + 160;
+    static constexpr int bars = scan + ((SCAN_INTS * 4 + 15) & ~15);
     static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, S_FULL = 4 * NS, S_FREE = S_FULL + NB,
                          P_FULL = S_FREE + NB, P_PEER = P_FULL + 1, STAGED = P_PEER + 1, PV_DONE = STAGED + 1, Q_FULL = PV_DONE + 1, O_FREE = Q_FULL + 1,
                          DRAIN = O_FREE + 1, VOTE = DRAIN + 1, TOP = VOTE + 2 * GROUPS, SEEN = TOP + 2 * GROUPS,

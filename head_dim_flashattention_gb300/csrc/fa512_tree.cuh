@@ -154,6 +154,7 @@ struct WalkOf {
     int per;
     int entry, kvh;             // current item: entry = sequence * groups + row group
     int entries, groups, group_rows;
+    int stride;                 // entries from one of the walk's to its next: 1, or groups in a team
     BandOf<TILE> band;
     // the current segment
     int b, grp, first, n;       // tiles [first, first + n) of the band
@@ -174,7 +175,7 @@ struct WalkOf {
                 base += w;
                 if (++kvh == p.n_kv_heads) {
                     kvh = 0;
-                    if (++entry == entries) return false;
+                    if ((entry += stride) >= entries) return false;
                     load(p);
                 }
                 continue;
@@ -201,7 +202,17 @@ struct WalkOf {
 
 // The range of cluster `me` of `clusters`: the total of all items' units, then
 // the item that holds the range's first unit.  Every thread of the block calls
-// it; s_scan: 36 int of shared memory.
+// it; s_scan: SCAN_INTS int of shared memory.
+//
+// The row groups of a KV head read the same keys.  One walk over all items
+// would come to them at different times, when L2 has lost them (8 sequences of
+// 600 rows a KV head, window 4,096: 1.36 GB from memory for 0.55 GB of keys), so
+// the clusters form teams of one cluster per row group: each walks its group's
+// items alone, and a team's members reach the same keys together (294 -> 262
+// us).  Where a padded batch leaves the groups unlike (the longest group's range more than a
+// tenth above everybody's equal share) all walk all items.
+constexpr int MAX_TEAM = 16;
+constexpr int SCAN_INTS = 36 + MAX_TEAM;
 template <int TILE, int THREADS>
 __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams& p, int clusters, int me, int* s_scan) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -214,16 +225,36 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
         const BandOf<TILE> d = band_of<TILE>(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
         return max(1, d.tiles) * p.n_kv_heads;
     };
+    int* s_team = s_scan + 36;                              // units of each row group
+    const int teams = walk.groups > 1 && walk.groups <= MAX_TEAM ? clusters / walk.groups : 0;
+    if (teams > 0) {
+        if (tid < MAX_TEAM) s_team[tid] = 0;
+        __syncthreads();
+    }
     int total = 0, mine0 = 0;                        // mine0: entry tid's units
     for (int e = tid; e < walk.entries; e += THREADS) {
         const int u = entry_units(e, blockIdx.x == 0);
         if (e == tid) mine0 = u;
         total += u;
+        if (teams > 0) atomicAdd(&s_team[e % walk.groups], u);
     }
     total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) s_scan[warp] = total;
     __syncthreads();
     total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
+    int start = 0;                                          // first entry of the walk's
+    walk.stride = 1;
+    if (teams > 0) {
+        const int most = __reduce_max_sync(0xffffffffu, lane < walk.groups ? s_team[lane] : 0);
+        const long long share = (total + clusters - 1) / clusters;
+        if (10LL * ((most + teams - 1) / teams) <= 11 * share) {
+            start = me % walk.groups;
+            walk.stride = walk.groups;
+            total = me / walk.groups < teams ? s_team[start] : 0;
+            clusters = teams;
+            me = min(me / walk.groups, teams);
+        }
+    }
     // ranges short enough to balance, long enough that no item has more
     // than num_splits segments
     walk.per = (total + clusters - 1) / clusters;
@@ -234,8 +265,9 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
     walk.end = min(total - walk.pos, walk.per) + walk.pos;
     int before = 0;
     if (walk.pos < walk.end) {
-        for (int e0 = 0; e0 < walk.entries; e0 += THREADS) {
-            const int u = e0 == 0 ? mine0 : entry_units(e0 + tid, false);
+        for (int e0 = start; e0 < walk.entries; e0 += THREADS * walk.stride) {
+            const int e = e0 + tid * walk.stride;
+            const int u = e == tid ? mine0 : entry_units(e, false);
             int x = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -249,7 +281,7 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
             x += before + __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
             const int sum = before + __reduce_add_sync(0xffffffffu, ws);
             if (walk.pos >= x - u && walk.pos < x) {
-                s_at[0] = e0 + tid;
+                s_at[0] = e;
                 s_at[1] = x - u;
             }
             before = sum;

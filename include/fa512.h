@@ -372,11 +372,16 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
  * tokens whose cached position would be negative, see nothing: O = 0,
  * LSE = -inf.
  *
- * A row is a (token, query head) pair; 64 rows of a KV head share one pass
- * over the keys, and the keys are split over CTAs as in fa512_decode_paged
- * (num_splits 0: fa512_decode_auto_splits_tree()).  Only pages that hold
- * positions inside the band of some row are read; slots that no row sees may
- * hold anything (NaN included) without reaching the output.
+ * A row is a (token, query head) pair.  Up to 64 rows of a KV head share one
+ * pass over its keys in one CTA; more are taken in groups of 128, each on a
+ * pair of SMs.  The keys of all sequences are cut into ranges of equal length,
+ * one per CTA or pair, so num_splits is the most segments that one row may be
+ * left in (1: no row is split; 0: fa512_decode_auto_splits_tree()).  Only
+ * pages that hold positions inside the band of some row are read; slots that
+ * no row sees may hold anything (NaN included) without reaching the output.
+ * The same inputs give the same bits every time.  out, lse and workspace must
+ * not overlap the inputs or one another; calls that may run at the same time
+ * need workspaces of their own.
  *
  * workspace must be at least fa512_decode_workspace_bytes_tree() bytes for
  * the split count used, 256-byte aligned; with one split it is not used and
@@ -412,8 +417,10 @@ fa512_status fa512_decode_paged_tree_fp8(const void *q, const void *k_pages, con
                                          int n_sinks, int num_splits, void *workspace,
                                          size_t workspace_bytes, fa512_stream_t stream);
 
-/* Split count of the tree calls when num_splits == 0.  Returns 1 when there
- * is nothing to split. */
+/* Split count of the tree calls when num_splits == 0: the segments that the
+ * longest sequence's row can be left in when the current device's SMs share
+ * the keys of max_kv_len equally, twice over for batches with shorter
+ * sequences.  Returns 1 when there is nothing to split. */
 int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
                                   int max_kv_len, int window, int n_sinks);
 

@@ -439,3 +439,14 @@ def test_two_graphs_share_a_workspace(fa):
         torch.cuda.synchronize()
         for _, got, want, _ in graphs:
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@FP8
+@pytest.mark.parametrize("cnts", [[300, 300, 300, 300], [300, 290, 295, 300], [300, 1, 0, 17], [0, 0, 0, 40]])
+def test_row_groups_of_padded_batches(fa, cnts, fp8):
+    """Alike and unlike numbers of row groups in a batch: the work is dealt out differently."""
+    pc, q, s = make([900, 300, 512, 777], 300, 8, 2, 64, 131, fp8)
+    ql = torch.tensor(cnts, dtype=torch.int32)
+    check(fa, pc, q, None, s, q_lens=ql)
+    check(fa, pc, q, None, s, q_lens=ql, window=200, n_sinks=5, num_splits=1)
+    check(fa, pc, q, None, s, q_lens=ql, window=600, num_splits=4)
