@@ -11,18 +11,19 @@
 //
 // Bound: the bytes of a cache that is read once (16 caches of 20,000 to 28,672
 // positions, 128 rows: 478 us, 6.1 TB/s, 90 % of the measured copy rate).
-// Where several row groups share the keys, which come from L2 then, the shared
-// memory of a pair and the changes of item (8 sequences, 600 rows a KV head,
-// window 4,096 and 4 sinks: 260 us, 0.47 PFLOP/s, 25 % of the measured rate): a
-// tile takes 4.2 us where a quarter of the pairs runs, 4.6 where all do, of
-// which 2.9 us are 128 bytes a cycle for the operands of 64 MMAs and the
-// loads; a change of item costs ~15 us of row sums, next Q, O and first
-// references.  Measured and not taken: slots of 16 KiB (window and sinks
-// 355 -> 378 us: barriers and commits a slot; two slots of 32 KiB instead of
-// three cost 12 us, so depth is not what bounds it), fetching the next tile
-// into L2 ahead (354 -> 367), a second warp that loads (262 -> 264; one alone
-// issues 76 bytes a ns, a tile wants 57), S^T two tiles ahead and P held in
-// registers until P V is done (262 -> 264 each).
+// Where several row groups share the keys, L2 brings them (8 sequences of up to
+// 75 tokens and 600 rows a KV head, window 4,096 and 4 sinks: 258 us, 0.47
+// PFLOP/s, 25 % of the measured rate; all of 75 tokens: 260 us, 0.63 PFLOP/s)
+// and the bound is the chain of a tile: its 64 MMAs take 2.1 us, and the MMA
+// warp waits another 2.4 for loads and 0.9 for P; a change of item costs ~15 us
+// of row sums, next Q, O and first references, two or three times a pair.
+// Measured and not taken: slots of 16 KiB (355 -> 378 us: barriers and commits
+// a slot; two slots of 32 KiB instead of three cost 12 us, so depth is not what
+// bounds it), fetching the next tile into L2 ahead (354 -> 367), S^T two tiles
+// ahead and P held in registers until P V is done (262 -> 264 each), a second
+// warp that loads, in the cleaner's place and with its work on the courier (258
+// -> 261; chunks of 300 tokens over 8,192 positions, where little is cleared,
+// 357 -> 338).
 //
 // A CTA's softmax threads hold its 128 keys against all 128 rows; Q and P^T,
 // the B operands, are split by rows, 64 in each CTA, so half of each P^T tile

@@ -206,7 +206,7 @@ struct WalkOf {
 //
 // The row groups of a KV head read the same keys.  One walk over all items
 // would come to them at different times, when L2 has lost them (8 sequences of
-// 600 rows a KV head, window 4,096: 1.36 GB from memory for 0.55 GB of keys), so
+// 600 rows a KV head, window 4,096: 1.36 GB from memory for 0.27 GB of keys), so
 // the clusters form teams of one cluster per row group: each walks its group's
 // items alone, and a team's members reach the same keys together (294 -> 262
 // us).  Where a padded batch leaves the groups unlike (the longest group's range more than a
