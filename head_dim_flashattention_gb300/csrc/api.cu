@@ -762,10 +762,10 @@ namespace {
 
 // ------------------------------------------- drafted tokens, cache management
 
-// Most key tiles that a row group of a tree call walks: every sink tile and
-// the tiles of its band (with a window: the window, the places its rows span
-// and one tile more for a band that starts inside a tile).
-long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks) {
+// Most key tiles that a row group of a tree call walks: with a window the
+// sinks, the window and the places its rows span, both rounded to boxes of
+// `box` positions.
+long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sinks, int box) {
     const fa512::TreeShape s = fa512::tree_shape(q_len, group);
     const int tile = s.tile;
     const long long all = (static_cast<long long>(max_kv_len) + tile - 1) / tile;
@@ -773,9 +773,9 @@ long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sin
     // a run's rows span their own tokens; a masked tree's all of its tokens
     const long long span = static_cast<long long>(s.rows) / group + 2;
     const long long tokens = q_len <= fa512::tree_max_nodes() || q_len < span ? q_len : span;
-    const long long band = (static_cast<long long>(window) + tokens + 1 + tile - 1) / tile + 1;
-    const long long sinks = (static_cast<long long>(n_sinks) + tile - 1) / tile;
-    return sinks + band < all ? sinks + band : all;
+    const long long sinks = (static_cast<long long>(n_sinks) + box - 1) / box * box;
+    const long long some = (sinks + window + tokens + box - 1 + tile - 1) / tile;
+    return some < all ? some : all;
 }
 
 // Partials of `rows` rows in `splits` segments, and the items' segment counts.
@@ -876,7 +876,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
     p.rows = shape.rows;
     p.row_groups = shape.groups;
-    p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks));
+    p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks, page_size < 128 ? page_size : 128));
     p.min_range = splits > 1 ? (p.max_tiles + splits - 2) / (splits - 1) : 0;
     if (static_cast<long long>(batch) * shape.groups * n_kv_heads * (p.max_tiles > 1 ? p.max_tiles : 1) > 0x7fffffffLL)
         return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
@@ -999,7 +999,7 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
     if (static_cast<long long>(batch) * q_len > 65535) return 1;   // the merge's grid
     const int G = n_q_heads / n_kv_heads;
     const fa512::TreeShape s = fa512::tree_shape(q_len, G);
-    const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks);
+    const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks, 128);
     const long long clusters = sm_count() / s.ctas > 0 ? sm_count() / s.ctas : 1;
     const long long per = (static_cast<long long>(batch) * n_kv_heads * s.groups * tiles + clusters - 1) / clusters;
     if (tiles <= 1 || per <= 0) return 1;

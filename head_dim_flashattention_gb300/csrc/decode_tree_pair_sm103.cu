@@ -169,21 +169,6 @@ __device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// A tile of cached keys inside every row's window: no key of it needs a mask.
-__device__ __forceinline__ bool whole_tile(const TreeParams& p, const Band& bd, int key0) {
-    return key0 + TILE <= min(bd.start, bd.hi) &&
-           (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
-}
-
-// Whether some key of a tile may be seen by no row, so that its V row has to
-// be cleared.  Without a mask every key of [lo, hi) and every sink is seen by
-// some row; with one, a drafted key may be named by nobody, and the window's
-// lower edge is known only to lie in [lo, place_max - window].
-__device__ __forceinline__ bool dirty_tile(const TreeParams& p, const Band& bd, int key0) {
-    if (p.tree_mask) return !whole_tile(p, bd, key0);
-    return key0 + TILE > bd.hi || (key0 < bd.lo && key0 + TILE > bd.sink_end);
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(THREADS, 1)
 tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -266,7 +251,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             // lane i: pool row of box i of tile t, or oob where no row sees a position of it
             auto row_of = [&](int t) -> int {
                 if (t >= n || lane >= 2 * boxes) return oob;
-                const int pos = d.key0(walk.first + t) + lane * box_rows;
+                const int pos = d.key((walk.first + t) * TILE + lane * box_rows);
                 if (pos >= d.hi || !(pos + box_rows > d.lo || pos < d.sink_end)) return oob;
                 const int page = p.page_table[static_cast<size_t>(walk.b) * p.max_pages_per_seq + pos / p.page_size];
                 if (page < 0 || page >= p.num_pages) {
@@ -290,7 +275,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     if (lane < 16) rows[lane] = row;
                     __syncwarp();
                 }
-                const bool raw = v && dirty_tile(p, d, d.key0(walk.first + t));
+                const bool raw = v && d.dirty(p, (walk.first + t) * TILE);
                 const CUtensorMap* tm = v ? &tmv : &tmk;
 #pragma unroll 1
                 for (int c = 0; c < C::SLOTS; ++c) {
@@ -441,7 +426,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                         if (ok)
                             ok = issue_pv(j == LOOK,
-                                          dirty_tile(p, walk.band, walk.band.key0(walk.first + j - LOOK)));
+                                          walk.band.dirty(p, (walk.first + j - LOOK) * TILE));
                     }
                 }
                 ++segment;
@@ -493,8 +478,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             for (int j = 0; j < n + LOOK && ok; ++j) {
                 if (j < n) slot = (slot + C::SLOTS) % NS;    // K(j)
                 if (j < LOOK) continue;
-                const int key0 = bd.key0(walk.first + j - LOOK);
-                if (!dirty_tile(p, bd, key0)) {
+                const int v0 = (walk.first + j - LOOK) * TILE;
+                if (!bd.dirty(p, v0)) {
                     slot = (slot + C::SLOTS) % NS;
                     continue;
                 }
@@ -525,7 +510,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int key = key0 + lane + 32 * k, pos = key & ~(box_rows - 1);
+                    const int key = bd.key(v0 + lane + 32 * k), pos = key & ~(box_rows - 1);
                     const bool loaded = pos < bd.hi && (pos + box_rows > bd.lo || pos < bd.sink_end);
                     const bool some = !p.tree_mask && key < bd.hi && (key >= bd.lo || key < bd.sink_end);
                     seen |= some || !loaded ? 1u << k : 0u;
@@ -749,7 +734,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             bool fresh = true;                               // some row may not have a reference yet
 #pragma unroll 1
             for (int t = 0; t < n; ++t, ++g) {
-                const int key0 = bd.key0(first + t), key = key0 + rank * HALF_TILE + kk;
+                const int v0 = (first + t) * TILE, key = bd.key(v0 + rank * HALF_TILE + kk);
                 ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
@@ -759,7 +744,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     sbuf = 0;
                     ++suse;
                 }
-                const bool whole = whole_tile(p, bd, key0);
+                const bool whole = bd.whole(p, v0);
                 uint32_t vis = 0xffffffffu;                  // bit i: row col0 + i sees this thread's key
                 if (!whole) {
                     const int c = key - bd.start;
@@ -940,7 +925,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
 
                 // with masks only the rows know whether some row sees a key
-                if (p.tree_mask && dirty_tile(p, bd, key0)) {
+                if (p.tree_mask && !whole) {
                     s_seen[grp * HALF_TILE + kk] = vis != 0u;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[C::SEEN_HERE]);

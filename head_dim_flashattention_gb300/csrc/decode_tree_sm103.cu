@@ -233,7 +233,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             auto row_of = [&](int t) -> int {
                 if (t >= n || lane >= boxes) return oob;
                 const Band& d = walk.band;
-                const int pos = d.key0(walk.first + t) + lane * box_rows;
+                const int pos = d.key((walk.first + t) * TILE + lane * box_rows);
                 if (pos >= d.hi || !(pos + box_rows > d.lo || pos < d.sink_end)) return oob;
                 const int page = p.page_table[static_cast<size_t>(walk.b) * p.max_pages_per_seq + pos / p.page_size];
                 if (page < 0 || page >= p.num_pages) {
@@ -546,7 +546,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             bool out = false;
             bool fresh = true;                               // some row may not have a reference yet
             for (int t = 0; t < n; ++t, ++g) {
-                const int key0 = bd.key0(first + t), key = key0 + kk;
+                const int v0 = (first + t) * TILE, key = bd.key(v0 + kk);
                 ok = ok && wait_or_abort(&bars[C::S_FULL + sbuf], suse & 1, p.err, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
@@ -575,8 +575,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     x[i + 3] = fmaf(x[i + 3], f.w, fresh && m[i + 3] == -INFINITY ? 0.f : -m[i + 3]);
                 }
                 // a tile of cached keys inside every row's window needs no mask
-                const bool whole = key0 + TILE <= min(bd.start, bd.hi) &&
-                                   (p.window <= 0 || key0 > bd.place_max - p.window || key0 + TILE <= bd.sink_end);
+                const bool whole = bd.whole(p, v0);
                 bool seen = true;                            // by some row of the group
                 if (!whole) {
                     const int c = key - bd.start;

@@ -105,11 +105,28 @@ struct BandOf {
     int len, cnt, start;        // cached positions, tokens, first token's position
     int lo, hi;                 // keys that some row may see: [lo, hi) and those below sink_end
     int sink_end;
-    int sink_tiles, lo_tile;    // tile i is i < sink_tiles ? i : lo_tile + i - sink_tiles
+    int span, shift;            // the walk's place v is key v below span (the sinks), else key v + shift
     int place_max;              // no row's place is above
     int tiles;
-    __device__ __forceinline__ int key0(int i) const {
-        return (i < sink_tiles ? i : lo_tile + i - sink_tiles) * TILE;
+    __device__ __forceinline__ int key(int v) const { return v < span ? v : v + shift; }
+    // Whether every row sees every key of the tile at place v0: cached keys
+    // inside every row's window, or sinks.
+    __device__ __forceinline__ bool whole(const TreeParams& p, int v0) const {
+        const int sinks = min(span, v0 + TILE);
+        if (v0 < span && sinks > min(sink_end, start)) return false;
+        const int first = max(v0, span) + shift, last = v0 + TILE - 1 + shift;
+        return v0 + TILE <= span ||
+               (last < min(start, hi) && (p.window <= 0 || first > place_max - p.window || last < sink_end));
+    }
+    // Whether some key of the tile may be seen by no row.  Without a mask every
+    // key of [lo, hi) and every sink is seen by some row; with one, a drafted
+    // key may be named by nobody, and the window's lower edge is known only to
+    // lie in [lo, place_max - window].
+    __device__ __forceinline__ bool dirty(const TreeParams& p, int v0) const {
+        if (p.tree_mask) return !whole(p, v0);
+        if (v0 < span && min(span, v0 + TILE) > sink_end) return true;
+        const int first = max(v0, span) + shift, last = v0 + TILE - 1 + shift;
+        return v0 + TILE > span && (last >= hi || (first < lo && last >= sink_end));
     }
 };
 
@@ -140,9 +157,14 @@ __device__ __noinline__ BandOf<TILE> band_of(const TreeParams& p, int b, int grp
         d.lo = from > p.window ? from - p.window : 0;
         d.sink_end = min(p.n_sinks, d.hi);
     }
-    d.lo_tile = d.lo / TILE;
-    d.sink_tiles = min((d.sink_end + TILE - 1) / TILE, d.lo_tile);
-    d.tiles = d.hi <= 0 ? 0 : d.sink_tiles + (d.hi + TILE - 1) / TILE - d.lo_tile;
+    // the walk is the sinks' boxes, then the boxes from lo on, so that neither
+    // edge costs a tile of its own (57 trees of 64 tokens, window 36 and 4 sinks:
+    // 220 -> 147 us)
+    const int box = min(p.page_size, 128), lo_box = d.lo / box * box;
+    d.span = (d.sink_end + box - 1) / box * box;
+    d.shift = lo_box - d.span;
+    if (d.shift <= 0) d.span = d.shift = 0;
+    d.tiles = d.hi <= 0 ? 0 : (d.hi - d.shift + TILE - 1) / TILE;
     return d;
 }
 
@@ -204,7 +226,13 @@ struct WalkOf {
 // the item that holds the range's first unit.  Every thread of the block calls
 // it; s_scan: SCAN_INTS int of shared memory.
 //
-// The row groups of a KV head read the same keys.  One walk over all items
+// Where there is a cluster for every item and equal segments of the longest
+// item are hardly longer than a range, a cluster takes one segment of one item,
+// for a change of item costs about as much as three tiles (8 sequences of 52
+// tokens with 8 heads on one KV head, 2,061 positions: 56.9 us with ranges, 46.6
+// with segments; 12 of 9 tokens, 4 KV heads, 1,937 positions in E4M3: 45.0, 36.7).
+//
+// Otherwise the ranges.  The row groups of a KV head read the same keys.  One walk over all items
 // would come to them at different times, when L2 has lost them (8 sequences of
 // 600 rows a KV head, window 4,096: 1.36 GB from memory for 0.27 GB of keys), so
 // the clusters form teams of one cluster per row group: each walks its group's
@@ -225,25 +253,49 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
         const BandOf<TILE> d = band_of<TILE>(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
         return max(1, d.tiles) * p.n_kv_heads;
     };
+    int* s_most = s_scan + 34;                              // units of the longest item
     int* s_team = s_scan + 36;                              // units of each row group
     const int teams = walk.groups > 1 && walk.groups <= MAX_TEAM ? clusters / walk.groups : 0;
-    if (teams > 0) {
-        if (tid < MAX_TEAM) s_team[tid] = 0;
-        __syncthreads();
-    }
-    int total = 0, mine0 = 0;                        // mine0: entry tid's units
+    if (tid == 0) *s_most = 0;
+    if (teams > 0 && tid < MAX_TEAM) s_team[tid] = 0;
+    __syncthreads();
+    int total = 0, longest = 0, mine0 = 0;           // mine0: entry tid's units
     for (int e = tid; e < walk.entries; e += THREADS) {
         const int u = entry_units(e, blockIdx.x == 0);
         if (e == tid) mine0 = u;
         total += u;
+        longest = max(longest, u / p.n_kv_heads);
         if (teams > 0) atomicAdd(&s_team[e % walk.groups], u);
     }
     total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) s_scan[warp] = total;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+        s_scan[warp] = total;
+        atomicMax(s_most, longest);
+    }
     __syncthreads();
     total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
-    int start = 0;                                          // first entry of the walk's
+    longest = *s_most;
     walk.stride = 1;
+    const long long items = static_cast<long long>(walk.entries) * p.n_kv_heads;
+    if (items <= clusters) {
+        const int segments = min(clusters / static_cast<int>(items), p.num_splits);
+        const int range = max((total + clusters - 1) / clusters, p.min_range);
+        if (segments == 1 ? p.num_splits == 1 || longest <= range + 2 : (longest + segments - 1) / segments <= range + 2) {
+            const int item = me / segments, segment = me - item * segments;
+            walk.pos = walk.end = walk.base = 0;
+            if (item < items) {
+                walk.entry = item / p.n_kv_heads;
+                walk.kvh = item - walk.entry * p.n_kv_heads;
+                walk.load(p);
+                walk.per = (walk.units() + segments - 1) / segments;
+                walk.pos = min(segment * walk.per, walk.units());
+                walk.end = min(walk.pos + walk.per, walk.units());
+            }
+            return;
+        }
+    }
+    int start = 0;                                          // first entry of the walk's
     if (teams > 0) {
         const int most = __reduce_max_sync(0xffffffffu, lane < walk.groups ? s_team[lane] : 0);
         const long long share = (total + clusters - 1) / clusters;

@@ -450,3 +450,19 @@ def test_row_groups_of_padded_batches(fa, cnts, fp8):
     check(fa, pc, q, None, s, q_lens=ql)
     check(fa, pc, q, None, s, q_lens=ql, window=200, n_sinks=5, num_splits=1)
     check(fa, pc, q, None, s, q_lens=ql, window=600, num_splits=4)
+
+
+@FP8
+@pytest.mark.parametrize("hq", [8, 40])
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+@pytest.mark.parametrize("window,n_sinks", [(40, 3), (300, 70), (129, 128), (400, 260)])
+def test_sinks_beside_a_window(fa, window, n_sinks, page, hq, fp8):
+    """The keys between the sinks and the window are left out page by page; what no row sees holds NaN."""
+    lens = [1100, 700, 271]
+    pc, q, s = make(lens, 9, hq, 4, page, 132, fp8)
+    mask = random_masks(3, 9, 132)
+    poison_unseen(pc, mask, [9] * 3, window, n_sinks)
+    check(fa, pc, q, mask, s, window=window, n_sinks=n_sinks)
+    pc, q, s = make(lens, 9, hq, 4, page, 133, fp8)
+    poison_unseen(pc, None, [9] * 3, window, n_sinks)
+    check(fa, pc, q, None, s, window=window, n_sinks=n_sinks)
