@@ -88,8 +88,8 @@ struct Cfg {
     static constexpr int low = mult + ROWS * 4;            // [ROWS] int: the rows' last key below the window; INT_MAX: sees nothing
     static constexpr int rows = low + ROWS * 4;        // [4 tiles][8 boxes] int: the producer's pool rows
     static constexpr int seen = rows + 4 * 8 * 4;         // [GROUPS][TILE] bytes: some row of the group sees the key
-    static constexpr int scan = seen + GROUPS * TILE;    // 32 int, then the walk's start
-    static constexpr int info = scan + 32 * 4 + 16;      // [ROWS] 16 bytes: what the epilogue writes
+    static constexpr int scan = seen + GROUPS * TILE;    // start_walk's
+    static constexpr int info = scan + (36 + 32) * 4;      // [ROWS] 16 bytes: what the epilogue writes
     static constexpr int bars = info + ROWS * 16;
     static constexpr int MAX_NS = 6;
     static constexpr int FULL = 0, EMPTY = MAX_NS, S_FULL = 2 * MAX_NS, S_FREE = S_FULL + NB, P_FULL = S_FREE + NB,

@@ -240,7 +240,7 @@ struct WalkOf {
 // us).  Where a padded batch leaves the groups unlike (the longest group's range more than a
 // tenth above everybody's equal share) all walk all items.
 constexpr int MAX_TEAM = 16;
-constexpr int SCAN_INTS = 36 + MAX_TEAM;
+constexpr int SCAN_INTS = 36 + 32 + MAX_TEAM;          // without teams: 36 + 32
 template <int TILE, int THREADS>
 __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams& p, int clusters, int me, int* s_scan) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -253,12 +253,13 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
         const BandOf<TILE> d = band_of<TILE>(p, eb, e - eb * walk.groups, walk.group_rows, record && e == eb * walk.groups);
         return max(1, d.tiles) * p.n_kv_heads;
     };
-    int* s_most = s_scan + 34;                              // units of the longest item
-    int* s_team = s_scan + 36;                              // units of each row group
+    int* s_most = s_scan + 36;                              // units of each warp's longest item
+    int* s_team = s_scan + 68;                              // units of each row group
     const int teams = walk.groups > 1 && walk.groups <= MAX_TEAM ? clusters / walk.groups : 0;
-    if (tid == 0) *s_most = 0;
-    if (teams > 0 && tid < MAX_TEAM) s_team[tid] = 0;
-    __syncthreads();
+    if (teams > 0) {
+        if (tid < MAX_TEAM) s_team[tid] = 0;
+        __syncthreads();
+    }
     int total = 0, longest = 0, mine0 = 0;           // mine0: entry tid's units
     for (int e = tid; e < walk.entries; e += THREADS) {
         const int u = entry_units(e, blockIdx.x == 0);
@@ -271,14 +272,14 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) {
         s_scan[warp] = total;
-        atomicMax(s_most, longest);
+        s_most[warp] = longest;
     }
     __syncthreads();
     total = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[lane] : 0);
-    longest = *s_most;
     walk.stride = 1;
     const long long items = static_cast<long long>(walk.entries) * p.n_kv_heads;
     if (items <= clusters) {
+        longest = __reduce_max_sync(0xffffffffu, lane < NW ? s_most[lane] : 0);
         const int segments = min(clusters / static_cast<int>(items), p.num_splits);
         const int range = max((total + clusters - 1) / clusters, p.min_range);
         if (segments == 1 ? p.num_splits == 1 || longest <= range + 2 : (longest + segments - 1) / segments <= range + 2) {
