@@ -21,9 +21,9 @@
 // rows over 16 caches of 20,000 to 28,672 positions).  Measured: 64 sequences
 // of 16,384 positions in E4M3, 32 rows: 629-647 us, 6.7-6.9 TB/s, 98-101 % of
 // the measured copy rate; 16 sequences of 8,192 positions in bf16: 172 us with
-// 32 rows, 183 us with 64; one of 4,096 positions with 16 rows: 19.2 us, of
-// which the stream of its 128 tiles, one an SM, is ~8: the rest is the chain of
-// launch, lengths, Q, one tile's two products and the merge.
+// 32 rows, 183 us with 64; one of 4,096 positions with 16 rows: 19.3 us, where
+// a bare read of its 32 MB takes ~12: start and lengths 4, Q 2, one tile's
+// products 3, O and its partials 5, the merge 4 us after one another.
 //
 // The row maxima lie across lanes here, so they are not reduced every tile:
 // each thread compares its scores with the reference its rows hold, and only
@@ -41,7 +41,8 @@
 //
 // Work: the (sequence, row group, KV head) items' tiles, one after another,
 // are cut into equal ranges, one per SM, so every SM streams the same number
-// of tiles whatever the lengths; an item that spans several ranges leaves
+// of tiles whatever the lengths (where there is an SM for every item, each
+// takes one equal segment of one item instead); an item in several pieces leaves
 // (O, m, l) partials that a merge kernel combines, any other is written
 // directly.
 #include <cuda.h>

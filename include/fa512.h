@@ -374,9 +374,10 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
  *
  * A row is a (token, query head) pair.  Up to 64 rows of a KV head share one
  * pass over its keys in one CTA; more are taken in groups of 128, each on a
- * pair of SMs.  The keys of all sequences are cut into ranges of equal length,
- * one per CTA or pair, so num_splits is the most segments that one row may be
- * left in (1: no row is split; 0: fa512_decode_auto_splits_tree()).  Only
+ * pair of SMs.  The keys of all sequences are cut into ranges of equal length
+ * (or each item's into equal segments), one per CTA or pair, so num_splits is
+ * the most segments that one row may be left in (1: no row is split; 0:
+ * fa512_decode_auto_splits_tree()).  Only
  * pages that hold positions inside the band of some row are read; slots that
  * no row sees may hold anything (NaN included) without reaching the output.
  * The same inputs give the same bits every time.  out, lse and workspace must
@@ -512,7 +513,8 @@ fa512_status fa512_cache_compact(void *k_pages, void *v_pages, const int32_t *pa
  *                holders) refer to each page; 0 is free
  *   new_page_table [n_children, max_pages_per_seq], new_kv_lens [n_children],
  *   new_page_refs [num_pages] int32, device, written; new_page_refs may be
- *                page_refs itself, the other two must not overlap the inputs
+ *                page_refs itself, the other two must not overlap the inputs; no two of
+ *                the three may overlap
  *
  * A sequence of n positions holds its first ceil(n / page_size) entries.
  * Child c shares the pages of parents[c].  A last page that is only partly
