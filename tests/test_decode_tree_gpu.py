@@ -466,3 +466,17 @@ def test_sinks_beside_a_window(fa, window, n_sinks, page, hq, fp8):
     pc, q, s = make(lens, 9, hq, 4, page, 133, fp8)
     poison_unseen(pc, None, [9] * 3, window, n_sinks)
     check(fa, pc, q, None, s, window=window, n_sinks=n_sinks)
+
+
+@FP8
+@pytest.mark.parametrize("nodes", [3, 20, 40])
+@pytest.mark.parametrize("shape", ["one long", "many"])
+def test_ranges_over_several_items(fa, shape, nodes, fp8):
+    """Lengths so unlike, or sequences so many, that a CTA's keys begin and end inside items of several sequences."""
+    lens = [9000, 100, 90, 0, 700] if shape == "one long" else [60 + 37 * (i % 11) for i in range(50)]
+    pc, q, s = make(lens, nodes, 8, 4, 64, 134, fp8)
+    a = check(fa, pc, q, None, s)
+    b = call(fa, pc, q, None, s)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    check(fa, pc, q, random_masks(len(lens), nodes, 134), s, num_splits=5)
+    check(fa, pc, q, None, s, window=300, n_sinks=20)
