@@ -169,6 +169,20 @@ __device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
+// Brings the query rows of the walk's segment into L2, a lane a token: the
+// softmax warps will ask for them when they come to it (22 runs of 46 tokens
+// with 8 heads on one KV head: 298 -> 294 us).
+__device__ __forceinline__ void prefetch_q(const TreeParams& p, const Walk& walk) {
+    const int row0 = walk.grp * ROWS;
+    const int end = min((row0 + ROWS - 1) / p.group + 1, walk.band.cnt);
+#pragma unroll 1
+    for (int t = row0 / p.group + static_cast<int>(threadIdx.x & 31); t < end; t += 32)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(p.q + ((static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * p.group) * D),
+                     "r"(p.group * D * 2)
+                     : "memory");
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(THREADS, 1)
 tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -244,10 +258,13 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         int slot = 0;
         uint32_t use = 0;
         bool ok = true;
+        bool start = true;                                   // the walk's first segment: its Q is being read
         uint32_t raw_used = 0, full_used = 0;                // per slot: parity of the uses of the two barriers
         while (ok && walk.next(p)) {
             const int n = walk.n;
             const Band& d = walk.band;
+            if (rank == 0 && !start && n > 0) prefetch_q(p, walk);
+            start = false;
             // lane i: pool row of box i of tile t, or oob where no row sees a position of it
             auto row_of = [&](int t) -> int {
                 if (t >= n || lane >= 2 * boxes) return oob;
