@@ -506,43 +506,44 @@ def fa512_decode_workspace_bytes_tree(batch: int, q_len: int, n_q_heads: int, n_
 
 def _decode_tree(fp8, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, lse, q_lens, k_scale,
                  v_scale, max_kv_len, scale, window, n_sinks, num_splits, workspace, return_lse, stream):
-    if q.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2 or q.shape[3] != HEAD_DIM \
-            or k_pages.shape[3] != HEAD_DIM:
+    qs, ks, ts = q.shape, k_pages.shape, page_table.shape
+    if len(qs) != 4 or len(ks) != 4 or len(ts) != 2 or qs[3] != HEAD_DIM or ks[3] != HEAD_DIM:
         raise Fa512Error(1, "q must be [batch, q_len, heads, 512], pages [n, page, heads, 512], page_table "
                             "[batch, max_pages_per_seq]")
-    bsz, qlen, hq, d = q.shape
-    npages, psz, hk, _ = k_pages.shape
-    mpps = page_table.shape[1]
+    bsz, qlen, hq, d = qs
+    npages, psz, hk, _ = ks
+    mpps = ts[1]
     dev = _device(q, "q")
     rows = (bsz, qlen, hq)
-    if max_kv_len is None:
-        max_kv_len = mpps * psz
-    if scale is None:
-        scale = d ** -0.5
+    max_kv_len = mpps * psz if max_kv_len is None else int(max_kv_len)
+    window, n_sinks, num_splits = int(window), int(n_sinks), int(num_splits)
     lib = _lib or load_library()
     mine = []
     if out is None:
-        out = torch.empty(rows + (d,), dtype=_BF16, device=q.device)
+        out = torch.empty(qs, dtype=_BF16, device=dev)
         mine.append(out)
     if lse is None and return_lse:
-        lse = torch.empty(rows, dtype=_F32, device=q.device)
+        lse = torch.empty(rows, dtype=_F32, device=dev)
         mine.append(lse)
     if workspace is None:
-        need = lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, int(max_kv_len), int(window),
-                                                     int(n_sinks), int(num_splits))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        # 0: a shape that the call below refuses
+        ws_bytes = lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, max_kv_len, window, n_sinks,
+                                                         num_splits) or 256
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         mine.append(workspace)
-    ws_bytes = workspace.numel() * workspace.element_size()
+        ws = workspace.data_ptr()
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _arg(workspace, "workspace", workspace.dtype, dev)
     kind = _E4M3 if fp8 else _BF16
     head = (_arg(q, "q", _BF16, dev), _arg(k_pages, "k_pages", kind, dev),
-            _arg(v_pages, "v_pages", kind, dev, k_pages.shape),
+            _arg(v_pages, "v_pages", kind, dev, ks),
             _arg(page_table, "page_table", _I32, dev, (bsz, mpps)), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
             _arg(q_lens, "q_lens", _I32, dev, (bsz,)),
             _arg(tree_mask, "tree_mask", _I32, dev, (bsz, qlen, (qlen + 31) // 32)),
-            _arg(out, "out", _BF16, dev, rows + (d,)), _arg(lse, "lse", _F32, dev, rows), bsz, qlen, hq, hk,
-            psz, npages, mpps, int(max_kv_len), float(scale))
-    tail = (int(window), int(n_sinks), int(num_splits), _arg(workspace, "workspace", workspace.dtype, dev),
-            ws_bytes, _stream(stream, dev))
+            _arg(out, "out", _BF16, dev, qs), _arg(lse, "lse", _F32, dev, rows), bsz, qlen, hq, hk,
+            psz, npages, mpps, max_kv_len, d ** -0.5 if scale is None else float(scale))
+    tail = (window, n_sinks, num_splits, ws, ws_bytes, _stream(stream, dev))
     if fp8:
         _check(lib.fa512_decode_paged_tree_fp8(*head, float(k_scale), float(v_scale), *tail))
     else:
