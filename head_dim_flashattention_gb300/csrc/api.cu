@@ -778,6 +778,11 @@ long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sin
     return some < all ? some : all;
 }
 
+// Whether that many tiles are walked in one piece: a merge costs about 4 us, a
+// tile of 128 keys 2 to 3.5 (24 runs of 2 tokens over 164 positions: 20.1 us in
+// two pieces, 18.5 in one; with three tiles as many shapes lose as gain).
+bool one_piece(const fa512::TreeShape& s, long long tiles) { return tiles <= (s.ctas == 1 ? 2 : 1); }
+
 // Partials of `rows` rows in `splits` segments, and the items' segment counts.
 size_t tree_workspace(long long batch, int q_len, int n_q_heads, int n_kv_heads, int splits) {
     const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
@@ -832,9 +837,12 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
          reinterpret_cast<uintptr_t>(q_lens) | reinterpret_cast<uintptr_t>(tree_mask) |
          reinterpret_cast<uintptr_t>(lse)) & 3u)
         return fail(FA512_ERR_INVALID_ARG, "int32 arrays and lse must be 4-byte aligned");
-    const int splits = num_splits > 0 ? num_splits
-                                      : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
-                                                                      max_kv_len, window, n_sinks);
+    const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
+    const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks, page_size < 128 ? page_size : 128);
+    const int splits = num_splits > 0           ? num_splits
+                       : one_piece(shape, tiles) ? 1
+                                                 : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
+                                                                                 max_kv_len, window, n_sinks);
     if (splits > 1) {
         if (static_cast<long long>(batch) * q_len > 65535)
             return fail(FA512_ERR_UNSUPPORTED, "more than 65535 tokens with more than one split");
@@ -873,10 +881,9 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.n_q_heads = n_q_heads;
     p.n_kv_heads = n_kv_heads;
     p.group = G;
-    const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
     p.rows = shape.rows;
     p.row_groups = shape.groups;
-    p.max_tiles = static_cast<int>(tree_tiles(q_len, G, max_kv_len, window, n_sinks, page_size < 128 ? page_size : 128));
+    p.max_tiles = static_cast<int>(tiles);
     p.min_range = splits > 1 ? (p.max_tiles + splits - 2) / (splits - 1) : 0;
     if (static_cast<long long>(batch) * shape.groups * n_kv_heads * (p.max_tiles > 1 ? p.max_tiles : 1) > 0x7fffffffLL)
         return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
@@ -1002,7 +1009,7 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
     const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks, 128);
     const long long clusters = sm_count() / s.ctas > 0 ? sm_count() / s.ctas : 1;
     const long long per = (static_cast<long long>(batch) * n_kv_heads * s.groups * tiles + clusters - 1) / clusters;
-    if (tiles <= 1 || per <= 0) return 1;
+    if (one_piece(s, tiles) || per <= 0) return 1;
     // the ranges of a batch of this length touch ceil(tiles / per) + 1 of an
     // item's segments at most; a batch with shorter sequences has shorter
     // ranges, so twice as many are allowed

@@ -376,8 +376,8 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
  * pass over its keys in one CTA; more are taken in groups of 128, each on a
  * pair of SMs.  The keys of all sequences are cut into ranges of equal length
  * (or each item's into equal segments), one per CTA or pair, so num_splits is
- * the most segments that one row may be left in (1: no row is split; 0:
- * fa512_decode_auto_splits_tree()).  Only
+ * the most segments that one row may be left in (1: no row is split; 0: at
+ * most fa512_decode_auto_splits_tree()).  Only
  * pages that hold positions inside the band of some row are read; slots that
  * no row sees may hold anything (NaN included) without reaching the output.
  * The same inputs give the same bits every time.  out, lse and workspace must
