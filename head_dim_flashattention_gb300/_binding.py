@@ -147,6 +147,30 @@ def _stream(stream, dev: int | None = None) -> int | None:
     return int(stream)
 
 
+def _side(stream):
+    """The stream that a call is given as a torch stream; None where it is the current one."""
+    if stream is None or _stream(stream) == _stream(None):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _new(side, shape, dtype, device, returned: bool = True) -> torch.Tensor:
+    """A tensor that a call makes for itself.  It comes from the memory of the
+    stream that writes it: a block of the current stream's may have a user that
+    is still queued there, which the other stream does not wait for.  What is
+    returned is not given back to that stream before the current one's work on
+    it is done."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def fa512_status_string(status: int) -> str:
     return load_library().fa512_status_string(int(status)).decode()
 
@@ -165,10 +189,11 @@ def fa512_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         raise Fa512Error(1, "q, k, v must be [seq, heads, 512] with k.shape == v.shape")
     sq, hq, d = q.shape
     sk, hk, _ = k.shape
+    side = _side(stream)
     if out is None:
-        out = torch.empty((sq, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _new(side, (sq, hq, d), torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((hq, sq), dtype=torch.float32, device=q.device)
+        lse = _new(side, (hq, sq), torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
@@ -194,10 +219,11 @@ def fa512_prefill_d256(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     sk, hk, dk = k.shape
     if d != 256 or dk != 256:
         raise Fa512Error(1, "fa512_prefill_d256 takes heads of 256 dimensions")
+    side = _side(stream)
     if out is None:
-        out = torch.empty((sq, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _new(side, (sq, hq, d), torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((hq, sq), dtype=torch.float32, device=q.device)
+        lse = _new(side, (hq, sq), torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
@@ -232,10 +258,11 @@ def fa512_prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     bsz, mpps = page_table.shape
     if cu_seqlens_q.shape[0] != bsz + 1 or seqused_k.shape[0] != bsz:
         raise Fa512Error(1, "cu_seqlens_q must have batch + 1 entries and seqused_k batch")
+    side = _side(stream)
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _new(side, (total_q, hq, d), torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((hq, total_q), dtype=torch.float32, device=q.device)
+        lse = _new(side, (hq, total_q), torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
@@ -294,17 +321,18 @@ def fa512_decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     mpps = page_table.shape[1]
     if max_kv_len is None:
         max_kv_len = mpps * psz
+    side = _side(stream)
     if out is None:
-        out = torch.empty((bsz, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _new(side, (bsz, hq, d), torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((bsz, hq), dtype=torch.float32, device=q.device)
+        lse = _new(side, (bsz, hq), torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
     need = int(lib.fa512_decode_workspace_bytes(bsz, hq, hk, psz, int(max_kv_len),
                                                 int(num_splits)))
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(side, max(need, 256), torch.uint8, q.device, returned=False)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.fa512_decode_paged(
         _dptr(q, "q", torch.bfloat16), _dptr(k_pages, "k_pages", torch.bfloat16),
@@ -367,17 +395,18 @@ def fa512_decode_paged_q(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     mpps = page_table.shape[1]
     if max_kv_len is None:
         max_kv_len = mpps * psz
+    side = _side(stream)
     if out is None:
-        out = torch.empty((bsz, qlen, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _new(side, (bsz, qlen, hq, d), torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((bsz, qlen, hq), dtype=torch.float32, device=q.device)
+        lse = _new(side, (bsz, qlen, hq), torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
     need = int(lib.fa512_decode_workspace_bytes_q(bsz, qlen, hq, hk, psz, int(max_kv_len),
                                                   int(num_splits)))
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(side, max(need, 256), torch.uint8, q.device, returned=False)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.fa512_decode_paged_q(
         _dptr(q, "q", torch.bfloat16), _dptr(k_pages, "k_pages", torch.bfloat16),
@@ -423,17 +452,18 @@ def fa512_decode_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     mpps = page_table.shape[1]
     if max_kv_len is None:
         max_kv_len = mpps * psz
+    side = _side(stream)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _new(side, q.shape, torch.bfloat16, q.device)
     if lse is None and return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        lse = _new(side, q.shape[:-1], torch.float32, q.device)
     if scale is None:
         scale = d ** -0.5
     lib = load_library()
     need = int(lib.fa512_decode_workspace_bytes_fp8(bsz, qlen, hq, hk, psz, int(max_kv_len),
                                                     int(num_splits)))
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(side, max(need, 256), torch.uint8, q.device, returned=False)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.fa512_decode_paged_fp8(
         _dptr(q, "q", torch.bfloat16), _e4m3_bytes(k_pages, "k_pages"),
@@ -480,17 +510,6 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _CACHE = (torch.bfloat16,) + _E4M3
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tells the allocator that tensors it made here are used on another stream."""
-    if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
-
-
 def fa512_decode_auto_splits_tree(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
                                   max_kv_len: int, window: int = 0, n_sinks: int = 0) -> int:
     return int(load_library().fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
@@ -518,19 +537,16 @@ def _decode_tree(fp8, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, 
     max_kv_len = mpps * psz if max_kv_len is None else int(max_kv_len)
     window, n_sinks, num_splits = int(window), int(n_sinks), int(num_splits)
     lib = _lib or load_library()
-    mine = []
+    side = _side(stream)
     if out is None:
-        out = torch.empty(qs, dtype=_BF16, device=dev)
-        mine.append(out)
+        out = _new(side, qs, _BF16, dev)
     if lse is None and return_lse:
-        lse = torch.empty(rows, dtype=_F32, device=dev)
-        mine.append(lse)
+        lse = _new(side, rows, _F32, dev)
     if workspace is None:
         # 0: a shape that the call below refuses
         ws_bytes = lib.fa512_decode_workspace_bytes_tree(bsz, qlen, hq, hk, max_kv_len, window, n_sinks,
                                                          num_splits) or 256
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        mine.append(workspace)
+        workspace = _new(side, ws_bytes, torch.uint8, dev, returned=False)
         ws = workspace.data_ptr()
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
@@ -548,7 +564,6 @@ def _decode_tree(fp8, q, k_pages, v_pages, page_table, kv_lens, tree_mask, out, 
         _check(lib.fa512_decode_paged_tree_fp8(*head, float(k_scale), float(v_scale), *tail))
     else:
         _check(lib.fa512_decode_paged_tree(*head, *tail))
-    _used_on(stream, *mine)
     return out, lse
 
 
@@ -678,16 +693,13 @@ def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table
     bsz, mpps = page_table.shape
     most = accepted.shape[1]
     one = (bsz,)
-    mine = []
     if new_kv_lens is None:
-        new_kv_lens = torch.empty(one, dtype=_I32, device=k_pages.device)
-        mine.append(new_kv_lens)
+        new_kv_lens = _new(_side(stream), one, _I32, dev)
     _check((_lib or load_library()).fa512_cache_compact(
         kp, vp, _arg(page_table, "page_table", _I32, dev), _arg(kv_lens, "kv_lens", _I32, dev, one),
         _arg(q_lens, "q_lens", _I32, dev, one), _arg(accepted, "accepted", _I32, dev, (bsz, most)),
         _arg(n_accepted, "n_accepted", _I32, dev, one), _arg(new_kv_lens, "new_kv_lens", _I32, dev, one),
         layers, bsz, int(q_len), most, hk, eb, psz, npages, mpps, _stream(stream, dev)))
-    _used_on(stream, *mine)
     return new_kv_lens
 
 
@@ -709,13 +721,10 @@ def fa512_cache_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: t
         raise Fa512Error(1, "page_table must be [batch, pages], parents [n_children]")
     bsz, mpps = page_table.shape
     kids = parents.shape[0]
-    mine = []
+    side = _side(stream)
 
     def out(t, shape):
-        if t is None:
-            t = torch.empty(shape, dtype=_I32, device=k_pages.device)
-            mine.append(t)
-        return t
+        return _new(side, shape, _I32, dev) if t is None else t
     new_page_table = out(new_page_table, (kids, mpps))
     new_kv_lens = out(new_kv_lens, (kids,))
     new_page_refs = out(new_page_refs, (npages,))
@@ -726,7 +735,6 @@ def fa512_cache_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: t
         _arg(new_kv_lens, "new_kv_lens", _I32, dev, (kids,)),
         _arg(new_page_refs, "new_page_refs", _I32, dev, (npages,)), layers, bsz, kids, hk, eb, psz, npages,
         mpps, _stream(stream, dev)))
-    _used_on(stream, *mine)
     return new_page_table, new_kv_lens, new_page_refs
 
 
@@ -744,20 +752,17 @@ def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_l
     bsz, mpps = page_table.shape
     npages = page_refs.shape[0]
     dev = _device(page_table, "page_table")
-    mine = []
+    side = _side(stream)
     if new_page_table is None:
-        new_page_table = torch.empty_like(page_table)
-        mine.append(new_page_table)
+        new_page_table = _new(side, page_table.shape, _I32, dev)
     if new_page_refs is None:
-        new_page_refs = torch.empty_like(page_refs)
-        mine.append(new_page_refs)
+        new_page_refs = _new(side, page_refs.shape, _I32, dev)
     _check((_lib or load_library()).fa512_cache_resize(
         _arg(page_table, "page_table", _I32, dev), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
         _arg(new_kv_lens, "new_kv_lens", _I32, dev, (bsz,)), _arg(page_refs, "page_refs", _I32, dev),
         _arg(new_page_table, "new_page_table", _I32, dev, (bsz, mpps)),
         _arg(new_page_refs, "new_page_refs", _I32, dev, (npages,)), bsz, int(page_size), npages, mpps,
         _stream(stream, dev)))
-    _used_on(stream, *mine)
     return new_page_table, new_page_refs
 
 
