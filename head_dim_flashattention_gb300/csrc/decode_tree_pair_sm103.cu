@@ -971,7 +971,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
             if (speaker) {
                 const float top = s_m[cl];
                 const int r = row0 + cl, t = r / G;
-                const bool some = s_low[cl] != INT_MAX && top != -INFINITY;
+                const bool some = some_key(s_low[cl], top, sum);
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
                 const size_t at = direct ? row : row * static_cast<size_t>(p.num_splits) + walk.index;
                 const float unit = p.o_scale * (1.f / C::P_SCALE);
@@ -981,7 +981,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     make_uint4(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), __float_as_uint(factor), real);
                 if (real && rank == 0) {
                     if (!direct) {
-                        p.ws_ml[at * 2] = some ? top : -INFINITY;
+                        p.ws_ml[at * 2] = partial_max(some, top, sum);
                         p.ws_ml[at * 2 + 1] = some ? sum : 0.f;
                     } else if (p.lse) {
                         p.lse[row] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;

@@ -756,7 +756,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 for (int i = 0; i < GW; ++i) top = lane == i ? m[i] : top;
                 const int cl = col0 + (lane & (GW - 1)), r = row0 + cl, t = r / G;
                 const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
-                const bool some = s_low[cl] != INT_MAX && top != -INFINITY;
+                const bool some = some_key(s_low[cl], top, sum);
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
                 const size_t at = direct ? row : row * S + walk.index;
                 const float unit = p.o_scale * (1.f / C::P_SCALE);
@@ -768,7 +768,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                     if (mine && direct && p.lse)
                         p.lse[row] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
                     if (mine && !direct) {
-                        p.ws_ml[at * 2] = some ? top : -INFINITY;
+                        p.ws_ml[at * 2] = partial_max(some, top, sum);
                         p.ws_ml[at * 2 + 1] = some ? sum : 0.f;
                     }
                 }

@@ -352,6 +352,18 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
     }
 }
 
+// Whether a row's softmax has weight, from the row's `low` (INT_MAX: it sees
+// nothing), maximum and sum.  A NaN score is no maximum (fmaxf passes over it)
+// but makes the sum NaN, and so it has to come out.
+__device__ __forceinline__ bool some_key(int low, float top, float sum) {
+    return low != INT_MAX && (top != -INFINITY || sum != 0.f);
+}
+// The maximum that goes with a partial: +inf beside a NaN sum, which makes the
+// merged row NaN whatever its other segments hold.
+__device__ __forceinline__ float partial_max(bool some, float top, float sum) {
+    return !some ? -INFINITY : sum != sum ? INFINITY : top;
+}
+
 // Word w of token t's mask; bits at and behind cnt name no token.
 __device__ __forceinline__ uint32_t mask_word(const TreeParams& p, int b, int cnt, int t, int w) {
     const int left = cnt - 32 * w;
