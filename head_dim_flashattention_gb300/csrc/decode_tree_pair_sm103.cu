@@ -41,6 +41,8 @@
 // clears the rows of such keys and hands each slot to the MMA.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "fa512_tree.cuh"
 
 namespace fa512 {
@@ -64,6 +66,7 @@ constexpr int THREADS = (CLEANER + 1) * 32;
 constexpr int LOOK = 1;                  // S^T tiles computed ahead of O^T += V^T P^T
 constexpr int NB = LOOK + 1;
 constexpr uint32_t TM_O = 0, TM_S = 256;
+constexpr int PLAIN = 0, FUSED = 1, LESS = 2;       // forms of the scores
 using Walk = WalkOf<TILE>;
 using Band = BandOf<TILE>;
 
@@ -92,7 +95,7 @@ struct Cfg {
     static constexpr int depth = cols + MAX_NODES * GROUPS * 4;
     static constexpr int red = depth + MAX_NODES * 4;    // [4][ROWS] float
     static constexpr int m = red + 4 * ROWS * 4;         // [ROWS] float: references
-    static constexpr int mb = m + ROWS * 4;              // [ROWS] float2: score -> log2 units, less the reference
+    static constexpr int mb = m + ROWS * 4;              // [ROWS / 2] float4: a row pair's factors (score -> log2 units) and negated references
     static constexpr int low = mb + ROWS * 8;            // [ROWS] int: the rows' last key below the window; INT_MAX: sees nothing
     static constexpr int info = low + ROWS * 4;        // [ROWS] 16 bytes: what the epilogue writes
     static constexpr int rows = info + ROWS * 16;        // [4 tiles][16 boxes] int: the producer's pool rows
@@ -571,6 +574,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
         float* s_red = reinterpret_cast<float*>(smem + C::red);
         float* s_m = reinterpret_cast<float*>(smem + C::m);
         float2* s_mb = reinterpret_cast<float2*>(smem + C::mb);
+        auto mult_of = [&](int r) -> float& { return reinterpret_cast<float*>(s_mb + (r & ~1))[r & 1]; };
+        auto less_of = [&](int r) -> float& { return reinterpret_cast<float*>(s_mb + (r & ~1))[2 + (r & 1)]; };
         int* s_low = reinterpret_cast<int*>(smem + C::low);
         uint8_t* s_seen = smem + C::seen;
         bool ok = true;
@@ -657,7 +662,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             const int E = (__float_as_uint(amax) >> 23) & 0xff;
                             const int biased = min(7 + 2 * 127 - E, 254);
                             const float qs = (amax > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
-                            if (lane == 0) s_mb[half * HALF_ROWS + r] = make_float2(p.scale_log2 / qs, 0.f);
+                            if (lane == 0) mult_of(half * HALF_ROWS + r) = p.scale_log2 / qs;
                             if (half != rank) continue;
                             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -689,7 +694,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const int place = bd.start + (p.tree_mask && real && n > 0 ? s_depth[t] : t);
                 s_low[r] = !real ? INT_MAX : p.window > 0 && place >= INT_MIN + p.window ? place - p.window : INT_MIN;
                 s_m[r] = -INFINITY;
-                if (!FP8) s_mb[r] = make_float2(p.scale_log2, 0.f);
+                less_of(r) = 0.f;
+                if (!FP8) mult_of(r) = p.scale_log2;
             }
             bar_sync(ALL, SW * 32);
         };
@@ -788,18 +794,27 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         }
                     }
                 }
-                // Scores of 16 of the group's rows, log2 units less the rows'
-                // references.  They are read from tensor memory where they are
-                // needed, not kept: 32 scores beside the 32 row sums would spill.
-                auto scores = [&](int c0, float (&x)[16]) {
+                // Scores of 16 of the group's rows in log2 units (PLAIN) or less
+                // the rows' references.  They are read from tensor memory where they
+                // are needed, not kept: 32 scores beside the 32 row sums would spill.
+                // A reference is one of these scores, rounded as it is here: a
+                // product that is not rounded before the reference is taken off
+                // would leave half its last place, for a score of 2^32 and more an
+                // exponent that overflows.  The vote may take one (FUSED): what it
+                // finds below THR, a power of two, comes to at most THR when rounded.
+                auto scores = [&](int c0, float (&x)[16], auto form) {
                     uint32_t raw[16];
                     tmem_ld16(s_at + static_cast<uint32_t>(c0), raw);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float4 f = *reinterpret_cast<const float4*>(&s_mb[col0 + c0 + i]);
-                        x[i] = fmaf(__uint_as_float(raw[i]), f.x, f.y);
-                        x[i + 1] = fmaf(__uint_as_float(raw[i + 1]), f.z, f.w);
+                        const float2 r = make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
+                        const float2 mult = make_float2(f.x, f.y), less = make_float2(f.z, f.w);
+                        const float2 y = ffma2(r, mult, form.value == FUSED ? less : make_float2(0.f, 0.f));
+                        const float2 z = form.value == LESS ? fadd2(y, less) : y;
+                        x[i] = z.x;
+                        x[i + 1] = z.y;
                     }
                     if (!whole) {
                         const uint32_t v = vis >> c0;
@@ -815,11 +830,11 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll 1
                     for (int c0 = 0; c0 < GW; c0 += 16) {
                         float x[16];
-                        scores(c0, x);
+                        scores(c0, x, std::integral_constant<int, FUSED>());
 #pragma unroll
                         for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
                     }
-                    over = bar_or(bar, 128, high > C::THR || fresh || !ok);
+                    over = bar_or(bar, 128, high >= C::THR || fresh || !ok);
                     const int par = votes & 1;
                     uint64_t* vb = &bars[C::VOTE + par * GROUPS + grp];
                     int* sv = reinterpret_cast<int*>(smem + C::vote) + par * GROUPS + grp;
@@ -838,7 +853,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll 1
                     for (int c0 = 0; c0 < GW; c0 += 16) {
                         float x[16];
-                        scores(c0, x);
+                        scores(c0, x, std::integral_constant<int, PLAIN>());
                         const float mx = reduce_columns(x, [](float a, float c) { return fmaxf(a, c); });
                         if (lane < 16) s_red[quad * ROWS + col0 + c0 + lane] = mx;
                     }
@@ -846,12 +861,10 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     const int cl = col0 + lane;
                     float up = fmaxf(fmaxf(s_red[cl], s_red[ROWS + cl]), fmaxf(s_red[2 * ROWS + cl], s_red[3 * ROWS + cl]));
                     up = fmaxf(up, swap_columns(up));
-                    // column `lane`: growth over the reference (over 0 where there was none)
+                    // column `lane`: the highest score so far and the factor that it costs
                     const float m0 = s_m[cl];
-                    const bool none = m0 == -INFINITY;
-                    const float shift = none ? (up == -INFINITY ? 0.f : up) : fmaxf(up, 0.f);
-                    const float a = none ? 1.f : fast_exp2(-shift);
-                    const float m1 = none ? up : m0 + shift;
+                    const float m1 = fmaxf(m0, up);
+                    const float a = m0 == m1 || m0 == -INFINITY ? 1.f : fast_exp2(m0 - m1);
                     fresh = __any_sync(0xffffffffu, m1 == -INFINITY);
 #pragma unroll
                     for (int i = 0; i < GW; ++i) l[i] *= __shfl_sync(0xffffffffu, a, i);
@@ -879,7 +892,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     bar_sync(bar, 128);                      // everyone has read the references
                     if (speaker) {
                         s_m[cl] = m1;
-                        s_mb[cl].y = m1 == -INFINITY ? 0.f : -m1;
+                        less_of(cl) = m1 == -INFINITY ? 0.f : -m1;
                     }
                     bar_sync(bar, 128);
                 }
@@ -891,7 +904,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll
                 for (int h = 0; h < GW / 16; ++h) {
                     float x[16];
-                    scores(16 * h, x);
+                    scores(16 * h, x, std::integral_constant<int, LESS>());
                     if (h == GW / 16 - 1) {
                         tc_fence_before_sync();
                         __syncwarp();
