@@ -649,37 +649,14 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                             *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = x[i][0];
                             *reinterpret_cast<uint4*>(line + (((c + 1) ^ (r & 7)) << 4)) = x[i][1];
                         } else {
-                            const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                                                   x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-                            float amax = 0.f;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
-                                                         fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-#pragma unroll
-                            for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                            // 2^(7 - exponent of amax): the largest element comes to [128, 256)
-                            const int E = (__float_as_uint(amax) >> 23) & 0xff;
-                            const int biased = min(7 + 2 * 127 - E, 254);
-                            const float qs = (amax > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+                            const float qs = query_scale(x[i]);
                             if (lane == 0) mult_of(half * HALF_ROWS + r) = p.scale_log2 / qs;
                             if (half != rank) continue;
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                hi[j] = lo[j] = 0u;
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const float a = __uint_as_float(w[2 * j + k] << 16) * qs;
-                                    const float c = __uint_as_float(w[2 * j + k] & 0xffff0000u) * qs;
-                                    float va, vc, ra, rc;
-                                    hi[j] |= e4m3_pair(a, c, va, vc) << (16 * k);
-                                    lo[j] |= e4m3_pair(a - va, c - vc, ra, rc) << (16 * k);
-                                }
-                            }
+                            uint4 hi, lo;
+                            split_query(x[i], qs, hi, lo);
                             uint8_t* line = smem + C::q + (lane >> 3) * C::Q_CHUNK + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                            *reinterpret_cast<uint4*>(line) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(line + C::Q_TERM) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(line) = hi;
+                            *reinterpret_cast<uint4*>(line + C::Q_TERM) = lo;
                         }
                     }
                 }

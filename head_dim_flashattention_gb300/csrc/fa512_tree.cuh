@@ -99,6 +99,43 @@ __device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi, float& vlo, fl
     return e;
 }
 
+// A query row over an E4M3 cache, 16 elements a lane (x): scaled by a power of
+// two so that its largest element comes to [128, 256), and written as the sum
+// of two E4M3 terms.  An infinity has no such form (it would saturate to a
+// finite code): it makes the scale NaN, and with it the terms and the scores.
+__device__ __forceinline__ float query_scale(const uint4 (&x)[2]) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // 2^(7 - exponent of amax)
+    const int E = (__float_as_uint(amax) >> 23) & 0xff;
+    const int biased = E == 255 ? 255 : min(7 + 2 * 127 - E, 254);
+    const uint32_t bits = static_cast<uint32_t>(biased) << 23 | (E == 255 ? 1u << 22 : 0u);
+    return amax > 0.f ? __uint_as_float(bits) : 1.f;
+}
+__device__ __forceinline__ void split_query(const uint4 (&x)[2], float scale, uint4& first, uint4& second) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        hi[j] = lo[j] = 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float a = __uint_as_float(w[2 * j + k] << 16) * scale;
+            const float c = __uint_as_float(w[2 * j + k] & 0xffff0000u) * scale;
+            float va, vc, ra, rc;
+            hi[j] |= e4m3_pair(a, c, va, vc) << (16 * k);
+            lo[j] |= e4m3_pair(a - va, c - vc, ra, rc) << (16 * k);
+        }
+    }
+    first = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    second = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
 // The keys that a row group of a sequence walks.
 template <int TILE>
 struct BandOf {

@@ -380,6 +380,8 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
  * most fa512_decode_auto_splits_tree()).  Only
  * pages that hold positions inside the band of some row are read; slots that
  * no row sees may hold anything (NaN included) without reaching the output.
+ * A row that sees a score of NaN or +infinity is NaN, as is, over an E4M3
+ * cache, a row whose query holds an infinity.
  * The same inputs give the same bits every time.  out, lse and workspace must
  * not overlap the inputs or one another; calls that may run at the same time
  * need workspaces of their own.
