@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
     const int len = p.kv_lens[b];
     if (n_new < 0 || n_new > p.q_len) {
         if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        n_new = n_new < 0 ? 0 : p.q_len;
+        n_new = 0;                                        // no telling where its tokens belong
     }
     uint4 k[APPEND_RUN][V], v[APPEND_RUN][V];
     size_t at[APPEND_RUN];

@@ -1,0 +1,26 @@
+"""Counts, layers, pages and tables at the edges of what the cache calls take."""
+import numpy as np
+import pytest
+import torch
+
+from head_dim_flashattention_gb300 import workloads
+from oracle import paged
+from test_cache_gpu import FP8, bits, fa, i32, random_pages  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+D = 512
+
+
+@FP8
+@pytest.mark.parametrize("count", [4, 1000, 2 ** 31 - 1, -1, -2 ** 31])
+def test_append_writes_nothing_for_a_count_out_of_range(fa, count, fp8):   # noqa: F811
+    """The other sequence's rows are written."""
+    k = random_pages((4, 16, 2, D), fp8, 5)
+    kn = workloads.randn_bf16((2, 3, 2, D), 97)
+    pt, lens = i32([[0, 1], [2, 3]]), [10, 12]
+    kc, vc = k.cuda(), k.cuda()
+    f = fa.fa512_cache_append_fp8 if fp8 else fa.fa512_cache_append
+    f(kn.cuda(), kn.cuda(), kc, vc, pt.cuda(), i32(lens).cuda(), q_lens=i32([count, 3]).cuda())
+    assert fa.fa512_device_status() == 6
+    want = paged.cache_append(kn, bits(k), pt, lens, i32([0, 3]), 1.0 if fp8 else None)
+    assert np.array_equal(bits(kc), want) and np.array_equal(bits(vc), want)
