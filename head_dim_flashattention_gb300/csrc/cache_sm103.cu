@@ -534,7 +534,8 @@ int compact_max_accepted() { return cache::COMPACT_MAX; }
 
 cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t stream) {
     using namespace cache;
-    const long long units = 2LL * p.n_layers * (p.row_bytes / 16);
+    // a cache without layers has new lengths all the same
+    const long long units = 2LL * (p.n_layers > 0 ? p.n_layers : 1) * (p.row_bytes / 16);
     const dim3 grid(static_cast<unsigned>((units + COMPACT_THREADS - 1) / COMPACT_THREADS), p.batch);
     compact_kernel<<<grid, COMPACT_THREADS, 0, stream>>>(p);
     return cudaGetLastError();

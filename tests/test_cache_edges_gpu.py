@@ -24,3 +24,10 @@ def test_append_writes_nothing_for_a_count_out_of_range(fa, count, fp8):   # noq
     assert fa.fa512_device_status() == 6
     want = paged.cache_append(kn, bits(k), pt, lens, i32([0, 3]), 1.0 if fp8 else None)
     assert np.array_equal(bits(kc), want) and np.array_equal(bits(vc), want)
+
+
+def test_compact_of_a_cache_without_layers(fa):                    # noqa: F811
+    k = torch.empty((0, 4, 16, 1, D), dtype=torch.bfloat16, device="cuda")
+    args = (i32([[0, 1], [2, 3]]).cuda(), i32([20, 30]).cuda(), i32([[1, 2], [0, 3]]).cuda(), i32([2, 1]).cuda())
+    new = fa.fa512_cache_compact(k, k, *args, q_len=8)
+    assert new.tolist() == [14, 23] and fa.fa512_device_status() == 0
