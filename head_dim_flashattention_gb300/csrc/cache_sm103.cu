@@ -221,7 +221,7 @@ struct PlanSmem {
     int rank[PLAN_CHUNK];                // free pages before each word of it
 };
 inline size_t plan_smem_bytes(int n_new, int batch, bool fork) {
-    return sizeof(PlanSmem) + 4 * (3 * static_cast<size_t>(n_new) + 1 + (fork ? batch : 0));
+    return sizeof(PlanSmem) + 4 * (3 * static_cast<size_t>(n_new) + 1 + (fork ? 2 * static_cast<size_t>(batch) : 0));
 }
 
 // Exclusive scan of one value per thread; *total gets the block's sum.
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
     int* s_from = s_off + p.n_new + 1;                             // fork: parent or -1; resize: pages held now
     int* s_held = s_from + p.n_new;                                // pages held by the new table
     int* s_first = s_held + p.n_new;                               // fork: first child of each parent
+    int* s_len = s_first + p.batch;                                // fork: its length; ~length: its partly filled page is none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, blocks = gridDim.x;               // the grid is one cluster
     const int gtid = rank * PLAN_THREADS + tid, all = blocks * PLAN_THREADS;
@@ -325,7 +326,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
         for (int i = done + gtid; i < p.num_pages; i += all) p.new_refs[i] = p.page_refs[i];
     }
     if constexpr (FORK) {
-        for (int i = tid; i < p.batch; i += PLAN_THREADS) s_first[i] = INT_MAX;
+        // from the last thread down: the first ones copy a small pool's counts
+        // meanwhile (4 sequences 9.5 -> 9.1 us)
+        for (int a = PLAN_THREADS - 1 - tid; a < p.batch; a += PLAN_THREADS) {
+            s_first[a] = INT_MAX;
+            int n = p.kv_lens[a];
+            n = n < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(width) * ps));
+            if (n % ps != 0) {
+                const int page = p.page_table[static_cast<size_t>(a) * width + n / ps];
+                if (page < 0 || page >= p.num_pages) n = ~n;       // recorded in B
+            }
+            s_len[a] = n;
+        }
         __syncthreads();
         for (int c = tid; c < p.n_new; c += PLAN_THREADS) {
             int a = p.parents[c];
@@ -346,10 +358,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(const PagePlanP
         if (b < p.n_new) {
             if constexpr (FORK) {
                 const int a = s_from[b];
-                int n = a >= 0 ? p.kv_lens[a] : 0;
-                s_held[b] = pages_of(n, p);
-                n = n < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(width) * ps));
-                need = n % ps != 0 && s_first[a] != b ? 1 : 0;
+                int n = a >= 0 ? s_len[a] : 0;
+                const bool copies = n >= 0 && n % ps != 0 && s_first[a] != b;
+                need = copies ? 1 : 0;
+                n = n < 0 ? ~n : n;
+                s_held[b] = static_cast<int>((static_cast<long long>(n) + ps - 1) / ps);
                 if (rank == 0) p.new_lens[b] = n;
             } else {
                 s_from[b] = pages_of(p.kv_lens[b], p);

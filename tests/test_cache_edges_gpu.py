@@ -31,3 +31,21 @@ def test_compact_of_a_cache_without_layers(fa):                    # noqa: F811
     args = (i32([[0, 1], [2, 3]]).cuda(), i32([20, 30]).cuda(), i32([[1, 2], [0, 3]]).cuda(), i32([2, 1]).cuda())
     new = fa.fa512_cache_compact(k, k, *args, q_len=8)
     assert new.tolist() == [14, 23] and fa.fa512_device_status() == 0
+
+
+@FP8
+@pytest.mark.parametrize("bad", [9, 4, -1, -2 ** 31])
+def test_fork_of_a_partly_filled_page_that_is_none(fa, bad, fp8):  # noqa: F811
+    """No child gets a page for it; the other parent's second child gets the lowest free one, and its rows."""
+    k = random_pages((2, 4, 16, 1, D), fp8, 13)
+    v = random_pages((2, 4, 16, 1, D), fp8, 14)
+    kc, vc = k.cuda(), v.cuda()
+    t, n, r = fa.fa512_cache_fork(kc, vc, i32([[3, bad], [0, -1]]).cuda(), i32([20, 3]).cuda(), i32([0, 0, 1, 1]).cuda(),
+                                  i32([1, 0, 0, 1]).cuda())
+    assert fa.fa512_device_status() == 6
+    assert t.tolist() == [[3, -1], [3, -1], [0, -1], [1, -1]] and n.tolist() == [20, 20, 3, 3]
+    assert r.tolist() == [1, 1, 0, 2]
+    for got, was in ((bits(kc), bits(k)), (bits(vc), bits(v))):
+        want = was.copy()
+        want[:, 1, :3] = was[:, 0, :3]
+        assert np.array_equal(got, want)
