@@ -492,8 +492,9 @@ fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_
  * inside [0, q_lens[b]), whose n_accepted[b] is outside
  * [0, min(max_accepted, q_lens[b])] or whose lengths are impossible is
  * recorded in the error word; it is left as it is, its new length kv_lens[b].
- * The same holds for pages outside the pool: such rows are neither read nor
- * written.  max_accepted is at most 1024.
+ * A row that would move from or to a page outside the pool is recorded too and
+ * stays where it is; the sequence's other rows move and its new length is the
+ * usual one.  max_accepted is at most 1024.
  */
 fa512_status fa512_cache_compact(void *k_pages, void *v_pages, const int32_t *page_table,
                                  const int32_t *kv_lens, const int32_t *q_lens,

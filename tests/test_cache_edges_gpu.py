@@ -49,3 +49,15 @@ def test_fork_of_a_partly_filled_page_that_is_none(fa, bad, fp8):  # noqa: F811
         want = was.copy()
         want[:, 1, :3] = was[:, 0, :3]
         assert np.array_equal(got, want)
+
+
+def test_compact_with_a_page_outside_the_pool(fa):                 # noqa: F811
+    """The rows that lie in it stay, the others move, and the length is the usual one."""
+    k = random_pages((2, 4, 16, 1, D), False, 15)
+    kc, vc = k.cuda(), k.cuda()
+    pt, lens = [[0, 77], [2, 3]], [20, 30]
+    new = fa.fa512_cache_compact(kc, vc, i32(pt).cuda(), i32(lens).cuda(), i32([[1, 2, 7], [0, 2, 3]]).cuda(), i32([3, 3]).cuda(),
+                                 q_len=8)
+    assert fa.fa512_device_status() == 6 and new.tolist() == [15, 25]
+    want, _ = paged.cache_compact(bits(k), i32([[0, 0], [2, 3]]), lens, [[1, 2, -1], [0, 2, 3]], [2, 3], 8)
+    assert np.array_equal(bits(kc), want) and np.array_equal(bits(vc), want)
