@@ -745,7 +745,9 @@ def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_l
     behind it; returns ``(new_page_table, new_page_refs)``.
 
     page_table [batch, max_pages_per_seq]; page_refs [num_pages] int32, 0 =
-    free.  The outputs may be the inputs themselves.
+    free.  The outputs may be the inputs themselves.  A sequence that is
+    shortened to inside a page that others hold must not grow there: fork it
+    into two children and end the first.
     """
     if page_table.dim() != 2 or page_refs.dim() != 1:
         raise Fa512Error(1, "page_table must be [batch, pages], page_refs [num_pages]")

@@ -449,7 +449,9 @@ size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, in
  *
  * Token t of sequence b goes to position kv_lens[b] - q_lens[b] + t; tokens
  * from q_lens[b] on are padding and are not written.  Nothing else in the
- * pages is touched.  Two positions that share a slot are the caller's error.
+ * pages is touched.  Two positions that share a slot are the caller's error;
+ * a slot of a page that several sequences hold is written for all of them (see
+ * fa512_cache_resize).
  * On the device, q_lens[b] outside [0, q_len], positions outside
  * [0, max_pages_per_seq * page_size) and page indices outside the pool are
  * recorded in the error word and their rows are not written.
@@ -521,9 +523,10 @@ fa512_status fa512_cache_compact(void *k_pages, void *v_pages, const int32_t *pa
  *
  * A sequence of n positions holds its first ceil(n / page_size) entries.
  * Child c shares the pages of parents[c].  A last page that is only partly
- * filled goes to the first child of its parent; every other child gets a free
- * page of its own with the filled rows copied, the lowest free pages in the
- * order of the children.  Table entries that a child does not hold are -1.
+ * filled goes to the first child of its parent, whoever else holds it; every
+ * other child gets a free page of its own with the filled rows copied, the
+ * lowest free pages in the order of the children.  Table entries that a child
+ * does not hold are -1.
  * The counts lose one for each entry the old sequences held and gain one for
  * each the children hold; pages whose count comes to 0 are free, also within
  * this call.  When the free pages do not suffice, the children without one
@@ -558,6 +561,12 @@ fa512_status fa512_cache_fork(void *k_pages, void *v_pages, const int32_t *page_
  * entry), with a count of 1.  All other entries behind the new length are -1.
  * Pages of a full pool, bad lengths and bad pages as fa512_cache_fork.
  * new_kv_lens 0 ends a sequence.  batch is at most 8192.
+ *
+ * The counts say how many hold a page, not which of its rows.  A sequence that
+ * is shortened to inside a page that others hold too (it was whole when a fork
+ * shared it) keeps that page, and appending to the sequence then would write
+ * over their rows.  To let it grow, fork it into two children: the second has
+ * a page of its own with its rows, and the first is ended with a length of 0.
  */
 fa512_status fa512_cache_resize(const int32_t *page_table, const int32_t *kv_lens,
                                 const int32_t *new_kv_lens, const int32_t *page_refs,

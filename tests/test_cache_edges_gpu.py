@@ -61,3 +61,32 @@ def test_compact_with_a_page_outside_the_pool(fa):                 # noqa: F811
     assert fa.fa512_device_status() == 6 and new.tolist() == [15, 25]
     want, _ = paged.cache_compact(bits(k), i32([[0, 0], [2, 3]]), lens, [[1, 2, -1], [0, 2, 3]], [2, 3], 8)
     assert np.array_equal(bits(kc), want) and np.array_equal(bits(vc), want)
+
+
+@FP8
+def test_a_sequence_shortened_into_a_shared_page_grows_on_its_own(fa, fp8):    # noqa: F811
+    """Two children share a whole page; one is cut back to inside it, forked into two, the first of them ended, and the
+    second takes new rows: the sibling's rows are as they were, and the counts agree with the tables."""
+    psz, pool, hk = 16, 12, 2
+    k = random_pages((1, pool, psz, hk, D), fp8, 16).cuda()
+    refs = torch.zeros(pool, dtype=torch.int32, device="cuda")
+    table, refs = fa.fa512_cache_resize(torch.full((1, 4), -1, dtype=torch.int32, device="cuda"), i32([0]).cuda(),
+                                        i32([40]).cuda(), refs, page_size=psz)
+    table, lens, refs = fa.fa512_cache_fork(k, k, table, i32([40]).cuda(), i32([0, 0]).cuda(), refs)
+    shorter = i32([21, 40]).cuda()                                 # inside the second page, which both hold
+    table, refs = fa.fa512_cache_resize(table, lens, shorter, refs, page_size=psz)
+    assert table[0, 1] == table[1, 1] and refs[table[0, 1]] == 2
+    table, lens, refs = fa.fa512_cache_fork(k, k, table, shorter, i32([0, 0, 1]).cuda(), refs)
+    grown = i32([0, 30, 40]).cuda()
+    table, refs = fa.fa512_cache_resize(table, lens, grown, refs, page_size=psz)
+    before = bits(k)
+    assert table[1, 1] != table[2, 1]
+    new = workloads.randn_bf16((3, 9, hk, D), 98).cuda()
+    append = fa.fa512_cache_append_fp8 if fp8 else fa.fa512_cache_append
+    append(new, new, k[0], k[0], table, grown, q_lens=i32([0, 9, 0]).cuda())
+    t, after = table.cpu().numpy(), bits(k)
+    for page in t[2, :3]:
+        assert np.array_equal(after[0, page], before[0, page])
+    mine = paged.cache_append(new.cpu(), before[0], t, [0, 30, 40], i32([0, 9, 0]), 1.0 if fp8 else None)
+    assert np.array_equal(after[0], mine) and np.array_equal(after[0, t[1, 1], :5], before[0, t[2, 1], :5])
+    assert np.array_equal(refs.cpu().numpy(), np.bincount(t[t >= 0], minlength=pool)) and fa.fa512_device_status() == 0
