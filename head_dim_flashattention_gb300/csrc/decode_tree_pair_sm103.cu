@@ -963,7 +963,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const int r = row0 + cl, t = r / G;
                 const bool some = some_key(s_low[cl], top, sum);
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
-                const size_t at = direct ? row : row * static_cast<size_t>(p.num_splits) + walk.index;
+                const size_t at = direct ? row : partial_at(p, row, cl, walk.index, blockIdx.x / 2);
                 const float unit = p.o_scale * (1.f / C::P_SCALE);
                 const float factor = !some ? 0.f : direct ? unit / sum : unit;
                 const bool real = t < p.q_len;
@@ -979,7 +979,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
             }
             if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0 && rank == 0)
-                p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
+                leave_item(p, walk.entry, walk.kvh, walk.count, walk.stride, blockIdx.x / 2);
             done = n;
         }
     }
@@ -1046,7 +1046,8 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
                             (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(units < resident ? units : resident) * 2);
+    const int most = resident < p.clusters ? resident : p.clusters;
+    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? units : most) * 2);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = Cfg<FP8>::total + 1024;
     cfg.stream = stream;

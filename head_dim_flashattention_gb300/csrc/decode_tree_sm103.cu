@@ -726,7 +726,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
             // ---- what to write: O / sum where this is the whole row, else the
             // unnormalised partial (zeros for a row that saw nothing)
             direct = walk.count == 1;
-            const size_t S = static_cast<size_t>(p.num_splits);
             if (quad == 0) {
                 float top = -INFINITY;                       // lane i: row col0 + i
 #pragma unroll
@@ -735,7 +734,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 const float sum = (s_red[cl] + s_red[ROWS + cl]) + (s_red[2 * ROWS + cl] + s_red[3 * ROWS + cl]);
                 const bool some = some_key(s_low[cl], top, sum);
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
-                const size_t at = direct ? row : row * S + walk.index;
+                const size_t at = direct ? row : partial_at(p, row, cl, walk.index, blockIdx.x);
                 const float unit = p.o_scale * (1.f / C::P_SCALE);
                 const float factor = !some ? 0.f : direct ? unit / sum : unit;
                 if (lane < GW) {
@@ -751,7 +750,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 }
             }
             if (p.num_splits > 1 && walk.index == 0 && sw == 0 && lane == 0)
-                p.ws_count[static_cast<size_t>(walk.entry) * p.n_kv_heads + walk.kvh] = walk.count;
+                leave_item(p, walk.entry, walk.kvh, walk.count, walk.stride, blockIdx.x);
             done = n;
         }
     }
@@ -788,7 +787,8 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
     if (blocks < 1) return cudaErrorLaunchOutOfResources;
     const long long units = static_cast<long long>(p.batch) * p.n_kv_heads *
                             (p.num_splits == 1 ? 1 : p.max_tiles > 1 ? p.max_tiles : 1);
-    tree_kernel<FP8, ROWS><<<static_cast<unsigned>(units < blocks ? units : blocks), Cfg<FP8, ROWS>::THREADS,
+    const int most = blocks < p.clusters ? blocks : p.clusters;
+    tree_kernel<FP8, ROWS><<<static_cast<unsigned>(units < most ? units : most), Cfg<FP8, ROWS>::THREADS,
                              Cfg<FP8, ROWS>::total + 1024, stream>>>(tmk, tmv, p);
     return cudaGetLastError();
 }
@@ -816,24 +816,25 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int h = blockIdx.x, bt = blockIdx.y;
     const int b = bt / p.q_len, t = bt - b * p.q_len;
-    const int grp = (t * p.group + h % p.group) / group_rows;
-    // an attention that ran into a timeout may not have left its counts
-    const int S = min(p.num_splits, p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group]);
+    const size_t row = static_cast<size_t>(bt) * p.n_q_heads + h;
+    const Segments segs = segments_of(p, row, b, t, h, group_rows);
+    const int S = segs.n;
     if (S <= 1) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = tid % QB, g = tid / QB;
     const int col = blockIdx.z * (D / CS) + quad * 4;
-    const size_t row = static_cast<size_t>(bt) * p.n_q_heads + h;
-    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.num_splits;
-    const float* ob = p.ws_o + row * p.num_splits * D + col;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml);
+    const float* ob = p.ws_o + segs.base * D + col;
+    const float* ob0 = p.ws_o + segs.at(g) * D + col;
+    const size_t step = static_cast<size_t>(segs.step) * D;
     float4 x[MERGE_AHEAD];
 #pragma unroll
     for (int i = 0; i < MERGE_AHEAD; ++i) {
         const int s = g + i * NG;
-        if (s < S) x[i] = *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D);
+        if (s < S) x[i] = *reinterpret_cast<const float4*>(i == 0 ? ob0 : ob + s * step);
     }
     float M = -INFINITY;
-    for (int s = tid; s < S; s += MERGE_THREADS) M = fmaxf(M, ml[s].x);
+    for (int s = tid; s < S; s += MERGE_THREADS) M = fmaxf(M, ml[segs.at(s)].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) sred[0][warp] = M;
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
     for (int w = 0; w < MERGE_THREADS / 32; ++w) M = fmaxf(M, sred[0][w]);
     float L = 0.f;
     for (int s = tid; s < S; s += MERGE_THREADS) {
-        const float2 v = ml[s];
+        const float2 v = ml[segs.at(s)];
         const float w = M == -INFINITY ? 0.f : fast_exp2(v.x - M);
         sw[s] = w;
         L = fmaf(w, v.y, L);
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
         if (g + i * NG < S) add(g + i * NG, x[i]);
 #pragma unroll 4
     for (int s = g + MERGE_AHEAD * NG; s < S; s += NG)
-        add(s, *reinterpret_cast<const float4*>(ob + static_cast<size_t>(s) * D));
+        add(s, *reinterpret_cast<const float4*>(ob + s * step));
     if (g > 0) sacc[g - 1][quad] = acc;
     __syncthreads();
     if (g > 0) return;
@@ -904,21 +905,25 @@ __global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeP
     const int h = static_cast<int>(row % p.n_q_heads);
     const size_t bt = row / p.n_q_heads;
     const int b = static_cast<int>(bt / p.q_len), t = static_cast<int>(bt - static_cast<size_t>(b) * p.q_len);
-    const int grp = (t * p.group + h % p.group) / group_rows;
-    const int S = min(p.num_splits, p.ws_count[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group]);
+    const Segments segs = segments_of(p, row, b, t, h, group_rows);
+    const int S = segs.n;
     if (S <= 1) return;
-    const float4* ob = reinterpret_cast<const float4*>(p.ws_o + row * p.num_splits * D) + lane;
     constexpr int Q = D / 128, AHEAD = 2;           // column quads of a lane; segments loaded at once
     float4 x[AHEAD][Q];
+    const float4* ob = reinterpret_cast<const float4*>(p.ws_o) + segs.at(0) * (D / 4) + lane;      // of the next segment
+    int step = (segs.step - segs.first) * (D / 4);
     auto load = [&](int s0) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
+        for (int a = 0; a < AHEAD; ++a) {
             if (s0 + a < S)
 #pragma unroll
-                for (int q = 0; q < Q; ++q) x[a][q] = ob[(s0 + a) * (D / 4) + 32 * q];
+                for (int q = 0; q < Q; ++q) x[a][q] = ob[32 * q];
+            ob += step;
+            step = segs.step * (D / 4);
+        }
     };
     load(0);
-    const float2 ml = lane < S ? reinterpret_cast<const float2*>(p.ws_ml)[row * p.num_splits + lane]
+    const float2 ml = lane < S ? reinterpret_cast<const float2*>(p.ws_ml)[segs.at(lane)]
                                : make_float2(-INFINITY, 0.f);
     float M = ml.x;
 #pragma unroll

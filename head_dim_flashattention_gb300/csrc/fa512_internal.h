@@ -62,9 +62,15 @@ struct TreeParams {
     const int32_t* kv_lens;        // [batch]
     const int32_t* q_lens;         // [batch] or null: q_len each
     const int32_t* tree_mask;      // [batch, q_len, mask_words] or null: a run of tokens
-    float* ws_o;                   // [batch, q_len, n_q_heads, num_splits, 512] unnormalised O
-    float* ws_ml;                  // [batch, q_len, n_q_heads, num_splits, 2]
-    int32_t* ws_count;             // [batch, row_groups, n_kv_heads] segments of each item
+    // Partials: unnormalised O (512 floats each) and (m, l).  Either a place per
+    // row and segment, [batch, q_len, n_q_heads, num_splits], or (slot_rows > 0)
+    // a slot of slot_rows rows for the first and for the last segment of each
+    // cluster, [clusters, 2, slot_rows]: no other of its segments is a partial.
+    float* ws_o;
+    float* ws_ml;
+    int32_t* ws_item;              // [batch, row_groups, n_kv_heads, 2] segments | cluster step << 16, first cluster
+    int slot_rows;
+    int clusters;                  // most CTAs (or pairs) of the launch
     __nv_bfloat16* out;            // [batch, q_len, n_q_heads, 512]
     float* lse;                    // [batch, q_len, n_q_heads] or null
     int batch, q_len, n_q_heads, n_kv_heads, group, mask_words;

@@ -389,6 +389,41 @@ __device__ __forceinline__ void start_walk(WalkOf<TILE>& walk, const TreeParams&
     }
 }
 
+// Place of row r (of its group; `row` of the call) of the walk's segment among
+// the partials, for cluster `me`.
+__device__ __forceinline__ size_t partial_at(const TreeParams& p, size_t row, int r, int index, int me) {
+    if (p.slot_rows == 0) return row * p.num_splits + index;
+    // an item's first segment is the last of its cluster, any other the first
+    return static_cast<size_t>((2 * me + (index == 0)) * p.slot_rows + r);
+}
+// Where the merge finds a row's segments, as an item's first one left it.
+__device__ __forceinline__ void leave_item(const TreeParams& p, int entry, int kvh, int count, int stride, int me) {
+    reinterpret_cast<int2*>(p.ws_item)[static_cast<size_t>(entry) * p.n_kv_heads + kvh] = make_int2(count | stride << 16, me);
+}
+struct Segments {
+    size_t base;                // place of segment s > 0: base + s * step; of segment 0: base + first
+    int first, step, n;
+    __device__ __forceinline__ size_t at(int s) const { return base + (s == 0 ? first : static_cast<size_t>(s) * step); }
+};
+__device__ __forceinline__ Segments segments_of(const TreeParams& p, size_t row, int b, int t, int h, int group_rows) {
+    const int kvh = h / p.group, r = t * p.group + h % p.group, grp = r / group_rows;
+    const int2 item = reinterpret_cast<const int2*>(p.ws_item)[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + kvh];
+    Segments s;
+    // an attention that ran into a timeout may not have left its items
+    s.n = min(p.num_splits, item.x & 0xffff);
+    s.first = p.slot_rows;
+    if (p.slot_rows == 0) {
+        s.base = row * p.num_splits;
+        s.step = 1;
+    } else {
+        const int stride = item.x >> 16;
+        if (item.y < 0 || stride < 1 || item.y + static_cast<long long>(s.n - 1) * stride >= p.clusters) s.n = 0;
+        s.base = static_cast<size_t>(2 * item.y) * p.slot_rows + (r - grp * group_rows);
+        s.step = 2 * stride * p.slot_rows;
+    }
+    return s;
+}
+
 // Whether a row's softmax has weight, from the row's `low` (INT_MAX: it sees
 // nothing), maximum and sum.  A NaN score is no maximum (fmaxf passes over it)
 // but makes the sum NaN, and so it has to come out.
