@@ -812,8 +812,14 @@ size_t tree_workspace(long long batch, int q_len, int n_q_heads, int n_kv_heads,
            round256(static_cast<size_t>(batch) * s.groups * n_kv_heads * 2 * sizeof(int32_t));
 }
 
+// Sizes whose products fit the kernels' counts and grids.
+bool tree_size_ok(int batch, int q_len, int group, int n_kv_heads) {
+    return batch <= 65535 && n_kv_heads <= 65535 && static_cast<long long>(q_len) * group <= 0x7fffffffLL / 1024;
+}
+
 bool tree_shape_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int n_sinks) {
     return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
+           n_q_heads / n_kv_heads <= 128 && tree_size_ok(batch, q_len, n_q_heads / n_kv_heads, n_kv_heads) &&
            max_kv_len >= 0 && n_sinks >= 0;
 }
 
@@ -846,9 +852,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     if (!(scale == scale) || isinf(scale)) return fail(FA512_ERR_INVALID_ARG, "scale is not finite");
     if (fp8 && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
-    if (batch > 65535 || n_kv_heads > 65535 ||
-        static_cast<long long>(q_len) * G > 0x7fffffffLL / 1024)
-        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (!tree_size_ok(batch, q_len, G, n_kv_heads)) return fail(FA512_ERR_UNSUPPORTED, "grid too large");
     if (batch == 0) return FA512_OK;
     if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out)
         return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
@@ -1029,8 +1033,10 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
     const fa512::TreeShape s = fa512::tree_shape(q_len, G);
     const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks, 128);
     const long long clusters = sm_count() / s.ctas > 0 ? sm_count() / s.ctas : 1;
-    const long long per = (static_cast<long long>(batch) * n_kv_heads * s.groups * tiles + clusters - 1) / clusters;
-    if (one_piece(s, tiles) || per <= 0) return 1;
+    const long long items = static_cast<long long>(batch) * n_kv_heads * s.groups;
+    if (items > 0x7fffffffLL || one_piece(s, tiles)) return 1;
+    const long long per = (items * tiles + clusters - 1) / clusters;
+    if (per <= 0) return 1;
     // the ranges of a batch of this length touch ceil(tiles / per) + 1 of an
     // item's segments at most; a batch with shorter sequences has shorter
     // ranges, so twice as many are allowed

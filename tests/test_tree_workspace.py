@@ -27,6 +27,17 @@ def test_the_size_is_bounded(shape, splits):
     assert fa.fa512_decode_workspace_bytes_tree(*shape, 0, 0, splits) <= 152 * 2 * 64 * 2056 + 8 * items + 3 * 256
 
 
+@pytest.mark.parametrize("shape", [(2, 4, 516, 4, 200), (65536, 1, 8, 4, 200), (2, 1, 65536, 65536, 200),
+                                   (2, 1 << 20, 8, 4, 1 << 21), (1, 2 ** 31 - 1, 128, 1, 200),
+                                   (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 2 ** 31 - 1)])
+def test_shapes_that_the_calls_refuse_have_no_size(shape):
+    """And one split, whatever their products overflow to."""
+    assert fa.fa512_decode_workspace_bytes_tree(*shape) == 0
+    assert fa.fa512_decode_workspace_bytes_tree(*shape, 0, 0, 7) == 0
+    assert fa.fa512_decode_auto_splits_tree(*shape) == 1
+    assert fa.fa512_decode_auto_splits_tree(4, 16383, 8388480, 65535, 2 ** 31 - 1) == 1     # accepted by itself, not with as many keys
+
+
 @pytest.mark.gpu
 @FP8
 @pytest.mark.parametrize("batch,q_len,hq,splits", [(50, 20, 8, 0), (30, 5, 8, 9), (3, 300, 8, 0), (4, 300, 8, 40), (5, 75, 32, 3),
