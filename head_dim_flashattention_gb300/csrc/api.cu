@@ -864,6 +864,9 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
         return fail(FA512_ERR_INVALID_ARG, "int32 arrays and lse must be 4-byte aligned");
     const fa512::TreeShape shape = fa512::tree_shape(q_len, G);
     const long long tiles = tree_tiles(q_len, G, max_kv_len, window, n_sinks, page_size < 128 ? page_size : 128);
+    const long long items = static_cast<long long>(batch) * shape.groups * n_kv_heads;
+    if (items > 0x7fffffffLL || items * (tiles > 1 ? tiles : 1) > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
     const int splits = num_splits > 0           ? num_splits
                        : one_piece(shape, tiles) ? 1
                                                  : fa512_decode_auto_splits_tree(batch, q_len, n_q_heads, n_kv_heads,
@@ -910,8 +913,6 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
     p.row_groups = shape.groups;
     p.max_tiles = static_cast<int>(tiles);
     p.min_range = splits > 1 ? (p.max_tiles + splits - 2) / (splits - 1) : 0;
-    if (static_cast<long long>(batch) * shape.groups * n_kv_heads * (p.max_tiles > 1 ? p.max_tiles : 1) > 0x7fffffffLL)
-        return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
     p.mask_words = (q_len + 31) / 32;
     p.page_size = page_size;
     p.num_pages = num_pages;

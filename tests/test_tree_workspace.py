@@ -77,3 +77,12 @@ def test_a_long_run_agrees_with_the_paged_prefill(splits):
         assert np.all(np.abs(o[b, :n] - want) <= 2.0 ** -7 * np.abs(want) + 2 * (2.0 ** -8 + 1e-3))
         assert np.max(np.abs(l[b, :n] - wl)) <= 2e-3
         assert np.all(o[b, n:] == 0) and np.all(np.isneginf(l[b, n:]))
+
+
+def test_more_key_tiles_than_fit_are_refused():
+    """2^15 sequences, 2^13 row groups, 2^15 KV heads and 2^21 tiles: 2^64 of them."""
+    lib = fa.load_library()
+    for tiles in (1 << 21, 1 << 20, 1):
+        status = lib.fa512_decode_paged_tree(16, 16, 16, 16, 16, None, None, 16, None, 1 << 15, 1 << 13, 1 << 22, 1 << 15, 256, 4,
+                                             1 << 21, tiles * 256, 0.05, 0, 0, 1, None, 0, None)
+        assert status == 2, tiles
