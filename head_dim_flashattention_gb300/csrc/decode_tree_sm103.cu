@@ -964,7 +964,8 @@ cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t 
     using namespace tree;
     const long long rows = static_cast<long long>(p.n_q_heads) * p.batch * p.q_len;
     const bool sliced = decode_merge_sliced(rows);
-    const bool by_warp = rows > 3 * 2 * 152 && p.num_splits <= 32;
+    const int sms = p.clusters * (p.rows == 128 ? 2 : 1);
+    const bool by_warp = rows > 3 * 2 * sms && p.num_splits <= 32;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = by_warp ? dim3(static_cast<unsigned>((rows + MERGE_ROWS - 1) / MERGE_ROWS))
