@@ -154,24 +154,6 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uns
     return mbar_try_wait_cluster(smem_u32(bar), parity) || wait_cluster_slow(bar, parity, err, abort);
 }
 
-// Reduces 16 values per lane over the warp at once: lane i gets everyone's
-// v[i % 16] (15 shuffles in which halves swap the values that the other half
-// keeps, and one that joins the warp's halves).
-template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int j = 0; j < o; ++j) {
-            const float keep = up ? v[j + o] : v[j], give = up ? v[j] : v[j + o];
-            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-        }
-    }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-}
-
 // Brings the query rows of the walk's segment into L2, a lane a token: the
 // softmax warps will ask for them when they come to it (22 runs of 46 tokens
 // with 8 heads on one KV head: 298 -> 294 us).
@@ -746,31 +728,9 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 }
                 const bool whole = bd.whole(p, v0);
                 uint32_t vis = 0xffffffffu;                  // bit i: row col0 + i sees this thread's key
-                if (!whole) {
-                    const int c = key - bd.start;
-                    if (key >= bd.hi) {
-                        vis = 0u;
-                    } else if (!p.tree_mask) {
-                        // token t sees the key iff c <= t and (t < c + window or the key is a sink):
-                        // the rows [t0 G, t1 G) of the item, here [t0 G - r0, t1 G - r0) of the group
-                        const int r0 = row0 + col0;
-                        const int t0 = max(c, 0);
-                        const bool ends = p.window > 0 && key >= bd.sink_end && c < bd.cnt - p.window;
-                        const int t1 = ends ? max(0, c + p.window) : bd.cnt;
-                        const int a = max(0, t0 * G - r0), z = min(GW, t1 * G - r0);
-                        vis = a >= z ? 0u : (0xffffffffu >> (GW - z)) & (0xffffffffu << a);
-                    } else {
-                        // the key's place; a drafted key's rows by their masks
-                        const int kp = c >= 0 ? bd.start + s_depth[c] : key;
-                        vis = c >= 0 ? s_cols[c * GROUPS + grp] : 0xffffffffu;
-                        if (p.window > 0 && kp >= bd.sink_end) {
-                            uint32_t in = 0u;
-#pragma unroll 8
-                            for (int i = 0; i < GW; ++i) in |= kp > s_low[col0 + i] ? 1u << i : 0u;
-                            vis &= in;
-                        }
-                    }
-                }
+                if (!whole)
+                    vis = rows_that_see<GW>(p, bd, key, row0 + col0, s_depth, s_low + col0,
+                                            [&](int c) { return s_cols[c * GROUPS + grp]; });
                 // Scores of 16 of the group's rows in log2 units (PLAIN) or less
                 // the rows' references.  They are read from tensor memory where they
                 // are needed, not kept: 32 scores beside the 32 row sums would spill.
@@ -898,22 +858,12 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         ok = __all_sync(0xffffffffu, got) && ok;
                     }
                     if constexpr (FP8) {
-                        uint32_t w[3][4] = {};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float a = x[2 * j] * C::P_SCALE, d = x[2 * j + 1] * C::P_SCALE;
-#pragma unroll
-                            for (int e = 0; e < 3; ++e) {
-                                float va, vd;
-                                w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
-                                a -= va;
-                                d -= vd;
-                            }
-                        }
+                        uint4 w[3];
+                        split_weights(x, C::P_SCALE, w);
                         const int piece = line_piece<C::P_LINE>(kk, (grp & 1) * (GW / 16) + h);
 #pragma unroll
                         for (int e = 0; e < 3; ++e)
-                            *reinterpret_cast<uint4*>(dst + e * term + piece) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+                            *reinterpret_cast<uint4*>(dst + e * term + piece) = w[e];
                     } else {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)

@@ -123,24 +123,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-// Reduces 16 values per lane over the warp at once: lane i gets everyone's
-// v[i % 16] (15 shuffles in which halves swap the values that the other half
-// keeps, and one that joins the warp's halves).
-template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[GW], Op op) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = GW / 2; o >= 1; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int j = 0; j < o; ++j) {
-            const float keep = up ? v[j + o] : v[j], give = up ? v[j] : v[j + o];
-            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-        }
-    }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-}
-
 template <bool FP8, int ROWS>
 __global__ void __launch_bounds__(Cfg<FP8, ROWS>::THREADS, 1)
 tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -556,30 +538,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 const bool whole = bd.whole(p, v0);
                 bool seen = true;                            // by some row of the group
                 if (!whole) {
-                    const int c = key - bd.start;
-                    uint32_t vis;                            // bit i: row col0 + i sees this thread's key
-                    if (key >= bd.hi) {
-                        vis = 0u;
-                    } else if (!p.tree_mask) {
-                        // token t sees the key iff c <= t and (t < c + window or the key is a sink):
-                        // the rows [t0 G, t1 G), here [t0 G - col0, t1 G - col0) of the group
-                        const int t0 = max(c, 0);
-                        const bool ends = p.window > 0 && key >= bd.sink_end && c < bd.cnt - p.window;
-                        const int t1 = ends ? max(0, c + p.window) : bd.cnt;
-                        const int a = max(0, t0 * G - col0), z = min(GW, t1 * G - col0);
-                        vis = a >= z ? 0u : (0xffffffffu >> (32 - z)) & (0xffffffffu << a);
-                    } else {
-                        // the key's place; a drafted key's rows by their masks
-                        const int kp = c >= 0 ? bd.start + s_depth[c] : key;
-                        vis = c >= 0 ? s_cols[c * (ROWS / 32) + (col0 >> 5)] >> (col0 & 31) : 0xffffffffu;
-                        if (p.window > 0 && kp >= bd.sink_end) {
-                            uint32_t in = 0u;
-#pragma unroll 8
-                            for (int i = 0; i < GW; ++i) in |= kp > s_low[col0 + i] ? 1u << i : 0u;
-                            vis &= in;
-                        }
-                        vis &= (1u << GW) - 1u;
-                    }
+                    // bit i: row col0 + i sees this thread's key
+                    const uint32_t vis = rows_that_see<GW>(p, bd, key, col0, s_depth, s_low + col0,
+                                                           [&](int c) { return s_cols[c * (ROWS / 32) + (col0 >> 5)] >> (col0 & 31); });
                     seen = vis != 0u;
 #pragma unroll
                     for (int i = 0; i < GW; ++i) x[i] = vis & (1u << i) ? x[i] : -INFINITY;
@@ -649,22 +610,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUt
                 }
                 uint8_t* line = smem + C::p + kk * C::P_LINE;
                 if constexpr (FP8) {
-                    uint32_t w[3][4] = {};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float a = x[2 * j] * C::P_SCALE, d = x[2 * j + 1] * C::P_SCALE;
-#pragma unroll
-                        for (int e = 0; e < 3; ++e) {
-                            float va, vd;
-                            w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
-                            a -= va;
-                            d -= vd;
-                        }
-                    }
+                    uint4 w[3];
+                    split_weights(x, C::P_SCALE, w);
                     const int piece = line_piece<C::P_LINE>(kk, grp);
 #pragma unroll
                     for (int e = 0; e < 3; ++e)
-                        *reinterpret_cast<uint4*>(line + e * C::P_TERM + piece) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+                        *reinterpret_cast<uint4*>(line + e * C::P_TERM + piece) = w[e];
                 } else {
 #pragma unroll
                     for (int c = 0; c < GW / 8; ++c)

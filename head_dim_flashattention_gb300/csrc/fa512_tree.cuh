@@ -99,6 +99,42 @@ __device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi, float& vlo, fl
     return e;
 }
 
+// 16 weights of one key as the sum of three E5M2 terms.
+__device__ __forceinline__ void split_weights(const float (&x)[16], float scale, uint4 (&term)[3]) {
+    uint32_t w[3][4] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float a = x[2 * j] * scale, d = x[2 * j + 1] * scale;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            float va, vd;
+            w[e][j >> 1] |= e5m2_pair(a, d, va, vd) << (16 * (j & 1));
+            a -= va;
+            d -= vd;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e) term[e] = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+}
+
+// Reduces 16 values per lane over the warp at once: lane i gets everyone's
+// v[i % 16] (15 shuffles in which halves swap the values that the other half
+// keeps, and one that joins the warp's halves).
+template <class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float keep = up ? v[j + o] : v[j], give = up ? v[j] : v[j + o];
+            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
 // A query row over an E4M3 cache, 16 elements a lane (x): scaled by a power of
 // two so that its largest element comes to [128, 256), and written as the sum
 // of two E4M3 terms.  An infinity has no such form (it would saturate to a
@@ -166,6 +202,36 @@ struct BandOf {
         return v0 + TILE > span && (last >= hi || (first < lo && last >= sink_end));
     }
 };
+
+// Which of GW rows (the first is row r0 of its item) see a key of the walk: bit
+// i, row r0 + i.  low: the rows' last key below the window; of_mask(c): the bits
+// of the rows whose masks name token c.
+template <int GW, int TILE, class OfMask>
+__device__ __forceinline__ uint32_t rows_that_see(const TreeParams& p, const BandOf<TILE>& d, int key, int r0, const int* depth,
+                                                  const int* low, OfMask of_mask) {
+    constexpr uint32_t ALL = 0xffffffffu >> (32 - GW);
+    const int c = key - d.start;
+    if (key >= d.hi) return 0u;
+    if (!p.tree_mask) {
+        // token t sees the key iff c <= t and (t < c + window or the key is a sink):
+        // the rows [t0 G, t1 G) of the item, here [t0 G - r0, t1 G - r0)
+        const int t0 = max(c, 0);
+        const bool ends = p.window > 0 && key >= d.sink_end && c < d.cnt - p.window;
+        const int t1 = ends ? max(0, c + p.window) : d.cnt;
+        const int a = max(0, t0 * p.group - r0), z = min(GW, t1 * p.group - r0);
+        return a >= z ? 0u : (0xffffffffu >> (32 - z)) & (0xffffffffu << a);
+    }
+    // the key's place; a drafted key's rows by their masks
+    const int kp = c >= 0 ? d.start + depth[c] : key;
+    uint32_t vis = c >= 0 ? of_mask(c) : 0xffffffffu;
+    if (p.window > 0 && kp >= d.sink_end) {
+        uint32_t in = 0u;
+#pragma unroll 8
+        for (int i = 0; i < GW; ++i) in |= kp > low[i] ? 1u << i : 0u;
+        vis &= in;
+    }
+    return vis & ALL;
+}
 
 // Band of row group `grp` (group_rows rows) of sequence b.  It follows from
 // the lengths alone: with a mask a token's place is only known to lie in
