@@ -784,8 +784,10 @@ long long tree_tiles(int q_len, int group, int max_kv_len, int window, int n_sin
 bool one_piece(const fa512::TreeShape& s, long long tiles) { return tiles <= (s.ctas == 1 ? 2 : 1); }
 
 // Partials of a call with `splits` > 1, in rows: a place for each row and
-// segment, or the first and the last segment of each cluster where that is less
-// (8 sequences of 4,096 tokens and 32 heads: 40 MB instead of 6.5 GB).
+// segment, or, where that is above 64 MB, two slots a cluster (40 MB at most; 8
+// sequences of 4,096 tokens and 32 heads would take 6.5 GB).  Small calls would
+// pay for the slots' arithmetic in the merge (47 sequences of 2 tokens 43.2 us
+// without them, 43.5 with).
 struct TreePartials {
     size_t rows;
     int slot_rows;                  // see TreeParams
@@ -800,7 +802,7 @@ TreePartials tree_partials(long long batch, int q_len, int n_q_heads, int n_kv_h
     w.rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
     w.slot_rows = static_cast<int>(in_group < s.rows ? in_group : s.rows);
     const size_t slots = 2 * static_cast<size_t>(w.clusters) * w.slot_rows;
-    if (slots < w.rows) w.rows = slots;
+    if (w.rows * (kHeadDim + 2) * sizeof(float) > (64u << 20) && slots < w.rows) w.rows = slots;
     else w.slot_rows = 0;
     return w;
 }

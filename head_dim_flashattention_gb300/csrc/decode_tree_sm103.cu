@@ -752,12 +752,14 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreePar
 // segments; every thread issues its first 16 segments' O loads before it
 // needs a weight, so the merge costs about one round trip to memory.  Rows too
 // few to give every SM a block are merged in four column slices each (CS = 4):
-// 16 rows of 131,072 positions 91 us instead of 94 with the attention.
+// 16 rows of 131,072 positions 91 us instead of 94 with the attention.  SLOTS:
+// the partials are in slots (TreeParams); a step known when the kernel is
+// compiled leaves the loads without address arithmetic (0.3 of 43 us).
 constexpr int MERGE_THREADS = 256;
 constexpr int MERGE_AHEAD = 16;
 constexpr int MAX_SPLITS = 1024;
 
-template <int CS>
+template <int CS, bool SLOTS>
 __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p, int group_rows) {
     constexpr int QB = D / 4 / CS;                  // column quads of the slice
     constexpr int NG = MERGE_THREADS / QB;          // groups of segments
@@ -768,7 +770,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
     const int h = blockIdx.x, bt = blockIdx.y;
     const int b = bt / p.q_len, t = bt - b * p.q_len;
     const size_t row = static_cast<size_t>(bt) * p.n_q_heads + h;
-    const Segments segs = segments_of(p, row, b, t, h, group_rows);
+    const Segments segs = segments_of<SLOTS>(p, row, b, t, h, group_rows);
     const int S = segs.n;
     if (S <= 1) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const TreeParams p
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml);
     const float* ob = p.ws_o + segs.base * D + col;
     const float* ob0 = p.ws_o + segs.at(g) * D + col;
-    const size_t step = static_cast<size_t>(segs.step) * D;
+    const size_t step = SLOTS ? static_cast<size_t>(segs.step) * D : D;
     float4 x[MERGE_AHEAD];
 #pragma unroll
     for (int i = 0; i < MERGE_AHEAD; ++i) {
@@ -856,7 +858,8 @@ __global__ void __launch_bounds__(MERGE_ROWS * 32) merge_rows_kernel(const TreeP
     const int h = static_cast<int>(row % p.n_q_heads);
     const size_t bt = row / p.n_q_heads;
     const int b = static_cast<int>(bt / p.q_len), t = static_cast<int>(bt - static_cast<size_t>(b) * p.q_len);
-    const Segments segs = segments_of(p, row, b, t, h, group_rows);
+    const Segments segs = p.slot_rows > 0 ? segments_of<true>(p, row, b, t, h, group_rows)
+                                            : segments_of<false>(p, row, b, t, h, group_rows);
     const int S = segs.n;
     if (S <= 1) return;
     constexpr int Q = D / 128, AHEAD = 2;           // column quads of a lane; segments loaded at once
@@ -928,9 +931,12 @@ cudaError_t launch_tree_merge(const TreeParams& p, int group_rows, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return by_warp ? cudaLaunchKernelEx(&cfg, merge_rows_kernel, p, group_rows)
-           : sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4>, p, group_rows)
-                    : cudaLaunchKernelEx(&cfg, merge_kernel<1>, p, group_rows);
+    if (by_warp) return cudaLaunchKernelEx(&cfg, merge_rows_kernel, p, group_rows);
+    if (p.slot_rows > 0)
+        return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4, true>, p, group_rows)
+                      : cudaLaunchKernelEx(&cfg, merge_kernel<1, true>, p, group_rows);
+    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4, false>, p, group_rows)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<1, false>, p, group_rows);
 }
 
 int tree_max_nodes() { return tree::MAX_NODES; }

@@ -471,21 +471,25 @@ struct Segments {
     int first, step, n;
     __device__ __forceinline__ size_t at(int s) const { return base + (s == 0 ? first : static_cast<size_t>(s) * step); }
 };
+template <bool SLOTS>
 __device__ __forceinline__ Segments segments_of(const TreeParams& p, size_t row, int b, int t, int h, int group_rows) {
-    const int kvh = h / p.group, r = t * p.group + h % p.group, grp = r / group_rows;
-    const int2 item = reinterpret_cast<const int2*>(p.ws_item)[(static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + kvh];
+    const int r = t * p.group + h % p.group, grp = r / group_rows;
+    const int32_t* item = p.ws_item + 2 * ((static_cast<size_t>(b) * p.row_groups + grp) * p.n_kv_heads + h / p.group);
     Segments s;
     // an attention that ran into a timeout may not have left its items
-    s.n = min(p.num_splits, item.x & 0xffff);
-    s.first = p.slot_rows;
-    if (p.slot_rows == 0) {
-        s.base = row * p.num_splits;
-        s.step = 1;
-    } else {
-        const int stride = item.x >> 16;
-        if (item.y < 0 || stride < 1 || item.y + static_cast<long long>(s.n - 1) * stride >= p.clusters) s.n = 0;
-        s.base = static_cast<size_t>(2 * item.y) * p.slot_rows + (r - grp * group_rows);
+    if constexpr (SLOTS) {
+        const int2 left = *reinterpret_cast<const int2*>(item);
+        const int stride = left.x >> 16;
+        s.n = min(p.num_splits, left.x & 0xffff);
+        if (left.y < 0 || stride < 1 || left.y + static_cast<long long>(s.n - 1) * stride >= p.clusters) s.n = 0;
+        s.base = static_cast<size_t>(2 * left.y) * p.slot_rows + (r - grp * group_rows);
+        s.first = p.slot_rows;
         s.step = 2 * stride * p.slot_rows;
+    } else {
+        s.n = min(p.num_splits, *item & 0xffff);
+        s.base = row * p.num_splits;
+        s.first = 0;
+        s.step = 1;
     }
     return s;
 }

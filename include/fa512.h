@@ -429,9 +429,8 @@ int fa512_decode_auto_splits_tree(int batch, int q_len, int n_q_heads, int n_kv_
 
 /* Workspace bytes of the tree calls for this shape and split count
  * (num_splits 0: the automatic choice); at least 256 for a valid shape, 0
- * for an invalid one.  Whatever the shape, not more than 2 x 64 rows of 2,056
- * bytes for each SM and 8 bytes for each (sequence, row group, KV head), with
- * less than 1 KB of rounding. */
+ * for an invalid one.  Whatever the shape, not more than 64 MB and 8 bytes for
+ * each (sequence, row group, KV head), with less than 1 KB of rounding. */
 size_t fa512_decode_workspace_bytes_tree(int batch, int q_len, int n_q_heads, int n_kv_heads,
                                          int max_kv_len, int window, int n_sinks, int num_splits);
 

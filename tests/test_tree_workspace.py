@@ -20,11 +20,11 @@ def built():
                                    (64, 64, 8, 4, 28672), (1, 65535, 128, 1, 65536), (16, 300, 128, 1, 131072)])
 @pytest.mark.parametrize("splits", [0, 2, 1024])
 def test_the_size_is_bounded(shape, splits):
-    """Two segments a CTA of 64 rows, or a pair of SMs with 128, are partials at most: 152 x 2 x 64 rows of 512 floats
-    and two; and 8 bytes for each (sequence, row group, KV head)."""
+    """64 MB of partials (above that two segments a CTA or pair: 152 x 2 x 64 rows of 512 floats and two, 40 MB), and 8
+    bytes for each (sequence, row group, KV head)."""
     batch, q_len, hq, hk, _ = shape
     items = batch * -(-q_len * (hq // hk) // 32) * hk
-    assert fa.fa512_decode_workspace_bytes_tree(*shape, 0, 0, splits) <= 152 * 2 * 64 * 2056 + 8 * items + 3 * 256
+    assert fa.fa512_decode_workspace_bytes_tree(*shape, 0, 0, splits) <= (64 << 20) + 8 * items + 3 * 256
 
 
 @pytest.mark.parametrize("shape", [(2, 4, 516, 4, 200), (65536, 1, 8, 4, 200), (2, 1, 65536, 65536, 200),
@@ -41,7 +41,7 @@ def test_shapes_that_the_calls_refuse_have_no_size(shape):
 @pytest.mark.gpu
 @FP8
 @pytest.mark.parametrize("batch,q_len,hq,splits", [(50, 20, 8, 0), (30, 5, 8, 9), (3, 300, 8, 0), (4, 300, 8, 40), (5, 75, 32, 3),
-                                                   (2, 4, 8, 5)])
+                                                   (2, 4, 8, 5), (3, 3, 8, 1024), (2, 16, 8, 1024), (1, 70, 8, 1024), (1, 4, 8, 1024)])
 def test_nothing_behind_it_is_written(batch, q_len, hq, splits, fp8):
     lens = [q_len + 37 * (i % 11) + 900 * (i % 3 == 0) for i in range(batch)]
     pc, q, s = make(lens, q_len, hq, 4, 64, 161, fp8)
