@@ -83,7 +83,9 @@ struct Cfg {
     static constexpr int P_TERM = TILE * P_LINE;
     static constexpr int P_TERMS = FP8 ? 3 : 1;
     static constexpr float THR = FP8 ? 4.f : 8.f;
-    static constexpr float P_SCALE = FP8 ? 2048.f : 1.f;
+    // E5M2 terms of small weights stay normal: the weights are 2^P_LOG times
+    // theirs, by way of the references
+    static constexpr float P_LOG = FP8 ? 11.f : 0.f, P_SCALE = FP8 ? 2048.f : 1.f;
     // shared memory, from a 1 KiB aligned base
     static constexpr int ring = 0;
     static constexpr int q = ring + NS * SLOT;
@@ -738,7 +740,8 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 // product that is not rounded before the reference is taken off
                 // would leave half its last place, for a score of 2^32 and more an
                 // exponent that overflows.  The vote may take one (FUSED): what it
-                // finds below THR, a power of two, comes to at most THR when rounded.
+                // finds below its limit is above it when rounded only where a score's
+                // last place is 2 and more, and then by less than that.
                 auto scores = [&](int c0, float (&x)[16], auto form) {
                     uint32_t raw[16];
                     tmem_ld16(s_at + static_cast<uint32_t>(c0), raw);
@@ -748,8 +751,15 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                         const float4 f = *reinterpret_cast<const float4*>(&s_mb[col0 + c0 + i]);
                         const float2 r = make_float2(__uint_as_float(raw[i]), __uint_as_float(raw[i + 1]));
                         const float2 mult = make_float2(f.x, f.y), less = make_float2(f.z, f.w);
-                        const float2 y = ffma2(r, mult, form.value == FUSED ? less : make_float2(0.f, 0.f));
-                        const float2 z = form.value == LESS ? fadd2(y, less) : y;
+                        float2 z;
+                        if constexpr (FP8 && form.value == FUSED) {
+                            // beside this kernel's conversions two FMAs are faster than a
+                            // packed one (263 -> 257 us), in bf16 slower (268 -> 270)
+                            z = make_float2(__fmaf_rn(r.x, mult.x, less.x), __fmaf_rn(r.y, mult.y, less.y));
+                        } else {
+                            z = ffma2(r, mult, form.value == FUSED ? less : make_float2(0.f, 0.f));
+                            if constexpr (form.value == LESS) z = fadd2(z, less);
+                        }
                         x[i] = z.x;
                         x[i + 1] = z.y;
                     }
@@ -771,7 +781,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
                     }
-                    over = bar_or(bar, 128, high >= C::THR || fresh || !ok);
+                    over = bar_or(bar, 128, high >= C::THR + C::P_LOG || fresh || !ok);
                     const int par = votes & 1;
                     uint64_t* vb = &bars[C::VOTE + par * GROUPS + grp];
                     int* sv = reinterpret_cast<int*>(smem + C::vote) + par * GROUPS + grp;
@@ -829,7 +839,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     bar_sync(bar, 128);                      // everyone has read the references
                     if (speaker) {
                         s_m[cl] = m1;
-                        less_of(cl) = m1 == -INFINITY ? 0.f : -m1;
+                        less_of(cl) = m1 == -INFINITY ? 0.f : C::P_LOG - m1;
                     }
                     bar_sync(bar, 128);
                 }
@@ -859,7 +869,7 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                     if constexpr (FP8) {
                         uint4 w[3];
-                        split_weights(x, C::P_SCALE, w);
+                        split_weights(x, 1.f, w);
                         const int piece = line_piece<C::P_LINE>(kk, (grp & 1) * (GW / 16) + h);
 #pragma unroll
                         for (int e = 0; e < 3; ++e)
@@ -914,17 +924,16 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                 const bool some = some_key(s_low[cl], top, sum);
                 const size_t row = (static_cast<size_t>(walk.b) * p.q_len + t) * p.n_q_heads + walk.kvh * G + (r - t * G);
                 const size_t at = direct ? row : partial_at(p, row, cl, walk.index, blockIdx.x / 2);
-                const float unit = p.o_scale * (1.f / C::P_SCALE);
-                const float factor = !some ? 0.f : direct ? unit / sum : unit;
+                const float factor = !some ? 0.f : direct ? p.o_scale / sum : p.o_scale * (1.f / C::P_SCALE);
                 const bool real = t < p.q_len;
                 *reinterpret_cast<uint4*>(smem + C::info + cl * 16) =
                     make_uint4(static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32), __float_as_uint(factor), real);
                 if (real && rank == 0) {
                     if (!direct) {
                         p.ws_ml[at * 2] = partial_max(some, top, sum);
-                        p.ws_ml[at * 2 + 1] = some ? sum : 0.f;
+                        p.ws_ml[at * 2 + 1] = some ? sum * (1.f / C::P_SCALE) : 0.f;
                     } else if (p.lse) {
-                        p.lse[row] = some ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+                        p.lse[row] = some ? (top + (log2f(sum) - C::P_LOG)) * 0.69314718055994530942f : -INFINITY;
                     }
                 }
             }
