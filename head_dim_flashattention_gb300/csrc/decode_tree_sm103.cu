@@ -31,10 +31,14 @@
 // the four warps of a column group reduce the maxima and rescale O.  The row
 // sums stay per-thread partials until the end.
 //
+// The 16-bit MMA takes P rounded to bf16 (half a step, 2^-8 of each weight);
+// the row sums take the weights as they are, so that the LSE carries none of it
+// and O is off by at most 2^-8 sum p |v| / sum p.
+//
 // FP8 E4M3 cache: the bytes are MMA operands as stored (kind::f8f6f4).  Each
 // query row is scaled by a power of two so that its largest element is in
-// [128, 256) and written as the sum of two E4M3 terms (exact for elements
-// above 2^-10 of the largest, off by at most 2^-18 of it below), and P as the
+// [128, 256) and written as the sum of two E4M3 terms (exact for elements from
+// 2^-9 of the largest upward, off by at most 2^-17 of it below), and P as the
 // sum of three E5M2 terms (relative error 2^-9, down to 2^-28 of the
 // reference), so every product keeps at least the accuracy of the bf16 path
 // without widening a byte of the cache.
