@@ -10,11 +10,10 @@
 // Tensor memory: O^T 2 x 128 columns, S^T 2 buffers x 128 columns.
 //
 // Bound: the bytes of a cache that is read once (16 caches of 20,000 to 28,672
-// positions, 128 rows: 478 us, 6.1 TB/s, 90 % of the measured copy rate).
-// Where several row groups share the keys, L2 brings them (8 sequences of up to
-// 75 tokens and 600 rows a KV head, window 4,096 and 4 sinks: 258 us, 0.47
-// PFLOP/s, 25 % of the measured rate; all of 75 tokens: 260 us, 0.63 PFLOP/s)
-// and the bound is the chain of a tile: its 64 MMAs take 2.1 us, and the MMA
+// positions, 128 rows: 476-490 us from box to box, 5.9-6.1 TB/s, 88-90 % of the
+// measured copy rate).  Where several row groups share the keys, L2 brings them (8
+// sequences of up to 75 tokens and 600 rows a KV head, window 4,096 and 4 sinks:
+// 256-269 us, 0.45-0.48 PFLOP/s, 25 % of the measured rate) and the bound is the chain of a tile: its 64 MMAs take 2.1 us, and the MMA
 // warp waits another 2.4 for loads and 0.9 for P; a change of item costs ~15 us
 // of row sums, next Q, O and first references, two or three times a pair.
 // Measured and not taken: slots of 16 KiB (355 -> 378 us: barriers and commits

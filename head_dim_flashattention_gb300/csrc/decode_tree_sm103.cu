@@ -18,12 +18,12 @@
 // shared memory at 128 bytes a cycle).  So the ring takes all shared memory
 // that Q and P leave, in slots of 32 KiB (few barriers, one elected lane that
 // issues; slots of 8 KiB left the producer the bound: 889 -> 617 us for 64
-// rows over 16 caches of 20,000 to 28,672 positions).  Measured: 64 sequences
-// of 16,384 positions in E4M3, 32 rows: 629-647 us, 6.7-6.9 TB/s, 98-101 % of
-// the measured copy rate; 16 sequences of 8,192 positions in bf16: 172 us with
-// 32 rows, 183 us with 64; one of 4,096 positions with 16 rows: 19.3 us, where
-// a bare read of its 32 MB takes ~12: start and lengths 4, Q 2, one tile's
-// products 3, O and its partials 5, the merge 4 us after one another.
+// rows over 16 caches of 20,000 to 28,672 positions).  Measured (box to box): 64
+// sequences of 16,384 positions in E4M3, 32 rows: 625-648 us, 6.7-6.9 TB/s, 98-102
+// % of the measured copy rate; 16 sequences of 8,192 positions in bf16: 172-174 us
+// with 32 rows, 183-186 us with 64; one of 4,096 positions with 16 rows: 19.3-20.1
+// us, where a bare read of its 32 MB takes ~12: start and lengths 4, Q 2, one
+// tile's products 3, O and its partials 5, the merge 4 us after one another.
 //
 // The row maxima lie across lanes here, so they are not reduced every tile:
 // each thread compares its scores with the reference its rows hold, and only

@@ -382,6 +382,11 @@ fa512_status fa512_decode_paged_noalloc(const void *q, const void *k_pages,
  * no row sees may hold anything (NaN included) without reaching the output.
  * A row that sees a score of NaN or +infinity is NaN, as is, over an E4M3
  * cache, a row whose query holds an infinity.
+ * Without a mask and sinks the older calls do the same: fa512_decode_paged_q and
+ * _fp8 (up to 16 rows) are faster for one sequence with a few tokens,
+ * fa512_prefill_paged (bf16, pages of 64 and more) from some hundred rows of a KV
+ * head on.  max_kv_len also bounds how evenly the keys are dealt out: give it as
+ * tightly as the host knows it.
  * The same inputs give the same bits every time.  out, lse and workspace must
  * not overlap the inputs or one another; calls that may run at the same time
  * need workspaces of their own.
