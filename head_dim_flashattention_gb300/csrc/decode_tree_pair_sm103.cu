@@ -102,8 +102,8 @@ struct Cfg {
     static constexpr int rows = info + ROWS * 16;        // [4 tiles][16 boxes] int: the producer's pool rows
     static constexpr int seen = rows + 4 * 16 * 4;       // [GROUPS][HALF_TILE] bytes
     static constexpr int pseen = seen + GROUPS * HALF_TILE;          // [2][HALF_TILE] int: the other CTA's keys
-    static constexpr int vote = pseen + 2 * HALF_TILE * 4;           // [2][GROUPS] int
-    static constexpr int top = vote + 2 * GROUPS * 4;                // [2][ROWS] float
+    static constexpr int vote = pseen + 2 * HALF_TILE * 4;           // [2][GROUPS][4] int: the other CTA's warps'
+    static constexpr int top = vote + 2 * GROUPS * 16;               // [2][ROWS] float
     static constexpr int scan = top + 2 * ROWS * 4;
     static constexpr int bars = scan + ((SCAN_INTS * 4 + 15) & ~15);
     static constexpr int FULL = 0, EMPTY = NS, V_RAW = 2 * NS, V_CLEAN = 3 * NS, S_FULL = 4 * NS, S_FREE = S_FULL + NB,
@@ -113,6 +113,7 @@ struct Cfg {
     static constexpr int misc = bars + N_BARS * 8;       // tmem address, abort flag
     static constexpr int total = misc + 16;
     static_assert(total + 1024 <= 232448, "shared memory of an SM");
+    static_assert(vote % 16 == 0, "votes are read four at a time");
 };
 
 __device__ __forceinline__ void mma2_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -769,7 +770,11 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
                     }
                 };
                 // ---- the vote, with the other CTA's keys; a segment's first tile
-                // sets the references in any case
+                // sets the references in any case.  Each warp sends its own, and the
+                // group's barrier comes after the answers: its four warps have to
+                // come to one decision also when the wait runs out in some of them
+                // only (a warp that took the branch alone would wait at its barriers
+                // for ever).
                 bool over = true;
                 if (t > 0) {
                     float high = -INFINITY;
@@ -780,17 +785,19 @@ tree_pair_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) high = fmaxf(high, x[i]);
                     }
-                    over = bar_or(bar, 128, high >= C::THR + C::P_LOG || fresh || !ok);
+                    const bool mine = __any_sync(0xffffffffu, high >= C::THR + C::P_LOG || fresh || !ok);
                     const int par = votes & 1;
                     uint64_t* vb = &bars[C::VOTE + par * GROUPS + grp];
-                    int* sv = reinterpret_cast<int*>(smem + C::vote) + par * GROUPS + grp;
-                    if (speaker && lane == 0) {
-                        mbar_arrive_expect_tx(vb, 4);
-                        st_async_b32(map_to_cta(smem_u32(sv), peer), over ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
+                    const uint32_t sv = smem_u32(smem + C::vote) + (par * GROUPS + grp) * 16;
+                    if (lane == 0) {
+                        if (speaker) mbar_arrive_expect_tx(vb, 16);
+                        st_async_b32(map_to_cta(sv + (sw & 3) * 4, peer), mine ? 1u : 0u, bar_of(C::VOTE + par * GROUPS + grp, peer));
                     }
                     const bool got = wait_cluster(vb, (votes >> 1) & 1, p.err, abort);
                     ok = __all_sync(0xffffffffu, got) && ok;
-                    over = over || !ok || *reinterpret_cast<volatile int*>(sv) != 0;
+                    uint32_t a0, a1, a2, a3;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3) : "r"(sv) : "memory");
+                    over = bar_or(bar, 128, mine || (a0 | a1 | a2 | a3) != 0u || !ok);
                     ++votes;
                 }
                 bool pv_waited = g == 0;
