@@ -131,3 +131,26 @@ def test_results_of_a_side_stream_outlive_their_readers_here(fa):
         junk = [torch.full_like(want, 9) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and len(junk) == 4
+
+
+@pytest.mark.parametrize("name", ["decode", "fork", "resize", "tree"])
+def test_a_side_stream_inside_a_capture(fa, name):
+    """The call's own tensors belong to the graph: replays find them, and later allocations do not."""
+    run = CALLS[name](fa)
+    want = [t.clone() for t in run()]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        junk = [torch.full_like(t, 9) for t in want for _ in range(4)]
+        for t in got:
+            t.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.all(t == 9) for t in junk)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert fa.fa512_device_status() == 0
