@@ -102,6 +102,29 @@ def load_library():
         lib.fa512_cache_fork.restype = I
         lib.fa512_cache_resize.argtypes = [P] * 6 + [I] * 4 + [P]
         lib.fa512_cache_resize.restype = I
+        lib.fa512_cache_append_fp4.argtypes = [P, P, L, L, L, L, P, P, P, P, P, F, F] + [I] * 6 + [P]
+        lib.fa512_cache_append_fp4.restype = I
+        lib.fa512_decode_paged_fp4.argtypes = [P] * 7 + [I] * 8 + [F, F, F, I, I, P, Z, P]
+        lib.fa512_decode_paged_fp4.restype = I
+        lib.fa512_decode_auto_splits_fp4.argtypes = [I] * 6
+        lib.fa512_decode_auto_splits_fp4.restype = I
+        lib.fa512_decode_workspace_bytes_fp4.argtypes = [I] * 7
+        lib.fa512_decode_workspace_bytes_fp4.restype = Z
+        lib.fa512_cache_page_bounds.argtypes = [P] * 5 + [I] * 7 + [P]
+        lib.fa512_cache_page_bounds.restype = I
+        lib.fa512_select_pages.argtypes = [P] * 5 + [I] * 11 + [P, Z, P]
+        lib.fa512_select_pages.restype = I
+        lib.fa512_select_workspace_bytes.argtypes = [I] * 4
+        lib.fa512_select_workspace_bytes.restype = Z
+        lib.fa512_decode_paged_sparse.argtypes = [P] * 8 + [I] * 9 + [F, I, P, Z, P]
+        lib.fa512_decode_paged_sparse.restype = I
+        for name in ("fa512_decode_paged_sparse_fp8", "fa512_decode_paged_sparse_fp4"):
+            getattr(lib, name).argtypes = [P] * 8 + [I] * 9 + [F, F, F, I, P, Z, P]
+            getattr(lib, name).restype = I
+        lib.fa512_decode_auto_splits_sparse.argtypes = [I] * 8
+        lib.fa512_decode_auto_splits_sparse.restype = I
+        lib.fa512_decode_workspace_bytes_sparse.argtypes = [I] * 9
+        lib.fa512_decode_workspace_bytes_sparse.restype = Z
         lib.fa512_device_status.argtypes = [P, I]
         lib.fa512_device_status.restype = I
         lib.fa512_status_string.argtypes = [I]
@@ -505,6 +528,8 @@ def _arg(t: torch.Tensor | None, name: str, dtype, dev: int, shape=None) -> int 
     raise Fa512Error(1, "%s must be %s, got %s" % (name, dtype, t.dtype))
 
 
+FP4_ROW_BYTES = 288     # row of one head in a 4-bit cache: 256 bytes of codes, 32 of scales
+_ELEMENT_FP4 = -4       # FA512_ELEMENT_FP4
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _CACHE = (torch.bfloat16,) + _E4M3
@@ -616,10 +641,11 @@ def _new_rows(t: torch.Tensor, name: str, dev: int, shape):
     return t.data_ptr(), b if shape[0] > 1 else 0, n if shape[1] > 1 else 0
 
 
-def _append(fp8, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale, stream):
-    if k_new.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2 or k_pages.shape[3] != HEAD_DIM:
-        raise Fa512Error(1, "k_new, v_new must be [batch, q_len, heads, 512], pages [n, page, heads, 512], "
-                            "page_table [batch, max_pages_per_seq]")
+def _append(bits, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale, stream):
+    row = FP4_ROW_BYTES if bits == 4 else HEAD_DIM
+    if k_new.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2 or k_pages.shape[3] != row:
+        raise Fa512Error(1, "k_new, v_new must be [batch, q_len, heads, 512], pages [n, page, heads, %d], "
+                            "page_table [batch, max_pages_per_seq]" % row)
     npages, psz, hk, _ = k_pages.shape
     bsz, mpps = page_table.shape
     qlen = k_new.shape[1]
@@ -627,16 +653,17 @@ def _append(fp8, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_
     dev = _device(k_pages, "k_pages")
     kp, kb, kt = _new_rows(k_new, "k_new", dev, shape)
     vp, vb, vt = _new_rows(v_new, "v_new", dev, shape)
-    kind = _E4M3 if fp8 else _BF16
+    kind = _BF16 if bits == 16 else _E4M3 if bits == 8 else torch.uint8
     head = (kp, vp, kb, kt, vb, vt, _arg(k_pages, "k_pages", kind, dev),
             _arg(v_pages, "v_pages", kind, dev, k_pages.shape), _arg(page_table, "page_table", _I32, dev),
             _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)), _arg(q_lens, "q_lens", _I32, dev, (bsz,)))
     tail = (bsz, qlen, hk, psz, npages, mpps, _stream(stream, dev))
     lib = _lib or load_library()
-    if fp8:
-        _check(lib.fa512_cache_append_fp8(*head, float(k_scale), float(v_scale), *tail))
-    else:
+    if bits == 16:
         _check(lib.fa512_cache_append(*head, *tail))
+    else:
+        call = lib.fa512_cache_append_fp8 if bits == 8 else lib.fa512_cache_append_fp4
+        _check(call(*head, float(k_scale), float(v_scale), *tail))
     return k_pages, v_pages
 
 
@@ -650,7 +677,7 @@ def fa512_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.
     sequence and token strides that are multiples of 8; ``kv_lens`` counts the
     new tokens, ``q_lens`` [batch] int32 says how many there are (None: q_len).
     """
-    return _append(False, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, 1.0, 1.0, stream)
+    return _append(16, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, 1.0, 1.0, stream)
 
 
 def fa512_cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
@@ -660,19 +687,33 @@ def fa512_cache_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: to
     """:func:`fa512_cache_append` into an FP8 E4M3 cache (uint8 codes or
     torch.float8_e4m3fn): x is stored as the E4M3 value nearest to x / scale,
     beyond +-448 as +-448."""
-    return _append(True, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale,
+    return _append(8, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale,
+                   stream)
+
+
+def fa512_cache_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                           v_pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, *,
+                           q_lens: torch.Tensor | None = None, k_scale: float = 1.0,
+                           v_scale: float = 1.0, stream=None):
+    """:func:`fa512_cache_append` into a cache held in 4 bits an element: pages
+    [num_pages, page_size, n_kv_heads, 288] uint8, the row of a head being 256
+    bytes of E2M1 codes (element 2 i in the low half of byte i) and 32 E4M3
+    scales of 16 elements each; an element stands for tensor scale * group
+    scale * code."""
+    return _append(4, k_new, v_new, k_pages, v_pages, page_table, kv_lens, q_lens, k_scale, v_scale,
                    stream)
 
 
 def _whole_cache(k_pages, v_pages):
     """(device, k pointer, v pointer, layers, pages, page size, heads, bytes) of a cache of one or several layers."""
-    if k_pages.dim() not in (4, 5) or k_pages.dtype is not v_pages.dtype or k_pages.shape[-1] != HEAD_DIM:
-        raise Fa512Error(1, "pages must be [(layers,) n, page, heads, 512], k_pages like v_pages")
+    fp4 = k_pages.shape[-1] == FP4_ROW_BYTES and k_pages.dtype is torch.uint8
+    if k_pages.dim() not in (4, 5) or k_pages.dtype is not v_pages.dtype or not (fp4 or k_pages.shape[-1] == HEAD_DIM):
+        raise Fa512Error(1, "pages must be [(layers,) n, page, heads, 512] (288 in 4 bits), k_pages like v_pages")
     dev = _device(k_pages, "k_pages")
     shape = k_pages.shape
     layers = shape[0] if len(shape) == 5 else 1
     return (dev, _arg(k_pages, "k_pages", _CACHE, dev), _arg(v_pages, "v_pages", _CACHE, dev, shape), layers,
-            shape[-4], shape[-3], shape[-2], k_pages.element_size())
+            shape[-4], shape[-3], shape[-2], _ELEMENT_FP4 if fp4 else k_pages.element_size())
 
 
 def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
@@ -682,7 +723,7 @@ def fa512_cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table
     """Moves the accepted drafted tokens' rows together; returns ``new_kv_lens``.
 
     k_pages / v_pages [(n_layers,) num_pages, page_size, n_kv_heads, 512], bf16
-    or E4M3, changed in place; accepted [batch, max_accepted] int32, rising,
+    or E4M3, or [..., 288] uint8 in 4 bits, changed in place; accepted [batch, max_accepted] int32, rising,
     the first n_accepted[b] of each row used; ``q_len`` drafted tokens per
     sequence (or ``q_lens`` [batch] int32, each at most q_len), which kv_lens
     counts.
@@ -766,6 +807,231 @@ def fa512_cache_resize(page_table: torch.Tensor, kv_lens: torch.Tensor, new_kv_l
         _arg(new_page_refs, "new_page_refs", _I32, dev, (npages,)), bsz, int(page_size), npages, mpps,
         _stream(stream, dev)))
     return new_page_table, new_page_refs
+
+
+def fa512_decode_auto_splits_fp4(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                 page_size: int, max_kv_len: int) -> int:
+    return int(load_library().fa512_decode_auto_splits_fp4(batch, q_len, n_q_heads, n_kv_heads,
+                                                           page_size, max_kv_len))
+
+
+def fa512_decode_workspace_bytes_fp4(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                     page_size: int, max_kv_len: int, num_splits: int = 0) -> int:
+    return int(load_library().fa512_decode_workspace_bytes_fp4(batch, q_len, n_q_heads, n_kv_heads,
+                                                               page_size, max_kv_len, num_splits))
+
+
+def fa512_decode_auto_splits_sparse(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                    element_bits: int, page_size: int, n_selected: int,
+                                    max_kv_len: int) -> int:
+    return int(load_library().fa512_decode_auto_splits_sparse(
+        batch, q_len, n_q_heads, n_kv_heads, element_bits, page_size, n_selected, max_kv_len))
+
+
+def fa512_decode_workspace_bytes_sparse(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int,
+                                        element_bits: int, page_size: int, n_selected: int,
+                                        max_kv_len: int, num_splits: int = 0) -> int:
+    return int(load_library().fa512_decode_workspace_bytes_sparse(
+        batch, q_len, n_q_heads, n_kv_heads, element_bits, page_size, n_selected, max_kv_len, num_splits))
+
+
+def _decode_bits(bits, q, k_pages, v_pages, page_table, kv_lens, selected, out, lse, k_scale, v_scale,
+                 max_kv_len, scale, window, num_splits, workspace, return_lse, stream):
+    """The decode calls over a 4-bit cache and over selected pages (``selected`` None: all)."""
+    qs, ks, ts = q.shape, k_pages.shape, page_table.shape
+    row = FP4_ROW_BYTES if bits == 4 else HEAD_DIM
+    if len(qs) not in (3, 4) or len(ks) != 4 or len(ts) != 2 or qs[-1] != HEAD_DIM or ks[3] != row:
+        raise Fa512Error(1, "q must be [batch, (q_len,) heads, 512], pages [n, page, heads, %d], page_table "
+                            "[batch, max_pages_per_seq]" % row)
+    bsz, hq, qlen = qs[0], qs[-2], qs[1] if len(qs) == 4 else 1
+    npages, psz, hk, _ = ks
+    mpps = ts[1]
+    dev = _device(q, "q")
+    rows = qs[:-1]
+    max_kv_len = mpps * psz if max_kv_len is None else int(max_kv_len)
+    window, num_splits = int(window), int(num_splits)
+    lib = _lib or load_library()
+    kind = _BF16 if bits == 16 else _E4M3 if bits == 8 else torch.uint8
+    sparse = selected is not None
+    if sparse:
+        if not isinstance(selected, torch.Tensor) or selected.dim() != 3:
+            raise Fa512Error(1, "selected must be [batch, n_kv_heads, n_selected]")
+        n_sel = selected.shape[2]
+    side = _side(stream)
+    if out is None:
+        out = _new(side, qs, _BF16, dev)
+    if lse is None and return_lse:
+        lse = _new(side, rows, _F32, dev)
+    if workspace is None:
+        # 0: a shape that the call below refuses
+        ws_bytes = (lib.fa512_decode_workspace_bytes_sparse(bsz, qlen, hq, hk, bits, psz, n_sel, max_kv_len, num_splits)
+                    if sparse else
+                    lib.fa512_decode_workspace_bytes_fp4(bsz, qlen, hq, hk, psz, max_kv_len, num_splits)) or 256
+        workspace = _new(side, ws_bytes, torch.uint8, dev, returned=False)
+        ws = workspace.data_ptr()
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _arg(workspace, "workspace", workspace.dtype, dev)
+    head = (_arg(q, "q", _BF16, dev), _arg(k_pages, "k_pages", kind, dev), _arg(v_pages, "v_pages", kind, dev, ks),
+            _arg(page_table, "page_table", _I32, dev, (bsz, mpps)), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)))
+    outs = (_arg(out, "out", _BF16, dev, qs), _arg(lse, "lse", _F32, dev, rows), bsz, qlen, hq, hk, psz, npages, mpps)
+    scales = (HEAD_DIM ** -0.5 if scale is None else float(scale),)
+    if bits != 16:
+        scales += (float(k_scale), float(v_scale))
+    tail = (num_splits, ws, ws_bytes, _stream(stream, dev))
+    if not sparse:
+        _check(lib.fa512_decode_paged_fp4(*head, *outs, max_kv_len, *scales, window, *tail))
+    else:
+        call = {16: lib.fa512_decode_paged_sparse, 8: lib.fa512_decode_paged_sparse_fp8,
+                4: lib.fa512_decode_paged_sparse_fp4}[bits]
+        _check(call(*head, _arg(selected, "selected", _I32, dev, (bsz, hk, n_sel)), *outs, n_sel, max_kv_len,
+                    *scales, *tail))
+    return out, lse
+
+
+def fa512_decode_paged_fp4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                           page_table: torch.Tensor, kv_lens: torch.Tensor,
+                           out: torch.Tensor | None = None, lse: torch.Tensor | None = None, *,
+                           k_scale: float = 1.0, v_scale: float = 1.0,
+                           max_kv_len: int | None = None, scale: float | None = None,
+                           window: int = 0, num_splits: int = 0,
+                           workspace: torch.Tensor | None = None, return_lse: bool = True,
+                           stream=None):
+    """Decode over a paged KV cache held in 4 bits; returns ``(out, lse)``.
+
+    q [batch, n_q_heads, 512] (one token) or [batch, q_len, n_q_heads, 512] bf16;
+    k_pages / v_pages [num_pages, page_size, n_kv_heads, 288] uint8 as
+    :func:`fa512_cache_append_fp4` writes them.  out / lse are shaped like q (lse
+    without the head dim).  Other arguments as :func:`fa512_decode_paged_q`.
+    """
+    return _decode_bits(4, q, k_pages, v_pages, page_table, kv_lens, None, out, lse, k_scale, v_scale, max_kv_len,
+                        scale, window, num_splits, workspace, return_lse, stream)
+
+
+def fa512_cache_page_bounds(k_pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                            bounds: torch.Tensor, *, q_len: int, q_lens: torch.Tensor | None = None,
+                            stream=None):
+    """Writes the bounds of the pages that hold each sequence's newest ``q_len``
+    (``q_lens[b]``) positions; returns ``bounds``.
+
+    k_pages [num_pages, page_size, n_kv_heads, 512] bf16 or E4M3, or [..., 288]
+    uint8 in 4 bits; bounds [num_pages, n_kv_heads, 2, 512] bf16: each channel's
+    smallest and largest key element, without the tensor scale.
+    """
+    ks = k_pages.shape
+    bits = 4 if ks[-1] == FP4_ROW_BYTES and k_pages.dtype is torch.uint8 else 8 * k_pages.element_size()
+    if len(ks) != 4 or page_table.dim() != 2 or (bits != 4 and ks[3] != HEAD_DIM):
+        raise Fa512Error(1, "k_pages must be [n, page, heads, 512] (288 in 4 bits), page_table [batch, pages]")
+    npages, psz, hk, _ = ks
+    bsz, mpps = page_table.shape
+    dev = _device(k_pages, "k_pages")
+    _check((_lib or load_library()).fa512_cache_page_bounds(
+        _arg(k_pages, "k_pages", _CACHE, dev), _arg(page_table, "page_table", _I32, dev),
+        _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)), _arg(q_lens, "q_lens", _I32, dev, (bsz,)),
+        _arg(bounds, "bounds", _BF16, dev, (npages, hk, 2, HEAD_DIM)), bsz, int(q_len), hk, bits, psz, npages, mpps,
+        _stream(stream, dev)))
+    return bounds
+
+
+def fa512_select_workspace_bytes(batch: int, n_kv_heads: int, page_size: int, max_kv_len: int) -> int:
+    return int(load_library().fa512_select_workspace_bytes(batch, n_kv_heads, page_size, max_kv_len))
+
+
+def fa512_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                       selected: torch.Tensor | None = None, *, page_size: int, n_select: int | None = None,
+                       max_kv_len: int | None = None, n_first: int = 1, n_last: int = 1,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """The pages whose bounds allow the largest products with the queries, for
+    each sequence and KV head; returns ``selected`` [batch, n_kv_heads, n_select]
+    int32: logical pages in rising order, then -1.
+
+    q [batch, n_q_heads, 512] or [batch, q_len, n_q_heads, 512] bf16; bounds
+    [num_pages, n_kv_heads, 2, 512] bf16.  The ``n_first`` first and ``n_last``
+    last pages of a sequence are always selected.  ``n_select`` is the last size
+    of ``selected`` where that is given.
+    """
+    qs, bs = q.shape, bounds.shape
+    if len(qs) not in (3, 4) or qs[-1] != HEAD_DIM or len(bs) != 4 or page_table.dim() != 2:
+        raise Fa512Error(1, "q must be [batch, (q_len,) heads, 512], bounds [n, heads, 2, 512], page_table "
+                            "[batch, max_pages_per_seq]")
+    bsz, hq, qlen = qs[0], qs[-2], qs[1] if len(qs) == 4 else 1
+    npages, hk = bs[0], bs[1]
+    mpps = page_table.shape[1]
+    dev = _device(q, "q")
+    psz = int(page_size)
+    max_kv_len = mpps * psz if max_kv_len is None else int(max_kv_len)
+    lib = _lib or load_library()
+    side = _side(stream)
+    if n_select is None:
+        if not isinstance(selected, torch.Tensor) or selected.dim() != 3:
+            raise Fa512Error(1, "n_select, or selected [batch, n_kv_heads, n_select], must be given")
+        n_select = selected.shape[2]
+    n_select = int(n_select)
+    if selected is None:
+        selected = _new(side, (bsz, hk, max(n_select, 0)), _I32, dev)
+    if workspace is None:
+        # 0: a shape that the call below refuses
+        ws_bytes = lib.fa512_select_workspace_bytes(bsz, hk, psz, max_kv_len) or 256
+        workspace = _new(side, ws_bytes, torch.uint8, dev, returned=False)
+        ws = workspace.data_ptr()
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _arg(workspace, "workspace", workspace.dtype, dev)
+    _check(lib.fa512_select_pages(
+        _arg(q, "q", _BF16, dev), _arg(bounds, "bounds", _BF16, dev, (npages, hk, 2, HEAD_DIM)),
+        _arg(page_table, "page_table", _I32, dev, (bsz, mpps)), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
+        _arg(selected, "selected", _I32, dev, (bsz, hk, max(n_select, 0))), bsz, qlen, hq, hk, psz, npages, mpps,
+        max_kv_len, n_select, int(n_first), int(n_last), ws, ws_bytes, _stream(stream, dev)))
+    return selected
+
+
+def fa512_decode_paged_sparse(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                              page_table: torch.Tensor, kv_lens: torch.Tensor, selected: torch.Tensor,
+                              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, *,
+                              max_kv_len: int | None = None, scale: float | None = None,
+                              num_splits: int = 0, workspace: torch.Tensor | None = None,
+                              return_lse: bool = True, stream=None):
+    """Decode over the selected pages of each sequence; returns ``(out, lse)``.
+
+    q [batch, n_q_heads, 512] (one token) or [batch, q_len, n_q_heads, 512] bf16;
+    ``selected`` [batch, n_kv_heads, n_selected] int32 as
+    :func:`fa512_select_pages` writes it.  Other arguments as
+    :func:`fa512_decode_paged_q`.
+    """
+    if selected is None:
+        raise Fa512Error(1, "selected must be [batch, n_kv_heads, n_selected]")
+    return _decode_bits(16, q, k_pages, v_pages, page_table, kv_lens, selected, out, lse, 1.0, 1.0, max_kv_len,
+                        scale, 0, num_splits, workspace, return_lse, stream)
+
+
+def fa512_decode_paged_sparse_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                  page_table: torch.Tensor, kv_lens: torch.Tensor, selected: torch.Tensor,
+                                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None, *,
+                                  k_scale: float = 1.0, v_scale: float = 1.0,
+                                  max_kv_len: int | None = None, scale: float | None = None,
+                                  num_splits: int = 0, workspace: torch.Tensor | None = None,
+                                  return_lse: bool = True, stream=None):
+    """:func:`fa512_decode_paged_sparse` over a cache stored in FP8 E4M3 (uint8
+    codes or torch.float8_e4m3fn)."""
+    if selected is None:
+        raise Fa512Error(1, "selected must be [batch, n_kv_heads, n_selected]")
+    return _decode_bits(8, q, k_pages, v_pages, page_table, kv_lens, selected, out, lse, k_scale, v_scale,
+                        max_kv_len, scale, 0, num_splits, workspace, return_lse, stream)
+
+
+def fa512_decode_paged_sparse_fp4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                  page_table: torch.Tensor, kv_lens: torch.Tensor, selected: torch.Tensor,
+                                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None, *,
+                                  k_scale: float = 1.0, v_scale: float = 1.0,
+                                  max_kv_len: int | None = None, scale: float | None = None,
+                                  num_splits: int = 0, workspace: torch.Tensor | None = None,
+                                  return_lse: bool = True, stream=None):
+    """:func:`fa512_decode_paged_sparse` over a cache held in 4 bits (pages
+    [num_pages, page_size, n_kv_heads, 288] uint8)."""
+    if selected is None:
+        raise Fa512Error(1, "selected must be [batch, n_kv_heads, n_selected]")
+    return _decode_bits(4, q, k_pages, v_pages, page_table, kv_lens, selected, out, lse, k_scale, v_scale,
+                        max_kv_len, scale, 0, num_splits, workspace, return_lse, stream)
 
 
 def fa512_device_status(stream=None, clear: bool = True) -> int:

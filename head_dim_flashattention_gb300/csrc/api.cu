@@ -128,8 +128,7 @@ bool pow2_page(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 ||
 
 // Tiles of the decode band (upper bound over sequences) for a host-side bound
 // on the kv length.  A window can straddle one extra tile boundary.
-long long band_tiles(int max_kv_len, int window) {
-    const int tk = fa512::decode_tile_positions();
+long long band_tiles(int max_kv_len, int window, int tk = fa512::decode_tile_positions()) {
     long long band = max_kv_len;
     if (window > 0 && window < band) band = window;
     long long t = (band + tk - 1) / tk;
@@ -190,6 +189,26 @@ int choose_splits_fp8(long long items, long long tiles, int n_sm, long long rows
             cost = (x > 1.0 ? x : 1.0) * (per + 2.0) + 0.75 * per +
                    0.2 * static_cast<double>(s > 32 ? s - 32 : 0);
         }
+        if (cost < best) {
+            best = cost;
+            best_s = s;
+        }
+    }
+    return static_cast<int>(best_s);
+}
+
+// Split count of the 4-bit kernel: items of `tiles` tiles of 64 positions, a
+// fixed number of CTAs per SM.
+int choose_splits_fp4(long long items, long long tiles, int n_sm, int rows) {
+    if (items <= 0 || tiles <= 1) return 1;
+    const double slots = static_cast<double>(fa512::decode_fp4_ctas_per_sm(rows)) * n_sm;
+    long long best_s = 1;
+    double best = 1e300;
+    const long long s_max = tiles < 128 ? tiles : 128;
+    for (long long s = 1; s <= s_max; ++s) {
+        const double per = static_cast<double>((tiles + s - 1) / s);
+        const double x = static_cast<double>(items * s) / slots;
+        const double cost = (x > 1.0 ? x : 1.0) * (per + 1.0) + 0.75 * per + 0.1 * static_cast<double>(s > 32 ? s - 32 : 0);
         if (cost < best) {
             best = cost;
             best_s = s;
@@ -567,15 +586,53 @@ size_t fa512_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, in
 
 namespace {
 
-// Body of the decode entry points.  fp8: k_pages / v_pages hold e4m3 bytes
-// and a key (value) element is k_scale (v_scale) times its e4m3 value.
+// Whether a 4-bit or sparse decode call takes these sizes.
+bool decode_size_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int num_splits) {
+    return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
+           static_cast<long long>(q_len) * (n_q_heads / n_kv_heads) <= 16 && max_kv_len >= 0 && num_splits >= 0 &&
+           num_splits <= 1024 && batch <= 65535 && static_cast<long long>(batch) * q_len <= 65535 && n_kv_heads <= 65535;
+}
+
+// Positions that a list of n_listed pages of a sequence of max_kv_len can have.
+int listed_positions(int page_size, int n_listed, int max_kv_len) {
+    const long long list = static_cast<long long>(n_listed) * page_size;
+    const long long seq = (static_cast<long long>(max_kv_len) + page_size - 1) / page_size * page_size;
+    const long long n = list < seq ? list : seq;
+    return static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
+}
+
+// Split count of a decode call over `positions` positions at most, by the bits of
+// a cached element.
+int decode_splits(int bits, int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size, int positions) {
+    if (bits == 16) return fa512_decode_auto_splits(batch, n_kv_heads, page_size, positions);
+    if (bits == 8) return fa512_decode_auto_splits_fp8(batch, q_len, n_q_heads, n_kv_heads, page_size, positions);
+    if (batch <= 0 || positions <= 0) return 1;
+    const int tile = fa512::decode_fp4_tile_positions();
+    return choose_splits_fp4(static_cast<long long>(batch) * n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile,
+                             sm_count(), q_len * (n_q_heads / n_kv_heads));
+}
+
+// What a decode call reads: the bits of a cached element (16: bf16; 8: e4m3
+// bytes; 4: rows of codes and group scales; a key element of the last two is
+// k_scale times, a value element v_scale times what is stored), and which pages.
+struct DecodeCache {
+    int bits;
+    float k_scale, v_scale;
+    bool sparse;
+    const int32_t* listed;
+    int n_listed;
+};
+
+// Body of the decode entry points.
 fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages,
                          const int32_t* page_table, const int32_t* kv_lens, void* out, float* lse,
                          int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                          int num_pages, int max_pages_per_seq, int max_kv_len, float scale,
                          int window, int num_splits, void* workspace, size_t workspace_bytes,
-                         bool fp8, float k_scale, float v_scale, fa512_stream_t stream) {
+                         const DecodeCache& cache, fa512_stream_t stream) {
     g_last_error[0] = 0;
+    const bool fp8 = cache.bits == 8, fp4 = cache.bits == 4, coded = cache.bits != 16;
+    const float k_scale = cache.k_scale, v_scale = cache.v_scale;
     if (batch < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch");
     if (q_len < 1) return fail(FA512_ERR_INVALID_ARG, "q_len must be >= 1");
     if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0)
@@ -595,21 +652,32 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
         return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
     if (num_splits < 0 || num_splits > 1024) return fail(FA512_ERR_INVALID_ARG, "num_splits outside [0, 1024]");
     if (!(scale == scale) || isinf(scale)) return fail(FA512_ERR_INVALID_ARG, "scale is not finite");
-    if (fp8 && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
+    if (coded && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
+    if (cache.sparse) {
+        if (cache.n_listed < 1) return fail(FA512_ERR_INVALID_ARG, "n_selected must be >= 1");
+        if (static_cast<long long>(cache.n_listed) * page_size > 0x7fffffffLL - 256 ||
+            static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+            return fail(FA512_ERR_UNSUPPORTED, "list of pages or page table too large for int32 positions");
+    }
+    if (fp4 && static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+        return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
+    if ((fp4 || cache.sparse) && static_cast<long long>(batch) * q_len > 65535)
+        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
     if (batch == 0) return FA512_OK;
-    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out)
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out || (cache.sparse && !cache.listed))
         return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
         return fail(FA512_ERR_INVALID_ARG, "q, pages and out must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(cache.listed) & 3u)
+        return fail(FA512_ERR_INVALID_ARG, "selected must be 4-byte aligned");
     if ((reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u) ||
         (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
         return fail(FA512_ERR_INVALID_ARG, "page_table, kv_lens and lse must be 4-byte aligned");
 
+    const int positions = cache.sparse ? listed_positions(page_size, cache.n_listed, max_kv_len) : max_kv_len;
     const int splits = num_splits > 0 ? num_splits
-                       : fp8 ? fa512_decode_auto_splits_fp8(batch, q_len, n_q_heads, n_kv_heads,
-                                                            page_size, max_kv_len)
-                             : fa512_decode_auto_splits(batch, n_kv_heads, page_size, max_kv_len);
+                                      : decode_splits(cache.bits, batch, q_len, n_q_heads, n_kv_heads, page_size, positions);
     const size_t need = workspace_for(batch * q_len, n_q_heads, splits);
     if (!workspace || workspace_bytes < need)
         return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
@@ -626,7 +694,7 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     fa512::DecodeParams p;
     memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16*>(q);
-    if (fp8) {
+    if (coded) {
         p.k8 = static_cast<const uint8_t*>(k_pages);
         p.v8 = static_cast<const uint8_t*>(v_pages);
         p.o_scale = v_scale;
@@ -648,23 +716,26 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.group = G;
     p.q_len = q_len;
     p.page_size = page_size;
-    p.box_rows = page_size < 32 ? page_size : 32;
+    const int tile = fp4 ? fa512::decode_fp4_tile_positions() : fa512::decode_tile_positions();
+    p.box_rows = page_size < tile ? page_size : tile;
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.len_cap = max_kv_len;
     p.window = window > 0 ? window : 0;
-    const long long tiles = band_tiles(max_kv_len, p.window);
+    const long long tiles = band_tiles(positions, p.window, tile);
     p.num_splits = splits;
+    p.listed = cache.sparse ? cache.listed : nullptr;
+    p.n_listed = cache.n_listed;
     p.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
     if (p.tiles_per_split < 1) p.tiles_per_split = 1;
     p.scale_log2 = scale * 1.4426950408889634f;
     // FP8: k_scale scales every score; applied after the bf16 path's factor
     // so that a power-of-two k_scale changes no rounding
-    if (fp8) p.scale_log2 *= k_scale;
+    if (coded) p.scale_log2 *= k_scale;
     p.err = err;
 
     CUtensorMap tmk, tmv;
-    const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(n_kv_heads),
+    const uint64_t dims[3] = {static_cast<uint64_t>(fp4 ? fa512::kFp4RowBytes / 4 : kHeadDim), static_cast<uint64_t>(n_kv_heads),
                               static_cast<uint64_t>(num_pages) * page_size};
     fa512_status st;
     if (fp8) {
@@ -681,6 +752,14 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
                         dims, strides, box);
         if (st != FA512_OK) return st;
         e = fa512::launch_decode_fp8(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
+    } else if (fp4) {
+        const uint64_t strides[2] = {fa512::kFp4RowBytes, static_cast<uint64_t>(n_kv_heads) * fa512::kFp4RowBytes};
+        const uint32_t box[3] = {fa512::kFp4RowBytes / 4, 1u, static_cast<uint32_t>(p.box_rows)};
+        st = encode_map(&tmk, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, k_pages, 3, dims, strides, box);
+        if (st != FA512_OK) return st;
+        st = encode_map(&tmv, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, v_pages, 3, dims, strides, box);
+        if (st != FA512_OK) return st;
+        e = fa512::launch_decode_fp4(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
     } else {
         const uint64_t strides[2] = {kHeadDim * 2ull, static_cast<uint64_t>(n_kv_heads) * kHeadDim * 2ull};
         const uint32_t box[3] = {64u, 1u, static_cast<uint32_t>(p.box_rows)};
@@ -707,7 +786,7 @@ fa512_status fa512_decode_paged_q(const void* q, const void* k_pages, const void
                                   fa512_stream_t stream) {
     return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
                        n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
-                       window, num_splits, workspace, workspace_bytes, false, 1.f, 1.f, stream);
+                       window, num_splits, workspace, workspace_bytes, {16, 1.f, 1.f, false, nullptr, 0}, stream);
 }
 
 fa512_status fa512_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -720,8 +799,95 @@ fa512_status fa512_decode_paged_fp8(const void* q, const void* k_pages, const vo
                                     fa512_stream_t stream) {
     return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
                        n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
-                       window, num_splits, workspace, workspace_bytes, true, k_scale, v_scale,
-                       stream);
+                       window, num_splits, workspace, workspace_bytes,
+                       {8, k_scale, v_scale, false, nullptr, 0}, stream);
+}
+
+fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* page_table, const int32_t* kv_lens, void* out,
+                                    float* lse, int batch, int q_len, int n_q_heads,
+                                    int n_kv_heads, int page_size, int num_pages,
+                                    int max_pages_per_seq, int max_kv_len, float scale,
+                                    float k_scale, float v_scale, int window, int num_splits,
+                                    void* workspace, size_t workspace_bytes,
+                                    fa512_stream_t stream) {
+    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
+                       n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
+                       window, num_splits, workspace, workspace_bytes,
+                       {4, k_scale, v_scale, false, nullptr, 0}, stream);
+}
+
+fa512_status fa512_decode_paged_sparse(const void* q, const void* k_pages, const void* v_pages,
+                                       const int32_t* page_table, const int32_t* kv_lens,
+                                       const int32_t* selected, void* out, float* lse, int batch, int q_len,
+                                       int n_q_heads, int n_kv_heads, int page_size, int num_pages,
+                                       int max_pages_per_seq, int n_selected, int max_kv_len, float scale,
+                                       int num_splits, void* workspace, size_t workspace_bytes,
+                                       fa512_stream_t stream) {
+    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
+                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
+                       workspace_bytes, {16, 1.f, 1.f, true, selected, n_selected}, stream);
+}
+
+fa512_status fa512_decode_paged_sparse_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, const int32_t* kv_lens,
+                                           const int32_t* selected, void* out, float* lse, int batch,
+                                           int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                           int num_pages, int max_pages_per_seq, int n_selected,
+                                           int max_kv_len, float scale, float k_scale, float v_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           fa512_stream_t stream) {
+    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
+                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
+                       workspace_bytes, {8, k_scale, v_scale, true, selected, n_selected}, stream);
+}
+
+fa512_status fa512_decode_paged_sparse_fp4(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, const int32_t* kv_lens,
+                                           const int32_t* selected, void* out, float* lse, int batch,
+                                           int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                           int num_pages, int max_pages_per_seq, int n_selected,
+                                           int max_kv_len, float scale, float k_scale, float v_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           fa512_stream_t stream) {
+    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
+                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
+                       workspace_bytes, {4, k_scale, v_scale, true, selected, n_selected}, stream);
+}
+
+int fa512_decode_auto_splits_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                 int max_kv_len) {
+    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0)) return 1;
+    return decode_splits(4, batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len);
+}
+
+size_t fa512_decode_workspace_bytes_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                        int max_kv_len, int num_splits) {
+    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits)) return 0;
+    return workspace_for(batch * q_len, n_q_heads,
+                         num_splits > 0 ? num_splits
+                                        : decode_splits(4, batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len));
+}
+
+int fa512_decode_auto_splits_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads, int element_bits,
+                                    int page_size, int n_selected, int max_kv_len) {
+    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0) || !pow2_page(page_size) ||
+        n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
+        return 1;
+    return decode_splits(element_bits, batch, q_len, n_q_heads, n_kv_heads, page_size,
+                         listed_positions(page_size, n_selected, max_kv_len));
+}
+
+size_t fa512_decode_workspace_bytes_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                           int element_bits, int page_size, int n_selected, int max_kv_len,
+                                           int num_splits) {
+    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits) || !pow2_page(page_size) ||
+        n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
+        return 0;
+    const int s = num_splits > 0 ? num_splits
+                                 : fa512_decode_auto_splits_sparse(batch, q_len, n_q_heads, n_kv_heads, element_bits,
+                                                                   page_size, n_selected, max_kv_len);
+    return workspace_for(batch * q_len, n_q_heads, s);
 }
 
 fa512_status fa512_decode_paged(const void* q, const void* k_pages, const void* v_pages,
@@ -946,7 +1112,7 @@ fa512_status tree_call(const void* q, const void* k_pages, const void* v_pages, 
 fa512_status append_call(const void* k_new, const void* v_new, int64_t kb, int64_t kt, int64_t vb, int64_t vt,
                          void* k_pages, void* v_pages, const int32_t* page_table, const int32_t* kv_lens,
                          const int32_t* q_lens, int batch, int q_len, int n_kv_heads, int page_size,
-                         int num_pages, int max_pages_per_seq, bool fp8, float k_scale, float v_scale,
+                         int num_pages, int max_pages_per_seq, int bits, float k_scale, float v_scale,
                          fa512_stream_t stream) {
     g_last_error[0] = 0;
     if (batch < 0 || q_len < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch or q_len");
@@ -958,7 +1124,7 @@ fa512_status append_call(const void* k_new, const void* v_new, int64_t kb, int64
         return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
     if ((kb | kt | vb | vt) & 7)
         return fail(FA512_ERR_INVALID_ARG, "strides of k_new and v_new must be multiples of 8 elements");
-    if (fp8 && (!(k_scale > 0.f) || isinf(k_scale) || !(v_scale > 0.f) || isinf(v_scale)))
+    if (bits != 16 && (!(k_scale > 0.f) || isinf(k_scale) || !(v_scale > 0.f) || isinf(v_scale)))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite and above 0");
     if (batch > 65535 || static_cast<long long>(q_len) * n_kv_heads > 0x7fffffffLL / 64)
         return fail(FA512_ERR_UNSUPPORTED, "grid too large");
@@ -995,7 +1161,7 @@ fa512_status append_call(const void* k_new, const void* v_new, int64_t kb, int64
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.err = err;
-    e = fa512::launch_cache_append(p, fp8, reinterpret_cast<cudaStream_t>(stream));
+    e = fa512::launch_cache_append(p, bits, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
     return FA512_OK;
 }
@@ -1005,8 +1171,8 @@ fa512_status cache_shape(int n_layers, int batch, int n_kv_heads, int element_by
                          int num_pages, int max_pages_per_seq) {
     if (batch < 0 || n_layers < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch or n_layers");
     if (n_kv_heads < 1 || n_kv_heads > 65535) return fail(FA512_ERR_INVALID_ARG, "n_kv_heads outside [1, 65535]");
-    if (element_bytes != 1 && element_bytes != 2)
-        return fail(FA512_ERR_INVALID_ARG, "element_bytes must be 1 (E4M3) or 2 (bf16)");
+    if (element_bytes != 1 && element_bytes != 2 && element_bytes != FA512_ELEMENT_FP4)
+        return fail(FA512_ERR_INVALID_ARG, "element_bytes must be 1 (E4M3), 2 (bf16) or FA512_ELEMENT_FP4");
     if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
     if (num_pages < 1 || max_pages_per_seq < 1)
         return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
@@ -1015,6 +1181,11 @@ fa512_status cache_shape(int n_layers, int batch, int n_kv_heads, int element_by
         return fail(FA512_ERR_UNSUPPORTED, "page pool or page table too large for int32 rows");
     if (n_layers > 32767) return fail(FA512_ERR_UNSUPPORTED, "more than 32767 layers");
     return FA512_OK;
+}
+
+// Bytes of a cached position's row, all KV heads.
+int cache_row_bytes(int n_kv_heads, int element_bytes) {
+    return n_kv_heads * (element_bytes == FA512_ELEMENT_FP4 ? fa512::kFp4RowBytes : kHeadDim * element_bytes);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -1092,7 +1263,7 @@ fa512_status fa512_cache_append(const void* k_new, const void* v_new, int64_t k_
                                 fa512_stream_t stream) {
     return append_call(k_new, v_new, k_batch_stride, k_token_stride, v_batch_stride, v_token_stride, k_pages,
                        v_pages, page_table, kv_lens, q_lens, batch, q_len, n_kv_heads, page_size, num_pages,
-                       max_pages_per_seq, false, 1.f, 1.f, stream);
+                       max_pages_per_seq, 16, 1.f, 1.f, stream);
 }
 
 fa512_status fa512_cache_append_fp8(const void* k_new, const void* v_new, int64_t k_batch_stride,
@@ -1103,7 +1274,133 @@ fa512_status fa512_cache_append_fp8(const void* k_new, const void* v_new, int64_
                                     int num_pages, int max_pages_per_seq, fa512_stream_t stream) {
     return append_call(k_new, v_new, k_batch_stride, k_token_stride, v_batch_stride, v_token_stride, k_pages,
                        v_pages, page_table, kv_lens, q_lens, batch, q_len, n_kv_heads, page_size, num_pages,
-                       max_pages_per_seq, true, k_scale, v_scale, stream);
+                       max_pages_per_seq, 8, k_scale, v_scale, stream);
+}
+
+fa512_status fa512_cache_append_fp4(const void* k_new, const void* v_new, int64_t k_batch_stride,
+                                    int64_t k_token_stride, int64_t v_batch_stride, int64_t v_token_stride,
+                                    void* k_pages, void* v_pages, const int32_t* page_table,
+                                    const int32_t* kv_lens, const int32_t* q_lens, float k_scale,
+                                    float v_scale, int batch, int q_len, int n_kv_heads, int page_size,
+                                    int num_pages, int max_pages_per_seq, fa512_stream_t stream) {
+    return append_call(k_new, v_new, k_batch_stride, k_token_stride, v_batch_stride, v_token_stride, k_pages,
+                       v_pages, page_table, kv_lens, q_lens, batch, q_len, n_kv_heads, page_size, num_pages,
+                       max_pages_per_seq, 4, k_scale, v_scale, stream);
+}
+
+fa512_status fa512_cache_page_bounds(const void* k_pages, const int32_t* page_table, const int32_t* kv_lens,
+                                     const int32_t* q_lens, void* bounds, int batch, int q_len, int n_kv_heads,
+                                     int element_bits, int page_size, int num_pages, int max_pages_per_seq,
+                                     fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    if (batch < 0 || q_len < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch or q_len");
+    if (n_kv_heads < 1) return fail(FA512_ERR_INVALID_ARG, "n_kv_heads must be >= 1");
+    if (element_bits != 16 && element_bits != 8 && element_bits != 4)
+        return fail(FA512_ERR_INVALID_ARG, "element_bits must be 16 (bf16), 8 (E4M3) or 4 (E2M1)");
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
+    if (batch > 65535 || n_kv_heads > 65535) return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0 || q_len == 0) return FA512_OK;
+    if (!k_pages || !page_table || !kv_lens || !bounds) return fail(FA512_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k_pages) || !aligned16(bounds))
+        return fail(FA512_ERR_INVALID_ARG, "pages and bounds must be 16-byte aligned");
+    if (misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(q_lens))
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::BoundsParams p;
+    memset(&p, 0, sizeof p);
+    p.k_pages = static_cast<const uint8_t*>(k_pages);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.bounds = static_cast<__nv_bfloat16*>(bounds);
+    p.batch = batch;
+    p.q_len = q_len;
+    p.n_kv_heads = n_kv_heads;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.err = err;
+    e = fa512::launch_page_bounds(p, element_bits, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "page bounds launch");
+    return FA512_OK;
+}
+
+size_t fa512_select_workspace_bytes(int batch, int n_kv_heads, int page_size, int max_kv_len) {
+    if (batch < 0 || n_kv_heads < 1 || !pow2_page(page_size) || max_kv_len < 0) return 0;
+    const size_t pages = (static_cast<size_t>(max_kv_len) + page_size - 1) / page_size;
+    const size_t n = round256(static_cast<size_t>(batch) * n_kv_heads * pages * 4);
+    return n ? n : 256;
+}
+
+fa512_status fa512_select_pages(const void* q, const void* bounds, const int32_t* page_table,
+                                const int32_t* kv_lens, int32_t* selected, int batch, int q_len, int n_q_heads,
+                                int n_kv_heads, int page_size, int num_pages, int max_pages_per_seq,
+                                int max_kv_len, int n_select, int n_first, int n_last, void* workspace,
+                                size_t workspace_bytes, fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    if (batch < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch");
+    if (q_len < 1) return fail(FA512_ERR_INVALID_ARG, "q_len must be >= 1");
+    if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0)
+        return fail(FA512_ERR_INVALID_ARG, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)",
+                    n_q_heads, n_kv_heads);
+    const int G = n_q_heads / n_kv_heads;
+    if (static_cast<long long>(q_len) * G > 16)
+        return fail(FA512_ERR_UNSUPPORTED, "q_len x query heads per KV head (%d x %d) must be at most 16", q_len, G);
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+        return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
+    if (max_kv_len < 0 || static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages_per_seq) * page_size)
+        return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
+    if (n_first < 0 || n_last < 0 || n_select < 1 || static_cast<long long>(n_first) + n_last > n_select)
+        return fail(FA512_ERR_INVALID_ARG, "n_select must be >= 1 and n_first + n_last at most that, neither negative");
+    if (batch > 65535 || n_kv_heads > 65535) return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0) return FA512_OK;
+    if (!q || !bounds || !page_table || !kv_lens || !selected) return fail(FA512_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q) || !aligned16(bounds))
+        return fail(FA512_ERR_INVALID_ARG, "q and bounds must be 16-byte aligned");
+    if (misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(selected))
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    const size_t need = fa512_select_workspace_bytes(batch, n_kv_heads, page_size, max_kv_len);
+    if (!workspace || workspace_bytes < need)
+        return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(FA512_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::SelectParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.bounds = static_cast<const __nv_bfloat16*>(bounds);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.selected = selected;
+    p.keys = static_cast<uint32_t*>(workspace);
+    p.batch = batch;
+    p.q_len = q_len;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = G;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.len_cap = max_kv_len;
+    p.max_pages = (max_kv_len + page_size - 1) / page_size;
+    p.n_select = n_select;
+    p.n_first = n_first;
+    p.n_last = n_last;
+    p.err = err;
+    e = fa512::launch_select_pages(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "select pages launch");
+    return FA512_OK;
 }
 
 fa512_status fa512_cache_compact(void* k_pages, void* v_pages, const int32_t* page_table,
@@ -1150,7 +1447,7 @@ fa512_status fa512_cache_compact(void* k_pages, void* v_pages, const int32_t* pa
     p.batch = batch;
     p.q_len = q_len;
     p.max_accepted = max_accepted;
-    p.row_bytes = n_kv_heads * kHeadDim * element_bytes;
+    p.row_bytes = cache_row_bytes(n_kv_heads, element_bytes);
     p.page_size = page_size;
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
@@ -1213,7 +1510,7 @@ fa512_status fa512_cache_fork(void* k_pages, void* v_pages, const int32_t* page_
     p.k_pages = static_cast<uint8_t*>(k_pages);
     p.v_pages = static_cast<uint8_t*>(v_pages);
     p.n_layers = n_layers;
-    p.row_bytes = n_kv_heads * kHeadDim * element_bytes;
+    p.row_bytes = cache_row_bytes(n_kv_heads, element_bytes);
     p.err = err;
     e = fa512::launch_page_plan(p, true, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache fork launch");

@@ -117,6 +117,106 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
     }
 }
 
+// ----------------------------------------------------------- append, 4 bits
+//
+// A row of a head is 288 bytes: 256 bytes of E2M1 codes (element 2 i in the
+// low half of byte i), then 32 E4M3 scales, one for 16 elements.  With y = x /
+// tensor scale (the nearest fp32 quotient) a group's scale is the E4M3 value
+// nearest to max |y| / 6, and a code the E2M1 value nearest to the fp32
+// quotient y / scale, ties to even; both saturate.  A group that holds NaN gets
+// the NaN scale; a scale that rounds to 0 makes the codes 0.
+//
+// A warp rounds one row, a group of 16 elements a lane, up to APPEND_RUN rows
+// with all loads first.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+    return r;
+}
+
+// 16 bf16 elements -> codes and the scale byte
+__device__ __forceinline__ uint2 to_4bit(const uint4 a, const uint4 b, float tensor_scale, uint8_t* scale_byte) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float y[16], most = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[2 * i] = __fdiv_rn(__uint_as_float(w[i] << 16), tensor_scale);
+        y[2 * i + 1] = __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), tensor_scale);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        most = fmaxf(most, fabsf(y[i]));
+        nan |= y[i] != y[i];
+    }
+    uint16_t s8;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fdiv_rn(most, 6.f)));
+    uint32_t s2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(s8));
+    float s;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"(static_cast<unsigned short>(s2 & 0xffffu)));
+    float z[2][8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i >> 3][i & 7] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
+    *scale_byte = nan ? 0x7f : static_cast<uint8_t>(s8 & 0xff);
+    return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+}
+
+__global__ void __launch_bounds__(APPEND_THREADS) append_fp4_kernel(const AppendParams p) {
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
+    int n_new = p.q_lens ? p.q_lens[b] : p.q_len;
+    const int len = p.kv_lens[b];
+    if (n_new < 0 || n_new > p.q_len) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        n_new = 0;
+    }
+    uint4 k[APPEND_RUN][2], v[APPEND_RUN][2];
+    size_t at[APPEND_RUN];
+    bool there[APPEND_RUN];
+#pragma unroll
+    for (int r = 0; r < APPEND_RUN; ++r) {
+        const unsigned row = (blockIdx.x * APPEND_RUN + r) * (APPEND_THREADS / 32) + (threadIdx.x >> 5);
+        const int t = static_cast<int>(row / static_cast<unsigned>(p.n_kv_heads));
+        const int h = static_cast<int>(row % static_cast<unsigned>(p.n_kv_heads));
+        const long long pos = static_cast<long long>(len) - n_new + t;
+        there[r] = t < n_new;
+        if (there[r] && (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size)) {
+            if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            there[r] = false;
+        }
+        if (!there[r]) continue;
+        const int lp = static_cast<int>(pos) / p.page_size;
+        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
+        const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + b * p.k_batch_stride + t * p.k_token_stride) + h * 64 + 2 * lane;
+        const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + b * p.v_batch_stride + t * p.v_token_stride) + h * 64 + 2 * lane;
+        k[r][0] = ks[0];
+        k[r][1] = ks[1];
+        v[r][0] = vs[0];
+        v[r][1] = vs[1];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            there[r] = false;
+        }
+        at[r] = ((static_cast<size_t>(page) * p.page_size + static_cast<int>(pos) % p.page_size) * p.n_kv_heads + h) *
+                kFp4RowBytes;
+    }
+#pragma unroll
+    for (int r = 0; r < APPEND_RUN; ++r) {
+        if (!there[r]) continue;
+        uint8_t *kd = static_cast<uint8_t*>(p.k_pages) + at[r], *vd = static_cast<uint8_t*>(p.v_pages) + at[r];
+        uint8_t s;
+        *reinterpret_cast<uint2*>(kd + 8 * lane) = to_4bit(k[r][0], k[r][1], p.k_scale, &s);
+        kd[256 + lane] = s;
+        *reinterpret_cast<uint2*>(vd + 8 * lane) = to_4bit(v[r][0], v[r][1], p.v_scale, &s);
+        vd[256 + lane] = s;
+    }
+}
+
 // ------------------------------------------------------------------ compact
 //
 // accepted[i] >= i, rising: a row only ever moves down.  A thread owns one
@@ -520,8 +620,16 @@ __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const PagePlanP
 
 }  // namespace cache
 
-cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t stream) {
+cudaError_t launch_cache_append(const AppendParams& p, int element_bits, cudaStream_t stream) {
     using namespace cache;
+    if (element_bits == 4) {
+        const long long rows = static_cast<long long>(p.q_len) * p.n_kv_heads;
+        constexpr int ROWS = APPEND_THREADS / 32 * APPEND_RUN;
+        const dim3 grid(static_cast<unsigned>((rows + ROWS - 1) / ROWS), p.batch);
+        append_fp4_kernel<<<grid, APPEND_THREADS, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    const bool fp8 = element_bits == 8;
     const long long units = static_cast<long long>(p.q_len) * p.n_kv_heads * (fp8 ? D / 16 : D / 8);
     constexpr int BLOCK = APPEND_THREADS * APPEND_RUN;
     const dim3 grid(static_cast<unsigned>((units + BLOCK - 1) / BLOCK), p.batch);

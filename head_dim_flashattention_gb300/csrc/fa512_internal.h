@@ -33,6 +33,11 @@ struct DecodeParams {
     int tiles_per_split, num_splits;
     float scale_log2;              // scale * log2(e)
     unsigned* err;                 // device error word
+    // Selected pages (null: all of the band): [batch, n_kv_heads, n_listed] logical
+    // pages in rising order, then -1.  Positions are then counted along the list:
+    // position v is slot v % page_size of entry v / page_size.
+    const int32_t* listed;
+    int n_listed;
 };
 
 int decode_smem_bytes();
@@ -52,6 +57,41 @@ int decode_fp8_ctas_per_sm();
 bool decode_merge_sliced(long long rows);
 cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const DecodeParams& p, cudaStream_t stream);
+// Combines the split partials of a kernel that has allowed a dependent launch.
+cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
+
+// 4-bit cache: tmk / tmv map rows of kFp4RowBytes as 32-bit words, boxes of a
+// whole row x box_rows positions (min(page_size, decode_fp4_tile_positions())),
+// no swizzle; k8 / v8 are unused.
+constexpr int kFp4RowBytes = 288;  // 256 bytes of E2M1 pairs, 32 E4M3 scales
+int decode_fp4_tile_positions();
+int decode_fp4_ctas_per_sm(int rows);   // rows of a KV head
+cudaError_t launch_decode_fp4(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
+                              cudaStream_t stream);
+
+// Bounds of a page's keys, and the pages whose bounds allow the largest products.
+struct BoundsParams {
+    const uint8_t* k_pages;        // rows of one head: 1024, 512 or kFp4RowBytes bytes
+    const int32_t *page_table, *kv_lens, *q_lens;
+    __nv_bfloat16* bounds;         // [num_pages, n_kv_heads, 2, 512] smallest, largest
+    int batch, q_len, n_kv_heads, page_size, num_pages, max_pages_per_seq;
+    unsigned* err;
+};
+cudaError_t launch_page_bounds(const BoundsParams& p, int element_bits, cudaStream_t stream);
+
+struct SelectParams {
+    const __nv_bfloat16* q;        // [batch, q_len, n_q_heads, 512]
+    const __nv_bfloat16* bounds;
+    const int32_t *page_table, *kv_lens;
+    int32_t* selected;             // [batch, n_kv_heads, n_select]
+    uint32_t* keys;                // [batch, n_kv_heads, max_pages] ordered like the scores
+    int batch, q_len, n_q_heads, n_kv_heads, group;
+    int page_size, num_pages, max_pages_per_seq, len_cap;
+    int max_pages;                 // pages of len_cap
+    int n_select, n_first, n_last;
+    unsigned* err;
+};
+cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream);
 
 // Drafted tokens (a tree or a run of them) over a paged cache.
 struct TreeParams {
@@ -102,11 +142,12 @@ struct AppendParams {
     long long k_batch_stride, k_token_stride, v_batch_stride, v_token_stride;   // elements
     void *k_pages, *v_pages;
     const int32_t *page_table, *kv_lens, *q_lens;
-    float k_scale, v_scale;        // E4M3 cache
+    float k_scale, v_scale;        // E4M3 and 4-bit caches
     int batch, q_len, n_kv_heads, page_size, num_pages, max_pages_per_seq;
     unsigned* err;
 };
-cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t stream);
+// element_bits: 16 (bf16), 8 (E4M3) or 4 (E2M1 with group scales)
+cudaError_t launch_cache_append(const AppendParams& p, int element_bits, cudaStream_t stream);
 
 struct CompactParams {
     uint8_t *k_pages, *v_pages;    // rows of row_bytes (all KV heads of a position)

@@ -43,6 +43,13 @@
  *    the cache they were just appended to; with a window, the first n_sinks
  *    positions can stay visible.
  *
+ *  fa512_decode_paged_fp4 -- the decode calls over a cache held in 4 bits an
+ *    element, filled by fa512_cache_append_fp4.
+ *
+ *  fa512_cache_page_bounds, fa512_select_pages, fa512_decode_paged_sparse,
+ *    _sparse_fp8, _sparse_fp4 -- a decode step that reads only the pages whose
+ *    keys can have large products with the queries.
+ *
  *  fa512_cache_append, _append_fp8, _compact, _fork, _resize -- the cache
  *    around those calls: writing new rows, moving accepted rows together,
  *    sharing and copying pages between sequences, handing out and taking back
@@ -482,11 +489,203 @@ fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_
                                     int num_pages, int max_pages_per_seq, fa512_stream_t stream);
 
 /*
+ * fa512_cache_append_fp4 -- the same into a cache held in 4 bits an element.
+ *
+ *   k_pages, v_pages [num_pages, page_size, n_kv_heads, FA512_FP4_ROW_BYTES]
+ *                uint8, device.  The row of a head at a position is 256 bytes of
+ *                E2M1 codes, element 2 i in the low half of byte i and element
+ *                2 i + 1 in the high half, then 32 E4M3 scales, the one in byte
+ *                256 + j for elements 16 j .. 16 j + 15.  An E2M1 code is a sign
+ *                bit and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 in the order of its
+ *                three lower bits.  Key element = k_scale * scale * code, value
+ *                element = v_scale * scale * code.
+ *
+ * With y = x / k_scale (x / v_scale), the nearest fp32 quotient, the scale of a
+ * group is the E4M3 value nearest to max |y| / 6 and a code the E2M1 value
+ * nearest to the fp32 quotient y / scale; ties to even, beyond the largest value
+ * the largest value.  A group whose scale rounds to 0 (max |y| up to 6 * 2^-10)
+ * gets codes 0.  A group that holds a NaN gets the NaN scale: all its elements
+ * read as NaN.  k_scale and v_scale are finite and above 0; a power of two is
+ * faster, and the choice only matters for what lies outside the scales' range.
+ * Other arguments and errors as fa512_cache_append.
+ */
+#define FA512_FP4_ROW_BYTES 288
+
+fa512_status fa512_cache_append_fp4(const void* k_new, const void* v_new, int64_t k_batch_stride,
+                                    int64_t k_token_stride, int64_t v_batch_stride,
+                                    int64_t v_token_stride, void* k_pages, void* v_pages,
+                                    const int32_t* page_table, const int32_t* kv_lens,
+                                    const int32_t* q_lens, float k_scale, float v_scale,
+                                    int batch, int q_len, int n_kv_heads, int page_size,
+                                    int num_pages, int max_pages_per_seq, fa512_stream_t stream);
+
+/*
+ * fa512_decode_paged_fp4 -- fa512_decode_paged_q over a paged KV cache held in 4
+ * bits an element, in the rows of fa512_cache_append_fp4: 576 bytes of K and V a
+ * position and KV head instead of bf16's 2,048.
+ *
+ *   k_scale, v_scale per-tensor scales, finite
+ *   q, out, lse, positions and every other argument as fa512_decode_paged_q
+ *              (q_len >= 1, q_len * G <= 16)
+ *   num_splits 0 picks fa512_decode_auto_splits_fp4(); workspace must be at
+ *              least fa512_decode_workspace_bytes_fp4() bytes, 256-byte aligned
+ *
+ * Codes and group scales are widened exactly, the queries (bf16) scaled by a
+ * power of two per row and held in f16, sums are fp32; the softmax weights round
+ * to f16.  Slots that no row sees may hold anything without reaching the output.
+ * A row that sees a score of NaN or +infinity is NaN.  The same inputs give the
+ * same bits every time.  batch * q_len is at most 65535.
+ */
+fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* page_table, const int32_t* kv_lens, void* out,
+                                    float* lse, int batch, int q_len, int n_q_heads,
+                                    int n_kv_heads, int page_size, int num_pages,
+                                    int max_pages_per_seq, int max_kv_len, float scale,
+                                    float k_scale, float v_scale, int window, int num_splits,
+                                    void* workspace, size_t workspace_bytes,
+                                    fa512_stream_t stream);
+
+/* Split count of fa512_decode_paged_fp4 when num_splits == 0; 1 when there is
+ * nothing to split. */
+int fa512_decode_auto_splits_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                 int page_size, int max_kv_len);
+
+/* Workspace bytes fa512_decode_paged_fp4 needs for this shape and split count
+ * (num_splits 0: the automatic choice).  0 for an invalid shape. */
+size_t fa512_decode_workspace_bytes_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                        int page_size, int max_kv_len, int num_splits);
+
+/*
+ * fa512_cache_page_bounds -- the smallest and the largest key element of each
+ * channel, of the pages that hold the newest tokens.
+ *
+ *   k_pages      [num_pages, page_size, n_kv_heads, 512] bf16 (element_bits 16)
+ *                or E4M3 (8), or [..., FA512_FP4_ROW_BYTES] bytes (4), device
+ *   page_table   [batch, max_pages_per_seq], kv_lens [batch] int32, device
+ *   q_lens       [batch] int32, device: newest tokens of sequence b; NULL: q_len
+ *   bounds       [num_pages, n_kv_heads, 2, 512] bf16, device, written: smallest,
+ *                largest
+ *
+ * The pages of positions kv_lens[b] - q_lens[b] .. kv_lens[b] - 1 are read, up to
+ * position kv_lens[b] - 1, and their bounds written; no others.  Of a coded cache
+ * the bounds are those of what is stored, without the tensor scale; they are
+ * exact.  A channel with a NaN has NaN bounds.  Call it after each append (with
+ * the same kv_lens and q_lens), after fa512_cache_compact (with the new lengths)
+ * and, with a q_len of 1, after fa512_cache_fork.  A page that several sequences
+ * hold gets its bounds from each call that names it: give it no sequence that
+ * ends inside a page that others hold beyond.
+ * On the device, q_lens[b] outside [0, q_len], kv_lens[b] below it or beyond the
+ * page table and page indices outside the pool are recorded in the error word
+ * and skipped.
+ */
+fa512_status fa512_cache_page_bounds(const void* k_pages, const int32_t* page_table,
+                                     const int32_t* kv_lens, const int32_t* q_lens, void* bounds,
+                                     int batch, int q_len, int n_kv_heads, int element_bits,
+                                     int page_size, int num_pages, int max_pages_per_seq,
+                                     fa512_stream_t stream);
+
+/*
+ * fa512_select_pages -- the pages that a sparse decode step reads.
+ *
+ *   q          [batch, q_len, n_q_heads, 512] bf16, device
+ *   bounds     [num_pages, n_kv_heads, 2, 512] bf16, device
+ *   page_table, kv_lens, max_kv_len as fa512_decode_paged_q
+ *   selected   [batch, n_kv_heads, n_select] int32, device, written: logical pages
+ *              of the sequence in rising order, then -1
+ *
+ * The score of page p for a KV head is the largest, over its query rows (token,
+ * query head), of sum_d max(q_d lo_d, q_d hi_d): with lo and hi the page's bounds,
+ * no product of the row with a key of the page is larger.  Selected are the
+ * n_first first and the n_last last pages of the sequence, and of the others
+ * those with the largest scores, equal ones by their number, n_select in all; of
+ * a sequence with no more pages, all.  (The page that is filling and those of
+ * drafted tokens are among the last: n_last counts them.)  Rows whose position
+ * kv_lens[b] - q_len + t is negative are left out.  A page with a bound that is
+ * not finite comes before all others; one whose index lies outside the pool
+ * comes last and is recorded in the error word.
+ *
+ * Sums are fp32 in a fixed order (channels c and c + 256, then c % 8 by halves,
+ * then c / 8 by halves), so the choice is the same for every launch shape.
+ *
+ * Requirements: q_len * G <= 16, page_size one of 16, 32, 64, 128, 256, n_first +
+ * n_last <= n_select; workspace of fa512_select_workspace_bytes() bytes, 256-byte
+ * aligned, not shared by calls that may run at the same time.
+ */
+fa512_status fa512_select_pages(const void* q, const void* bounds, const int32_t* page_table,
+                                const int32_t* kv_lens, int32_t* selected, int batch, int q_len,
+                                int n_q_heads, int n_kv_heads, int page_size, int num_pages,
+                                int max_pages_per_seq, int max_kv_len, int n_select, int n_first,
+                                int n_last, void* workspace, size_t workspace_bytes,
+                                fa512_stream_t stream);
+
+/* Workspace bytes of fa512_select_pages; 0 for an invalid shape. */
+size_t fa512_select_workspace_bytes(int batch, int n_kv_heads, int page_size, int max_kv_len);
+
+/*
+ * fa512_decode_paged_sparse -- fa512_decode_paged_q over some pages of each
+ * sequence.
+ *
+ *   selected   [batch, n_kv_heads, n_selected] int32, device: the logical pages
+ *              that the rows of a KV head see, rising, then -1
+ *   other tensors and arguments as fa512_decode_paged_q
+ *
+ * Query t of sequence b sits at position kv_lens[b] - q_len + t and sees the
+ * positions up to its own that lie in a selected page.  Only those pages are
+ * read.  A row that sees nothing returns O = 0, LSE = -inf.
+ * Entries that do not rise, follow a -1 or lie outside the sequence's pages are
+ * recorded in the error word; nothing is read out of bounds for them, but the
+ * outputs of their (sequence, KV head) mean nothing.
+ *
+ * num_splits 0 picks fa512_decode_auto_splits_sparse(); workspace must be at
+ * least fa512_decode_workspace_bytes_sparse() bytes, 256-byte aligned.
+ * n_selected >= 1; n_selected * page_size and max_pages_per_seq * page_size are
+ * below 2^31 - 256, batch * q_len is at most 65535.
+ */
+fa512_status fa512_decode_paged_sparse(const void* q, const void* k_pages, const void* v_pages,
+                                       const int32_t* page_table, const int32_t* kv_lens,
+                                       const int32_t* selected, void* out, float* lse, int batch,
+                                       int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                       int num_pages, int max_pages_per_seq, int n_selected,
+                                       int max_kv_len, float scale, int num_splits, void* workspace,
+                                       size_t workspace_bytes, fa512_stream_t stream);
+
+/* The same over a cache in FP8 E4M3 (as fa512_decode_paged_fp8). */
+fa512_status fa512_decode_paged_sparse_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, const int32_t* kv_lens,
+                                           const int32_t* selected, void* out, float* lse, int batch,
+                                           int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                           int num_pages, int max_pages_per_seq, int n_selected,
+                                           int max_kv_len, float scale, float k_scale, float v_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           fa512_stream_t stream);
+
+/* The same over a cache in 4 bits (as fa512_decode_paged_fp4). */
+fa512_status fa512_decode_paged_sparse_fp4(const void* q, const void* k_pages, const void* v_pages,
+                                           const int32_t* page_table, const int32_t* kv_lens,
+                                           const int32_t* selected, void* out, float* lse, int batch,
+                                           int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                                           int num_pages, int max_pages_per_seq, int n_selected,
+                                           int max_kv_len, float scale, float k_scale, float v_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           fa512_stream_t stream);
+
+/* Split count and workspace bytes of the sparse calls; element_bits 16 (bf16), 8
+ * (E4M3) or 4.  1 and 0 for an invalid shape. */
+int fa512_decode_auto_splits_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                    int element_bits, int page_size, int n_selected,
+                                    int max_kv_len);
+size_t fa512_decode_workspace_bytes_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads,
+                                           int element_bits, int page_size, int n_selected,
+                                           int max_kv_len, int num_splits);
+
+/*
  * fa512_cache_compact -- after a verification step: moves the accepted
  * tokens' rows together, in all layers of a cache.
  *
  *   k_pages, v_pages [n_layers, num_pages, page_size, n_kv_heads, 512] of
- *                element_bytes 1 (E4M3) or 2 (bf16), device, written
+ *                element_bytes 1 (E4M3) or 2 (bf16), or rows of
+ *                FA512_FP4_ROW_BYTES bytes instead (FA512_ELEMENT_FP4), device,
+ *                written
  *   kv_lens      [batch] int32, device: cached positions, the q_lens[b]
  *                (NULL: q_len) drafted tokens included
  *   accepted     [batch, max_accepted] int32, device: the accepted tokens of
@@ -504,6 +703,8 @@ fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_
  * stays where it is; the sequence's other rows move and its new length is the
  * usual one.  max_accepted is at most 1024.
  */
+#define FA512_ELEMENT_FP4 (-4)
+
 fa512_status fa512_cache_compact(void *k_pages, void *v_pages, const int32_t *page_table,
                                  const int32_t *kv_lens, const int32_t *q_lens,
                                  const int32_t *accepted, const int32_t *n_accepted,

@@ -189,3 +189,136 @@ def cache_resize(page_table, kv_lens, new_kv_lens, page_refs, page_size: int):
         table[b, i] = page
         refs[page] = 1
     return table, refs
+
+
+# ------------------------------------------------- 4-bit rows, selected pages
+
+FP4_ROW = 288
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def widen_fp4(rows) -> np.ndarray:
+    """4-bit rows [..., 288] -> the values [..., 512] they stand for without the tensor scale, in fp64."""
+    r = _u8(rows)
+    pairs = r[..., :256]
+    code = np.stack([pairs & 15, pairs >> 4], axis=-1).reshape(*pairs.shape[:-1], 512)
+    value = E2M1[code & 7] * np.where(code & 8, -1.0, 1.0)
+    with np.errstate(invalid="ignore"):
+        return value * np.repeat(e4m3_table()[r[..., 256:]], 16, axis=-1)
+
+
+def fp4_rows(new, scale: float) -> np.ndarray:
+    """bf16 rows [..., 512] -> 4-bit rows: fp32 quotients, each then to the nearest value, ties to even."""
+    x = widen_bf16(new).astype(np.float32)
+    with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
+        y = x / np.float32(scale)
+        g = y.reshape(*y.shape[:-1], 32, 16)
+        s8 = e4m3_round((np.max(np.abs(g), axis=-1) / np.float32(6)).astype(np.float64))
+        s = e4m3_table()[s8].astype(np.float32)[..., None]
+        z = np.where(s > 0, g / np.where(s > 0, s, np.float32(1)), np.float32(0)).astype(np.float64)
+    a = np.minimum(np.where(np.isnan(z), 0.0, np.abs(z)), 6.0)
+    hi = np.clip(np.searchsorted(E2M1, a), 0, 7)
+    lo = np.maximum(hi - 1, 0)
+    dlo, dhi = a - E2M1[lo], E2M1[hi] - a
+    code = np.where((dlo < dhi) | ((dlo == dhi) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
+    code = (code | (np.signbit(z).astype(np.uint8) << 3)).reshape(*y.shape[:-1], 256, 2)
+    return np.concatenate([code[..., 0] | (code[..., 1] << 4), s8], axis=-1)
+
+
+def widen_cache(pages) -> np.ndarray:
+    """Cached rows of any format in fp64, without the tensor scale."""
+    if tuple(pages.shape)[-1] == FP4_ROW:
+        return widen_fp4(pages)
+    return widen_bf16(pages) if "bfloat16" in str(pages.dtype) else widen_e4m3(pages)
+
+
+def decode_paged_any(q, k_pages, v_pages, page_table, kv_lens, selected=None, *, scale=None, window: int = 0,
+                     k_scale: float = 1.0, v_scale: float = 1.0):
+    """``(out, lse, weight)`` as decode_paged_tree, of the last q_len tokens of each sequence over a cache of any
+    format; with ``selected`` [batch, n_kv_heads, n] over the listed pages alone."""
+    qf, pt, kl = widen_bf16(q), _i32(page_table), _i32(kv_lens)
+    sel = None if selected is None else _i32(selected)
+    bsz, qlen, hq, d = qf.shape
+    psz, hk = (int(x) for x in tuple(k_pages.shape)[1:3])
+    G = hq // hk
+    scale = d ** -0.5 if scale is None else float(scale)
+    out, weight = np.zeros(qf.shape), np.zeros(qf.shape)
+    lse = np.full((bsz, qlen, hq), -np.inf)
+    for b in range(bsz):
+        n = int(kl[b])
+        here = n - qlen + np.arange(qlen)
+        for h in range(hk):
+            pages = np.arange(pages_of(n, psz)) if sel is None else sel[b, h][sel[b, h] >= 0]
+            j = (pages[:, None] * psz + np.arange(psz)).reshape(-1)
+            j = j[j < n]
+            vis = j[None] <= here[:, None]
+            if window > 0:
+                vis &= j[None] > here[:, None] - window
+            j, vis = j[vis.any(axis=0)], vis[:, vis.any(axis=0)]
+            if not len(j):
+                continue
+            k = widen_cache(k_pages[pt[b, j // psz], j % psz, h]) * k_scale
+            v = widen_cache(v_pages[pt[b, j // psz], j % psz, h]) * v_scale
+            for i in range(h * G, (h + 1) * G):
+                s = np.where(vis, qf[b, :, i] @ k.T * scale, -np.inf)
+                m = s.max(axis=1)
+                some = m > -np.inf
+                p = np.exp(s - np.where(some, m, 0.0)[:, None])
+                l = np.where(some, p.sum(axis=1), 1.0)
+                out[b, :, i] = (p @ v) / l[:, None]
+                weight[b, :, i] = (p @ np.abs(v)) / l[:, None]
+                lse[b, :, i] = np.where(some, m + np.log(l), -np.inf)
+    return out, lse, weight
+
+
+def page_bounds(k_pages, page_table, kv_lens, bounds, q_len: int, q_lens=None) -> np.ndarray:
+    """The bounds (fp64 [num_pages, n_kv_heads, 2, 512]) after the call, from ``bounds`` before it."""
+    pt, kl = _i32(page_table), _i32(kv_lens)
+    psz = int(tuple(k_pages.shape)[1])
+    out = widen_bf16(bounds)
+    for b in range(len(kl)):
+        cnt = q_len if q_lens is None else int(_i32(q_lens)[b])
+        n = int(kl[b])
+        if cnt == 0:
+            continue
+        for p in range((n - cnt) // psz, (n - 1) // psz + 1):
+            k = widen_cache(k_pages[pt[b, p], :min(psz, n - p * psz)])
+            out[pt[b, p], :, 0], out[pt[b, p], :, 1] = k.min(axis=0), k.max(axis=0)
+    return out
+
+
+def page_scores(q, bounds, page_table, kv_lens, b: int, psz: int, kind=np.float64) -> np.ndarray:
+    """[n_kv_heads, pages] scores of sequence b: in fp64, or in fp32 in the operation's order of sums."""
+    qf, bf = widen_bf16(q).astype(kind), widen_bf16(bounds).astype(kind)
+    pt, n = _i32(page_table), int(_i32(kv_lens)[b])
+    _, qlen, hq, d = qf.shape
+    hk = bf.shape[1]
+    w = bf[pt[b, :pages_of(n, psz)]]
+    got = np.full((hk, w.shape[0]), -np.inf)
+    for h in range(hk):
+        for t in range(max(0, qlen - n), qlen):
+            for i in range(h * (hq // hk), (h + 1) * (hq // hk)):
+                x = np.maximum(qf[b, t, i] * w[:, h, 0], qf[b, t, i] * w[:, h, 1])
+                x = x.reshape(-1, 2, 32, 8).transpose(0, 1, 3, 2).reshape(-1, d)
+                while x.shape[1] > 1:
+                    x = x[:, :x.shape[1] // 2] + x[:, x.shape[1] // 2:]
+                got[h] = np.maximum(got[h], x[:, 0])
+    return got
+
+
+def select_pages(q, bounds, page_table, kv_lens, psz: int, n_select: int, n_first: int, n_last: int) -> np.ndarray:
+    """[batch, n_kv_heads, n_select] int32."""
+    kl = _i32(kv_lens)
+    hk = int(tuple(bounds.shape)[1])
+    got = np.full((len(kl), hk, n_select), -1, dtype=np.int32)
+    for b in range(len(kl)):
+        held = pages_of(int(kl[b]), psz)
+        if not held:
+            continue
+        score = page_scores(q, bounds, page_table, kl, b, psz, np.float32)
+        score[:, :n_first] = np.inf
+        score[:, max(0, held - n_last):] = np.inf
+        for h in range(hk):
+            best = np.sort(np.argsort(-score[h], kind="stable")[:n_select])
+            got[b, h, :len(best)] = best
+    return got
