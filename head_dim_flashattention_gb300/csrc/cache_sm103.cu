@@ -127,7 +127,9 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // the NaN scale; a scale that rounds to 0 makes the codes 0.
 //
 // A warp rounds one row, a group of 16 elements a lane, up to APPEND_RUN rows
-// with all loads first.
+// with all loads first.  17 divisions a group cost more issue slots than the bytes
+// take (8 sequences of up to 4,096 tokens, 4 heads: 170 us), so tensor scales that
+// are powers of two have a path without them (to_4bit_pow2).
 __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -137,6 +139,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
         : "=r"(r)
         : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
     return r;
+}
+
+// The group's scale byte for max |y|, and its value.
+__device__ __forceinline__ float group_scale(float most, uint8_t* byte) {
+    uint16_t s8;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fdiv_rn(most, 6.f)));
+    uint32_t s2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(s8));
+    float s;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"(static_cast<unsigned short>(s2 & 0xffffu)));
+    *byte = static_cast<uint8_t>(s8 & 0xff);
+    return s;
 }
 
 // 16 bf16 elements -> codes and the scale byte
@@ -154,19 +168,44 @@ __device__ __forceinline__ uint2 to_4bit(const uint4 a, const uint4 b, float ten
         most = fmaxf(most, fabsf(y[i]));
         nan |= y[i] != y[i];
     }
-    uint16_t s8;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fdiv_rn(most, 6.f)));
-    uint32_t s2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(s8));
-    float s;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(s) : "h"(static_cast<unsigned short>(s2 & 0xffffu)));
+    const float s = group_scale(most, scale_byte);
     float z[2][8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i >> 3][i & 7] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
-    *scale_byte = nan ? 0x7f : static_cast<uint8_t>(s8 & 0xff);
+    if (nan) *scale_byte = 0x7f;
     return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
 }
 
+// The same for a tensor scale whose reciprocal `by` is a power of two.  Then y has
+// 8 significant bits and the scale s 4, so y / s, where it is no midpoint of two
+// E2M1 values, lies 2^-11 or more from all of them (the lowest bit of a y above s / 8
+// is at least 2^-11 s, and a midpoint times s is a multiple of it).  x times the rounded by / s, off by
+// less than 2^-23 of it, plus 1.5 * 2^11 rounds to a multiple of 2^-12: midpoints
+// come out exactly, and nothing crosses one.
+__device__ __forceinline__ uint2 to_4bit_pow2(const uint4 a, const uint4 b, float by, uint8_t* scale_byte) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t top = 0;                                     // largest magnitudes of the halves, NaN where there is one
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[i] & 0x7fff7fffu));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"((top << 16) | (top >> 16)));
+    const float most = __uint_as_float(top & 0xffff0000u);
+    const bool nan = most != most;
+    const float s = group_scale(nan ? 0.f : most * by, scale_byte);
+    const float r = s > 0.f ? __fdiv_rn(1.f, s) * by : 0.f;
+    constexpr float SNAP = 3072.f;
+    float z[2][8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        const float q = __fadd_rn(__fmaf_rn(x, r, SNAP), -SNAP);
+        // its sign also where it came to 0
+        z[i >> 3][i & 7] = s > 0.f ? __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u)) : 0.f;
+    }
+    if (nan) *scale_byte = 0x7f;
+    return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+}
+
+template <bool POW2>
 __global__ void __launch_bounds__(APPEND_THREADS) append_fp4_kernel(const AppendParams p) {
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     int n_new = p.q_lens ? p.q_lens[b] : p.q_len;
@@ -210,9 +249,11 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_fp4_kernel(const Append
         if (!there[r]) continue;
         uint8_t *kd = static_cast<uint8_t*>(p.k_pages) + at[r], *vd = static_cast<uint8_t*>(p.v_pages) + at[r];
         uint8_t s;
-        *reinterpret_cast<uint2*>(kd + 8 * lane) = to_4bit(k[r][0], k[r][1], p.k_scale, &s);
+        *reinterpret_cast<uint2*>(kd + 8 * lane) = POW2 ? to_4bit_pow2(k[r][0], k[r][1], p.k_scale, &s)
+                                                         : to_4bit(k[r][0], k[r][1], p.k_scale, &s);
         kd[256 + lane] = s;
-        *reinterpret_cast<uint2*>(vd + 8 * lane) = to_4bit(v[r][0], v[r][1], p.v_scale, &s);
+        *reinterpret_cast<uint2*>(vd + 8 * lane) = POW2 ? to_4bit_pow2(v[r][0], v[r][1], p.v_scale, &s)
+                                                         : to_4bit(v[r][0], v[r][1], p.v_scale, &s);
         vd[256 + lane] = s;
     }
 }
@@ -622,32 +663,30 @@ __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const PagePlanP
 
 cudaError_t launch_cache_append(const AppendParams& p, int element_bits, cudaStream_t stream) {
     using namespace cache;
+    // scales that are powers of two with a normal reciprocal
+    auto pow2 = [](float x) {
+        int e;
+        return frexpf(x, &e) == 0.5f && e > -100 && e < 100;
+    };
+    const bool both = element_bits != 16 && pow2(p.k_scale) && pow2(p.v_scale);
+    AppendParams by = p;                                  // reciprocals in the place of the scales
+    by.k_scale = 1.f / p.k_scale;
+    by.v_scale = 1.f / p.v_scale;
     if (element_bits == 4) {
         const long long rows = static_cast<long long>(p.q_len) * p.n_kv_heads;
         constexpr int ROWS = APPEND_THREADS / 32 * APPEND_RUN;
         const dim3 grid(static_cast<unsigned>((rows + ROWS - 1) / ROWS), p.batch);
-        append_fp4_kernel<<<grid, APPEND_THREADS, 0, stream>>>(p);
+        if (both) append_fp4_kernel<true><<<grid, APPEND_THREADS, 0, stream>>>(by);
+        else append_fp4_kernel<false><<<grid, APPEND_THREADS, 0, stream>>>(p);
         return cudaGetLastError();
     }
     const bool fp8 = element_bits == 8;
     const long long units = static_cast<long long>(p.q_len) * p.n_kv_heads * (fp8 ? D / 16 : D / 8);
     constexpr int BLOCK = APPEND_THREADS * APPEND_RUN;
     const dim3 grid(static_cast<unsigned>((units + BLOCK - 1) / BLOCK), p.batch);
-    // scales that are powers of two with a normal reciprocal
-    auto pow2 = [](float x) {
-        int e;
-        return frexpf(x, &e) == 0.5f && e > -100 && e < 100;
-    };
-    if (!fp8) {
-        append_kernel<0><<<grid, APPEND_THREADS, 0, stream>>>(p);
-    } else if (pow2(p.k_scale) && pow2(p.v_scale)) {
-        AppendParams q = p;
-        q.k_scale = 1.f / p.k_scale;
-        q.v_scale = 1.f / p.v_scale;
-        append_kernel<2><<<grid, APPEND_THREADS, 0, stream>>>(q);
-    } else {
-        append_kernel<1><<<grid, APPEND_THREADS, 0, stream>>>(p);
-    }
+    if (!fp8) append_kernel<0><<<grid, APPEND_THREADS, 0, stream>>>(p);
+    else if (both) append_kernel<2><<<grid, APPEND_THREADS, 0, stream>>>(by);
+    else append_kernel<1><<<grid, APPEND_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

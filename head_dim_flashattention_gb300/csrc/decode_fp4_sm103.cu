@@ -7,15 +7,16 @@
 // bits and lies between 2^-10 and 2,688, so it is exact in f16, and the products
 // run on mma.sync with f16 operands and fp32 sums over the cache's exact values.
 //
-// A CTA of four warps takes one split of the keys of a (sequence, KV head) in
-// tiles of 64 positions, K and V rows brought by TMA into two slots each.  For a
-// tile, warp w forms S^T = K Q^T of positions 16 w .. 16 w + 15 over the whole
-// head dim, with the query rows in N, their softmax against a reference of its
-// own, and leaves P^T and the reference in shared memory; after one barrier every
-// warp adds V^T P^T of all 64 positions for its 128 columns of O.  So nothing is
-// computed twice, and the four warps meet once in 64 positions.  References are
-// whole numbers in log2 units: what brings two of them together is a power of
-// two, exact in f16.
+// A CTA takes one split of the keys of a (sequence, KV head) in tiles of 64
+// positions, K and V rows brought by TMA into rings of slots.  Four warps form
+// S^T = K Q^T, 16 positions each over the whole head dim with the query rows in N,
+// and their softmax against a reference of their own, and leave P^T and the
+// reference in shared memory; four other warps add V^T P^T of all 64 positions,
+// 128 columns of O each.  Nothing is computed twice, and the two groups only meet
+// at barriers in shared memory with a tile of slack, so that both products of
+// different tiles overlap (one group that did both in turn read 5.0 TB/s, each
+// product alone as fast as the loads, 6.4).  References are whole numbers in log2
+// units: what brings two of them together is a power of two, exact in f16.
 //
 // K pairs are neighbouring codes of a row, as stored.  A V pair is the codes of
 // one column in two rows: a shift and a bit select turn two rows' words into
@@ -40,30 +41,31 @@ constexpr int D = 512;
 constexpr int ROW = kFp4RowBytes;
 constexpr int CODES = 256;                       // bytes of codes in a row
 constexpr int TILE = 64;                         // positions per tile
-constexpr int WARPS = 4;                         // 16 positions of a tile and 128 columns of O each
-constexpr int THREADS = WARPS * 32;
+constexpr int WARPS = 4;                         // per group: 16 positions of a tile, or 128 columns of O, each
+constexpr int THREADS = 2 * WARPS * 32;
+constexpr int CTAS_PER_SM = 2;
 constexpr int SLOT = TILE * ROW;                 // 18,432 bytes
 constexpr int KSTEPS = D / 16;
 constexpr int MTILES = D / WARPS / 16;           // m-tiles of 16 columns a warp
-constexpr int META = 4;                          // tiles whose positions are kept
-
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int META = 8;                          // tiles whose positions are kept
 
 template <int NT>
 struct Smem {
-    static constexpr int k = 0;                              // 2 slots
-    static constexpr int v = 2 * SLOT;                       // 2 slots
-    static constexpr int p = 4 * SLOT;                       // [parity][block][nt][lane] uint2
+    static constexpr int slots = NT == 1 ? 3 : 2;            // of K, and of V
+    static constexpr int k = 0;
+    static constexpr int v = slots * SLOT;
+    static constexpr int p = 2 * slots * SLOT;               // [parity][block][nt][lane] uint2
     static constexpr int q = p + 2 * WARPS * NT * 32 * 8;    // NT = 2: [nt][kstep][lane] uint2
     static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);   // [parity][block][8 NT] float
-    static constexpr int lsum = ref + 2 * WARPS * 8 * NT * 4;              // [warp][8 NT] float
-    static constexpr int base = lsum + WARPS * 8 * NT * 4;                 // [META][4] first position of 16
+    static constexpr int sums = ref + 2 * WARPS * 8 * NT * 4;              // [warp][8 NT] float2: reference, sum
+    static constexpr int base = sums + WARPS * 8 * NT * 8;                 // [META][4] first position of 16
     static constexpr int row = base + META * 16;                           // [META][4] first row of a run
-    static constexpr int bar = row + META * 16;                            // K slots, V slots
-    static constexpr int total = bar + 4 * 8;
+    static constexpr int bar = row + META * 16;
+    // barriers: K slots full, V slots full and empty, P buffers full and empty
+    static constexpr int total = bar + (3 * slots + 4) * 8;
 };
-static_assert(3 * (Smem<1>::total + 1024) <= 228 * 1024, "three CTAs fit an SM's shared memory");
-static_assert(2 * (Smem<2>::total + 1024) <= 228 * 1024, "two CTAs fit an SM's shared memory");
+static_assert(CTAS_PER_SM * (Smem<1>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
+static_assert(CTAS_PER_SM * (Smem<2>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
 
 __device__ __forceinline__ int turned(int r) { return r ^ ((r >> 2) & 1); }
 
@@ -81,6 +83,12 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
     return h;
+}
+
+__device__ __forceinline__ float f16_f32(uint32_t h) {
+    float f;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(static_cast<unsigned short>(h)));
+    return f;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t y, uint32_t sel) {
@@ -116,27 +124,231 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: 1 for up to 8 query rows (q_len * G) of a KV head, whose fragments stay in
-// registers, 2 for up to 16, whose fragments are read from shared memory.
-template <int NT, bool LIST>
-__global__ void __launch_bounds__(THREADS, ctas_per_sm(NT))
+// A reference to subtract: 0 while nothing was seen, so that 2^(-inf - 0) = 0.
+__device__ __forceinline__ float finite_ref(float x) { return x == -INFINITY ? 0.f : x; }
+
+constexpr uint32_t LOW_HALVES = 0x0f0f0f0fu;
+
+// S^T of 16 positions, positions turned(g) and + 8 of `block` to a lane, scales
+// applied to the codes; Q fragments in registers (NT = 1) or shared memory.
+template <int NT>
+__device__ __forceinline__ void scores(const uint8_t* block, int lane, const uint32_t (&qb)[NT == 1 ? KSTEPS : 1][2],
+                                       const uint2* s_q, float (&sc)[NT][4]) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t *a_row = block + turned(g) * ROW, *b_row = a_row + 8 * ROW;
+    const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
+    float acc[NT][2][4];                          // two chains of sums
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][0][e] = acc[n][1][e] = 0.f;
+#pragma unroll
+    for (int j4 = 0; j4 < 2; ++j4) {
+        // the rows' scales of 16 groups; this lane's are every fourth
+        const uint4 xa = *reinterpret_cast<const uint4*>(a_row + CODES + 16 * j4);
+        const uint4 xb = *reinterpret_cast<const uint4*>(b_row + CODES + 16 * j4);
+        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+            const uint32_t sa = e4m3x2_f16(prmt(wa[2 * j2], wa[2 * j2 + 1], pick) & 0xffffu);
+            const uint32_t sb = e4m3x2_f16(prmt(wb[2 * j2], wb[2 * j2 + 1], pick) & 0xffffu);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 4 * j4 + 2 * j2 + h;
+                const uint32_t fa = prmt(sa, sa, h ? 0x3232u : 0x1010u), fb = prmt(sb, sb, h ? 0x3232u : 0x1010u);
+                const uint2 ca = *reinterpret_cast<const uint2*>(a_row + 32 * j + 8 * t);
+                const uint2 cb = *reinterpret_cast<const uint2*>(b_row + 32 * j + 8 * t);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t ha[4], hb[4];
+                    e2m1x8_f16(x ? ca.y : ca.x, ha);
+                    e2m1x8_f16(x ? cb.y : cb.x, hb);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int k = 4 * j + 2 * x + s;
+                        const uint32_t a0 = mul_f16x2(ha[2 * s], fa), a2 = mul_f16x2(ha[2 * s + 1], fa);
+                        const uint32_t a1 = mul_f16x2(hb[2 * s], fb), a3 = mul_f16x2(hb[2 * s + 1], fb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t b0, b1;
+                            if constexpr (NT == 1) {
+                                b0 = qb[k][0];
+                                b1 = qb[k][1];
+                            } else {
+                                const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
+                                b0 = q2.x;
+                                b1 = q2.y;
+                            }
+                            mma_f16(acc[n][k & 1], a0, a1, a2, a3, b0, b1);
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = acc[n][0][e] + acc[n][1][e];
+}
+
+// The same for up to 2 rows: column 2 c + r of Q^T holds row r's elements of the
+// groups 4 j + c, and zeros.  A lane's sums of step j are those of group 4 j + t.
+__device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, const uint32_t (&qb)[KSTEPS][2],
+                                              float (&sc)[4]) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t *a_row = block + turned(g) * ROW, *b_row = a_row + 8 * ROW;
+    const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[e] = 0.f;
+#pragma unroll
+    for (int j4 = 0; j4 < 2; ++j4) {
+        const uint4 xa = *reinterpret_cast<const uint4*>(a_row + CODES + 16 * j4);
+        const uint4 xb = *reinterpret_cast<const uint4*>(b_row + CODES + 16 * j4);
+        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+            const uint32_t sa = e4m3x2_f16(prmt(wa[2 * j2], wa[2 * j2 + 1], pick) & 0xffffu);
+            const uint32_t sb = e4m3x2_f16(prmt(wb[2 * j2], wb[2 * j2 + 1], pick) & 0xffffu);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 4 * j4 + 2 * j2 + h;
+                const uint2 ca = *reinterpret_cast<const uint2*>(a_row + 32 * j + 8 * t);
+                const uint2 cb = *reinterpret_cast<const uint2*>(b_row + 32 * j + 8 * t);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t ha[4], hb[4];
+                    e2m1x8_f16(x ? ca.y : ca.x, ha);
+                    e2m1x8_f16(x ? cb.y : cb.x, hb);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        mma_f16(d, ha[2 * s], hb[2 * s], ha[2 * s + 1], hb[2 * s + 1], qb[4 * j + 2 * x + s][0],
+                                qb[4 * j + 2 * x + s][1]);
+                }
+                const float fa = f16_f32(h ? sa >> 16 : sa), fb = f16_f32(h ? sb >> 16 : sb);
+                sc[0] = fmaf(fa, d[0], sc[0]);
+                sc[1] = fmaf(fa, d[1], sc[1]);
+                sc[2] = fmaf(fb, d[2], sc[2]);
+                sc[3] = fmaf(fb, d[3], sc[3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {                 // the four classes
+        sc[e] += __shfl_xor_sync(0xffffffffu, sc[e], 1);
+        sc[e] += __shfl_xor_sync(0xffffffffu, sc[e], 2);
+    }
+}
+
+// Row of a block of 16 that lane t's i-th V operand is: the pairs (2 t, 2 t + 1)
+// and (2 t + 8, 2 t + 9).
+__device__ __forceinline__ int v_row(int t, int i) { return turned(2 * t + (i & 1)) + 8 * (i >> 1); }
+
+// O^T of columns 128 warp .. + 127 += V^T P^T over 16 positions, scales applied to
+// the codes; m-tile i is columns 16 g + 2 i, 16 g + 2 i + 1 of those.
+template <int NT>
+__device__ __forceinline__ void add_values(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[NT][2],
+                                           float (&o)[NT][MTILES][4]) {
+    const int g = lane >> 2, t = lane & 3;
+    uint2 c[4];
+    uint32_t sb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t* row = block + v_row(t, i) * ROW;
+        c[i] = *reinterpret_cast<const uint2*>(row + 64 * warp + 8 * g);
+        sb[i] = row[CODES + 8 * warp + g];
+    }
+    const uint32_t s01 = e4m3x2_f16(prmt(sb[0], sb[1], 0x0040u)), s23 = e4m3x2_f16(prmt(sb[2], sb[3], 0x0040u));
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const uint32_t w0 = x ? c[0].y : c[0].x, w1 = x ? c[1].y : c[1].x;
+        const uint32_t w2 = x ? c[2].y : c[2].x, w3 = x ? c[3].y : c[3].x;
+        // bytes of two rows' codes of one column: even columns, odd columns
+        uint32_t e01[4], d01[4], e23[4], d23[4];
+        e2m1x8_f16((w0 & LOW_HALVES) | ((w1 << 4) & ~LOW_HALVES), e01);
+        e2m1x8_f16(((w0 >> 4) & LOW_HALVES) | (w1 & ~LOW_HALVES), d01);
+        e2m1x8_f16((w2 & LOW_HALVES) | ((w3 << 4) & ~LOW_HALVES), e23);
+        e2m1x8_f16(((w2 >> 4) & LOW_HALVES) | (w3 & ~LOW_HALVES), d23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = mul_f16x2(e01[i], s01), a1 = mul_f16x2(d01[i], s01);
+            const uint32_t a2 = mul_f16x2(e23[i], s23), a3 = mul_f16x2(d23[i], s23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * x + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        }
+    }
+}
+
+// The same for up to 2 rows: column 2 c + r of P^T is row r's weights times the
+// scales of group 4 h + c; m-tile 4 h + i is columns 16 (4 h + g % 4) + 8 (g / 4) +
+// 2 i, + 1.  A lane's sums of class t = g % 4 are O, the others are not used.
+__device__ __forceinline__ void add_values_narrow(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[2],
+                                                  float (&o)[MTILES][4]) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* rows[4];
+    uint2 sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        rows[i] = block + v_row(t, i) * ROW;
+        sw[i] = *reinterpret_cast<const uint2*>(rows[i] + CODES + 8 * warp);
+    }
+    const uint32_t pick = static_cast<uint32_t>(g >> 1) | (static_cast<uint32_t>(4 + (g >> 1)) << 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint32_t*>(rows[i] + 64 * warp + 32 * h + 8 * (g & 3) + 4 * (g >> 2));
+        const uint32_t s01 = e4m3x2_f16(prmt(h ? sw[0].y : sw[0].x, h ? sw[1].y : sw[1].x, pick) & 0xffffu);
+        const uint32_t s23 = e4m3x2_f16(prmt(h ? sw[2].y : sw[2].x, h ? sw[3].y : sw[3].x, pick) & 0xffffu);
+        const uint32_t b0 = mul_f16x2(pb[0], s01), b1 = mul_f16x2(pb[1], s23);
+        uint32_t e01[4], d01[4], e23[4], d23[4];
+        e2m1x8_f16((w[0] & LOW_HALVES) | ((w[1] << 4) & ~LOW_HALVES), e01);
+        e2m1x8_f16(((w[0] >> 4) & LOW_HALVES) | (w[1] & ~LOW_HALVES), d01);
+        e2m1x8_f16((w[2] & LOW_HALVES) | ((w[3] << 4) & ~LOW_HALVES), e23);
+        e2m1x8_f16(((w[2] >> 4) & LOW_HALVES) | (w[3] & ~LOW_HALVES), d23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f16(o[4 * h + i], e01[i], d01[i], e23[i], d23[i], b0, b1);
+    }
+}
+
+// ROWS: the most query rows (q_len * G) of a KV head.  Up to 8 rows' fragments stay
+// in registers; up to 16 rows' (NT = 2 n-tiles) are read from shared memory.
+//
+// Up to 2 rows leave six of the eight columns of an n-tile free, and the group
+// scales move there (NARROW): column 2 c + r belongs to row r and scale class c.
+//   S^T: lane t holds K codes of groups 4 j + t, so with Q zero outside class t a
+//        lane's sums of step j are those of its own group, and take its scale in
+//        fp32: 32 multiply-adds a tile where scaling the codes takes 128.
+//   O^T: lane g holds codes of group 4 h + g % 4, and P is scaled once for each
+//        class: 4 multiplications a block where scaling the codes takes 32.  Of a
+//        lane's sums those of class t = g % 4 are O, the others are not used.
+template <int ROWS, bool LIST>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const DecodeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int NT = ROWS > 8 ? 2 : 1;
+    constexpr bool NARROW = ROWS == 2;
     using Smem = fp4::Smem<NT>;
+    constexpr int SLOTS = Smem::slots;
     extern __shared__ __align__(128) uint8_t fp4_smem[];
     uint8_t* smem = fp4_smem;
     uint2* s_p = reinterpret_cast<uint2*>(smem + Smem::p);
+    uint16_t* s_p2 = reinterpret_cast<uint16_t*>(smem + Smem::p);   // NARROW: [parity][block][row][16]
     uint2* s_q = reinterpret_cast<uint2*>(smem + Smem::q);
     float* s_ref = reinterpret_cast<float*>(smem + Smem::ref);
-    float* s_l = reinterpret_cast<float*>(smem + Smem::lsum);
+    float2* s_sums = reinterpret_cast<float2*>(smem + Smem::sums);
     int* s_base = reinterpret_cast<int*>(smem + Smem::base);
     int* s_row = reinterpret_cast<int*>(smem + Smem::row);
-    uint64_t* bar_k = reinterpret_cast<uint64_t*>(smem + Smem::bar);
-    uint64_t* bar_v = bar_k + 2;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Smem::bar);
+    uint64_t *v_full = k_full + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS, *p_empty = p_full + 2;
 
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) & (WARPS - 1);   // within its group
+    const bool k_group = threadIdx.x < WARPS * 32;
     const int g = lane >> 2, t = lane & 3;       // mma fragment coordinates
     const int G = p.group, R = p.q_len * G;      // query rows: (token, head) -> token * G + head
     const int ps = p.page_size;
@@ -165,247 +377,120 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         v1 = static_cast<int>(min(first + static_cast<long long>(p.tiles_per_split) * TILE, static_cast<long long>(hi)));
     }
     const int n_tiles = v1 > v0 ? (v1 - v0 + TILE - 1) / TILE : 0;
-    const int held = (len + ps - 1) / ps;        // pages of the sequence
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_k[i], 1);
-            mbar_init(&bar_v[i], 1);
-        }
-        fence_mbar_init();
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
-    }
-    __syncthreads();
-
-    // ---- loads, by warp 0.  A run is box_rows positions of one page; lane l
-    // keeps the first row and position of runs run0 + l (cur) and run0 + 32 + l.
+    // A run is box_rows positions of one page.
     const int box = p.box_rows, runs_per_tile = TILE / box, blocks_per_run = box / 16;
-    const int n_runs = n_tiles * runs_per_tile;
-    int run0 = 0, row_cur = -1, base_cur = -1, row_nxt = -1, base_nxt = -1;
-    auto look_up = [&](int r, int& row, int& base) {
-        row = base = -1;
-        if (r >= n_runs) return;
-        const int v = v0 + r * box;
-        int lp = v / ps, at = v;
-        if constexpr (LIST) {
-            if (v >= v1) return;
-            const int off = v - lp * ps;
-            lp = list_page(p, list, lp, held);
-            if (lp < 0) return;
-            at = lp * ps + off;
-        }
-        if (at >= hi || at + box <= lo) return;
-        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
-        if (page < 0 || page >= p.num_pages) {
-            report_error(p.err, FA512_DEVICE_ERR_INDEX);
-            return;
-        }
-        row = page * ps + (at - lp * ps);
-        base = at;
-    };
-    // K rows of tile i into their slot; what the V load and the masks need is kept
-    auto load_k = [&](int i) {
-        if (i >= n_tiles) return;
-        const int r = i * runs_per_tile;
-        if (r >= run0 + 32) {
-            run0 += 32;
-            row_cur = row_nxt;
-            base_cur = base_nxt;
-            look_up(run0 + 32 + lane, row_nxt, base_nxt);
-        }
-        const int l = (r - run0) + lane / blocks_per_run;      // lanes 0 .. 3: their 16 positions' run
-        const int base = __shfl_sync(0xffffffffu, base_cur, l & 31);
-        const int slot = (i & (META - 1)) * 4;
-        if (lane < 4) s_base[slot + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
-        const int run_row = __shfl_sync(0xffffffffu, row_cur, (r - run0 + lane) & 31);
-        const unsigned some = __ballot_sync(0xffffffffu, lane < runs_per_tile && run_row >= 0);
-        if (lane < runs_per_tile) s_row[slot + lane] = run_row;
+    auto done_with = [&](uint64_t* bar) {        // this warp has read what the barrier guards
         __syncwarp();
-        uint64_t* bar = &bar_k[i & 1];
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(some) * box * ROW);
-        __syncwarp();
-        if (lane < runs_per_tile && run_row >= 0)
-            tma_load_3d(smem + Smem::k + (i & 1) * SLOT + lane * box * ROW, &tmk, bar, 0, kvh, run_row);
+        if (lane == 0) mbar_arrive(bar);
     };
-    auto load_v = [&](int i) {
-        if (i >= n_tiles) return;
-        const int run_row = lane < runs_per_tile ? s_row[(i & (META - 1)) * 4 + lane] : -1;
-        const unsigned some = __ballot_sync(0xffffffffu, run_row >= 0);
-        uint64_t* bar = &bar_v[i & 1];
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(some) * box * ROW);
-        __syncwarp();
-        if (run_row >= 0)
-            tma_load_3d(smem + Smem::v + (i & 1) * SLOT + lane * box * ROW, &tmv, bar, 0, kvh, run_row);
-    };
-    if (warp == 0) {
-        look_up(lane, row_cur, base_cur);
-        look_up(32 + lane, row_nxt, base_nxt);
-        load_k(0);
-        load_v(0);
-        load_k(1);
-        load_v(1);
-    }
+    // Every wait of a warp that follows another role's phase of a barrier guards what
+    // that role cannot pass before this warp has arrived, so a phase is never missed.
+    auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.err)) != 0; };
+    const size_t S = static_cast<size_t>(p.num_splits);
+    bool ok = true;                              // the same in all lanes of a warp
+    int k_loaded = 0, v_loaded = 0;              // tiles whose load this warp has issued
 
-    // ---- Q^T fragments: b0/b1 of k-step 4 j + s hold row g's elements 64 j + 16
-    // t + 4 s + {0, 1} / {2, 3}, in f16 after a power-of-two scale per row that
-    // keeps its largest element below 2^15 (exact for elements down to 2^-39 of
-    // that; a score is unscaled before the softmax)
-    uint32_t qb[NT == 1 ? KSTEPS : 1][2];
-    float rs[NT][2];                              // 1 / scale of rows 8 n + 2 t, 8 n + 2 t + 1
+    if (k_group) {
+        // ---- Q^T fragments: b0/b1 of k-step 4 j + s hold row g's elements 64 j + 16
+        // t + 4 s + {0, 1} / {2, 3}, in f16 after a power-of-two scale per row that
+        // keeps its largest element below 2^15 (exact for elements down to 2^-39 of
+        // that; a score is unscaled before the softmax)
+        uint32_t qb[NT == 1 ? KSTEPS : 1][2];
+        float rs[NT][2];                          // 1 / scale of rows 8 n + 2 t, 8 n + 2 t + 1
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        // NT = 2: each warp holds a quarter of the k-steps, all of them the maxima
-        const int r = 8 * n + g;
-        const bool row_ok = r < R;
-        const size_t qrow = (static_cast<size_t>(b) * p.q_len + (row_ok ? r / G : 0)) * p.n_q_heads + kvh * G +
-                            (row_ok ? r % G : 0);
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * D);
-        float most = 0.f;
+        for (int n = 0; n < NT; ++n) {
+            // NT = 2: each warp holds a quarter of the k-steps, all of them the maxima
+            const int r = NARROW ? g & 1 : 8 * n + g;
+            const bool row_ok = r < R;
+            const size_t qrow = (static_cast<size_t>(b) * p.q_len + (row_ok ? r / G : 0)) * p.n_q_heads + kvh * G +
+                                (row_ok ? r % G : 0);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * D);
+            float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-                if constexpr (NT == 1) {
-                    qb[4 * j + 2 * e][0] = a.x;
-                    qb[4 * j + 2 * e][1] = a.y;
-                    qb[4 * j + 2 * e + 1][0] = a.z;
-                    qb[4 * j + 2 * e + 1][1] = a.w;
-                }
-            }
-        }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^(14 - E), E = exponent of the maximum (0 or not finite: 1)
-        const int E = (__float_as_uint(most) >> 23) & 0xff;
-        const int biased = min(127 + 14 + 127 - E, 254);
-        const float scale = (most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
-        auto to_f16 = [&](uint32_t w) {
-            return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
-        };
-        if constexpr (NT == 1) {
-#pragma unroll
-            for (int k = 0; k < KSTEPS; ++k) {
-                qb[k][0] = to_f16(qb[k][0]);
-                qb[k][1] = to_f16(qb[k][1]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 2 * warp; j < 2 * warp + 2; ++j)
+            for (int j = 0; j < 8; ++j) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
-                    s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
-                    s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
-                }
-        }
-        rs[n][0] = 1.f / __shfl_sync(0xffffffffu, scale, 4 * (2 * t));
-        rs[n][1] = 1.f / __shfl_sync(0xffffffffu, scale, 4 * (2 * t + 1));
-    }
-    if constexpr (NT == 2) __syncthreads();
-
-    // positions of rows 8 n + 2 t + i (-1: padding row, sees nothing); a row sees
-    // the keys whose distance to it is in [0, reach)
-    int qpos[NT][2];
+                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 8 * n + 2 * t + i;
-            qpos[n][i] = r < R ? len - p.q_len + r / G : -1;
-        }
-    const unsigned reach = p.window > 0 ? static_cast<unsigned>(p.window) : 0x7fffffffu;
-
-    float m[NT][2], mg[NT], l[NT][2];             // references of rows 2 t + i and g; this lane's part of the sums
-    float o[NT][MTILES][4];                       // O^T: m-tile i = columns 16 g + 2 i, 16 g + 2 i + 1 of this warp's 128
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = mg[n] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < MTILES; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-    }
-    auto finite_ref = [](float x) { return x == -INFINITY ? 0.f : x; };   // nothing seen yet: 2^(-inf - 0) = 0
-
-    const int ra = turned(g);                     // this lane's rows of 16 positions: ra, ra + 8
-    bool ok = true;
-    int done = 0;
-    for (int it = 0; it < n_tiles; ++it) {
-        const int par = it & 1, phase = (it >> 1) & 1;
-        const int* base4 = s_base + (it & (META - 1)) * 4;
-        if (!mbar_wait(&bar_k[par], phase, p.err)) ok = false;
-
-        // ---- S^T of this warp's 16 positions, softmax against their own maximum
-        {
-            const int base = base4[warp];
-            float sc[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-            if (base >= 0) {
-                const uint8_t* a_row = smem + Smem::k + par * SLOT + (16 * warp + ra) * ROW;
-                const uint8_t* b_row = a_row + 8 * ROW;
-                uint32_t wa[8], wb[8];            // the rows' scales
-                {
-                    const uint4 x = *reinterpret_cast<const uint4*>(a_row + CODES);
-                    const uint4 y = *reinterpret_cast<const uint4*>(a_row + CODES + 16);
-                    const uint4 z = *reinterpret_cast<const uint4*>(b_row + CODES);
-                    const uint4 w = *reinterpret_cast<const uint4*>(b_row + CODES + 16);
-                    wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[3] = x.w; wa[4] = y.x; wa[5] = y.y; wa[6] = y.z; wa[7] = y.w;
-                    wb[0] = z.x; wb[1] = z.y; wb[2] = z.z; wb[3] = z.w; wb[4] = w.x; wb[5] = w.y; wb[6] = w.z; wb[7] = w.w;
-                }
-                const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
-                float other[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) other[n][0] = other[n][1] = other[n][2] = other[n][3] = 0.f;
-#pragma unroll
-                for (int j2 = 0; j2 < 4; ++j2) {
-                    const uint32_t sa = e4m3x2_f16(prmt(wa[2 * j2], wa[2 * j2 + 1], pick) & 0xffffu);
-                    const uint32_t sb = e4m3x2_f16(prmt(wb[2 * j2], wb[2 * j2 + 1], pick) & 0xffffu);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int j = 2 * j2 + h;
-                        const uint32_t fa = prmt(sa, sa, h ? 0x3232u : 0x1010u), fb = prmt(sb, sb, h ? 0x3232u : 0x1010u);
-                        const uint2 ca = *reinterpret_cast<const uint2*>(a_row + 32 * j + 8 * t);
-                        const uint2 cb = *reinterpret_cast<const uint2*>(b_row + 32 * j + 8 * t);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t ha[4], hb[4];
-                            e2m1x8_f16(x ? ca.y : ca.x, ha);
-                            e2m1x8_f16(x ? cb.y : cb.x, hb);
-#pragma unroll
-                            for (int s = 0; s < 2; ++s) {
-                                const int k = 4 * j + 2 * x + s;
-                                const uint32_t a0 = mul_f16x2(ha[2 * s], fa), a2 = mul_f16x2(ha[2 * s + 1], fa);
-                                const uint32_t a1 = mul_f16x2(hb[2 * s], fb), a3 = mul_f16x2(hb[2 * s + 1], fb);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    uint32_t b0, b1;
-                                    if constexpr (NT == 1) {
-                                        b0 = qb[k][0];
-                                        b1 = qb[k][1];
-                                    } else {
-                                        const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
-                                        b0 = q2.x;
-                                        b1 = q2.y;
-                                    }
-                                    mma_f16(h ? other[n] : sc[n], a0, a1, a2, a3, b0, b1);
-                                }
-                            }
-                        }
+                    for (int i = 0; i < 4; ++i)
+                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+                    if constexpr (NT == 1) {
+                        qb[4 * j + 2 * e][0] = a.x;
+                        qb[4 * j + 2 * e][1] = a.y;
+                        qb[4 * j + 2 * e + 1][0] = a.z;
+                        qb[4 * j + 2 * e + 1][1] = a.w;
                     }
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[n][e] += other[n][e];
             }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // 2^(14 - E), E = exponent of the maximum (0 or not finite: 1)
+            const int E = (__float_as_uint(most) >> 23) & 0xff;
+            const int biased = min(127 + 14 + 127 - E, 254);
+            const float scale = (most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+            auto to_f16 = [&](uint32_t w) {
+                return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+            };
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int k = 0; k < KSTEPS; ++k) {
+                    const bool mine = !NARROW || g >> 1 == t;
+                    qb[k][0] = mine ? to_f16(qb[k][0]) : 0u;
+                    qb[k][1] = mine ? to_f16(qb[k][1]) : 0u;
+                }
+            } else {
+#pragma unroll
+                for (int j = 2 * warp; j < 2 * warp + 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
+                        s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
+                        s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
+                    }
+            }
+            rs[n][0] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 0 : 4 * (2 * t));
+            rs[n][1] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 4 : 4 * (2 * t + 1));
+        }
+        __syncthreads();                          // barriers, the first tiles' notes, NT = 2: the queries
+
+        // row 8 n + i (NARROW) or 8 n + 2 t + i
+        auto row_of = [&](int n, int i) { return NARROW ? i : 8 * n + 2 * t + i; };
+        // their positions (-1: padding row, sees nothing); a row sees
+        // the keys whose distance to it is in [0, reach)
+        int qpos[NT][2];
+        float m[NT][2], l[NT][2];                 // this warp's running reference and sum (a lane's part) of those rows
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = row_of(n, i);
+                qpos[n][i] = r < R ? len - p.q_len + r / G : -1;
+                m[n][i] = -INFINITY;
+                l[n][i] = 0.f;
+            }
+        const unsigned reach = p.window > 0 ? static_cast<unsigned>(p.window) : 0x7fffffffu;
+        const int ra = turned(g);                 // this lane's rows of 16 positions: ra, ra + 8
+
+        for (int it = 0; it < n_tiles; ++it) {
+            const int slot = it % SLOTS, par = it & 1;
+            if (!ok || !wait(&k_full[slot], it / SLOTS)) {
+                ok = false;
+                break;
+            }
+            const int base = s_base[(it & (META - 1)) * 4 + warp];
+            // (an unloaded block's rows are stale: its scores are masked)
+            float sc[NT][4];
+            const uint8_t* block = smem + Smem::k + slot * SLOT + 16 * warp * ROW;
+            if constexpr (NARROW) scores_narrow(block, lane, qb, sc[0]);
+            else scores<NT>(block, lane, qb, s_q, sc);
+            // ---- softmax against this block's own maximum, rounded up to a whole number,
+            // less 7: weights up to 2^7 keep small ones, and those times a group scale
+            // (448 at most), in f16's range
             const int kp = base + ra;
-            float* ref = s_ref + (par * WARPS + warp) * 8 * NT;
+            uint2 frag[NT];
+            float ref[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float sv[2][2], cm[2];
@@ -427,48 +512,168 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 float pr[2][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    cm[i] = ceilf(cm[i]);
-                    const float sh = finite_ref(cm[i]);
+                    ref[n][i] = ceilf(cm[i]) - 7.f;
+                    const float sh = finite_ref(ref[n][i]);
                     pr[i][0] = fast_exp2(sv[i][0] - sh);
                     pr[i][1] = fast_exp2(sv[i][1] - sh);
+                    // the sums keep the fp32 weights
+                    const float mn = fmaxf(m[n][i], ref[n][i]), to = finite_ref(mn);
+                    l[n][i] = l[n][i] * fast_exp2(m[n][i] - to) + (pr[i][0] + pr[i][1]) * fast_exp2(ref[n][i] - to);
+                    m[n][i] = mn;
                 }
-                // P rounds to f16 (2^-12 of a weight, 2^-25 of the largest one's
-                // block); the sums keep the fp32 values
-                const uint32_t b0 = transpose8x8(pack_f16x2(pr[0][0], pr[1][0]));
-                const uint32_t b1 = transpose8x8(pack_f16x2(pr[0][1], pr[1][1]));
-                s_p[((par * WARPS + warp) * NT + n) * 32 + lane] = make_uint2(b0, b1);
-                if (g == 0) *reinterpret_cast<float2*>(ref + 8 * n + 2 * t) = make_float2(cm[0], cm[1]);
-                // this lane's part of the sums, until all references are known
-                sc[n][0] = pr[0][0] + pr[0][1];
-                sc[n][1] = pr[1][0] + pr[1][1];
-                sc[n][2] = cm[0];
-                sc[n][3] = cm[1];
+                // P rounds to f16: 2^-11 of a weight, or 2^-32 of the block's largest
+                if constexpr (NARROW) {
+                    frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
+                } else {
+                    frag[n].x = transpose8x8(pack_f16x2(pr[0][0], pr[1][0]));
+                    frag[n].y = transpose8x8(pack_f16x2(pr[0][1], pr[1][1]));
+                }
             }
-            if (__syncthreads_or(!ok)) {
+            if (it >= 2 && !wait(&p_empty[par], it / 2 - 1)) ok = false;
+            if (!ok) break;
+            float* out_ref = s_ref + (par * WARPS + warp) * 8 * NT;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (NARROW)             // a row's 16: positions 2 i, 2 i + 1, 2 i + 8, 2 i + 9 together
+                    s_p2[(par * WARPS + warp) * 32 + 16 * (t & 1) + (g >> 1) * 4 + (t & 2) + (g & 1)] =
+                        static_cast<uint16_t>(frag[n].x);
+                else
+                    s_p[((par * WARPS + warp) * NT + n) * 32 + lane] = frag[n];
+                if (g == 0 && (!NARROW || t == 0))
+                    *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(ref[n][0], ref[n][1]);
+            }
+            done_with(&p_full[par]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
+                if (g == 0 && (!NARROW || t == 0)) s_sums[warp * 8 * NT + row_of(n, i)] = make_float2(m[n][i], l[n][i]);
+            }
+    } else {
+        // ---- loads, by warp 0 of this group: lane l keeps the first row and position
+        // of run run0 + l
+        const int held = (len + ps - 1) / ps;    // pages of the sequence
+        const int n_runs = n_tiles * runs_per_tile;
+        int run0 = 0, run_row = -1, run_base = -1;
+        auto look_up = [&]() {
+            const int r = run0 + lane;
+            run_row = run_base = -1;
+            if (r >= n_runs) return;
+            const int v = v0 + r * box;
+            int lp = v / ps, at = v;
+            if constexpr (LIST) {
+                if (v >= v1) return;
+                const int off = v - lp * ps;
+                lp = list_page(p, list, lp, held);
+                if (lp < 0) return;
+                at = lp * ps + off;
+            }
+            if (at >= hi || at + box <= lo) return;
+            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
+            if (page < 0 || page >= p.num_pages) {
+                report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                return;
+            }
+            run_row = page * ps + (at - lp * ps);
+            run_base = at;
+        };
+        // K rows of tile i into their slot; what the V load and the masks need is noted
+        auto load_k = [&](int i) {
+            if (i >= n_tiles) return;
+            const int slot = i % SLOTS, r = i * runs_per_tile;
+            if (r >= run0 + 32) {
+                run0 += 32;
+                look_up();
+            }
+            // lanes 0 .. 3: the run of their 16 positions
+            const int base = __shfl_sync(0xffffffffu, run_base, (r - run0 + lane / blocks_per_run) & 31);
+            const int row = __shfl_sync(0xffffffffu, run_row, (r - run0 + lane) & 31);
+            const bool mine = lane < runs_per_tile && row >= 0;
+            const unsigned some = __ballot_sync(0xffffffffu, mine);
+            const int meta = (i & (META - 1)) * 4;
+            if (lane < 4) s_base[meta + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
+            if (lane < runs_per_tile) s_row[meta + lane] = row;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], __popc(some) * box * ROW);
+            __syncwarp();
+            if (mine) tma_load_3d(smem + Smem::k + slot * SLOT + lane * box * ROW, &tmk, &k_full[slot], 0, kvh, row);
+            k_loaded = i + 1;
+        };
+        // V rows of tile i once the slot's last tile is read
+        auto load_v = [&](int i) {
+            if (i >= n_tiles) return;
+            const int slot = i % SLOTS;
+            if (i >= SLOTS && !wait(&v_empty[slot], i / SLOTS - 1)) {
+                ok = false;
+                return;
+            }
+            const int row = lane < runs_per_tile ? s_row[(i & (META - 1)) * 4 + lane] : -1;
+            const unsigned some = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[slot], __popc(some) * box * ROW);
+            __syncwarp();
+            if (row >= 0) tma_load_3d(smem + Smem::v + slot * SLOT + lane * box * ROW, &tmv, &v_full[slot], 0, kvh, row);
+            v_loaded = i + 1;
+        };
+        if (warp == 0) {
+            if (lane == 0) {
+                for (int i = 0; i < SLOTS; ++i) {
+                    mbar_init(&k_full[i], 1);
+                    mbar_init(&v_full[i], 1);
+                    mbar_init(&v_empty[i], WARPS);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(&p_full[i], WARPS);
+                    mbar_init(&p_empty[i], WARPS);
+                }
+                fence_mbar_init();
+                tma_prefetch_desc(&tmk);
+                tma_prefetch_desc(&tmv);
+            }
+            __syncwarp();
+            look_up();
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                load_k(i);
+                if (i < SLOTS - 1) load_v(i);
+            }
+        }
+        __syncthreads();                          // barriers, the first tiles' notes
+        // references of rows 2 t + i and g (NARROW: i and g % 2)
+        float m[NT][2], mg[NT];
+        float o[NT][MTILES][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = mg[n] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < MTILES; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        }
+        for (int it = 0; it < n_tiles && ok; ++it) {
+            const int slot = it % SLOTS, par = it & 1;
+            if (!wait(&p_full[par], it / 2)) {
                 ok = false;
                 break;
             }
-            if (warp == 0) {
-                load_k(it + 2);                   // K of this tile is read, V of the last one too
-                if (it > 0) load_v(it + 1);
-            }
             // ---- one reference for the tile
+            uint32_t pb[WARPS][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float* all = s_ref + par * WARPS * 8 * NT + 8 * n;
-                float mn[2] = {m[n][0], m[n][1]};
+                float mn[2] = {m[n][0], m[n][1]}, rg[WARPS];
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
-                    const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + 2 * t);
+                    const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + (NARROW ? 0 : 2 * t));
+                    rg[w] = NARROW ? (g & 1 ? x.y : x.x) : all[w * 8 * NT + g];
                     mn[0] = fmaxf(mn[0], x.x);
                     mn[1] = fmaxf(mn[1], x.y);
+                    mg[n] = fmaxf(mg[n], rg[w]);
                 }
                 float al[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float sh = finite_ref(mn[i]);
-                    al[i] = fast_exp2(m[n][i] - sh);
-                    l[n][i] = l[n][i] * al[i] + sc[n][i] * fast_exp2(sc[n][2 + i] - sh);
+                    al[i] = fast_exp2(m[n][i] - finite_ref(mn[i]));
                     m[n][i] = mn[i];
                 }
                 if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
@@ -481,129 +686,132 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     }
                 }
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) mg[n] = fmaxf(mg[n], all[w * 8 * NT + g]);
-            }
-        }
-        if (!mbar_wait(&bar_v[par], phase, p.err)) ok = false;
-
-        // ---- O^T += V^T P^T for this warp's columns, 16 positions at a time
-        const uint8_t* vst = smem + Smem::v + par * SLOT;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const int base = base4[w];
-            if (base < 0) continue;
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float f = fast_exp2(s_ref[(par * WARPS + w) * 8 * NT + 8 * n + g] - finite_ref(mg[n]));
-                const uint32_t f2 = pack_f16x2(f, f);
-                const uint2 x = s_p[((par * WARPS + w) * NT + n) * 32 + lane];
-                pb[n][0] = mul_f16x2(x.x, f2);
-                pb[n][1] = mul_f16x2(x.y, f2);
-            }
-            // rows of the pairs (2 t, 2 t + 1) and (2 t + 8, 2 t + 9); a position that no
-            // row sees gets the scale 0 (its bytes may be anything: codes are finite)
-            uint2 c[4];
-            uint32_t sb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = turned(2 * t + (i & 1)) + 8 * (i >> 1);
-                const uint8_t* row = vst + (16 * w + r) * ROW;
-                c[i] = *reinterpret_cast<const uint2*>(row + 64 * warp + 8 * g);
-                const uint32_t s = row[CODES + 8 * warp + g];
-                sb[i] = base + r < hi && base + r >= lo ? s : 0u;
-            }
-            const uint32_t s01 = e4m3x2_f16(sb[0] | (sb[1] << 8)), s23 = e4m3x2_f16(sb[2] | (sb[3] << 8));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t w0 = x ? c[0].y : c[0].x, w1 = x ? c[1].y : c[1].x;
-                const uint32_t w2 = x ? c[2].y : c[2].x, w3 = x ? c[3].y : c[3].x;
-                // bytes of two rows' codes of one column: even columns, odd columns
-                constexpr uint32_t LOW = 0x0f0f0f0fu;
-                uint32_t e01[4], d01[4], e23[4], d23[4];
-                e2m1x8_f16((w0 & LOW) | ((w1 << 4) & ~LOW), e01);
-                e2m1x8_f16(((w0 >> 4) & LOW) | (w1 & ~LOW), d01);
-                e2m1x8_f16((w2 & LOW) | ((w3 << 4) & ~LOW), e23);
-                e2m1x8_f16(((w2 >> 4) & LOW) | (w3 & ~LOW), d23);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = mul_f16x2(e01[i], s01), a1 = mul_f16x2(d01[i], s01);
-                    const uint32_t a2 = mul_f16x2(e23[i], s23), a3 = mul_f16x2(d23[i], s23);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * x + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                for (int w = 0; w < WARPS; ++w) {
+                    const float f = fast_exp2(rg[w] - finite_ref(mg[n]));
+                    const uint32_t f2 = pack_f16x2(f, f);
+                    const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (par * WARPS + w) * 32 + 16 * (g & 1) + 4 * t)
+                                           : s_p[((par * WARPS + w) * NT + n) * 32 + lane];
+                    pb[w][n][0] = mul_f16x2(x.x, f2);
+                    pb[w][n][1] = mul_f16x2(x.y, f2);
                 }
             }
+            done_with(&p_empty[par]);
+            // P of this tile says that its K is read
+            if (warp == 0) {
+                load_k(it + SLOTS);
+                load_v(it + SLOTS - 1);
+            }
+            if (!ok || !wait(&v_full[slot], it / SLOTS)) {
+                ok = false;
+                break;
+            }
+            // ---- A position that no row sees gets the scale 0 (its bytes may be anything:
+            // codes are finite); lane l: positions l and l + 32 of the tile
+            uint8_t* vst = smem + Smem::v + slot * SLOT;
+            const int4 base4 = *reinterpret_cast<const int4*>(s_base + (it & (META - 1)) * 4);
+            const int first = min(min(base4.x, base4.y), min(base4.z, base4.w));
+            const int last = max(max(base4.x, base4.y), max(base4.z, base4.w));
+            if (first < lo || last + 16 > hi) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int base = lane < 16 ? (i ? base4.z : base4.x) : (i ? base4.w : base4.y);
+                    const int kp = base + (lane & 15);
+                    if (base < 0 || kp < lo || kp >= hi)
+                        *reinterpret_cast<uint2*>(vst + (lane + 32 * i) * ROW + CODES + 8 * warp) = make_uint2(0u, 0u);
+                }
+                fence_proxy_async_smem();         // before the slot is loaded again
+                __syncwarp();
+            }
+            // ---- O^T += V^T P^T for this warp's columns, 16 positions at a time
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                if constexpr (NARROW) add_values_narrow(vst + 16 * w * ROW, warp, lane, pb[w][0], o[0]);
+                else add_values<NT>(vst + 16 * w * ROW, warp, lane, pb[w], o);
+            }
+            done_with(&v_empty[slot]);
         }
-        done = it + 1;
+        // ---- this split's partial, unnormalised and times v_scale
+        const float f = ok ? p.o_scale : 0.f;
+        if constexpr (NARROW) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (r >= R || (g & 3) != t) continue;
+                const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
+                float* dst = p.ws_o + (hq * S + split) * D + 128 * warp + 16 * t + 8 * (g >> 2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
+                            make_float4(o[0][4 * h + 2 * j][r] * f, o[0][4 * h + 2 * j][2 + r] * f,
+                                        o[0][4 * h + 2 * j + 1][r] * f, o[0][4 * h + 2 * j + 1][2 + r] * f);
+            }
+        } else
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * t + i;
+                if (r >= R) continue;
+                const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
+                float4* dst = reinterpret_cast<float4*>(p.ws_o + (hq * S + split) * D + 128 * warp + 16 * g);
+#pragma unroll
+                for (int j = 0; j < MTILES / 2; ++j)
+                    dst[j] = make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
+                                         o[n][2 * j + 1][2 + i] * f);
+            }
     }
     // A wait that ran out: bounded waits for the copies in flight, so that none
-    // lands after this CTA has gone.  `done` tiles were gone through; the V wait of
-    // the last one may be the one that ran out.
-    if (__syncthreads_or(!ok)) {
-        ok = false;
-        if (threadIdx.x == 0)
-            for (int i = max(done - 1, 0); i < n_tiles && i < done + 2; ++i) {
-                if (i >= done) mbar_wait(&bar_k[i & 1], (i >> 1) & 1, p.err);
-                mbar_wait(&bar_v[i & 1], (i >> 1) & 1, p.err);
-            }
+    // lands after this CTA has gone.
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {
+        for (int i = max(0, k_loaded - SLOTS); i < k_loaded; ++i) mbar_wait(&k_full[i % SLOTS], (i / SLOTS) & 1, p.err);
+        for (int i = max(0, v_loaded - SLOTS); i < v_loaded; ++i) mbar_wait(&v_full[i % SLOTS], (i / SLOTS) & 1, p.err);
     }
-
-    // ---- this split's partial, unnormalised and times v_scale
+    // ---- (m, l): the K warps' sums brought to one reference
+    if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        float ref = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, s_sums[w * 8 * NT + r].x);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
-            if (g == 0) s_l[warp * 8 * NT + 8 * n + 2 * t + i] = l[n][i];
+        for (int w = 0; w < WARPS; ++w) {
+            const float2 x = s_sums[w * 8 * NT + r];
+            sum += x.y * fast_exp2(x.x - finite_ref(ref));
         }
-    __syncthreads();
-    const size_t S = static_cast<size_t>(p.num_splits);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 8 * n + 2 * t + i;
-            if (r >= R) continue;
-            const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
-            float4* dst = reinterpret_cast<float4*>(p.ws_o + (hq * S + split) * D + 128 * warp + 16 * g);
-            const float f = ok ? p.o_scale : 0.f;
-#pragma unroll
-            for (int j = 0; j < MTILES / 2; ++j)
-                dst[j] = make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
-                                     o[n][2 * j + 1][2 + i] * f);
-            if (warp == 0 && g == 0) {
-                float sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) sum += s_l[w * 8 * NT + r];
-                float ref = m[n][i];
-                if (sum != sum && ref == -INFINITY) ref = 0.f;   // only scores of NaN: not an empty split
-                p.ws_ml[(hq * S + split) * 2 + 0] = ok ? ref : -INFINITY;
-                p.ws_ml[(hq * S + split) * 2 + 1] = ok && ref != -INFINITY ? sum : 0.f;
-            }
-        }
+        if (sum != sum && ref == -INFINITY) ref = 0.f;   // only scores of NaN: not an empty split
+        const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
+        p.ws_ml[(hq * S + split) * 2 + 0] = failed ? -INFINITY : ref;
+        p.ws_ml[(hq * S + split) * 2 + 1] = failed || ref == -INFINITY ? 0.f : sum;
+    }
 }
 
-template <int NT, bool LIST>
+template <int ROWS, bool LIST>
 cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Smem<NT>::total);
+    constexpr int SMEM = Smem<(ROWS > 8 ? 2 : 1)>::total;
+    cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<ROWS, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.num_splits, p.n_kv_heads, p.batch);
-    decode_fp4_kernel<NT, LIST><<<grid, THREADS, Smem<NT>::total, stream>>>(tmk, tmv, p);
+    decode_fp4_kernel<ROWS, LIST><<<grid, THREADS, SMEM, stream>>>(tmk, tmv, p);
     return cudaGetLastError();
+}
+
+template <bool LIST>
+cudaError_t launch_rows(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, cudaStream_t stream) {
+    const int rows = p.q_len * p.group;
+    return rows <= 2   ? launch<2, LIST>(tmk, tmv, p, stream)
+           : rows <= 8 ? launch<8, LIST>(tmk, tmv, p, stream)
+                       : launch<16, LIST>(tmk, tmv, p, stream);
 }
 
 }  // namespace fp4
 
 int decode_fp4_tile_positions() { return fp4::TILE; }
-int decode_fp4_ctas_per_sm(int rows) { return fp4::ctas_per_sm(rows <= 8 ? 1 : 2); }
+int decode_fp4_ctas_per_sm() { return fp4::CTAS_PER_SM; }
 
 cudaError_t launch_decode_fp4(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
                               cudaStream_t stream) {
-    const bool two = p.q_len * p.group > 8;
-    const cudaError_t e = p.listed ? (two ? fp4::launch<2, true>(tmk, tmv, p, stream) : fp4::launch<1, true>(tmk, tmv, p, stream))
-                                   : (two ? fp4::launch<2, false>(tmk, tmv, p, stream) : fp4::launch<1, false>(tmk, tmv, p, stream));
+    const cudaError_t e = p.listed ? fp4::launch_rows<true>(tmk, tmv, p, stream) : fp4::launch_rows<false>(tmk, tmv, p, stream);
     return e != cudaSuccess ? e : launch_decode_merge(p, stream);
 }
 

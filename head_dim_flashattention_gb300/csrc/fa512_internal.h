@@ -65,7 +65,7 @@ cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
 // no swizzle; k8 / v8 are unused.
 constexpr int kFp4RowBytes = 288;  // 256 bytes of E2M1 pairs, 32 E4M3 scales
 int decode_fp4_tile_positions();
-int decode_fp4_ctas_per_sm(int rows);   // rows of a KV head
+int decode_fp4_ctas_per_sm();
 cudaError_t launch_decode_fp4(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
                               cudaStream_t stream);
 

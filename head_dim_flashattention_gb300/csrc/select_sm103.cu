@@ -29,9 +29,9 @@ constexpr int D = 512;
 
 // ------------------------------------------------------------------- bounds
 //
-// A block takes one touched page of one KV head; a thread 16 bytes of a row (32
-// codes in 4 bits), the rows dealt to 4, 8 or 16 groups of threads whose results
-// meet in shared memory.  NaN elements make both bounds NaN.
+// A block takes one touched page of one KV head; a thread 8 elements of a row (16
+// of a coded one, in 4 bits those of one scale), the rows dealt to 4 or 8 groups of
+// threads whose results meet in shared memory.  NaN elements make both bounds NaN.
 constexpr int BOUNDS_THREADS = 256;
 
 struct MinMax {
@@ -59,8 +59,8 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 template <int BITS>
 __global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsParams p) {
     constexpr int ROW = BITS == 16 ? 2 * D : BITS == 8 ? D : kFp4RowBytes;
-    constexpr int PAIRS = 64 / BITS;                // x 2 elements in 16 bytes
-    constexpr int LANES = D / (2 * PAIRS);          // threads of a row: 64, 32, 16
+    constexpr int PAIRS = BITS == 16 ? 4 : 8;       // x 2 elements of a thread
+    constexpr int LANES = D / (2 * PAIRS);          // threads of a row: 64, 32
     constexpr int GROUPS = BOUNDS_THREADS / LANES;
     constexpr bool F16 = BITS != 16;
     __shared__ uint32_t s_lo[GROUPS - 1][D / 2], s_hi[GROUPS - 1][D / 2];
@@ -87,38 +87,52 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsPara
     const uint32_t inf = F16 ? 0x7c007c00u : 0x7f807f80u;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) m[i] = {inf, inf | 0x80008000u};
-#pragma unroll 4
-    for (int r = grp; r < live; r += GROUPS) {
-        const uint8_t* row = src + r * step;
-        const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * u);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        if constexpr (BITS == 16) {
+    constexpr int RUN = 8;                          // rows in flight
+    for (int r0 = grp; r0 < live; r0 += RUN * GROUPS) {
+        uint4 x[RUN];
+        uint8_t scale[RUN];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) widen_to<F16>(m[i], w[i]);
-        } else if constexpr (BITS == 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t y;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)))));
-                widen_to<F16>(m[i], y);
+        for (int k = 0; k < RUN; ++k) {
+            // (a row past the end is the first one again)
+            const int r = r0 + k * GROUPS < live ? r0 + k * GROUPS : r0;
+            const uint8_t* row = src + r * step;
+            if constexpr (BITS == 4) {
+                const uint2 y = *reinterpret_cast<const uint2*>(row + 8 * u);
+                x[k] = make_uint4(y.x, y.y, 0u, 0u);
+                scale[k] = row[256 + u];
+            } else {
+                x[k] = *reinterpret_cast<const uint4*>(row + 16 * u);
             }
-        } else {
-            const uint32_t two = *reinterpret_cast<const uint16_t*>(row + 256 + 2 * u);   // scales of 16 elements each
-            uint32_t s;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<unsigned short>(two)));
-            const uint32_t s2[2] = {(s & 0xffffu) * 0x10001u, (s >> 16) * 0x10001u};
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t y[4];
-                asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-                    "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-                    "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-                    : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                    : "r"(w[i]));
+        for (int k = 0; k < RUN; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            if constexpr (BITS == 16) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[j]) : "r"(s2[i >> 1]));
-                    widen_to<F16>(m[4 * i + j], y[j]);
+                for (int i = 0; i < 4; ++i) widen_to<F16>(m[i], w[i]);
+            } else if constexpr (BITS == 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t y;
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)))));
+                    widen_to<F16>(m[i], y);
+                }
+            } else {
+                uint32_t s;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<unsigned short>(scale[k] * 0x101u)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t y[4];
+                    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+                        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+                        : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                        : "r"(w[i]));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[j]) : "r"(s));
+                        widen_to<F16>(m[4 * i + j], y[j]);
+                    }
                 }
             }
         }
@@ -159,13 +173,14 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsPara
 
 // ------------------------------------------------------------------- scores
 //
-// A warp scores PAGES pages at a time: lane l holds channels 8 l .. 8 l + 7 and
-// 256 + 8 l .. of their bounds in fp32, goes through the query rows (in shared
-// memory, as fp32) and keeps each page's largest score.  max(q lo, q hi) is
-// max(q, 0) hi + min(q, 0) lo, of which one term is 0: two packed multiply-adds
-// a pair of channels, and each sum below rounds once.
-constexpr int SCORE_WARPS = 8;
+// A warp scores two pages at a time, the bounds of its next two on their way: lane
+// l holds channels 8 l .. 8 l + 7 and 256 + 8 l .. of them, goes through the query
+// rows (in shared memory, as fp32) and keeps each page's largest score.  max(q lo,
+// q hi) is max(q, 0) hi + min(q, 0) lo, of which one term is 0: two packed
+// multiply-adds a pair of channels, and each sum below rounds once.
+constexpr int SCORE_WARPS = 4;
 constexpr int SCORE_PAGES = 2;
+constexpr int SCORE_BLOCKS = 6 * 152;                // blocks to spread the pages over
 constexpr int SCORE_ROWS = 16;                       // most query rows of a KV head
 
 // Unsigned integers in the order of the scores, -0 and 0 equal.  Largest of all,
@@ -214,26 +229,32 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
     __syncthreads();
     const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
     uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
-    for (int lp0 = (blockIdx.x * SCORE_WARPS + warp) * SCORE_PAGES; lp0 < held; lp0 += step) {
-        float2 lo[SCORE_PAGES][8], hi[SCORE_PAGES][8];
-        float best[SCORE_PAGES];
-        bool there[SCORE_PAGES], always[SCORE_PAGES];
-        uint4 raw[SCORE_PAGES][4];
+    // the page of lp: -1 none (always chosen, or past the end), -2 outside the pool
+    auto page_of = [&](int lp) {
+        if (lp >= held || lp < p.n_first || lp >= held - p.n_last) return -1;
+        const int page = table[lp];
+        return page < 0 || page >= p.num_pages ? -2 : page;
+    };
+    uint4 raw[SCORE_PAGES][4];
+    int page[SCORE_PAGES], page_next[SCORE_PAGES];
+    auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < SCORE_PAGES; ++i) {
-            const int lp = lp0 + i;
-            always[i] = lp < p.n_first || lp >= held - p.n_last;
-            there[i] = lp < held && !always[i];
-            int page = there[i] ? table[lp] : 0;
-            if (there[i] && (page < 0 || page >= p.num_pages)) {
-                if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                there[i] = false;                    // the lowest of all scores
-            }
-            if (!there[i]) page = 0;
-            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<size_t>(page) * p.n_kv_heads + h) * 2 * D);
+            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<size_t>(max(page[i], 0)) * p.n_kv_heads + h) * 2 * D);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) raw[i][j] = there[i] ? src[32 * j + lane] : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 4; ++j) raw[i][j] = page[i] >= 0 ? src[32 * j + lane] : make_uint4(0u, 0u, 0u, 0u);
         }
+    };
+    int lp0 = (blockIdx.x * SCORE_WARPS + warp) * SCORE_PAGES;
+#pragma unroll
+    for (int i = 0; i < SCORE_PAGES; ++i) page[i] = page_of(lp0 + i);
+    load();
+#pragma unroll
+    for (int i = 0; i < SCORE_PAGES; ++i) page_next[i] = page_of(lp0 + step + i);
+    for (; lp0 < held; lp0 += step) {
+        float2 lo[SCORE_PAGES][8], hi[SCORE_PAGES][8];
+        float best[SCORE_PAGES];
+        int now[SCORE_PAGES];
 #pragma unroll
         for (int i = 0; i < SCORE_PAGES; ++i) {
 #pragma unroll
@@ -247,7 +268,12 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
                 for (int e = 0; e < 4; ++e) hi[i][4 * j + e] = f[e];
             }
             best[i] = -INFINITY;
+            now[i] = page[i];
+            page[i] = page_next[i];
         }
+        if (lp0 + step < held) load();
+#pragma unroll
+        for (int i = 0; i < SCORE_PAGES; ++i) page_next[i] = page_of(lp0 + 2 * step + i);
         bool nan[SCORE_PAGES] = {};
         for (int r = r0; r < R; ++r) {
             float2 x[SCORE_PAGES][4];
@@ -281,7 +307,10 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
             uint32_t key = 0;
 #pragma unroll
             for (int i = 0; i < SCORE_PAGES; ++i)
-                if (lane == i) key = always[i] || nan[i] ? KEY_MOST : there[i] ? key_of(best[i]) : 0u;
+                if (lane == i) {
+                    if (now[i] == -2) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                    key = now[i] == -1 || nan[i] ? KEY_MOST : now[i] >= 0 ? key_of(best[i]) : 0u;   // outside: lowest
+                }
             keys[lp0 + lane] = key;
         }
     }
@@ -381,8 +410,10 @@ cudaError_t launch_page_bounds(const BoundsParams& p, int element_bits, cudaStre
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
     using namespace select;
     if (p.max_pages > p.n_select) {
-        const int per = SCORE_WARPS * SCORE_PAGES;
-        const dim3 grid((p.max_pages + per - 1) / per, p.n_kv_heads, p.batch);
+        // enough blocks for six on each SM, and none with less than a round of pages
+        const int rounds = (p.max_pages + SCORE_WARPS * SCORE_PAGES - 1) / (SCORE_WARPS * SCORE_PAGES);
+        const long long items = static_cast<long long>(p.n_kv_heads) * p.batch, want = (SCORE_BLOCKS + items - 1) / items;
+        const dim3 grid(static_cast<unsigned>(want < rounds ? want : rounds), p.n_kv_heads, p.batch);
         score_kernel<<<grid, SCORE_WARPS * 32, 0, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -3,7 +3,7 @@ selected pages within the tolerance below, and the calls of one decode step
 together, on a side stream and in a captured graph.
 
 Tolerance of an output element, A = sum p |v| / sum p (fp64): 2^-8 |O| (bf16), the
-weights' rounding 2^-8 A (bf16 cache) or 2^-11 A (coded caches, f16) with 2^-24 n
+weights' rounding 2^-8 A (bf16 cache) or 2^-10 A (coded caches, f16) with 2^-24 n
 vmax for f16 weights below its normal range, 1e-3 A for the fp32 scores (an FP8
 cache keeps its row's maxima in bf16, which moves no weight), plus 1e-6.  From 9
 rows a KV head on an E4M3 cache is read as bf16 tiles, its weights as bf16.
@@ -99,7 +99,7 @@ class Case:
         ro, rl, weight = paged.decode_paged_any(self.q, self.k, self.v, self.table, self.lens, self.sel,
                                                 **SCALES[self.kind])
         f16 = self.kind == "e2m1" or (self.kind == "e4m3" and self.rows <= 8)
-        tol = 2.0 ** -8 * np.abs(ro) + ((2.0 ** -11 if f16 else 2.0 ** -8) + 1e-3) * weight + 1e-6
+        tol = 2.0 ** -8 * np.abs(ro) + ((2.0 ** -10 if f16 else 2.0 ** -8) + 1e-3) * weight + 1e-6
         if f16:
             tol += 2.0 ** -24 * self.sel.shape[2] * self.psz * 6
         assert np.all(np.isfinite(o))
