@@ -87,7 +87,8 @@ fa512_status get_encoder(EncodeTiledFn* fn) {
 // 1..rank-1.
 fa512_status encode_map(CUtensorMap* m, CUtensorMapDataType dtype, CUtensorMapSwizzle swizzle,
                         const void* base, int rank, const uint64_t* dims,
-                        const uint64_t* strides_bytes, const uint32_t* box) {
+                        const uint64_t* strides_bytes, const uint32_t* box,
+                        CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     EncodeTiledFn enc;
     fa512_status st = get_encoder(&enc);
     if (st != FA512_OK) return st;
@@ -101,7 +102,7 @@ fa512_status encode_map(CUtensorMap* m, CUtensorMapDataType dtype, CUtensorMapSw
     for (int i = 0; i < rank - 1; ++i) gs[i] = strides_bytes[i];
     CUresult r = enc(m, dtype, static_cast<cuuint32_t>(rank),
                      const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     swizzle, promotion,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(FA512_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return FA512_OK;
@@ -197,30 +198,35 @@ int choose_splits_fp8(long long items, long long tiles, int n_sm, long long rows
     return static_cast<int>(best_s);
 }
 
-// Split count of the 4-bit kernel, which runs two CTAs per SM, for items of
-// `tiles` tiles of 64 positions.  The busiest SM's CTAs go in pairs, a last one
-// alone takes 0.6 of a pair's time per tile (1.1 us against 1.8), a CTA's start
-// and end cost about a tile, a split's merge 0.02:
-//   pairs x (tiles per split + 1) + single x (0.6 x tiles per split + 1) + 0.02 s
-// Within 3 % of the best of some 25 counts in 15 of 18 shapes of batch 1 to 64,
-// lengths of 1,000 to 28,672 and 1 or 4 KV heads; 9 % at worst.
-int choose_splits_fp4(long long items, long long tiles, int n_sm) {
-    if (items <= 0 || tiles <= 1) return 1;
-    const long long ctas = fa512::decode_fp4_ctas_per_sm();
-    const long long s_max = tiles < ctas * n_sm ? tiles : ctas * n_sm;
-    long long best_s = 1;
-    double best = 1e300;
-    for (long long s = 1; s <= s_max && s <= 1024; ++s) {
-        const long long per = (tiles + s - 1) / s, busiest = (items * s + n_sm - 1) / n_sm;
-        const double cost = static_cast<double>(busiest / 2 * (per + 1)) +
-                            static_cast<double>(busiest % 2) * (0.6 * static_cast<double>(per) + 1.0) +
-                            0.02 * static_cast<double>(s);
-        if (cost < best) {
-            best = cost;
-            best_s = s;
+// The 4-bit kernel deals the tiles (64 positions) of all sequences in ranges of equal
+// length to groups of CTAs, one CTA for each KV head, as many as one or two CTAs per
+// SM make.
+struct Fp4Plan {
+    int groups;
+    int segments;                  // most segments that a sequence may be left in
+};
+// For sequences of at most `tiles` tiles.  Times in tile times of a CTA that shares
+// its SM (1.8 us for 2 rows; alone it takes 0.6 of that), a tile for a CTA's start and
+// end, 0.02 for each of a sequence's segments in the merge.  A batch with shorter
+// sequences has shorter ranges, so a batch of several may leave twice the segments.
+Fp4Plan plan_fp4(long long batch, int n_kv_heads, long long tiles, int n_sm) {
+    Fp4Plan best{1, 1};
+    if (batch <= 0 || n_kv_heads <= 0) return best;
+    double cost = 1e300;
+    for (int per_sm = 1; per_sm <= fa512::decode_fp4_ctas_per_sm(); ++per_sm) {
+        long long groups = static_cast<long long>(per_sm) * n_sm / n_kv_heads;
+        if (groups < 1) groups = 1;
+        const long long all = batch * (tiles > 1 ? tiles : 1), range = (all + groups - 1) / groups;
+        const long long cut = (tiles + range - 1) / range;
+        const double c = (per_sm == 1 ? 0.6 : 1.0) * static_cast<double>(range) + 1.0 + 0.02 * static_cast<double>(cut);
+        if (c < cost) {
+            cost = c;
+            const long long used = (all + range - 1) / range, segments = (batch > 1 ? 2 : 1) * cut + 1;
+            best.groups = static_cast<int>(batch > 1 && tiles > 1 ? groups : used);
+            best.segments = static_cast<int>(tiles <= 1 ? 1 : segments < 1024 ? segments : 1024);
         }
     }
-    return static_cast<int>(best_s);
+    return best;
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -614,8 +620,7 @@ int decode_splits(int bits, int batch, int q_len, int n_q_heads, int n_kv_heads,
     if (bits == 8) return fa512_decode_auto_splits_fp8(batch, q_len, n_q_heads, n_kv_heads, page_size, positions);
     if (batch <= 0 || positions <= 0) return 1;
     const int tile = fa512::decode_fp4_tile_positions();
-    return choose_splits_fp4(static_cast<long long>(batch) * n_kv_heads,
-                             (static_cast<long long>(positions) + tile - 1) / tile, sm_count());
+    return plan_fp4(batch, n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile, sm_count()).segments;
 }
 
 // What a decode call reads: the bits of a cached element (16: bf16; 8: e4m3
@@ -722,6 +727,7 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.group = G;
     p.q_len = q_len;
     p.page_size = page_size;
+    while ((1 << p.page_shift) < page_size) ++p.page_shift;
     const int tile = fp4 ? fa512::decode_fp4_tile_positions() : fa512::decode_tile_positions();
     p.box_rows = page_size < tile ? page_size : tile;
     p.num_pages = num_pages;
@@ -734,6 +740,17 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.n_listed = cache.n_listed;
     p.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
     if (p.tiles_per_split < 1) p.tiles_per_split = 1;
+    if (fp4) {
+        // the rows of a KV head span q_len - 1 positions beside the window, LIST tiles begin at 0
+        const long long seen = p.window > 0 ? static_cast<long long>(p.window) + q_len - 1 : positions;
+        long long most = (positions + tile - 1LL) / tile;
+        if (p.window > 0 && (seen + tile - 1) / tile + 1 < most) most = (seen + tile - 1) / tile + 1;
+        if (most < 1) most = 1;
+        if (batch > 0x7fffffffLL / most) return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
+        p.groups = plan_fp4(batch, n_kv_heads, most, sm_count()).groups;
+        // a sequence of n tiles touches (n - 1) / range + 2 ranges at most
+        p.tiles_per_split = splits > 1 ? static_cast<int>((most - 1) / (splits - 1) + 1) : 1;
+    }
     p.scale_log2 = scale * 1.4426950408889634f;
     // FP8: k_scale scales every score; applied after the bf16 path's factor
     // so that a power-of-two k_scale changes no rounding
@@ -761,9 +778,13 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     } else if (fp4) {
         const uint64_t strides[2] = {fa512::kFp4RowBytes, static_cast<uint64_t>(n_kv_heads) * fa512::kFp4RowBytes};
         const uint32_t box[3] = {fa512::kFp4RowBytes / 4, 1u, static_cast<uint32_t>(p.box_rows)};
-        st = encode_map(&tmk, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, k_pages, 3, dims, strides, box);
+        // Selected pages are read a head at a time: what a load brings into L2 beside its 288
+        // bytes is another head's (64 sequences, 64 of 448 pages: 133 us with 64-byte pieces,
+        // 144 with 128, 156 with 256); dense calls read all heads and do not differ.
+        const CUtensorMapL2promotion l2 = cache.sparse ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+        st = encode_map(&tmk, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, k_pages, 3, dims, strides, box, l2);
         if (st != FA512_OK) return st;
-        st = encode_map(&tmv, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, v_pages, 3, dims, strides, box);
+        st = encode_map(&tmv, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, v_pages, 3, dims, strides, box, l2);
         if (st != FA512_OK) return st;
         e = fa512::launch_decode_fp4(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
     } else {

@@ -7,11 +7,16 @@
 // bits and lies between 2^-10 and 2,688, so it is exact in f16, and the products
 // run on mma.sync with f16 operands and fp32 sums over the cache's exact values.
 //
-// A CTA takes one split of the keys of a (sequence, KV head) in tiles of 64
-// positions, K and V rows brought by TMA into rings of slots.  Four warps form
-// S^T = K Q^T, 16 positions each over the whole head dim with the query rows in N,
-// and their softmax against a reference of their own, and leave P^T and the
-// reference in shared memory; four other warps add V^T P^T of all 64 positions,
+// The key tiles (64 positions) of all sequences stand in a row and are dealt in ranges
+// of equal length to groups of CTAs, one CTA for each KV head, two CTAs to an SM for
+// the whole launch; what a CTA has of a sequence is a segment, with an (O, m, l)
+// partial of its own.  (The heads of a position lie side by side, 288 bytes each:
+// read at about the same time they share the memory's lines.  Ranges that did not
+// keep the heads together took 997 us instead of 690 for 64 sequences of 28,672.)
+// K and V rows come by TMA into rings of slots that run on across segments.  Four
+// warps form S^T = K Q^T, 16 positions each over the whole head dim with the query
+// rows in N, and their softmax against a reference of their own, and leave P^T and
+// the reference in shared memory; four other warps add V^T P^T of all 64 positions,
 // 128 columns of O each.  Nothing is computed twice, and the two groups only meet
 // at barriers in shared memory with a tile of slack, so that both products of
 // different tiles overlap (one group that did both in turn read 5.0 TB/s, each
@@ -47,7 +52,7 @@ constexpr int CTAS_PER_SM = 2;
 constexpr int SLOT = TILE * ROW;                 // 18,432 bytes
 constexpr int KSTEPS = D / 16;
 constexpr int MTILES = D / WARPS / 16;           // m-tiles of 16 columns a warp
-constexpr int META = 8;                          // tiles whose positions are kept
+constexpr int META = 8;                          // tiles and segments whose notes are kept
 
 template <int NT>
 struct Smem {
@@ -57,10 +62,12 @@ struct Smem {
     static constexpr int p = 2 * slots * SLOT;               // [parity][block][nt][lane] uint2
     static constexpr int q = p + 2 * WARPS * NT * 32 * 8;    // NT = 2: [nt][kstep][lane] uint2
     static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);   // [parity][block][8 NT] float
-    static constexpr int sums = ref + 2 * WARPS * 8 * NT * 4;              // [warp][8 NT] float2: reference, sum
-    static constexpr int base = sums + WARPS * 8 * NT * 8;                 // [META][4] first position of 16
+    static constexpr int sums = ref + 2 * WARPS * 8 * NT * 4;              // [parity][warp][8 NT] float2: reference, sum
+    static constexpr int base = sums + 2 * WARPS * 8 * NT * 8;             // [META][4] first position of 16
     static constexpr int row = base + META * 16;                           // [META][4] first row of a run
-    static constexpr int bar = row + META * 16;
+    static constexpr int seg = row + META * 16;                            // [META] int4: see Segment
+    static constexpr int total_tiles = seg + META * 16;
+    static constexpr int bar = total_tiles + 8;
     // barriers: K slots full, V slots full and empty, P buffers full and empty
     static constexpr int total = bar + (3 * slots + 4) * 8;
 };
@@ -313,6 +320,109 @@ __device__ __forceinline__ void add_values_narrow(const uint8_t* block, int warp
     }
 }
 
+struct Item {
+    int len;                                      // live positions
+    int lo;                                       // first position that some row sees
+    int tiles;                                    // LIST: along the list of pages
+    int held;                                     // pages
+};
+template <bool LIST>
+__device__ __forceinline__ Item item_with(const DecodeParams& p, int len) {
+    Item x;
+    x.len = min(max(len, 0), p.len_cap);
+    // union of the rows' bands (the row of token t sees [pos - window + 1, pos])
+    const int w_lo = x.len - p.q_len + 1 - p.window;
+    x.lo = p.window > 0 && w_lo > 0 ? w_lo : 0;
+    x.held = static_cast<int>((static_cast<unsigned>(x.len) + p.page_size - 1) >> p.page_shift);
+    const int end = LIST ? min(p.n_listed, x.held) << p.page_shift : x.len;
+    x.tiles = (end + TILE - 1) / TILE - x.lo / TILE;
+    return x;
+}
+template <bool LIST>
+__device__ __forceinline__ Item item_of(const DecodeParams& p, int b) { return item_with<LIST>(p, p.kv_lens[b]); }
+
+// What the loading warp notes of a segment.
+struct Segment {
+    int b, len;                                   // sequence, live positions
+    int run;                                      // tiles
+    int index;                                    // of the sequence's segments, + LAST for its last one
+    static constexpr int LAST = 1 << 30;
+};
+
+// A CTA's way through its range of tiles.
+template <bool LIST>
+struct Walk {
+    int b;                                        // sequence
+    Item item;
+    int tile;                                     // its next tile
+    int start;                                    // tiles of the sequences before it
+    int left;                                     // tiles of the range that are left
+    __device__ __forceinline__ int run() const { return min(item.tiles - tile, left); }   // those of this sequence
+    __device__ __forceinline__ void next(const DecodeParams& p, int n) {
+        tile += n;
+        left -= n;
+        while (left > 0 && tile == item.tiles) {
+            start += item.tiles;
+            tile = 0;
+            item = item_of<LIST>(p, ++b);
+        }
+    }
+};
+
+// Where the `index`-th of `groups` ranges begins, and the length of the ranges.
+// num_splits = 1: ranges of whole sequences.  All lanes of a warp together.
+template <bool LIST>
+__device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int index, int groups, int* range) {
+    const int lane = threadIdx.x & 31;
+    Walk<LIST> w;
+    w.b = w.tile = w.start = w.left = 0;
+    *range = 0x7fffffff;
+    if (p.num_splits == 1) {
+        const int per = (p.batch + groups - 1) / groups;
+        const int begin = min(p.batch, index * per), end = min(p.batch, begin + per);
+        if (begin == end) return w;
+        int left = 0;
+        for (int b = begin + lane; b < end; b += 32) left += item_of<LIST>(p, b).tiles;
+        w.left = __reduce_add_sync(0xffffffffu, left);
+        w.b = begin;
+        w.item = item_of<LIST>(p, begin);
+        w.next(p, 0);                             // past sequences without a tile
+        return w;
+    }
+    int total = 0, len = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        len = b0 + lane < p.batch ? p.kv_lens[b0 + lane] : 0;
+        total += __reduce_add_sync(0xffffffffu, item_with<LIST>(p, len).tiles);
+    }
+    const int r = max((total + groups - 1) / groups, p.tiles_per_split);
+    const long long at = static_cast<long long>(index) * r;
+    if (at >= total) return w;
+    *range = r;
+    w.left = min(r, total - static_cast<int>(at));
+    // the sequence that the range begins in
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        if (p.batch > 32) len = b0 + lane < p.batch ? p.kv_lens[b0 + lane] : 0;
+        const int n = item_with<LIST>(p, len).tiles;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, w.start + sum > static_cast<int>(at));
+        if (here) {
+            const int l = __ffs(here) - 1;
+            w.b = b0 + l;
+            w.start += __shfl_sync(0xffffffffu, sum - n, l);
+            w.item = item_with<LIST>(p, __shfl_sync(0xffffffffu, len, l));
+            break;
+        }
+        w.start += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    w.tile = static_cast<int>(at) - w.start;
+    return w;
+}
+
 // ROWS: the most query rows (q_len * G) of a KV head.  Up to 8 rows' fragments stay
 // in registers; up to 16 rows' (NT = 2 n-tiles) are read from shared memory.
 //
@@ -342,44 +452,23 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     float2* s_sums = reinterpret_cast<float2*>(smem + Smem::sums);
     int* s_base = reinterpret_cast<int*>(smem + Smem::base);
     int* s_row = reinterpret_cast<int*>(smem + Smem::row);
+    Segment* s_seg = reinterpret_cast<Segment*>(smem + Smem::seg);
+    int* s_total = reinterpret_cast<int*>(smem + Smem::total_tiles);
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Smem::bar);
     uint64_t *v_full = k_full + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS, *p_empty = p_full + 2;
 
-    const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int lane = threadIdx.x & 31;
     const int warp = (threadIdx.x >> 5) & (WARPS - 1);   // within its group
     const bool k_group = threadIdx.x < WARPS * 32;
     const int g = lane >> 2, t = lane & 3;       // mma fragment coordinates
     const int G = p.group, R = p.q_len * G;      // query rows: (token, head) -> token * G + head
     const int ps = p.page_size;
+    const int S = p.num_splits;
+    const int kvh = blockIdx.x % p.n_kv_heads, index = blockIdx.x / p.n_kv_heads;
+    auto row_index = [&](int b, int r) {
+        return (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
+    };
 
-    int len = p.kv_lens[b];
-    if (len < 0 || len > p.len_cap) {
-        if (threadIdx.x == 0 && split == 0 && kvh == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        len = len < 0 ? 0 : p.len_cap;
-    }
-    // union of the rows' bands (the row of token t sees [pos - window + 1, pos])
-    const int hi = len;
-    const int w_lo = len - p.q_len + 1 - p.window;
-    const int lo = (p.window > 0 && w_lo > 0) ? w_lo : 0;
-    // the split's positions: absolute, or counted along the list of pages
-    const int32_t* list = LIST ? list_of(p, b, kvh) : nullptr;
-    int v0, v1;
-    if constexpr (LIST) {
-        const long long first = static_cast<long long>(split) * p.tiles_per_split * TILE;
-        const int all = p.n_listed * ps;
-        v0 = static_cast<int>(min(first, static_cast<long long>(all)));
-        v1 = static_cast<int>(min(first + static_cast<long long>(p.tiles_per_split) * TILE, static_cast<long long>(all)));
-        v1 = list_end(p, list, v0, v1);
-    } else {
-        const long long first = static_cast<long long>(lo / TILE + static_cast<long long>(split) * p.tiles_per_split) * TILE;
-        v0 = static_cast<int>(min(first, static_cast<long long>(hi)));
-        v1 = static_cast<int>(min(first + static_cast<long long>(p.tiles_per_split) * TILE, static_cast<long long>(hi)));
-    }
-    const int n_tiles = v1 > v0 ? (v1 - v0 + TILE - 1) / TILE : 0;
-
-    // A run is box_rows positions of one page.
-    const int box = p.box_rows, runs_per_tile = TILE / box, blocks_per_run = box / 16;
     auto done_with = [&](uint64_t* bar) {        // this warp has read what the barrier guards
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -387,7 +476,6 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     // Every wait of a warp that follows another role's phase of a barrier guards what
     // that role cannot pass before this warp has arrived, so a phase is never missed.
     auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.err)) != 0; };
-    const size_t S = static_cast<size_t>(p.num_splits);
     bool ok = true;                              // the same in all lanes of a warp
     int k_loaded = 0, v_loaded = 0;              // tiles whose load this warp has issued
 
@@ -397,182 +485,227 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         // keeps its largest element below 2^15 (exact for elements down to 2^-39 of
         // that; a score is unscaled before the softmax)
         uint32_t qb[NT == 1 ? KSTEPS : 1][2];
-        float rs[NT][2];                          // 1 / scale of rows 8 n + 2 t, 8 n + 2 t + 1
+        float rs[NT][2];                          // 1 / scale of rows row_of(n, 0), row_of(n, 1)
+        auto load_q = [&](int b) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            // NT = 2: each warp holds a quarter of the k-steps, all of them the maxima
-            const int r = NARROW ? g & 1 : 8 * n + g;
-            const bool row_ok = r < R;
-            const size_t qrow = (static_cast<size_t>(b) * p.q_len + (row_ok ? r / G : 0)) * p.n_q_heads + kvh * G +
-                                (row_ok ? r % G : 0);
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * D);
-            float most = 0.f;
+            for (int n = 0; n < NT; ++n) {
+                // NT = 2: each warp holds a quarter of the k-steps, all of them the maxima
+                const int r = NARROW ? g & 1 : 8 * n + g;
+                const bool row_ok = r < R;
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + row_index(b, row_ok ? r : 0) * D);
+                float most = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-                    if constexpr (NT == 1) {
-                        qb[4 * j + 2 * e][0] = a.x;
-                        qb[4 * j + 2 * e][1] = a.y;
-                        qb[4 * j + 2 * e + 1][0] = a.z;
-                        qb[4 * j + 2 * e + 1][1] = a.w;
-                    }
-                }
-            }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // 2^(14 - E), E = exponent of the maximum (0 or not finite: 1)
-            const int E = (__float_as_uint(most) >> 23) & 0xff;
-            const int biased = min(127 + 14 + 127 - E, 254);
-            const float scale = (most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
-            auto to_f16 = [&](uint32_t w) {
-                return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
-            };
-            if constexpr (NT == 1) {
-#pragma unroll
-                for (int k = 0; k < KSTEPS; ++k) {
-                    const bool mine = !NARROW || g >> 1 == t;
-                    qb[k][0] = mine ? to_f16(qb[k][0]) : 0u;
-                    qb[k][1] = mine ? to_f16(qb[k][1]) : 0u;
-                }
-            } else {
-#pragma unroll
-                for (int j = 2 * warp; j < 2 * warp + 2; ++j)
+                for (int j = 0; j < 8; ++j) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
-                        s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
-                        s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
+                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+                        if constexpr (NT == 1) {
+                            qb[4 * j + 2 * e][0] = a.x;
+                            qb[4 * j + 2 * e][1] = a.y;
+                            qb[4 * j + 2 * e + 1][0] = a.z;
+                            qb[4 * j + 2 * e + 1][1] = a.w;
+                        }
                     }
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                // 2^(14 - E), E = exponent of the maximum (0 or not finite: 1)
+                const int E = (__float_as_uint(most) >> 23) & 0xff;
+                const int biased = min(127 + 14 + 127 - E, 254);
+                const float scale = (most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+                auto to_f16 = [&](uint32_t w) {
+                    return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+                };
+                if constexpr (NT == 1) {
+#pragma unroll
+                    for (int k = 0; k < KSTEPS; ++k) {
+                        const bool mine = !NARROW || g >> 1 == t;
+                        qb[k][0] = mine ? to_f16(qb[k][0]) : 0u;
+                        qb[k][1] = mine ? to_f16(qb[k][1]) : 0u;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 2 * warp; j < 2 * warp + 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
+                            s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
+                            s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
+                        }
+                }
+                rs[n][0] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 0 : 4 * (2 * t));
+                rs[n][1] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 4 : 4 * (2 * t + 1));
             }
-            rs[n][0] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 0 : 4 * (2 * t));
-            rs[n][1] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 4 : 4 * (2 * t + 1));
-        }
-        __syncthreads();                          // barriers, the first tiles' notes, NT = 2: the queries
-
-        // row 8 n + i (NARROW) or 8 n + 2 t + i
+        };
+        auto k_warps = [&]() {                    // the group meets, and agrees on whether to go on
+            uint32_t bad;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                         "bar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(bad)
+                         : "r"(ok ? 0u : 1u), "n"(WARPS * 32)
+                         : "memory");
+            ok = bad == 0;
+        };
+        // this lane's rows: i (NARROW) or 8 n + 2 t + i
         auto row_of = [&](int n, int i) { return NARROW ? i : 8 * n + 2 * t + i; };
-        // their positions (-1: padding row, sees nothing); a row sees
-        // the keys whose distance to it is in [0, reach)
-        int qpos[NT][2];
-        float m[NT][2], l[NT][2];                 // this warp's running reference and sum (a lane's part) of those rows
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = row_of(n, i);
-                qpos[n][i] = r < R ? len - p.q_len + r / G : -1;
-                m[n][i] = -INFINITY;
-                l[n][i] = 0.f;
-            }
         const unsigned reach = p.window > 0 ? static_cast<unsigned>(p.window) : 0x7fffffffu;
         const int ra = turned(g);                 // this lane's rows of 16 positions: ra, ra + 8
+        int range;
+        const int first_b = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range).b;
+        load_q(first_b);                          // (of sequence 0 where the range is empty)
+        __syncthreads();                          // barriers, the first tiles' notes, NT = 2: the queries
+        const int total = *s_total;
 
-        for (int it = 0; it < n_tiles; ++it) {
-            const int slot = it % SLOTS, par = it & 1;
-            if (!ok || !wait(&k_full[slot], it / SLOTS)) {
-                ok = false;
-                break;
+        int it = 0;                               // tiles of the range gone through
+        for (int segment = 0; it < total && ok; ++segment) {
+            if (segment > 0) {
+                // a segment's notes are there once its first tile is asked for
+                if (!wait(&k_full[it % SLOTS], it / SLOTS)) ok = false;
+                if constexpr (NT == 2) k_warps();     // the last sequence's queries are read
+                if (!ok) break;
+                load_q(s_seg[segment & (META - 1)].b);
+                if constexpr (NT == 2) k_warps();
             }
-            const int base = s_base[(it & (META - 1)) * 4 + warp];
-            // (an unloaded block's rows are stale: its scores are masked)
-            float sc[NT][4];
-            const uint8_t* block = smem + Smem::k + slot * SLOT + 16 * warp * ROW;
-            if constexpr (NARROW) scores_narrow(block, lane, qb, sc[0]);
-            else scores<NT>(block, lane, qb, s_q, sc);
-            // ---- softmax against this block's own maximum, rounded up to a whole number,
-            // less 7: weights up to 2^7 keep small ones, and those times a group scale
-            // (448 at most), in f16's range
-            const int kp = base + ra;
-            uint2 frag[NT];
-            float ref[NT][2];
+            const Segment seg = s_seg[segment & (META - 1)];
+            // positions of the rows (-1: padding row, sees nothing); a row sees the keys
+            // whose distance to it is in [0, reach)
+            int qpos[NT][2];
+            float m[NT][2], l[NT][2];             // this warp's running reference and sum (a lane's part) of those rows
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float sv[2][2], cm[2];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const bool va = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp) < reach;
-                    const bool vb = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp - 8) < reach;
-                    sv[i][0] = va ? sc[n][i] * rs[n][i] * p.scale_log2 : -INFINITY;
-                    sv[i][1] = vb ? sc[n][2 + i] * rs[n][i] * p.scale_log2 : -INFINITY;
-                    cm[i] = fmaxf(sv[i][0], sv[i][1]);
+                    const int r = row_of(n, i);
+                    qpos[n][i] = r < R ? seg.len - p.q_len + r / G : -1;
+                    m[n][i] = -INFINITY;
+                    l[n][i] = 0.f;
                 }
+            for (const int end = it + seg.run; it < end; ++it) {
+                const int slot = it % SLOTS, par = it & 1;
+                if (!wait(&k_full[slot], it / SLOTS)) {
+                    ok = false;
+                    break;
+                }
+                const int base = s_base[(it & (META - 1)) * 4 + warp];
+                // (an unloaded block's rows are stale: its scores are masked)
+                float sc[NT][4];
+                const uint8_t* block = smem + Smem::k + slot * SLOT + 16 * warp * ROW;
+                if constexpr (NARROW) scores_narrow(block, lane, qb, sc[0]);
+                else scores<NT>(block, lane, qb, s_q, sc);
+                // ---- softmax against this block's own maximum, rounded up to a whole number,
+                // less 7: weights up to 2^7 keep small ones, and those times a group scale
+                // (448 at most), in f16's range
+                const int kp = base + ra;
+                uint2 frag[NT];
+                float ref[NT][2];
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    const float x0 = __shfl_xor_sync(0xffffffffu, cm[0], off);
-                    const float x1 = __shfl_xor_sync(0xffffffffu, cm[1], off);
-                    cm[0] = fmaxf(cm[0], x0);
-                    cm[1] = fmaxf(cm[1], x1);
+                for (int n = 0; n < NT; ++n) {
+                    float sv[2][2], cm[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool va = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp) < reach;
+                        const bool vb = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp - 8) < reach;
+                        sv[i][0] = va ? sc[n][i] * rs[n][i] * p.scale_log2 : -INFINITY;
+                        sv[i][1] = vb ? sc[n][2 + i] * rs[n][i] * p.scale_log2 : -INFINITY;
+                        cm[i] = fmaxf(sv[i][0], sv[i][1]);
+                    }
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                        const float x0 = __shfl_xor_sync(0xffffffffu, cm[0], off);
+                        const float x1 = __shfl_xor_sync(0xffffffffu, cm[1], off);
+                        cm[0] = fmaxf(cm[0], x0);
+                        cm[1] = fmaxf(cm[1], x1);
+                    }
+                    float pr[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ref[n][i] = ceilf(cm[i]) - 7.f;
+                        const float sh = finite_ref(ref[n][i]);
+                        pr[i][0] = fast_exp2(sv[i][0] - sh);
+                        pr[i][1] = fast_exp2(sv[i][1] - sh);
+                        // the sums keep the fp32 weights
+                        const float mn = fmaxf(m[n][i], ref[n][i]), to = finite_ref(mn);
+                        l[n][i] = l[n][i] * fast_exp2(m[n][i] - to) + (pr[i][0] + pr[i][1]) * fast_exp2(ref[n][i] - to);
+                        m[n][i] = mn;
+                    }
+                    // P rounds to f16: 2^-11 of a weight, or 2^-32 of the block's largest
+                    if constexpr (NARROW) {
+                        frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
+                    } else {
+                        frag[n].x = transpose8x8(pack_f16x2(pr[0][0], pr[1][0]));
+                        frag[n].y = transpose8x8(pack_f16x2(pr[0][1], pr[1][1]));
+                    }
                 }
-                float pr[2][2];
+                if (it >= 2 && !wait(&p_empty[par], it / 2 - 1)) {
+                    ok = false;
+                    break;
+                }
+                float* out_ref = s_ref + (par * WARPS + warp) * 8 * NT;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (NARROW)         // a row's 16: positions 2 i, 2 i + 1, 2 i + 8, 2 i + 9 together
+                        s_p2[(par * WARPS + warp) * 32 + 16 * (t & 1) + (g >> 1) * 4 + (t & 2) + (g & 1)] =
+                            static_cast<uint16_t>(frag[n].x);
+                    else
+                        s_p[((par * WARPS + warp) * NT + n) * 32 + lane] = frag[n];
+                    if (g == 0 && (!NARROW || t == 0))
+                        *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(ref[n][0], ref[n][1]);
+                }
+                done_with(&p_full[par]);
+            }
+            // ---- (m, l) of the segment: the four warps' sums brought to one reference
+            float2* sums = s_sums + (segment & 1) * WARPS * 8 * NT;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    ref[n][i] = ceilf(cm[i]) - 7.f;
-                    const float sh = finite_ref(ref[n][i]);
-                    pr[i][0] = fast_exp2(sv[i][0] - sh);
-                    pr[i][1] = fast_exp2(sv[i][1] - sh);
-                    // the sums keep the fp32 weights
-                    const float mn = fmaxf(m[n][i], ref[n][i]), to = finite_ref(mn);
-                    l[n][i] = l[n][i] * fast_exp2(m[n][i] - to) + (pr[i][0] + pr[i][1]) * fast_exp2(ref[n][i] - to);
-                    m[n][i] = mn;
-                }
-                // P rounds to f16: 2^-11 of a weight, or 2^-32 of the block's largest
-                if constexpr (NARROW) {
-                    frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
-                } else {
-                    frag[n].x = transpose8x8(pack_f16x2(pr[0][0], pr[1][0]));
-                    frag[n].y = transpose8x8(pack_f16x2(pr[0][1], pr[1][1]));
-                }
-            }
-            if (it >= 2 && !wait(&p_empty[par], it / 2 - 1)) ok = false;
-            if (!ok) break;
-            float* out_ref = s_ref + (par * WARPS + warp) * 8 * NT;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (NARROW)             // a row's 16: positions 2 i, 2 i + 1, 2 i + 8, 2 i + 9 together
-                    s_p2[(par * WARPS + warp) * 32 + 16 * (t & 1) + (g >> 1) * 4 + (t & 2) + (g & 1)] =
-                        static_cast<uint16_t>(frag[n].x);
-                else
-                    s_p[((par * WARPS + warp) * NT + n) * 32 + lane] = frag[n];
-                if (g == 0 && (!NARROW || t == 0))
-                    *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(ref[n][0], ref[n][1]);
+                    for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
+                    if (g == 0 && (!NARROW || t == 0)) sums[warp * 8 * NT + row_of(n, i)] = make_float2(m[n][i], l[n][i]);
+                }
+            k_warps();
+            if (ok && warp == 0 && lane < R) {
+                float ref = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, sums[w * 8 * NT + lane].x);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const float2 x = sums[w * 8 * NT + lane];
+                    sum += x.y * fast_exp2(x.x - finite_ref(ref));
+                }
+                if (sum != sum && ref == -INFINITY) ref = 0.f;   // only scores of NaN: not an empty segment
+                float2* ml = reinterpret_cast<float2*>(p.ws_ml) + row_index(seg.b, lane) * S;
+                const int mine = seg.index & ~Segment::LAST;
+                ml[mine] = make_float2(ref, ref == -INFINITY ? 0.f : sum);
+                if (seg.index & Segment::LAST)    // the places behind it are empty
+                    for (int i = mine + 1; i < S; ++i) ml[i] = make_float2(-INFINITY, 0.f);
             }
-            done_with(&p_full[par]);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
-                if (g == 0 && (!NARROW || t == 0)) s_sums[warp * 8 * NT + row_of(n, i)] = make_float2(m[n][i], l[n][i]);
-            }
     } else {
-        // ---- loads, by warp 0 of this group: lane l keeps the first row and position
-        // of run run0 + l
-        const int held = (len + ps - 1) / ps;    // pages of the sequence
-        const int n_runs = n_tiles * runs_per_tile;
-        int run0 = 0, run_row = -1, run_base = -1;
+        // ---- loads, by warp 0 of this group, which walks ahead: lane l keeps the first
+        // row and position of run run0 + l of the sequence (a run: box_rows positions of a page)
+        const int box = p.box_rows, runs_per_tile = TILE / box, blocks_per_run = box / 16;
+        Walk<LIST> ahead = {};
+        int range = 0, segments = 0;
+        int run0 = 0, run_row = -1, run_base = -1, seg_tile = 0, seg_end = 0;
         auto look_up = [&]() {
-            const int r = run0 + lane;
             run_row = run_base = -1;
-            if (r >= n_runs) return;
-            const int v = v0 + r * box;
-            int lp = v / ps, at = v;
+            const int v = (ahead.item.lo / TILE) * TILE + (run0 + lane) * box;
+            const Item& x = ahead.item;
+            int lp = v >> p.page_shift, at = v;
             if constexpr (LIST) {
-                if (v >= v1) return;
-                const int off = v - lp * ps;
-                lp = list_page(p, list, lp, held);
+                const int off = v & (ps - 1);
+                if (lp >= min(p.n_listed, x.held)) return;
+                lp = list_page(p, list_of(p, ahead.b, kvh), lp, x.held);
                 if (lp < 0) return;
                 at = lp * ps + off;
             }
-            if (at >= hi || at + box <= lo) return;
-            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
+            if (at >= x.len || at + box <= x.lo) return;
+            const int page = p.page_table[static_cast<size_t>(ahead.b) * p.max_pages_per_seq + lp];
             if (page < 0 || page >= p.num_pages) {
                 report_error(p.err, FA512_DEVICE_ERR_INDEX);
                 return;
@@ -580,10 +713,23 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             run_row = page * ps + (at - lp * ps);
             run_base = at;
         };
-        // K rows of tile i into their slot; what the V load and the masks need is noted
+        // K rows of tile i of the range into their slot; what the V load and the masks need is noted
         auto load_k = [&](int i) {
-            if (i >= n_tiles) return;
-            const int slot = i % SLOTS, r = i * runs_per_tile;
+            if (seg_tile == seg_end) {            // on to the next segment
+                if (ahead.left == 0) return;
+                if (i > 0) ahead.next(p, seg_end - ahead.tile);
+                if (ahead.left == 0) return;
+                seg_tile = ahead.tile;
+                seg_end = ahead.tile + ahead.run();
+                if (lane == 0)
+                    s_seg[segments & (META - 1)] = {ahead.b, ahead.item.len, ahead.run(),
+                                                    (S == 1 ? 0 : index - ahead.start / range) +
+                                                        (seg_end == ahead.item.tiles ? Segment::LAST : 0)};
+                ++segments;
+                run0 = seg_tile * runs_per_tile;
+                look_up();
+            }
+            const int slot = i % SLOTS, r = seg_tile * runs_per_tile;
             if (r >= run0 + 32) {
                 run0 += 32;
                 look_up();
@@ -601,10 +747,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             __syncwarp();
             if (mine) tma_load_3d(smem + Smem::k + slot * SLOT + lane * box * ROW, &tmk, &k_full[slot], 0, kvh, row);
             k_loaded = i + 1;
+            ++seg_tile;
         };
         // V rows of tile i once the slot's last tile is read
         auto load_v = [&](int i) {
-            if (i >= n_tiles) return;
+            if (i >= k_loaded) return;
             const int slot = i % SLOTS;
             if (i >= SLOTS && !wait(&v_empty[slot], i / SLOTS - 1)) {
                 ok = false;
@@ -633,156 +780,162 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 tma_prefetch_desc(&tmv);
             }
             __syncwarp();
-            look_up();
+            ahead = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range);
+            if (lane == 0) *s_total = ahead.left;
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) {
                 load_k(i);
                 if (i < SLOTS - 1) load_v(i);
             }
+        } else if (warp == 3) {
+            // lengths out of range; sequences without a tile leave partials that say so
+            for (int b = blockIdx.x * 32 + lane; b < p.batch; b += gridDim.x * 32)
+                if (p.kv_lens[b] < 0 || p.kv_lens[b] > p.len_cap) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+                if (item_of<LIST>(p, b).tiles == 0)
+                    for (int i = lane; i < p.q_len * p.n_q_heads * S; i += 32)
+                        reinterpret_cast<float2*>(p.ws_ml)[static_cast<size_t>(b) * p.q_len * p.n_q_heads * S + i] =
+                            make_float2(-INFINITY, 0.f);
         }
         __syncthreads();                          // barriers, the first tiles' notes
-        // references of rows 2 t + i and g (NARROW: i and g % 2)
-        float m[NT][2], mg[NT];
-        float o[NT][MTILES][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = mg[n] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < MTILES; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-        }
-        for (int it = 0; it < n_tiles && ok; ++it) {
-            const int slot = it % SLOTS, par = it & 1;
-            if (!wait(&p_full[par], it / 2)) {
+        const int total = *s_total;
+
+        int it = 0;
+        for (int segment = 0; it < total && ok; ++segment) {
+            // (P of a segment's first tile comes after its notes)
+            if (!wait(&p_full[it & 1], it / 2)) {
                 ok = false;
                 break;
             }
-            // ---- one reference for the tile
-            uint32_t pb[WARPS][NT][2];
+            const Segment seg = s_seg[segment & (META - 1)];
+            // references of rows 2 t + i and g (NARROW: i and g % 2)
+            float m[NT][2], mg[NT];
+            float o[NT][MTILES][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float* all = s_ref + par * WARPS * 8 * NT + 8 * n;
-                float mn[2] = {m[n][0], m[n][1]}, rg[WARPS];
+                m[n][0] = m[n][1] = mg[n] = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + (NARROW ? 0 : 2 * t));
-                    rg[w] = NARROW ? (g & 1 ? x.y : x.x) : all[w * 8 * NT + g];
-                    mn[0] = fmaxf(mn[0], x.x);
-                    mn[1] = fmaxf(mn[1], x.y);
-                    mg[n] = fmaxf(mg[n], rg[w]);
+                for (int i = 0; i < MTILES; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+            }
+            const int w_lo = seg.len - p.q_len + 1 - p.window, lo = p.window > 0 && w_lo > 0 ? w_lo : 0, hi = seg.len;
+            for (const int end = it + seg.run; it < end; ++it) {
+                const int slot = it % SLOTS, par = it & 1;
+                if (!wait(&p_full[par], it / 2)) {
+                    ok = false;
+                    break;
                 }
-                float al[2];
+                // ---- one reference for the tile
+                uint32_t pb[WARPS][NT][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    al[i] = fast_exp2(m[n][i] - finite_ref(mn[i]));
-                    m[n][i] = mn[i];
-                }
-                if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+                for (int n = 0; n < NT; ++n) {
+                    const float* all = s_ref + par * WARPS * 8 * NT + 8 * n;
+                    float mn[2] = {m[n][0], m[n][1]}, rg[WARPS];
 #pragma unroll
-                    for (int i = 0; i < MTILES; ++i) {
-                        o[n][i][0] *= al[0];
-                        o[n][i][1] *= al[1];
-                        o[n][i][2] *= al[0];
-                        o[n][i][3] *= al[1];
+                    for (int w = 0; w < WARPS; ++w) {
+                        const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + (NARROW ? 0 : 2 * t));
+                        rg[w] = NARROW ? (g & 1 ? x.y : x.x) : all[w * 8 * NT + g];
+                        mn[0] = fmaxf(mn[0], x.x);
+                        mn[1] = fmaxf(mn[1], x.y);
+                        mg[n] = fmaxf(mg[n], rg[w]);
+                    }
+                    float al[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        al[i] = fast_exp2(m[n][i] - finite_ref(mn[i]));
+                        m[n][i] = mn[i];
+                    }
+                    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+                        for (int i = 0; i < MTILES; ++i) {
+                            o[n][i][0] *= al[0];
+                            o[n][i][1] *= al[1];
+                            o[n][i][2] *= al[0];
+                            o[n][i][3] *= al[1];
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < WARPS; ++w) {
+                        const float f = fast_exp2(rg[w] - finite_ref(mg[n]));
+                        const uint32_t f2 = pack_f16x2(f, f);
+                        const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (par * WARPS + w) * 32 + 16 * (g & 1) + 4 * t)
+                                               : s_p[((par * WARPS + w) * NT + n) * 32 + lane];
+                        pb[w][n][0] = mul_f16x2(x.x, f2);
+                        pb[w][n][1] = mul_f16x2(x.y, f2);
                     }
                 }
+                done_with(&p_empty[par]);
+                // P of this tile says that its K is read
+                if (warp == 0) {
+                    load_k(it + SLOTS);
+                    load_v(it + SLOTS - 1);
+                }
+                if (!ok || !wait(&v_full[slot], it / SLOTS)) {
+                    ok = false;
+                    break;
+                }
+                // ---- A position that no row sees gets the scale 0 (its bytes may be anything:
+                // codes are finite); lane l: positions l and l + 32 of the tile
+                uint8_t* vst = smem + Smem::v + slot * SLOT;
+                const int4 base4 = *reinterpret_cast<const int4*>(s_base + (it & (META - 1)) * 4);
+                const int first = min(min(base4.x, base4.y), min(base4.z, base4.w));
+                const int last = max(max(base4.x, base4.y), max(base4.z, base4.w));
+                if (first < lo || last + 16 > hi) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int base = lane < 16 ? (i ? base4.z : base4.x) : (i ? base4.w : base4.y);
+                        const int kp = base + (lane & 15);
+                        if (base < 0 || kp < lo || kp >= hi)
+                            *reinterpret_cast<uint2*>(vst + (lane + 32 * i) * ROW + CODES + 8 * warp) = make_uint2(0u, 0u);
+                    }
+                    fence_proxy_async_smem();     // before the slot is loaded again
+                    __syncwarp();
+                }
+                // ---- O^T += V^T P^T for this warp's columns, 16 positions at a time
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
-                    const float f = fast_exp2(rg[w] - finite_ref(mg[n]));
-                    const uint32_t f2 = pack_f16x2(f, f);
-                    const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (par * WARPS + w) * 32 + 16 * (g & 1) + 4 * t)
-                                           : s_p[((par * WARPS + w) * NT + n) * 32 + lane];
-                    pb[w][n][0] = mul_f16x2(x.x, f2);
-                    pb[w][n][1] = mul_f16x2(x.y, f2);
+                    if constexpr (NARROW) add_values_narrow(vst + 16 * w * ROW, warp, lane, pb[w][0], o[0]);
+                    else add_values<NT>(vst + 16 * w * ROW, warp, lane, pb[w], o);
                 }
+                done_with(&v_empty[slot]);
             }
-            done_with(&p_empty[par]);
-            // P of this tile says that its K is read
-            if (warp == 0) {
-                load_k(it + SLOTS);
-                load_v(it + SLOTS - 1);
-            }
-            if (!ok || !wait(&v_full[slot], it / SLOTS)) {
-                ok = false;
-                break;
-            }
-            // ---- A position that no row sees gets the scale 0 (its bytes may be anything:
-            // codes are finite); lane l: positions l and l + 32 of the tile
-            uint8_t* vst = smem + Smem::v + slot * SLOT;
-            const int4 base4 = *reinterpret_cast<const int4*>(s_base + (it & (META - 1)) * 4);
-            const int first = min(min(base4.x, base4.y), min(base4.z, base4.w));
-            const int last = max(max(base4.x, base4.y), max(base4.z, base4.w));
-            if (first < lo || last + 16 > hi) {
+            // ---- the segment's partial, unnormalised and times v_scale
+            const int mine = seg.index & ~Segment::LAST;
+            const float f = p.o_scale;
+            if constexpr (NARROW) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int base = lane < 16 ? (i ? base4.z : base4.x) : (i ? base4.w : base4.y);
-                    const int kp = base + (lane & 15);
-                    if (base < 0 || kp < lo || kp >= hi)
-                        *reinterpret_cast<uint2*>(vst + (lane + 32 * i) * ROW + CODES + 8 * warp) = make_uint2(0u, 0u);
+                for (int r = 0; r < 2; ++r) {
+                    if (r >= R || (g & 3) != t) continue;
+                    float* dst = p.ws_o + (row_index(seg.b, r) * S + mine) * D + 128 * warp + 16 * t + 8 * (g >> 2);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
+                                make_float4(o[0][4 * h + 2 * j][r] * f, o[0][4 * h + 2 * j][2 + r] * f,
+                                            o[0][4 * h + 2 * j + 1][r] * f, o[0][4 * h + 2 * j + 1][2 + r] * f);
                 }
-                fence_proxy_async_smem();         // before the slot is loaded again
-                __syncwarp();
-            }
-            // ---- O^T += V^T P^T for this warp's columns, 16 positions at a time
+            } else {
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                if constexpr (NARROW) add_values_narrow(vst + 16 * w * ROW, warp, lane, pb[w][0], o[0]);
-                else add_values<NT>(vst + 16 * w * ROW, warp, lane, pb[w], o);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 8 * n + 2 * t + i;
+                        if (r >= R) continue;
+                        float4* dst = reinterpret_cast<float4*>(p.ws_o + (row_index(seg.b, r) * S + mine) * D +
+                                                                128 * warp + 16 * g);
+#pragma unroll
+                        for (int j = 0; j < MTILES / 2; ++j)
+                            dst[j] = make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
+                                                 o[n][2 * j + 1][2 + i] * f);
+                    }
             }
-            done_with(&v_empty[slot]);
         }
-        // ---- this split's partial, unnormalised and times v_scale
-        const float f = ok ? p.o_scale : 0.f;
-        if constexpr (NARROW) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (r >= R || (g & 3) != t) continue;
-                const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
-                float* dst = p.ws_o + (hq * S + split) * D + 128 * warp + 16 * t + 8 * (g >> 2);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
-                            make_float4(o[0][4 * h + 2 * j][r] * f, o[0][4 * h + 2 * j][2 + r] * f,
-                                        o[0][4 * h + 2 * j + 1][r] * f, o[0][4 * h + 2 * j + 1][2 + r] * f);
-            }
-        } else
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * n + 2 * t + i;
-                if (r >= R) continue;
-                const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
-                float4* dst = reinterpret_cast<float4*>(p.ws_o + (hq * S + split) * D + 128 * warp + 16 * g);
-#pragma unroll
-                for (int j = 0; j < MTILES / 2; ++j)
-                    dst[j] = make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
-                                         o[n][2 * j + 1][2 + i] * f);
-            }
     }
     // A wait that ran out: bounded waits for the copies in flight, so that none
     // lands after this CTA has gone.
-    const bool failed = __syncthreads_or(!ok);
-    if (failed) {
+    if (__syncthreads_or(!ok)) {
         for (int i = max(0, k_loaded - SLOTS); i < k_loaded; ++i) mbar_wait(&k_full[i % SLOTS], (i / SLOTS) & 1, p.err);
         for (int i = max(0, v_loaded - SLOTS); i < v_loaded; ++i) mbar_wait(&v_full[i % SLOTS], (i / SLOTS) & 1, p.err);
-    }
-    // ---- (m, l): the K warps' sums brought to one reference
-    if (threadIdx.x < R) {
-        const int r = threadIdx.x;
-        float ref = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) ref = fmaxf(ref, s_sums[w * 8 * NT + r].x);
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const float2 x = s_sums[w * 8 * NT + r];
-            sum += x.y * fast_exp2(x.x - finite_ref(ref));
-        }
-        if (sum != sum && ref == -INFINITY) ref = 0.f;   // only scores of NaN: not an empty split
-        const size_t hq = (static_cast<size_t>(b) * p.q_len + r / G) * p.n_q_heads + kvh * G + r % G;
-        p.ws_ml[(hq * S + split) * 2 + 0] = failed ? -INFINITY : ref;
-        p.ws_ml[(hq * S + split) * 2 + 1] = failed || ref == -INFINITY ? 0.f : sum;
     }
 }
 
@@ -791,7 +944,7 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeP
     constexpr int SMEM = Smem<(ROWS > 8 ? 2 : 1)>::total;
     cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<ROWS, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    const dim3 grid(p.num_splits, p.n_kv_heads, p.batch);
+    const int grid = p.groups * p.n_kv_heads;
     decode_fp4_kernel<ROWS, LIST><<<grid, THREADS, SMEM, stream>>>(tmk, tmv, p);
     return cudaGetLastError();
 }

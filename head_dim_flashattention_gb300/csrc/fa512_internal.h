@@ -31,6 +31,8 @@ struct DecodeParams {
     int len_cap;                   // min(max_kv_len, max_pages_per_seq * page_size)
     int window;
     int tiles_per_split, num_splits;
+    int page_shift;                // page_size = 1 << page_shift
+    int groups;                    // 4-bit kernel: ranges that the tiles of all sequences are dealt in, tiles_per_split long at least
     float scale_log2;              // scale * log2(e)
     unsigned* err;                 // device error word
     // Selected pages (null: all of the band): [batch, n_kv_heads, n_listed] logical
