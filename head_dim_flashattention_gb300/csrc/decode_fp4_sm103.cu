@@ -47,7 +47,7 @@ constexpr int ROW = kFp4RowBytes;
 constexpr int CODES = 256;                       // bytes of codes in a row
 constexpr int TILE = 64;                         // positions per tile
 constexpr int WARPS = 4;                         // per group: 16 positions of a tile, or 128 columns of O, each
-constexpr int THREADS = 2 * WARPS * 32;
+constexpr int THREADS = 3 * WARPS * 32;          // K group, V group, loads
 constexpr int CTAS_PER_SM = 2;
 constexpr int SLOT = TILE * ROW;                 // 18,432 bytes
 constexpr int KSTEPS = D / 16;
@@ -64,12 +64,11 @@ struct Smem {
     static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);   // [parity][block][8 NT] float
     static constexpr int sums = ref + 2 * WARPS * 8 * NT * 4;              // [parity][warp][8 NT] float2: reference, sum
     static constexpr int base = sums + 2 * WARPS * 8 * NT * 8;             // [META][4] first position of 16
-    static constexpr int row = base + META * 16;                           // [META][4] first row of a run
-    static constexpr int seg = row + META * 16;                            // [META] int4: see Segment
+    static constexpr int seg = base + META * 16;                           // [META] int4: see Segment
     static constexpr int total_tiles = seg + META * 16;
     static constexpr int bar = total_tiles + 8;
-    // barriers: K slots full, V slots full and empty, P buffers full and empty
-    static constexpr int total = bar + (3 * slots + 4) * 8;
+    // barriers: K and V slots full and empty, P buffers full and empty
+    static constexpr int total = bar + (4 * slots + 4) * 8;
 };
 static_assert(CTAS_PER_SM * (Smem<1>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
 static_assert(CTAS_PER_SM * (Smem<2>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
@@ -451,15 +450,15 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     float* s_ref = reinterpret_cast<float*>(smem + Smem::ref);
     float2* s_sums = reinterpret_cast<float2*>(smem + Smem::sums);
     int* s_base = reinterpret_cast<int*>(smem + Smem::base);
-    int* s_row = reinterpret_cast<int*>(smem + Smem::row);
     Segment* s_seg = reinterpret_cast<Segment*>(smem + Smem::seg);
     int* s_total = reinterpret_cast<int*>(smem + Smem::total_tiles);
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Smem::bar);
-    uint64_t *v_full = k_full + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS, *p_empty = p_full + 2;
+    uint64_t *k_empty = k_full + SLOTS, *v_full = k_empty + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS,
+             *p_empty = p_full + 2;
 
     const int lane = threadIdx.x & 31;
     const int warp = (threadIdx.x >> 5) & (WARPS - 1);   // within its group
-    const bool k_group = threadIdx.x < WARPS * 32;
+    const int role = threadIdx.x / (WARPS * 32); // 0 K group, 1 V group, 2 loads
     const int g = lane >> 2, t = lane & 3;       // mma fragment coordinates
     const int G = p.group, R = p.q_len * G;      // query rows: (token, head) -> token * G + head
     const int ps = p.page_size;
@@ -477,9 +476,13 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     // that role cannot pass before this warp has arrived, so a phase is never missed.
     auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.err)) != 0; };
     bool ok = true;                              // the same in all lanes of a warp
-    int k_loaded = 0, v_loaded = 0;              // tiles whose load this warp has issued
+    int loaded = 0;                              // tiles whose load this warp has issued
 
-    if (k_group) {
+    // The launch's 80 registers a thread are dealt anew: a share for each role.
+    constexpr int K_REGS = NT == 1 ? 128 : 88, V_REGS = NT == 1 ? 80 : 120, LOAD_REGS = 32;
+    static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * 80, "no more than the launch has");
+    if (role == 0) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K_REGS));
         // ---- Q^T fragments: b0/b1 of k-step 4 j + s hold row g's elements 64 j + 16
         // t + 4 s + {0, 1} / {2, 3}, in f16 after a power-of-two scale per row that
         // keeps its largest element below 2^15 (exact for elements down to 2^-39 of
@@ -596,6 +599,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 const uint8_t* block = smem + Smem::k + slot * SLOT + 16 * warp * ROW;
                 if constexpr (NARROW) scores_narrow(block, lane, qb, sc[0]);
                 else scores<NT>(block, lane, qb, s_q, sc);
+                done_with(&k_empty[slot]);
                 // ---- softmax against this block's own maximum, rounded up to a whole number,
                 // less 7: weights up to 2^7 keep small ones, and those times a group scale
                 // (448 at most), in f16's range
@@ -685,118 +689,9 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int i = mine + 1; i < S; ++i) ml[i] = make_float2(-INFINITY, 0.f);
             }
         }
-    } else {
-        // ---- loads, by warp 0 of this group, which walks ahead: lane l keeps the first
-        // row and position of run run0 + l of the sequence (a run: box_rows positions of a page)
-        const int box = p.box_rows, runs_per_tile = TILE / box, blocks_per_run = box / 16;
-        Walk<LIST> ahead = {};
-        int range = 0, segments = 0;
-        int run0 = 0, run_row = -1, run_base = -1, seg_tile = 0, seg_end = 0;
-        auto look_up = [&]() {
-            run_row = run_base = -1;
-            const int v = (ahead.item.lo / TILE) * TILE + (run0 + lane) * box;
-            const Item& x = ahead.item;
-            int lp = v >> p.page_shift, at = v;
-            if constexpr (LIST) {
-                const int off = v & (ps - 1);
-                if (lp >= min(p.n_listed, x.held)) return;
-                lp = list_page(p, list_of(p, ahead.b, kvh), lp, x.held);
-                if (lp < 0) return;
-                at = lp * ps + off;
-            }
-            if (at >= x.len || at + box <= x.lo) return;
-            const int page = p.page_table[static_cast<size_t>(ahead.b) * p.max_pages_per_seq + lp];
-            if (page < 0 || page >= p.num_pages) {
-                report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                return;
-            }
-            run_row = page * ps + (at - lp * ps);
-            run_base = at;
-        };
-        // K rows of tile i of the range into their slot; what the V load and the masks need is noted
-        auto load_k = [&](int i) {
-            if (seg_tile == seg_end) {            // on to the next segment
-                if (ahead.left == 0) return;
-                if (i > 0) ahead.next(p, seg_end - ahead.tile);
-                if (ahead.left == 0) return;
-                seg_tile = ahead.tile;
-                seg_end = ahead.tile + ahead.run();
-                if (lane == 0)
-                    s_seg[segments & (META - 1)] = {ahead.b, ahead.item.len, ahead.run(),
-                                                    (S == 1 ? 0 : index - ahead.start / range) +
-                                                        (seg_end == ahead.item.tiles ? Segment::LAST : 0)};
-                ++segments;
-                run0 = seg_tile * runs_per_tile;
-                look_up();
-            }
-            const int slot = i % SLOTS, r = seg_tile * runs_per_tile;
-            if (r >= run0 + 32) {
-                run0 += 32;
-                look_up();
-            }
-            // lanes 0 .. 3: the run of their 16 positions
-            const int base = __shfl_sync(0xffffffffu, run_base, (r - run0 + lane / blocks_per_run) & 31);
-            const int row = __shfl_sync(0xffffffffu, run_row, (r - run0 + lane) & 31);
-            const bool mine = lane < runs_per_tile && row >= 0;
-            const unsigned some = __ballot_sync(0xffffffffu, mine);
-            const int meta = (i & (META - 1)) * 4;
-            if (lane < 4) s_base[meta + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
-            if (lane < runs_per_tile) s_row[meta + lane] = row;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], __popc(some) * box * ROW);
-            __syncwarp();
-            if (mine) tma_load_3d(smem + Smem::k + slot * SLOT + lane * box * ROW, &tmk, &k_full[slot], 0, kvh, row);
-            k_loaded = i + 1;
-            ++seg_tile;
-        };
-        // V rows of tile i once the slot's last tile is read
-        auto load_v = [&](int i) {
-            if (i >= k_loaded) return;
-            const int slot = i % SLOTS;
-            if (i >= SLOTS && !wait(&v_empty[slot], i / SLOTS - 1)) {
-                ok = false;
-                return;
-            }
-            const int row = lane < runs_per_tile ? s_row[(i & (META - 1)) * 4 + lane] : -1;
-            const unsigned some = __ballot_sync(0xffffffffu, row >= 0);
-            if (lane == 0) mbar_arrive_expect_tx(&v_full[slot], __popc(some) * box * ROW);
-            __syncwarp();
-            if (row >= 0) tma_load_3d(smem + Smem::v + slot * SLOT + lane * box * ROW, &tmv, &v_full[slot], 0, kvh, row);
-            v_loaded = i + 1;
-        };
-        if (warp == 0) {
-            if (lane == 0) {
-                for (int i = 0; i < SLOTS; ++i) {
-                    mbar_init(&k_full[i], 1);
-                    mbar_init(&v_full[i], 1);
-                    mbar_init(&v_empty[i], WARPS);
-                }
-                for (int i = 0; i < 2; ++i) {
-                    mbar_init(&p_full[i], WARPS);
-                    mbar_init(&p_empty[i], WARPS);
-                }
-                fence_mbar_init();
-                tma_prefetch_desc(&tmk);
-                tma_prefetch_desc(&tmv);
-            }
-            __syncwarp();
-            ahead = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range);
-            if (lane == 0) *s_total = ahead.left;
-#pragma unroll
-            for (int i = 0; i < SLOTS; ++i) {
-                load_k(i);
-                if (i < SLOTS - 1) load_v(i);
-            }
-        } else if (warp == 3) {
-            // lengths out of range; sequences without a tile leave partials that say so
-            for (int b = blockIdx.x * 32 + lane; b < p.batch; b += gridDim.x * 32)
-                if (p.kv_lens[b] < 0 || p.kv_lens[b] > p.len_cap) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-            for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-                if (item_of<LIST>(p, b).tiles == 0)
-                    for (int i = lane; i < p.q_len * p.n_q_heads * S; i += 32)
-                        reinterpret_cast<float2*>(p.ws_ml)[static_cast<size_t>(b) * p.q_len * p.n_q_heads * S + i] =
-                            make_float2(-INFINITY, 0.f);
-        }
+    } else if (role == 1) {
+        if constexpr (V_REGS < 80) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(V_REGS));
+        else if constexpr (V_REGS > 80) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(V_REGS));
         __syncthreads();                          // barriers, the first tiles' notes
         const int total = *s_total;
 
@@ -864,12 +759,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     }
                 }
                 done_with(&p_empty[par]);
-                // P of this tile says that its K is read
-                if (warp == 0) {
-                    load_k(it + SLOTS);
-                    load_v(it + SLOTS - 1);
-                }
-                if (!ok || !wait(&v_full[slot], it / SLOTS)) {
+                if (!wait(&v_full[slot], it / SLOTS)) {
                     ok = false;
                     break;
                 }
@@ -930,12 +820,124 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     }
             }
         }
+    } else {
+        // ---- loads: warp 0 of K, warp 1 of V
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOAD_REGS));
+        if (warp == 0) {
+            if (lane == 0) {
+                for (int i = 0; i < SLOTS; ++i) {
+                    mbar_init(&k_full[i], 1);
+                    mbar_init(&k_empty[i], WARPS);
+                    mbar_init(&v_full[i], 1);
+                    mbar_init(&v_empty[i], WARPS);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(&p_full[i], WARPS);
+                    mbar_init(&p_empty[i], WARPS);
+                }
+                fence_mbar_init();
+            }
+            __syncwarp();
+        }
+        int range = 0;
+        Walk<LIST> walk = {};
+        if (warp < 2) walk = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range);
+        if (warp == 0 && lane == 0) *s_total = walk.left;
+        uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
+        const CUtensorMap* map = warp == 0 ? &tmk : &tmv;
+        uint8_t* ring = smem + (warp == 0 ? Smem::k : Smem::v);
+        // A run is box_rows positions of one page; lane l keeps the first row and position
+        // of run run0 + l of the sequence.
+        const int box = p.box_rows, runs_per_tile = TILE / box, blocks_per_run = box / 16;
+        int run0 = 0, run_row = -1, run_base = -1;
+        auto look_up = [&]() {
+            run_row = run_base = -1;
+            const Item& x = walk.item;
+            const int v = (x.lo / TILE) * TILE + (run0 + lane) * box;
+            int lp = v >> p.page_shift, at = v;
+            if constexpr (LIST) {
+                const int off = v & (ps - 1);
+                if (lp >= min(p.n_listed, x.held)) return;
+                lp = list_page(p, list_of(p, walk.b, kvh), lp, x.held);
+                if (lp < 0) return;
+                at = lp * ps + off;
+            }
+            if (at >= x.len || at + box <= x.lo) return;
+            const int page = p.page_table[static_cast<size_t>(walk.b) * p.max_pages_per_seq + lp];
+            if (page < 0 || page >= p.num_pages) {
+                report_error(p.err, FA512_DEVICE_ERR_INDEX);
+                return;
+            }
+            run_row = page * ps + (at - lp * ps);
+            run_base = at;
+        };
+        // tile i of the range, the sequence's `tile`-th, into its slot; K: what the masks need is noted
+        auto load = [&](int i, int tile) {
+            const int slot = i % SLOTS, r = tile * runs_per_tile;
+            if (r >= run0 + 32) {
+                run0 += 32;
+                look_up();
+            }
+            const int row = __shfl_sync(0xffffffffu, run_row, (r - run0 + lane) & 31);
+            const bool mine = lane < runs_per_tile && row >= 0;
+            const unsigned some = __ballot_sync(0xffffffffu, mine);
+            if (warp == 0) {
+                // lanes 0 .. 3: the run of their 16 positions
+                const int base = __shfl_sync(0xffffffffu, run_base, (r - run0 + lane / blocks_per_run) & 31);
+                if (lane < 4) s_base[(i & (META - 1)) * 4 + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(some) * box * ROW);
+            __syncwarp();
+            if (mine) tma_load_3d(ring + slot * SLOT + lane * box * ROW, map, &full[slot], 0, kvh, row);
+            loaded = i + 1;
+        };
+        // the first SLOTS tiles find their slots empty, and V's barriers wait for the one below
+        bool started = false;
+        auto start = [&]() {
+            if (!started) __syncthreads();        // barriers, the first tiles' notes
+            started = true;
+        };
+        if (warp >= 1) start();
+        if (warp == 2) {
+            // lengths out of range; sequences without a tile leave partials that say so
+            for (int b = blockIdx.x * 32 + lane; b < p.batch; b += gridDim.x * 32)
+                if (p.kv_lens[b] < 0 || p.kv_lens[b] > p.len_cap) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+                if (item_of<LIST>(p, b).tiles == 0)
+                    for (int i = lane; i < p.q_len * p.n_q_heads * S; i += 32)
+                        reinterpret_cast<float2*>(p.ws_ml)[static_cast<size_t>(b) * p.q_len * p.n_q_heads * S + i] =
+                            make_float2(-INFINITY, 0.f);
+        }
+        int it = 0;
+        for (int segment = 0; walk.left > 0 && ok; ++segment) {
+            const int run = walk.run(), end = it + run, from = walk.tile - it;
+            if (warp == 0 && lane == 0)
+                s_seg[segment & (META - 1)] = {walk.b, walk.item.len, run,
+                                               (S == 1 ? 0 : index - walk.start / range) +
+                                                   (walk.tile + run == walk.item.tiles ? Segment::LAST : 0)};
+            run0 = walk.tile * runs_per_tile;
+            look_up();
+            for (; it < end; ++it) {
+                if (it >= SLOTS) {
+                    start();
+                    if (!wait(&empty[it % SLOTS], it / SLOTS - 1)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                load(it, from + it);
+                if (it == 0) start();             // (the others wait for the first segment's notes)
+            }
+            walk.next(p, run);
+        }
+        start();
     }
     // A wait that ran out: bounded waits for the copies in flight, so that none
     // lands after this CTA has gone.
-    if (__syncthreads_or(!ok)) {
-        for (int i = max(0, k_loaded - SLOTS); i < k_loaded; ++i) mbar_wait(&k_full[i % SLOTS], (i / SLOTS) & 1, p.err);
-        for (int i = max(0, v_loaded - SLOTS); i < v_loaded; ++i) mbar_wait(&v_full[i % SLOTS], (i / SLOTS) & 1, p.err);
+    if (__syncthreads_or(!ok) && role == 2 && warp < 2) {
+        uint64_t* full = warp == 0 ? k_full : v_full;
+        for (int i = max(0, loaded - SLOTS); i < loaded; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, p.err);
     }
 }
 
