@@ -1188,6 +1188,7 @@ fa512_status append_call(const void* k_new, const void* v_new, int64_t kb, int64
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.err = err;
+    while ((1 << p.page_shift) < page_size) ++p.page_shift;
     e = fa512::launch_cache_append(p, bits, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
     return FA512_OK;

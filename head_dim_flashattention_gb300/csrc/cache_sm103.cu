@@ -126,10 +126,11 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // quotient y / scale, ties to even; both saturate.  A group that holds NaN gets
 // the NaN scale; a scale that rounds to 0 makes the codes 0.
 //
-// A warp rounds one row, a group of 16 elements a lane, up to APPEND_RUN rows
-// with all loads first.  17 divisions a group cost more issue slots than the bytes
-// take (8 sequences of up to 4,096 tokens, 4 heads: 170 us), so tensor scales that
-// are powers of two have a path without them (to_4bit_pow2).
+// A warp rounds one row of K and of V, a group of 16 elements a lane.  Bound: bytes (8
+// sequences of up to 4,096 new tokens, 4 heads: 335 MB in 55 us, 6.1 TB/s); the 18
+// divisions of a group cost more issue slots than that takes (170 us), so tensor
+// scales that are powers of two have a path without them (to_4bit_pow2).  One token of
+// 16 sequences takes 2.1 us.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -141,10 +142,10 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
     return r;
 }
 
-// The group's scale byte for max |y|, and its value.
-__device__ __forceinline__ float group_scale(float most, uint8_t* byte) {
+// E4M3 nearest to x: its byte, and its value.
+__device__ __forceinline__ float to_e4m3(float x, uint8_t* byte) {
     uint16_t s8;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(__fdiv_rn(most, 6.f)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(x));
     uint32_t s2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(s8));
     float s;
@@ -168,7 +169,7 @@ __device__ __forceinline__ uint2 to_4bit(const uint4 a, const uint4 b, float ten
         most = fmaxf(most, fabsf(y[i]));
         nan |= y[i] != y[i];
     }
-    const float s = group_scale(most, scale_byte);
+    const float s = to_e4m3(__fdiv_rn(most, 6.f), scale_byte);
     float z[2][8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i >> 3][i & 7] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
@@ -176,12 +177,16 @@ __device__ __forceinline__ uint2 to_4bit(const uint4 a, const uint4 b, float ten
     return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
 }
 
-// The same for a tensor scale whose reciprocal `by` is a power of two.  Then y has
-// 8 significant bits and the scale s 4, so y / s, where it is no midpoint of two
-// E2M1 values, lies 2^-11 or more from all of them (the lowest bit of a y above s / 8
-// is at least 2^-11 s, and a midpoint times s is a multiple of it).  x times the rounded by / s, off by
-// less than 2^-23 of it, plus 1.5 * 2^11 rounds to a multiple of 2^-12: midpoints
-// come out exactly, and nothing crosses one.
+// The same for a tensor scale whose reciprocal `by` is a power of two, without a
+// division.  Then y has 8 significant bits.
+//   Scale: max |y| / 6, where it is no midpoint of two E4M3 values (5 bits), differs
+//   from all of them by 2^-11 of it or more; the product with the rounded 1/6, off by
+//   2^-23 of it, rounded to 16 bits hits the midpoints exactly and crosses none.
+//   Codes: y / s, where it is no midpoint of two E2M1 values, lies 2^-11 or more from
+//   all of them (the lowest bit of a y above s / 8 is at least 2^-11 s, and a midpoint
+//   times s, which has 4 bits, is a multiple of it).  x times by / s, off by 2^-22 of
+//   it, plus 1.5 * 2^11 rounds to a multiple of 2^-12: midpoints come out exactly, and
+//   nothing crosses one.
 __device__ __forceinline__ uint2 to_4bit_pow2(const uint4 a, const uint4 b, float by, uint8_t* scale_byte) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t top = 0;                                     // largest magnitudes of the halves, NaN where there is one
@@ -190,8 +195,11 @@ __device__ __forceinline__ uint2 to_4bit_pow2(const uint4 a, const uint4 b, floa
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"((top << 16) | (top >> 16)));
     const float most = __uint_as_float(top & 0xffff0000u);
     const bool nan = most != most;
-    const float s = group_scale(nan ? 0.f : most * by, scale_byte);
-    const float r = s > 0.f ? __fdiv_rn(1.f, s) * by : 0.f;
+    const float sixth = most * by * (1.f / 6.f);
+    const float s = to_e4m3(nan ? 0.f : __uint_as_float((__float_as_uint(sixth) + 0x80u) & ~0xffu), scale_byte);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // 0 < s: 2^-9 at least
+    r *= by;
     constexpr float SNAP = 3072.f;
     float z[2][8];
 #pragma unroll
@@ -199,10 +207,11 @@ __device__ __forceinline__ uint2 to_4bit_pow2(const uint4 a, const uint4 b, floa
         const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
         const float q = __fadd_rn(__fmaf_rn(x, r, SNAP), -SNAP);
         // its sign also where it came to 0
-        z[i >> 3][i & 7] = s > 0.f ? __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u)) : 0.f;
+        z[i >> 3][i & 7] = __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u));
     }
     if (nan) *scale_byte = 0x7f;
-    return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+    const uint2 codes = make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+    return s > 0.f ? codes : make_uint2(0u, 0u);
 }
 
 template <bool POW2>
@@ -212,50 +221,33 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_fp4_kernel(const Append
     const int len = p.kv_lens[b];
     if (n_new < 0 || n_new > p.q_len) {
         if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-        n_new = 0;
+        n_new = 0;                                        // no telling where its tokens belong
     }
-    uint4 k[APPEND_RUN][2], v[APPEND_RUN][2];
-    size_t at[APPEND_RUN];
-    bool there[APPEND_RUN];
-#pragma unroll
-    for (int r = 0; r < APPEND_RUN; ++r) {
-        const unsigned row = (blockIdx.x * APPEND_RUN + r) * (APPEND_THREADS / 32) + (threadIdx.x >> 5);
-        const int t = static_cast<int>(row / static_cast<unsigned>(p.n_kv_heads));
-        const int h = static_cast<int>(row % static_cast<unsigned>(p.n_kv_heads));
-        const long long pos = static_cast<long long>(len) - n_new + t;
-        there[r] = t < n_new;
-        if (there[r] && (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size)) {
-            if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-            there[r] = false;
-        }
-        if (!there[r]) continue;
-        const int lp = static_cast<int>(pos) / p.page_size;
-        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
-        const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + b * p.k_batch_stride + t * p.k_token_stride) + h * 64 + 2 * lane;
-        const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + b * p.v_batch_stride + t * p.v_token_stride) + h * 64 + 2 * lane;
-        k[r][0] = ks[0];
-        k[r][1] = ks[1];
-        v[r][0] = vs[0];
-        v[r][1] = vs[1];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-            there[r] = false;
-        }
-        at[r] = ((static_cast<size_t>(page) * p.page_size + static_cast<int>(pos) % p.page_size) * p.n_kv_heads + h) *
-                kFp4RowBytes;
+    const unsigned row = blockIdx.x * (APPEND_THREADS / 32) + (threadIdx.x >> 5);
+    const int t = static_cast<int>(row / static_cast<unsigned>(p.n_kv_heads));
+    const int h = static_cast<int>(row - static_cast<unsigned>(t) * static_cast<unsigned>(p.n_kv_heads));
+    if (t >= n_new) return;
+    const long long pos = static_cast<long long>(len) - n_new + t;
+    if (pos < 0 || pos >= static_cast<long long>(p.max_pages_per_seq) * p.page_size) {
+        if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        return;
     }
-#pragma unroll
-    for (int r = 0; r < APPEND_RUN; ++r) {
-        if (!there[r]) continue;
-        uint8_t *kd = static_cast<uint8_t*>(p.k_pages) + at[r], *vd = static_cast<uint8_t*>(p.v_pages) + at[r];
-        uint8_t s;
-        *reinterpret_cast<uint2*>(kd + 8 * lane) = POW2 ? to_4bit_pow2(k[r][0], k[r][1], p.k_scale, &s)
-                                                         : to_4bit(k[r][0], k[r][1], p.k_scale, &s);
-        kd[256 + lane] = s;
-        *reinterpret_cast<uint2*>(vd + 8 * lane) = POW2 ? to_4bit_pow2(v[r][0], v[r][1], p.v_scale, &s)
-                                                         : to_4bit(v[r][0], v[r][1], p.v_scale, &s);
-        vd[256 + lane] = s;
+    const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + (static_cast<int>(pos) >> p.page_shift)];
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + b * p.k_batch_stride + t * p.k_token_stride) + h * 64 + 2 * lane;
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + b * p.v_batch_stride + t * p.v_token_stride) + h * 64 + 2 * lane;
+    const uint4 k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
+    if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        return;
     }
+    const size_t at = ((static_cast<size_t>(page) * p.page_size + (static_cast<int>(pos) & (p.page_size - 1))) * p.n_kv_heads + h) *
+                      kFp4RowBytes;
+    uint8_t *kd = static_cast<uint8_t*>(p.k_pages) + at, *vd = static_cast<uint8_t*>(p.v_pages) + at;
+    uint8_t s;
+    *reinterpret_cast<uint2*>(kd + 8 * lane) = POW2 ? to_4bit_pow2(k0, k1, p.k_scale, &s) : to_4bit(k0, k1, p.k_scale, &s);
+    kd[256 + lane] = s;
+    *reinterpret_cast<uint2*>(vd + 8 * lane) = POW2 ? to_4bit_pow2(v0, v1, p.v_scale, &s) : to_4bit(v0, v1, p.v_scale, &s);
+    vd[256 + lane] = s;
 }
 
 // ------------------------------------------------------------------ compact
@@ -674,7 +666,7 @@ cudaError_t launch_cache_append(const AppendParams& p, int element_bits, cudaStr
     by.v_scale = 1.f / p.v_scale;
     if (element_bits == 4) {
         const long long rows = static_cast<long long>(p.q_len) * p.n_kv_heads;
-        constexpr int ROWS = APPEND_THREADS / 32 * APPEND_RUN;
+        constexpr int ROWS = APPEND_THREADS / 32;
         const dim3 grid(static_cast<unsigned>((rows + ROWS - 1) / ROWS), p.batch);
         if (both) append_fp4_kernel<true><<<grid, APPEND_THREADS, 0, stream>>>(by);
         else append_fp4_kernel<false><<<grid, APPEND_THREADS, 0, stream>>>(p);

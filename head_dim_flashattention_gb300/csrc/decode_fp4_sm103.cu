@@ -898,6 +898,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (!started) __syncthreads();        // barriers, the first tiles' notes
             started = true;
         };
+        if (warp == 3 && lane == 0) {
+            tma_prefetch_desc(&tmk);
+            tma_prefetch_desc(&tmv);
+        }
         if (warp >= 1) start();
         if (warp == 2) {
             // lengths out of range; sequences without a tile leave partials that say so

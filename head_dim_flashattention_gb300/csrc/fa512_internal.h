@@ -146,6 +146,7 @@ struct AppendParams {
     const int32_t *page_table, *kv_lens, *q_lens;
     float k_scale, v_scale;        // E4M3 and 4-bit caches
     int batch, q_len, n_kv_heads, page_size, num_pages, max_pages_per_seq;
+    int page_shift;                // page_size = 1 << page_shift
     unsigned* err;
 };
 // element_bits: 16 (bf16), 8 (E4M3) or 4 (E2M1 with group scales)

@@ -30,9 +30,9 @@ constexpr int D = 512;
 // ------------------------------------------------------------------- bounds
 //
 // A block takes one touched page of one KV head; a thread 8 elements of a row (16
-// of a coded one, in 4 bits those of one scale), the rows dealt to 4 or 8 groups of
-// threads whose results meet in shared memory.  NaN elements make both bounds NaN.
-constexpr int BOUNDS_THREADS = 256;
+// of a coded one, in 4 bits those of one scale), the rows dealt to 4 groups of
+// threads, 16 of them in flight, whose results meet in shared memory.  NaN elements make both bounds NaN.
+__host__ __device__ constexpr int bounds_threads(int bits) { return bits == 16 ? 256 : 128; }
 
 struct MinMax {
     uint32_t lo, hi;
@@ -57,11 +57,11 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(bounds_threads(BITS)) bounds_kernel(const BoundsParams p) {
     constexpr int ROW = BITS == 16 ? 2 * D : BITS == 8 ? D : kFp4RowBytes;
     constexpr int PAIRS = BITS == 16 ? 4 : 8;       // x 2 elements of a thread
     constexpr int LANES = D / (2 * PAIRS);          // threads of a row: 64, 32
-    constexpr int GROUPS = BOUNDS_THREADS / LANES;
+    constexpr int GROUPS = bounds_threads(BITS) / LANES;
     constexpr bool F16 = BITS != 16;
     __shared__ uint32_t s_lo[GROUPS - 1][D / 2], s_hi[GROUPS - 1][D / 2];
     const int b = blockIdx.z, h = blockIdx.y;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsPara
     const uint32_t inf = F16 ? 0x7c007c00u : 0x7f807f80u;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) m[i] = {inf, inf | 0x80008000u};
-    constexpr int RUN = 8;                          // rows in flight
+    constexpr int RUN = 16;                         // rows in flight of a thread
     for (int r0 = grp; r0 < live; r0 += RUN * GROUPS) {
         uint4 x[RUN];
         uint8_t scale[RUN];
@@ -173,15 +173,19 @@ __global__ void __launch_bounds__(BOUNDS_THREADS) bounds_kernel(const BoundsPara
 
 // ------------------------------------------------------------------- scores
 //
-// A warp scores two pages at a time, the bounds of its next two on their way: lane
-// l holds channels 8 l .. 8 l + 7 and 256 + 8 l .. of them, goes through the query
-// rows (in shared memory, as fp32) and keeps each page's largest score.  max(q lo,
-// q hi) is max(q, 0) hi + min(q, 0) lo, of which one term is 0: two packed
-// multiply-adds a pair of channels, and each sum below rounds once.
+// The bounds of a warp's pages come through a ring of its own in shared memory, a
+// page (2 KiB) a stage; it scores two at a time.  Lane l holds channels 8 l .. 8 l +
+// 7 and 256 + 8 l .. of them, goes through the query rows (in shared memory, as fp32)
+// and keeps each page's largest score.  max(q lo, q hi) is max(q, 0) hi + min(q, 0)
+// lo, of which one term is 0: two packed multiply-adds a pair of channels, and each
+// sum below rounds once.
 constexpr int SCORE_WARPS = 4;
 constexpr int SCORE_PAGES = 2;
-constexpr int SCORE_BLOCKS = 6 * 152;                // blocks to spread the pages over
-constexpr int SCORE_ROWS = 16;                       // most query rows of a KV head
+constexpr int SCORE_STAGES = 6;                      // pages in the ring, a multiple of SCORE_PAGES
+constexpr int SCORE_BLOCKS = 12 * 152;               // blocks to spread the pages over (a third of them: 45 us instead of 42)
+constexpr int PAGE_BYTES = 2 * D * 2;                // a page's bounds
+// shared memory: the warps' rings, then the query rows as fp32
+constexpr int score_smem(int rows) { return SCORE_WARPS * SCORE_STAGES * PAGE_BYTES + rows * D * 4; }
 
 // Unsigned integers in the order of the scores, -0 and 0 equal.  Largest of all,
 // with the pages that are always chosen, are those with a NaN or infinite score:
@@ -208,14 +212,68 @@ __device__ __forceinline__ void unpack8(const uint4 x, float2 (&f)[4]) {
     for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
+// Sums over the lanes of four values at once, each by halves (lanes 16 apart, then 8,
+// ...): lane l gets value l / 8's.
+__device__ __forceinline__ float sum_of_four(const float (&v)[4], int lane) {
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                    // values i and i + 2
+        const float other = __shfl_xor_sync(0xffffffffu, lane & 16 ? v[i] : v[i + 2], 16);
+        x[i] = (lane & 16 ? v[i + 2] : v[i]) + other;
+    }
+    const float other = __shfl_xor_sync(0xffffffffu, lane & 8 ? x[0] : x[1], 8);
+    float y = (lane & 8 ? x[1] : x[0]) + other;
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    return y;
+}
+
 __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float4 s_q[SCORE_ROWS][2][2][32];     // [row][half of the channels][4 of 8][lane]
+    extern __shared__ __align__(16) uint8_t score_raw[];
     const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring = score_raw + warp * SCORE_STAGES * PAGE_BYTES;
+    // [row][half of the channels][4 of 8][lane]
+    float4* s_q = reinterpret_cast<float4*>(score_raw + SCORE_WARPS * SCORE_STAGES * PAGE_BYTES);
     const int len = length_of(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-    const int held = (len + p.page_size - 1) / p.page_size;
+    const int held = static_cast<int>((static_cast<unsigned>(len) + p.page_size - 1) / p.page_size);
     const int step = gridDim.x * SCORE_WARPS * SCORE_PAGES;
     if (blockIdx.x * SCORE_WARPS * SCORE_PAGES >= held || held <= p.n_select) return;   // all pages are chosen
+    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
+    // the i-th page of this warp; of its pool page: -1 none (always chosen, or past the
+    // end), -2 outside the pool
+    auto number = [&](int i) {
+        return (blockIdx.x * SCORE_WARPS + warp) * SCORE_PAGES + (i / SCORE_PAGES) * step + i % SCORE_PAGES;
+    };
+    auto page_of = [&](int i) {
+        const int lp = number(i);
+        if (lp >= held || lp < p.n_first || lp >= held - p.n_last) return -1;
+        const int page = table[lp];
+        return page < 0 || page >= p.num_pages ? -2 : page;
+    };
+    // lane l keeps the pool pages of the 32 of this warp's pages from `batch` on
+    int batch = 0, mine = page_of(lane);
+    auto load = [&](int i) {
+        if (i >= batch + 32) {
+            batch += 32;
+            mine = page_of(batch + lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, mine, i & 31);
+        if (page >= 0) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(p.bounds) + (static_cast<size_t>(page) * p.n_kv_heads + h) * PAGE_BYTES;
+            const uint32_t dst = smem_u32(ring + (i % SCORE_STAGES) * PAGE_BYTES);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (32 * j + lane) * 16),
+                             "l"(src + (32 * j + lane) * 16) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return page;
+    };
+    int pages[SCORE_STAGES];                         // of the stages, the next one to be scored first
+#pragma unroll
+    for (int i = 0; i < SCORE_STAGES; ++i) pages[i] = load(i);
+
     const int R = p.q_len * p.group;
     const int r0 = max(0, p.q_len - len) * p.group;  // rows of tokens before the sequence's first position see nothing
     for (int i = threadIdx.x; i < (R - r0) * 64; i += SCORE_WARPS * 32) {
@@ -223,126 +281,123 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
         const size_t row = (static_cast<size_t>(b) * p.q_len + r / p.group) * p.n_q_heads + h * p.group + r % p.group;
         float2 f[4];
         unpack8(reinterpret_cast<const uint4*>(p.q + row * D)[c], f);
-        s_q[r][c >> 5][0][c & 31] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        s_q[r][c >> 5][1][c & 31] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        float4* dst = s_q + ((r * 2 + (c >> 5)) * 2) * 32 + (c & 31);
+        dst[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        dst[32] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
     }
     __syncthreads();
-    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
     uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
-    // the page of lp: -1 none (always chosen, or past the end), -2 outside the pool
-    auto page_of = [&](int lp) {
-        if (lp >= held || lp < p.n_first || lp >= held - p.n_last) return -1;
-        const int page = table[lp];
-        return page < 0 || page >= p.num_pages ? -2 : page;
-    };
-    uint4 raw[SCORE_PAGES][4];
-    int page[SCORE_PAGES], page_next[SCORE_PAGES];
-    auto load = [&]() {
-#pragma unroll
-        for (int i = 0; i < SCORE_PAGES; ++i) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + (static_cast<size_t>(max(page[i], 0)) * p.n_kv_heads + h) * 2 * D);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[i][j] = page[i] >= 0 ? src[32 * j + lane] : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    int lp0 = (blockIdx.x * SCORE_WARPS + warp) * SCORE_PAGES;
-#pragma unroll
-    for (int i = 0; i < SCORE_PAGES; ++i) page[i] = page_of(lp0 + i);
-    load();
-#pragma unroll
-    for (int i = 0; i < SCORE_PAGES; ++i) page_next[i] = page_of(lp0 + step + i);
-    for (; lp0 < held; lp0 += step) {
+    for (int i = 0; number(i) < held; i += SCORE_PAGES) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(SCORE_STAGES - SCORE_PAGES) : "memory");
+        __syncwarp();
         float2 lo[SCORE_PAGES][8], hi[SCORE_PAGES][8];
-        float best[SCORE_PAGES];
-        int now[SCORE_PAGES];
 #pragma unroll
-        for (int i = 0; i < SCORE_PAGES; ++i) {
+        for (int k = 0; k < SCORE_PAGES; ++k) {
+            const uint4* src = reinterpret_cast<const uint4*>(ring + ((i + k) % SCORE_STAGES) * PAGE_BYTES) + lane;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float2 f[4];
-                unpack8(raw[i][j], f);
+                unpack8(src[32 * j], f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lo[i][4 * j + e] = f[e];
-                unpack8(raw[i][2 + j], f);
+                for (int e = 0; e < 4; ++e) lo[k][4 * j + e] = f[e];
+                unpack8(src[64 + 32 * j], f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) hi[i][4 * j + e] = f[e];
+                for (int e = 0; e < 4; ++e) hi[k][4 * j + e] = f[e];
             }
-            best[i] = -INFINITY;
-            now[i] = page[i];
-            page[i] = page_next[i];
         }
-        if (lp0 + step < held) load();
+        int now[SCORE_PAGES];
 #pragma unroll
-        for (int i = 0; i < SCORE_PAGES; ++i) page_next[i] = page_of(lp0 + 2 * step + i);
-        bool nan[SCORE_PAGES] = {};
-        for (int r = r0; r < R; ++r) {
-            float2 x[SCORE_PAGES][4];
+        for (int k = 0; k < SCORE_PAGES; ++k) now[k] = pages[k];
+        __syncwarp();                                // the stages are read
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int k = 0; k < SCORE_STAGES - SCORE_PAGES; ++k) pages[k] = pages[k + SCORE_PAGES];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 q4 = s_q[r][j][e >> 1][lane];
-                    const float2 q = e & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
-                    const float2 up = make_float2(fmaxf(q.x, 0.f), fmaxf(q.y, 0.f));
-                    const float2 down = make_float2(fminf(q.x, 0.f), fminf(q.y, 0.f));
+        for (int k = 0; k < SCORE_PAGES; ++k) pages[SCORE_STAGES - SCORE_PAGES + k] = load(i + SCORE_STAGES + k);
+
+        // two rows at a time (the last one twice where their number is odd): lane l gets
+        // the sum of row l / 8 % 2 and page l / 16
+        float best = -INFINITY;
+        bool nan = false;
+        for (int r = r0; r < R; r += 2) {
+            float v[4];
 #pragma unroll
-                    for (int i = 0; i < SCORE_PAGES; ++i) {
-                        x[i][e] = ffma2(down, lo[i][4 * j + e], j ? x[i][e] : make_float2(0.f, 0.f));
-                        x[i][e] = ffma2(up, hi[i][4 * j + e], x[i][e]);
+            for (int e2 = 0; e2 < 2; ++e2) {
+                const float4* q = s_q + min(r + e2, R - 1) * 128 + lane;
+                float2 x[SCORE_PAGES][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 q4 = q[(2 * j + (e >> 1)) * 32];
+                        const float2 qe = e & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+                        const float2 up = make_float2(fmaxf(qe.x, 0.f), fmaxf(qe.y, 0.f));
+                        const float2 down = make_float2(fminf(qe.x, 0.f), fminf(qe.y, 0.f));
+#pragma unroll
+                        for (int k = 0; k < SCORE_PAGES; ++k) {
+                            x[k][e] = ffma2(down, lo[k][4 * j + e], j ? x[k][e] : make_float2(0.f, 0.f));
+                            x[k][e] = ffma2(up, hi[k][4 * j + e], x[k][e]);
+                        }
                     }
+#pragma unroll
+                for (int k = 0; k < SCORE_PAGES; ++k) {
+                    // the eight of this lane: 0 + 4, 1 + 5, ..., then halves of those
+                    const float2 d = fadd2(fadd2(x[k][0], x[k][2]), fadd2(x[k][1], x[k][3]));
+                    v[2 * k + e2] = d.x + d.y;
                 }
-#pragma unroll
-            for (int i = 0; i < SCORE_PAGES; ++i) {
-                // the eight of this lane: 0 + 4, 1 + 5, ..., then halves of those
-                const float2 a = fadd2(x[i][0], x[i][2]), c = fadd2(x[i][1], x[i][3]);
-                const float2 d = fadd2(a, c);
-                float s = d.x + d.y;
-#pragma unroll
-                for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-                nan[i] |= s != s;
-                best[i] = fmaxf(best[i], s);
             }
+            const float s = sum_of_four(v, lane);
+            nan |= s != s;
+            best = fmaxf(best, s);
         }
-        if (lane < SCORE_PAGES && lp0 + lane < held) {
-            uint32_t key = 0;
-#pragma unroll
-            for (int i = 0; i < SCORE_PAGES; ++i)
-                if (lane == i) {
-                    if (now[i] == -2) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                    key = now[i] == -1 || nan[i] ? KEY_MOST : now[i] >= 0 ? key_of(best[i]) : 0u;   // outside: lowest
-                }
-            keys[lp0 + lane] = key;
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 8));
+        nan |= __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, 8) != 0;
+        const int k = lane >> 4, lp = number(i + k);
+        if ((lane & 15) == 0 && lp < held) {
+            const int page = k ? now[1] : now[0];
+            if (page == -2) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+            // (outside the pool: lowest)
+            keys[lp] = page == -2 ? 0u : page == -1 || nan ? KEY_MOST : key_of(best);
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------- choice
 //
 // A block per (sequence, KV head) finds the n-th largest key by its four bytes
 // from the top, a histogram of 256 each, then writes the pages above it, and the
-// lowest of those equal to it, in rising order.
+// lowest of those equal to it, in rising order.  The first SHARED keys wait in shared
+// memory, the rest is read again in each pass.  (A warp with 32 keys a lane in
+// registers, searching bit by bit, takes twice as long: its code runs once, and
+// fetching it is what that takes.)
 constexpr int CHOOSE_THREADS = 256;
+constexpr int CHOOSE_WARPS = CHOOSE_THREADS / 32;
+constexpr int SHARED = 4096;
 
 __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int hist[256], s_warp[2][CHOOSE_THREADS / 32];
+    __shared__ uint32_t s_keys[SHARED];
+    __shared__ int hist[256], s_warp[2][CHOOSE_WARPS];
     __shared__ int s_digit, s_left;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // also where no scores were needed: for whatever ran before
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = length_of(p, b, false);
-    const int held = (len + p.page_size - 1) / p.page_size;
+    const int held = static_cast<int>((static_cast<unsigned>(len) + p.page_size - 1) / p.page_size);
     int32_t* out = p.selected + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.n_select;
     if (held <= p.n_select) {
         for (int i = tid; i < p.n_select; i += CHOOSE_THREADS) out[i] = i < held ? i : -1;
         return;
     }
     const uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
+    for (int i = tid; i < min(held, SHARED); i += CHOOSE_THREADS) s_keys[i] = keys[i];
+    // (a thread only reads the keys it wrote itself)
+    auto key_at = [&](int i) { return i < SHARED ? s_keys[i] : keys[i]; };
     uint32_t prefix = 0;
     int left = p.n_select;                           // to take among the keys that begin with the prefix
     for (int shift = 24; shift >= 0; shift -= 8) {
         hist[tid] = 0;
         __syncthreads();
         for (int i = tid; i < held; i += CHOOSE_THREADS) {
-            const uint32_t k = keys[i];
+            const uint32_t k = key_at(i);
             if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
         }
         __syncthreads();
@@ -357,7 +412,8 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectPara
         if (lane == 31) s_warp[0][warp] = sum;
         __syncthreads();
         int before = sum - mine;
-        for (int w = 0; w < warp; ++w) before += s_warp[0][w];
+#pragma unroll
+        for (int w = 0; w < CHOOSE_WARPS; ++w) before += w < warp ? s_warp[0][w] : 0;
         if (before < left && before + mine >= left) {
             s_digit = 255 - tid;
             s_left = left - before;
@@ -365,33 +421,34 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectPara
         __syncthreads();
         prefix = (prefix << 8) | static_cast<uint32_t>(s_digit);
         left = s_left;
-        __syncthreads();
     }
     int above = 0, equal = 0;                        // chosen before this run of pages: above the n-th key, equal to it
     for (int i0 = 0; i0 < held; i0 += CHOOSE_THREADS) {
         const int i = i0 + tid;
-        const uint32_t k = i < held ? keys[i] : 0u;
+        const uint32_t k = i < held ? key_at(i) : 0u;
         const bool gt = i < held && k > prefix, eq = i < held && k == prefix;
         const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        __syncthreads();
         if (lane == 0) {
             s_warp[0][warp] = __popc(mg);
             s_warp[1][warp] = __popc(me);
         }
         __syncthreads();
         int g0 = above, e0 = equal;
-        for (int w = 0; w < CHOOSE_THREADS / 32; ++w) {
+#pragma unroll
+        for (int w = 0; w < CHOOSE_WARPS; ++w) {
+            const int a = s_warp[0][w], e = s_warp[1][w];
             if (w < warp) {
-                g0 += s_warp[0][w];
-                e0 += s_warp[1][w];
+                g0 += a;
+                e0 += e;
             }
-            above += s_warp[0][w];
-            equal += s_warp[1][w];
+            above += a;
+            equal += e;
         }
         const unsigned lower = (1u << lane) - 1u;
         g0 += __popc(mg & lower);
         e0 += __popc(me & lower);
         if (gt || (eq && e0 < left)) out[g0 + min(e0, left)] = i;
-        __syncthreads();
     }
 }
 
@@ -401,20 +458,23 @@ cudaError_t launch_page_bounds(const BoundsParams& p, int element_bits, cudaStre
     using namespace select;
     const int touched = min((p.q_len - 1) / p.page_size + ((p.q_len - 1) % p.page_size != 0) + 1, p.max_pages_per_seq);
     const dim3 grid(touched, p.n_kv_heads, p.batch);
-    if (element_bits == 16) bounds_kernel<16><<<grid, BOUNDS_THREADS, 0, stream>>>(p);
-    else if (element_bits == 8) bounds_kernel<8><<<grid, BOUNDS_THREADS, 0, stream>>>(p);
-    else bounds_kernel<4><<<grid, BOUNDS_THREADS, 0, stream>>>(p);
+    if (element_bits == 16) bounds_kernel<16><<<grid, bounds_threads(16), 0, stream>>>(p);
+    else if (element_bits == 8) bounds_kernel<8><<<grid, bounds_threads(8), 0, stream>>>(p);
+    else bounds_kernel<4><<<grid, bounds_threads(4), 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
     using namespace select;
     if (p.max_pages > p.n_select) {
-        // enough blocks for six on each SM, and none with less than a round of pages
+        // three rounds of four blocks on each SM, and none with less than a round of pages
         const int rounds = (p.max_pages + SCORE_WARPS * SCORE_PAGES - 1) / (SCORE_WARPS * SCORE_PAGES);
         const long long items = static_cast<long long>(p.n_kv_heads) * p.batch, want = (SCORE_BLOCKS + items - 1) / items;
         const dim3 grid(static_cast<unsigned>(want < rounds ? want : rounds), p.n_kv_heads, p.batch);
-        score_kernel<<<grid, SCORE_WARPS * 32, 0, stream>>>(p);
+        const int smem = score_smem(p.q_len * p.group);
+        const cudaError_t set = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score_smem(16));
+        if (set != cudaSuccess) return set;
+        score_kernel<<<grid, SCORE_WARPS * 32, smem, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
