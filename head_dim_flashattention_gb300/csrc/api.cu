@@ -129,7 +129,8 @@ bool pow2_page(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 ||
 
 // Tiles of the decode band (upper bound over sequences) for a host-side bound
 // on the kv length.  A window can straddle one extra tile boundary.
-long long band_tiles(int max_kv_len, int window, int tk = fa512::decode_tile_positions()) {
+long long band_tiles(int max_kv_len, int window) {
+    const int tk = fa512::decode_tile_positions();
     long long band = max_kv_len;
     if (window > 0 && window < band) band = window;
     long long t = (band + tk - 1) / tk;
@@ -196,37 +197,6 @@ int choose_splits_fp8(long long items, long long tiles, int n_sm, long long rows
         }
     }
     return static_cast<int>(best_s);
-}
-
-// The 4-bit kernel deals the tiles (64 positions) of all sequences in ranges of equal
-// length to groups of CTAs, one CTA for each KV head, as many as one or two CTAs per
-// SM make.
-struct Fp4Plan {
-    int groups;
-    int segments;                  // most segments that a sequence may be left in
-};
-// For sequences of at most `tiles` tiles.  Times in tile times of a CTA that shares
-// its SM (1.8 us for 2 rows; alone it takes 0.6 of that), a tile for a CTA's start and
-// end, 0.02 for each of a sequence's segments in the merge.  A batch with shorter
-// sequences has shorter ranges, so a batch of several may leave twice the segments.
-Fp4Plan plan_fp4(long long batch, int n_kv_heads, long long tiles, int n_sm) {
-    Fp4Plan best{1, 1};
-    if (batch <= 0 || n_kv_heads <= 0) return best;
-    double cost = 1e300;
-    for (int per_sm = 1; per_sm <= fa512::decode_fp4_ctas_per_sm(); ++per_sm) {
-        long long groups = static_cast<long long>(per_sm) * n_sm / n_kv_heads;
-        if (groups < 1) groups = 1;
-        const long long all = batch * (tiles > 1 ? tiles : 1), range = (all + groups - 1) / groups;
-        const long long cut = (tiles + range - 1) / range;
-        const double c = (per_sm == 1 ? 0.6 : 1.0) * static_cast<double>(range) + 1.0 + 0.02 * static_cast<double>(cut);
-        if (c < cost) {
-            cost = c;
-            const long long used = (all + range - 1) / range, segments = (batch > 1 ? 2 : 1) * cut + 1;
-            best.groups = static_cast<int>(batch > 1 && tiles > 1 ? groups : used);
-            best.segments = static_cast<int>(tiles <= 1 ? 1 : segments < 1024 ? segments : 1024);
-        }
-    }
-    return best;
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -598,52 +568,15 @@ size_t fa512_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, in
 
 namespace {
 
-// Whether a 4-bit or sparse decode call takes these sizes.
-bool decode_size_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int num_splits) {
-    return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
-           static_cast<long long>(q_len) * (n_q_heads / n_kv_heads) <= 16 && max_kv_len >= 0 && num_splits >= 0 &&
-           num_splits <= 1024 && batch <= 65535 && static_cast<long long>(batch) * q_len <= 65535 && n_kv_heads <= 65535;
-}
-
-// Positions that a list of n_listed pages of a sequence of max_kv_len can have.
-int listed_positions(int page_size, int n_listed, int max_kv_len) {
-    const long long list = static_cast<long long>(n_listed) * page_size;
-    const long long seq = (static_cast<long long>(max_kv_len) + page_size - 1) / page_size * page_size;
-    const long long n = list < seq ? list : seq;
-    return static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
-}
-
-// Split count of a decode call over `positions` positions at most, by the bits of
-// a cached element.
-int decode_splits(int bits, int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size, int positions) {
-    if (bits == 16) return fa512_decode_auto_splits(batch, n_kv_heads, page_size, positions);
-    if (bits == 8) return fa512_decode_auto_splits_fp8(batch, q_len, n_q_heads, n_kv_heads, page_size, positions);
-    if (batch <= 0 || positions <= 0) return 1;
-    const int tile = fa512::decode_fp4_tile_positions();
-    return plan_fp4(batch, n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile, sm_count()).segments;
-}
-
-// What a decode call reads: the bits of a cached element (16: bf16; 8: e4m3
-// bytes; 4: rows of codes and group scales; a key element of the last two is
-// k_scale times, a value element v_scale times what is stored), and which pages.
-struct DecodeCache {
-    int bits;
-    float k_scale, v_scale;
-    bool sparse;
-    const int32_t* listed;
-    int n_listed;
-};
-
-// Body of the decode entry points.
+// Body of the decode entry points.  fp8: k_pages / v_pages hold e4m3 bytes
+// and a key (value) element is k_scale (v_scale) times its e4m3 value.
 fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages,
                          const int32_t* page_table, const int32_t* kv_lens, void* out, float* lse,
                          int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                          int num_pages, int max_pages_per_seq, int max_kv_len, float scale,
                          int window, int num_splits, void* workspace, size_t workspace_bytes,
-                         const DecodeCache& cache, fa512_stream_t stream) {
+                         bool fp8, float k_scale, float v_scale, fa512_stream_t stream) {
     g_last_error[0] = 0;
-    const bool fp8 = cache.bits == 8, fp4 = cache.bits == 4, coded = cache.bits != 16;
-    const float k_scale = cache.k_scale, v_scale = cache.v_scale;
     if (batch < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch");
     if (q_len < 1) return fail(FA512_ERR_INVALID_ARG, "q_len must be >= 1");
     if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0)
@@ -663,32 +596,21 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
         return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
     if (num_splits < 0 || num_splits > 1024) return fail(FA512_ERR_INVALID_ARG, "num_splits outside [0, 1024]");
     if (!(scale == scale) || isinf(scale)) return fail(FA512_ERR_INVALID_ARG, "scale is not finite");
-    if (coded && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
+    if (fp8 && (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale)))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
-    if (cache.sparse) {
-        if (cache.n_listed < 1) return fail(FA512_ERR_INVALID_ARG, "n_selected must be >= 1");
-        if (static_cast<long long>(cache.n_listed) * page_size > 0x7fffffffLL - 256 ||
-            static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
-            return fail(FA512_ERR_UNSUPPORTED, "list of pages or page table too large for int32 positions");
-    }
-    if (fp4 && static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
-        return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
-    if ((fp4 || cache.sparse) && static_cast<long long>(batch) * q_len > 65535)
-        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
     if (batch == 0) return FA512_OK;
-    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out || (cache.sparse && !cache.listed))
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out)
         return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
         return fail(FA512_ERR_INVALID_ARG, "q, pages and out must be 16-byte aligned");
-    if (reinterpret_cast<uintptr_t>(cache.listed) & 3u)
-        return fail(FA512_ERR_INVALID_ARG, "selected must be 4-byte aligned");
     if ((reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u) ||
         (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
         return fail(FA512_ERR_INVALID_ARG, "page_table, kv_lens and lse must be 4-byte aligned");
 
-    const int positions = cache.sparse ? listed_positions(page_size, cache.n_listed, max_kv_len) : max_kv_len;
     const int splits = num_splits > 0 ? num_splits
-                                      : decode_splits(cache.bits, batch, q_len, n_q_heads, n_kv_heads, page_size, positions);
+                       : fp8 ? fa512_decode_auto_splits_fp8(batch, q_len, n_q_heads, n_kv_heads,
+                                                            page_size, max_kv_len)
+                             : fa512_decode_auto_splits(batch, n_kv_heads, page_size, max_kv_len);
     const size_t need = workspace_for(batch * q_len, n_q_heads, splits);
     if (!workspace || workspace_bytes < need)
         return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
@@ -705,7 +627,7 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     fa512::DecodeParams p;
     memset(&p, 0, sizeof p);
     p.q = static_cast<const __nv_bfloat16*>(q);
-    if (coded) {
+    if (fp8) {
         p.k8 = static_cast<const uint8_t*>(k_pages);
         p.v8 = static_cast<const uint8_t*>(v_pages);
         p.o_scale = v_scale;
@@ -727,38 +649,23 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.group = G;
     p.q_len = q_len;
     p.page_size = page_size;
-    while ((1 << p.page_shift) < page_size) ++p.page_shift;
-    const int tile = fp4 ? fa512::decode_fp4_tile_positions() : fa512::decode_tile_positions();
-    p.box_rows = page_size < tile ? page_size : tile;
+    p.box_rows = page_size < 32 ? page_size : 32;
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.len_cap = max_kv_len;
     p.window = window > 0 ? window : 0;
-    const long long tiles = band_tiles(positions, p.window, tile);
+    const long long tiles = band_tiles(max_kv_len, p.window);
     p.num_splits = splits;
-    p.listed = cache.sparse ? cache.listed : nullptr;
-    p.n_listed = cache.n_listed;
     p.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
     if (p.tiles_per_split < 1) p.tiles_per_split = 1;
-    if (fp4) {
-        // the rows of a KV head span q_len - 1 positions beside the window, LIST tiles begin at 0
-        const long long seen = p.window > 0 ? static_cast<long long>(p.window) + q_len - 1 : positions;
-        long long most = (positions + tile - 1LL) / tile;
-        if (p.window > 0 && (seen + tile - 1) / tile + 1 < most) most = (seen + tile - 1) / tile + 1;
-        if (most < 1) most = 1;
-        if (batch > 0x7fffffffLL / most) return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
-        p.groups = plan_fp4(batch, n_kv_heads, most, sm_count()).groups;
-        // a sequence of n tiles touches (n - 1) / range + 2 ranges at most
-        p.tiles_per_split = splits > 1 ? static_cast<int>((most - 1) / (splits - 1) + 1) : 1;
-    }
     p.scale_log2 = scale * 1.4426950408889634f;
     // FP8: k_scale scales every score; applied after the bf16 path's factor
     // so that a power-of-two k_scale changes no rounding
-    if (coded) p.scale_log2 *= k_scale;
+    if (fp8) p.scale_log2 *= k_scale;
     p.err = err;
 
     CUtensorMap tmk, tmv;
-    const uint64_t dims[3] = {static_cast<uint64_t>(fp4 ? fa512::kFp4RowBytes / 4 : kHeadDim), static_cast<uint64_t>(n_kv_heads),
+    const uint64_t dims[3] = {static_cast<uint64_t>(kHeadDim), static_cast<uint64_t>(n_kv_heads),
                               static_cast<uint64_t>(num_pages) * page_size};
     fa512_status st;
     if (fp8) {
@@ -775,18 +682,6 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
                         dims, strides, box);
         if (st != FA512_OK) return st;
         e = fa512::launch_decode_fp8(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
-    } else if (fp4) {
-        const uint64_t strides[2] = {fa512::kFp4RowBytes, static_cast<uint64_t>(n_kv_heads) * fa512::kFp4RowBytes};
-        const uint32_t box[3] = {fa512::kFp4RowBytes / 4, 1u, static_cast<uint32_t>(p.box_rows)};
-        // Selected pages are read a head at a time: what a load brings into L2 beside its 288
-        // bytes is another head's (64 sequences, 64 of 448 pages: 133 us with 64-byte pieces,
-        // 144 with 128, 156 with 256); dense calls read all heads and do not differ.
-        const CUtensorMapL2promotion l2 = cache.sparse ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-        st = encode_map(&tmk, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, k_pages, 3, dims, strides, box, l2);
-        if (st != FA512_OK) return st;
-        st = encode_map(&tmv, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, v_pages, 3, dims, strides, box, l2);
-        if (st != FA512_OK) return st;
-        e = fa512::launch_decode_fp4(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
     } else {
         const uint64_t strides[2] = {kHeadDim * 2ull, static_cast<uint64_t>(n_kv_heads) * kHeadDim * 2ull};
         const uint32_t box[3] = {64u, 1u, static_cast<uint32_t>(p.box_rows)};
@@ -796,6 +691,179 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
         if (st != FA512_OK) return st;
         e = fa512::launch_decode(tmk, tmv, p, reinterpret_cast<cudaStream_t>(stream));
     }
+    if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+    return FA512_OK;
+}
+
+// ---------------------------------------------- 4-bit caches, selected pages
+
+// Whether such a call takes these sizes.
+bool ranges_size_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int num_splits) {
+    return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
+           static_cast<long long>(q_len) * (n_q_heads / n_kv_heads) <= 16 && max_kv_len >= 0 && num_splits >= 0 &&
+           num_splits <= 1024 && static_cast<long long>(batch) * q_len <= 65535 && n_kv_heads <= 65535;
+}
+
+// Positions that a list of n_listed pages of a sequence of max_kv_len can have.
+int listed_positions(int page_size, int n_listed, int max_kv_len) {
+    const long long list = static_cast<long long>(n_listed) * page_size;
+    const long long seq = (static_cast<long long>(max_kv_len) + page_size - 1) / page_size * page_size;
+    const long long n = list < seq ? list : seq;
+    return static_cast<int>(n < 0x7fffffff ? n : 0x7fffffff);
+}
+
+// The kernels over ranges deal the key tiles of all sequences in ranges of equal
+// length to groups of CTAs, one CTA for each KV head, as many as one or two CTAs per
+// SM make.
+struct RangesPlan {
+    int groups;
+    int segments;                  // most segments that a sequence may be left in
+};
+// For sequences of at most `tiles` tiles.  Times in tile times of a CTA that shares
+// its SM (1.6 us; alone it takes 0.6 of that), a tile for a CTA's start and end, 0.02
+// for each of a sequence's segments in the merge.  A batch with shorter sequences has
+// shorter ranges, so a batch of several may leave twice the segments.
+RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm) {
+    RangesPlan best{1, 1};
+    if (batch <= 0 || n_kv_heads <= 0) return best;
+    double cost = 1e300;
+    for (int per_sm = 1; per_sm <= fa512::decode_ranges_ctas_per_sm(); ++per_sm) {
+        long long groups = static_cast<long long>(per_sm) * n_sm / n_kv_heads;
+        if (groups < 1) groups = 1;
+        const long long all = batch * (tiles > 1 ? tiles : 1), range = (all + groups - 1) / groups;
+        const long long cut = (tiles + range - 1) / range;
+        const double c = (per_sm == 1 ? 0.6 : 1.0) * static_cast<double>(range) + 1.0 + 0.02 * static_cast<double>(cut);
+        if (c < cost) {
+            cost = c;
+            const long long used = (all + range - 1) / range, segments = (batch > 1 ? 2 : 1) * cut + 1;
+            best.groups = static_cast<int>(batch > 1 && tiles > 1 ? groups : used);
+            best.segments = static_cast<int>(tiles <= 1 ? 1 : segments < 1024 ? segments : 1024);
+        }
+    }
+    return best;
+}
+
+// Most segments of a call over `positions` positions at most, by the bits of a cached element.
+int ranges_splits(int bits, int batch, int n_kv_heads, int positions) {
+    const int tile = fa512::decode_ranges_tile(bits);
+    return plan_ranges(batch, n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile, sm_count()).segments;
+}
+
+// Body of the calls over a 4-bit cache and over selected pages.  bits of a cached
+// element: 16 bf16; 8 e4m3 bytes; 4 rows of codes and group scales (a key element of
+// the last two is k_scale times, a value element v_scale times what is stored).
+fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                         const int32_t* kv_lens, bool sparse, const int32_t* selected, int n_selected, void* out,
+                         float* lse, int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
+                         int num_pages, int max_pages_per_seq, int max_kv_len, float scale, int window,
+                         int num_splits, void* workspace, size_t workspace_bytes, int bits, float k_scale,
+                         float v_scale, fa512_stream_t stream) {
+    g_last_error[0] = 0;
+    if (batch < 0) return fail(FA512_ERR_INVALID_ARG, "negative batch");
+    if (q_len < 1) return fail(FA512_ERR_INVALID_ARG, "q_len must be >= 1");
+    if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0)
+        return fail(FA512_ERR_INVALID_ARG, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)",
+                    n_q_heads, n_kv_heads);
+    const int G = n_q_heads / n_kv_heads;
+    if (static_cast<long long>(q_len) * G > 16)
+        return fail(FA512_ERR_UNSUPPORTED, "q_len x query heads per KV head (%d x %d) must be at most 16", q_len, G);
+    if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 256 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+        return fail(FA512_ERR_UNSUPPORTED, "page pool or page table too large for int32 key rows");
+    if (max_kv_len < 0 || static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages_per_seq) * page_size)
+        return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
+    if (num_splits < 0 || num_splits > 1024) return fail(FA512_ERR_INVALID_ARG, "num_splits outside [0, 1024]");
+    if (!(scale == scale) || isinf(scale)) return fail(FA512_ERR_INVALID_ARG, "scale is not finite");
+    if (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale))
+        return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
+    if (sparse && n_selected < 1) return fail(FA512_ERR_INVALID_ARG, "n_selected must be >= 1");
+    if (sparse && static_cast<long long>(n_selected) * page_size > 0x7fffffffLL - 256)
+        return fail(FA512_ERR_UNSUPPORTED, "list of pages too large for int32 positions");
+    if (static_cast<long long>(batch) * q_len > 65535 || n_kv_heads > 65535)
+        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    if (batch == 0) return FA512_OK;
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out || (sparse && !selected))
+        return fail(FA512_ERR_INVALID_ARG, "null tensor pointer");
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+        return fail(FA512_ERR_INVALID_ARG, "q, pages and out must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
+         reinterpret_cast<uintptr_t>(selected) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+        return fail(FA512_ERR_INVALID_ARG, "int32 arrays and lse must be 4-byte aligned");
+    const int positions = sparse ? listed_positions(page_size, n_selected, max_kv_len) : max_kv_len;
+    const int splits = num_splits > 0 ? num_splits : ranges_splits(bits, batch, n_kv_heads, positions);
+    const size_t need = workspace_for(batch * q_len, n_q_heads, splits);
+    if (!workspace || workspace_bytes < need)
+        return fail(FA512_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(FA512_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    // most tiles of a sequence; with a window its rows see a band of window + q_len - 1
+    const int tile = fa512::decode_ranges_tile(bits);
+    long long most = (static_cast<long long>(positions) + tile - 1) / tile;
+    if (window > 0) {
+        const long long band = (static_cast<long long>(window) + q_len - 1 + tile - 1) / tile + 1;
+        if (band < most) most = band;
+    }
+    if (most < 1) most = 1;
+    if (batch > 0x7fffffffLL / most) return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
+
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_ptr(&err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    fa512::DecodeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o_scale = v_scale;
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    const size_t rows = static_cast<size_t>(batch) * q_len * n_q_heads * splits;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows * kHeadDim * sizeof(float)));
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.batch = batch;
+    p.n_q_heads = n_q_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = G;
+    p.q_len = q_len;
+    p.page_size = page_size;
+    while ((1 << p.page_shift) < page_size) ++p.page_shift;
+    p.box_rows = page_size < tile ? page_size : tile;
+    p.num_pages = num_pages;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.len_cap = max_kv_len;
+    p.window = window > 0 ? window : 0;
+    p.listed = sparse ? selected : nullptr;
+    p.n_listed = n_selected;
+    p.num_splits = splits;
+    p.groups = plan_ranges(batch, n_kv_heads, most, sm_count()).groups;
+    // a sequence of n tiles touches (n - 1) / range + 2 ranges at most
+    p.tiles_per_split = splits > 1 ? static_cast<int>((most - 1) / (splits - 1) + 1) : 1;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 *= k_scale;
+    p.err = err;
+
+    CUtensorMap tmk, tmv;
+    const uint64_t row = bits == 16 ? 2ull * kHeadDim : bits == 8 ? kHeadDim : fa512::kFp4RowBytes;
+    const uint64_t elements = bits == 4 ? row / 4 : kHeadDim;
+    const uint64_t dims[3] = {elements, static_cast<uint64_t>(n_kv_heads), static_cast<uint64_t>(num_pages) * page_size};
+    const uint64_t strides[2] = {row, n_kv_heads * row};
+    const uint32_t box[3] = {bits == 4 ? static_cast<uint32_t>(elements) : 1024u / bits, 1u, static_cast<uint32_t>(p.box_rows)};
+    const CUtensorMapDataType type = bits == 16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : bits == 8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                 : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    const CUtensorMapSwizzle swizzle = bits == 4 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    // Selected pages are read a head at a time: what a load brings into L2 beside its rows
+    // is another head's (4 bits, 64 sequences, 64 of 448 pages: 133 us with 64-byte pieces,
+    // 144 with 128, 156 with 256); dense calls read all heads and do not differ.
+    const CUtensorMapL2promotion l2 = sparse ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    fa512_status st = encode_map(&tmk, type, swizzle, k_pages, 3, dims, strides, box, l2);
+    if (st != FA512_OK) return st;
+    st = encode_map(&tmv, type, swizzle, v_pages, 3, dims, strides, box, l2);
+    if (st != FA512_OK) return st;
+    e = fa512::launch_decode_ranges(tmk, tmv, p, bits, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     return FA512_OK;
 }
@@ -813,7 +881,7 @@ fa512_status fa512_decode_paged_q(const void* q, const void* k_pages, const void
                                   fa512_stream_t stream) {
     return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
                        n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
-                       window, num_splits, workspace, workspace_bytes, {16, 1.f, 1.f, false, nullptr, 0}, stream);
+                       window, num_splits, workspace, workspace_bytes, false, 1.f, 1.f, stream);
 }
 
 fa512_status fa512_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -826,8 +894,8 @@ fa512_status fa512_decode_paged_fp8(const void* q, const void* k_pages, const vo
                                     fa512_stream_t stream) {
     return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
                        n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
-                       window, num_splits, workspace, workspace_bytes,
-                       {8, k_scale, v_scale, false, nullptr, 0}, stream);
+                       window, num_splits, workspace, workspace_bytes, true, k_scale, v_scale,
+                       stream);
 }
 
 fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const void* v_pages,
@@ -838,10 +906,9 @@ fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const vo
                                     float k_scale, float v_scale, int window, int num_splits,
                                     void* workspace, size_t workspace_bytes,
                                     fa512_stream_t stream) {
-    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads,
-                       n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale,
-                       window, num_splits, workspace, workspace_bytes,
-                       {4, k_scale, v_scale, false, nullptr, 0}, stream);
+    return ranges_call(q, k_pages, v_pages, page_table, kv_lens, false, nullptr, 0, out, lse, batch, q_len, n_q_heads,
+                       n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, window, num_splits,
+                       workspace, workspace_bytes, 4, k_scale, v_scale, stream);
 }
 
 fa512_status fa512_decode_paged_sparse(const void* q, const void* k_pages, const void* v_pages,
@@ -851,9 +918,9 @@ fa512_status fa512_decode_paged_sparse(const void* q, const void* k_pages, const
                                        int max_pages_per_seq, int n_selected, int max_kv_len, float scale,
                                        int num_splits, void* workspace, size_t workspace_bytes,
                                        fa512_stream_t stream) {
-    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
-                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
-                       workspace_bytes, {16, 1.f, 1.f, true, selected, n_selected}, stream);
+    return ranges_call(q, k_pages, v_pages, page_table, kv_lens, true, selected, n_selected, out, lse, batch, q_len,
+                       n_q_heads, n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits,
+                       workspace, workspace_bytes, 16, 1.f, 1.f, stream);
 }
 
 fa512_status fa512_decode_paged_sparse_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -864,9 +931,9 @@ fa512_status fa512_decode_paged_sparse_fp8(const void* q, const void* k_pages, c
                                            int max_kv_len, float scale, float k_scale, float v_scale,
                                            int num_splits, void* workspace, size_t workspace_bytes,
                                            fa512_stream_t stream) {
-    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
-                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
-                       workspace_bytes, {8, k_scale, v_scale, true, selected, n_selected}, stream);
+    return ranges_call(q, k_pages, v_pages, page_table, kv_lens, true, selected, n_selected, out, lse, batch, q_len,
+                       n_q_heads, n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits,
+                       workspace, workspace_bytes, 8, k_scale, v_scale, stream);
 }
 
 fa512_status fa512_decode_paged_sparse_fp4(const void* q, const void* k_pages, const void* v_pages,
@@ -877,38 +944,36 @@ fa512_status fa512_decode_paged_sparse_fp4(const void* q, const void* k_pages, c
                                            int max_kv_len, float scale, float k_scale, float v_scale,
                                            int num_splits, void* workspace, size_t workspace_bytes,
                                            fa512_stream_t stream) {
-    return decode_call(q, k_pages, v_pages, page_table, kv_lens, out, lse, batch, q_len, n_q_heads, n_kv_heads,
-                       page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits, workspace,
-                       workspace_bytes, {4, k_scale, v_scale, true, selected, n_selected}, stream);
+    return ranges_call(q, k_pages, v_pages, page_table, kv_lens, true, selected, n_selected, out, lse, batch, q_len,
+                       n_q_heads, n_kv_heads, page_size, num_pages, max_pages_per_seq, max_kv_len, scale, 0, num_splits,
+                       workspace, workspace_bytes, 4, k_scale, v_scale, stream);
 }
 
 int fa512_decode_auto_splits_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                                  int max_kv_len) {
-    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0)) return 1;
-    return decode_splits(4, batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len);
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0)) return 1;
+    return ranges_splits(4, batch, n_kv_heads, max_kv_len);
 }
 
 size_t fa512_decode_workspace_bytes_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                                         int max_kv_len, int num_splits) {
-    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits)) return 0;
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits)) return 0;
     return workspace_for(batch * q_len, n_q_heads,
-                         num_splits > 0 ? num_splits
-                                        : decode_splits(4, batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len));
+                         num_splits > 0 ? num_splits : ranges_splits(4, batch, n_kv_heads, max_kv_len));
 }
 
 int fa512_decode_auto_splits_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads, int element_bits,
                                     int page_size, int n_selected, int max_kv_len) {
-    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0) || !pow2_page(page_size) ||
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0) || !pow2_page(page_size) ||
         n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
         return 1;
-    return decode_splits(element_bits, batch, q_len, n_q_heads, n_kv_heads, page_size,
-                         listed_positions(page_size, n_selected, max_kv_len));
+    return ranges_splits(element_bits, batch, n_kv_heads, listed_positions(page_size, n_selected, max_kv_len));
 }
 
 size_t fa512_decode_workspace_bytes_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads,
                                            int element_bits, int page_size, int n_selected, int max_kv_len,
                                            int num_splits) {
-    if (!decode_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits) || !pow2_page(page_size) ||
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits) || !pow2_page(page_size) ||
         n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
         return 0;
     const int s = num_splits > 0 ? num_splits

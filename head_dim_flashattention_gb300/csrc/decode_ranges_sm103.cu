@@ -1,33 +1,25 @@
-// Paged split-K decode over a cache held in 4 bits, sm_103a.
+// Paged decode over ranges of key tiles, sm_103a: caches held in 4 bits, and selected
+// pages of a cache in any format.
 //
-// A row of one head and position is 288 bytes: 256 bytes of E2M1 codes (element
-// 2 i in the low half of byte i) and 32 E4M3 scales, one for 16 elements, so a
-// position costs 576 bytes of K and V where bf16 costs 2,048.  An element is
-// tensor scale * group scale * code; group scale times code has 6 significant
-// bits and lies between 2^-10 and 2,688, so it is exact in f16, and the products
-// run on mma.sync with f16 operands and fp32 sums over the cache's exact values.
+// The key tiles of all sequences stand in a row and are dealt in ranges of equal length
+// to groups of CTAs, one CTA for each KV head, two CTAs to an SM for the whole launch;
+// what a CTA has of a sequence is a segment, with an (O, m, l) partial of its own.  (The
+// heads of a position lie side by side: read at about the same time they share the
+// memory's lines.  Ranges that did not keep the heads together took 997 us instead of
+// 741 for 64 sequences of 28,672 positions in 4 bits.)  With a list of pages the tiles
+// are counted along it.
 //
-// The key tiles (64 positions) of all sequences stand in a row and are dealt in ranges
-// of equal length to groups of CTAs, one CTA for each KV head, two CTAs to an SM for
-// the whole launch; what a CTA has of a sequence is a segment, with an (O, m, l)
-// partial of its own.  (The heads of a position lie side by side, 288 bytes each:
-// read at about the same time they share the memory's lines.  Ranges that did not
-// keep the heads together took 997 us instead of 690 for 64 sequences of 28,672.)
-// K and V rows come by TMA into rings of slots that run on across segments.  Four
-// warps form S^T = K Q^T, 16 positions each over the whole head dim with the query
-// rows in N, and their softmax against a reference of their own, and leave P^T and
-// the reference in shared memory; four other warps add V^T P^T of all 64 positions,
-// 128 columns of O each.  Nothing is computed twice, and the two groups only meet
-// at barriers in shared memory with a tile of slack, so that both products of
-// different tiles overlap (one group that did both in turn read 5.0 TB/s, each
-// product alone as fast as the loads, 6.4).  References are whole numbers in log2
-// units: what brings two of them together is a power of two, exact in f16.
-//
-// K pairs are neighbouring codes of a row, as stored.  A V pair is the codes of
-// one column in two rows: a shift and a bit select turn two rows' words into
-// bytes that hold such pairs.  Within a group of 8 positions a lane's rows are
-// taken in the order 0 1 2 3 5 4 7 6, with which both operands' shared-memory
-// reads (rows 288 bytes apart) touch every bank once.
+// K and V rows come by TMA, two warps' work, into rings of slots that run on across
+// segments.  Four warps form S^T = K Q^T, a block of 16 positions at a time over the
+// whole head dim with the query rows in N, and their softmax against a reference of
+// their own, and leave P^T and the reference in shared memory; four other warps add
+// V^T P^T of all blocks of the tile, 128 columns of O each.  Nothing is computed twice,
+// and the groups only meet at barriers in shared memory with tiles of slack, so that
+// both products of different tiles overlap.  (64 sequences of 28,672 positions in 4
+// bits: one group of warps that did both in turn 846 us, two groups 775, the group
+// scales in free columns for 2 rows 707, loads on warps of their own 649: 6.5 TB/s.)
+// References are whole numbers in log2 units: what brings two of them together is a
+// power of two, exact in f16 and bf16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,289 +27,45 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "decode_ranges.cuh"
 #include "fa512_device.cuh"
 #include "fa512_internal.h"
 #include "fa512_list.cuh"
 
 namespace fa512 {
-namespace fp4 {
+namespace ranges {
 
-constexpr int D = 512;
-constexpr int ROW = kFp4RowBytes;
-constexpr int CODES = 256;                       // bytes of codes in a row
-constexpr int TILE = 64;                         // positions per tile
-constexpr int WARPS = 4;                         // per group: 16 positions of a tile, or 128 columns of O, each
 constexpr int THREADS = 3 * WARPS * 32;          // K group, V group, loads
 constexpr int CTAS_PER_SM = 2;
-constexpr int SLOT = TILE * ROW;                 // 18,432 bytes
-constexpr int KSTEPS = D / 16;
-constexpr int MTILES = D / WARPS / 16;           // m-tiles of 16 columns a warp
-constexpr int META = 8;                          // tiles and segments whose notes are kept
+constexpr int META = 16;                         // tiles and segments whose notes are kept
 
-template <int NT>
+template <int BITS, int NT>
 struct Smem {
+    using F = Format<BITS>;
     static constexpr int slots = NT == 1 ? 3 : 2;            // of K, and of V
+    // A K warp takes every turns-th tile.  K's `full` barriers go by tiles, not slots, so
+    // that each is one warp's own, which then sees all of its phases: the first common
+    // multiple of both counts.
+    static constexpr int turns = WARPS / F::BLOCKS;
+    static constexpr int k_bars = slots % turns == 0 ? slots : turns == 2 || slots % 2 ? slots * turns : slots * turns / 2;
+    static_assert(k_bars % slots == 0 && k_bars % turns == 0, "a common multiple");
     static constexpr int k = 0;
-    static constexpr int v = slots * SLOT;
-    static constexpr int p = 2 * slots * SLOT;               // [parity][block][nt][lane] uint2
-    static constexpr int q = p + 2 * WARPS * NT * 32 * 8;    // NT = 2: [nt][kstep][lane] uint2
-    static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);   // [parity][block][8 NT] float
-    static constexpr int sums = ref + 2 * WARPS * 8 * NT * 4;              // [parity][warp][8 NT] float2: reference, sum
-    static constexpr int base = sums + 2 * WARPS * 8 * NT * 8;             // [META][4] first position of 16
-    static constexpr int seg = base + META * 16;                           // [META] int4: see Segment
+    static constexpr int v = slots * F::SLOT;
+    static constexpr int p = 2 * slots * F::SLOT;            // [buffer][block][nt][lane] uint2
+    static constexpr int q = p + F::P_BUFFERS * F::BLOCKS * NT * 32 * 8;    // NT = 2: [nt][kstep][lane] uint2
+    static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);    // [buffer][block][8 NT] float
+    static constexpr int sums = ref + F::P_BUFFERS * F::BLOCKS * 8 * NT * 4;   // [parity][warp][8 NT] float2: reference, sum
+    static constexpr int base = sums + 2 * WARPS * 8 * NT * 8;              // [META][BLOCKS] first position of 16
+    static constexpr int seg = base + META * F::BLOCKS * 4;                 // [META] Segment
     static constexpr int total_tiles = seg + META * 16;
     static constexpr int bar = total_tiles + 8;
     // barriers: K and V slots full and empty, P buffers full and empty
-    static constexpr int total = bar + (4 * slots + 4) * 8;
+    static constexpr int total = bar + (k_bars + 3 * slots + 2 * F::P_BUFFERS) * 8;
+    static_assert(CTAS_PER_SM * (total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
 };
-static_assert(CTAS_PER_SM * (Smem<1>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
-static_assert(CTAS_PER_SM * (Smem<2>::total + 1024) <= 228 * 1024, "the CTAs fit an SM's shared memory");
-
-__device__ __forceinline__ int turned(int r) { return r ^ ((r >> 2) & 1); }
-
-// Four bytes of two codes each -> four f16x2, exactly (low half of the byte first).
-__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-// Two e4m3 values (low byte first) -> f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
-    return h;
-}
-
-__device__ __forceinline__ float f16_f32(uint32_t h) {
-    float f;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(static_cast<unsigned short>(h)));
-    return f;
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t y, uint32_t sel) {
-    uint32_t t;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(t) : "r"(x), "r"(y), "r"(sel));
-    return t;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // A reference to subtract: 0 while nothing was seen, so that 2^(-inf - 0) = 0.
 __device__ __forceinline__ float finite_ref(float x) { return x == -INFINITY ? 0.f : x; }
-
-constexpr uint32_t LOW_HALVES = 0x0f0f0f0fu;
-
-// S^T of 16 positions, positions turned(g) and + 8 of `block` to a lane, scales
-// applied to the codes; Q fragments in registers (NT = 1) or shared memory.
-template <int NT>
-__device__ __forceinline__ void scores(const uint8_t* block, int lane, const uint32_t (&qb)[NT == 1 ? KSTEPS : 1][2],
-                                       const uint2* s_q, float (&sc)[NT][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t *a_row = block + turned(g) * ROW, *b_row = a_row + 8 * ROW;
-    const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
-    float acc[NT][2][4];                          // two chains of sums
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][0][e] = acc[n][1][e] = 0.f;
-#pragma unroll
-    for (int j4 = 0; j4 < 2; ++j4) {
-        // the rows' scales of 16 groups; this lane's are every fourth
-        const uint4 xa = *reinterpret_cast<const uint4*>(a_row + CODES + 16 * j4);
-        const uint4 xb = *reinterpret_cast<const uint4*>(b_row + CODES + 16 * j4);
-        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-#pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-            const uint32_t sa = e4m3x2_f16(prmt(wa[2 * j2], wa[2 * j2 + 1], pick) & 0xffffu);
-            const uint32_t sb = e4m3x2_f16(prmt(wb[2 * j2], wb[2 * j2 + 1], pick) & 0xffffu);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 4 * j4 + 2 * j2 + h;
-                const uint32_t fa = prmt(sa, sa, h ? 0x3232u : 0x1010u), fb = prmt(sb, sb, h ? 0x3232u : 0x1010u);
-                const uint2 ca = *reinterpret_cast<const uint2*>(a_row + 32 * j + 8 * t);
-                const uint2 cb = *reinterpret_cast<const uint2*>(b_row + 32 * j + 8 * t);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t ha[4], hb[4];
-                    e2m1x8_f16(x ? ca.y : ca.x, ha);
-                    e2m1x8_f16(x ? cb.y : cb.x, hb);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int k = 4 * j + 2 * x + s;
-                        const uint32_t a0 = mul_f16x2(ha[2 * s], fa), a2 = mul_f16x2(ha[2 * s + 1], fa);
-                        const uint32_t a1 = mul_f16x2(hb[2 * s], fb), a3 = mul_f16x2(hb[2 * s + 1], fb);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            uint32_t b0, b1;
-                            if constexpr (NT == 1) {
-                                b0 = qb[k][0];
-                                b1 = qb[k][1];
-                            } else {
-                                const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
-                                b0 = q2.x;
-                                b1 = q2.y;
-                            }
-                            mma_f16(acc[n][k & 1], a0, a1, a2, a3, b0, b1);
-                        }
-                    }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = acc[n][0][e] + acc[n][1][e];
-}
-
-// The same for up to 2 rows: column 2 c + r of Q^T holds row r's elements of the
-// groups 4 j + c, and zeros.  A lane's sums of step j are those of group 4 j + t.
-__device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, const uint32_t (&qb)[KSTEPS][2],
-                                              float (&sc)[4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t *a_row = block + turned(g) * ROW, *b_row = a_row + 8 * ROW;
-    const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sc[e] = 0.f;
-#pragma unroll
-    for (int j4 = 0; j4 < 2; ++j4) {
-        const uint4 xa = *reinterpret_cast<const uint4*>(a_row + CODES + 16 * j4);
-        const uint4 xb = *reinterpret_cast<const uint4*>(b_row + CODES + 16 * j4);
-        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-#pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-            const uint32_t sa = e4m3x2_f16(prmt(wa[2 * j2], wa[2 * j2 + 1], pick) & 0xffffu);
-            const uint32_t sb = e4m3x2_f16(prmt(wb[2 * j2], wb[2 * j2 + 1], pick) & 0xffffu);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 4 * j4 + 2 * j2 + h;
-                const uint2 ca = *reinterpret_cast<const uint2*>(a_row + 32 * j + 8 * t);
-                const uint2 cb = *reinterpret_cast<const uint2*>(b_row + 32 * j + 8 * t);
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t ha[4], hb[4];
-                    e2m1x8_f16(x ? ca.y : ca.x, ha);
-                    e2m1x8_f16(x ? cb.y : cb.x, hb);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        mma_f16(d, ha[2 * s], hb[2 * s], ha[2 * s + 1], hb[2 * s + 1], qb[4 * j + 2 * x + s][0],
-                                qb[4 * j + 2 * x + s][1]);
-                }
-                const float fa = f16_f32(h ? sa >> 16 : sa), fb = f16_f32(h ? sb >> 16 : sb);
-                sc[0] = fmaf(fa, d[0], sc[0]);
-                sc[1] = fmaf(fa, d[1], sc[1]);
-                sc[2] = fmaf(fb, d[2], sc[2]);
-                sc[3] = fmaf(fb, d[3], sc[3]);
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {                 // the four classes
-        sc[e] += __shfl_xor_sync(0xffffffffu, sc[e], 1);
-        sc[e] += __shfl_xor_sync(0xffffffffu, sc[e], 2);
-    }
-}
-
-// Row of a block of 16 that lane t's i-th V operand is: the pairs (2 t, 2 t + 1)
-// and (2 t + 8, 2 t + 9).
-__device__ __forceinline__ int v_row(int t, int i) { return turned(2 * t + (i & 1)) + 8 * (i >> 1); }
-
-// O^T of columns 128 warp .. + 127 += V^T P^T over 16 positions, scales applied to
-// the codes; m-tile i is columns 16 g + 2 i, 16 g + 2 i + 1 of those.
-template <int NT>
-__device__ __forceinline__ void add_values(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[NT][2],
-                                           float (&o)[NT][MTILES][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    uint2 c[4];
-    uint32_t sb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint8_t* row = block + v_row(t, i) * ROW;
-        c[i] = *reinterpret_cast<const uint2*>(row + 64 * warp + 8 * g);
-        sb[i] = row[CODES + 8 * warp + g];
-    }
-    const uint32_t s01 = e4m3x2_f16(prmt(sb[0], sb[1], 0x0040u)), s23 = e4m3x2_f16(prmt(sb[2], sb[3], 0x0040u));
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const uint32_t w0 = x ? c[0].y : c[0].x, w1 = x ? c[1].y : c[1].x;
-        const uint32_t w2 = x ? c[2].y : c[2].x, w3 = x ? c[3].y : c[3].x;
-        // bytes of two rows' codes of one column: even columns, odd columns
-        uint32_t e01[4], d01[4], e23[4], d23[4];
-        e2m1x8_f16((w0 & LOW_HALVES) | ((w1 << 4) & ~LOW_HALVES), e01);
-        e2m1x8_f16(((w0 >> 4) & LOW_HALVES) | (w1 & ~LOW_HALVES), d01);
-        e2m1x8_f16((w2 & LOW_HALVES) | ((w3 << 4) & ~LOW_HALVES), e23);
-        e2m1x8_f16(((w2 >> 4) & LOW_HALVES) | (w3 & ~LOW_HALVES), d23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = mul_f16x2(e01[i], s01), a1 = mul_f16x2(d01[i], s01);
-            const uint32_t a2 = mul_f16x2(e23[i], s23), a3 = mul_f16x2(d23[i], s23);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * x + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-        }
-    }
-}
-
-// The same for up to 2 rows: column 2 c + r of P^T is row r's weights times the
-// scales of group 4 h + c; m-tile 4 h + i is columns 16 (4 h + g % 4) + 8 (g / 4) +
-// 2 i, + 1.  A lane's sums of class t = g % 4 are O, the others are not used.
-__device__ __forceinline__ void add_values_narrow(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[2],
-                                                  float (&o)[MTILES][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* rows[4];
-    uint2 sw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        rows[i] = block + v_row(t, i) * ROW;
-        sw[i] = *reinterpret_cast<const uint2*>(rows[i] + CODES + 8 * warp);
-    }
-    const uint32_t pick = static_cast<uint32_t>(g >> 1) | (static_cast<uint32_t>(4 + (g >> 1)) << 4);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = *reinterpret_cast<const uint32_t*>(rows[i] + 64 * warp + 32 * h + 8 * (g & 3) + 4 * (g >> 2));
-        const uint32_t s01 = e4m3x2_f16(prmt(h ? sw[0].y : sw[0].x, h ? sw[1].y : sw[1].x, pick) & 0xffffu);
-        const uint32_t s23 = e4m3x2_f16(prmt(h ? sw[2].y : sw[2].x, h ? sw[3].y : sw[3].x, pick) & 0xffffu);
-        const uint32_t b0 = mul_f16x2(pb[0], s01), b1 = mul_f16x2(pb[1], s23);
-        uint32_t e01[4], d01[4], e23[4], d23[4];
-        e2m1x8_f16((w[0] & LOW_HALVES) | ((w[1] << 4) & ~LOW_HALVES), e01);
-        e2m1x8_f16(((w[0] >> 4) & LOW_HALVES) | (w[1] & ~LOW_HALVES), d01);
-        e2m1x8_f16((w[2] & LOW_HALVES) | ((w[3] << 4) & ~LOW_HALVES), e23);
-        e2m1x8_f16(((w[2] >> 4) & LOW_HALVES) | (w[3] & ~LOW_HALVES), d23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(o[4 * h + i], e01[i], d01[i], e23[i], d23[i], b0, b1);
-    }
-}
 
 struct Item {
     int len;                                      // live positions
@@ -325,7 +73,7 @@ struct Item {
     int tiles;                                    // LIST: along the list of pages
     int held;                                     // pages
 };
-template <bool LIST>
+template <int BITS, bool LIST>
 __device__ __forceinline__ Item item_with(const DecodeParams& p, int len) {
     Item x;
     x.len = min(max(len, 0), p.len_cap);
@@ -334,11 +82,14 @@ __device__ __forceinline__ Item item_with(const DecodeParams& p, int len) {
     x.lo = p.window > 0 && w_lo > 0 ? w_lo : 0;
     x.held = static_cast<int>((static_cast<unsigned>(x.len) + p.page_size - 1) >> p.page_shift);
     const int end = LIST ? min(p.n_listed, x.held) << p.page_shift : x.len;
+    constexpr int TILE = Format<BITS>::TILE;
     x.tiles = (end + TILE - 1) / TILE - x.lo / TILE;
     return x;
 }
-template <bool LIST>
-__device__ __forceinline__ Item item_of(const DecodeParams& p, int b) { return item_with<LIST>(p, p.kv_lens[b]); }
+template <int BITS, bool LIST>
+__device__ __forceinline__ Item item_of(const DecodeParams& p, int b) {
+    return item_with<BITS, LIST>(p, p.kv_lens[b]);
+}
 
 // What the loading warp notes of a segment.
 struct Segment {
@@ -349,7 +100,7 @@ struct Segment {
 };
 
 // A CTA's way through its range of tiles.
-template <bool LIST>
+template <int BITS, bool LIST>
 struct Walk {
     int b;                                        // sequence
     Item item;
@@ -363,17 +114,17 @@ struct Walk {
         while (left > 0 && tile == item.tiles) {
             start += item.tiles;
             tile = 0;
-            item = item_of<LIST>(p, ++b);
+            item = item_of<BITS, LIST>(p, ++b);
         }
     }
 };
 
 // Where the `index`-th of `groups` ranges begins, and the length of the ranges.
 // num_splits = 1: ranges of whole sequences.  All lanes of a warp together.
-template <bool LIST>
-__device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int index, int groups, int* range) {
+template <int BITS, bool LIST>
+__device__ __forceinline__ Walk<BITS, LIST> first_of_range(const DecodeParams& p, int index, int groups, int* range) {
     const int lane = threadIdx.x & 31;
-    Walk<LIST> w;
+    Walk<BITS, LIST> w;
     w.b = w.tile = w.start = w.left = 0;
     *range = 0x7fffffff;
     if (p.num_splits == 1) {
@@ -381,17 +132,17 @@ __device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int 
         const int begin = min(p.batch, index * per), end = min(p.batch, begin + per);
         if (begin == end) return w;
         int left = 0;
-        for (int b = begin + lane; b < end; b += 32) left += item_of<LIST>(p, b).tiles;
+        for (int b = begin + lane; b < end; b += 32) left += item_of<BITS, LIST>(p, b).tiles;
         w.left = __reduce_add_sync(0xffffffffu, left);
         w.b = begin;
-        w.item = item_of<LIST>(p, begin);
+        w.item = item_of<BITS, LIST>(p, begin);
         w.next(p, 0);                             // past sequences without a tile
         return w;
     }
     int total = 0, len = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         len = b0 + lane < p.batch ? p.kv_lens[b0 + lane] : 0;
-        total += __reduce_add_sync(0xffffffffu, item_with<LIST>(p, len).tiles);
+        total += __reduce_add_sync(0xffffffffu, item_with<BITS, LIST>(p, len).tiles);
     }
     const int r = max((total + groups - 1) / groups, p.tiles_per_split);
     const long long at = static_cast<long long>(index) * r;
@@ -401,7 +152,7 @@ __device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int 
     // the sequence that the range begins in
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         if (p.batch > 32) len = b0 + lane < p.batch ? p.kv_lens[b0 + lane] : 0;
-        const int n = item_with<LIST>(p, len).tiles;
+        const int n = item_with<BITS, LIST>(p, len).tiles;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -413,7 +164,7 @@ __device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int 
             const int l = __ffs(here) - 1;
             w.b = b0 + l;
             w.start += __shfl_sync(0xffffffffu, sum - n, l);
-            w.item = item_with<LIST>(p, __shfl_sync(0xffffffffu, len, l));
+            w.item = item_with<BITS, LIST>(p, __shfl_sync(0xffffffffu, len, l));
             break;
         }
         w.start += __shfl_sync(0xffffffffu, sum, 31);
@@ -433,19 +184,26 @@ __device__ __forceinline__ Walk<LIST> first_of_range(const DecodeParams& p, int 
 //   O^T: lane g holds codes of group 4 h + g % 4, and P is scaled once for each
 //        class: 4 multiplications a block where scaling the codes takes 32.  Of a
 //        lane's sums those of class t = g % 4 are O, the others are not used.
-template <int ROWS, bool LIST>
+template <int BITS, int ROWS, bool LIST>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const DecodeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int NT = ROWS > 8 ? 2 : 1;
     constexpr bool NARROW = ROWS == 2;
-    using Smem = fp4::Smem<NT>;
-    constexpr int SLOTS = Smem::slots;
-    extern __shared__ __align__(128) uint8_t fp4_smem[];
-    uint8_t* smem = fp4_smem;
+    static_assert(!NARROW || BITS == 4, "only group scales take free columns");
+    using F = Format<BITS>;
+    constexpr int TILE = F::TILE, BLOCKS = F::BLOCKS, P_BUFFERS = F::P_BUFFERS;
+    using Smem = ranges::Smem<BITS, NT>;
+    constexpr int SLOTS = Smem::slots, TURNS = Smem::turns, K_BARS = Smem::k_bars;
+    static_assert(P_BUFFERS % TURNS == 0, "a P buffer is one K warp's own");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {                // the swizzle goes by addresses
+        if (threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_LAYOUT);
+        return;
+    }
     uint2* s_p = reinterpret_cast<uint2*>(smem + Smem::p);
-    uint16_t* s_p2 = reinterpret_cast<uint16_t*>(smem + Smem::p);   // NARROW: [parity][block][row][16]
+    uint16_t* s_p2 = reinterpret_cast<uint16_t*>(smem + Smem::p);   // NARROW: [buffer][block][row][16]
     uint2* s_q = reinterpret_cast<uint2*>(smem + Smem::q);
     float* s_ref = reinterpret_cast<float*>(smem + Smem::ref);
     float2* s_sums = reinterpret_cast<float2*>(smem + Smem::sums);
@@ -453,8 +211,8 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     Segment* s_seg = reinterpret_cast<Segment*>(smem + Smem::seg);
     int* s_total = reinterpret_cast<int*>(smem + Smem::total_tiles);
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Smem::bar);
-    uint64_t *k_empty = k_full + SLOTS, *v_full = k_empty + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS,
-             *p_empty = p_full + 2;
+    uint64_t *k_empty = k_full + K_BARS, *v_full = k_empty + SLOTS, *v_empty = v_full + SLOTS, *p_full = v_empty + SLOTS,
+             *p_empty = p_full + P_BUFFERS;
 
     const int lane = threadIdx.x & 31;
     const int warp = (threadIdx.x >> 5) & (WARPS - 1);   // within its group
@@ -483,9 +241,8 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * 80, "no more than the launch has");
     if (role == 0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K_REGS));
-        // ---- Q^T fragments: b0/b1 of k-step 4 j + s hold row g's elements 64 j + 16
-        // t + 4 s + {0, 1} / {2, 3}, in f16 after a power-of-two scale per row that
-        // keeps its largest element below 2^15 (exact for elements down to 2^-39 of
+        // ---- Q^T fragments, bf16 as stored, else in f16 after a power-of-two scale per row
+        // that keeps its largest element below 2^15 (exact for elements down to 2^-39 of
         // that; a score is unscaled before the softmax)
         uint32_t qb[NT == 1 ? KSTEPS : 1][2];
         float rs[NT][2];                          // 1 / scale of rows row_of(n, 0), row_of(n, 1)
@@ -501,7 +258,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 for (int j = 0; j < 8; ++j) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 a = row_ok ? src[BITS == 16 ? 8 * j + 4 * e + t : 8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
                         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -519,9 +276,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 // 2^(14 - E), E = exponent of the maximum (0 or not finite: 1)
                 const int E = (__float_as_uint(most) >> 23) & 0xff;
                 const int biased = min(127 + 14 + 127 - E, 254);
-                const float scale = (most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
+                const float scale = (BITS != 16 && most > 0.f && E < 255) ? __uint_as_float(static_cast<uint32_t>(biased) << 23) : 1.f;
                 auto to_f16 = [&](uint32_t w) {
-                    return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+                    if constexpr (BITS == 16) return w;
+                    else return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
                 };
                 if constexpr (NT == 1) {
 #pragma unroll
@@ -535,7 +293,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int j = 2 * warp; j < 2 * warp + 2; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint4 a = row_ok ? src[8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
+                            const uint4 a = row_ok ? src[BITS == 16 ? 8 * j + 4 * e + t : 8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
                             s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
                             s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
                         }
@@ -556,9 +314,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         // this lane's rows: i (NARROW) or 8 n + 2 t + i
         auto row_of = [&](int n, int i) { return NARROW ? i : 8 * n + 2 * t + i; };
         const unsigned reach = p.window > 0 ? static_cast<unsigned>(p.window) : 0x7fffffffu;
-        const int ra = turned(g);                 // this lane's rows of 16 positions: ra, ra + 8
+        const int ra = F::order(g);               // this lane's rows of 16 positions: ra, ra + 8
+        const int block = warp % BLOCKS, turn = warp / BLOCKS;   // which of a tile, and of which tiles
         int range;
-        const int first_b = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range).b;
+        const int first_b = first_of_range<BITS, LIST>(p, index, gridDim.x / p.n_kv_heads, &range).b;
         load_q(first_b);                          // (of sequence 0 where the range is empty)
         __syncthreads();                          // barriers, the first tiles' notes, NT = 2: the queries
         const int total = *s_total;
@@ -566,14 +325,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int it = 0;                               // tiles of the range gone through
         for (int segment = 0; it < total && ok; ++segment) {
             if (segment > 0) {
-                // a segment's notes are there once its first tile is asked for
-                if (!wait(&k_full[it % SLOTS], it / SLOTS)) ok = false;
-                if constexpr (NT == 2) k_warps();     // the last sequence's queries are read
-                if (!ok) break;
-                load_q(s_seg[segment & (META - 1)].b);
+                load_q(s_seg[segment % META].b);
                 if constexpr (NT == 2) k_warps();
             }
-            const Segment seg = s_seg[segment & (META - 1)];
+            const Segment seg = s_seg[segment % META];
             // positions of the rows (-1: padding row, sees nothing); a row sees the keys
             // whose distance to it is in [0, reach)
             int qpos[NT][2];
@@ -587,18 +342,22 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     m[n][i] = -INFINITY;
                     l[n][i] = 0.f;
                 }
-            for (const int end = it + seg.run; it < end; ++it) {
-                const int slot = it % SLOTS, par = it & 1;
-                if (!wait(&k_full[slot], it / SLOTS)) {
+            const int end = it + seg.run;
+            for (; it < end; ++it) {
+                if (it % TURNS != turn) continue;
+                const int slot = it % SLOTS, buffer = it % P_BUFFERS;
+                if (!wait(&k_full[it % K_BARS], it / K_BARS)) {
                     ok = false;
                     break;
                 }
-                const int base = s_base[(it & (META - 1)) * 4 + warp];
+                const int base = s_base[(it % META) * BLOCKS + block];
                 // (an unloaded block's rows are stale: its scores are masked)
                 float sc[NT][4];
-                const uint8_t* block = smem + Smem::k + slot * SLOT + 16 * warp * ROW;
-                if constexpr (NARROW) scores_narrow(block, lane, qb, sc[0]);
-                else scores<NT>(block, lane, qb, s_q, sc);
+                const uint8_t* rows = smem + Smem::k + slot * F::SLOT;
+                if constexpr (NARROW) scores_narrow(rows + 16 * block * F::ROW, lane, qb, sc[0]);
+                else if constexpr (BITS == 4) scores_4<NT>(rows + 16 * block * F::ROW, lane, qb, s_q, sc);
+                else if constexpr (BITS == 8) scores_8<NT>(rows, 16 * block, lane, qb, s_q, sc);
+                else scores_16<NT>(rows, lane, qb, s_q, sc);
                 done_with(&k_empty[slot]);
                 // ---- softmax against this block's own maximum, rounded up to a whole number,
                 // less 7: weights up to 2^7 keep small ones, and those times a group scale
@@ -636,31 +395,35 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         l[n][i] = l[n][i] * fast_exp2(m[n][i] - to) + (pr[i][0] + pr[i][1]) * fast_exp2(ref[n][i] - to);
                         m[n][i] = mn;
                     }
-                    // P rounds to f16: 2^-11 of a weight, or 2^-32 of the block's largest
+                    // P rounds to bf16 (2^-8 of a weight), or to f16: 2^-11 of it or 2^-32 of the
+                    // block's largest
                     if constexpr (NARROW) {
                         frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
                     } else {
-                        frag[n].x = transpose8x8(pack_f16x2(pr[0][0], pr[1][0]));
-                        frag[n].y = transpose8x8(pack_f16x2(pr[0][1], pr[1][1]));
+                        frag[n].x = transpose8x8(pack_p<BITS>(pr[0][0], pr[1][0]));
+                        frag[n].y = transpose8x8(pack_p<BITS>(pr[0][1], pr[1][1]));
                     }
                 }
-                if (it >= 2 && !wait(&p_empty[par], it / 2 - 1)) {
+                if (it >= P_BUFFERS && !wait(&p_empty[buffer], it / P_BUFFERS - 1)) {
                     ok = false;
                     break;
                 }
-                float* out_ref = s_ref + (par * WARPS + warp) * 8 * NT;
+                float* out_ref = s_ref + (buffer * BLOCKS + block) * 8 * NT;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if constexpr (NARROW)         // a row's 16: positions 2 i, 2 i + 1, 2 i + 8, 2 i + 9 together
-                        s_p2[(par * WARPS + warp) * 32 + 16 * (t & 1) + (g >> 1) * 4 + (t & 2) + (g & 1)] =
+                        s_p2[(buffer * BLOCKS + block) * 32 + 16 * (t & 1) + (g >> 1) * 4 + (t & 2) + (g & 1)] =
                             static_cast<uint16_t>(frag[n].x);
                     else
-                        s_p[((par * WARPS + warp) * NT + n) * 32 + lane] = frag[n];
+                        s_p[((buffer * BLOCKS + block) * NT + n) * 32 + lane] = frag[n];
                     if (g == 0 && (!NARROW || t == 0))
                         *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(ref[n][0], ref[n][1]);
                 }
-                done_with(&p_full[par]);
+                done_with(&p_full[buffer]);
             }
+            // The next segment's notes are there once its first tile is: the warps that will
+            // read that tile wait for it, and the group meets below.
+            if (ok && end < total && end % TURNS == turn && !wait(&k_full[end % K_BARS], end / K_BARS)) ok = false;
             // ---- (m, l) of the segment: the four warps' sums brought to one reference
             float2* sums = s_sums + (segment & 1) * WARPS * 8 * NT;
 #pragma unroll
@@ -698,11 +461,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int it = 0;
         for (int segment = 0; it < total && ok; ++segment) {
             // (P of a segment's first tile comes after its notes)
-            if (!wait(&p_full[it & 1], it / 2)) {
+            if (!wait(&p_full[it % P_BUFFERS], it / P_BUFFERS)) {
                 ok = false;
                 break;
             }
-            const Segment seg = s_seg[segment & (META - 1)];
+            const Segment seg = s_seg[segment % META];
             // references of rows 2 t + i and g (NARROW: i and g % 2)
             float m[NT][2], mg[NT];
             float o[NT][MTILES][4];
@@ -714,19 +477,19 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             const int w_lo = seg.len - p.q_len + 1 - p.window, lo = p.window > 0 && w_lo > 0 ? w_lo : 0, hi = seg.len;
             for (const int end = it + seg.run; it < end; ++it) {
-                const int slot = it % SLOTS, par = it & 1;
-                if (!wait(&p_full[par], it / 2)) {
+                const int slot = it % SLOTS, buffer = it % P_BUFFERS;
+                if (!wait(&p_full[buffer], it / P_BUFFERS)) {
                     ok = false;
                     break;
                 }
                 // ---- one reference for the tile
-                uint32_t pb[WARPS][NT][2];
+                uint32_t pb[BLOCKS][NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float* all = s_ref + par * WARPS * 8 * NT + 8 * n;
-                    float mn[2] = {m[n][0], m[n][1]}, rg[WARPS];
+                    const float* all = s_ref + buffer * BLOCKS * 8 * NT + 8 * n;
+                    float mn[2] = {m[n][0], m[n][1]}, rg[BLOCKS];
 #pragma unroll
-                    for (int w = 0; w < WARPS; ++w) {
+                    for (int w = 0; w < BLOCKS; ++w) {
                         const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + (NARROW ? 0 : 2 * t));
                         rg[w] = NARROW ? (g & 1 ? x.y : x.x) : all[w * 8 * NT + g];
                         mn[0] = fmaxf(mn[0], x.x);
@@ -749,42 +512,50 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         }
                     }
 #pragma unroll
-                    for (int w = 0; w < WARPS; ++w) {
+                    for (int w = 0; w < BLOCKS; ++w) {
                         const float f = fast_exp2(rg[w] - finite_ref(mg[n]));
-                        const uint32_t f2 = pack_f16x2(f, f);
-                        const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (par * WARPS + w) * 32 + 16 * (g & 1) + 4 * t)
-                                               : s_p[((par * WARPS + w) * NT + n) * 32 + lane];
-                        pb[w][n][0] = mul_f16x2(x.x, f2);
-                        pb[w][n][1] = mul_f16x2(x.y, f2);
+                        const uint32_t f2 = pack_p<BITS>(f, f);
+                        const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (buffer * BLOCKS + w) * 32 + 16 * (g & 1) + 4 * t)
+                                               : s_p[((buffer * BLOCKS + w) * NT + n) * 32 + lane];
+                        pb[w][n][0] = mul_p<BITS>(x.x, f2);
+                        pb[w][n][1] = mul_p<BITS>(x.y, f2);
                     }
                 }
-                done_with(&p_empty[par]);
+                done_with(&p_empty[buffer]);
                 if (!wait(&v_full[slot], it / SLOTS)) {
                     ok = false;
                     break;
                 }
-                // ---- A position that no row sees gets the scale 0 (its bytes may be anything:
-                // codes are finite); lane l: positions l and l + 32 of the tile
-                uint8_t* vst = smem + Smem::v + slot * SLOT;
-                const int4 base4 = *reinterpret_cast<const int4*>(s_base + (it & (META - 1)) * 4);
-                const int first = min(min(base4.x, base4.y), min(base4.z, base4.w));
-                const int last = max(max(base4.x, base4.y), max(base4.z, base4.w));
-                if (first < lo || last + 16 > hi) {
+                // ---- This warp's columns of the positions that no row sees become 0, whatever they
+                // hold (in 4 bits their scales: codes are finite); a position a lane
+                uint8_t* rows = smem + Smem::v + slot * F::SLOT;
+                const int* bases = s_base + (it % META) * BLOCKS;
+                bool edge = false;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int base = lane < 16 ? (i ? base4.z : base4.x) : (i ? base4.w : base4.y);
-                        const int kp = base + (lane & 15);
-                        if (base < 0 || kp < lo || kp >= hi)
-                            *reinterpret_cast<uint2*>(vst + (lane + 32 * i) * ROW + CODES + 8 * warp) = make_uint2(0u, 0u);
+                for (int w = 0; w < BLOCKS; ++w) edge |= bases[w] < lo || bases[w] + 16 > hi;
+                if (edge) {
+                    for (int i = lane; i < TILE; i += 32) {
+                        const int base = bases[i / 16], kp = base + (i & 15);
+                        if (base >= 0 && kp >= lo && kp < hi) continue;
+                        if constexpr (BITS == 4) {
+                            *reinterpret_cast<uint2*>(rows + i * F::ROW + CODES + 8 * warp) = make_uint2(0u, 0u);
+                        } else {
+                            constexpr int BOXES = F::BOXES / WARPS;
+                            for (int j = 0; j < BOXES * 8; ++j)
+                                *reinterpret_cast<uint4*>(rows + ((warp * BOXES + j / 8) * TILE + i) * 128 + 16 * (j & 7)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     fence_proxy_async_smem();     // before the slot is loaded again
                     __syncwarp();
                 }
-                // ---- O^T += V^T P^T for this warp's columns, 16 positions at a time
+                // ---- O^T += V^T P^T for this warp's columns
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    if constexpr (NARROW) add_values_narrow(vst + 16 * w * ROW, warp, lane, pb[w][0], o[0]);
-                    else add_values<NT>(vst + 16 * w * ROW, warp, lane, pb[w], o);
+                for (int w = 0; w < BLOCKS; ++w) {
+                    if constexpr (NARROW) add_values_narrow(rows + 16 * w * F::ROW, warp, lane, pb[w][0], o[0]);
+                    else if constexpr (BITS == 4) add_values_4<NT>(rows + 16 * w * F::ROW, warp, lane, pb[w], o);
+                    else if constexpr (BITS == 8) add_values_8<NT>(rows, 16 * w, warp, lane, pb[w], o);
+                    else add_values_16<NT>(rows, warp, lane, pb[w], o);
                 }
                 done_with(&v_empty[slot]);
             }
@@ -811,11 +582,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int i = 0; i < 2; ++i) {
                         const int r = 8 * n + 2 * t + i;
                         if (r >= R) continue;
-                        float4* dst = reinterpret_cast<float4*>(p.ws_o + (row_index(seg.b, r) * S + mine) * D +
-                                                                128 * warp + 16 * g);
+                        float* dst = p.ws_o + (row_index(seg.b, r) * S + mine) * D + 128 * warp;
 #pragma unroll
                         for (int j = 0; j < MTILES / 2; ++j)
-                            dst[j] = make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
+                            *reinterpret_cast<float4*>(dst + (BITS == 16 ? 64 * (j / 2) + 8 * g + 4 * (j & 1) : 16 * g + 4 * j)) =
+                                make_float4(o[n][2 * j][i] * f, o[n][2 * j][2 + i] * f, o[n][2 * j + 1][i] * f,
                                                  o[n][2 * j + 1][2 + i] * f);
                     }
             }
@@ -825,14 +596,14 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOAD_REGS));
         if (warp == 0) {
             if (lane == 0) {
+                for (int i = 0; i < K_BARS; ++i) mbar_init(&k_full[i], 1);
                 for (int i = 0; i < SLOTS; ++i) {
-                    mbar_init(&k_full[i], 1);
-                    mbar_init(&k_empty[i], WARPS);
+                    mbar_init(&k_empty[i], BLOCKS);
                     mbar_init(&v_full[i], 1);
                     mbar_init(&v_empty[i], WARPS);
                 }
-                for (int i = 0; i < 2; ++i) {
-                    mbar_init(&p_full[i], WARPS);
+                for (int i = 0; i < P_BUFFERS; ++i) {
+                    mbar_init(&p_full[i], BLOCKS);
                     mbar_init(&p_empty[i], WARPS);
                 }
                 fence_mbar_init();
@@ -840,10 +611,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             __syncwarp();
         }
         int range = 0;
-        Walk<LIST> walk = {};
-        if (warp < 2) walk = first_of_range<LIST>(p, index, gridDim.x / p.n_kv_heads, &range);
+        Walk<BITS, LIST> walk = {};
+        if (warp < 2) walk = first_of_range<BITS, LIST>(p, index, gridDim.x / p.n_kv_heads, &range);
         if (warp == 0 && lane == 0) *s_total = walk.left;
         uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
+        const int n_full = warp == 0 ? K_BARS : SLOTS;
         const CUtensorMap* map = warp == 0 ? &tmk : &tmv;
         uint8_t* ring = smem + (warp == 0 ? Smem::k : Smem::v);
         // A run is box_rows positions of one page; lane l keeps the first row and position
@@ -873,23 +645,29 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         };
         // tile i of the range, the sequence's `tile`-th, into its slot; K: what the masks need is noted
         auto load = [&](int i, int tile) {
-            const int slot = i % SLOTS, r = tile * runs_per_tile;
+            const int slot = i % SLOTS, bar = i % n_full, r = tile * runs_per_tile;
             if (r >= run0 + 32) {
                 run0 += 32;
                 look_up();
             }
-            const int row = __shfl_sync(0xffffffffu, run_row, (r - run0 + lane) & 31);
-            const bool mine = lane < runs_per_tile && row >= 0;
+            // lane l: box l % BOXES of the tile's run l / BOXES
+            constexpr int BOXES = F::BOXES;
+            const int run = lane / BOXES, row = __shfl_sync(0xffffffffu, run_row, (r - run0 + run) & 31);
+            const bool mine = run < runs_per_tile && row >= 0;
             const unsigned some = __ballot_sync(0xffffffffu, mine);
             if (warp == 0) {
-                // lanes 0 .. 3: the run of their 16 positions
+                // lanes below BLOCKS: the run of their 16 positions
                 const int base = __shfl_sync(0xffffffffu, run_base, (r - run0 + lane / blocks_per_run) & 31);
-                if (lane < 4) s_base[(i & (META - 1)) * 4 + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
+                if (lane < BLOCKS) s_base[(i % META) * BLOCKS + lane] = base < 0 ? -1 : base + 16 * (lane % blocks_per_run);
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(some) * box * ROW);
+            if (lane == 0) mbar_arrive_expect_tx(&full[bar], __popc(some) * box * (F::ROW / BOXES));
             __syncwarp();
-            if (mine) tma_load_3d(ring + slot * SLOT + lane * box * ROW, map, &full[slot], 0, kvh, row);
+            if (mine) {
+                uint8_t* to = ring + slot * F::SLOT;
+                if constexpr (BITS == 4) tma_load_3d(to + run * box * F::ROW, map, &full[bar], 0, kvh, row);
+                else tma_load_3d(to + ((lane % BOXES) * TILE + run * box) * 128, map, &full[bar], (lane % BOXES) * (1024 / BITS), kvh, row);
+            }
             loaded = i + 1;
         };
         // the first SLOTS tiles find their slots empty, and V's barriers wait for the one below
@@ -908,7 +686,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             for (int b = blockIdx.x * 32 + lane; b < p.batch; b += gridDim.x * 32)
                 if (p.kv_lens[b] < 0 || p.kv_lens[b] > p.len_cap) report_error(p.err, FA512_DEVICE_ERR_INDEX);
             for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-                if (item_of<LIST>(p, b).tiles == 0)
+                if (item_of<BITS, LIST>(p, b).tiles == 0)
                     for (int i = lane; i < p.q_len * p.n_q_heads * S; i += 32)
                         reinterpret_cast<float2*>(p.ws_ml)[static_cast<size_t>(b) * p.q_len * p.n_q_heads * S + i] =
                             make_float2(-INFINITY, 0.f);
@@ -917,7 +695,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         for (int segment = 0; walk.left > 0 && ok; ++segment) {
             const int run = walk.run(), end = it + run, from = walk.tile - it;
             if (warp == 0 && lane == 0)
-                s_seg[segment & (META - 1)] = {walk.b, walk.item.len, run,
+                s_seg[segment % META] = {walk.b, walk.item.len, run,
                                                (S == 1 ? 0 : index - walk.start / range) +
                                                    (walk.tile + run == walk.item.tiles ? Segment::LAST : 0)};
             run0 = walk.tile * runs_per_tile;
@@ -941,36 +719,43 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     // lands after this CTA has gone.
     if (__syncthreads_or(!ok) && role == 2 && warp < 2) {
         uint64_t* full = warp == 0 ? k_full : v_full;
-        for (int i = max(0, loaded - SLOTS); i < loaded; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, p.err);
+        const int n_full = warp == 0 ? K_BARS : SLOTS;
+        for (int i = max(0, loaded - SLOTS); i < loaded; ++i) mbar_wait(&full[i % n_full], (i / n_full) & 1, p.err);
     }
 }
 
-template <int ROWS, bool LIST>
+template <int BITS, int ROWS, bool LIST>
 cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, cudaStream_t stream) {
-    constexpr int SMEM = Smem<(ROWS > 8 ? 2 : 1)>::total;
-    cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<ROWS, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    constexpr int SMEM = Smem<BITS, (ROWS > 8 ? 2 : 1)>::total;
+    auto kernel = decode_ranges_kernel<BITS, ROWS, LIST>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    const int grid = p.groups * p.n_kv_heads;
-    decode_fp4_kernel<ROWS, LIST><<<grid, THREADS, SMEM, stream>>>(tmk, tmv, p);
+    kernel<<<p.groups * p.n_kv_heads, THREADS, SMEM, stream>>>(tmk, tmv, p);
     return cudaGetLastError();
 }
 
-template <bool LIST>
+template <int BITS, bool LIST>
 cudaError_t launch_rows(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, cudaStream_t stream) {
     const int rows = p.q_len * p.group;
-    return rows <= 2   ? launch<2, LIST>(tmk, tmv, p, stream)
-           : rows <= 8 ? launch<8, LIST>(tmk, tmv, p, stream)
-                       : launch<16, LIST>(tmk, tmv, p, stream);
+    if constexpr (BITS == 4)
+        if (rows <= 2) return launch<BITS, 2, LIST>(tmk, tmv, p, stream);
+    return rows <= 8 ? launch<BITS, 8, LIST>(tmk, tmv, p, stream) : launch<BITS, 16, LIST>(tmk, tmv, p, stream);
 }
 
-}  // namespace fp4
+}  // namespace ranges
 
-int decode_fp4_tile_positions() { return fp4::TILE; }
-int decode_fp4_ctas_per_sm() { return fp4::CTAS_PER_SM; }
+int decode_ranges_tile(int bits) {
+    return bits == 16 ? ranges::Format<16>::TILE : bits == 8 ? ranges::Format<8>::TILE : ranges::Format<4>::TILE;
+}
+int decode_ranges_ctas_per_sm() { return ranges::CTAS_PER_SM; }
 
-cudaError_t launch_decode_fp4(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
-                              cudaStream_t stream) {
-    const cudaError_t e = p.listed ? fp4::launch_rows<true>(tmk, tmv, p, stream) : fp4::launch_rows<false>(tmk, tmv, p, stream);
+cudaError_t launch_decode_ranges(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, int bits,
+                                 cudaStream_t stream) {
+    cudaError_t e;
+    if (bits == 4)
+        e = p.listed ? ranges::launch_rows<4, true>(tmk, tmv, p, stream) : ranges::launch_rows<4, false>(tmk, tmv, p, stream);
+    else
+        e = bits == 8 ? ranges::launch_rows<8, true>(tmk, tmv, p, stream) : ranges::launch_rows<16, true>(tmk, tmv, p, stream);
     return e != cudaSuccess ? e : launch_decode_merge(p, stream);
 }
 

@@ -37,7 +37,6 @@
 
 #include "fa512_device.cuh"
 #include "fa512_internal.h"
-#include "fa512_list.cuh"
 
 namespace fa512 {
 namespace decode {
@@ -99,52 +98,15 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk16) {
 // a run of box_rows positions is loaded iff it overlaps [lo, hi) and its page
 // index is valid.  Returns a 32-bit mask of loaded positions and the number
 // of loaded runs.
-//
-// LIST: tile t is positions [32t, 32t + 32) counted along the list of pages of
-// KV head kvh; base[i] is the position of its 16 i-th one (-1: not loaded).
 struct TilePlan {
     uint32_t loaded;   // bit r: position 32t + r was loaded
     int runs;
-    int base[2];       // LIST
-    int row[2];        // LIST: row of the pool of each 16 positions
 };
 
-template <bool LIST>
-__device__ __forceinline__ TilePlan plan_tile(const DecodeParams& p, int b, int kvh, int t, int lo,
+__device__ __forceinline__ TilePlan plan_tile(const DecodeParams& p, int b, int t, int lo,
                                               int hi, bool record) {
-    TilePlan plan{0u, 0, {-1, -1}, {-1, -1}};
+    TilePlan plan{0u, 0};
     const int box_rows = p.box_rows;
-    if constexpr (LIST) {
-        const int held = (hi + p.page_size - 1) / p.page_size;
-        const int32_t* list = list_of(p, b, kvh);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int v = t * TILE_K + 16 * i;
-            const int e = v / p.page_size, off = v - e * p.page_size;
-            if (i == 1 && box_rows == TILE_K) {       // one run
-                if (plan.base[0] >= 0) {
-                    plan.base[1] = plan.base[0] + 16;
-                    plan.row[1] = plan.row[0] + 16;
-                }
-                break;
-            }
-            if (e >= p.n_listed) break;
-            const int lp = list_page(p, list, e, held);
-            if (lp < 0) continue;
-            const int pos0 = lp * p.page_size + off;
-            if (pos0 >= hi) continue;
-            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
-            if (page < 0 || page >= p.num_pages) {
-                if (record) report_error(p.err, FA512_DEVICE_ERR_INDEX);
-                continue;
-            }
-            plan.base[i] = pos0;
-            plan.row[i] = page * p.page_size + off;
-            plan.loaded |= ((box_rows >= 32) ? 0xffffffffu : 0xffffu) << (16 * i);
-            plan.runs += 1;
-        }
-        return plan;
-    }
     for (int r0 = 0; r0 < TILE_K; r0 += box_rows) {
         const int pos0 = t * TILE_K + r0;
         if (pos0 + box_rows <= lo || pos0 >= hi) continue;
@@ -161,34 +123,21 @@ __device__ __forceinline__ TilePlan plan_tile(const DecodeParams& p, int b, int 
     return plan;
 }
 
-// End of the tiles [t_begin, t_begin + n) along the list that hold pages.
-__device__ __forceinline__ int list_tiles(const DecodeParams& p, int b, int kvh, int t_begin, int n) {
-    const long long all = static_cast<long long>(p.n_listed) * p.page_size;
-    const int v0 = static_cast<int>(min(static_cast<long long>(t_begin) * TILE_K, all));
-    const int v1 = static_cast<int>(min((static_cast<long long>(t_begin) + n) * TILE_K, all));
-    return (list_end(p, list_of(p, b, kvh), v0, v1) + TILE_K - 1) / TILE_K;
-}
-
-template <bool FP8, bool LIST>
+template <bool FP8>
 __device__ __forceinline__ void issue_tile(const DecodeParams& p, const CUtensorMap* tmk,
                                            const CUtensorMap* tmv, uint8_t* stage,
                                            uint64_t* bar, int b, int kvh, int t, int lo, int hi) {
-    const TilePlan plan = plan_tile<LIST>(p, b, kvh, t, lo, hi, true);
+    const TilePlan plan = plan_tile(p, b, t, lo, hi, true);
     const int box_rows = p.box_rows;
     // K and V rows of every loaded run: 512 elements each
     const uint32_t row_bytes = FP8 ? static_cast<uint32_t>(D) : static_cast<uint32_t>(D) * 2u;
     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(plan.runs) * box_rows * row_bytes * 2u);
     for (int r0 = 0; r0 < TILE_K; r0 += box_rows) {
         if (!((plan.loaded >> r0) & 1u)) continue;
-        int row;
-        if constexpr (LIST) {
-            row = r0 ? plan.row[1] : plan.row[0];
-        } else {
-            const int pos0 = t * TILE_K + r0;
-            const int lp = pos0 / p.page_size;
-            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
-            row = page * p.page_size + (pos0 - lp * p.page_size);
-        }
+        const int pos0 = t * TILE_K + r0;
+        const int lp = pos0 / p.page_size;
+        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
+        const int row = page * p.page_size + (pos0 - lp * p.page_size);
         if constexpr (FP8) {
             for (int c = 0; c < D / F8_BOX_BYTES; ++c) {
                 const int off = c * (TILE_K * F8_BOX_BYTES) + r0 * F8_BOX_BYTES;
@@ -253,7 +202,7 @@ __device__ __forceinline__ void convert_fp8_stage(const uint8_t* stage, uint8_t*
 // NUM_STAGES-deep ring in shared memory filled by TMA (one box per page run),
 // computes S = Q K^T and O += P V for its rows with bf16 mma.sync (rows padded
 // to 16), and keeps the softmax state in the log2 domain.
-template <bool FP8, bool LIST>
+template <bool FP8>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 decode_split_kernel(const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const DecodeParams p) {
@@ -288,10 +237,9 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmk,
     const int w_lo = len - p.q_len + 1 - p.window;
     const int lo = (p.window > 0 && w_lo > 0) ? w_lo : 0;
     const int t_lo = lo / TILE_K;
-    int t_hi = (hi + TILE_K - 1) / TILE_K;
+    const int t_hi = (hi + TILE_K - 1) / TILE_K;
     const int t_begin = t_lo + split * p.tiles_per_split;
     int t_end = t_begin + p.tiles_per_split;
-    if constexpr (LIST) t_hi = list_tiles(p, b, kvh, t_begin, p.tiles_per_split);
     if (t_end > t_hi) t_end = t_hi;
     const int n_tiles = t_end > t_begin ? t_end - t_begin : 0;
 
@@ -319,7 +267,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmk,
     // prologue loads
     if (tid == 0) {
         for (int s = 0; s < NUM_STAGES - 1 && s < n_tiles; ++s)
-            issue_tile<FP8, LIST>(p, &tmk, &tmv, smem + s * Smem::stage_bytes, &full_bar[s], b, kvh,
+            issue_tile<FP8>(p, &tmk, &tmv, smem + s * Smem::stage_bytes, &full_bar[s], b, kvh,
                             t_begin + s, lo, hi);
     }
 
@@ -360,19 +308,13 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmk,
         // refill the stage consumed in the previous iteration
         if (tid == 0 && it + NUM_STAGES - 1 < n_tiles) {
             const int nst = (it + NUM_STAGES - 1) % NUM_STAGES;
-            issue_tile<FP8, LIST>(p, &tmk, &tmv, smem + nst * Smem::stage_bytes, &full_bar[nst], b,
+            issue_tile<FP8>(p, &tmk, &tmv, smem + nst * Smem::stage_bytes, &full_bar[nst], b,
                             kvh, t + NUM_STAGES - 1, lo, hi);
         }
-        const TilePlan plan = plan_tile<LIST>(p, b, kvh, t, lo, hi, false);
+        const TilePlan plan = plan_tile(p, b, t, lo, hi, false);
         // live positions of this tile: loaded and inside [lo, hi)
         uint32_t valid = plan.loaded;
-        if constexpr (LIST) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {             // positions of 16 before the sequence's end
-                const int n = plan.base[i] < 0 ? 0 : min(16, hi - plan.base[i]);
-                valid &= ~(((0xffffu << max(n, 0)) & 0xffffu) << (16 * i));
-            }
-        } else {
+        {
             const int pos0 = t * TILE_K;
             const int a = lo - pos0 > 0 ? lo - pos0 : 0;
             const int e = hi - pos0 < TILE_K ? hi - pos0 : TILE_K;
@@ -434,7 +376,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmk,
             const int r = nt * 8 + 2 * (lane & 3);
             const bool v0 = (valid >> r) & 1u, v1 = (valid >> (r + 1)) & 1u;
             // each row sees the live keys up to its own position (and inside its window)
-            const int pos = LIST ? (r < 16 ? plan.base[0] : plan.base[1]) + (r & 15) : t * TILE_K + r;
+            const int pos = t * TILE_K + r;
             auto sees = [&](int kpos, int qp) {
                 return kpos <= qp && (p.window <= 0 || kpos > qp - p.window);
             };
@@ -906,7 +848,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-template <bool LIST>
 __global__ void __launch_bounds__(F8_WARPS * 32, F8_CTAS_PER_SM)
 decode_fp8_mma_kernel(const DecodeParams p) {
     allow_merge_launch();
@@ -927,13 +868,8 @@ decode_fp8_mma_kernel(const DecodeParams p) {
     const int w_lo = len - p.q_len + 1 - p.window;
     const int lo = (p.window > 0 && w_lo > 0) ? w_lo : 0;
     const int t_begin = lo / TILE_K + split * p.tiles_per_split;
-    // LIST: positions are counted along the list of pages; a chunk lies in one page
-    const int32_t* list = LIST ? list_of(p, b, kvh) : nullptr;
-    const int held = (hi + p.page_size - 1) / p.page_size;
-    const int pb = LIST ? static_cast<int>(min(static_cast<long long>(t_begin) * TILE_K, static_cast<long long>(p.n_listed) * p.page_size))
-                        : max(lo, t_begin * TILE_K);
-    const int pe = LIST ? list_end(p, list, pb, static_cast<int>(min((static_cast<long long>(t_begin) + p.tiles_per_split) * TILE_K, static_cast<long long>(p.n_listed) * p.page_size)))
-                        : min(hi, (t_begin + p.tiles_per_split) * TILE_K);
+    const int pb = max(lo, t_begin * TILE_K);
+    const int pe = min(hi, (t_begin + p.tiles_per_split) * TILE_K);
     const int n_chunks = pe > pb ? (pe - pb + CPOS - 1) / CPOS : 0;
 
     // ---- Q^T fragments of this warp's slice: b0/b1 of k-step (j, s) hold
@@ -1003,25 +939,16 @@ decode_fp8_mma_kernel(const DecodeParams p) {
     // sectors.
     // page of this lane's position in chunk k, loaded one chunk before the
     // chunk's copies are issued (the copies never wait on the page table)
-    // LIST: the first position of chunk k, -1 where its entry names no page
-    auto first_of = [&](int k) -> int {
-        const int v = pb + k * CPOS;
-        if (k >= n_chunks || v >= pe) return -1;
-        const int e = v / p.page_size, lp = list_page(p, list, e, held);
-        return lp < 0 ? -1 : lp * p.page_size + (v - e * p.page_size);
-    };
-    auto page_of = [&](int k, int first) -> int {
-        if constexpr (LIST)
-            return first >= 0 ? p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + first / p.page_size] : 0;
+    auto page_of = [&](int k) -> int {
         const int pos = pb + k * CPOS + (lane >> 1);
         return (k < n_chunks && pos < pe)
                    ? p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + pos / p.page_size]
                    : 0;
     };
-    auto issue = [&](int k, int page, int first) {
+    auto issue = [&](int k, int page) {
         if (k < n_chunks) {
-            const int pos = (LIST ? first : pb + k * CPOS) + (lane >> 1);
-            bool valid = LIST ? first >= 0 && pos < hi : pos < pe;
+            const int pos = pb + k * CPOS + (lane >> 1);
+            bool valid = pos < pe;
             size_t row = 0;
             if (valid) {
                 if (page < 0 || page >= p.num_pages) {
@@ -1044,30 +971,19 @@ decode_fp8_mma_kernel(const DecodeParams p) {
         }
         cp_async_commit();
     };
-    // LIST: an entry is read one chunk before its page; the chunks in the ring keep their first positions
-    int first[STAGES + 1] = {};
-    if constexpr (LIST) {
+    int page_next = page_of(STAGES - 1);
 #pragma unroll
-        for (int k = 0; k <= STAGES; ++k) first[k] = first_of(k);
-    }
-    int page_next = page_of(STAGES - 1, LIST ? first[STAGES - 1] : 0);
-#pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) issue(k, page_of(k, LIST ? first[k] : 0), LIST ? first[k] : 0);
+    for (int k = 0; k < STAGES - 1; ++k) issue(k, page_of(k));
 
     for (int k = 0; k < n_chunks; ++k) {
         const int page_now = page_next;
-        page_next = page_of(k + STAGES, LIST ? first[STAGES] : 0);
-        issue(k + STAGES - 1, page_now, LIST ? first[STAGES - 1] : 0);
-        const int pos0 = LIST ? first[0] : pb + k * CPOS;
-        if constexpr (LIST) {
-#pragma unroll
-            for (int i = 0; i < STAGES; ++i) first[i] = first[i + 1];
-            first[STAGES] = first_of(k + STAGES + 1);
-        }
+        page_next = page_of(k + STAGES);
+        issue(k + STAGES - 1, page_now);
         cp_async_wait<STAGES - 1>();
         __syncwarp();                         // every lane's copies of chunk k are visible
         const uint8_t* kst = smem + (sl * STAGES + (k % STAGES)) * CHUNK_BYTES;
         const uint8_t* vst = kst + CPOS * SLICE;
+        const int pos0 = pb + k * CPOS;
 
         // ---- S^T slice = K_slice Q_slice^T, one accumulator chain per 64
         // head-dim elements, summed at the end
@@ -1108,7 +1024,7 @@ decode_fp8_mma_kernel(const DecodeParams p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             auto sees = [&](int kp) {
-                return (LIST ? pos0 >= 0 : kp < pe) && kp <= qpos[i] && (p.window <= 0 || kp > qpos[i] - p.window);
+                return kp < pe && kp <= qpos[i] && (p.window <= 0 || kp > qpos[i] - p.window);
             };
             sv[i][0] = sees(pos0 + g) ? sc[i] * p.scale_log2 : -INFINITY;
             sv[i][1] = sees(pos0 + g + 8) ? sc[2 + i] * p.scale_log2 : -INFINITY;
@@ -1265,7 +1181,6 @@ __device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t y, uint32_t sel) {
     return t;
 }
 
-template <bool LIST>
 __global__ void __launch_bounds__(WARPS * 32, 1)
 decode_bf16_mma_kernel(const DecodeParams p) {
     allow_merge_launch();
@@ -1290,13 +1205,8 @@ decode_bf16_mma_kernel(const DecodeParams p) {
     const int w_lo = len - p.q_len + 1 - p.window;
     const int lo = (p.window > 0 && w_lo > 0) ? w_lo : 0;
     const int t_begin = lo / TILE_K + split * p.tiles_per_split;
-    // LIST: positions are counted along the list of pages; a chunk lies in one page
-    const int32_t* list = LIST ? list_of(p, b, kvh) : nullptr;
-    const int held = (hi + p.page_size - 1) / p.page_size;
-    const int pb = LIST ? static_cast<int>(min(static_cast<long long>(t_begin) * TILE_K, static_cast<long long>(p.n_listed) * p.page_size))
-                        : max(lo, t_begin * TILE_K);
-    const int pe = LIST ? list_end(p, list, pb, static_cast<int>(min((static_cast<long long>(t_begin) + p.tiles_per_split) * TILE_K, static_cast<long long>(p.n_listed) * p.page_size)))
-                        : min(hi, (t_begin + p.tiles_per_split) * TILE_K);
+    const int pb = max(lo, t_begin * TILE_K);
+    const int pe = min(hi, (t_begin + p.tiles_per_split) * TILE_K);
     const int n_chunks = pe > pb ? (pe - pb + CPOS - 1) / CPOS : 0;
     const int my_chunks = n_chunks > pg ? (n_chunks - pg + GROUPS - 1) / GROUPS : 0;
 
@@ -1337,25 +1247,16 @@ decode_bf16_mma_kernel(const DecodeParams p) {
     // V slice (s >= 4): four lanes cover 64 contiguous bytes of a row
     // page of this lane's position in chunk k, loaded one chunk before the
     // chunk's copies are issued (the copies never wait on the page table)
-    // LIST: the first position of chunk k, -1 where its entry names no page
-    auto first_of = [&](int k) -> int {
-        const int v = pb + (pg + GROUPS * k) * CPOS;
-        if (k >= my_chunks || v >= pe) return -1;
-        const int e = v / p.page_size, lp = list_page(p, list, e, held);
-        return lp < 0 ? -1 : lp * p.page_size + (v - e * p.page_size);
-    };
-    auto page_of = [&](int k, int first) -> int {
-        if constexpr (LIST)
-            return first >= 0 ? p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + first / p.page_size] : 0;
+    auto page_of = [&](int k) -> int {
         const int pos = pb + (pg + GROUPS * k) * CPOS + (lane >> 2);
         return (k < my_chunks && pos < pe)
                    ? p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + pos / p.page_size]
                    : 0;
     };
-    auto issue = [&](int k, int page, int first) {
+    auto issue = [&](int k, int page) {
         if (k < my_chunks) {
-            const int pos = (LIST ? first : pb + (pg + GROUPS * k) * CPOS) + (lane >> 2);
-            bool valid = LIST ? first >= 0 && pos < hi : pos < pe;
+            const int pos = pb + (pg + GROUPS * k) * CPOS + (lane >> 2);
+            bool valid = pos < pe;
             size_t row = 0;
             if (valid) {
                 if (page < 0 || page >= p.num_pages) {
@@ -1379,30 +1280,19 @@ decode_bf16_mma_kernel(const DecodeParams p) {
         }
         mma8::cp_async_commit();
     };
-    // LIST: an entry is read one chunk before its page; the chunks in the ring keep their first positions
-    int first[STAGES + 1] = {};
-    if constexpr (LIST) {
+    int page_next = page_of(STAGES - 1);
 #pragma unroll
-        for (int k = 0; k <= STAGES; ++k) first[k] = first_of(k);
-    }
-    int page_next = page_of(STAGES - 1, LIST ? first[STAGES - 1] : 0);
-#pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) issue(k, page_of(k, LIST ? first[k] : 0), LIST ? first[k] : 0);
+    for (int k = 0; k < STAGES - 1; ++k) issue(k, page_of(k));
 
     for (int k = 0; k < my_chunks; ++k) {
         const int page_now = page_next;
-        page_next = page_of(k + STAGES, LIST ? first[STAGES] : 0);
-        issue(k + STAGES - 1, page_now, LIST ? first[STAGES - 1] : 0);
-        const int pos0 = LIST ? first[0] : pb + (pg + GROUPS * k) * CPOS;
-        if constexpr (LIST) {
-#pragma unroll
-            for (int i = 0; i < STAGES; ++i) first[i] = first[i + 1];
-            first[STAGES] = first_of(k + STAGES + 1);
-        }
+        page_next = page_of(k + STAGES);
+        issue(k + STAGES - 1, page_now);
         mma8::cp_async_wait<STAGES - 1>();
         __syncwarp();                         // every lane's copies of chunk k are visible
         const uint8_t* kst = smem + (warp * STAGES + (k % STAGES)) * CHUNK_BYTES;
         const uint8_t* vst = kst + CPOS * ROW;
+        const int pos0 = pb + (pg + GROUPS * k) * CPOS;
 
         // ---- S^T slice = K_slice Q_slice^T over positions g (rows g + 8 are zero);
         // one accumulator chain per 32 head-dim elements, summed at the end
@@ -1433,7 +1323,7 @@ decode_bf16_mma_kernel(const DecodeParams p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int kp = pos0 + g;
-            const bool sees = (LIST ? pos0 >= 0 : kp < pe) && kp <= qpos[i] && (p.window <= 0 || kp > qpos[i] - p.window);
+            const bool sees = kp < pe && kp <= qpos[i] && (p.window <= 0 || kp > qpos[i] - p.window);
             pr[i] = sees ? sc[i] * p.scale_log2 : -INFINITY;
             cm[i] = pr[i];
         }
@@ -1690,49 +1580,47 @@ static cudaError_t launch_stream(const DecodeParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <bool LIST>
 static cudaError_t launch_bf16_mma(const DecodeParams& p, cudaStream_t stream) {
     const int smem = decode::mma16::SMEM_BYTES;
-    cudaError_t e = cudaFuncSetAttribute(decode::mma16::decode_bf16_mma_kernel<LIST>,
+    cudaError_t e = cudaFuncSetAttribute(decode::mma16::decode_bf16_mma_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     dim3 grid(p.num_splits, p.n_kv_heads, p.batch);
-    decode::mma16::decode_bf16_mma_kernel<LIST><<<grid, decode::mma8::WARPS * 32, smem, stream>>>(p);
+    decode::mma16::decode_bf16_mma_kernel<<<grid, decode::mma8::WARPS * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <bool LIST>
 static cudaError_t launch_fp8_mma(const DecodeParams& p, cudaStream_t stream) {
     const int smem = decode::mma8::F8_SMEM_BYTES;
-    cudaError_t e = cudaFuncSetAttribute(decode::mma8::decode_fp8_mma_kernel<LIST>,
+    cudaError_t e = cudaFuncSetAttribute(decode::mma8::decode_fp8_mma_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     dim3 grid(p.num_splits, p.n_kv_heads, p.batch);
-    decode::mma8::decode_fp8_mma_kernel<LIST><<<grid, decode::mma8::F8_WARPS * 32, smem, stream>>>(p);
+    decode::mma8::decode_fp8_mma_kernel<<<grid, decode::mma8::F8_WARPS * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <bool FP8, bool LIST>
+template <bool FP8>
 static cudaError_t launch_split_and_merge(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                           const DecodeParams& p, cudaStream_t stream) {
     cudaError_t e;
     if (FP8 && p.q_len * p.group <= decode_fp8_mma_rows()) {
-        e = launch_fp8_mma<LIST>(p, stream);
-    } else if (!FP8 && !LIST && p.q_len == 1 && p.group <= 2 && p.tiles_per_split * TILE_POSITIONS < 1024) {
+        e = launch_fp8_mma(p, stream);
+    } else if (!FP8 && p.q_len == 1 && p.group <= 2 && p.tiles_per_split * TILE_POSITIONS < 1024) {
         // short splits (small batches): the FMA streaming kernel's lighter
         // set-up wins; from 1024 positions a split on, the tensor-core one
         e = p.group == 1 ? launch_stream<1>(p, stream) : launch_stream<2>(p, stream);
     } else if (!FP8 && p.q_len * p.group <= 8) {
-        e = launch_bf16_mma<LIST>(p, stream);
+        e = launch_bf16_mma(p, stream);
     } else {
         // larger query groups or several tokens: S and PV on the tensor cores
         // (q_len * G rows padded to 16)
         const int smem = decode::Smem<FP8>::total + 1024;
-        e = cudaFuncSetAttribute(decode::decode_split_kernel<FP8, LIST>,
+        e = cudaFuncSetAttribute(decode::decode_split_kernel<FP8>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         dim3 grid(p.num_splits, p.n_kv_heads, p.batch);
-        decode::decode_split_kernel<FP8, LIST><<<grid, decode::NUM_THREADS, smem, stream>>>(tmk, tmv, p);
+        decode::decode_split_kernel<FP8><<<grid, decode::NUM_THREADS, smem, stream>>>(tmk, tmv, p);
         e = cudaGetLastError();
     }
     return e != cudaSuccess ? e : launch_decode_merge(p, stream);
@@ -1760,14 +1648,12 @@ cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream) {
 
 cudaError_t launch_decode(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
                           cudaStream_t stream) {
-    return p.listed ? launch_split_and_merge<false, true>(tmk, tmv, p, stream)
-                    : launch_split_and_merge<false, false>(tmk, tmv, p, stream);
+    return launch_split_and_merge<false>(tmk, tmv, p, stream);
 }
 
 cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const DecodeParams& p, cudaStream_t stream) {
-    return p.listed ? launch_split_and_merge<true, true>(tmk, tmv, p, stream)
-                    : launch_split_and_merge<true, false>(tmk, tmv, p, stream);
+    return launch_split_and_merge<true>(tmk, tmv, p, stream);
 }
 
 }  // namespace fa512

@@ -32,7 +32,7 @@ struct DecodeParams {
     int window;
     int tiles_per_split, num_splits;
     int page_shift;                // page_size = 1 << page_shift
-    int groups;                    // 4-bit kernel: ranges that the tiles of all sequences are dealt in, tiles_per_split long at least
+    int groups;                    // kernels over ranges: ranges that the tiles of all sequences are dealt in, tiles_per_split long at least
     float scale_log2;              // scale * log2(e)
     unsigned* err;                 // device error word
     // Selected pages (null: all of the band): [batch, n_kv_heads, n_listed] logical
@@ -62,14 +62,15 @@ cudaError_t launch_decode_fp8(const CUtensorMap& tmk, const CUtensorMap& tmv,
 // Combines the split partials of a kernel that has allowed a dependent launch.
 cudaError_t launch_decode_merge(const DecodeParams& p, cudaStream_t stream);
 
-// 4-bit cache: tmk / tmv map rows of kFp4RowBytes as 32-bit words, boxes of a
-// whole row x box_rows positions (min(page_size, decode_fp4_tile_positions())),
-// no swizzle; k8 / v8 are unused.
+// Kernels over ranges of tiles: a 4-bit cache (bits 4), or listed pages of any (16, 8, 4).
+// tmk / tmv: 4 bits, rows of kFp4RowBytes as 32-bit words, boxes of a whole row x
+// box_rows positions (min(page_size, decode_ranges_tile())), no swizzle; else boxes of
+// 128 bytes x box_rows positions, 128-byte swizzle.  The pages' pointers are unused.
 constexpr int kFp4RowBytes = 288;  // 256 bytes of E2M1 pairs, 32 E4M3 scales
-int decode_fp4_tile_positions();
-int decode_fp4_ctas_per_sm();
-cudaError_t launch_decode_fp4(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p,
-                              cudaStream_t stream);
+int decode_ranges_tile(int bits);  // positions
+int decode_ranges_ctas_per_sm();
+cudaError_t launch_decode_ranges(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, int bits,
+                                 cudaStream_t stream);
 
 // Bounds of a page's keys, and the pages whose bounds allow the largest products.
 struct BoundsParams {

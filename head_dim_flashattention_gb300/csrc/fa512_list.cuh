@@ -25,18 +25,4 @@ __device__ __forceinline__ int list_page(const DecodeParams& p, const int32_t* l
     return page;
 }
 
-// End of the positions [v0, v1), counted along the list, after the entries
-// without a page at their end are left out.  All lanes of a warp together;
-// v0 is a multiple of 16.
-__device__ __forceinline__ int list_end(const DecodeParams& p, const int32_t* list, int v0, int v1) {
-    const int lane = threadIdx.x & 31;
-    const int e0 = v0 / p.page_size, e1 = min(p.n_listed, (v1 + p.page_size - 1) / p.page_size);
-    int last = -1;
-    for (int e = e0; e < e1; e += 32) {
-        const unsigned some = __ballot_sync(0xffffffffu, e + lane < e1 && list[e + lane] >= 0);
-        if (some) last = e + 31 - __clz(some);
-    }
-    return last < 0 ? v0 : min(v1, (last + 1) * p.page_size);
-}
-
 }  // namespace fa512
