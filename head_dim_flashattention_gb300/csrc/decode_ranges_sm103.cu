@@ -236,8 +236,12 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     bool ok = true;                              // the same in all lanes of a warp
     int loaded = 0;                              // tiles whose load this warp has issued
 
-    // The launch's 80 registers a thread are dealt anew: a share for each role.
-    constexpr int K_REGS = NT == 1 ? 128 : 88, V_REGS = NT == 1 ? 80 : 120, LOAD_REGS = 32;
+    // The launch's 80 registers a thread are dealt anew: a share for each role.  V^T in
+    // bf16 and E4M3 needs fewer than in 4 bits, and its smaller tiles come from more
+    // pages, for which the loads take more (16 sequences, 200 pages of 16, E4M3: 57 us
+    // with 32, 51 with 40; 16 x 64 pages of 64, bf16: 95 and 90).
+    constexpr int K_REGS = NT == 1 ? 128 : 88, V_REGS = (NT == 1 ? 80 : 120) - (BITS == 4 ? 0 : 8),
+                  LOAD_REGS = BITS == 4 ? 32 : 40;
     static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * 80, "no more than the launch has");
     if (role == 0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K_REGS));
