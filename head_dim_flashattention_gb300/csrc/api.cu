@@ -776,10 +776,11 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
     if (static_cast<long long>(q_len) * G > 16)
         return fail(FA512_ERR_UNSUPPORTED, "q_len x query heads per KV head (%d x %d) must be at most 16", q_len, G);
     if (!pow2_page(page_size)) return fail(FA512_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+    // (the kernel looks up to 32 runs of up to 64 positions ahead of a sequence's end)
     if (num_pages < 1 || max_pages_per_seq < 1)
         return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
-    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 256 ||
-        static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 256)
+    if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL - 4096 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL - 4096)
         return fail(FA512_ERR_UNSUPPORTED, "page pool or page table too large for int32 key rows");
     if (max_kv_len < 0 || static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages_per_seq) * page_size)
         return fail(FA512_ERR_INVALID_ARG, "max_kv_len outside [0, max_pages_per_seq * page_size]");
@@ -788,7 +789,7 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
     if (!(k_scale == k_scale) || isinf(k_scale) || !(v_scale == v_scale) || isinf(v_scale))
         return fail(FA512_ERR_INVALID_ARG, "k_scale and v_scale must be finite");
     if (sparse && n_selected < 1) return fail(FA512_ERR_INVALID_ARG, "n_selected must be >= 1");
-    if (sparse && static_cast<long long>(n_selected) * page_size > 0x7fffffffLL - 256)
+    if (sparse && static_cast<long long>(n_selected) * page_size > 0x7fffffffLL - 4096)
         return fail(FA512_ERR_UNSUPPORTED, "list of pages too large for int32 positions");
     if (static_cast<long long>(batch) * q_len > 65535 || n_kv_heads > 65535)
         return fail(FA512_ERR_UNSUPPORTED, "grid too large");
@@ -815,7 +816,7 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
         if (band < most) most = band;
     }
     if (most < 1) most = 1;
-    if (batch > 0x7fffffffLL / most) return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
+    if (batch > (1LL << 30) / most) return fail(FA512_ERR_UNSUPPORTED, "more key tiles than int32 counts");
 
     unsigned* err = nullptr;
     cudaError_t e = device_error_ptr(&err);

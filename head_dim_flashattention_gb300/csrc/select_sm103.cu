@@ -187,12 +187,12 @@ constexpr int PAGE_BYTES = 2 * D * 2;                // a page's bounds
 // shared memory: the warps' rings, then the query rows as fp32
 constexpr int score_smem(int rows) { return SCORE_WARPS * SCORE_STAGES * PAGE_BYTES + rows * D * 4; }
 
-// Unsigned integers in the order of the scores, -0 and 0 equal.  Largest of all,
-// with the pages that are always chosen, are those with a NaN or infinite score:
-// the formula above turns every bound that is not finite into one of the two.
-constexpr uint32_t KEY_MOST = 0xffffffffu;
+// Unsigned integers in the order of the scores, -0 and 0 equal.  Largest of all are the
+// pages that are always chosen, then those with a NaN or infinite score: the formula
+// above turns every bound that is not finite into one of the two.
+constexpr uint32_t KEY_ALWAYS = 0xffffffffu, KEY_NOT_FINITE = 0xfffffffeu;
 __device__ __forceinline__ uint32_t key_of(float x) {
-    if (x != x || x == INFINITY) return KEY_MOST;
+    if (x != x || x == INFINITY) return KEY_NOT_FINITE;
     const uint32_t u = __float_as_uint(x + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
             const int page = k ? now[1] : now[0];
             if (page == -2) report_error(p.err, FA512_DEVICE_ERR_INDEX);
             // (outside the pool: lowest)
-            keys[lp] = page == -2 ? 0u : page == -1 || nan ? KEY_MOST : key_of(best);
+            keys[lp] = page == -2 ? 0u : page == -1 ? KEY_ALWAYS : nan ? KEY_NOT_FINITE : key_of(best);
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");

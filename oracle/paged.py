@@ -316,9 +316,12 @@ def select_pages(q, bounds, page_table, kv_lens, psz: int, n_select: int, n_firs
         if not held:
             continue
         score = page_scores(q, bounds, page_table, kl, b, psz, np.float32)
-        score[:, :n_first] = np.inf
-        score[:, max(0, held - n_last):] = np.inf
+        # those always chosen, then those with a bound that is not finite, then by the score
+        rank = np.full(score.shape, 2)
+        rank[~np.isfinite(widen_bf16(bounds)[_i32(page_table)[b, :held]]).all(axis=(2, 3)).T] = 1
+        rank[:, :n_first] = 0
+        rank[:, max(0, held - n_last):] = 0
         for h in range(hk):
-            best = np.sort(np.argsort(-score[h], kind="stable")[:n_select])
+            best = np.sort(np.lexsort((np.where(rank[h] == 2, -score[h], 0.0), rank[h]))[:n_select])
             got[b, h, :len(best)] = best
     return got

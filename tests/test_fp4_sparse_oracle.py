@@ -108,6 +108,8 @@ def test_bounds_hold_and_the_largest_are_chosen():
         mid = score[h, 1:8]
         assert set(got[0, h]) - {0, 8, 9} == set(1 + np.argsort(-mid)[:2])
     assert paged.select_pages(q, bounds, pt, kl, psz, 12, 1, 2)[0, 0].tolist() == list(range(10)) + [-1, -1]
+    bounds[2:8, 1, 0, 5] = float("inf")                  # before the others, but for the first and the last
+    assert paged.select_pages(q, bounds, pt, kl, psz, 5, 1, 2)[0, 1].tolist() == [0, 2, 3, 8, 9]
 
 
 # ------------------------------------------------------- refusals before a launch
@@ -144,14 +146,16 @@ DECODE = [(1, dict(b=-1)), (1, dict(qlen=0)), (1, dict(hq=6)), (1, dict(hk=0)), 
 
 
 def test_fp4_decode_refusals(lib):
-    for want, kw in DECODE + [(1, dict(ks=INF)), (1, dict(vs=NAN)), (2, dict(mpps=1 << 25, ps=64))]:
+    for want, kw in DECODE + [(1, dict(ks=INF)), (1, dict(vs=NAN)), (2, dict(mpps=1 << 25, ps=64)),
+                              (2, dict(b=30000, mpps=1 << 20, ps=256, maxlen=1 << 28, splits=1))]:
         assert _fp4(lib, **kw) == want, kw
 
 
 @pytest.mark.parametrize("bits", [16, 8, 4])
 def test_sparse_refusals(lib, bits):
     more = [(1, dict(nsel=0)), (1, dict(nsel=-3)), (1, dict(sel=None)), (1, dict(sel=18)), (2, dict(nsel=1 << 26)),
-            (2, dict(mpps=1 << 25, ps=64))]
+            (2, dict(mpps=1 << 25, ps=64)),
+            (2, dict(b=30000, mpps=1 << 20, ps=256, maxlen=1 << 28, nsel=1 << 20, splits=1))]
     for want, kw in DECODE + more + ([(1, dict(ks=INF)), (1, dict(vs=NAN))] if bits != 16 else []):
         assert _sparse(lib, bits, **kw) == want, kw
 

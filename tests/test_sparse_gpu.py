@@ -98,7 +98,7 @@ class Case:
         assert fa.fa512_device_status() == 0
         ro, rl, weight = paged.decode_paged_any(self.q, self.k, self.v, self.table, self.lens, self.sel,
                                                 **SCALES[self.kind])
-        f16 = self.kind == "e2m1" or (self.kind == "e4m3" and self.rows <= 8)
+        f16 = self.kind != "bf16"
         tol = 2.0 ** -8 * np.abs(ro) + ((2.0 ** -10 if f16 else 2.0 ** -8) + 1e-3) * weight + 1e-6
         if f16:
             tol += 2.0 ** -24 * self.sel.shape[2] * self.psz * 6
@@ -223,6 +223,17 @@ def test_bounds_that_are_not_finite_come_first(fa):
     assert got.cpu()[0, 0].tolist() == [11, 33, 44, 59]
 
 
+def test_first_and_last_pages_come_before_those_that_are_not_finite(fa):
+    q, bounds, table, n = select_case([60 * 16], 1, 4, 2, 16, 65)
+    for i, p in enumerate((4, 9, 30, 31, 32, 50)):
+        bounds[int(table[0, p]), 1, i % 2, 3 * i] = float("nan") if i % 3 else float("-inf")
+    for pick in (3, 5, 7, 12):
+        got = fa.fa512_select_pages(q.cuda(), bounds.cuda(), table.cuda(), n.cuda(), page_size=16, n_select=pick, n_first=1,
+                                    n_last=2).cpu().numpy()
+        assert np.array_equal(got, paged.select_pages(q, bounds, table, n, 16, pick, 1, 2))
+        assert {0, 58, 59} <= set(got[0, 1].tolist())
+
+
 def test_select_records_what_lies_outside(fa):
     q, bounds, table, n = select_case([60 * 16, 30 * 16], 1, 2, 1, 16, 64)
     table[0, 5] = 1 << 25
@@ -255,6 +266,23 @@ def test_sparse_rows(fa, kind, q_len, hq, hk):
 @pytest.mark.parametrize("rows", [2, 12])
 def test_sparse_split_counts(fa, kind, splits, rows):
     Case([3000, 65, 0], 1, rows, 1, 16, 70, kind, 73).check(fa, num_splits=splits)
+
+
+@KINDS
+@pytest.mark.parametrize("splits", [0, 1, 6])
+@pytest.mark.parametrize("batch,hk", [(33, 3), (150, 2)])
+def test_many_ragged_lists(fa, kind, batch, hk, splits):
+    rng = np.random.RandomState(batch)
+    lens = np.where(rng.rand(batch) < 0.2, 0, rng.randint(1, 500, batch))
+    lens[-1] = 900
+    Case(lens.tolist(), 2, 4 * hk, hk, 16, 12, kind, 90).poisoned().check(fa, num_splits=splits)
+
+
+@KINDS
+@pytest.mark.parametrize("batch,pick", [(2, 16), (3, 16), (16, 20), (5, 30)])
+def test_full_lists_of_equal_length(fa, kind, batch, pick):
+    """Ranges that a number of groups for each sequence cuts evenly, and not."""
+    Case([600] * batch, 1, 8, 4, 16, pick, kind, 91).poisoned().check(fa)
 
 
 @KINDS
