@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // tensor scale (the nearest fp32 quotient) a group's scale is the E4M3 value
 // nearest to max |y| / 6, and a code the E2M1 value nearest to the fp32
 // quotient y / scale, ties to even; both saturate.  A group that holds NaN gets
-// the NaN scale; a scale that rounds to 0 makes the codes 0.
+// the NaN scale and codes 0; a scale that rounds to 0 makes the codes 0.
 //
 // A warp rounds one row of K and of V, a group of 16 elements a lane.  Bound: bytes (8
 // sequences of up to 4,096 new tokens, 4 heads: 335 MB in 55 us, 6.1 TB/s); the 18
@@ -173,8 +173,9 @@ __device__ __forceinline__ uint2 to_4bit(const uint4 a, const uint4 b, float ten
     float z[2][8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) z[i >> 3][i & 7] = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
-    if (nan) *scale_byte = 0x7f;
-    return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+    if (!nan) return make_uint2(e2m1x8(z[0]), e2m1x8(z[1]));
+    *scale_byte = 0x7f;
+    return make_uint2(0u, 0u);
 }
 
 // The same for a tensor scale whose reciprocal `by` is a power of two, without a
@@ -200,7 +201,7 @@ __device__ __forceinline__ uint2 to_4bit_pow2(const uint4 a, const uint4 b, floa
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // 0 < s: 2^-9 at least
     r *= by;
-    constexpr float SNAP = 3072.f;
+    constexpr float SNAP = 1.5f * 2048.f;
     float z[2][8];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

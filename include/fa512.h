@@ -504,8 +504,8 @@ fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_
  * group is the E4M3 value nearest to max |y| / 6 and a code the E2M1 value
  * nearest to the fp32 quotient y / scale; ties to even, beyond the largest value
  * the largest value.  A group whose scale rounds to 0 (max |y| up to 6 * 2^-10)
- * gets codes 0.  A group that holds a NaN gets the NaN scale: all its elements
- * read as NaN.  k_scale and v_scale are finite and above 0; a power of two is
+ * gets codes 0.  A group that holds a NaN gets the NaN scale and codes 0: all its
+ * elements read as NaN.  k_scale and v_scale are finite and above 0; a power of two is
  * faster, and the choice only matters for what lies outside the scales' range.
  * Other arguments and errors as fa512_cache_append.
  */
@@ -527,14 +527,20 @@ fa512_status fa512_cache_append_fp4(const void* k_new, const void* v_new, int64_
  *   k_scale, v_scale per-tensor scales, finite
  *   q, out, lse, positions and every other argument as fa512_decode_paged_q
  *              (q_len >= 1, q_len * G <= 16)
- *   num_splits 0 picks fa512_decode_auto_splits_fp4(); workspace must be at
- *              least fa512_decode_workspace_bytes_fp4() bytes, 256-byte aligned
+ *   num_splits most pieces that a sequence may be cut into, at most 1024 (the
+ *              SMs take equal ranges of the keys of all sequences; 1: whole
+ *              sequences); 0 picks fa512_decode_auto_splits_fp4(); workspace
+ *              must be at least fa512_decode_workspace_bytes_fp4() bytes,
+ *              256-byte aligned, not shared by calls that may run at the same time
  *
  * Codes and group scales are widened exactly, the queries (bf16) scaled by a
  * power of two per row and held in f16, sums are fp32; the softmax weights round
- * to f16.  Slots that no row sees may hold anything without reaching the output.
- * A row that sees a score of NaN or +infinity is NaN.  The same inputs give the
- * same bits every time.  batch * q_len is at most 65535.
+ * to f16.  Slots that no row sees may hold anything without reaching the output;
+ * a value that is not finite in a slot that one row of a KV head sees may reach
+ * the head's other rows.  A row that sees a score of NaN or +infinity is NaN.  The
+ * same inputs give the same bits every time.  batch * q_len is at most 65535, and
+ * so is n_kv_heads; num_pages * page_size and max_pages_per_seq * page_size are
+ * below 2^31 - 4096, batch * max_kv_len is at most 2^34.
  */
 fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const void* v_pages,
                                     const int32_t* page_table, const int32_t* kv_lens, void* out,
@@ -545,8 +551,8 @@ fa512_status fa512_decode_paged_fp4(const void* q, const void* k_pages, const vo
                                     void* workspace, size_t workspace_bytes,
                                     fa512_stream_t stream);
 
-/* Split count of fa512_decode_paged_fp4 when num_splits == 0; 1 when there is
- * nothing to split. */
+/* num_splits of fa512_decode_paged_fp4 when it is 0; 1 when there is nothing to
+ * split. */
 int fa512_decode_auto_splits_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads,
                                  int page_size, int max_kv_len);
 
@@ -636,10 +642,13 @@ size_t fa512_select_workspace_bytes(int batch, int n_kv_heads, int page_size, in
  * recorded in the error word; nothing is read out of bounds for them, but the
  * outputs of their (sequence, KV head) mean nothing.
  *
- * num_splits 0 picks fa512_decode_auto_splits_sparse(); workspace must be at
- * least fa512_decode_workspace_bytes_sparse() bytes, 256-byte aligned.
- * n_selected >= 1; n_selected * page_size and max_pages_per_seq * page_size are
- * below 2^31 - 256, batch * q_len is at most 65535.
+ * num_splits and workspace as fa512_decode_paged_fp4: 0 picks
+ * fa512_decode_auto_splits_sparse(), the workspace holds at least
+ * fa512_decode_workspace_bytes_sparse() bytes.  Slots that no row sees, and
+ * scores and values that are not finite, as there.
+ * n_selected >= 1; n_selected * page_size, num_pages * page_size and
+ * max_pages_per_seq * page_size are below 2^31 - 4096, batch * q_len and n_kv_heads
+ * at most 65535, batch times the positions of a list at most 2^34.
  */
 fa512_status fa512_decode_paged_sparse(const void* q, const void* k_pages, const void* v_pages,
                                        const int32_t* page_table, const int32_t* kv_lens,

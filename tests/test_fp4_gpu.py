@@ -144,6 +144,13 @@ def test_append_of_values_that_have_no_nearest(fa):
     assert np.isnan(got[0, 0, :16]).all() and np.array_equal(got, want, equal_nan=True)
     assert got[1, 0, 40] == 2688 and got[2, 0, 100] == -2688 and not got[3].any()
     assert np.array_equal(k.cpu().numpy(), v.cpu().numpy())
+    # the same bytes as the oracle's, also with scales that are no powers of two
+    for s in (1.0, 0.7):
+        fa.fa512_cache_append_fp4(x.cuda(), x.cuda(), k, v, i32([[0]]).cuda(), i32([4]).cuda(), k_scale=s, v_scale=s)
+        want = paged.fp4_rows(x, s)[0]
+        nan = (want[..., 256:] & 0x7f) == 0x7f           # their codes mean nothing, and are 0
+        want[..., :256] *= ~nan.repeat(8, -1)
+        assert np.array_equal(k.cpu().numpy()[0, :4], want)
 
 
 def test_append_skips_what_lies_outside(fa):
@@ -191,6 +198,45 @@ def test_long_and_empty_sequences(fa):
     c = Case([0, 20011, 0], 1, 8, 4, 64, 16)
     o, l = c.check(fa)
     assert not o[0].any() and np.isneginf(l[0]).all()
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("batch,hk", [(33, 3), (160, 4), (400, 1)])
+def test_many_ragged_sequences(fa, batch, hk, splits):
+    rng = np.random.RandomState(batch)
+    lens = np.where(rng.rand(batch) < 0.2, 0, rng.randint(1, 400, batch))
+    lens[batch // 2:batch // 2 + 35] = 0                 # more than a warp's worth without a tile
+    lens[-1] = 1500
+    c = Case(lens.tolist(), 1, 2 * hk, hk, 16, 17)
+    c.check(fa, num_splits=splits)
+    c.check(fa, num_splits=splits, max_kv_len=c.table.shape[1] * 16)     # a loose bound
+
+
+def test_more_kv_heads_than_ctas(fa):
+    Case([70, 5, 0], 1, 310, 310, 32, 18).check(fa)
+
+
+def test_sequences_that_share_their_pages(fa):
+    c = Case([500, 500, 500], 2, 8, 4, 32, 19, poison=False)
+    c.table[1] = c.table[0]
+    c.table[2, :7] = c.table[0, :7]
+    c.check(fa)
+
+
+def test_two_calls_at_once(fa):
+    cases = [Case([3000, 77], 1, 8, 4, 64, 20 + i) for i in range(2)]
+    want = [c.run(fa) for c in cases]
+    dev = [[x.cuda() for x in (c.q, c.k, c.v, c.table, c.lens)] for c in cases]
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(fa.fa512_decode_paged_fp4(*dev[i], k_scale=0.37, v_scale=1.3, max_kv_len=3000))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for o, l in got[i]:
+            assert np.array_equal(o.float().cpu().numpy(), want[i][0]) and np.array_equal(l.cpu().numpy(), want[i][1])
 
 
 def test_the_same_bits_every_time(fa):
