@@ -654,7 +654,9 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.max_pages_per_seq = max_pages_per_seq;
     p.len_cap = max_kv_len;
     p.window = window > 0 ? window : 0;
-    const long long tiles = band_tiles(max_kv_len, p.window);
+    // (the rows of several tokens see a band of window + q_len - 1 together)
+    const long long band = static_cast<long long>(p.window) + q_len - 1;
+    const long long tiles = band_tiles(max_kv_len, p.window > 0 && band < max_kv_len ? static_cast<int>(band) : 0);
     p.num_splits = splits;
     p.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
     if (p.tiles_per_split < 1) p.tiles_per_split = 1;
