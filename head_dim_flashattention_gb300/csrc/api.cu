@@ -653,7 +653,8 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.len_cap = max_kv_len;
-    p.window = window > 0 ? window : 0;
+    // (a window of max_kv_len leaves nothing out; one near 2^31 would pass int32 below)
+    p.window = window > 0 && window < max_kv_len ? window : 0;
     // (the rows of several tokens see a band of window + q_len - 1 together)
     const long long band = static_cast<long long>(p.window) + q_len - 1;
     const long long tiles = band_tiles(max_kv_len, p.window > 0 && band < max_kv_len ? static_cast<int>(band) : 0);
@@ -813,6 +814,7 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
     // most tiles of a sequence; with a window its rows see a band of window + q_len - 1
     const int tile = fa512::decode_ranges_tile(bits);
     long long most = (static_cast<long long>(positions) + tile - 1) / tile;
+    if (window < 0 || window >= max_kv_len) window = 0;   // leaves nothing out
     if (window > 0) {
         const long long band = (static_cast<long long>(window) + q_len - 1 + tile - 1) / tile + 1;
         if (band < most) most = band;
@@ -845,7 +847,7 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
     p.num_pages = num_pages;
     p.max_pages_per_seq = max_pages_per_seq;
     p.len_cap = max_kv_len;
-    p.window = window > 0 ? window : 0;
+    p.window = window;
     p.listed = sparse ? selected : nullptr;
     p.n_listed = n_selected;
     p.num_splits = splits;
