@@ -212,6 +212,11 @@ def test_many_ragged_sequences(fa, batch, hk, splits):
     c.check(fa, num_splits=splits, max_kv_len=c.table.shape[1] * 16)     # a loose bound
 
 
+@pytest.mark.parametrize("splits", [0, 33, 70, 1024])
+def test_many_rows_some_of_many_segments(fa, splits):
+    Case([8000] + [17] * 70 + [0], 1, 8, 4, 64, 23).check(fa, num_splits=splits)
+
+
 def test_more_kv_heads_than_ctas(fa):
     Case([70, 5, 0], 1, 310, 310, 32, 18).check(fa)
 
