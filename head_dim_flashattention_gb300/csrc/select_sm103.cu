@@ -364,22 +364,31 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
 
 // ------------------------------------------------------------------- choice
 //
-// A block per (sequence, KV head) finds the n-th largest key by its four bytes
-// from the top, a histogram of 256 each, then writes the pages above it, and the
-// lowest of those equal to it, in rising order.  The first SHARED keys wait in shared
-// memory, the rest is read again in each pass.  (A warp with 32 keys a lane in
-// registers, searching bit by bit, takes twice as long: its code runs once, and
-// fetching it is what that takes.)
+// A block per (sequence, KV head) finds the last key that is chosen by its digits, eight
+// bits at a time from the highest in which two keys differ, a histogram each, until all
+// of a digit's keys are chosen (two digits for a few hundred scores of about a size);
+// then each warp writes the chosen pages of its part of the sequence, in rising order.
+// What takes the time is the way from one step to the next: 64 sequences of up to 448
+// pages, 4 heads, take 5 us, four digits of all 32 bits took 8.  The first SHARED keys
+// wait in shared memory, the rest is read again for each digit.  (A warp with 32 keys a lane in registers, searching bit by bit,
+// takes twice as long: its code runs once, and fetching it is what that takes.)
 constexpr int CHOOSE_THREADS = 256;
 constexpr int CHOOSE_WARPS = CHOOSE_THREADS / 32;
 constexpr int SHARED = 4096;
+constexpr int DIGITS = 4;
 
 __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectParams p) {
     __shared__ uint32_t s_keys[SHARED];
-    __shared__ int hist[256], s_warp[2][CHOOSE_WARPS];
-    __shared__ int s_digit, s_left;
+    __shared__ __align__(16) int s_hist[DIGITS][256];
+    __shared__ uint32_t s_most[CHOOSE_WARPS], s_least[CHOOSE_WARPS];
+    __shared__ int s_above[CHOOSE_WARPS], s_equal[CHOOSE_WARPS];
+    __shared__ int s_digit, s_left, s_count;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // also where no scores were needed: for whatever ran before
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
+    // (the first keys are on their way before the length is known)
+    const uint32_t key0 = tid < p.max_pages ? keys[tid] : 0u;
+    const uint32_t key1 = tid + CHOOSE_THREADS < p.max_pages ? keys[tid + CHOOSE_THREADS] : 0u;
     const int len = length_of(p, b, false);
     const int held = static_cast<int>((static_cast<unsigned>(len) + p.page_size - 1) / p.page_size);
     int32_t* out = p.selected + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.n_select;
@@ -387,68 +396,111 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectPara
         for (int i = tid; i < p.n_select; i += CHOOSE_THREADS) out[i] = i < held ? i : -1;
         return;
     }
-    const uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
-    for (int i = tid; i < min(held, SHARED); i += CHOOSE_THREADS) s_keys[i] = keys[i];
-    // (a thread only reads the keys it wrote itself)
-    auto key_at = [&](int i) { return i < SHARED ? s_keys[i] : keys[i]; };
-    uint32_t prefix = 0;
-    int left = p.n_select;                           // to take among the keys that begin with the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < held; i += CHOOSE_THREADS) {
-            const uint32_t k = key_at(i);
-            if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        // how many lie above each digit: a scan from the top
-        const int mine = hist[255 - tid];
-        int sum = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+    for (int i = 0; i < DIGITS; ++i) s_hist[i][tid] = 0;
+    static_assert(CHOOSE_THREADS == 256, "a thread a digit");
+    // the largest and the smallest key but for the pages that are always chosen
+    uint32_t most = 0u, least = KEY_ALWAYS;
+    for (int i = tid; i < held; i += CHOOSE_THREADS) {
+        const uint32_t k = i == tid ? key0 : i == tid + CHOOSE_THREADS ? key1 : keys[i];
+        if (i < SHARED) s_keys[i] = k;
+        if (k != KEY_ALWAYS) {
+            most = max(most, k);
+            least = min(least, k);
         }
-        if (lane == 31) s_warp[0][warp] = sum;
-        __syncthreads();
-        int before = sum - mine;
-#pragma unroll
-        for (int w = 0; w < CHOOSE_WARPS; ++w) before += w < warp ? s_warp[0][w] : 0;
-        if (before < left && before + mine >= left) {
-            s_digit = 255 - tid;
-            s_left = left - before;
-        }
-        __syncthreads();
-        prefix = (prefix << 8) | static_cast<uint32_t>(s_digit);
-        left = s_left;
     }
-    int above = 0, equal = 0;                        // chosen before this run of pages: above the n-th key, equal to it
-    for (int i0 = 0; i0 < held; i0 += CHOOSE_THREADS) {
-        const int i = i0 + tid;
-        const uint32_t k = i < held ? key_at(i) : 0u;
-        const bool gt = i < held && k > prefix, eq = i < held && k == prefix;
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        __syncthreads();
-        if (lane == 0) {
-            s_warp[0][warp] = __popc(mg);
-            s_warp[1][warp] = __popc(me);
-        }
-        __syncthreads();
-        int g0 = above, e0 = equal;
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+        s_most[warp] = most;
+        s_least[warp] = least;
+    }
+    __syncthreads();
 #pragma unroll
-        for (int w = 0; w < CHOOSE_WARPS; ++w) {
-            const int a = s_warp[0][w], e = s_warp[1][w];
-            if (w < warp) {
-                g0 += a;
-                e0 += e;
+    for (int w = 0; w < CHOOSE_WARPS; ++w) {
+        most = max(most, s_most[w]);
+        least = min(least, s_least[w]);
+    }
+    auto key_at = [&](int i) { return i < SHARED ? s_keys[i] : keys[i]; };
+    // `left` to take among the keys whose bits from `shift` on are `prefix`, all of the larger ones
+    int left = p.n_select - p.n_first - p.n_last, shift = 0;
+    uint32_t prefix = KEY_ALWAYS;
+    if (left > 0) {
+        int known = 32 - __clz(most ^ least);            // the bits from here on are all keys'
+        prefix = known < 32 ? most >> known : 0u;
+        for (int d = 0;; ++d) {
+            shift = max(0, known - 8);
+            for (int i = tid; i < held; i += CHOOSE_THREADS) {
+                const uint32_t k = key_at(i);
+                if (k != KEY_ALWAYS && (known == 32 || k >> known == prefix)) atomicAdd(&s_hist[d][(k >> shift) & 255u], 1);
             }
-            above += a;
-            equal += e;
+            __syncthreads();
+            if (warp == 0) {                             // lane l: digits 255 - 8 l downwards
+                const int4* hist = reinterpret_cast<const int4*>(&s_hist[d][248 - 8 * lane]);
+                const int4 lo = hist[0], hi = hist[1];
+                const int n[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+                int sum = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += n[e];
+                int before = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += y;
+                }
+                before -= sum;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (before < left && before + n[e] >= left) {
+                        s_digit = 255 - 8 * lane - e;
+                        s_left = left - before;
+                        s_count = n[e];
+                    }
+                    before += n[e];
+                }
+            }
+            __syncthreads();
+            // (where the digit has bits that were known, they are the prefix's)
+            const int bits = known - shift;
+            prefix = (prefix << bits) | (static_cast<uint32_t>(s_digit) & ((1u << bits) - 1u));
+            left = s_left;
+            known = shift;
+            if (s_count == left || shift == 0) break;
         }
-        const unsigned lower = (1u << lane) - 1u;
-        g0 += __popc(mg & lower);
-        e0 += __popc(me & lower);
-        if (gt || (eq && e0 < left)) out[g0 + min(e0, left)] = i;
+    }
+    // a warp's part of the pages: counted, then written behind the parts before it
+    const int part = (held + CHOOSE_THREADS - 1) / CHOOSE_THREADS * 32, end = min(held, (warp + 1) * part);
+    auto look = [&](int i, bool* equal) {
+        const uint32_t k = i < end ? key_at(i) : 0u;
+        *equal = i < end && k != KEY_ALWAYS && k >> shift == prefix;
+        return i < end && (k == KEY_ALWAYS || k >> shift > prefix);
+    };
+    int above = 0, equal = 0;
+    for (int i = warp * part; i < end; i += 32) {
+        bool eq;
+        const bool gt = look(i + lane, &eq);
+        above += __popc(__ballot_sync(0xffffffffu, gt));
+        equal += __popc(__ballot_sync(0xffffffffu, eq));
+    }
+    if (lane == 0) {
+        s_above[warp] = above;
+        s_equal[warp] = equal;
+    }
+    __syncthreads();
+    above = equal = 0;
+#pragma unroll
+    for (int w = 0; w < CHOOSE_WARPS; ++w) {
+        above += w < warp ? s_above[w] : 0;
+        equal += w < warp ? s_equal[w] : 0;
+    }
+    for (int i = warp * part; i < end; i += 32) {
+        bool eq;
+        const bool gt = look(i + lane, &eq);
+        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq), lower = (1u << lane) - 1u;
+        const int g0 = above + __popc(mg & lower), e0 = equal + __popc(me & lower);
+        if (gt || (eq && e0 < left)) out[g0 + min(e0, left)] = i + lane;
+        above += __popc(mg);
+        equal += __popc(me);
     }
 }
 

@@ -223,6 +223,24 @@ def test_bounds_that_are_not_finite_come_first(fa):
     assert got.cpu()[0, 0].tolist() == [11, 33, 44, 59]
 
 
+@pytest.mark.parametrize("pages", [7, 300, 4500])
+def test_scores_that_differ_in_any_bit(fa, pages):
+    """Scores that are equal but for one of 32 bits or their sign, and only those always chosen."""
+    q, bounds, table, n = select_case([pages * 16], 1, 2, 1, 16, 66)
+    q[:] = 0
+    q[0, 0, :, 0] = 1.0
+    rng = np.random.RandomState(pages)
+    value = torch.tensor(np.exp2(rng.randint(-120, 120, pages)) * rng.choice([-1.0, 1.0, 1.0078125], pages),
+                         dtype=torch.float32).to(torch.bfloat16)
+    bounds[:] = 0
+    bounds[table[0, :pages].long(), 0, :, 0] = value[:, None]
+    for pick, first, last in ((1, 0, 0), (3, 1, 2), (5, 2, 1), (6, 0, 1), (pages - 1, 1, 1)):
+        got = fa.fa512_select_pages(q.cuda(), bounds.cuda(), table.cuda(), n.cuda(), page_size=16, n_select=pick,
+                                    n_first=first, n_last=last).cpu().numpy()
+        assert np.array_equal(got, paged.select_pages(q, bounds, table, n, 16, pick, first, last))
+    assert fa.fa512_device_status() == 0
+
+
 def test_first_and_last_pages_come_before_those_that_are_not_finite(fa):
     q, bounds, table, n = select_case([60 * 16], 1, 4, 2, 16, 65)
     for i, p in enumerate((4, 9, 30, 31, 32, 50)):
