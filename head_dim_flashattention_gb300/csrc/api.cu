@@ -726,12 +726,15 @@ struct RangesPlan {
 // its SM (1.6 us; alone it takes 0.6 of that), a tile for a CTA's start and end, 0.02
 // for each of a sequence's segments in the merge.  A batch with shorter sequences has
 // shorter ranges, so a batch of several may leave twice the segments.
-// Lists of pages are mostly full, their sequences `even`: where a number of groups for
-// each sequence divides its tiles and its ranges are no more than a quarter longer, no
-// range goes over two sequences and starts a second time (16 sequences, 200 pages of
-// 16, E4M3: 52 us with 76 ranges of 22 tiles, 47 with 64 of 25; 4 x 64 pages of 64,
-// bf16: 33 and 29; but 20 x 32 pages of 64, 4 bits: 28 with 72 of 9, 37 with 40 of 16).
-RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm, bool even) {
+// Lists of pages (list_bits: of a cached element; 0: no lists) are mostly full: where a
+// number of groups for each sequence divides its tiles and its ranges are no more than a
+// quarter longer, no range goes over two sequences and starts a second time (16
+// sequences, 200 pages of 16, E4M3: 50 us with 76 ranges of 22 tiles, 45 with 64 of 25;
+// 64 x 64 pages of 64: 178 and 166, in bf16 319 and 306; but 20 x 32 pages of 64, 4 bits:
+// 28 with 72 of 9, 37 with 40 of 16).  In 4 bits a CTA has more to compute for its bytes,
+// and fewer of them take longer unless the ranges are short (64 x 64 pages of 64: 115 us
+// with 76 ranges of 54, 123 with 64 of 64; 16 x 64: 40.5 with 76 of 14, 39 with 64 of 16).
+RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm, int list_bits) {
     RangesPlan best{1, 1};
     if (batch <= 0 || n_kv_heads <= 0) return best;
     double cost = 1e300;
@@ -741,9 +744,10 @@ RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_s
         const long long all = batch * (tiles > 1 ? tiles : 1), range = (all + groups - 1) / groups;
         const long long cut = (tiles + range - 1) / range;
         const double c = (per_sm == 1 ? 0.6 : 1.0) * static_cast<double>(range) + 1.0 + 0.02 * static_cast<double>(cut);
-        long long whole = even ? groups / batch : 0;
+        long long whole = list_bits ? groups / batch : 0, longer = range / 4;
+        if (list_bits == 4 && longer > 4) longer = 4;
         while (whole > 1 && tiles % whole != 0) --whole;
-        if (batch > 1 && whole >= 1 && tiles / whole <= range + range / 4) groups = batch * whole;
+        if (batch > 1 && whole >= 1 && tiles / whole <= range + longer) groups = batch * whole;
         if (c < cost) {
             cost = c;
             const long long used = (all + range - 1) / range, segments = (batch > 1 ? 2 : 1) * cut + 1;
@@ -757,7 +761,8 @@ RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_s
 // Most segments of a call over `positions` positions at most, by the bits of a cached element.
 int ranges_splits(int bits, int batch, int n_kv_heads, int positions, bool sparse) {
     const int tile = fa512::decode_ranges_tile(bits);
-    return plan_ranges(batch, n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile, sm_count(), sparse).segments;
+    return plan_ranges(batch, n_kv_heads, (static_cast<long long>(positions) + tile - 1) / tile, sm_count(), sparse ? bits : 0)
+        .segments;
 }
 
 // Body of the calls over a 4-bit cache and over selected pages.  bits of a cached
@@ -851,7 +856,7 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
     p.listed = sparse ? selected : nullptr;
     p.n_listed = n_selected;
     p.num_splits = splits;
-    p.groups = plan_ranges(batch, n_kv_heads, most, sm_count(), sparse).groups;
+    p.groups = plan_ranges(batch, n_kv_heads, most, sm_count(), sparse ? bits : 0).groups;
     // a sequence of n tiles touches (n - 1) / range + 2 ranges at most
     p.tiles_per_split = splits > 1 ? static_cast<int>((most - 1) / (splits - 1) + 1) : 1;
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -869,8 +874,8 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT32;
     const CUtensorMapSwizzle swizzle = bits == 4 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     // Selected pages are read a head at a time: what a load brings into L2 beside its rows
-    // is another head's (4 bits, 64 sequences, 64 of 448 pages: 133 us with 64-byte pieces,
-    // 144 with 128, 156 with 256); dense calls read all heads and do not differ.
+    // is another head's (4 bits, 64 sequences, 64 of 448 pages: 124 us with 64-byte pieces,
+    // 136 with 128, 149 with 256); dense calls read all heads and do not differ.
     const CUtensorMapL2promotion l2 = sparse ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     fa512_status st = encode_map(&tmk, type, swizzle, k_pages, 3, dims, strides, box, l2);
     if (st != FA512_OK) return st;

@@ -238,8 +238,8 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 
     // The launch's 80 registers a thread are dealt anew: a share for each role.  V^T in
     // bf16 and E4M3 needs fewer than in 4 bits, and its smaller tiles come from more
-    // pages, for which the loads take more (16 sequences, 200 pages of 16, E4M3: 57 us
-    // with 32, 51 with 40; 16 x 64 pages of 64, bf16: 95 and 90).
+    // pages, for which the loads take more (16 sequences, 200 pages of 16, E4M3: 51 us
+    // with 32, 46 with 40; one sequence, 64 pages of 64, bf16: 13.7 and 12.6).
     constexpr int K_REGS = NT == 1 ? 128 : 88, V_REGS = (NT == 1 ? 80 : 120) - (BITS == 4 ? 0 : 8),
                   LOAD_REGS = BITS == 4 ? 32 : 40;
     static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * 80, "no more than the launch has");

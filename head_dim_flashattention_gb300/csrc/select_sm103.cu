@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(bounds_threads(BITS)) bounds_kernel(const Boun
 constexpr int SCORE_WARPS = 4;
 constexpr int SCORE_PAGES = 2;
 constexpr int SCORE_STAGES = 6;                      // pages in the ring, a multiple of SCORE_PAGES
-constexpr int SCORE_BLOCKS = 12 * 152;               // blocks to spread the pages over (a third of them: 45 us instead of 42)
+// Blocks to spread the pages over (a third of them, or twice as many: 43 us a selection instead of 40).
+constexpr int SCORE_BLOCKS = 12 * 152;
 constexpr int PAGE_BYTES = 2 * D * 2;                // a page's bounds
 // shared memory: the warps' rings, then the query rows as fp32
 constexpr int score_smem(int rows) { return SCORE_WARPS * SCORE_STAGES * PAGE_BYTES + rows * D * 4; }
