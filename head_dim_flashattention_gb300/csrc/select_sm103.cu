@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(bounds_threads(BITS), BITS == 16 ? 2 : 6) boun
 // sum below rounds once.
 constexpr int SCORE_WARPS = 4;
 constexpr int SCORE_PAGES = 2;
-constexpr int SCORE_STAGES = 6;                      // pages in the ring, a multiple of SCORE_PAGES
+constexpr int SCORE_STAGES = 4;                      // pages in the ring, a multiple of SCORE_PAGES
 // Blocks to spread the pages over (a third of them, or twice as many: 43 us a selection instead of 40).
 constexpr int SCORE_BLOCKS = 12 * 152;
 constexpr int PAGE_BYTES = 2 * D * 2;                // a page's bounds
@@ -259,26 +259,27 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
     };
     // lane l keeps the pool pages of the 32 of this warp's pages from `batch` on
     int batch = 0, mine = page_of(lane);
-    auto load = [&](int i) {
+    const uint8_t* head = reinterpret_cast<const uint8_t*>(p.bounds) + static_cast<size_t>(h) * PAGE_BYTES + lane * 16;
+    const unsigned apart = static_cast<unsigned>(p.n_kv_heads) * PAGE_BYTES;   // from a page to the next
+    auto load = [&](int i, int stage) {
         if (i >= batch + 32) {
             batch += 32;
             mine = page_of(batch + lane);
         }
         const int page = __shfl_sync(0xffffffffu, mine, i & 31);
         if (page >= 0) {
-            const uint8_t* src = reinterpret_cast<const uint8_t*>(p.bounds) + (static_cast<size_t>(page) * p.n_kv_heads + h) * PAGE_BYTES;
-            const uint32_t dst = smem_u32(ring + (i % SCORE_STAGES) * PAGE_BYTES);
+            const uint8_t* src = head + static_cast<size_t>(static_cast<unsigned>(page)) * apart;
+            const uint32_t dst = smem_u32(ring + stage * PAGE_BYTES + lane * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (32 * j + lane) * 16),
-                             "l"(src + (32 * j + lane) * 16) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * j), "l"(src + 512 * j) : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return page;
     };
     int pages[SCORE_STAGES];                         // of the stages, the next one to be scored first
 #pragma unroll
-    for (int i = 0; i < SCORE_STAGES; ++i) pages[i] = load(i);
+    for (int i = 0; i < SCORE_STAGES; ++i) pages[i] = load(i, i);
 
     const int R = p.q_len * p.group;
     const int r0 = max(0, p.q_len - len) * p.group;  // rows of tokens before the sequence's first position see nothing
@@ -293,13 +294,14 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
     }
     __syncthreads();
     uint32_t* keys = p.keys + (static_cast<size_t>(b) * p.n_kv_heads + h) * p.max_pages;
-    for (int i = 0; number(i) < held; i += SCORE_PAGES) {
+    int at = 0;                                      // stage of page i
+    for (int i = 0; number(i) < held; i += SCORE_PAGES, at = at + SCORE_PAGES < SCORE_STAGES ? at + SCORE_PAGES : 0) {
         asm volatile("cp.async.wait_group %0;" ::"n"(SCORE_STAGES - SCORE_PAGES) : "memory");
         __syncwarp();
         float2 lo[SCORE_PAGES][8], hi[SCORE_PAGES][8];
 #pragma unroll
         for (int k = 0; k < SCORE_PAGES; ++k) {
-            const uint4* src = reinterpret_cast<const uint4*>(ring + ((i + k) % SCORE_STAGES) * PAGE_BYTES) + lane;
+            const uint4* src = reinterpret_cast<const uint4*>(ring + (at + k) * PAGE_BYTES) + lane;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float2 f[4];
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
 #pragma unroll
         for (int k = 0; k < SCORE_STAGES - SCORE_PAGES; ++k) pages[k] = pages[k + SCORE_PAGES];
 #pragma unroll
-        for (int k = 0; k < SCORE_PAGES; ++k) pages[SCORE_STAGES - SCORE_PAGES + k] = load(i + SCORE_STAGES + k);
+        for (int k = 0; k < SCORE_PAGES; ++k) pages[SCORE_STAGES - SCORE_PAGES + k] = load(i + SCORE_STAGES + k, at + k);
 
         // two rows at a time (the last one twice where their number is odd): lane l gets
         // the sum of row l / 8 % 2 and page l / 16
