@@ -42,7 +42,11 @@ constexpr int META = 16;                         // tiles and segments whose not
 template <int BITS, int NT>
 struct Smem {
     using F = Format<BITS>;
-    static constexpr int slots = NT == 1 ? 3 : 2;            // of K, and of V
+    // Slots of K, and of V.  Three where there is room, more loads in flight, are slower
+    // but for bf16 (4 bits, 64 x 28,672 positions: 654 us, with two 645; 64 lists of up to
+    // 64 pages of 64: 123 and 117; E4M3, 48 x 32 pages of 64, 2 heads: 49 and 45; 64 x 64
+    // pages of 64: E4M3 170 and 171, bf16 311 and 320).
+    static constexpr int slots = NT == 1 && BITS == 16 ? 3 : 2;
     // A K warp takes every turns-th tile.  K's `full` barriers go by tiles, not slots, so
     // that each is one warp's own, which then sees all of its phases: the first common
     // multiple of both counts.
