@@ -367,44 +367,47 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 else if constexpr (BITS == 8) scores_8<NT>(rows, 16 * block, lane, qb, s_q, sc);
                 else scores_16<NT>(rows, lane, qb, s_q, sc);
                 done_with(&k_empty[slot]);
-                // ---- softmax against this block's own maximum, rounded up to a whole number,
-                // less 7: weights up to 2^7 keep small ones, and those times a group scale
-                // (448 at most), in f16's range
+                // ---- softmax against this warp's reference, which rises where a weight would pass
+                // 2^7 (times a group scale, 448 at most, that stays in f16's range), to the block's
+                // maximum rounded up to a whole number, less 3: few blocks raise it
                 const int kp = base + ra;
                 uint2 frag[NT];
-                float ref[NT][2];
+                float sv[NT][2][2];
+                bool above = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float sv[2][2], cm[2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bool va = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp) < reach;
                         const bool vb = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp - 8) < reach;
-                        sv[i][0] = va ? sc[n][i] * rs[n][i] * p.scale_log2 : -INFINITY;
-                        sv[i][1] = vb ? sc[n][2 + i] * rs[n][i] * p.scale_log2 : -INFINITY;
-                        cm[i] = fmaxf(sv[i][0], sv[i][1]);
+                        sv[n][i][0] = va ? sc[n][i] * rs[n][i] * p.scale_log2 : -INFINITY;
+                        sv[n][i][1] = vb ? sc[n][2 + i] * rs[n][i] * p.scale_log2 : -INFINITY;
+                        above |= fmaxf(sv[n][i][0], sv[n][i][1]) > m[n][i] + 7.f;
                     }
+                if (__any_sync(0xffffffffu, above))
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) {
-                        const float x0 = __shfl_xor_sync(0xffffffffu, cm[0], off);
-                        const float x1 = __shfl_xor_sync(0xffffffffu, cm[1], off);
-                        cm[0] = fmaxf(cm[0], x0);
-                        cm[1] = fmaxf(cm[1], x1);
-                    }
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float most = fmaxf(sv[n][i][0], sv[n][i][1]);
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                            const float to = most > m[n][i] + 7.f ? ceilf(most) - 3.f : m[n][i];
+                            l[n][i] *= fast_exp2(m[n][i] - finite_ref(to));
+                            m[n][i] = to;
+                        }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
                     float pr[2][2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        ref[n][i] = ceilf(cm[i]) - 7.f;
-                        const float sh = finite_ref(ref[n][i]);
-                        pr[i][0] = fast_exp2(sv[i][0] - sh);
-                        pr[i][1] = fast_exp2(sv[i][1] - sh);
-                        // the sums keep the fp32 weights
-                        const float mn = fmaxf(m[n][i], ref[n][i]), to = finite_ref(mn);
-                        l[n][i] = l[n][i] * fast_exp2(m[n][i] - to) + (pr[i][0] + pr[i][1]) * fast_exp2(ref[n][i] - to);
-                        m[n][i] = mn;
+                        const float ref = finite_ref(m[n][i]);
+                        pr[i][0] = fast_exp2(sv[n][i][0] - ref);
+                        pr[i][1] = fast_exp2(sv[n][i][1] - ref);
+                        l[n][i] += pr[i][0] + pr[i][1];      // the sums keep the fp32 weights
                     }
-                    // P rounds to bf16 (2^-8 of a weight), or to f16: 2^-11 of it or 2^-32 of the
-                    // block's largest
+                    // P rounds to bf16 (2^-8 of a weight), or to f16: 2^-11 of it or 2^-25, where some
+                    // weight is above 4
                     if constexpr (NARROW) {
                         frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
                     } else {
@@ -425,7 +428,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     else
                         s_p[((buffer * BLOCKS + block) * NT + n) * 32 + lane] = frag[n];
                     if (g == 0 && (!NARROW || t == 0))
-                        *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(ref[n][0], ref[n][1]);
+                        *reinterpret_cast<float2*>(out_ref + row_of(n, 0)) = make_float2(m[n][0], m[n][1]);
                 }
                 done_with(&p_full[buffer]);
             }
@@ -474,12 +477,14 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 break;
             }
             const Segment seg = s_seg[segment % META];
-            // references of rows 2 t + i and g (NARROW: i and g % 2)
-            float m[NT][2], mg[NT];
+            // O's references are the largest of the K warps'; lane 8 w + r keeps K warp w's of row
+            // 8 n + r (NARROW: r), O's, and the factor from the one to the other
+            float ref[NT], top[NT], factor[NT];
             float o[NT][MTILES][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                m[n][0] = m[n][1] = mg[n] = -INFINITY;
+                ref[n] = top[n] = -INFINITY;
+                factor[n] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MTILES; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
             }
@@ -490,38 +495,33 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     ok = false;
                     break;
                 }
-                // ---- one reference for the tile
+                // ---- one reference for the tile; most change nothing
                 uint32_t pb[BLOCKS][NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float* all = s_ref + buffer * BLOCKS * 8 * NT + 8 * n;
-                    float mn[2] = {m[n][0], m[n][1]}, rg[BLOCKS];
-#pragma unroll
-                    for (int w = 0; w < BLOCKS; ++w) {
-                        const float2 x = *reinterpret_cast<const float2*>(all + w * 8 * NT + (NARROW ? 0 : 2 * t));
-                        rg[w] = NARROW ? (g & 1 ? x.y : x.x) : all[w * 8 * NT + g];
-                        mn[0] = fmaxf(mn[0], x.x);
-                        mn[1] = fmaxf(mn[1], x.y);
-                        mg[n] = fmaxf(mg[n], rg[w]);
-                    }
-                    float al[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        al[i] = fast_exp2(m[n][i] - finite_ref(mn[i]));
-                        m[n][i] = mn[i];
-                    }
-                    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+                    // K warp lane / 8 wrote this tile's block of its, in its turn
+                    const bool wrote = lane / 8 / BLOCKS == it % TURNS && (!NARROW || (lane & 7) < 2);
+                    const float now = wrote ? s_ref[(buffer * BLOCKS + lane / 8 % BLOCKS) * 8 * NT + 8 * n + (lane & 7)] : ref[n];
+                    if (__any_sync(0xffffffffu, now != ref[n])) {
+                        ref[n] = now;
+                        float to = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+                        to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
+                        const float al = fast_exp2(top[n] - finite_ref(to));
+                        top[n] = to;
+                        factor[n] = fast_exp2(now - finite_ref(to));
+                        const float al0 = __shfl_sync(0xffffffffu, al, NARROW ? 0 : 2 * t);
+                        const float al1 = __shfl_sync(0xffffffffu, al, NARROW ? 1 : 2 * t + 1);
 #pragma unroll
                         for (int i = 0; i < MTILES; ++i) {
-                            o[n][i][0] *= al[0];
-                            o[n][i][1] *= al[1];
-                            o[n][i][2] *= al[0];
-                            o[n][i][3] *= al[1];
+                            o[n][i][0] *= al0;
+                            o[n][i][1] *= al1;
+                            o[n][i][2] *= al0;
+                            o[n][i][3] *= al1;
                         }
                     }
 #pragma unroll
                     for (int w = 0; w < BLOCKS; ++w) {
-                        const float f = fast_exp2(rg[w] - finite_ref(mg[n]));
+                        const float f = __shfl_sync(0xffffffffu, factor[n], (it % TURNS * BLOCKS + w) * 8 + (NARROW ? g & 1 : g));
                         const uint32_t f2 = pack_p<BITS>(f, f);
                         const uint2 x = NARROW ? *reinterpret_cast<const uint2*>(s_p2 + (buffer * BLOCKS + w) * 32 + 16 * (g & 1) + 4 * t)
                                                : s_p[((buffer * BLOCKS + w) * NT + n) * 32 + lane];
