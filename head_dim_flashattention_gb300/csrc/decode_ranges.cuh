@@ -122,11 +122,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 constexpr uint32_t LOW_HALVES = 0x0f0f0f0fu;
 
 // 4 bits: S^T of a block of 16 positions, scales applied to the codes; Q fragments in
-// registers (NT = 1) or shared memory.  b0/b1 of k-step 4 j + s are a row's elements
+// shared memory.  b0/b1 of k-step 4 j + s are a row's elements
 // 64 j + 16 t + 4 s + {0, 1} / {2, 3}.
 template <int NT>
-__device__ __forceinline__ void scores_4(const uint8_t* block, int lane, const uint32_t (&qb)[NT == 1 ? KSTEPS : 1][2],
-                                       const uint2* s_q, float (&sc)[NT][4]) {
+__device__ __forceinline__ void scores_4(const uint8_t* block, int lane, const uint2* s_q, float (&sc)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     const uint8_t *a_row = block + Format<4>::order(g) * Format<4>::ROW, *b_row = a_row + 8 * Format<4>::ROW;
     const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
@@ -163,16 +162,8 @@ __device__ __forceinline__ void scores_4(const uint8_t* block, int lane, const u
                         const uint32_t a1 = mul_f16x2(hb[2 * s], fb), a3 = mul_f16x2(hb[2 * s + 1], fb);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            uint32_t b0, b1;
-                            if constexpr (NT == 1) {
-                                b0 = qb[k][0];
-                                b1 = qb[k][1];
-                            } else {
-                                const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
-                                b0 = q2.x;
-                                b1 = q2.y;
-                            }
-                            mma_f16(acc[n][k & 1], a0, a1, a2, a3, b0, b1);
+                            const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
+                            mma_f16(acc[n][k & 1], a0, a1, a2, a3, q2.x, q2.y);
                         }
                     }
                 }
@@ -187,8 +178,7 @@ __device__ __forceinline__ void scores_4(const uint8_t* block, int lane, const u
 
 // The same for up to 2 rows: column 2 c + r of Q^T holds row r's elements of the
 // groups 4 j + c, and zeros.  A lane's sums of step j are those of group 4 j + t.
-__device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, const uint32_t (&qb)[KSTEPS][2],
-                                              float (&sc)[4]) {
+__device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, const uint2* s_q, float (&sc)[4]) {
     const int g = lane >> 2, t = lane & 3;
     const uint8_t *a_row = block + Format<4>::order(g) * Format<4>::ROW, *b_row = a_row + 8 * Format<4>::ROW;
     const uint32_t pick = static_cast<uint32_t>(t) | (static_cast<uint32_t>(4 + t) << 4);
@@ -215,9 +205,10 @@ __device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, co
                     e2m1x8_f16(x ? ca.y : ca.x, ha);
                     e2m1x8_f16(x ? cb.y : cb.x, hb);
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        mma_f16(d, ha[2 * s], hb[2 * s], ha[2 * s + 1], hb[2 * s + 1], qb[4 * j + 2 * x + s][0],
-                                qb[4 * j + 2 * x + s][1]);
+                    for (int s = 0; s < 2; ++s) {
+                        const uint2 q2 = s_q[(4 * j + 2 * x + s) * 32 + lane];
+                        mma_f16(d, ha[2 * s], hb[2 * s], ha[2 * s + 1], hb[2 * s + 1], q2.x, q2.y);
+                    }
                 }
                 const float fa = f16_f32(h ? sa >> 16 : sa), fb = f16_f32(h ? sb >> 16 : sb);
                 sc[0] = fmaf(fa, d[0], sc[0]);
@@ -305,7 +296,7 @@ __device__ __forceinline__ void add_values_narrow(const uint8_t* block, int warp
 // E4M3: the same, from a slot of boxes of TILE rows; the operands' elements as in 4 bits.
 template <int NT>
 __device__ __forceinline__ void scores_8(const uint8_t* slot, int first, int lane,
-                                         const uint32_t (&qb)[NT == 1 ? KSTEPS : 1][2], const uint2* s_q, float (&sc)[NT][4]) {
+                                         const uint2* s_q, float (&sc)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     const int row = first + Format<8>::order(g);
     float acc[NT][2][4];                          // two chains of sums
@@ -325,9 +316,7 @@ __device__ __forceinline__ void scores_8(const uint8_t* slot, int first, int lan
             const uint32_t a1 = e4m3x2_f16(wb[s] & 0xffffu), a3 = e4m3x2_f16(wb[s] >> 16);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint2 q2;
-                if constexpr (NT == 1) q2 = make_uint2(qb[k][0], qb[k][1]);
-                else q2 = s_q[(n * KSTEPS + k) * 32 + lane];
+                const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
                 mma_f16(acc[n][k & 1], a0, a1, a2, a3, q2.x, q2.y);
             }
         }
@@ -368,8 +357,7 @@ __device__ __forceinline__ void add_values_8(const uint8_t* slot, int first, int
 
 // bf16: b0/b1 of k-step 2 j + s are a row's elements 32 j + 8 t + 4 s + {0, 1} / {2, 3}.
 template <int NT>
-__device__ __forceinline__ void scores_16(const uint8_t* slot, int lane, const uint32_t (&qb)[NT == 1 ? KSTEPS : 1][2],
-                                          const uint2* s_q, float (&sc)[NT][4]) {
+__device__ __forceinline__ void scores_16(const uint8_t* slot, int lane,                                           const uint2* s_q, float (&sc)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     const int row = Format<16>::order(g);
     float acc[NT][2][4];                          // two chains of sums
@@ -386,9 +374,7 @@ __device__ __forceinline__ void scores_16(const uint8_t* slot, int lane, const u
             const int k = 2 * j + s;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                uint2 q2;
-                if constexpr (NT == 1) q2 = make_uint2(qb[k][0], qb[k][1]);
-                else q2 = s_q[(n * KSTEPS + k) * 32 + lane];
+                const uint2 q2 = s_q[(n * KSTEPS + k) * 32 + lane];
                 mma_bf16_16816(acc[n][s], {s ? a.z : a.x, s ? b.z : b.x, s ? a.w : a.y, s ? b.w : b.y}, q2.x, q2.y);
             }
         }

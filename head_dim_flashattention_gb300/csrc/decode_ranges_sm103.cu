@@ -56,8 +56,8 @@ struct Smem {
     static constexpr int k = 0;
     static constexpr int v = slots * F::SLOT;
     static constexpr int p = 2 * slots * F::SLOT;            // [buffer][block][nt][lane] uint2
-    static constexpr int q = p + F::P_BUFFERS * F::BLOCKS * NT * 32 * 8;    // NT = 2: [nt][kstep][lane] uint2
-    static constexpr int ref = q + (NT == 2 ? NT * KSTEPS * 32 * 8 : 0);    // [buffer][block][8 NT] float
+    static constexpr int q = p + F::P_BUFFERS * F::BLOCKS * NT * 32 * 8;    // [nt][kstep][lane] uint2
+    static constexpr int ref = q + NT * KSTEPS * 32 * 8;    // [buffer][block][8 NT] float
     static constexpr int sums = ref + F::P_BUFFERS * F::BLOCKS * 8 * NT * 4;   // [parity][warp][8 NT] float2: reference, sum
     static constexpr int base = sums + 2 * WARPS * 8 * NT * 8;              // [META][BLOCKS] first position of 16
     static constexpr int seg = base + META * F::BLOCKS * 4;                 // [META] Segment
@@ -177,8 +177,7 @@ __device__ __forceinline__ Walk<BITS, LIST> first_of_range(const DecodeParams& p
     return w;
 }
 
-// ROWS: the most query rows (q_len * G) of a KV head.  Up to 8 rows' fragments stay
-// in registers; up to 16 rows' (NT = 2 n-tiles) are read from shared memory.
+// ROWS: the most query rows (q_len * G) of a KV head, in NT n-tiles of 8.
 //
 // Up to 2 rows leave six of the eight columns of an n-tile free, and the group
 // scales move there (NARROW): column 2 c + r belongs to row r and scale class c.
@@ -240,24 +239,24 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     bool ok = true;                              // the same in all lanes of a warp
     int loaded = 0;                              // tiles whose load this warp has issued
 
-    // The launch's 80 registers a thread are dealt anew: a share for each role.  V^T in
-    // bf16 and E4M3 needs fewer than in 4 bits, and its smaller tiles come from more
-    // pages, for which the loads take more (16 sequences, 200 pages of 16, E4M3: 51 us
-    // with 32, 46 with 40; one sequence, 64 pages of 64, bf16: 13.7 and 12.6).
-    constexpr int K_REGS = NT == 1 ? 128 : 88, V_REGS = (NT == 1 ? 80 : 120) - (BITS == 4 ? 0 : 8),
-                  LOAD_REGS = BITS == 4 ? 32 : 40;
-    static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * 80, "no more than the launch has");
+    // The launch's 80 registers a thread are dealt anew: a share for each role, the K
+    // group's and the V group's no less than 80, the loads' no more, as the instructions
+    // that take and give them ask.  (64 x 28,672 positions in 4 bits, K, V and loads: 128,
+    // 80, 32 with Q in registers 641 us; with Q in shared memory 104, 96, 40 630; 88, 104,
+    // 48 623; 88, 88, 64 630.)
+    constexpr int LAUNCH_REGS = 80, K_REGS = 88, V_REGS = 104, LOAD_REGS = 48;
+    static_assert(K_REGS + V_REGS + LOAD_REGS <= 3 * LAUNCH_REGS, "no more than the launch has");
+    static_assert(K_REGS >= LAUNCH_REGS && V_REGS >= LAUNCH_REGS && LOAD_REGS <= LAUNCH_REGS, "taken, taken, given");
     if (role == 0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K_REGS));
         // ---- Q^T fragments, bf16 as stored, else in f16 after a power-of-two scale per row
         // that keeps its largest element below 2^15 (exact for elements down to 2^-39 of
         // that; a score is unscaled before the softmax)
-        uint32_t qb[NT == 1 ? KSTEPS : 1][2];
         float rs[NT][2];                          // 1 / scale of rows row_of(n, 0), row_of(n, 1)
         auto load_q = [&](int b) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                // NT = 2: each warp holds a quarter of the k-steps, all of them the maxima
+                // each warp writes a quarter of the k-steps, all of them find the maxima
                 const int r = NARROW ? g & 1 : 8 * n + g;
                 const bool row_ok = r < R;
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + row_index(b, row_ok ? r : 0) * D);
@@ -271,12 +270,6 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-                        if constexpr (NT == 1) {
-                            qb[4 * j + 2 * e][0] = a.x;
-                            qb[4 * j + 2 * e][1] = a.y;
-                            qb[4 * j + 2 * e + 1][0] = a.z;
-                            qb[4 * j + 2 * e + 1][1] = a.w;
-                        }
                     }
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
@@ -289,23 +282,15 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     if constexpr (BITS == 16) return w;
                     else return pack_f16x2(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
                 };
-                if constexpr (NT == 1) {
+                const bool mine = row_ok && (!NARROW || g >> 1 == t);
 #pragma unroll
-                    for (int k = 0; k < KSTEPS; ++k) {
-                        const bool mine = !NARROW || g >> 1 == t;
-                        qb[k][0] = mine ? to_f16(qb[k][0]) : 0u;
-                        qb[k][1] = mine ? to_f16(qb[k][1]) : 0u;
+                for (int j = 2 * warp; j < 2 * warp + 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint4 a = mine ? src[BITS == 16 ? 8 * j + 4 * e + t : 8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
+                        s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
+                        s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
                     }
-                } else {
-#pragma unroll
-                    for (int j = 2 * warp; j < 2 * warp + 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint4 a = row_ok ? src[BITS == 16 ? 8 * j + 4 * e + t : 8 * j + 2 * t + e] : make_uint4(0u, 0u, 0u, 0u);
-                            s_q[(n * KSTEPS + 4 * j + 2 * e) * 32 + lane] = make_uint2(to_f16(a.x), to_f16(a.y));
-                            s_q[(n * KSTEPS + 4 * j + 2 * e + 1) * 32 + lane] = make_uint2(to_f16(a.z), to_f16(a.w));
-                        }
-                }
                 rs[n][0] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 0 : 4 * (2 * t));
                 rs[n][1] = 1.f / __shfl_sync(0xffffffffu, scale, NARROW ? 4 : 4 * (2 * t + 1));
             }
@@ -327,14 +312,14 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         int range;
         const int first_b = first_of_range<BITS, LIST>(p, index, gridDim.x / p.n_kv_heads, &range).b;
         load_q(first_b);                          // (of sequence 0 where the range is empty)
-        __syncthreads();                          // barriers, the first tiles' notes, NT = 2: the queries
+        __syncthreads();                          // barriers, the first tiles' notes, the queries
         const int total = *s_total;
 
         int it = 0;                               // tiles of the range gone through
         for (int segment = 0; it < total && ok; ++segment) {
             if (segment > 0) {
                 load_q(s_seg[segment % META].b);
-                if constexpr (NT == 2) k_warps();
+                k_warps();
             }
             const Segment seg = s_seg[segment % META];
             // positions of the rows (-1: padding row, sees nothing); a row sees the keys
@@ -362,10 +347,10 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 // (an unloaded block's rows are stale: its scores are masked)
                 float sc[NT][4];
                 const uint8_t* rows = smem + Smem::k + slot * F::SLOT;
-                if constexpr (NARROW) scores_narrow(rows + 16 * block * F::ROW, lane, qb, sc[0]);
-                else if constexpr (BITS == 4) scores_4<NT>(rows + 16 * block * F::ROW, lane, qb, s_q, sc);
-                else if constexpr (BITS == 8) scores_8<NT>(rows, 16 * block, lane, qb, s_q, sc);
-                else scores_16<NT>(rows, lane, qb, s_q, sc);
+                if constexpr (NARROW) scores_narrow(rows + 16 * block * F::ROW, lane, s_q, sc[0]);
+                else if constexpr (BITS == 4) scores_4<NT>(rows + 16 * block * F::ROW, lane, s_q, sc);
+                else if constexpr (BITS == 8) scores_8<NT>(rows, 16 * block, lane, s_q, sc);
+                else scores_16<NT>(rows, lane, s_q, sc);
                 done_with(&k_empty[slot]);
                 // ---- softmax against this warp's reference, which rises where a weight would pass
                 // 2^7 (times a group scale, 448 at most, that stays in f16's range), to the block's
@@ -464,8 +449,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             }
         }
     } else if (role == 1) {
-        if constexpr (V_REGS < 80) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(V_REGS));
-        else if constexpr (V_REGS > 80) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(V_REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(V_REGS));
         __syncthreads();                          // barriers, the first tiles' notes
         const int total = *s_total;
 
