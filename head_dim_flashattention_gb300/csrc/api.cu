@@ -729,11 +729,12 @@ struct RangesPlan {
 // Lists of pages (list_bits: of a cached element; 0: no lists) are mostly full: where a
 // number of groups for each sequence divides its tiles and its ranges are no more than a
 // quarter longer, no range goes over two sequences and starts a second time (16
-// sequences, 200 pages of 16, E4M3: 50 us with 76 ranges of 22 tiles, 45 with 64 of 25;
-// 64 x 64 pages of 64: 178 and 166, in bf16 319 and 306; but 20 x 32 pages of 64, 4 bits:
-// 28 with 72 of 9, 37 with 40 of 16).  In 4 bits a CTA has more to compute for its bytes,
-// and fewer of them take longer unless the ranges are short (64 x 64 pages of 64: 115 us
-// with 76 ranges of 54, 123 with 64 of 64; 16 x 64: 40.5 with 76 of 14, 39 with 64 of 16).
+// sequences, 200 pages of 16, E4M3: 45.1 us with 76 ranges of 22 tiles, 43.6 with 64 of
+// 25; in bf16 77 and 71; 64 x 64 pages of 64, bf16: 317 and 307; but 20 x 32 pages of 64,
+// 4 bits: 26 with 72 of 9, 35 with 40 of 16).  Over coded caches a CTA has more to compute
+// for its bytes, and fewer of them take longer where ranges are long (64 x 64 pages of
+// 64, E4M3: 163 us with 76 ranges of 108, 166 with 64 of 128; 4 bits: 107 with 76 of 54,
+// 115 with 64 of 64).
 RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm, int list_bits) {
     RangesPlan best{1, 1};
     if (batch <= 0 || n_kv_heads <= 0) return best;
@@ -745,7 +746,7 @@ RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_s
         const long long cut = (tiles + range - 1) / range;
         const double c = (per_sm == 1 ? 0.6 : 1.0) * static_cast<double>(range) + 1.0 + 0.02 * static_cast<double>(cut);
         long long whole = list_bits ? groups / batch : 0, longer = range / 4;
-        if (list_bits == 4 && longer > 4) longer = 4;
+        if (list_bits != 16 && longer > 4) longer = 4;
         while (whole > 1 && tiles % whole != 0) --whole;
         if (batch > 1 && whole >= 1 && tiles / whole <= range + longer) groups = batch * whole;
         if (c < cost) {
@@ -874,8 +875,8 @@ fa512_status ranges_call(const void* q, const void* k_pages, const void* v_pages
                                                  : CU_TENSOR_MAP_DATA_TYPE_UINT32;
     const CUtensorMapSwizzle swizzle = bits == 4 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     // Selected pages are read a head at a time: what a load brings into L2 beside its rows
-    // is another head's (4 bits, 64 sequences, 64 of 448 pages: 124 us with 64-byte pieces,
-    // 136 with 128, 149 with 256); dense calls read all heads and do not differ.
+    // is another head's (4 bits, 64 sequences, 64 of 448 pages: 109 us with 64-byte pieces,
+    // 125 with 128, 141 with 256); dense calls read all heads and do not differ.
     const CUtensorMapL2promotion l2 = sparse ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     fa512_status st = encode_map(&tmk, type, swizzle, k_pages, 3, dims, strides, box, l2);
     if (st != FA512_OK) return st;

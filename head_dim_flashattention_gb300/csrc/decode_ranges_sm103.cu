@@ -17,9 +17,10 @@
 // and the groups only meet at barriers in shared memory with tiles of slack, so that
 // both products of different tiles overlap.  (64 sequences of 28,672 positions in 4
 // bits: one group of warps that did both in turn 846 us, two groups 775, the group
-// scales in free columns for 2 rows 707, loads on warps of their own 649: 6.5 TB/s.)
-// References are whole numbers in log2 units: what brings two of them together is a
-// power of two, exact in f16 and bf16.
+// scales in free columns for 2 rows 707, loads on warps of their own 649, references
+// that seldom change 641, Q in shared memory and registers where they are needed 622:
+// 6.8 TB/s.)  References are whole numbers in log2 units: what brings two of them
+// together is a power of two, exact in f16 and bf16.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,10 +43,10 @@ constexpr int META = 16;                         // tiles and segments whose not
 template <int BITS, int NT>
 struct Smem {
     using F = Format<BITS>;
-    // Slots of K, and of V.  Three where there is room, more loads in flight, are slower
-    // but for bf16 (4 bits, 64 x 28,672 positions: 654 us, with two 645; 64 lists of up to
-    // 64 pages of 64: 123 and 117; E4M3, 48 x 32 pages of 64, 2 heads: 49 and 45; 64 x 64
-    // pages of 64: E4M3 170 and 171, bf16 311 and 320).
+    // Slots of K, and of V.  Three, more loads in flight, are slower but for bf16 (E4M3, 48
+    // sequences, 32 pages of 64, 2 heads: 45.9 us, with two 43.6; 64 x 64 pages of 64: E4M3
+    // 165 and 166, bf16 307 and 310).  In 4 bits they took 654 us instead of 645 for 64 x
+    // 28,672 positions when Q still left room for them.
     static constexpr int slots = NT == 1 && BITS == 16 ? 3 : 2;
     // A K warp takes every turns-th tile.  K's `full` barriers go by tiles, not slots, so
     // that each is one warp's own, which then sees all of its phases: the first common
@@ -721,8 +722,9 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
 // nothing waits but for memory, and only segments with keys are read.  For many rows;
 // few rows of many segments go faster where several groups of threads share a row's
 // segments, in the merge of the other decode calls.  (300 sequences of up to 300
-// positions, 8 heads: 52 us, with that merge 62; 64 x 8,192, 32 heads 214 and 222; but
-// 16 x 16,384, 16 heads, up to 39 segments a row 54 and 52.)
+// positions, 8 heads: 47 us, with that merge 58; 64 x 8,192, 32 heads 198 and 207; but
+// 16 x 16,384, 16 heads, up to 39 segments a row 51.4 and 50.1, 1 x 4,096, 8 heads 11.4
+// and 9.1.)
 constexpr int MERGE_AHEAD = 4;                       // segments whose O is read at a time, the first ones before the weights
 __global__ void __launch_bounds__(128) merge_segments_kernel(const DecodeParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
