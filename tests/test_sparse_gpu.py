@@ -353,6 +353,37 @@ def test_sparse_nan_scores(fa, kind, rows):
 
 
 @KINDS
+@pytest.mark.parametrize("rows", [2, 8, 12])
+@pytest.mark.parametrize("shape", ["rising", "falling", "one above many", "one below many", "steps", "far below", "late"])
+def test_scores_that_rise_and_fall(fa, kind, rows, shape):
+    """The softmax's references rise with the scores, and only now and then: scores set by one channel."""
+    n, hk, psz = 3000, 2, 64
+    j, rng = np.arange(n), np.random.RandomState(7)
+    score = {"rising": 0.02 * j, "falling": 60 - 0.02 * j, "one above many": np.where(j == 5, 0.0, -10.5),
+             "one below many": np.where(j == 5, -30.0, 1.0), "steps": rng.randint(-4, 5, n) * 2.0 + 6.0 * (j // 500),
+             "far below": -300.0 + 0.01 * j, "late": np.where(j < 2900, -20.0, 0.0)}[shape]
+    c = Case([n, 700], rows // 2, 2 * hk, hk, psz, 47, kind, 95)
+    c.q[:] = 0
+    c.q[..., 0] = 1.0
+    x = torch.zeros(*c.k.shape[:3], D)
+    for b, m in enumerate((n, 700)):
+        x[c.table[b].long()[j[:m] // psz], j[:m] % psz, :, 0] = torch.tensor(score[:m], dtype=torch.float32)[:, None]
+    x = x.to(torch.bfloat16)
+    c.k = x if kind == "bf16" else torch.from_numpy(paged.fp4_rows(x, 0.37)) if kind == "e2m1" else (
+        (x.float() / 0.0371 / 32).to(torch.float8_e4m3fn).view(torch.uint8))
+    scale = 1.0 if kind != "e4m3" else 32.0
+    o, l = c.run(fa, scale=scale)
+    assert fa.fa512_device_status() == 0
+    ro, rl, weight = paged.decode_paged_any(c.q, c.k, c.v, c.table, c.lens, c.sel, scale=scale, **SCALES[kind])
+    # as in Case.check; f16 weights below its normal range are off by 2^-25 where the largest is above 1
+    tol = 2.0 ** -8 * np.abs(ro) + ((2.0 ** -8 if kind == "bf16" else 2.0 ** -10) + 1e-3) * weight + 1e-6
+    if kind != "bf16":
+        tol += 2.0 ** -24 * n * 6
+    assert np.all(np.isfinite(o)) and np.max(np.abs(o - ro) - tol) <= 0
+    assert np.max(np.abs(l - rl)) <= 1e-3
+
+
+@KINDS
 def test_sparse_repeats_bitwise(fa, kind):
     c = Case([3000, 700, 64], 1, 8, 4, 64, 9, kind, 78)
     a = c.run(fa)
