@@ -218,22 +218,26 @@ __device__ __forceinline__ void unpack8(const uint4 x, float2 (&f)[4]) {
     for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-// Sums over the lanes of four values at once, each by halves (lanes 16 apart, then 8,
-// ...): lane l gets value l / 8's.
-__device__ __forceinline__ float sum_of_four(const float (&v)[4], int lane) {
-    float x[2];
+// Sums over the lanes of N values at once, each by halves (lanes 16 apart, then 8, ...):
+// lane l gets value l / (32 / N)'s.
+template <int N>
+__device__ __forceinline__ float sum_of(float (&v)[N], int lane) {
+    int off = 16;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {                    // values i and i + 2
-        const float other = __shfl_xor_sync(0xffffffffu, lane & 16 ? v[i] : v[i + 2], 16);
-        x[i] = (lane & 16 ? v[i + 2] : v[i]) + other;
-    }
-    const float other = __shfl_xor_sync(0xffffffffu, lane & 8 ? x[0] : x[1], 8);
-    float y = (lane & 8 ? x[1] : x[0]) + other;
+    for (int n = N / 2; n >= 1; n >>= 1, off >>= 1)
 #pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-    return y;
+        for (int i = 0; i < n; ++i) {                // values i and i + n
+            const float other = __shfl_xor_sync(0xffffffffu, lane & off ? v[i] : v[i + n], off);
+            v[i] = (lane & off ? v[i + n] : v[i]) + other;
+        }
+#pragma unroll
+    for (; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    return v[0];
 }
 
+// ROWS: query rows at a time, 2 for up to 2 rows (64 sequences of up to 448 pages, 4 heads:
+// 38 us a selection, with 4 at a time 46), else 4 (8 rows: 69, with 2 72).
+template <int ROWS>
 __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) uint8_t score_raw[];
@@ -322,14 +326,14 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
 #pragma unroll
         for (int k = 0; k < SCORE_PAGES; ++k) pages[SCORE_STAGES - SCORE_PAGES + k] = load(i + SCORE_STAGES + k, at + k);
 
-        // two rows at a time (the last one twice where their number is odd): lane l gets
-        // the sum of row l / 8 % 2 and page l / 16
+        // ROWS rows at a time (the last one again where they run out): lane l gets the sum of
+        // row l / (16 / ROWS) % ROWS of them and page l / 16
         float best = -INFINITY;
         bool nan = false;
-        for (int r = r0; r < R; r += 2) {
-            float v[4];
+        for (int r = r0; r < R; r += ROWS) {
+            float v[SCORE_PAGES * ROWS];
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {
+            for (int e2 = 0; e2 < ROWS; ++e2) {
                 const float4* q = s_q + min(r + e2, R - 1) * 128 + lane;
                 float2 x[SCORE_PAGES][4];
 #pragma unroll
@@ -350,15 +354,18 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
                 for (int k = 0; k < SCORE_PAGES; ++k) {
                     // the eight of this lane: 0 + 4, 1 + 5, ..., then halves of those
                     const float2 d = fadd2(fadd2(x[k][0], x[k][2]), fadd2(x[k][1], x[k][3]));
-                    v[2 * k + e2] = d.x + d.y;
+                    v[ROWS * k + e2] = d.x + d.y;
                 }
             }
-            const float s = sum_of_four(v, lane);
+            const float s = sum_of(v, lane);
             nan |= s != s;
             best = fmaxf(best, s);
         }
-        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 8));
-        nan |= __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, 8) != 0;
+#pragma unroll
+        for (int off = 8; off >= 16 / ROWS; off >>= 1) {
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, off));
+            nan |= __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, off) != 0;
+        }
         const int k = lane >> 4, lp = number(i + k);
         if ((lane & 15) == 0 && lp < held) {
             const int page = k ? now[1] : now[0];
@@ -532,9 +539,10 @@ cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
         const long long items = static_cast<long long>(p.n_kv_heads) * p.batch, want = (SCORE_BLOCKS + items - 1) / items;
         const dim3 grid(static_cast<unsigned>(want < rounds ? want : rounds), p.n_kv_heads, p.batch);
         const int smem = score_smem(p.q_len * p.group);
-        const cudaError_t set = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score_smem(16));
+        auto kernel = p.q_len * p.group <= 2 ? score_kernel<2> : score_kernel<4>;
+        const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, score_smem(16));
         if (set != cudaSuccess) return set;
-        score_kernel<<<grid, SCORE_WARPS * 32, smem, stream>>>(p);
+        kernel<<<grid, SCORE_WARPS * 32, smem, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
