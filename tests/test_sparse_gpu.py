@@ -4,9 +4,7 @@ together, on a side stream and in a captured graph.
 
 Tolerance of an output element, A = sum p |v| / sum p (fp64): 2^-8 |O| (bf16), the
 weights' rounding 2^-8 A (bf16 cache) or 2^-10 A (coded caches, f16) with 2^-24 n
-vmax for f16 weights below its normal range, 1e-3 A for the fp32 scores (an FP8
-cache keeps its row's maxima in bf16, which moves no weight), plus 1e-6.  From 9
-rows a KV head on an E4M3 cache is read as bf16 tiles, its weights as bf16.
+vmax for f16 weights below its normal range, 1e-3 A for the fp32 scores, plus 1e-6.
 """
 import numpy as np
 import pytest
