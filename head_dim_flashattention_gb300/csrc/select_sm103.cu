@@ -32,11 +32,12 @@ constexpr int D = 512;
 // A block takes one touched page of one KV head; a thread 8 elements of a row (16
 // of a coded one, in 4 bits those of one scale), the rows dealt to 4 groups of
 // threads, 16 of them in flight, whose results meet in shared memory.  NaN elements
-// make both bounds NaN.  What it takes is the two look-ups before a block's first row
-// and, in 4 bits, the arithmetic (24 conversions and comparisons for 16 elements): 8
-// sequences of up to 4,096 new tokens, 4 heads, 4 bits: 37 MB in 10.6 us (four blocks
-// an SM instead of six: 11.0; with 64-bit products of row and stride 12.5), one token
-// of 16 sequences, bf16, 2.3 us.
+// make both bounds NaN.  The blocks of a page's heads, whose rows lie side by side, come
+// one after another.  What it takes is the two look-ups before a block's first row and,
+// in 4 bits, the arithmetic (24 conversions and comparisons for 16 elements): 8 sequences
+// of up to 4,096 new tokens, 4 heads, 4 bits: 37 MB in 13.0 us from memory (six blocks an
+// SM instead of eight: 13.9, five 14.2; E4M3 15.2 with seven, 15.9 with six, 15.7 with
+// eight); one token of 16 sequences, bf16, 2.3 us.
 __host__ __device__ constexpr int bounds_threads(int bits) { return bits == 16 ? 256 : 128; }
 
 struct MinMax {
@@ -62,22 +63,22 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(bounds_threads(BITS), BITS == 16 ? 2 : 6) bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(bounds_threads(BITS), BITS == 16 ? 2 : BITS == 8 ? 7 : 8) bounds_kernel(const BoundsParams p) {
     constexpr int ROW = BITS == 16 ? 2 * D : BITS == 8 ? D : kFp4RowBytes;
     constexpr int PAIRS = BITS == 16 ? 4 : 8;       // x 2 elements of a thread
     constexpr int LANES = D / (2 * PAIRS);          // threads of a row: 64, 32
     constexpr int GROUPS = bounds_threads(BITS) / LANES;
     constexpr bool F16 = BITS != 16;
     __shared__ uint32_t s_lo[GROUPS - 1][D / 2], s_hi[GROUPS - 1][D / 2];
-    const int b = blockIdx.z, h = blockIdx.y;
+    const int b = blockIdx.y, h = blockIdx.x % p.n_kv_heads, nth = blockIdx.x / p.n_kv_heads;   // nth touched page
     const int len = p.kv_lens[b];
     const int n_new = p.q_lens ? p.q_lens[b] : p.q_len;
     if (n_new < 0 || n_new > p.q_len || len < n_new ||
         len > static_cast<long long>(p.max_pages_per_seq) * p.page_size) {
-        if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
+        if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
         return;
     }
-    const int lp = (len - n_new) / p.page_size + blockIdx.x;
+    const int lp = (len - n_new) / p.page_size + nth;
     if (n_new == 0 || lp > (len - 1) / p.page_size) return;
     const int page = p.page_table[static_cast<size_t>(b) * p.max_pages_per_seq + lp];
     if (page < 0 || page >= p.num_pages) {
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_kernel(const SelectPara
 cudaError_t launch_page_bounds(const BoundsParams& p, int element_bits, cudaStream_t stream) {
     using namespace select;
     const int touched = min((p.q_len - 1) / p.page_size + ((p.q_len - 1) % p.page_size != 0) + 1, p.max_pages_per_seq);
-    const dim3 grid(touched, p.n_kv_heads, p.batch);
+    const dim3 grid(static_cast<unsigned>(touched) * static_cast<unsigned>(p.n_kv_heads), p.batch);
     if (element_bits == 16) bounds_kernel<16><<<grid, bounds_threads(16), 0, stream>>>(p);
     else if (element_bits == 8) bounds_kernel<8><<<grid, bounds_threads(8), 0, stream>>>(p);
     else bounds_kernel<4><<<grid, bounds_threads(4), 0, stream>>>(p);
