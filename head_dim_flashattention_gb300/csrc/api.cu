@@ -1414,7 +1414,11 @@ fa512_status fa512_cache_page_bounds(const void* k_pages, const int32_t* page_ta
         return fail(FA512_ERR_INVALID_ARG, "num_pages and max_pages_per_seq must be >= 1");
     if (static_cast<long long>(max_pages_per_seq) * page_size > 0x7fffffffLL)
         return fail(FA512_ERR_UNSUPPORTED, "page table too large for int32 positions");
-    if (batch > 65535 || n_kv_heads > 65535) return fail(FA512_ERR_UNSUPPORTED, "grid too large");
+    // (at most this many touched pages of a sequence, a block for each of their heads)
+    const long long touched = static_cast<long long>(q_len) / page_size + 2 < max_pages_per_seq
+                                  ? static_cast<long long>(q_len) / page_size + 2 : max_pages_per_seq;
+    if (batch > 65535 || n_kv_heads > 65535 || touched * n_kv_heads > 0x7fffffffLL)
+        return fail(FA512_ERR_UNSUPPORTED, "grid too large");
     if (batch == 0 || q_len == 0) return FA512_OK;
     if (!k_pages || !page_table || !kv_lens || !bounds) return fail(FA512_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(k_pages) || !aligned16(bounds))

@@ -185,7 +185,7 @@ def test_bounds_refusals(lib):
                      (1, dict(npages=0)), (1, dict(mpps=0)), (1, dict(kp=None)), (1, dict(bounds=None)),
                      (1, dict(kl=None)), (1, dict(kp=8)), (1, dict(bounds=24)), (1, dict(ql=3)), (1, dict(pt=2)),
                      (2, dict(ps=48)), (2, dict(b=65536)), (2, dict(hk=65536)), (2, dict(mpps=1 << 26)),
-                     (0, dict(b=0, kp=None)), (0, dict(qlen=0, kp=None))]:
+                     (2, dict(hk=65535, qlen=1 << 30, mpps=1 << 22)), (0, dict(b=0, kp=None)), (0, dict(qlen=0, kp=None))]:
         assert call(**kw) == want, kw
 
 
