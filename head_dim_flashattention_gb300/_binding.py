@@ -194,27 +194,11 @@ def _new(side, shape, dtype, device, returned: bool = True) -> torch.Tensor:
     return t
 
 
-# Memory of a stream without building a tensor (7 us of a call's host time between
-# launches, against 1.4 us).
+# A stream's memory without building a tensor, for a workspace that a call makes for
+# itself (7 us of a call's host time as a tensor, 1.4 us so).  Given back once the call is
+# queued: what follows on that stream may have it then.
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
-
-
-class _Scratch:
-    """A workspace that a call makes for itself, from the memory of the stream that it runs
-    on; what follows on that stream may have it as soon as the call is queued."""
-    __slots__ = ("ptr", "owner")
-
-    def __init__(self, size: int, handle: int, dev: int, stream):
-        if _raw_alloc is not None and _raw_free is not None:
-            self.owner, self.ptr = None, _raw_alloc(size, handle)
-        else:
-            self.owner = _new(_side(stream), size, torch.uint8, dev, returned=False)
-            self.ptr = self.owner.data_ptr()
-
-    def free(self):
-        if self.owner is None:
-            _raw_free(self.ptr)
 
 
 def fa512_status_string(status: int) -> str:
@@ -899,8 +883,7 @@ def _decode_bits(bits, q, k_pages, v_pages, page_table, kv_lens, selected, out, 
         ws_bytes = (lib.fa512_decode_workspace_bytes_sparse(bsz, qlen, hq, hk, bits, psz, n_sel, max_kv_len, num_splits)
                     if sparse else
                     lib.fa512_decode_workspace_bytes_fp4(bsz, qlen, hq, hk, psz, max_kv_len, num_splits)) or 256
-        scratch = _Scratch(ws_bytes, handle, dev, stream)
-        ws = scratch.ptr
+        ws = scratch = _raw_alloc(ws_bytes, handle)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _arg(workspace, "workspace", workspace.dtype, dev)
@@ -913,7 +896,7 @@ def _decode_bits(bits, q, k_pages, v_pages, page_table, kv_lens, selected, out, 
             _check(call(*head, *outs, n_sel, max_kv_len, *scales, num_splits, ws, ws_bytes, handle))
     finally:
         if scratch is not None:
-            scratch.free()
+            _raw_free(scratch)
     return out, lse
 
 
@@ -1005,8 +988,7 @@ def fa512_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
     if workspace is None:
         # 0: a shape that the call below refuses
         ws_bytes = lib.fa512_select_workspace_bytes(bsz, hk, psz, max_kv_len) or 256
-        scratch = _Scratch(ws_bytes, handle, dev, stream)
-        ws = scratch.ptr
+        ws = scratch = _raw_alloc(ws_bytes, handle)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _arg(workspace, "workspace", workspace.dtype, dev)
@@ -1014,7 +996,7 @@ def fa512_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
         _check(lib.fa512_select_pages(*args, ws, ws_bytes, handle))
     finally:
         if scratch is not None:
-            scratch.free()
+            _raw_free(scratch)
     return selected
 
 
