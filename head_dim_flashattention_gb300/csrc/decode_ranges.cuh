@@ -226,7 +226,10 @@ __device__ __forceinline__ void scores_narrow(const uint8_t* block, int lane, co
 }
 
 // O^T of columns 128 warp .. + 127 += V^T P^T over a block, scales applied to the codes;
-// m-tile i is columns 16 g + 2 i, 16 g + 2 i + 1 of those.
+// m-tile i is columns 16 g + 2 i, 16 g + 2 i + 1 of those.  (Multiplying
+// the weights by the scales instead takes 4 multiplications a block for up to 2 rows where
+// this takes 32, but the products do not fit f16: 18 binades of scales times the weights'
+// own.  It is no faster either, 621 and 626 us for 64 x 28,672 positions.)
 template <int NT>
 __device__ __forceinline__ void add_values_4(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[NT][2],
                                            float (&o)[NT][MTILES][4]) {
@@ -257,39 +260,6 @@ __device__ __forceinline__ void add_values_4(const uint8_t* block, int warp, int
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * x + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
         }
-    }
-}
-
-// The same for up to 2 rows: column 2 c + r of P^T is row r's weights times the
-// scales of group 4 h + c; m-tile 4 h + i is columns 16 (4 h + g % 4) + 8 (g / 4) +
-// 2 i, + 1.  A lane's sums of class t = g % 4 are O, the others are not used.
-__device__ __forceinline__ void add_values_narrow(const uint8_t* block, int warp, int lane, const uint32_t (&pb)[2],
-                                                  float (&o)[MTILES][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* rows[4];
-    uint2 sw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        rows[i] = block + v_row<4>(t, i) * Format<4>::ROW;
-        sw[i] = *reinterpret_cast<const uint2*>(rows[i] + CODES + 8 * warp);
-    }
-    const uint32_t pick = static_cast<uint32_t>(g >> 1) | (static_cast<uint32_t>(4 + (g >> 1)) << 4);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = *reinterpret_cast<const uint32_t*>(rows[i] + 64 * warp + 32 * h + 8 * (g & 3) + 4 * (g >> 2));
-        const uint32_t s01 = e4m3x2_f16(prmt(h ? sw[0].y : sw[0].x, h ? sw[1].y : sw[1].x, pick) & 0xffffu);
-        const uint32_t s23 = e4m3x2_f16(prmt(h ? sw[2].y : sw[2].x, h ? sw[3].y : sw[3].x, pick) & 0xffffu);
-        const uint32_t b0 = mul_f16x2(pb[0], s01), b1 = mul_f16x2(pb[1], s23);
-        uint32_t e01[4], d01[4], e23[4], d23[4];
-        e2m1x8_f16((w[0] & LOW_HALVES) | ((w[1] << 4) & ~LOW_HALVES), e01);
-        e2m1x8_f16(((w[0] >> 4) & LOW_HALVES) | (w[1] & ~LOW_HALVES), d01);
-        e2m1x8_f16((w[2] & LOW_HALVES) | ((w[3] << 4) & ~LOW_HALVES), e23);
-        e2m1x8_f16(((w[2] >> 4) & LOW_HALVES) | (w[3] & ~LOW_HALVES), d23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(o[4 * h + i], e01[i], d01[i], e23[i], d23[i], b0, b1);
     }
 }
 

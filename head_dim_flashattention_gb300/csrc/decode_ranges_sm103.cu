@@ -180,14 +180,13 @@ __device__ __forceinline__ Walk<BITS, LIST> first_of_range(const DecodeParams& p
 
 // ROWS: the most query rows (q_len * G) of a KV head, in NT n-tiles of 8.
 //
-// Up to 2 rows leave six of the eight columns of an n-tile free, and the group
+// Up to 2 rows leave six of the eight columns of an n-tile free, and the keys' group
 // scales move there (NARROW): column 2 c + r belongs to row r and scale class c.
 //   S^T: lane t holds K codes of groups 4 j + t, so with Q zero outside class t a
 //        lane's sums of step j are those of its own group, and take its scale in
 //        fp32: 32 multiply-adds a tile where scaling the codes takes 128.
-//   O^T: lane g holds codes of group 4 h + g % 4, and P is scaled once for each
-//        class: 4 multiplications a block where scaling the codes takes 32.  Of a
-//        lane's sums those of class t = g % 4 are O, the others are not used.
+//   O^T: the weights of row r stand in all columns 2 c + r, so that every lane has O,
+//        of which it writes a quarter.
 template <int BITS, int ROWS, bool LIST>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
 decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -354,8 +353,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 else scores_16<NT>(rows, lane, s_q, sc);
                 done_with(&k_empty[slot]);
                 // ---- softmax against this warp's reference, which rises where a weight would pass
-                // 2^7 (times a group scale, 448 at most, that stays in f16's range), to the block's
-                // maximum rounded up to a whole number, less 3: few blocks raise it
+                // 2^7, to the block's maximum rounded up to a whole number, less 3: few blocks raise it
                 const int kp = base + ra;
                 uint2 frag[NT];
                 float sv[NT][2][2];
@@ -545,8 +543,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 // ---- O^T += V^T P^T for this warp's columns
 #pragma unroll
                 for (int w = 0; w < BLOCKS; ++w) {
-                    if constexpr (NARROW) add_values_narrow(rows + 16 * w * F::ROW, warp, lane, pb[w][0], o[0]);
-                    else if constexpr (BITS == 4) add_values_4<NT>(rows + 16 * w * F::ROW, warp, lane, pb[w], o);
+                    if constexpr (BITS == 4) add_values_4<NT>(rows + 16 * w * F::ROW, warp, lane, pb[w], o);
                     else if constexpr (BITS == 8) add_values_8<NT>(rows, 16 * w, warp, lane, pb[w], o);
                     else add_values_16<NT>(rows, warp, lane, pb[w], o);
                 }
@@ -558,15 +555,14 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             if constexpr (NARROW) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    if (r >= R || (g & 3) != t) continue;
-                    float* dst = p.ws_o + (row_index(seg.b, r) * S + mine) * D + 128 * warp + 16 * t + 8 * (g >> 2);
+                    if (r >= R) continue;
+                    float* dst = p.ws_o + (row_index(seg.b, r) * S + mine) * D + 128 * warp + 16 * g;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
-                                make_float4(o[0][4 * h + 2 * j][r] * f, o[0][4 * h + 2 * j][2 + r] * f,
-                                            o[0][4 * h + 2 * j + 1][r] * f, o[0][4 * h + 2 * j + 1][2 + r] * f);
+                    for (int j = 0; j < MTILES / 2; ++j)
+                        if (t == j)
+                            *reinterpret_cast<float4*>(dst + 4 * j) =
+                                make_float4(o[0][2 * j][r] * f, o[0][2 * j][2 + r] * f, o[0][2 * j + 1][r] * f,
+                                            o[0][2 * j + 1][2 + r] * f);
                 }
             } else {
 #pragma unroll
