@@ -366,7 +366,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         const bool vb = base >= 0 && static_cast<unsigned>(qpos[n][i] - kp - 8) < reach;
                         sv[n][i][0] = va ? sc[n][i] * rs[n][i] * p.scale_log2 : -INFINITY;
                         sv[n][i][1] = vb ? sc[n][2 + i] * rs[n][i] * p.scale_log2 : -INFINITY;
-                        above |= fmaxf(sv[n][i][0], sv[n][i][1]) > m[n][i] + 7.f;
+                        above |= fmaxf(sv[n][i][0], sv[n][i][1]) - m[n][i] > 7.f;   // (a sum with m may round)
                     }
                 if (__any_sync(0xffffffffu, above))
 #pragma unroll
@@ -376,7 +376,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                             float most = fmaxf(sv[n][i][0], sv[n][i][1]);
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                            const float to = most > m[n][i] + 7.f ? ceilf(most) - 3.f : m[n][i];
+                            const float to = most - m[n][i] > 7.f ? ceilf(most) - 3.f : m[n][i];
                             l[n][i] *= fast_exp2(m[n][i] - finite_ref(to));
                             m[n][i] = to;
                         }
@@ -390,8 +390,8 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         pr[i][1] = fast_exp2(sv[n][i][1] - ref);
                         l[n][i] += pr[i][0] + pr[i][1];      // the sums keep the fp32 weights
                     }
-                    // P rounds to bf16 (2^-8 of a weight), or to f16: 2^-11 of it or 2^-25, where some
-                    // weight is above 4
+                    // P rounds to bf16 (2^-8 of a weight), the type of the values it meets, or to f16:
+                    // 2^-11 of it or 2^-25, where some weight is above 4
                     if constexpr (NARROW) {
                         frag[n].x = pack_f16x2(t & 2 ? (t & 1 ? pr[1][1] : pr[0][1]) : (t & 1 ? pr[1][0] : pr[0][0]), 0.f);
                     } else {
@@ -461,7 +461,12 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             }
             const Segment seg = s_seg[segment % META];
             // O's references are the largest of the K warps'; lane 8 w + r keeps K warp w's of row
-            // 8 n + r (NARROW: r), O's, and the factor from the one to the other
+            // 8 n + r (NARROW: r), O's, and the factor from the one to the other.  A warp's weights
+            // reach 2^7 whatever its reference, so the factor counts down to where they end: times
+            // JOIN, as O is then, f16 holds it to 2^-32, and the largest product is 2^15.  (From
+            // 2^-33 on it is 0: such weights are below 2^-28 of the row's largest, which is above
+            // 2^2.  Without JOIN that came at 2^-20.)
+            constexpr float JOIN = BITS == 16 ? 1.f : 256.f;
             float ref[NT], top[NT], factor[NT];
             float o[NT][MTILES][4];
 #pragma unroll
@@ -491,7 +496,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 16));
                         const float al = fast_exp2(top[n] - finite_ref(to));
                         top[n] = to;
-                        factor[n] = fast_exp2(now - finite_ref(to));
+                        factor[n] = fast_exp2(now - finite_ref(to)) * JOIN;
                         const float al0 = __shfl_sync(0xffffffffu, al, NARROW ? 0 : 2 * t);
                         const float al1 = __shfl_sync(0xffffffffu, al, NARROW ? 1 : 2 * t + 1);
 #pragma unroll
@@ -551,7 +556,7 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             }
             // ---- the segment's partial, unnormalised and times v_scale
             const int mine = seg.index & ~Segment::LAST;
-            const float f = p.o_scale;
+            const float f = p.o_scale * (1.f / JOIN);
             if constexpr (NARROW) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

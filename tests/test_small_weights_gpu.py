@@ -97,3 +97,63 @@ def test_small_group_scales_under_a_dominating_key(fa, n, rest, rows, sparse, sp
     q[..., :16] = 1
     score = math.log((n - 1) * (1 - rest) / rest)         # the others have `rest` of the weight together
     check(fa, "e2m1", sparse, q.to(torch.bfloat16), k, v, n, score / 96, num_splits=splits)
+
+
+def sums(x):
+    """[n] multiples of 0.5 up to 96 in size -> [n, 512] E2M1 values whose first 16 add up to them."""
+    out, left = np.zeros((len(x), D)), np.abs(np.asarray(x, dtype=np.float64))
+    for j in range(16):
+        out[:, j] = paged.E2M1[np.searchsorted(paged.E2M1, np.minimum(left, 6), side="right") - 1]
+        left -= out[:, j]
+    assert not left.any()
+    return out * np.sign(x)[:, None]
+
+
+def stored(kind, values, scale_byte):
+    """Rows of a cache that stand for ``values`` times the scale (4 bits) or for ``values`` (E4M3)."""
+    if kind == "e2m1":
+        return cache(fp4(values, np.full((len(values), 32), scale_byte)))
+    return cache(torch.tensor(values, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+KINDS = pytest.mark.parametrize("kind,sparse", [("e2m1", False), ("e2m1", True), ("e4m3", True)])
+
+
+@KINDS
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("rows", [1, 2, 3, 8, 16])
+@pytest.mark.parametrize("first,later", [(-24.5, -20.5), (-25.5, -21.5), (-30.5, -22.5), (-20.5, -20.5)])
+def test_weights_far_below_another_block_s(fa, first, later, rows, splits, kind, sparse):
+    """A dominating key in one block, all others in blocks whose reference, taken from lower scores than most of
+    theirs, is 25 binades or more below."""
+    n = 20000
+    score = np.full(n, later)                             # log2 of the weights
+    score[0], score[1:16], score[16:64] = 0.5, -60, first
+    values = np.broadcast_to(3 * np.sign(np.random.RandomState(rows).randn(D)), (n, D)).copy()
+    values[0] = 0
+    q = torch.zeros(1, rows, D)
+    q[..., :16] = 1
+    check(fa, kind, sparse, q.to(torch.bfloat16), stored(kind, sums(score), 0x38), stored(kind, values, 0x38), n,
+          math.log(2), num_splits=splits)
+
+
+@KINDS
+@pytest.mark.parametrize("rows", [1, 2, 3, 16])
+@pytest.mark.parametrize("e", [22, 23, 24, 25, 26, 27, 28, 30])
+def test_scores_a_step_of_fp32_apart(fa, e, rows, kind, sparse):
+    """Scores near 2^e in log2 units, rising by one step of fp32 from block to block: no weight passes f16.  All
+    values of a column are the same, and so is the output, within half a step of its bf16 and the weights' 2^-10."""
+    n = 1500
+    step = np.minimum(np.arange(n) // 16, 90).astype(np.float64)
+    k_values = sums(np.full(n, 64.0))
+    k_values[:, 16:32] = sums(step)[:, :16]
+    top = 2688 if kind == "e2m1" else 448                 # the largest that the format holds
+    sign = np.sign(np.random.RandomState(rows).randn(D))
+    values = np.broadcast_to((6 if kind == "e2m1" else 448) * sign, (n, D))
+    q = torch.zeros(1, rows, D)
+    q[..., :16], q[..., 16:32] = 2.0 ** (e - 6), 2.0 ** (e - 23)
+    for splits in (0, 1):
+        o, l, _, _ = run(fa, kind, sparse, q.to(torch.bfloat16), stored(kind, k_values, 0x38),
+                         stored(kind, values, 0x7E), n, math.log(2), num_splits=splits)
+        assert np.max(np.abs(o - top * sign)) <= (2.0 ** -8 + 2.0 ** -10) * top
+        assert np.all(np.abs(l / (2.0 ** e * math.log(2)) - 1) <= 2.0 ** -15)
