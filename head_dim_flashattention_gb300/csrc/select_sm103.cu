@@ -196,7 +196,8 @@ constexpr int score_smem(int rows) { return SCORE_WARPS * SCORE_STAGES * PAGE_BY
 
 // Unsigned integers in the order of the scores, -0 and 0 equal.  Largest of all are the
 // pages that are always chosen, then those with a NaN or infinite score: the formula
-// above turns every bound that is not finite into one of the two.
+// above turns every bound that is not finite into one of the two.  (A NaN in a query
+// makes all scores NaN, so the pages are chosen by their number.)
 constexpr uint32_t KEY_ALWAYS = 0xffffffffu, KEY_NOT_FINITE = 0xfffffffeu;
 __device__ __forceinline__ uint32_t key_of(float x) {
     if (x != x || x == INFINITY) return KEY_NOT_FINITE;
@@ -217,6 +218,18 @@ __device__ __forceinline__ void unpack8(const uint4 x, float2 (&f)[4]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+// max(q, 0) and min(q, 0), NaN of NaN
+__device__ __forceinline__ float above_0(float q) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(q));
+    return r;
+}
+__device__ __forceinline__ float below_0(float q) {
+    float r;
+    asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(q));
+    return r;
 }
 
 // Sums over the lanes of N values at once, each by halves (lanes 16 apart, then 8, ...):
@@ -343,8 +356,8 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
                     for (int e = 0; e < 4; ++e) {
                         const float4 q4 = q[(2 * j + (e >> 1)) * 32];
                         const float2 qe = e & 1 ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
-                        const float2 up = make_float2(fmaxf(qe.x, 0.f), fmaxf(qe.y, 0.f));
-                        const float2 down = make_float2(fminf(qe.x, 0.f), fminf(qe.y, 0.f));
+                        const float2 up = make_float2(above_0(qe.x), above_0(qe.y));
+                        const float2 down = make_float2(below_0(qe.x), below_0(qe.y));
 #pragma unroll
                         for (int k = 0; k < SCORE_PAGES; ++k) {
                             x[k][e] = ffma2(down, lo[k][4 * j + e], j ? x[k][e] : make_float2(0.f, 0.f));

@@ -608,7 +608,8 @@ fa512_status fa512_cache_page_bounds(const void* k_pages, const int32_t* page_ta
  * drafted tokens are among the last: n_last counts them.)  Rows whose position
  * kv_lens[b] - q_len + t is negative are left out.  A page with a bound that is
  * not finite comes before all others; one whose index lies outside the pool
- * comes last and is recorded in the error word.
+ * comes last and is recorded in the error word.  A NaN in a row that counts makes
+ * all scores of its KV head equal.
  *
  * Sums are fp32 in a fixed order (channels c and c + 256, then c % 8 by halves,
  * then c / 8 by halves), so the choice is the same for every launch shape.
