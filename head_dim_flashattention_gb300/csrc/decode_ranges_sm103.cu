@@ -684,6 +684,12 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     for (int i = lane; i < p.q_len * p.n_q_heads * S; i += 32)
                         reinterpret_cast<float2*>(p.ws_ml)[static_cast<size_t>(b) * p.q_len * p.n_q_heads * S + i] =
                             make_float2(-INFINITY, 0.f);
+            // entries of a list that is longer than its sequence's pages: none of them can name one (a page
+            // there would be one too many, or not rise)
+            if constexpr (LIST)
+                for (int b = index; b < p.batch; b += static_cast<int>(gridDim.x) / p.n_kv_heads)
+                    for (int e = item_of<BITS, LIST>(p, b).held + lane; e < p.n_listed; e += 32)
+                        if (list_of(p, b, kvh)[e] >= 0) report_error(p.err, FA512_DEVICE_ERR_INDEX);
         }
         int it = 0;
         for (int segment = 0; walk.left > 0 && ok; ++segment) {

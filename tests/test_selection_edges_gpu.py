@@ -52,3 +52,54 @@ def test_select_with_a_nan_in_a_query(fa, q_len, hq, hk, channel):
         by_number = list(range(pick - 2)) + [need[b] - 2, need[b] - 1]
         assert want[b, h].tolist() == by_number and got[b, h].tolist() == by_number
     assert np.array_equal(got, want)
+
+
+def list_call(fa, kind, rows, lens, lists, hk):
+    """Attention over lists [batch][hk] of entries, padded with -1; pages of 16, in order."""
+    width = max(1, max(paged.pages_of(n, 16) for n in lens))
+    n_sel = max(len(x) for per in lists for x in per)
+    sel = np.full((len(lens), hk, n_sel), -1, dtype=np.int32)
+    for b, per in enumerate(lists):
+        for h, x in enumerate(per):
+            sel[b, h, :len(x)] = x
+    table = torch.arange(len(lens) * width, dtype=torch.int32).view(len(lens), width)
+    shape = (len(lens) * width, 16, hk)
+    if kind == "bf16":
+        call, k = fa.fa512_decode_paged_sparse, torch.ones(*shape, D, dtype=torch.bfloat16)
+    elif kind == "e4m3":
+        call, k = fa.fa512_decode_paged_sparse_fp8, torch.full((*shape, D), 0x38, dtype=torch.uint8)
+    else:
+        call, k = fa.fa512_decode_paged_sparse_fp4, torch.full((*shape, 288), 0x22, dtype=torch.uint8)
+    q = workloads.draft_queries(len(lens), 1, rows * hk, seed=5)
+    o, l = call(q.cuda(), k.cuda(), k.cuda(), table.cuda(), i32(lens).cuda(), torch.from_numpy(sel).cuda(),
+                max_kv_len=width * 16)
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all()
+    return l.view(len(lens), hk, rows).cpu()
+
+
+KINDS = pytest.mark.parametrize("kind", ["bf16", "e4m3", "e2m1"])
+
+
+@KINDS
+@pytest.mark.parametrize("rows", [2, 12])
+def test_entries_behind_a_sequence_s_pages_are_recorded(fa, kind, rows):
+    """A list may have more entries than its sequence has pages; those name none."""
+    late = [[-1] * 54 + list(range(10)), list(range(10)) + [10], list(range(10)) + [3], [0, 1] + [-1] * 60 + [5],
+            [-1] * 10 + [0], [9] + [-1] * 9 + [1 << 30]]
+    every = list(range(10))
+    l = list_call(fa, kind, rows, [160, 150, 0, 1], [[[9] + [-1] * 70, every], [[0, 3, 9], every], [[], []], [[0], []]], 2)
+    assert fa.fa512_device_status() == 0
+    assert torch.isneginf(l[2]).all()
+    for bad in late:
+        list_call(fa, kind, rows, [150], [[bad]], 1)
+        assert fa.fa512_device_status() == 6, bad
+        for b in range(3):                               # beside others, of the second KV head
+            lists = [[list(range(4)), list(range(4))] for _ in range(3)]
+            lists[b][1] = bad
+            list_call(fa, kind, rows, [150, 160, 145], lists, 2)
+            assert fa.fa512_device_status() == 6, (bad, b)
+    for bad in ([0], [-1, 0], [-1] * 70 + [7]):           # no pages at all
+        l = list_call(fa, kind, rows, [0, 150], [[bad], [[0, 1]]], 1)
+        assert fa.fa512_device_status() == 6, bad
+        assert torch.isneginf(l[0]).all()
