@@ -194,11 +194,20 @@ def _new(side, shape, dtype, device, returned: bool = True) -> torch.Tensor:
     return t
 
 
-# A stream's memory without building a tensor, for a workspace that a call makes for
-# itself (7 us of a call's host time as a tensor, 1.4 us so).  Given back once the call is
-# queued: what follows on that stream may have it then.
+# A stream's memory without building a tensor (7 us of a call's host time as a tensor,
+# 1.4 us so).
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _scratch(size: int, handle: int, stream, dev: int):
+    """(address, tensor or None) of a workspace that a call makes for itself, from the
+    memory of the stream it runs on.  Without a tensor the address goes to _raw_free once
+    the call is queued: what follows on that stream may have it then."""
+    if _raw_alloc is not None and _raw_free is not None:
+        return _raw_alloc(size, handle), None
+    t = _new(_side(stream), size, torch.uint8, dev, returned=False)
+    return t.data_ptr(), t
 
 
 def fa512_status_string(status: int) -> str:
@@ -877,13 +886,14 @@ def _decode_bits(bits, q, k_pages, v_pages, page_table, kv_lens, selected, out, 
         scales += (float(k_scale), float(v_scale))
     if sparse:
         head += (_arg(selected, "selected", _I32, dev, (bsz, hk, n_sel)),)
-    handle, scratch = _stream(stream, dev), None
+    handle, raw = _stream(stream, dev), False
     if workspace is None:
         # 0: a shape that the call below refuses
         ws_bytes = (lib.fa512_decode_workspace_bytes_sparse(bsz, qlen, hq, hk, bits, psz, n_sel, max_kv_len, num_splits)
                     if sparse else
                     lib.fa512_decode_workspace_bytes_fp4(bsz, qlen, hq, hk, psz, max_kv_len, num_splits)) or 256
-        ws = scratch = _raw_alloc(ws_bytes, handle)
+        ws, owner = _scratch(ws_bytes, handle, stream, dev)
+        raw = owner is None
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _arg(workspace, "workspace", workspace.dtype, dev)
@@ -895,8 +905,8 @@ def _decode_bits(bits, q, k_pages, v_pages, page_table, kv_lens, selected, out, 
                     lib.fa512_decode_paged_sparse_fp8 if bits == 8 else lib.fa512_decode_paged_sparse_fp4)
             _check(call(*head, *outs, n_sel, max_kv_len, *scales, num_splits, ws, ws_bytes, handle))
     finally:
-        if scratch is not None:
-            _raw_free(scratch)
+        if raw:
+            _raw_free(ws)
     return out, lse
 
 
@@ -984,19 +994,20 @@ def fa512_select_pages(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.
             _arg(page_table, "page_table", _I32, dev, (bsz, mpps)), _arg(kv_lens, "kv_lens", _I32, dev, (bsz,)),
             _arg(selected, "selected", _I32, dev, (bsz, hk, max(n_select, 0))), bsz, qlen, hq, hk, psz, npages, mpps,
             max_kv_len, n_select, int(n_first), int(n_last))
-    handle, scratch = _stream(stream, dev), None
+    handle, raw = _stream(stream, dev), False
     if workspace is None:
         # 0: a shape that the call below refuses
         ws_bytes = lib.fa512_select_workspace_bytes(bsz, hk, psz, max_kv_len) or 256
-        ws = scratch = _raw_alloc(ws_bytes, handle)
+        ws, owner = _scratch(ws_bytes, handle, stream, dev)
+        raw = owner is None
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _arg(workspace, "workspace", workspace.dtype, dev)
     try:
         _check(lib.fa512_select_pages(*args, ws, ws_bytes, handle))
     finally:
-        if scratch is not None:
-            _raw_free(scratch)
+        if raw:
+            _raw_free(ws)
     return selected
 
 
