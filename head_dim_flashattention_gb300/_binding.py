@@ -722,7 +722,7 @@ def fa512_cache_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: to
 
 def _whole_cache(k_pages, v_pages):
     """(device, k pointer, v pointer, layers, pages, page size, heads, bytes) of a cache of one or several layers."""
-    fp4 = k_pages.shape[-1] == FP4_ROW_BYTES and k_pages.dtype is torch.uint8
+    fp4 = k_pages.dtype is torch.uint8 and k_pages.shape[-1:] == (FP4_ROW_BYTES,)
     if k_pages.dim() not in (4, 5) or k_pages.dtype is not v_pages.dtype or not (fp4 or k_pages.shape[-1] == HEAD_DIM):
         raise Fa512Error(1, "pages must be [(layers,) n, page, heads, 512] (288 in 4 bits), k_pages like v_pages")
     dev = _device(k_pages, "k_pages")
@@ -940,7 +940,7 @@ def fa512_cache_page_bounds(k_pages: torch.Tensor, page_table: torch.Tensor, kv_
     smallest and largest key element, without the tensor scale.
     """
     ks = k_pages.shape
-    bits = 4 if ks[-1] == FP4_ROW_BYTES and k_pages.dtype is torch.uint8 else 8 * k_pages.element_size()
+    bits = 4 if k_pages.dtype is torch.uint8 and ks[-1:] == (FP4_ROW_BYTES,) else 8 * k_pages.element_size()
     if len(ks) != 4 or page_table.dim() != 2 or (bits != 4 and ks[3] != HEAD_DIM):
         raise Fa512Error(1, "k_pages must be [n, page, heads, 512] (288 in 4 bits), page_table [batch, pages]")
     npages, psz, hk, _ = ks

@@ -247,3 +247,16 @@ def test_the_binding_refuses_before_it_launches():
         fa.fa512_select_pages(x.view(1, 1, 1), x, x, x, page_size=64, n_select=3)
     with pytest.raises(fa.Fa512Error):
         fa.fa512_cache_page_bounds(x.view(1, 1, 1, 1), x.view(1, 1), x, x, q_len=1)
+
+
+def test_caches_without_dimensions_are_refused():
+    x, z = torch.zeros(1), torch.zeros(())
+    t, n = torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for f in (lambda: fa.fa512_cache_compact(z, z, t, n, t, n, q_len=1),
+              lambda: fa.fa512_cache_fork(z, z, t, n, n, x),
+              lambda: fa.fa512_cache_page_bounds(z, t, n, x, q_len=1),
+              lambda: fa.fa512_cache_append_fp4(z, z, z, z, t, n),
+              lambda: fa.fa512_decode_paged_fp4(z, z, z, t, n),
+              lambda: fa.fa512_select_pages(z, z, t, n, page_size=64, n_select=1)):
+        with pytest.raises(fa.Fa512Error):
+            f()
