@@ -701,8 +701,8 @@ fa512_status decode_call(const void* q, const void* k_pages, const void* v_pages
 // ---------------------------------------------- 4-bit caches, selected pages
 
 // Whether such a call takes these sizes.
-bool ranges_size_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int max_kv_len, int num_splits) {
-    return batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
+bool ranges_size_ok(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size, int max_kv_len, int num_splits) {
+    return pow2_page(page_size) && batch >= 0 && q_len >= 1 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 &&
            static_cast<long long>(q_len) * (n_q_heads / n_kv_heads) <= 16 && max_kv_len >= 0 && num_splits >= 0 &&
            num_splits <= 1024 && static_cast<long long>(batch) * q_len <= 65535 && n_kv_heads <= 65535;
 }
@@ -970,20 +970,20 @@ fa512_status fa512_decode_paged_sparse_fp4(const void* q, const void* k_pages, c
 
 int fa512_decode_auto_splits_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                                  int max_kv_len) {
-    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0)) return 1;
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len, 0)) return 1;
     return ranges_splits(4, batch, n_kv_heads, max_kv_len, false);
 }
 
 size_t fa512_decode_workspace_bytes_fp4(int batch, int q_len, int n_q_heads, int n_kv_heads, int page_size,
                                         int max_kv_len, int num_splits) {
-    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits)) return 0;
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len, num_splits)) return 0;
     return workspace_for(batch * q_len, n_q_heads,
                          num_splits > 0 ? num_splits : ranges_splits(4, batch, n_kv_heads, max_kv_len, false));
 }
 
 int fa512_decode_auto_splits_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads, int element_bits,
                                     int page_size, int n_selected, int max_kv_len) {
-    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, 0) || !pow2_page(page_size) ||
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len, 0) ||
         n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
         return 1;
     return ranges_splits(element_bits, batch, n_kv_heads, listed_positions(page_size, n_selected, max_kv_len), true);
@@ -992,7 +992,7 @@ int fa512_decode_auto_splits_sparse(int batch, int q_len, int n_q_heads, int n_k
 size_t fa512_decode_workspace_bytes_sparse(int batch, int q_len, int n_q_heads, int n_kv_heads,
                                            int element_bits, int page_size, int n_selected, int max_kv_len,
                                            int num_splits) {
-    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, max_kv_len, num_splits) || !pow2_page(page_size) ||
+    if (!ranges_size_ok(batch, q_len, n_q_heads, n_kv_heads, page_size, max_kv_len, num_splits) ||
         n_selected < 1 || (element_bits != 16 && element_bits != 8 && element_bits != 4))
         return 0;
     const int s = num_splits > 0 ? num_splits

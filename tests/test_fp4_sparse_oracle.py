@@ -260,3 +260,11 @@ def test_caches_without_dimensions_are_refused():
               lambda: fa.fa512_select_pages(z, z, t, n, page_size=64, n_select=1)):
         with pytest.raises(fa.Fa512Error):
             f()
+
+
+def test_sizes_for_pages_that_no_call_takes(lib):
+    for psz in (0, -64, 8, 48, 512):
+        assert fa.fa512_decode_workspace_bytes_fp4(1, 1, 8, 4, psz, 4096) == 0
+        assert fa.fa512_decode_auto_splits_fp4(1, 1, 8, 4, psz, 4096) == 1
+        assert fa.fa512_decode_workspace_bytes_sparse(1, 1, 8, 4, 16, psz, 9, 4096) == 0
+        assert fa.fa512_decode_auto_splits_sparse(1, 1, 8, 4, 16, psz, 9, 4096) == 1
