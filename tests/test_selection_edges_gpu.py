@@ -103,3 +103,52 @@ def test_entries_behind_a_sequence_s_pages_are_recorded(fa, kind, rows):
         l = list_call(fa, kind, rows, [0, 150], [[bad], [[0, 1]]], 1)
         assert fa.fa512_device_status() == 6, bad
         assert torch.isneginf(l[0]).all()
+
+
+@KINDS
+@pytest.mark.parametrize("q_len,hq,hk", [(1, 8, 4), (1, 8, 1), (4, 8, 2), (2, 3, 1)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_against_the_dense_call(fa, kind, q_len, hq, hk, window):
+    """Lists of all pages against the dense call, and the dense 4-bit call under a window against the reference.
+
+    Tolerance of each call's output, A = sum p |v| / sum p (fp64): 2^-8 |O| (bf16), 1e-3 A (the scores), 1e-6, and
+    the weights' rounding: 2^-8 A to bf16 (dense E4M3 too, for the rows it widens to bf16), 2^-10 A to f16 with 2^-26 n
+    vmax for those below its normal range.
+    """
+    lens, psz = [1000, 130, 64, q_len], 64
+    need = [paged.pages_of(n, psz) for n in lens]
+    table = np.zeros((len(lens), max(need)), dtype=np.int32)
+    sel = np.full((len(lens), hk, max(need)), -1, dtype=np.int32)
+    at = 0
+    for b, k in enumerate(need):
+        table[b, :k] = np.arange(at, at + k)[::-1]
+        sel[b, :, :k] = np.arange(k)
+        at += k
+    rng = np.random.RandomState(9)
+    x = [torch.tensor(rng.randn(at, psz, hk, D), dtype=torch.float32).to(torch.bfloat16) for _ in range(2)]
+    kw, vmax = {}, float(x[1].float().abs().max())
+    if kind == "e4m3":
+        kw = {"k_scale": 0.0371, "v_scale": 0.0517}
+        x = [(y.float() / s).to(torch.float8_e4m3fn).view(torch.uint8) for y, s in zip(x, (0.0371, 0.0517))]
+    elif kind == "e2m1":
+        kw = {"k_scale": 0.25, "v_scale": 1.3}
+        x = [torch.from_numpy(paged.fp4_rows(y, s)) for y, s in zip(x, (0.25, 1.3))]
+    table, n, sel = torch.from_numpy(table), i32(lens), torch.from_numpy(sel)
+    q = workloads.draft_queries(len(lens), q_len, hq, seed=4)
+    args = (q, x[0], x[1], table, n)
+    dense, lists = {"bf16": (fa.fa512_decode_paged_q, fa.fa512_decode_paged_sparse),
+                    "e4m3": (fa.fa512_decode_paged_fp8, fa.fa512_decode_paged_sparse_fp8),
+                    "e2m1": (fa.fa512_decode_paged_fp4, fa.fa512_decode_paged_sparse_fp4)}[kind]
+    on = [y.cuda() for y in args]
+    ref, rl, weight = paged.decode_paged_any(*args, window=window, **kw)
+    base = 2.0 ** -8 * np.abs(ref) + 1e-3 * weight + 1e-6
+    f16 = 2.0 ** -10 * weight + 2.0 ** -26 * max(lens) * 1.5 * vmax
+    bf16 = 2.0 ** -8 * weight
+    of_dense, of_lists = base + (f16 if kind == "e2m1" else bf16), base + (bf16 if kind == "bf16" else f16)
+    o, l = (y.float().cpu().numpy().astype(np.float64) for y in dense(*on, max_kv_len=1000, window=window, **kw))
+    assert np.all(np.abs(o - ref) <= of_dense) and np.max(np.abs(l - rl)) <= 1e-3
+    if not window:
+        s, m = (y.float().cpu().numpy().astype(np.float64) for y in lists(*on, sel.cuda(), max_kv_len=1000, **kw))
+        assert np.all(np.abs(s - ref) <= of_lists) and np.max(np.abs(m - rl)) <= 1e-3
+        assert np.all(np.abs(s - o) <= of_dense + of_lists) and np.max(np.abs(m - l)) <= 1e-4
+    assert fa.fa512_device_status() == 0
