@@ -725,7 +725,11 @@ struct RangesPlan {
 // For sequences of at most `tiles` tiles.  Times in tile times of a CTA that shares
 // its SM (1.6 us; alone it takes 0.6 of that), a tile for a CTA's start and end, 0.02
 // for each of a sequence's segments in the merge.  A batch with shorter sequences has
-// shorter ranges, so a batch of several may leave twice the segments.
+// shorter ranges, so a batch of several may leave twice the segments: enough for lengths
+// down to half the bound.  What is shorter on the whole keeps ranges that are too long, and
+// CTAs without any (4 bits: 64 x 4,096 positions 101 us with that bound, 511 with 131,072;
+// 1 x 28,672 beside 63 x 200 153, 59 with 1,024 segments allowed; but 64 x 28,672 626 and
+// 645, for the partials of more segments are more to go through).
 // Lists of pages (list_bits: of a cached element; 0: no lists) are mostly full: where a
 // number of groups for each sequence divides its tiles and its ranges are no more than a
 // quarter longer, no range goes over two sequences and starts a second time (16
@@ -734,7 +738,7 @@ struct RangesPlan {
 // 4 bits: 26 with 72 of 9, 35 with 40 of 16).  Over coded caches a CTA has more to compute
 // for its bytes, and fewer of them take longer where ranges are long (64 x 64 pages of
 // 64, E4M3: 163 us with 76 ranges of 108, 166 with 64 of 128; 4 bits: 107 with 76 of 54,
-// 115 with 64 of 64).
+// 115 with 64 of 64, on one box; 108 to 116 as it is from box to box).
 RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm, int list_bits) {
     RangesPlan best{1, 1};
     if (batch <= 0 || n_kv_heads <= 0) return best;

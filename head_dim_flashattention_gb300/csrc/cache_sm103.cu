@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // the NaN scale and codes 0; a scale that rounds to 0 makes the codes 0.
 //
 // A warp rounds one row of K and of V, a group of 16 elements a lane.  Bound: bytes (8
-// sequences of up to 4,096 new tokens, 4 heads: 335 MB in 55 us, 6.1 TB/s); the 18
-// divisions of a group cost more issue slots than that takes (170 us), so tensor
-// scales that are powers of two have a path without them (to_4bit_pow2).  One token of
-// 16 sequences takes 2.1 us.
+// sequences of up to 4,096 new tokens, 4 heads: 335 MB in 55 us, 6.1 TB/s); the 33
+// divisions of a group cost more issue slots than that takes (147 us), so tensor
+// scales that are both powers of two have a path without them (to_4bit_pow2).  One token
+// of 16 sequences takes 2.1 us.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

@@ -327,7 +327,7 @@ __device__ __forceinline__ void add_values_8(const uint8_t* slot, int first, int
 
 // bf16: b0/b1 of k-step 2 j + s are a row's elements 32 j + 8 t + 4 s + {0, 1} / {2, 3}.
 template <int NT>
-__device__ __forceinline__ void scores_16(const uint8_t* slot, int lane,                                           const uint2* s_q, float (&sc)[NT][4]) {
+__device__ __forceinline__ void scores_16(const uint8_t* slot, int lane, const uint2* s_q, float (&sc)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     const int row = Format<16>::order(g);
     float acc[NT][2][4];                          // two chains of sums

@@ -7,7 +7,9 @@
 // heads of a position lie side by side: read at about the same time they share the
 // memory's lines.  Ranges that did not keep the heads together took 997 us instead of
 // 741 for 64 sequences of 28,672 positions in 4 bits.)  With a list of pages the tiles
-// are counted along it.
+// are counted along it.  Ranges are long enough that no sequence is left in more than
+// num_splits segments, the places that its partials have: the host's choice of those is
+// for lengths between half of max_kv_len and all of it.
 //
 // K and V rows come by TMA, two warps' work, into rings of slots that run on across
 // segments.  Four warps form S^T = K Q^T, a block of 16 positions at a time over the
@@ -18,8 +20,10 @@
 // both products of different tiles overlap.  (64 sequences of 28,672 positions in 4
 // bits: one group of warps that did both in turn 846 us, two groups 775, the group
 // scales in free columns for 2 rows 707, loads on warps of their own 649, references
-// that seldom change 641, Q in shared memory and registers where they are needed 622:
-// 6.8 TB/s.)  References are whole numbers in log2 units: what brings two of them
+// that seldom change 641, Q in shared memory and registers where they are needed 622,
+// values' scales back on their codes 622 to 627: 6.8 TB/s.  9 to 16 rows spill a few
+// registers: 64 x 8,192, 16 heads over 1, 83 us for 45 us of bytes; 32 over 4 with 2
+// tokens 278 for 178.)  References are whole numbers in log2 units: what brings two of them
 // together is a power of two, exact in f16 and bf16.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -250,8 +254,9 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
     if (role == 0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K_REGS));
         // ---- Q^T fragments, bf16 as stored, else in f16 after a power-of-two scale per row
-        // that keeps its largest element below 2^15 (exact for elements down to 2^-39 of
-        // that; a score is unscaled before the softmax)
+        // that keeps its largest element below 2^15 (exact down to 2^-32 of that, where all 8
+        // bits of an element still fit, and off by at most 2^-40 of it below; a score is
+        // unscaled before the softmax)
         float rs[NT][2];                          // 1 / scale of rows row_of(n, 0), row_of(n, 1)
         auto load_q = [&](int b) {
 #pragma unroll

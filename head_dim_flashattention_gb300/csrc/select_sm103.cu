@@ -33,8 +33,9 @@ constexpr int D = 512;
 // of a coded one, in 4 bits those of one scale), the rows dealt to 4 groups of
 // threads, 16 of them in flight, whose results meet in shared memory.  NaN elements
 // make both bounds NaN.  The blocks of a page's heads, whose rows lie side by side, come
-// one after another.  What it takes is the two look-ups before a block's first row and,
-// in 4 bits, the arithmetic (24 conversions and comparisons for 16 elements): 8 sequences
+// one after another.  What it takes is the two look-ups before a block's first row, anew
+// for the second wave of blocks (of 2,024 with work 1,216 are resident), and, in 4 bits,
+// the arithmetic (24 conversions and comparisons for 16 elements): 8 sequences
 // of up to 4,096 new tokens, 4 heads, 4 bits: 37 MB in 13.0 us from memory (six blocks an
 // SM instead of eight: 13.9, five 14.2; E4M3 15.2 with seven, 15.9 with six, 15.7 with
 // eight); one token of 16 sequences, bf16, 2.3 us.
@@ -188,7 +189,8 @@ __global__ void __launch_bounds__(bounds_threads(BITS), BITS == 16 ? 2 : BITS ==
 constexpr int SCORE_WARPS = 4;
 constexpr int SCORE_PAGES = 2;
 constexpr int SCORE_STAGES = 4;                      // pages in the ring, a multiple of SCORE_PAGES
-// Blocks to spread the pages over (a third of them, or twice as many: 43 us a selection instead of 40).
+// Blocks to spread the pages over, 12 for each SM of a GB300 (a third of them, or twice as
+// many: 43 us a selection instead of 40).
 constexpr int SCORE_BLOCKS = 12 * 152;
 constexpr int PAGE_BYTES = 2 * D * 2;                // a page's bounds
 // shared memory: the warps' rings, then the query rows as fp32
@@ -399,8 +401,9 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) score_kernel(const SelectPar
 // then each warp writes the chosen pages of its part of the sequence, in rising order.
 // What takes the time is the way from one step to the next: 64 sequences of up to 448
 // pages, 4 heads, take 5 us, four digits of all 32 bits took 8.  The first SHARED keys
-// wait in shared memory, the rest is read again for each digit.  (A warp with 32 keys a lane in registers, searching bit by bit,
-// takes twice as long: its code runs once, and fetching it is what that takes.)
+// wait in shared memory, the rest is read again for each digit.  (A warp with 32 keys a
+// lane in registers, searching bit by bit, takes twice as long: its code runs once, and
+// fetching it is what that takes.)
 constexpr int CHOOSE_THREADS = 256;
 constexpr int CHOOSE_WARPS = CHOOSE_THREADS / 32;
 constexpr int SHARED = 4096;

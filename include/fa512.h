@@ -505,8 +505,9 @@ fa512_status fa512_cache_append_fp8(const void *k_new, const void *v_new, int64_
  * nearest to the fp32 quotient y / scale; ties to even, beyond the largest value
  * the largest value.  A group whose scale rounds to 0 (max |y| up to 6 * 2^-10)
  * gets codes 0.  A group that holds a NaN gets the NaN scale and codes 0: all its
- * elements read as NaN.  k_scale and v_scale are finite and above 0; a power of two is
- * faster, and the choice only matters for what lies outside the scales' range.
+ * elements read as NaN.  k_scale and v_scale are finite and above 0; where both are
+ * powers of two the call is faster (8 sequences of up to 4,096 tokens, 4 heads: 55 us,
+ * else 147), and the choice only matters for what lies outside the scales' range.
  * Other arguments and errors as fa512_cache_append.
  */
 #define FA512_FP4_ROW_BYTES 288
@@ -529,13 +530,19 @@ fa512_status fa512_cache_append_fp4(const void* k_new, const void* v_new, int64_
  *              (q_len >= 1, q_len * G <= 16)
  *   num_splits most pieces that a sequence may be cut into, at most 1024 (the
  *              SMs take equal ranges of the keys of all sequences; 1: whole
- *              sequences); 0 picks fa512_decode_auto_splits_fp4(); workspace
+ *              sequences); 0 picks fa512_decode_auto_splits_fp4(), which is for
+ *              lengths of half of max_kv_len and more.  Give max_kv_len as tightly
+ *              as the host knows it; where the lengths are much shorter, or few of
+ *              many are long, 1024 spreads the keys over all SMs (64 sequences of
+ *              4,096 positions: 101 us with that bound, 511 with 131,072, 117 with
+ *              1024) at the price of a larger workspace; workspace
  *              must be at least fa512_decode_workspace_bytes_fp4() bytes,
  *              256-byte aligned, not shared by calls that may run at the same time
  *
  * Codes and group scales are widened exactly, the queries (bf16) scaled by a
  * power of two per row and held in f16, sums are fp32; the softmax weights round
- * to f16.  Slots that no row sees may hold anything without reaching the output;
+ * to f16: to 11 bits, or, below 2^-16 of the row's largest, within 2^-26 of that,
+ * whatever the group scales of their values.  Slots that no row sees may hold anything without reaching the output;
  * a value that is not finite in a slot that one row of a KV head sees may reach
  * the head's other rows.  A row that sees a score of NaN or +infinity is NaN.  The
  * same inputs give the same bits every time.  batch * q_len is at most 65535, and
@@ -646,7 +653,8 @@ size_t fa512_select_workspace_bytes(int batch, int n_kv_heads, int page_size, in
  * num_splits and workspace as fa512_decode_paged_fp4: 0 picks
  * fa512_decode_auto_splits_sparse(), the workspace holds at least
  * fa512_decode_workspace_bytes_sparse() bytes.  Slots that no row sees, and
- * scores and values that are not finite, as there.
+ * scores and values that are not finite, as there; weights too over coded caches,
+ * over bf16 they round to bf16.
  * n_selected >= 1; n_selected * page_size, num_pages * page_size and
  * max_pages_per_seq * page_size are below 2^31 - 4096, batch * q_len and n_kv_heads
  * at most 65535, batch times the positions of a list at most 2^34.
