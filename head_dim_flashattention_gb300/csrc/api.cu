@@ -738,7 +738,7 @@ struct RangesPlan {
 // 4 bits: 26 with 72 of 9, 35 with 40 of 16).  Over coded caches a CTA has more to compute
 // for its bytes, and fewer of them take longer where ranges are long (64 x 64 pages of
 // 64, E4M3: 163 us with 76 ranges of 108, 166 with 64 of 128; 4 bits: 107 with 76 of 54,
-// 115 with 64 of 64, on one box; 108 to 116 as it is from box to box).
+// 115 with 64 of 64, side by side).
 RangesPlan plan_ranges(long long batch, int n_kv_heads, long long tiles, int n_sm, int list_bits) {
     RangesPlan best{1, 1};
     if (batch <= 0 || n_kv_heads <= 0) return best;

@@ -561,7 +561,13 @@ decode_ranges_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             }
             // ---- the segment's partial, unnormalised and times v_scale
             const int mine = seg.index & ~Segment::LAST;
-            const float f = p.o_scale * (1.f / JOIN);
+            const float f = p.o_scale;            // (JOIN comes off before it: it may be next to the smallest float)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < MTILES; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][i][e] *= 1.f / JOIN;
             if constexpr (NARROW) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

@@ -157,3 +157,26 @@ def test_scores_a_step_of_fp32_apart(fa, e, rows, kind, sparse):
                          stored(kind, values, 0x7E), n, math.log(2), num_splits=splits)
         assert np.max(np.abs(o - top * sign)) <= (2.0 ** -8 + 2.0 ** -10) * top
         assert np.all(np.abs(l / (2.0 ** e * math.log(2)) - 1) <= 2.0 ** -15)
+
+
+@KINDS
+@pytest.mark.parametrize("size", [1, 64])
+@pytest.mark.parametrize("rows", [2, 3, 16])
+def test_tensor_scales_next_to_the_smallest_float(fa, rows, size, kind, sparse):
+    """A v_scale that is no normal float.  The tolerance of an ordinary one, times this one; beside it a step of 2^-149
+    in each product and sum of a partial, and half a step of the output: bf16's smallest is 2^-133, and the outputs, up
+    to 6 size v_scale = 2^-129, are multiples of it."""
+    n, v_scale = 700, float(np.float32(2.0 ** -138 * 1.359375))
+    rng = np.random.RandomState(rows)
+    values = np.broadcast_to(4.0 + 2 * (rng.rand(D) < 0.5), (n, D)) * np.sign(rng.randn(D))
+    if kind == "e4m3":
+        values = values * size
+    k, v = stored(kind, sums(rng.randint(0, 8, n) * 0.5), 0x38), stored(kind, values, {1: 0x38, 64: 0x68}[size])
+    q = torch.zeros(1, rows, D)
+    q[..., :16] = 1
+    q = q.to(torch.bfloat16)
+    for splits in (0, 1):
+        o, _, table, lens = run(fa, kind, sparse, q, k, v, n, 0.125, v_scale=v_scale, num_splits=splits)
+        ro, _, weight = paged.decode_paged_any(q[:, None], k, v, table, lens, scale=0.125, v_scale=v_scale)
+        tol = (2.0 ** -10 + 1e-3) * weight[:, 0] + 64 * 2.0 ** -149 + 2.0 ** -134
+        assert np.all(np.abs(o - ro[:, 0]) <= tol), np.max(np.abs(o - ro[:, 0]) / tol)
